@@ -31,7 +31,7 @@
  *     fails;
  *   - dimensions: k must be a positive multiple of 256 (every row then starts 16-byte
  *     aligned, which the bulk/TMA copies need); n >= 1; m as stated per call;
- *   - alignment: every pointer must be 16-byte aligned.
+ *   - alignment: every pointer must be 16-byte aligned, unless the call says otherwise.
  *   - stream order: the calls keep the stream's order.  Most of their kernels are launched
  *     as programmatic dependents of the stream's previous kernel (they become resident early
  *     and wait for it to complete before touching memory), and every kernel lets the next
@@ -66,7 +66,13 @@ extern "C" {
 #define Q8ACT_ERR_TIMEOUT (-6)    /* a kernel gave up waiting (see q8act_device_status) */
 #define Q8ACT_ERR_DRAIN_TIMEOUT (-7) /* a kernel gave up waiting for its own copies
                                         before exiting (see q8act_device_status)       */
+#define Q8ACT_ERR_TYPE (-8)       /* an element type that the call does not take       */
 #define Q8ACT_ERR_CUDA_BASE 1000  /* 1000 + cudaError_t                                */
+
+/* Element types of the calls that take more than one. */
+#define Q8ACT_F32 0
+#define Q8ACT_F16 1               /* IEEE binary16                                     */
+#define Q8ACT_BF16 2
 
 /* Largest supported k (values per row). */
 #define Q8ACT_MAX_K 65536
@@ -354,6 +360,83 @@ int q8act_debug_gemv_q4_k_block_dots(const void *w, const int8_t *xq, int32_t *D
                                      int64_t n, int64_t k, void *stream);
 int q8act_debug_gemv_q5_k_block_dots(const void *w, const int8_t *xq, int32_t *D, int64_t m,
                                      int64_t n, int64_t k, void *stream);
+
+/*
+ * The norm in front of a product: residual addition, root-mean-square norm and q8_1
+ * quantization of each of m rows in one call.
+ *   s = x + residual (f32),  y = s * (mean(s^2) + eps)^-1/2 * weight (f32),
+ *   and y's q8_1 quants and scales, exactly as q8act_quantize_q8_1 (_mmq) gives them for y.
+ *   x [m][k], residual [m][k], residual_out [m][k]: elements of `type` (Q8ACT_F32, F16, BF16),
+ *       rows ldx, ldr, ldro elements apart (at least k; rows 16-byte aligned).  residual may be
+ *       NULL (s = x).  residual_out, when not NULL, receives s rounded once to `type`; it may be
+ *       x's or residual's own rows.  The norm is taken of the unrounded f32 sum.
+ *   weight [k] of `wtype`, or NULL (ones).  eps >= 0 (a row of zeros with eps = 0 divides 0 by
+ *       0: its quants are 0, as the quantizers give for NaN).
+ *   y: NULL, or [m][k] of `type`: the normed values, rounded once.
+ *   rmsnorm_q8_1:     xq [m][k] int8, xd [m][k/32] f32 (the GEMVs' activation);
+ *   rmsnorm_q8_1_mmq: xqh [m][k] binary16 quants, xdt [k/32][q8act_mmq_ldm(m)] f32 (the GEMM's).
+ */
+int q8act_rmsnorm_q8_1(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int wtype,
+                       float eps, void *residual_out, int64_t ldro, void *y, int8_t *xq, float *xd, int64_t m,
+                       int64_t k, int type, void *stream);
+int q8act_rmsnorm_q8_1_mmq(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                           int wtype, float eps, void *residual_out, int64_t ldro, void *y, uint16_t *xqh, float *xdt,
+                           int64_t m, int64_t k, int type, void *stream);
+
+/*
+ * MXFP4 -- the OCP microscaling 4-bit format, weights and activations alike.  A block of 32
+ * values shares a scale 2^(b - 127), b one byte (e8m0; 255 stands for NaN); a value is an e2m1
+ * code: bit 3 the sign, bits 0-2 the magnitude 0 0.5 1 1.5 2 3 4 6.
+ *   codes  [rows][k/2]: value 2i of a row in the low nibble of its byte i, 2i + 1 in the high one.
+ *   scales q8act_mxfp4_scale_bytes(rows, k) bytes, in tiles of 128 rows x 4 blocks (the order in
+ *          which the tensor cores take them): the byte of row r, block b stands at
+ *          ((r / 128) * (k / 128) + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.
+ *          Rows are padded to a multiple of 128; the padding's bytes are written as 0.
+ * k: a positive multiple of 256 up to Q8ACT_MAX_K; pointers and rows 16-byte aligned.
+ *
+ * q8act_quantize_mxfp4: x [m][k] of `type`, rows ldx elements apart.  Per block
+ *   E = floor(log2 max|x|) - 2, not below -127; codes = x / 2^E rounded to nearest, ties to the
+ *   even code, saturating at 6.  A block with a NaN or an infinity gets b = 255 and codes 0.
+ * q8act_dequant_mxfp4: y [m][k] of `type` = the values, rounded once (exact in f32 and BF16
+ *   unless below their normal range; F16 may overflow to infinity).
+ * q8act_tile_mxfp4_scales: row-major scale bytes [m][k/32] (as checkpoints store them) -> tiles.
+ */
+size_t q8act_mxfp4_scale_bytes(int64_t rows, int64_t k);   /* 0 for invalid dimensions */
+int q8act_quantize_mxfp4(const void *x, int64_t ldx, int type, void *codes, void *scales, int64_t m, int64_t k,
+                         void *stream);
+int q8act_dequant_mxfp4(const void *codes, const void *scales, void *y, int type, int64_t m, int64_t k, void *stream);
+int q8act_tile_mxfp4_scales(const void *scales, void *tiled, int64_t m, int64_t k, void *stream);
+
+/*
+ * The product of MXFP4 matrices, for one token or thousands:
+ *   y[t][r] = sum_b 2^(Ew + Ex) sum_{i<32} w[r][32b+i] * x[t][32b+i], accumulated in f32.
+ *   w, wscales: n weight rows; y [m][n] of `ytype`, rounded once, overwritten.  m, n >= 1.
+ *   gemm_mxfp4 quantizes the activation x [m][k] of `xtype` (rows ldx elements apart) as
+ *     q8act_quantize_mxfp4 does, into ws (q8act_gemm_mxfp4_workspace_bytes(m, k) bytes; 0 for
+ *     invalid dimensions), the product being a programmatic dependent of that quantizer;
+ *   gemm_mxfp4_preq takes the quantized activation xq, xscales.
+ */
+size_t q8act_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k);
+int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t ldx, int xtype, void *y, int ytype,
+                     int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);
+int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
+                          int64_t m, int64_t n, int64_t k, void *stream);
+
+/*
+ * What a decoder answers with: for each of m rows of v logits (`type`, rows ld >= v elements
+ * apart, any ld; every array needs only its elements' alignment),
+ *   logprob [m] f32: log softmax of the token tokens[row] (int32).  A negative token asks for
+ *       nothing and gets 0; one >= v gets NaN.  tokens and logprob may both be NULL.
+ *   entropy [m] f32 (or NULL): - sum p log p, in nats.
+ *   top_ids [m][top] int32, top_logprobs [m][top] f32: the `top` most likely tokens, most likely
+ *       first, equal logits by the lower index; 0 <= top <= Q8ACT_MAX_TOP (both NULL when 0).
+ * Masked logits are -inf: they count nothing and are never an alternative; places of the list
+ * beyond the unmasked tokens hold id -1 and -inf.  A row that is masked as a whole has entropy 0
+ * and log probabilities -inf.  A row that holds a NaN or +inf has no softmax: NaN, ids -1.
+ */
+#define Q8ACT_MAX_TOP 32
+int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *tokens, float *logprob, float *entropy,
+                   int32_t *top_ids, float *top_logprobs, int64_t m, int64_t v, int top, void *stream);
 
 /*
  * Synchronizes `stream`, then reads and clears the device-side status word that kernels set

@@ -26,7 +26,11 @@ Q8ACT_ERR_WORKSPACE = -4
 Q8ACT_ERR_DEVICE = -5
 Q8ACT_ERR_TIMEOUT = -6
 Q8ACT_ERR_DRAIN_TIMEOUT = -7
+Q8ACT_ERR_TYPE = -8
 Q8ACT_ERR_CUDA_BASE = 1000
+Q8ACT_F32 = 0
+Q8ACT_F16 = 1
+Q8ACT_BF16 = 2
 Q8ACT_MAX_K = 65536
 Q8ACT_GEMV_MAX_M = 15
 Q8ACT_GEMV_MAX_GROUP = 8
@@ -43,8 +47,12 @@ EXPORTED = (
     "q8act_dequant_q6_k_f16", "q8act_dequant_q4_k_f16", "q8act_dequant_q5_k_f16",
     "q8act_gemv_q6_k", "q8act_gemv_q4_k", "q8act_gemv_q5_k",
     "q8act_debug_gemv_q6_k_block_dots", "q8act_debug_gemv_q4_k_block_dots", "q8act_debug_gemv_q5_k_block_dots",
+    "q8act_rmsnorm_q8_1", "q8act_rmsnorm_q8_1_mmq",
+    "q8act_mxfp4_scale_bytes", "q8act_quantize_mxfp4", "q8act_dequant_mxfp4", "q8act_tile_mxfp4_scales",
+    "q8act_gemm_mxfp4_workspace_bytes", "q8act_gemm_mxfp4", "q8act_gemm_mxfp4_preq", "q8act_logprobs",
 )
 Q8ACT_GEMV_KQ_MAX_M = 8
+Q8ACT_MAX_TOP = 32
 Q8ACT_NOALLOC_WS_BYTES = 24 << 20
 Q8ACT_GEMM_SPLIT_BYTES = 320 * 65536 + 160 * 64
 
@@ -71,6 +79,7 @@ def lib() -> ctypes.CDLL:
                     "`python -m q8_block_quantized_act_gb300.build` (no CPU fallback exists)")
             L = ctypes.CDLL(LIB_PATH)
             P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+            F32 = ctypes.c_float
             sig = {
                 "q8act_version": ([], I32),
                 "q8act_strerror": ([I32], ctypes.c_char_p),
@@ -99,7 +108,17 @@ def lib() -> ctypes.CDLL:
                 "q8act_gemv_workspace_bytes": ([I64, I64], SZ),
                 "q8act_gemv_q8_0_f32": ([P, P, P, I64, I64, I64, P, SZ, P], I32),
                 "q8act_debug_wait_timeout": ([I64, P], I32),
+                "q8act_mxfp4_scale_bytes": ([I64, I64], SZ),
+                "q8act_quantize_mxfp4": ([P, I64, I32, P, P, I64, I64, P], I32),
+                "q8act_dequant_mxfp4": ([P, P, P, I32, I64, I64, P], I32),
+                "q8act_tile_mxfp4_scales": ([P, P, I64, I64, P], I32),
+                "q8act_gemm_mxfp4_workspace_bytes": ([I64, I64], SZ),
+                "q8act_gemm_mxfp4": ([P, P, P, I64, I32, P, I32, I64, I64, I64, P, SZ, P], I32),
+                "q8act_gemm_mxfp4_preq": ([P, P, P, P, P, I32, I64, I64, I64, P], I32),
+                "q8act_logprobs": ([P, I64, I32, P, P, P, P, P, I64, I64, I32, P], I32),
             }
+            for f in ("q8act_rmsnorm_q8_1", "q8act_rmsnorm_q8_1_mmq"):
+                sig[f] = ([P, I64, P, I64, P, I32, F32, P, I64, P, P, P, I64, I64, I32, P], I32)
             for f in ("q6_k", "q4_k", "q5_k"):
                 sig[f"q8act_dequant_{f}_f16"] = ([P, P, I64, I64, P], I32)
                 sig[f"q8act_gemv_{f}"] = ([P, P, P, P, I64, I64, I64, P], I32)
@@ -295,3 +314,49 @@ def q8act_debug_gemv_q4_k_block_dots(w, xq, D, m, n, k, stream=None) -> int:
 
 def q8act_debug_gemv_q5_k_block_dots(w, xq, D, m, n, k, stream=None) -> int:
     return lib().q8act_debug_gemv_q5_k_block_dots(_p(w), _p(xq), _p(D), m, n, k, _s(stream))
+
+
+def q8act_rmsnorm_q8_1(x, ldx, residual, ldr, weight, wtype, eps, residual_out, ldro, y, xq, xd, m, k, type,
+                       stream=None) -> int:
+    return lib().q8act_rmsnorm_q8_1(_p(x), ldx, _p(residual), ldr, _p(weight), wtype, eps, _p(residual_out), ldro,
+                                    _p(y), _p(xq), _p(xd), m, k, type, _s(stream))
+
+
+def q8act_rmsnorm_q8_1_mmq(x, ldx, residual, ldr, weight, wtype, eps, residual_out, ldro, y, xqh, xdt, m, k, type,
+                           stream=None) -> int:
+    return lib().q8act_rmsnorm_q8_1_mmq(_p(x), ldx, _p(residual), ldr, _p(weight), wtype, eps, _p(residual_out), ldro,
+                                        _p(y), _p(xqh), _p(xdt), m, k, type, _s(stream))
+
+
+def q8act_mxfp4_scale_bytes(rows, k) -> int:
+    return lib().q8act_mxfp4_scale_bytes(rows, k)
+
+
+def q8act_quantize_mxfp4(x, ldx, type, codes, scales, m, k, stream=None) -> int:
+    return lib().q8act_quantize_mxfp4(_p(x), ldx, type, _p(codes), _p(scales), m, k, _s(stream))
+
+
+def q8act_dequant_mxfp4(codes, scales, y, type, m, k, stream=None) -> int:
+    return lib().q8act_dequant_mxfp4(_p(codes), _p(scales), _p(y), type, m, k, _s(stream))
+
+
+def q8act_tile_mxfp4_scales(scales, tiled, m, k, stream=None) -> int:
+    return lib().q8act_tile_mxfp4_scales(_p(scales), _p(tiled), m, k, _s(stream))
+
+
+def q8act_gemm_mxfp4_workspace_bytes(m, k) -> int:
+    return lib().q8act_gemm_mxfp4_workspace_bytes(m, k)
+
+
+def q8act_gemm_mxfp4(w, wscales, x, ldx, xtype, y, ytype, m, n, k, ws, ws_bytes, stream=None) -> int:
+    return lib().q8act_gemm_mxfp4(_p(w), _p(wscales), _p(x), ldx, xtype, _p(y), ytype, m, n, k, _p(ws), ws_bytes,
+                                  _s(stream))
+
+
+def q8act_gemm_mxfp4_preq(w, wscales, xq, xscales, y, ytype, m, n, k, stream=None) -> int:
+    return lib().q8act_gemm_mxfp4_preq(_p(w), _p(wscales), _p(xq), _p(xscales), _p(y), ytype, m, n, k, _s(stream))
+
+
+def q8act_logprobs(logits, ld, type, tokens, logprob, entropy, top_ids, top_logprobs, m, v, top, stream=None) -> int:
+    return lib().q8act_logprobs(_p(logits), ld, type, _p(tokens), _p(logprob), _p(entropy), _p(top_ids),
+                                _p(top_logprobs), m, v, top, _s(stream))

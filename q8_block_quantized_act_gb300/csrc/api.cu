@@ -80,6 +80,23 @@ int check_gemm_dims(int64_t m, int64_t n, int64_t k)
     return Q8ACT_OK;
 }
 
+bool known_type(int type) { return type == Q8ACT_F32 || type == Q8ACT_F16 || type == Q8ACT_BF16; }
+
+int64_t type_size(int type) { return type == Q8ACT_F32 ? 4 : 2; }
+
+// Rows of k elements of a known type, ld elements apart, each 16-byte aligned.
+int check_rows(const void *p, int64_t ld, int64_t k, int type)
+{
+    if (ld < k || ld > ((int64_t)1 << 40)) return Q8ACT_ERR_DIMS;
+    return aligned16(p) && ld * type_size(type) % 16 == 0 ? Q8ACT_OK : Q8ACT_ERR_ALIGN;
+}
+
+// m x k values of an MXFP4 matrix.
+int check_mxfp4_dims(int64_t m, int64_t k)
+{
+    return check_k(k) == Q8ACT_OK && m >= 1 && m <= INT32_MAX / 2 && m * k <= ((int64_t)1 << 36) ? Q8ACT_OK : Q8ACT_ERR_DIMS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -96,6 +113,7 @@ const char *q8act_strerror(int rc)
     case Q8ACT_ERR_WORKSPACE: return "workspace missing or too small";
     case Q8ACT_ERR_DEVICE: return "the current device is not an sm_103 (GB300) GPU";
     case Q8ACT_ERR_TIMEOUT: return "a kernel timed out waiting in its pipeline";
+    case Q8ACT_ERR_TYPE: return "an element type that the call does not take";
     case Q8ACT_ERR_DRAIN_TIMEOUT: return "a kernel timed out waiting for its own copies before exit";
     default:
         if (rc >= Q8ACT_ERR_CUDA_BASE) return cudaGetErrorString((cudaError_t)(rc - Q8ACT_ERR_CUDA_BASE));
@@ -513,6 +531,156 @@ int q8act_debug_gemm_block_dots(const void *w, const uint16_t *xqh, int32_t *D, 
     // The dot stage needs a readable (unused) scale array of the right shape: reuse the
     // quants, which are larger than the scale array.
     return gemm_core(w, xqh, reinterpret_cast<const float *>(xqh), nullptr, D, m, n, k, nullptr, 0, false, stream);
+}
+
+// ---- the norm in front of a product ----
+
+static int rmsnorm_common(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int wtype,
+                          float eps, void *residual_out, int64_t ldro, void *y, void *q, float *d, bool mmq, int64_t m,
+                          int64_t k, int type, void *stream)
+{
+    if (!x || !q || !d) return Q8ACT_ERR_NULL;
+    if (!known_type(type) || (weight && !known_type(wtype))) return Q8ACT_ERR_TYPE;
+    if (check_k(k) != Q8ACT_OK || m < 1 || m > ((int64_t)1 << 34) / k || !(eps >= 0.0f)) return Q8ACT_ERR_DIMS;
+    if (mmq && m * k > kMaxGemmElems) return Q8ACT_ERR_DIMS;
+    int rc = check_rows(x, ldx, k, type);
+    if (!rc && residual) rc = check_rows(residual, ldr, k, type);
+    if (!rc && residual_out) rc = check_rows(residual_out, ldro, k, type);
+    if (rc) return rc;
+    if (!aligned16(weight) || !aligned16(y) || !aligned16(q) || !aligned16(d)) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    const q8::NormArgs a{x, residual, weight, residual_out, y, q, d, ldx, ldr, ldro, q8act_mmq_ldm(m), eps, wtype};
+    return cuda_rc(q8::launch_rmsnorm_q8_1(*dev, a, mmq, m, k, type, (cudaStream_t)stream));
+}
+
+int q8act_rmsnorm_q8_1(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int wtype,
+                       float eps, void *residual_out, int64_t ldro, void *y, int8_t *xq, float *xd, int64_t m,
+                       int64_t k, int type, void *stream)
+{
+    return rmsnorm_common(x, ldx, residual, ldr, weight, wtype, eps, residual_out, ldro, y, xq, xd, false, m, k, type,
+                          stream);
+}
+
+int q8act_rmsnorm_q8_1_mmq(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                           int wtype, float eps, void *residual_out, int64_t ldro, void *y, uint16_t *xqh, float *xdt,
+                           int64_t m, int64_t k, int type, void *stream)
+{
+    return rmsnorm_common(x, ldx, residual, ldr, weight, wtype, eps, residual_out, ldro, y, xqh, xdt, true, m, k, type,
+                          stream);
+}
+
+// ---- MXFP4 ----
+
+size_t q8act_mxfp4_scale_bytes(int64_t rows, int64_t k)
+{
+    if (check_mxfp4_dims(rows, k) != Q8ACT_OK) return 0;
+    return (size_t)((rows + 127) / 128) * (size_t)(k / 128) * 512;
+}
+
+int q8act_quantize_mxfp4(const void *x, int64_t ldx, int type, void *codes, void *scales, int64_t m, int64_t k,
+                         void *stream)
+{
+    if (!x || !codes || !scales) return Q8ACT_ERR_NULL;
+    if (!known_type(type)) return Q8ACT_ERR_TYPE;
+    if (check_mxfp4_dims(m, k) != Q8ACT_OK) return Q8ACT_ERR_DIMS;
+    int rc = check_rows(x, ldx, k, type);
+    if (rc) return rc;
+    if (!aligned16(codes) || !aligned16(scales)) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    return cuda_rc(q8::launch_quantize_mxfp4(*dev, x, ldx, type, static_cast<uint8_t *>(codes),
+                                             static_cast<uint8_t *>(scales), m, k, (cudaStream_t)stream));
+}
+
+int q8act_dequant_mxfp4(const void *codes, const void *scales, void *y, int type, int64_t m, int64_t k, void *stream)
+{
+    if (!codes || !scales || !y) return Q8ACT_ERR_NULL;
+    if (!known_type(type)) return Q8ACT_ERR_TYPE;
+    if (check_mxfp4_dims(m, k) != Q8ACT_OK) return Q8ACT_ERR_DIMS;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    return cuda_rc(q8::launch_dequant_mxfp4(*dev, static_cast<const uint8_t *>(codes),
+                                            static_cast<const uint8_t *>(scales), y, type, m, k, (cudaStream_t)stream));
+}
+
+int q8act_tile_mxfp4_scales(const void *scales, void *tiled, int64_t m, int64_t k, void *stream)
+{
+    if (!scales || !tiled) return Q8ACT_ERR_NULL;
+    if (check_mxfp4_dims(m, k) != Q8ACT_OK) return Q8ACT_ERR_DIMS;
+    if (!aligned16(scales) || !aligned16(tiled)) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    return cuda_rc(q8::launch_tile_mxfp4_scales(*dev, static_cast<const uint8_t *>(scales),
+                                                static_cast<uint8_t *>(tiled), m, k, (cudaStream_t)stream));
+}
+
+// Workspace of the fused product: the activation's codes, rounded up to 256 bytes, then its scales.
+size_t q8act_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k)
+{
+    if (check_mxfp4_dims(m, k) != Q8ACT_OK) return 0;
+    return ((size_t)m * k / 2 + 255) / 256 * 256 + q8act_mxfp4_scale_bytes(m, k);
+}
+
+static int gemm_mxfp4_check(int ytype, int64_t m, int64_t n, int64_t k)
+{
+    if (!known_type(ytype)) return Q8ACT_ERR_TYPE;
+    if (check_mxfp4_dims(m, k) != Q8ACT_OK || check_mxfp4_dims(n, k) != Q8ACT_OK) return Q8ACT_ERR_DIMS;
+    return m * n <= ((int64_t)1 << 40) ? Q8ACT_OK : Q8ACT_ERR_DIMS;
+}
+
+int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
+                          int64_t m, int64_t n, int64_t k, void *stream)
+{
+    if (!w || !wscales || !xq || !xscales || !y) return Q8ACT_ERR_NULL;
+    int rc = gemm_mxfp4_check(ytype, m, n, k);
+    if (rc) return rc;
+    if (!aligned16(w) || !aligned16(wscales) || !aligned16(xq) || !aligned16(xscales) || !aligned16(y))
+        return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    return cuda_rc(q8::launch_gemm_mxfp4(*dev, static_cast<const uint8_t *>(w), static_cast<const uint8_t *>(wscales),
+                                         static_cast<const uint8_t *>(xq), static_cast<const uint8_t *>(xscales), y,
+                                         ytype, m, n, k, (cudaStream_t)stream));
+}
+
+int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t ldx, int xtype, void *y, int ytype,
+                     int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!w || !wscales || !x || !y) return Q8ACT_ERR_NULL;
+    if (!known_type(xtype)) return Q8ACT_ERR_TYPE;
+    int rc = gemm_mxfp4_check(ytype, m, n, k);
+    if (rc) return rc;
+    if (!ws || ws_bytes < q8act_gemm_mxfp4_workspace_bytes(m, k)) return Q8ACT_ERR_WORKSPACE;
+    if (!aligned16(w) || !aligned16(wscales) || !aligned16(y) || !aligned16(ws)) return Q8ACT_ERR_ALIGN;
+    uint8_t *xq = static_cast<uint8_t *>(ws), *xsc = xq + ((size_t)m * k / 2 + 255) / 256 * 256;
+    rc = q8act_quantize_mxfp4(x, ldx, xtype, xq, xsc, m, k, stream);
+    if (rc) return rc;
+    return q8act_gemm_mxfp4_preq(w, wscales, xq, xsc, y, ytype, m, n, k, stream);
+}
+
+// ---- log probabilities ----
+
+int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *tokens, float *logprob, float *entropy,
+                   int32_t *top_ids, float *top_logprobs, int64_t m, int64_t v, int top, void *stream)
+{
+    if (!logits || !tokens != !logprob || (top > 0 && (!top_ids || !top_logprobs))) return Q8ACT_ERR_NULL;
+    if (!known_type(type)) return Q8ACT_ERR_TYPE;
+    if (m < 1 || v < 1 || v > (1 << 30) || top < 0 || top > Q8ACT_MAX_TOP || ld < v || ld > ((int64_t)1 << 40) ||
+        m > ((int64_t)1 << 46) / ld)
+        return Q8ACT_ERR_DIMS;
+    // Rows start wherever ld puts them, so the arrays need their elements' alignment only.
+    const uintptr_t words = (uintptr_t)tokens | (uintptr_t)logprob | (uintptr_t)entropy | (uintptr_t)top_ids |
+                            (uintptr_t)top_logprobs;
+    if ((uintptr_t)logits % type_size(type) || words % 4) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    const q8::LogprobArgs a{logits, tokens, logprob, entropy, top_ids, top_logprobs, ld, top};
+    return cuda_rc(q8::launch_logprobs(*dev, a, m, v, type, (cudaStream_t)stream));
 }
 
 // Test hook: one thread waits on an mbarrier that nothing arrives on, through the pipelines'

@@ -95,4 +95,43 @@ cudaError_t launch_gemm_q8_0_repacked(const DeviceInfo &dev, const uint16_t *wq1
                                       int32_t *dots, int64_t m, int64_t n, int64_t k, int64_t ldm,
                                       void *split_ws, size_t split_bytes, bool pdl, cudaStream_t stream);
 
+// Residual addition + RMS norm + q8_1 quantization.  Strides in elements; residual,
+// residual_out, weight and y may be null.  q: int8 [m][k] with d [m][k/32], or (mmq) binary16
+// [m][k] with d [k/32][ldm].
+struct NormArgs {
+    const void *x, *residual, *weight;
+    void *residual_out, *y, *q;
+    float *d;
+    int64_t ldx, ldr, ldro, ldm;
+    float eps;
+    int wtype;
+};
+cudaError_t launch_rmsnorm_q8_1(const DeviceInfo &dev, const NormArgs &a, bool mmq, int64_t m, int64_t k, int type,
+                                cudaStream_t stream);
+
+// MXFP4: quantization, mirror, tiling of row-major scales, product (mxfp4.cuh has the format).
+cudaError_t launch_quantize_mxfp4(const DeviceInfo &dev, const void *x, int64_t ldx, int type, uint8_t *codes,
+                                  uint8_t *scales, int64_t m, int64_t k, cudaStream_t stream);
+cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, const uint8_t *scales, void *y, int type,
+                                 int64_t m, int64_t k, cudaStream_t stream);
+cudaError_t launch_tile_mxfp4_scales(const DeviceInfo &dev, const uint8_t *src, uint8_t *dst, int64_t m, int64_t k,
+                                     cudaStream_t stream);
+cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
+                              const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k,
+                              cudaStream_t stream);
+
+// Log probabilities of logits rows (stride ld elements): the given tokens' (tokens, logprob), the
+// entropy and the `top` most likely tokens; each of the three may be left out (null, top = 0).
+struct LogprobArgs {
+    const void *logits;
+    const int32_t *tokens;
+    float *logprob, *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+    int64_t ld;
+    int top;
+};
+cudaError_t launch_logprobs(const DeviceInfo &dev, const LogprobArgs &a, int64_t m, int64_t v, int type,
+                            cudaStream_t stream);
+
 }  // namespace q8

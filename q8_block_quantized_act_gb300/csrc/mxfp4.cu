@@ -1,0 +1,120 @@
+// mxfp4.cu -- MXFP4 quantization (activations and weights), its mirror, and the tiling of
+// row-major scales.  Elementwise passes bound by memory.
+#include "launch.h"
+#include "mxfp4.cuh"
+#include "types.cuh"
+
+namespace q8 {
+namespace {
+
+// One thread per 8 consecutive values, 4 lanes per block.  Rows m .. 128 ceil(m / 128) - 1 get
+// zero scale bytes, so that the whole scale array is defined.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict__ x, int64_t ldx,
+                                                             uint32_t *__restrict__ codes,
+                                                             uint8_t *__restrict__ scales, int64_t m, int k)
+{
+    griddep_enter();
+    const int chunks = k / 8;
+    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    if (c >= chunks) return;          // k / 8 is a multiple of 32: warps are whole
+    const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
+    for (int64_t r = blockIdx.y; r < padded; r += gridDim.y) {
+        uint32_t b = 0;
+        if (r < m) {
+            float v[8];
+            const uint4 *src = reinterpret_cast<const uint4 *>(x + r * ldx + (int64_t)c * 8);
+            if constexpr (sizeof(T) == 4) {
+                float lo[4], hi[4];
+                unpack<T>(src[0], lo);
+                unpack<T>(src[1], hi);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
+            } else {
+                unpack<T>(src[0], v);
+            }
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            b = mx_scale_byte(a);
+            const float inv = b == 255u ? 0.0f : mx_inverse(b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = b == 255u ? 0.0f : v[i] * inv;
+            codes[r * chunks + c] = mx_codes8(v);
+        }
+        if ((c & 3) == 0) scales[mx_scale_at(r, c >> 2, k / MX_TILE_K)] = (uint8_t)b;
+    }
+}
+
+// One thread per 8 codes.
+template <typename T>
+__global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__restrict__ codes,
+                                                            const uint8_t *__restrict__ scales, T *__restrict__ y,
+                                                            int64_t m, int k)
+{
+    griddep_enter();
+    const int chunks = k / 8;
+    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    if (c >= chunks) return;
+    for (int64_t r = blockIdx.y; r < m; r += gridDim.y) {
+        const uint32_t w = codes[r * chunks + c];
+        const float s = mx_scale(scales[mx_scale_at(r, c >> 2, k / MX_TILE_K)]);
+        T *dst = y + r * k + (int64_t)c * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = from_f32<T>(0.5f * (float)mx_twice(w >> (4 * i)) * s);
+    }
+}
+
+__global__ void __launch_bounds__(256) tile_mxfp4_scales_kernel(const uint8_t *__restrict__ src,
+                                                                uint8_t *__restrict__ dst, int64_t m, int kb)
+{
+    griddep_enter();
+    const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < padded * kb; i += stride) {
+        const int64_t r = i / kb;
+        const int b = (int)(i % kb);
+        dst[mx_scale_at(r, b, kb / 4)] = r < m ? src[i] : 0;
+    }
+}
+
+dim3 grid_rows(int64_t rows, int64_t chunks)
+{
+    return dim3((unsigned)((chunks + 255) / 256), (unsigned)(rows < 65535 ? rows : 65535));
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_mxfp4(const DeviceInfo &dev, const void *x, int64_t ldx, int type, uint8_t *codes,
+                                  uint8_t *scales, int64_t m, int64_t k, cudaStream_t stream)
+{
+    return with_type(type, [&](auto t) {
+        using T = decltype(t);
+        const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
+        return launch_dependent(quantize_mxfp4_kernel<T>, grid_rows(padded, k / 8), 256, 0, stream,
+                                static_cast<const T *>(x), ldx, reinterpret_cast<uint32_t *>(codes), scales, m, (int)k);
+    });
+}
+
+cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, const uint8_t *scales, void *y, int type,
+                                 int64_t m, int64_t k, cudaStream_t stream)
+{
+    return with_type(type, [&](auto t) {
+        using T = decltype(t);
+        return launch_dependent(dequant_mxfp4_kernel<T>, grid_rows(m, k / 8), 256, 0, stream,
+                                reinterpret_cast<const uint32_t *>(codes), scales, static_cast<T *>(y), m, (int)k);
+    });
+}
+
+cudaError_t launch_tile_mxfp4_scales(const DeviceInfo &dev, const uint8_t *src, uint8_t *dst, int64_t m, int64_t k,
+                                     cudaStream_t stream)
+{
+    const int64_t total = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS * (k / QK);
+    const int64_t want = (total + 255) / 256, cap = (int64_t)dev.num_sms * 8;
+    return launch_dependent(tile_mxfp4_scales_kernel, dim3((unsigned)(want < cap ? want : cap)), 256, 0, stream, src,
+                            dst, m, (int)(k / QK));
+}
+
+}  // namespace q8

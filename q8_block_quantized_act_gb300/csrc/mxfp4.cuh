@@ -1,0 +1,63 @@
+// mxfp4.cuh -- the MXFP4 block format: 32 values share a power-of-two scale (one e8m0 byte b,
+// 2^(b - 127), b = 255 for a block that holds a NaN or an infinity), each value is an e2m1 code
+// (sign, magnitude 0 0.5 1 1.5 2 3 4 6).  Codes: two to a byte, the even one in the low nibble,
+// rows of k / 2 bytes.  Scales: tiles of 128 rows x 128 values (4 blocks), 512 bytes each, the
+// order that the block-scaled tensor-core product copies into tensor memory as it stands.
+#pragma once
+
+#include "common.cuh"
+
+namespace q8 {
+
+constexpr int MX_TILE_ROWS = 128;
+constexpr int MX_TILE_K = 128;
+constexpr int MX_TILE_BYTES = 512;
+
+// Offset of the scale byte of row r, block b.
+__host__ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int b, int ktiles)
+{
+    return ((r >> 7) * ktiles + (b >> 2)) * MX_TILE_BYTES + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+
+// 2^(b - 127) for a scale byte (b = 255: NaN); b = 0 is the subnormal 2^-127.
+__device__ __forceinline__ float mx_scale(uint32_t b)
+{
+    return __uint_as_float(b == 255u ? 0x7fffffffu : (b == 0u ? 0x00400000u : b << 23));
+}
+
+// The scale byte of a block from the largest of its values' absolute bits:
+// E = floor(log2 amax) - 2 (the largest code's exponent), clamped to 2^-127 from below.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits)
+{
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const uint32_t e = amax_bits >> 23;
+    return e > 2u ? e - 2u : 0u;
+}
+
+// 2^(127 - b), the exact factor that brings a block's values onto the code's grid (b <= 252).
+__device__ __forceinline__ float mx_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// Eight values already scaled by mx_inverse to eight codes: nearest, ties to the even code,
+// saturating at 6.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Twice the value of a code (an integer), from its low four bits: magnitudes 0 1 2 3 4 6 8 12.
+__device__ __forceinline__ int mx_twice(uint32_t c)
+{
+    const int mag = (int)((0xC8643210u >> (4 * (c & 7u))) & 15u);
+    return (c & 8u) ? -mag : mag;
+}
+
+}  // namespace q8
