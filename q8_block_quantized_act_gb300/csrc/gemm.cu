@@ -25,6 +25,7 @@
 // odd chunks; six operand stages instead of four.
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace q8 {
 namespace {
@@ -81,19 +82,6 @@ struct Cfg {
     static_assert(OFF_A % 1024 == 0 && OFF_RAW % 1024 == 0 && OFF_SC % 128 == 0, "alignment");
 };
 
-// Shared-memory matrix descriptor for a K-major operand stored in 128-byte swizzled rows
-// (8-row atoms of 1024 bytes): start address >> 4 (bits 0-13), leading byte offset
-// (unused for this layout, bits 16-29), stride byte offset = 1024 >> 4 (bits 32-45),
-// descriptor version 1 (bits 46-47), swizzle mode 2 = 128-byte (bits 61-63).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate)
 {
@@ -102,14 +90,6 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-        ::"r"(smem_u32(bar))
         : "memory");
 }
 
@@ -180,24 +160,6 @@ __device__ __forceinline__ Bars carve_bars(uint8_t *base)
     r.pair_empty = b; b += D_PAIRS;
     r.mma_done = b;
     return r;
-}
-
-// A wait that also gives up as soon as another role of this CTA has given up.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *status,
-                                              volatile int *abort_flag)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-#pragma unroll 1
-    while (true) {
-        if (mbar_try_wait_sleep(bar, parity, WAIT_HINT_NS)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > WAIT_TIMEOUT_NS) {
-            atomicOr(status, STATUS_TIMEOUT);
-            *abort_flag = 1;
-            return false;
-        }
-    }
 }
 
 // Work schedule of one launch.  The work is the sequence of units (tile, 256-wide k group),
@@ -282,9 +244,7 @@ __global__ void __launch_bounds__(Cfg<BN_T, !REPACKED>::THREADS, Cfg<BN_T, !REPA
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_alloc(tmem_slot, TMEM_COLS);
     }
     if (warp == PRODUCER_WARP && lane == 0) {
         prefetch_tensormap(&tm_w);
@@ -631,51 +591,9 @@ __global__ void __launch_bounds__(Cfg<BN_T, !REPACKED>::THREADS, Cfg<BN_T, !REPA
     __syncthreads();
     if (warp == MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"(TMEM_COLS) : "memory");
+        tc_dealloc(tmem_base, TMEM_COLS);
     }
 }
-
-// ---------------------------------------------------------------------------------------
-// Host: tensor maps through the driver entry point (no libcuda link dependency).
-// ---------------------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
-bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t dim0,
-               uint64_t dim1, uint64_t stride1_bytes, uint32_t box0, uint32_t box1,
-               CUtensorMapSwizzle swz)
-{
-    EncodeTiledFn fn = get_encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {dim0, dim1};
-    const cuuint64_t strides[1] = {stride1_bytes};
-    const cuuint32_t box[2] = {box0, box1};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
-namespace {
 
 }  // namespace
 
