@@ -632,8 +632,9 @@ static int gemm_mxfp4_check(int ytype, int64_t m, int64_t n, int64_t k)
     return m * n <= ((int64_t)1 << 40) ? Q8ACT_OK : Q8ACT_ERR_DIMS;
 }
 
-int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
-                          int64_t m, int64_t n, int64_t k, void *stream)
+// pdl: the stream's previous operation is the quantizer of the same call.
+static int gemm_mxfp4_core(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
+                           int64_t m, int64_t n, int64_t k, bool pdl, void *stream)
 {
     if (!w || !wscales || !xq || !xscales || !y) return Q8ACT_ERR_NULL;
     int rc = gemm_mxfp4_check(ytype, m, n, k);
@@ -644,7 +645,13 @@ int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, co
     if ((rc = current_device(&dev))) return rc;
     return cuda_rc(q8::launch_gemm_mxfp4(*dev, static_cast<const uint8_t *>(w), static_cast<const uint8_t *>(wscales),
                                          static_cast<const uint8_t *>(xq), static_cast<const uint8_t *>(xscales), y,
-                                         ytype, m, n, k, (cudaStream_t)stream));
+                                         ytype, m, n, k, pdl, (cudaStream_t)stream));
+}
+
+int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
+                          int64_t m, int64_t n, int64_t k, void *stream)
+{
+    return gemm_mxfp4_core(w, wscales, xq, xscales, y, ytype, m, n, k, false, stream);
 }
 
 int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t ldx, int xtype, void *y, int ytype,
@@ -659,7 +666,7 @@ int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t 
     uint8_t *xq = static_cast<uint8_t *>(ws), *xsc = xq + ((size_t)m * k / 2 + 255) / 256 * 256;
     rc = q8act_quantize_mxfp4(x, ldx, xtype, xq, xsc, m, k, stream);
     if (rc) return rc;
-    return q8act_gemm_mxfp4_preq(w, wscales, xq, xsc, y, ytype, m, n, k, stream);
+    return gemm_mxfp4_core(w, wscales, xq, xsc, y, ytype, m, n, k, true, stream);
 }
 
 // ---- log probabilities ----

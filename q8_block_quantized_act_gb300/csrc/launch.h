@@ -110,6 +110,8 @@ cudaError_t launch_rmsnorm_q8_1(const DeviceInfo &dev, const NormArgs &a, bool m
                                 cudaStream_t stream);
 
 // MXFP4: quantization, mirror, tiling of row-major scales, product (mxfp4.cuh has the format).
+// pdl: the stream's previous kernel is the call's own quantizer producing x / xsc; the product
+// then starts reading its weights before that kernel has finished.
 cudaError_t launch_quantize_mxfp4(const DeviceInfo &dev, const void *x, int64_t ldx, int type, uint8_t *codes,
                                   uint8_t *scales, int64_t m, int64_t k, cudaStream_t stream);
 cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, const uint8_t *scales, void *y, int type,
@@ -117,7 +119,7 @@ cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, co
 cudaError_t launch_tile_mxfp4_scales(const DeviceInfo &dev, const uint8_t *src, uint8_t *dst, int64_t m, int64_t k,
                                      cudaStream_t stream);
 cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
-                              const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k,
+                              const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k, bool pdl,
                               cudaStream_t stream);
 
 // Log probabilities of logits rows (stride ld elements): the given tokens' (tokens, logprob), the
