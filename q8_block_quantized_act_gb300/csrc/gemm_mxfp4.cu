@@ -434,7 +434,7 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
         auto split = [&](int bn) {
             const int64_t tiles = rows * ((m + bn - 1) / bn);
             int CL = 1;
-            while (CL < 8 && tiles * CL * 2 <= 2 * dev.num_sms && CL * 2 <= k / BK) CL *= 2;
+            while (CL < 8 && tiles * CL * 2 <= dev.num_sms && CL * 2 <= k / BK) CL *= 2;
             return CL;
         };
         if (m <= 16) return launch_tiles<Cfg<16, 9>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(16), pdl, stream);

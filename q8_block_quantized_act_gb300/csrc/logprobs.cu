@@ -84,25 +84,70 @@ __device__ __forceinline__ void rescale(Stats &a, float m)
     a.m = m;
 }
 
+// The sums of n <= 32 parts, one a lane, in a fixed order.
+__device__ __forceinline__ Stats join(Stats a)
+{
+    float mx = a.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
+    rescale(a, mx);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a.s += __shfl_xor_sync(ALL, a.s, o);
+        a.t += __shfl_xor_sync(ALL, a.t, o);
+    }
+    return a;
+}
+
 // The row on the grid of 16-byte vectors: vector L holds elements L V - lead .. + V - 1, of which
-// the first and the last vector may have only some.
+// the first and the last vector may have only some (the others read as -inf).
 template <typename T>
 struct Row {
     const T *x;          // the row's first element
     int lead, v;
     __device__ __forceinline__ int vectors() const { return (lead + v + VEC<T> - 1) / VEC<T>; }
-    __device__ __forceinline__ void load(int L, float (&f)[VEC<T>]) const
+    __device__ __forceinline__ static uint4 none()
+    {
+        const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+        return make_uint4(w, w, w, w);
+    }
+    __device__ __forceinline__ uint4 load(int L) const
     {
         const int e0 = L * VEC<T> - lead;
-        if (e0 >= 0 && e0 + VEC<T> <= v) {
-            unpack<T>(__ldg(reinterpret_cast<const uint4 *>(x + e0)), f);
-        } else {
+        if (e0 >= 0 && e0 + VEC<T> <= v) return __ldg(reinterpret_cast<const uint4 *>(x + e0));
+        float f[VEC<T>];
 #pragma unroll
-            for (int j = 0; j < VEC<T>; ++j)
-                f[j] = e0 + j >= 0 && e0 + j < v ? to_f32(x[e0 + j]) : __int_as_float(0xff800000);
-        }
+        for (int j = 0; j < VEC<T>; ++j)
+            f[j] = e0 + j >= 0 && e0 + j < v ? to_f32(x[e0 + j]) : __int_as_float(0xff800000);
+        return pack<T>(f);
     }
 };
+
+// The largest element of U vectors (NaN ignored).
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 (&r)[U])
+{
+    float f[VEC<T>];
+    if constexpr (sizeof(T) == 4) {
+        float mx = __int_as_float(0xff800000);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            unpack<T>(r[u], f);
+            mx = fmaxf(mx, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+        }
+        return mx;
+    } else {
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        T2 mx = *reinterpret_cast<const T2 *>(&r[0].x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = __hmax2(mx, *reinterpret_cast<const T2 *>(&w[i]));
+        }
+        return fmaxf(to_f32(mx.x), to_f32(mx.y));
+    }
+}
 
 template <int W>
 struct Shared {
@@ -141,45 +186,55 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         x.v = v;
         const int64_t nv = x.vectors();
         const int L0 = (int)(nv * rank / CL), L1 = (int)(nv * (rank + 1) / CL);
-        int32_t token = -1;
+        // ---- the pass: a step's vectors are loaded while the step before it is summed ----
+        Stats st{LOWEST, 0.0f, 0.0f};
+        float2 sum = make_float2(0.0f, 0.0f), tsum = make_float2(0.0f, 0.0f);   // two partial sums each
+        int rose = 0;                      // the step in which this thread's maximum rose last
+        int step = 0;
+        uint4 next[U];
+        auto fetch = [&](int L) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) next[u] = L + u * THREADS < L1 ? x.load(L + u * THREADS) : Row<T>::none();
+        };
+        fetch(L0 + (int)threadIdx.x);
+        for (int L = L0 + (int)threadIdx.x; L < L1; L += U * THREADS, ++step) {
+            uint4 cur[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) cur[u] = next[u];
+            if (L + U * THREADS < L1) fetch(L + U * THREADS);
+            const float mx = largest<T>(cur);
+            if (mx > st.m) {
+                Stats lo{st.m, sum.x, tsum.x}, hi{st.m, sum.y, tsum.y};
+                rescale(lo, mx);
+                rescale(hi, mx);
+                sum = make_float2(lo.s, hi.s);
+                tsum = make_float2(lo.t, hi.t);
+                st.m = mx;
+                rose = step;
+            }
+            const float2 neg = make_float2(-st.m, -st.m);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[V];
+                unpack<T>(cur[u], f);
+#pragma unroll
+                for (int j = 0; j < V; j += 2) {
+                    const float2 z = __fadd2_rn(make_float2(f[j], f[j + 1]), neg);
+                    const float2 p = __fmul2_rn(z, make_float2(LOG2E, LOG2E));
+                    const float2 e = make_float2(ex2(p.x), ex2(p.y));
+                    sum = __fadd2_rn(sum, e);                     // a NaN or +inf makes it NaN
+                    // masked: 0 times a finite number
+                    tsum = __ffma2_rn(make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST)), e, tsum);
+                }
+            }
+        }
+        st.s = sum.x + sum.y;
+        st.t = tsum.x + tsum.y;
         float asked = 0.0f;
+        int32_t token = -1;
         if (a.tokens && threadIdx.x == 0 && rank == 0) {
             token = a.tokens[row];
             if (token >= 0 && token < v) asked = to_f32(x.x[token]);
-        }
-
-        // ---- the pass ----
-        Stats st{LOWEST, 0.0f, 0.0f};
-        int rose = 0;                      // the step in which this thread's maximum rose last
-        int step = 0;
-        for (int L = L0 + (int)threadIdx.x; L < L1; L += U * THREADS, ++step) {
-            float f[U][V];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (L + u * THREADS < L1) {
-                    x.load(L + u * THREADS, f[u]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) f[u][j] = ninf;
-                }
-            }
-            float mx = f[0][0];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < V; ++j) mx = fmaxf(mx, f[u][j]);
-            if (mx > st.m || (step == 0 && mx > ninf)) {
-                rescale(st, fmaxf(mx, st.m));
-                rose = step;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = f[u][j] - st.m, e = ex2(z * LOG2E);
-                    st.s += e;                                    // a NaN or +inf makes it NaN
-                    st.t = fmaf(fmaxf(z, LOWEST), e, st.t);       // masked: 0 times a finite number
-                }
         }
 
         // ---- a bound that `top` keys reach: in each warp, top / W of its threads' maxima ----
@@ -195,15 +250,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         }
         // ---- the CTA's sums ----
         const float own_m = st.m;
-        float mx = st.m;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
-        rescale(st, mx);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            st.s += __shfl_xor_sync(ALL, st.s, o);
-            st.t += __shfl_xor_sync(ALL, st.t, o);
-        }
+        st = join(st);
         if (lane == 0) sh.stats[warp] = st;
         __syncthreads();
 
@@ -221,9 +268,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                 const int i = i0 + lane;
                 const int L = i < total ? mine0 + (int)__fns(sel, 0, i / per_lane + 1) + i % per_lane * THREADS : L1;
                 float f[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = ninf;
-                if (L < L1) x.load(L, f);
+                unpack<T>(L < L1 ? x.load(L) : Row<T>::none(), f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const uint64_t k = key_of(f[j], (uint32_t)(L * V - x.lead + j));
@@ -236,20 +281,25 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
             __syncthreads();
         }
 
-        // ---- join the warps, then the cluster's CTAs ----
-        if (warp == 0) {
-            Stats all = sh.stats[0];
-            for (int w = 1; w < W; ++w) {
-                Stats o = sh.stats[w];
-                const float top_m = fmaxf(all.m, o.m);
-                rescale(all, top_m);
-                rescale(o, top_m);
-                all.s += o.s;
-                all.t += o.t;
-                if (a.top > 0) merge32(list, sh.list[w][lane], lane);
+        // ---- join the warps, then the cluster's CTAs: lists pairwise, warp w taking w + half ----
+        auto join_lists = [&](uint64_t (*lists)[32], int n) {
+            for (int half = n / 2; half; half >>= 1) {
+                if (warp < half) {
+                    merge32(list, lists[warp + half][lane], lane);
+                    lists[warp][lane] = list;
+                }
+                __syncthreads();
             }
-            if (CL > 1) {
-                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        };
+        if (a.top > 0) join_lists(sh.list, W);
+        Stats all{LOWEST, 0.0f, 0.0f};
+        if (warp == 0) {
+            if (lane < W) all = sh.stats[lane];
+            all = join(all);
+        }
+        if (CL > 1) {
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");       // rank 0 runs
+            if (warp == 0) {
                 if (a.top > 0)
                     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(&sh.part_list[rank][lane], 0)), "l"(list)
                                  : "memory");
@@ -259,21 +309,21 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(all.s) : "memory");
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(all.t) : "memory");
                 }
-                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-                if (rank == 0) {
-                    all = sh.part_stats[0];
-                    list = a.top > 0 ? sh.part_list[0][lane] : 0;
-                    for (int c = 1; c < CL; ++c) {
-                        Stats o = sh.part_stats[c];
-                        const float top_m = fmaxf(all.m, o.m);
-                        rescale(all, top_m);
-                        rescale(o, top_m);
-                        all.s += o.s;
-                        all.t += o.t;
-                        if (a.top > 0) merge32(list, sh.part_list[c][lane], lane);
-                    }
+            }
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if (rank == 0) {
+                if (a.top > 0) {
+                    if (warp < CL) list = sh.part_list[warp][lane];
+                    join_lists(sh.part_list, CL);
+                }
+                if (warp == 0) {
+                    all = Stats{LOWEST, 0.0f, 0.0f};
+                    if (lane < CL) all = sh.part_stats[lane];
+                    all = join(all);
                 }
             }
+        }
+        if (warp == 0) {
             if (rank == 0) {
                 const bool bad = !(all.s >= 0.0f), empty = all.s == 0.0f;
                 const float lse = logf(all.s), mxr = all.m;
@@ -287,9 +337,6 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                     a.top_logprobs[row * a.top + lane] = bad ? nan : list == 0 ? ninf : (value_of(list) - mxr) - lse;
                 }
             }
-        } else if (CL > 1) {
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         }
         __syncthreads();
     }
