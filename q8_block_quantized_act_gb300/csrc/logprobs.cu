@@ -20,6 +20,7 @@ namespace {
 constexpr unsigned ALL = 0xffffffffu;
 constexpr int U = 4;              // vectors in flight per thread
 constexpr int MAX_CL = 8;
+constexpr int CAP = 256;          // keys that the CTA's list holds
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 constexpr float LOWEST = -3.4028235e38f;
 
@@ -44,12 +45,13 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 // ---- lists of 32 keys, one a lane, largest first ----
-__device__ __forceinline__ void exchange(uint64_t &k, int o, bool larger)
+template <typename K>
+__device__ __forceinline__ void exchange(K &k, int o, bool larger)
 {
-    const uint64_t other = __shfl_xor_sync(ALL, k, o);
+    const K other = __shfl_xor_sync(ALL, k, o);
     k = (k > other) == larger ? k : other;
 }
-__device__ __forceinline__ void sort32(uint64_t &k, int lane)
+__device__ __forceinline__ void sort32(uint32_t &k, int lane)
 {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
@@ -152,8 +154,11 @@ __device__ __forceinline__ float largest(const uint4 (&r)[U])
 template <int W>
 struct Shared {
     uint64_t list[W][32];
+    uint64_t found[CAP];               // keys that reach the bound, in no order
     Stats stats[W];
-    uint64_t bound[W];
+    uint32_t bound[W];
+    int chosen[W * 32];                // threads whose maximum reaches it
+    int n_chosen, n_found;
     uint64_t part_list[MAX_CL][32];    // rank 0: every rank's list and sums
     Stats part_stats[MAX_CL];
 };
@@ -163,6 +168,18 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank)
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
+}
+
+// n (a power of two) lists to one, pairwise: warp w takes over list w + half.
+__device__ __forceinline__ void join_lists(uint64_t (*lists)[32], int n, uint64_t &list, int warp, int lane)
+{
+    for (int half = n / 2; half; half >>= 1) {
+        if (warp < half) {
+            merge32(list, lists[warp + half][lane], lane);
+            lists[warp][lane] = list;
+        }
+        __syncthreads();
+    }
 }
 
 template <typename T, int THREADS>
@@ -177,6 +194,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA runs
     }
+    if (threadIdx.x == 0) sh.n_chosen = sh.n_found = 0;
     griddep_enter();
     // CL > 1: one row per cluster (the grid holds them all)
     for (int64_t row = blockIdx.x / CL; row < m; row += gridDim.x / CL) {
@@ -189,15 +207,13 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         // ---- the pass: a step's vectors are loaded while the step before it is summed ----
         Stats st{LOWEST, 0.0f, 0.0f};
         float2 sum = make_float2(0.0f, 0.0f), tsum = make_float2(0.0f, 0.0f);   // two partial sums each
-        int rose = 0;                      // the step in which this thread's maximum rose last
-        int step = 0;
         uint4 next[U];
         auto fetch = [&](int L) {
 #pragma unroll
             for (int u = 0; u < U; ++u) next[u] = L + u * THREADS < L1 ? x.load(L + u * THREADS) : Row<T>::none();
         };
         fetch(L0 + (int)threadIdx.x);
-        for (int L = L0 + (int)threadIdx.x; L < L1; L += U * THREADS, ++step) {
+        for (int L = L0 + (int)threadIdx.x; L < L1; L += U * THREADS) {
             uint4 cur[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) cur[u] = next[u];
@@ -210,7 +226,6 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                 sum = make_float2(lo.s, hi.s);
                 tsum = make_float2(lo.t, hi.t);
                 st.m = mx;
-                rose = step;
             }
             const float2 neg = make_float2(-st.m, -st.m);
 #pragma unroll
@@ -237,61 +252,89 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
             if (token >= 0 && token < v) asked = to_f32(x.x[token]);
         }
 
-        // ---- a bound that `top` keys reach: in each warp, top / W of its threads' maxima ----
-        const bool live = st.s > 0.0f;
-        uint64_t thr = 0;
+        // ---- a bound that `top` logits reach: in each warp, top / W of its threads' maxima do ----
+        const uint32_t own = st.s > 0.0f ? order_of(st.m) : 0;      // 0: nothing but masked logits
         if (a.top > 0) {
-            // no smaller than the index of the element that holds the maximum
-            const int64_t last = ((int64_t)L0 + threadIdx.x + ((int64_t)rose * U + U) * THREADS) * V;
-            uint64_t k = live ? key_of(st.m, (uint32_t)(last < v ? last : v)) : 0;
+            uint32_t k = own;
             sort32(k, lane);
-            const int per = (a.top + W - 1) / W;
-            if (lane == per - 1) sh.bound[warp] = k;
+            if (lane == (a.top + W - 1) / W - 1) sh.bound[warp] = k;
         }
-        // ---- the CTA's sums ----
-        const float own_m = st.m;
         st = join(st);
         if (lane == 0) sh.stats[warp] = st;
         __syncthreads();
 
-        // ---- the alternatives: the warp's list of the keys that reach the bound ----
+        // ---- the alternatives ----
         uint64_t list = 0;
         if (a.top > 0) {
-            thr = sh.bound[0];
+            uint32_t thr = sh.bound[0];
 #pragma unroll
-            for (int w = 1; w < W; ++w) thr = sh.bound[w] < thr ? sh.bound[w] : thr;
-            unsigned sel = __ballot_sync(ALL, live && order_of(own_m) >= (uint32_t)(thr >> 32));
-            const int mine0 = L0 + warp * 32;                         // lane 0's first vector
-            const int per_lane = mine0 < L1 ? (L1 - mine0 + THREADS - 1) / THREADS : 0;
-            const int total = __popc(sel) * per_lane;
-            for (int i0 = 0; i0 < total; i0 += 32) {
-                const int i = i0 + lane;
-                const int L = i < total ? mine0 + (int)__fns(sel, 0, i / per_lane + 1) + i % per_lane * THREADS : L1;
-                float f[V];
-                unpack<T>(L < L1 ? x.load(L) : Row<T>::none(), f);
+            for (int w = 1; w < W; ++w) thr = min(thr, sh.bound[w]);
+            thr = max(thr, 1u);
+            const float least = thr > 1u ? value_of((uint64_t)thr << 32) : LOWEST;
+            const unsigned sel = __ballot_sync(ALL, own >= thr);
+            if (sel) {
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&sh.n_chosen, __popc(sel));
+                at = __shfl_sync(ALL, at, 0);
+                if (own >= thr) sh.chosen[at + __popc(sel & ((1u << lane) - 1))] = threadIdx.x;
+            }
+            sh.list[warp][lane] = 0;
+            __syncthreads();
+            const int each = (L1 - L0 + THREADS - 1) / THREADS;     // a thread's vectors, one less for some
+            const int total = sh.n_chosen * each;
+            for (int i0 = threadIdx.x; i0 < total; i0 += U * THREADS) {
+                uint4 r[U];
+                int at[U];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const uint64_t k = key_of(f[j], (uint32_t)(L * V - x.lead + j));
-                    const uint64_t worst = __shfl_sync(ALL, list, a.top - 1);
-                    unsigned some = __ballot_sync(ALL, f[j] > ninf && k >= thr && k > worst);
-                    for (; some; some &= some - 1) insert32(list, __shfl_sync(ALL, k, __ffs(some) - 1), lane);
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * THREADS;
+                    at[u] = i < total ? L0 + sh.chosen[i / each] + i % each * THREADS : L1;
+                    r[u] = at[u] < L1 ? x.load(at[u]) : Row<T>::none();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[V];
+                    unpack<T>(r[u], f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (f[j] >= least) {
+                            const int n = atomicAdd(&sh.n_found, 1);
+                            if (n < CAP) sh.found[n] = key_of(f[j], (uint32_t)(at[u] * V - x.lead + j));
+                        }
                 }
             }
-            sh.list[warp][lane] = list;
             __syncthreads();
-        }
-
-        // ---- join the warps, then the cluster's CTAs: lists pairwise, warp w taking w + half ----
-        auto join_lists = [&](uint64_t (*lists)[32], int n) {
-            for (int half = n / 2; half; half >>= 1) {
-                if (warp < half) {
-                    merge32(list, lists[warp + half][lane], lane);
-                    lists[warp][lane] = list;
+            const int n = sh.n_found;
+            if (n <= CAP) {
+                // A key's place is the number of larger ones; the keys differ, so places do.
+                if ((int)threadIdx.x < n) {
+                    const uint64_t k = sh.found[threadIdx.x];
+                    int place = 0;
+                    for (int i = 0; i < n; ++i) place += sh.found[i] > k;
+                    if (place < 32) sh.list[0][place] = k;
                 }
                 __syncthreads();
+                list = sh.list[0][lane];
+            } else {
+                const int mine0 = L0 + warp * 32;                     // this warp's vectors, 32 at a time
+                for (int L = mine0 + lane; L - lane < L1; L += THREADS) {
+                    float f[V];
+                    unpack<T>(L < L1 ? x.load(L) : Row<T>::none(), f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const uint64_t k = key_of(f[j], (uint32_t)(L * V - x.lead + j));
+                        const uint64_t worst = __shfl_sync(ALL, list, a.top - 1);
+                        unsigned some = __ballot_sync(ALL, f[j] >= least && k > worst);
+                        for (; some; some &= some - 1) insert32(list, __shfl_sync(ALL, k, __ffs(some) - 1), lane);
+                    }
+                }
+                sh.list[warp][lane] = list;
+                __syncthreads();
+                join_lists(sh.list, W, list, warp, lane);
             }
-        };
-        if (a.top > 0) join_lists(sh.list, W);
+        }
+
+        // ---- join the warps' sums, then the cluster's parts ----
         Stats all{LOWEST, 0.0f, 0.0f};
         if (warp == 0) {
             if (lane < W) all = sh.stats[lane];
@@ -314,7 +357,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
             if (rank == 0) {
                 if (a.top > 0) {
                     if (warp < CL) list = sh.part_list[warp][lane];
-                    join_lists(sh.part_list, CL);
+                    join_lists(sh.part_list, CL, list, warp, lane);
                 }
                 if (warp == 0) {
                     all = Stats{LOWEST, 0.0f, 0.0f};
@@ -338,6 +381,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                 }
             }
         }
+        if (threadIdx.x == 0) sh.n_chosen = sh.n_found = 0;       // read by everyone before the last barrier
         __syncthreads();
     }
 }
