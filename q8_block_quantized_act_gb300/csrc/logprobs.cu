@@ -21,6 +21,8 @@ constexpr unsigned ALL = 0xffffffffu;
 constexpr int U = 4;              // vectors in flight per thread
 constexpr int MAX_CL = 8;
 constexpr int CAP = 256;          // keys that the CTA's list holds
+constexpr int MAX_J = 8;
+constexpr int SLOTS = 16;         // maxima kept of each thread's steps
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 constexpr float LOWEST = -3.4028235e38f;
 
@@ -37,26 +39,20 @@ __device__ __forceinline__ float value_of(uint64_t key)
     return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
 
+// 2^x, results below the normal numbers as 0 (they count nothing against a sum of 1 at least;
+// keeping them takes three more instructions for each element).
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
 // ---- lists of 32 keys, one a lane, largest first ----
-template <typename K>
-__device__ __forceinline__ void exchange(K &k, int o, bool larger)
+__device__ __forceinline__ void exchange(uint64_t &k, int o, bool larger)
 {
-    const K other = __shfl_xor_sync(ALL, k, o);
+    const uint64_t other = __shfl_xor_sync(ALL, k, o);
     k = (k > other) == larger ? k : other;
-}
-__device__ __forceinline__ void sort32(uint32_t &k, int lane)
-{
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int o = size / 2; o; o >>= 1) exchange(k, o, ((lane & o) == 0) == ((lane & size) == 0));
 }
 // The 32 largest of two lists (a bitonic sequence, then its five half-cleaners).
 __device__ __forceinline__ void merge32(uint64_t &k, uint64_t other, int lane)
@@ -101,29 +97,13 @@ __device__ __forceinline__ Stats join(Stats a)
     return a;
 }
 
-// The row on the grid of 16-byte vectors: vector L holds elements L V - lead .. + V - 1, of which
-// the first and the last vector may have only some (the others read as -inf).
+// A vector of masked logits.
 template <typename T>
-struct Row {
-    const T *x;          // the row's first element
-    int lead, v;
-    __device__ __forceinline__ int vectors() const { return (lead + v + VEC<T> - 1) / VEC<T>; }
-    __device__ __forceinline__ static uint4 none()
-    {
-        const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-        return make_uint4(w, w, w, w);
-    }
-    __device__ __forceinline__ uint4 load(int L) const
-    {
-        const int e0 = L * VEC<T> - lead;
-        if (e0 >= 0 && e0 + VEC<T> <= v) return __ldg(reinterpret_cast<const uint4 *>(x + e0));
-        float f[VEC<T>];
-#pragma unroll
-        for (int j = 0; j < VEC<T>; ++j)
-            f[j] = e0 + j >= 0 && e0 + j < v ? to_f32(x[e0 + j]) : __int_as_float(0xff800000);
-        return pack<T>(f);
-    }
-};
+__device__ __forceinline__ uint4 none()
+{
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
 
 // The largest element of U vectors (NaN ignored).
 template <typename T>
@@ -156,8 +136,9 @@ struct Shared {
     uint64_t list[W][32];
     uint64_t found[CAP];               // keys that reach the bound, in no order
     Stats stats[W];
-    uint32_t bound[W];
-    int chosen[W * 32];                // threads whose maximum reaches it
+    float slot[SLOTS][W * 32];         // each thread's maxima
+    int chosen[SLOTS * W * 32];        // (thread, slot) pairs whose maximum reaches the bound
+    uint32_t best[W * MAX_J];          // each warp's J largest thread maxima
     int n_chosen, n_found;
     uint64_t part_list[MAX_CL][32];    // rank 0: every rank's list and sums
     Stats part_stats[MAX_CL];
@@ -183,7 +164,7 @@ __device__ __forceinline__ void join_lists(uint64_t (*lists)[32], int n, uint64_
 }
 
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_t m, int v, int CL)
+__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int64_t m, int v, int CL)
 {
     constexpr int V = VEC<T>, W = THREADS / 32;
     __shared__ Shared<W> sh;
@@ -198,27 +179,53 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
     griddep_enter();
     // CL > 1: one row per cluster (the grid holds them all)
     for (int64_t row = blockIdx.x / CL; row < m; row += gridDim.x / CL) {
-        Row<T> x;
-        x.x = static_cast<const T *>(a.logits) + row * a.ld;
-        x.lead = (int)((reinterpret_cast<uintptr_t>(x.x) & 15u) / sizeof(T));
-        x.v = v;
-        const int64_t nv = x.vectors();
-        const int L0 = (int)(nv * rank / CL), L1 = (int)(nv * (rank + 1) / CL);
+        const T *x = static_cast<const T *>(a.logits) + row * a.ld;
+        // The row's whole 16-byte vectors, of which this CTA has [L0, L1); up to V - 1 elements at
+        // either end are left over (edges), one for each of rank 0's first threads.
+        const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+        const int head = lead ? min(V - lead, v) : 0, whole = (v - head) / V, tail = v - head - whole * V;
+        const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
+        const int L0 = (int)((int64_t)whole * rank / CL), L1 = (int)((int64_t)whole * (rank + 1) / CL);
+
         // ---- the pass: a step's vectors are loaded while the step before it is summed ----
         Stats st{LOWEST, 0.0f, 0.0f};
         float2 sum = make_float2(0.0f, 0.0f), tsum = make_float2(0.0f, 0.0f);   // two partial sums each
         uint4 next[U];
-        auto fetch = [&](int L) {
+        constexpr int STEP = U * THREADS;                            // vectors of a step
+        auto fetch = [&](int base) {
+            const int L = base + (int)threadIdx.x;
+            if (base + STEP <= L1) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) next[u] = L + u * THREADS < L1 ? x.load(L + u * THREADS) : Row<T>::none();
+                for (int u = 0; u < U; ++u) next[u] = __ldg(vec + L + u * THREADS);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) next[u] = L + u * THREADS < L1 ? __ldg(vec + L + u * THREADS) : none<T>();
+            }
         };
-        fetch(L0 + (int)threadIdx.x);
-        for (int L = L0 + (int)threadIdx.x; L < L1; L += U * THREADS) {
+        fetch(L0);
+        float edge = ninf;                                           // its element is edge_at
+        const int edge_at = (int)threadIdx.x < head ? (int)threadIdx.x : v - tail + (int)threadIdx.x - head;
+        if (rank == 0 && (int)threadIdx.x < head + tail) {
+            edge = to_f32(x[edge_at]);
+            st = edge > ninf ? Stats{edge, 1.0f, 0.0f} : st;
+            if (!(edge < __int_as_float(0x7f800000))) st.s = nan;
+            sum.x = st.s;
+        }
+        const int steps = (L1 - L0 + STEP - 1) / STEP, per_slot = (steps + SLOTS - 1) / SLOTS;
+        int left = per_slot, slots = 0;
+        float slot_max = ninf;
+        for (int step = 0; step < steps; ++step) {
             uint4 cur[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) cur[u] = next[u];
-            if (L + U * THREADS < L1) fetch(L + U * THREADS);
+            if (step + 1 < steps) fetch(L0 + (step + 1) * STEP);
             const float mx = largest<T>(cur);
+            slot_max = fmaxf(slot_max, mx);
+            if (--left == 0 || step + 1 == steps) {
+                sh.slot[slots++][threadIdx.x] = slot_max;
+                slot_max = ninf;
+                left = per_slot;
+            }
             if (mx > st.m) {
                 Stats lo{st.m, sum.x, tsum.x}, hi{st.m, sum.y, tsum.y};
                 rescale(lo, mx);
@@ -249,15 +256,22 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         int32_t token = -1;
         if (a.tokens && threadIdx.x == 0 && rank == 0) {
             token = a.tokens[row];
-            if (token >= 0 && token < v) asked = to_f32(x.x[token]);
+            if (token >= 0 && token < v) asked = to_f32(x[token]);
         }
 
-        // ---- a bound that `top` logits reach: in each warp, top / W of its threads' maxima do ----
+        // ---- a bound that `top` logits reach: the top-th of the warps' J largest thread maxima ----
         const uint32_t own = st.s > 0.0f ? order_of(st.m) : 0;      // 0: nothing but masked logits
+        const int J = min((a.top + W - 1) / W + 2, MAX_J);
         if (a.top > 0) {
             uint32_t k = own;
-            sort32(k, lane);
-            if (lane == (a.top + W - 1) / W - 1) sh.bound[warp] = k;
+#pragma unroll 1
+            for (int i = 0; i < J; ++i) {
+                const uint32_t best = __reduce_max_sync(ALL, k);
+                if (lane == __ffs(__ballot_sync(ALL, k == best)) - 1) {
+                    sh.best[warp * J + i] = best;
+                    k = 0;
+                }
+            }
         }
         st = join(st);
         if (lane == 0) sh.stats[warp] = st;
@@ -266,42 +280,72 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
         // ---- the alternatives ----
         uint64_t list = 0;
         if (a.top > 0) {
-            uint32_t thr = sh.bound[0];
+            // every warp ranks the W J <= 64 values, two a lane, equal ones by their place
+            uint32_t mine[2] = {0, 0};
+            int place[2] = {0, 0};
 #pragma unroll
-            for (int w = 1; w < W; ++w) thr = min(thr, sh.bound[w]);
+            for (int h = 0; h < 2; ++h)
+                if (lane + 32 * h < W * J) mine[h] = sh.best[lane + 32 * h];
+#pragma unroll 8
+            for (int i = 0; i < W * J; ++i) {
+                const uint32_t other = sh.best[i];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) place[h] += other > mine[h] || (other == mine[h] && i < lane + 32 * h);
+            }
+            uint32_t thr = __reduce_max_sync(ALL, place[0] == a.top - 1 ? mine[0] : place[1] == a.top - 1 ? mine[1] : 0u);
             thr = max(thr, 1u);
             const float least = thr > 1u ? value_of((uint64_t)thr << 32) : LOWEST;
-            const unsigned sel = __ballot_sync(ALL, own >= thr);
-            if (sel) {
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&sh.n_chosen, __popc(sel));
-                at = __shfl_sync(ALL, at, 0);
-                if (own >= thr) sh.chosen[at + __popc(sel & ((1u << lane) - 1))] = threadIdx.x;
-            }
             sh.list[warp][lane] = 0;
+            uint32_t reach = 0;
+            if (own >= thr) {
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (i < slots) reach |= (sh.slot[i][threadIdx.x] >= least ? 1u : 0u) << i;
+                if (edge >= least) {
+                    const int n = atomicAdd(&sh.n_found, 1);
+                    if (n < CAP) sh.found[n] = key_of(edge, (uint32_t)edge_at);
+                }
+            }
+            if (__any_sync(ALL, reach != 0)) {
+                int upto = __popc(reach);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int below = __shfl_up_sync(ALL, upto, o);
+                    if (lane >= o) upto += below;
+                }
+                int at = 0;
+                if (lane == 31) at = atomicAdd(&sh.n_chosen, upto);
+                at = __shfl_sync(ALL, at, 31) + upto - __popc(reach);
+                for (; reach; reach &= reach - 1) sh.chosen[at++] = (int)threadIdx.x * SLOTS + __ffs(reach) - 1;
+            }
             __syncthreads();
-            const int each = (L1 - L0 + THREADS - 1) / THREADS;     // a thread's vectors, one less for some
-            const int total = sh.n_chosen * each;
-            for (int i0 = threadIdx.x; i0 < total; i0 += U * THREADS) {
-                uint4 r[U];
-                int at[U];
+            // Each warp reads the U V elements of a chosen thread's step, one a lane (f32: two
+            // steps at once), several in flight.
+            constexpr int LANES = U * V, AT_ONCE = 32 / LANES, DEPTH = 8 / AT_ONCE;
+            const int total = sh.n_chosen * per_slot;
+#pragma unroll 1
+            for (int i0 = warp * AT_ONCE + lane / LANES; i0 - lane / LANES < total; i0 += W * AT_ONCE * DEPTH) {
+                float f[DEPTH];
+                int at[DEPTH];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * THREADS;
-                    at[u] = i < total ? L0 + sh.chosen[i / each] + i % each * THREADS : L1;
-                    r[u] = at[u] < L1 ? x.load(at[u]) : Row<T>::none();
+                for (int d = 0; d < DEPTH; ++d) {
+                    const int i = i0 + d * W * AT_ONCE;
+                    f[d] = ninf;
+                    at[d] = 0;
+                    if (i < total) {
+                        const int pair = sh.chosen[i / per_slot];
+                        const int step = pair % SLOTS * per_slot + i % per_slot;
+                        const int L = L0 + step * STEP + pair / SLOTS + lane % LANES / V * THREADS;
+                        at[d] = head + L * V + lane % V;
+                        if (L < L1) f[d] = to_f32(x[at[d]]);
+                    }
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[V];
-                    unpack<T>(r[u], f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (f[j] >= least) {
-                            const int n = atomicAdd(&sh.n_found, 1);
-                            if (n < CAP) sh.found[n] = key_of(f[j], (uint32_t)(at[u] * V - x.lead + j));
-                        }
-                }
+                for (int d = 0; d < DEPTH; ++d)
+                    if (f[d] >= least) {
+                        const int n = atomicAdd(&sh.n_found, 1);
+                        if (n < CAP) sh.found[n] = key_of(f[d], (uint32_t)at[d]);
+                    }
             }
             __syncthreads();
             const int n = sh.n_found;
@@ -310,24 +354,26 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobArgs a, int64_
                 if ((int)threadIdx.x < n) {
                     const uint64_t k = sh.found[threadIdx.x];
                     int place = 0;
-                    for (int i = 0; i < n; ++i) place += sh.found[i] > k;
+#pragma unroll 1
+                    for (int i = 0; i < n; i += 8)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) place += i + j < n && sh.found[i + j] > k;
                     if (place < 32) sh.list[0][place] = k;
                 }
                 __syncthreads();
                 list = sh.list[0][lane];
             } else {
-                const int mine0 = L0 + warp * 32;                     // this warp's vectors, 32 at a time
-                for (int L = mine0 + lane; L - lane < L1; L += THREADS) {
-                    float f[V];
-                    unpack<T>(L < L1 ? x.load(L) : Row<T>::none(), f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const uint64_t k = key_of(f[j], (uint32_t)(L * V - x.lead + j));
-                        const uint64_t worst = __shfl_sync(ALL, list, a.top - 1);
-                        unsigned some = __ballot_sync(ALL, f[j] >= least && k > worst);
-                        for (; some; some &= some - 1) insert32(list, __shfl_sync(ALL, k, __ffs(some) - 1), lane);
-                    }
-                }
+                auto offer = [&](float f, int at) {
+                    const uint64_t k = key_of(f, (uint32_t)at);
+                    const uint64_t worst = __shfl_sync(ALL, list, a.top - 1);
+                    unsigned some = __ballot_sync(ALL, f >= least && k > worst);
+                    for (; some; some &= some - 1) insert32(list, __shfl_sync(ALL, k, __ffs(some) - 1), lane);
+                };
+                if (warp == 0) offer(edge, edge_at);
+                const int e1 = head + L1 * V;
+#pragma unroll 1
+                for (int e = head + L0 * V + warp * 32; e < e1; e += THREADS)
+                    offer(e + lane < e1 ? to_f32(x[e + lane]) : ninf, e + lane);
                 sh.list[warp][lane] = list;
                 __syncthreads();
                 join_lists(sh.list, W, list, warp, lane);
