@@ -45,7 +45,7 @@ struct Cfg {
     static constexpr int OFF_SB = OFF_SA + STAGES * SC_BYTES;
     static constexpr int OFF_RED = OFF_SB + STAGES * NSB * SC_BYTES;
     static constexpr int OFF_BAR = OFF_RED + (SPLIT ? BN * BM * 4 : 0);
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4 + 2) * 8;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4 + 3) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;   // + slack for 1024-byte base alignment
     // Tensor memory: two accumulators, then two slots of scales (weights 8 columns, tokens 8 per
     // scale tile), so that a step's copies do not wait for the previous step's MMAs.
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + STAGES, *acc_full = empty + STAGES, *acc_empty = acc_full + 2;
-    uint64_t *red_full = acc_empty + 2, *red_empty = red_full + 1;
+    uint64_t *red_full = acc_empty + 2, *red_empty = red_full + 1, *drained = red_empty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int s = 0; s < 2; ++s) { mbar_init(&acc_full[s], 1); mbar_init(&acc_empty[s], 4); }
         mbar_init(red_full, 4 * CL);
         mbar_init(red_empty, 4 * CL);
+        mbar_init(drained, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -180,80 +181,93 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 4) {
         // ------------------------------ producer ------------------------------
-        if (lane == 0) {
-            auto load_w = [&](int it, int tile, int ks) {
-                const int st = it % STAGES;
-                const int rt = tile / wk.token_tiles;
-                tma_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, rt * BM, &full[st]);
-                bulk_g2s(smem + C::OFF_SA + st * SC_BYTES,
-                         wsc + ((int64_t)rt * ktiles + ks * (BK / MX_TILE_K)) * MX_TILE_BYTES, SC_BYTES, &full[st]);
-            };
-            const int last_sb = (wk.m + MX_TILE_ROWS - 1) / MX_TILE_ROWS;    // scale tiles of the tokens
-            auto first_sb = [&](int tile) { return tile % wk.token_tiles * BN / MX_TILE_ROWS; };
-            auto count_sb = [&](int tile) { return min(NSB, last_sb - first_sb(tile)); };
-            auto load_x = [&](int it, int tile, int ks) {
-                const int st = it % STAGES;
-                tma_load_2d(smem + C::OFF_B + st * B_BYTES, &tm_x, ks * ROW_BYTES, tile % wk.token_tiles * BN, &full[st]);
-                for (int i = 0; i < count_sb(tile); ++i)
-                    bulk_g2s(smem + C::OFF_SB + (st * NSB + i) * SC_BYTES,
-                             xsc + ((int64_t)(first_sb(tile) + i) * ktiles + ks * (BK / MX_TILE_K)) * MX_TILE_BYTES,
-                             SC_BYTES, &full[st]);
-            };
-            auto expect = [&](int it, int tile) {
-                mbar_arrive_expect_tx(&full[it % STAGES], A_BYTES + B_BYTES + SC_BYTES * (1 + count_sb(tile)));
-            };
-            // The first stages' weights before the wait for the previous kernel, which in a fused
-            // call is the activation's quantizer and does not write them.
-            if (wk.first_wait) griddep_wait();
-            int early = 0;
-            for (int tile = cluster; tile < wk.tiles && early < STAGES; tile += clusters)
-                for (int ks = ks0; ks < ks1 && early < STAGES; ++ks, ++early) {
-                    expect(early, tile);
-                    load_w(early, tile, ks);
-                }
-            if (!wk.first_wait) griddep_wait();
-            griddep_launch_dependents();
-            int it = 0;
-            bool ok = true;
-            for (int tile = cluster; ok && tile < wk.tiles; tile += clusters)
-                for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                    if (it >= early) {
-                        if (!wait_or_abort(&empty[it % STAGES], ((it / STAGES) & 1) ^ 1, status, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        expect(it, tile);
-                        load_w(it, tile, ks);
-                    }
-                    load_x(it, tile, ks);
-                }
-            // Never leave with a copy into this CTA's shared memory in flight.
-            for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-                mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1, status);
+        // Everything that a tile fixes is computed once per tile: this thread's issue latency
+        // paces the pipeline, and a division costs as much as several of its copies.
+        const int last_sb = (wk.m + MX_TILE_ROWS - 1) / MX_TILE_ROWS;    // scale tiles of the tokens
+        const int64_t sc_tile = (int64_t)ktiles * MX_TILE_BYTES;         // bytes of 128 rows' scales
+        int row0, tok0, nsb;
+        const uint8_t *wsp, *xsp;
+        uint32_t bytes;
+        auto enter = [&](int tile) {
+            const int rt = tile / wk.token_tiles, tt = tile - rt * wk.token_tiles;
+            const int sb0 = tt * BN / MX_TILE_ROWS;
+            row0 = rt * BM;
+            tok0 = tt * BN;
+            nsb = min(NSB, last_sb - sb0);
+            wsp = wsc + rt * sc_tile + ks0 * SC_BYTES;
+            xsp = xsc + sb0 * sc_tile + ks0 * SC_BYTES;
+            bytes = A_BYTES + B_BYTES + SC_BYTES * (1 + nsb);
+        };
+        auto load_w = [&](int st, int ks) {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            tma_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, row0, &full[st]);
+            bulk_g2s(smem + C::OFF_SA + st * SC_BYTES, wsp, SC_BYTES, &full[st]);
+        };
+        auto load_x = [&](int st, int ks) {
+            tma_load_2d(smem + C::OFF_B + st * B_BYTES, &tm_x, ks * ROW_BYTES, tok0, &full[st]);
+            bulk_g2s(smem + C::OFF_SB + st * NSB * SC_BYTES, xsp, SC_BYTES, &full[st]);
+            if (NSB > 1 && nsb > 1) bulk_g2s(smem + C::OFF_SB + (st * NSB + 1) * SC_BYTES, xsp + sc_tile, SC_BYTES, &full[st]);
+        };
+        // The first stages' weights before the wait for the previous kernel, which in a fused
+        // call is the activation's quantizer and does not write them.
+        if (wk.first_wait) griddep_wait();
+        int early = 0;
+        for (int tile = cluster; tile < wk.tiles && early < STAGES; tile += clusters) {
+            enter(tile);
+            for (int ks = ks0; ks < ks1 && early < STAGES; ++ks, ++early) {
+                if (elect_one()) load_w(early, ks);
+                wsp += SC_BYTES;
+            }
         }
+        if (!wk.first_wait) griddep_wait();
+        griddep_launch_dependents();
+        int it = 0, st = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int tile = cluster; ok && tile < wk.tiles; tile += clusters) {
+            enter(tile);
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                if (it >= early) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], phase, status, abort_flag));
+                    if (!ok) break;
+                }
+                if (elect_one()) {
+                    if (it >= early) load_w(st, ks);
+                    load_x(st, ks);
+                }
+                wsp += SC_BYTES;
+                xsp += SC_BYTES;
+                if (++st == STAGES) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // Never leave with a copy into this CTA's shared memory in flight.
+        for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+            mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1, status);
     } else if (warp == 5) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
-            const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_A));
-            const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
-            const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
-            const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SB));
-            int it = 0, i = 0;
-            bool ok = true;
-            for (int tile = cluster; ok && tile < wk.tiles; tile += clusters, ++i) {
-                const int acc = i & 1;
-                if (!wait_or_abort(&acc_empty[acc], ((i >> 1) & 1) ^ 1, status, abort_flag)) break;
-                const uint32_t d_tmem = tmem + acc * BN;
-                // the first of the tile's tokens within its 128-row scale tile: a column for each 32
-                const uint32_t sb_shift = (uint32_t)(tile % wk.token_tiles * BN % MX_TILE_ROWS / 32);
-                for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                    const int st = it % STAGES;
-                    if (!wait_or_abort(&full[st], (it / STAGES) & 1, status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = tmem + C::COL_SC + (it & 1) * C::SC_COLS, sb = sa + 8;
+        const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_A));
+        const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
+        const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
+        const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SB));
+        int it = 0, st = 0, i = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = cluster; ok && tile < wk.tiles; tile += clusters, ++i) {
+            const int acc = i & 1;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&acc_empty[acc], ((i >> 1) & 1) ^ 1, status, abort_flag));
+            if (!ok) break;
+            const uint32_t d_tmem = tmem + acc * BN;
+            // the first of the tile's tokens within its 128-row scale tile: a column for each 32
+            const uint32_t sb_shift = (uint32_t)(tile % wk.token_tiles * BN % MX_TILE_ROWS / 32);
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], phase, status, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sa = tmem + C::COL_SC + (it & 1) * C::SC_COLS, sb = sa + 8;
+                if (elect_one()) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {        // the step's two groups of 128 values
                         tc_copy_scales(sa + 4 * g, sadesc0 + (uint64_t)((st * SC_BYTES + g * MX_TILE_BYTES) >> 4));
@@ -271,13 +285,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     sb + 4 * NSB * (j >> 1) + sb_shift, ks > ks0 || j > 0);
                     }
                     tc_commit(&empty[st]);
+                    if (ks == ks1 - 1) tc_commit(&acc_full[acc]);
                 }
-                tc_commit(&acc_full[acc]);
+                if (++st == STAGES) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
-            // The last accumulators' phases complete once every MMA has: wait for them, so that
-            // tensor memory is not freed under an MMA (a commit is an arrival after all of them).
-            for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait_drain(&acc_full[j & 1], (j >> 1) & 1, status);
         }
+        // Tensor memory is not freed under an MMA: a last commit arrives after all of them.
+        if (elect_one()) tc_commit(drained);
+        mbar_wait_drain(drained, 0, status);
     } else {
         // ------------------------------ epilogue ------------------------------
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t r = (int64_t)(tile / wk.token_tiles) * BM + row;
             const int tok0 = tile % wk.token_tiles * BN;
             const int cols = min(BN, wk.m - tok0);
-            if (!wait_or_abort(&acc_full[acc], (i >> 1) & 1, status, abort_flag)) break;
+            if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[acc], (i >> 1) & 1, status, abort_flag))) break;
             tc_fence_after();
             T *dst = y + (int64_t)tok0 * wk.n + r;
             if (CL == 1) {
@@ -307,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&acc_empty[acc]);
             } else if constexpr (C::SPLIT) {
                 const int per = BN / CL;                                // columns that a rank owns
-                if (!wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag)) break;
+                if (!__all_sync(0xffffffffu, wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag))) break;
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
                     uint32_t v[16];
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive(&acc_empty[acc]);
                     for (int c = 0; c < CL; ++c) cluster_arrive(cluster_addr(smem_u32(red_full), c));
                 }
-                if (!wait_cluster(red_full, i & 1, status, abort_flag)) break;
+                if (!__all_sync(0xffffffffu, wait_cluster(red_full, i & 1, status, abort_flag))) break;
                 const int own0 = (int)rank * per;
                 for (int c = 0; c < per && own0 + c < cols; ++c) {
                     float s = red[c * BM + row];

@@ -27,6 +27,21 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar)
         : "memory");
 }
 
+// One lane of a converged warp, the same one each time.  The tcgen05 and TMA instructions take
+// their operands from uniform registers: a warp that runs its loop as a whole and elects a lane
+// around them only keeps descriptors and addresses there, where a loop under `lane == 0` moves each
+// operand over before each instruction (measured: about 65 cycles an instruction).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // Tensor memory: a warp allocates `cols` columns (a power of two, 32 at least) and gives up the
 // right to allocate more; the address is written to *slot.
 __device__ __forceinline__ void tc_alloc(uint32_t *slot, uint32_t cols)
