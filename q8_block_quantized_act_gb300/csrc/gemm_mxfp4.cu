@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Warp-uniform to the compiler too: the roles' loops then live in uniform registers.
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CL > 1 ? cluster_rank() : 0;
     const int cluster = blockIdx.x / CL, clusters = gridDim.x / CL;
     const int ks0 = wk.steps * (int)rank / CL, ks1 = wk.steps * ((int)rank + 1) / CL;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (CL > 1) cluster_sync_all();         // every rank's barriers exist before anyone arrives on them
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == 4) {
         // ------------------------------ producer ------------------------------
