@@ -253,45 +253,58 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
         const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
         const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SB));
-        int it = 0, st = 0, i = 0;
+        // Steps go in pairs where the second one's data is there: the tensor pipe runs copies and
+        // MMAs in order and pays for each change between them.
+        auto copy_scales = [&](int slot, int st) {
+            const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {        // the step's two groups of 128 values
+                tc_copy_scales(sa + 4 * g, sadesc0 + (uint64_t)((st * SC_BYTES + g * MX_TILE_BYTES) >> 4));
+#pragma unroll
+                for (int b = 0; b < NSB; ++b)
+                    tc_copy_scales(sb + 4 * (NSB * g + b),
+                                   sbdesc0 + (uint64_t)(((st * NSB + b) * SC_BYTES + g * MX_TILE_BYTES) >> 4));
+            }
+        };
+        auto multiply = [&](int slot, int st, uint32_t d_tmem, uint32_t sb_shift, bool first) {
+            const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8 + sb_shift;
+            const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
+            const uint64_t bd = bdesc0 + (uint64_t)(st * (B_BYTES >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {        // 64 values: bytes 2 (j % 2) and next of each scale word
+                const uint32_t id = C::IDESC | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
+                tc_mma_mxf4(d_tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * NSB * (j >> 1), !first || j > 0);
+            }
+            tc_commit(&empty[st]);
+        };
+        int st = 0, i = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = cluster; ok && tile < wk.tiles; tile += clusters, ++i) {
             const int acc = i & 1;
             ok = __all_sync(0xffffffffu, wait_or_abort(&acc_empty[acc], ((i >> 1) & 1) ^ 1, status, abort_flag));
             if (!ok) break;
-            const uint32_t d_tmem = tmem + acc * BN;
             // the first of the tile's tokens within its 128-row scale tile: a column for each 32
             const uint32_t sb_shift = (uint32_t)(tile % wk.token_tiles * BN % MX_TILE_ROWS / 32);
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+            for (int ks = ks0; ks < ks1;) {
                 ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], phase, status, abort_flag));
                 if (!ok) break;
+                const int st1 = st + 1 == STAGES ? 0 : st + 1;
+                const bool two = ks + 1 < ks1 &&
+                                 __all_sync(0xffffffffu, mbar_try_wait(&full[st1], st1 == 0 ? phase ^ 1 : phase));
                 tc_fence_after();
-                const uint32_t sa = tmem + C::COL_SC + (it & 1) * C::SC_COLS, sb = sa + 8;
                 if (elect_one()) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {        // the step's two groups of 128 values
-                        tc_copy_scales(sa + 4 * g, sadesc0 + (uint64_t)((st * SC_BYTES + g * MX_TILE_BYTES) >> 4));
-#pragma unroll
-                        for (int b = 0; b < NSB; ++b)
-                            tc_copy_scales(sb + 4 * (NSB * g + b),
-                                           sbdesc0 + (uint64_t)(((st * NSB + b) * SC_BYTES + g * MX_TILE_BYTES) >> 4));
-                    }
-                    const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
-                    const uint64_t bd = bdesc0 + (uint64_t)(st * (B_BYTES >> 4));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {        // 64 values: bytes 2 (j % 2) and next of each scale word
-                        const uint32_t id = C::IDESC | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
-                        tc_mma_mxf4(d_tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1),
-                                    sb + 4 * NSB * (j >> 1) + sb_shift, ks > ks0 || j > 0);
-                    }
-                    tc_commit(&empty[st]);
-                    if (ks == ks1 - 1) tc_commit(&acc_full[acc]);
+                    copy_scales(0, st);
+                    if (two) copy_scales(1, st1);
+                    multiply(0, st, tmem + acc * BN, sb_shift, ks == ks0);
+                    if (two) multiply(1, st1, tmem + acc * BN, sb_shift, false);
+                    if (ks + (two ? 2 : 1) == ks1) tc_commit(&acc_full[acc]);
                 }
-                if (++st == STAGES) {
-                    st = 0;
-                    phase ^= 1;
-                }
+                for (int n = two ? 2 : 1; n; --n, ++ks)
+                    if (++st == STAGES) {
+                        st = 0;
+                        phase ^= 1;
+                    }
             }
         }
         // Tensor memory is not freed under an MMA: a last commit arrives after all of them.
