@@ -452,6 +452,323 @@ cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     return cudaLaunchKernelEx(&cfg, gemm_mxfp4_kernel<C, T>, tm_w, tm_x, wsc, xsc, y, wk, CL, dev.status);
 }
 
+// ---------------------------------------------------------------------------------------
+// Many tokens: a pair of CTAs (two SMs) on one tile of 256 weight rows x 256 tokens.
+//
+// What bounds one CTA's MMAs is reading their operands from shared memory: at 64 values of k,
+// 128 x N takes (128 + N) * 32 bytes, and the measured times (126, 151, 180 cycles for N = 128,
+// 192, 256) are 64 bytes a cycle.  A pair's MMA (cta_group::2) leaves half of the tokens' operand to
+// each SM: 8 KB for 128 x 256 outputs an SM, which is what its arithmetic takes (128 cycles).
+//
+// Each CTA loads its 128 weight rows, its 128 of the tokens, its rows' scales and all tokens' scales;
+// all copies of a stage arrive on the first CTA's barrier, whose issuer runs the MMAs of both, each
+// SM keeping its 128 rows' results.  The accumulator takes half of tensor memory and the scales some,
+// so there is one: eight epilogue warps take it into registers at once (128 columns each) and let
+// the next tile's MMAs go, then store.
+// ---------------------------------------------------------------------------------------
+struct PairCfg {
+    static constexpr int BN = 256, STAGES = 6;
+    static constexpr int B_BYTES = BN / 2 * ROW_BYTES, SB_BYTES = 2 * SC_BYTES;
+    static constexpr int OFF_A = 0;
+    static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+    static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_SB = OFF_SA + STAGES * SC_BYTES;
+    static constexpr int OFF_BAR = OFF_SB + STAGES * SB_BYTES;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 3) * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+    static constexpr int EPI_WARPS = 8, THREADS = (EPI_WARPS + 2) * 32;
+    static constexpr int COL_SC = BN, SC_COLS = 24, TMEM_COLS = 512;
+    static constexpr uint32_t STAGE_TX = 2 * (A_BYTES + B_BYTES + SC_BYTES + SB_BYTES);   // both CTAs' bytes
+    static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
+                                      ((uint32_t)(2 * BM >> 4) << 24);
+    static_assert(SMEM_BYTES <= SMEM_MAX, "capacity");
+};
+
+__device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+// Arrives on both CTAs' barrier of that place once the MMAs issued before have completed.
+__device__ __forceinline__ void pair_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+// A TMA load into this CTA's shared memory that completes on a barrier of the pair's first CTA.
+__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// 32 lanes x 32 columns, asynchronous: the registers are valid after tc_wait_ld.
+__device__ __forceinline__ void tc_ld_x32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's loads from tensor memory; binds the registers to the wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&a)[4][32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(a[i][j]));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(PairCfg::THREADS, 1)
+    gemm_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                           const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
+                           T *__restrict__ y, Work wk, int *status)
+{
+    using C = PairCfg;
+    constexpr int BN = C::BN, STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);        // used in the first CTA
+    uint64_t *empty = full + STAGES, *acc_full = empty + STAGES, *acc_empty = acc_full + 1, *drained = acc_empty + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * C::EPI_WARPS);
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::EPI_WARPS + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(C::TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == C::EPI_WARPS && lane == 0) {
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_ws);
+        prefetch_tensormap(&tm_xs);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+    if (warp == C::EPI_WARPS) {
+        // ------------------------------ producer ------------------------------
+        int st = 0, it = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        griddep_wait();
+        griddep_launch_dependents();
+        for (int tile = pair; ok && tile < wk.tiles; tile += pairs) {
+            const int rt = tile / wk.token_tiles, tt = tile - rt * wk.token_tiles;
+            const int rows = 2 * rt + (int)rank;                        // this CTA's 128-row tile
+            for (int ks = 0; ks < wk.steps; ++ks, ++it) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], phase, status, abort_flag));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], C::STAGE_TX);
+                    pair_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, rows * BM, bar);
+                    pair_load_2d(smem + C::OFF_B + st * C::B_BYTES, &tm_x, ks * ROW_BYTES, tt * BN + (int)rank * (BN / 2), bar);
+                    pair_load_2d(smem + C::OFF_SA + st * SC_BYTES, &tm_ws, ks * (SC_BYTES / 8), rows, bar);
+                    pair_load_2d(smem + C::OFF_SB + st * C::SB_BYTES, &tm_xs, ks * (SC_BYTES / 8), 2 * tt, bar);
+                }
+                if (++st == STAGES) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // Neither CTA leaves with a copy in flight: the first one's barriers count both CTAs' copies,
+        // and the other waits for it at the cluster's last barrier.
+        if (rank == 0)
+            for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+                mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1, status);
+        // Nor does it leave before the first CTA's last commits have arrived on its barriers.
+        for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+            wait_or_abort(&empty[i % STAGES], (i / STAGES) & 1, status, abort_flag);
+    } else if (warp == C::EPI_WARPS + 1) {
+        // ------------------------------ MMA issuer (first CTA) ------------------------------
+        if (rank == 0) {
+            const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_A));
+            const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
+            const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
+            const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SB));
+            auto copy_scales = [&](int slot, int st) {
+                const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    pair_copy_scales(sa + 4 * g, sadesc0 + (uint64_t)((st * SC_BYTES + g * MX_TILE_BYTES) >> 4));
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        pair_copy_scales(sb + 8 * g + 4 * b,
+                                         sbdesc0 + (uint64_t)((st * C::SB_BYTES + b * SC_BYTES + g * MX_TILE_BYTES) >> 4));
+                }
+            };
+            auto multiply = [&](int slot, int st, bool first) {
+                const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8;
+                const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
+                const uint64_t bd = bdesc0 + (uint64_t)(st * (C::B_BYTES >> 4));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t id = C::IDESC | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
+                    pair_mma(tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 8 * (j >> 1), !first || j > 0);
+                }
+                pair_commit(&empty[st]);
+            };
+            int st = 0, i = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < wk.tiles; tile += pairs, ++i) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(acc_empty, (i & 1) ^ 1, status, abort_flag));
+                if (!ok) break;
+                for (int ks = 0; ks < wk.steps;) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], phase, status, abort_flag));
+                    if (!ok) break;
+                    const int st1 = st + 1 == STAGES ? 0 : st + 1;
+                    const bool two = ks + 1 < wk.steps &&
+                                     __all_sync(0xffffffffu, mbar_try_wait(&full[st1], st1 == 0 ? phase ^ 1 : phase));
+                    tc_fence_after();
+                    if (elect_one()) {
+                        copy_scales(0, st);
+                        if (two) copy_scales(1, st1);
+                        multiply(0, st, ks == 0);
+                        if (two) multiply(1, st1, false);
+                        if (ks + (two ? 2 : 1) == wk.steps) pair_commit(acc_full);
+                    }
+                    for (int n = two ? 2 : 1; n; --n, ++ks)
+                        if (++st == STAGES) {
+                            st = 0;
+                            phase ^= 1;
+                        }
+                }
+            }
+            // Tensor memory is not freed under an MMA: a last commit arrives after all of them.
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                             ::"r"(smem_u32(drained)) : "memory");
+            mbar_wait_drain(drained, 0, status);
+        }
+    } else {
+        // ------------------------------ epilogue ------------------------------
+        const int quarter = warp & 3, half = warp >> 2;                  // 32 lanes, 128 of the columns
+        int i = 0;
+        for (int tile = pair; tile < wk.tiles; tile += pairs, ++i) {
+            const int rt = tile / wk.token_tiles, tt = tile - rt * wk.token_tiles;
+            const int64_t r = (int64_t)(2 * rt + (int)rank) * BM + 32 * quarter + lane;
+            const int tok0 = tt * BN + half * (BN / 2);
+            const int cols = min(BN / 2, wk.m - tok0);
+            if (!__all_sync(0xffffffffu, wait_or_abort(acc_full, i & 1, status, abort_flag))) break;
+            tc_fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                tc_ld_x32(tmem + ((uint32_t)(32 * quarter) << 16) + half * (BN / 2) + 32 * q, v[q]);
+            tc_wait_ld(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) cluster_arrive(cluster_addr(smem_u32(acc_empty), 0));
+            if (r < wk.n) {
+                T *dst = y + (int64_t)tok0 * wk.n + r;
+                if (cols == BN / 2) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c, dst += wk.n) *dst = from_f32<T>(__uint_as_float(v[q][c]));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c, dst += wk.n)
+                            if (32 * q + c < cols) *dst = from_f32<T>(__uint_as_float(v[q][c]));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == C::EPI_WARPS + 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
+    }
+}
+
+template <typename T>
+cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
+                         const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, cudaStream_t stream)
+{
+    cudaError_t e = set_kernel_smem<gemm_mxfp4_pair_kernel<T>>(dev.device, PairCfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const uint64_t sc_row = (uint64_t)k / MX_TILE_K * MX_TILE_BYTES;      // bytes of 128 rows' scales
+    CUtensorMap tm_w, tm_x, tm_ws, tm_xs;
+    if (!encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)k / 2, (uint64_t)n, (uint64_t)k / 2, ROW_BYTES, BM,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
+                   PairCfg::BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&tm_ws, CU_TENSOR_MAP_DATA_TYPE_UINT64, wsc, sc_row / 8, (uint64_t)(n + 127) / 128, sc_row,
+                   SC_BYTES / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_2d(&tm_xs, CU_TENSOR_MAP_DATA_TYPE_UINT64, xsc, sc_row / 8, (uint64_t)(m + 127) / 128, sc_row,
+                   SC_BYTES / 8, 2, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    Work wk{};
+    wk.m = (int)m;
+    wk.n = (int)n;
+    wk.steps = (int)(k / BK);
+    wk.token_tiles = (int)((m + PairCfg::BN - 1) / PairCfg::BN);
+    const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * wk.token_tiles;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    wk.tiles = (int)tiles;
+    const int64_t pairs = tiles < dev.num_sms / 2 ? tiles : dev.num_sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(PairCfg::THREADS);
+    cfg.dynamicSmemBytes = PairCfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<T>, tm_w, tm_x, tm_ws, tm_xs, y, wk, dev.status);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
@@ -473,6 +790,7 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
         if (m <= 32) return launch_tiles<Cfg<32, 8>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(32), pdl, stream);
         if (m <= 64) return launch_tiles<Cfg<64, 6>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(64), pdl, stream);
         if (m <= 128) return launch_tiles<Cfg<128, 4>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(128), pdl, stream);
+        if (m > 192) return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, stream);
         return launch_tiles<Cfg<192, 5>, T>(dev, w, wsc, x, xsc, out, m, n, k, 1, pdl, stream);
     });
 }
