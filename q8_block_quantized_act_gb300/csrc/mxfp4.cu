@@ -7,8 +7,11 @@
 namespace q8 {
 namespace {
 
-// One thread per 8 consecutive values, 4 lanes per block.  Rows m .. 128 ceil(m / 128) - 1 get
-// zero scale bytes, so that the whole scale array is defined.
+constexpr int ROWS = 4;            // rows in flight per thread
+
+// A thread has 8 consecutive values of each of ROWS rows, 4 lanes a block; the four scale bytes of
+// 128 values leave as one word.  Rows m .. 128 ceil(m / 128) - 1 get zero scale bytes, so that the
+// whole scale array is defined.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict__ x, int64_t ldx,
                                                              uint32_t *__restrict__ codes,
@@ -19,36 +22,51 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
     if (c >= chunks) return;          // k / 8 is a multiple of 32: warps are whole
     const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
-    for (int64_t r = blockIdx.y; r < padded; r += gridDim.y) {
-        uint32_t b = 0;
-        if (r < m) {
+    for (int64_t r0 = (int64_t)blockIdx.y * ROWS; r0 < padded; r0 += (int64_t)gridDim.y * ROWS) {
+        uint4 in[ROWS][sizeof(T) / 2];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                in[j][h] = r0 + j < m ? __ldcs(reinterpret_cast<const uint4 *>(x + (r0 + j) * ldx + (int64_t)c * 8) + h)
+                                      : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
             float v[8];
-            const uint4 *src = reinterpret_cast<const uint4 *>(x + r * ldx + (int64_t)c * 8);
             if constexpr (sizeof(T) == 4) {
                 float lo[4], hi[4];
-                unpack<T>(src[0], lo);
-                unpack<T>(src[1], hi);
+                unpack<T>(in[j][0], lo);
+                unpack<T>(in[j][1], hi);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
             } else {
-                unpack<T>(src[0], v);
+                unpack<T>(in[j][0], v);
             }
             uint32_t a = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            b = mx_scale_byte(a);
+            const uint32_t b = mx_scale_byte(a);
             const float inv = b == 255u ? 0.0f : mx_inverse(b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = b == 255u ? 0.0f : v[i] * inv;
-            codes[r * chunks + c] = mx_codes8(v);
+            uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
+            word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
+            if (r0 + j < m) codes[(r0 + j) * chunks + c] = mx_codes8(v);
+            if ((c & 15) == 0)
+                *reinterpret_cast<uint32_t *>(scales + mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)) = r0 + j < m ? word : 0u;
         }
-        if ((c & 3) == 0) scales[mx_scale_at(r, c >> 2, k / MX_TILE_K)] = (uint8_t)b;
     }
 }
 
-// One thread per 8 codes.
+// A code's value times 2^-126 is the f32 whose exponent and top fraction bits are the code's.
+__device__ __forceinline__ float mx_code_value(uint32_t code)
+{
+    return __uint_as_float(((code & 8u) << 28) | ((code & 7u) << 22)) * __uint_as_float(253u << 23);
+}
+
+// A thread has 8 codes of each of ROWS rows.
 template <typename T>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, T *__restrict__ y,
@@ -58,12 +76,28 @@ __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__re
     const int chunks = k / 8;
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
     if (c >= chunks) return;
-    for (int64_t r = blockIdx.y; r < m; r += gridDim.y) {
-        const uint32_t w = codes[r * chunks + c];
-        const float s = mx_scale(scales[mx_scale_at(r, c >> 2, k / MX_TILE_K)]);
-        T *dst = y + r * k + (int64_t)c * 8;
+    for (int64_t r0 = (int64_t)blockIdx.y * ROWS; r0 < m; r0 += (int64_t)gridDim.y * ROWS) {
+        uint32_t w[ROWS], b[ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = from_f32<T>(0.5f * (float)mx_twice(w >> (4 * i)) * s);
+        for (int j = 0; j < ROWS; ++j) {
+            w[j] = r0 + j < m ? codes[(r0 + j) * chunks + c] : 0u;
+            b[j] = r0 + j < m ? scales[mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            if (r0 + j >= m) break;
+            const float s = mx_scale(b[j]);
+            uint4 *dst = reinterpret_cast<uint4 *>(y + (r0 + j) * k + (int64_t)c * 8);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = mx_code_value(w[j] >> (4 * i)) * s;
+            if constexpr (sizeof(T) == 4) {
+                dst[0] = pack<T>({v[0], v[1], v[2], v[3]});
+                dst[1] = pack<T>({v[4], v[5], v[6], v[7]});
+            } else {
+                dst[0] = pack<T>(v);
+            }
+        }
     }
 }
 
@@ -82,7 +116,8 @@ __global__ void __launch_bounds__(256) tile_mxfp4_scales_kernel(const uint8_t *_
 
 dim3 grid_rows(int64_t rows, int64_t chunks)
 {
-    return dim3((unsigned)((chunks + 255) / 256), (unsigned)(rows < 65535 ? rows : 65535));
+    const int64_t groups = (rows + ROWS - 1) / ROWS;
+    return dim3((unsigned)((chunks + 255) / 256), (unsigned)(groups < 65535 ? groups : 65535));
 }
 
 }  // namespace

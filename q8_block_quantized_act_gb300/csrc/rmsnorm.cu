@@ -1,7 +1,8 @@
 // rmsnorm.cu -- residual addition, root-mean-square norm and q8_1 quantization in one pass:
 //   s = x + r (f32),  y = s * (mean(s^2) + eps)^-1/2 * w,  then the q8_1 blocks of y.
 //
-// Simple form: one CTA per row; the row is read twice (once for the sum of squares).
+// Bound by memory: x, the residual in, the residual, the quants and scales out.  The row stays in
+// registers between the sum of squares and the quantization, so each is moved once.
 #include "launch.h"
 #include "q8_1.cuh"
 #include "types.cuh"
@@ -9,82 +10,185 @@
 namespace q8 {
 namespace {
 
-constexpr int THREADS = 256;
-
-__device__ __forceinline__ float load_weight(const void *w, int wtype, int64_t i)
+// V consecutive weights as f32.
+template <int V, typename W>
+__device__ __forceinline__ void load_weights(const W *w, float (&f)[V])
 {
-    if (wtype == Q8ACT_F32) return static_cast<const float *>(w)[i];
-    if (wtype == Q8ACT_F16) return to_f32(static_cast<const __half *>(w)[i]);
-    return to_f32(static_cast<const __nv_bfloat16 *>(w)[i]);
+    if constexpr (V == VEC<W>) {
+        unpack<W>(__ldg(reinterpret_cast<const uint4 *>(w)), f);
+    } else if constexpr (V > VEC<W>) {             // 8 of 4 bytes
+        float g[4];
+        unpack<W>(__ldg(reinterpret_cast<const uint4 *>(w)), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = g[j];
+        unpack<W>(__ldg(reinterpret_cast<const uint4 *>(w) + 1), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[4 + j] = g[j];
+    } else {                                       // 4 of 2 bytes
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(w));
+        float g[8];
+        unpack<W>(make_uint4(u.x, u.y, 0, 0), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = g[j];
+    }
 }
 
-// V consecutive values of the sum x + r as f32.
-template <typename T>
-__device__ __forceinline__ void load_sum(const T *x, const T *r, int64_t i, float (&v)[VEC<T>])
+// y's quants and scale: V values of the block that starts at a multiple of 32 / V lanes.
+template <typename T, bool MMQ>
+__device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k, int c, float (&v)[VEC<T>], float inv)
 {
-    unpack<T>(*reinterpret_cast<const uint4 *>(x + i), v);
+    constexpr int V = VEC<T>;
+    const int64_t i = (int64_t)c * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = v[j] * inv;
+    if (a.weight) {
+        float w[V];
+        if (a.wtype == Q8ACT_F32) load_weights<V>(static_cast<const float *>(a.weight) + i, w);
+        else if (a.wtype == Q8ACT_F16) load_weights<V>(static_cast<const __half *>(a.weight) + i, w);
+        else load_weights<V>(static_cast<const __nv_bfloat16 *>(a.weight) + i, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] *= w[j];
+    }
+    if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + t * k + i) = pack<T>(v);
+    const BlockQ<V> b = quantize_block<V>(v);
+    const bool first = c % (QK / V) == 0;
+    if constexpr (MMQ) {
+        uint32_t w[V / 2];                         // small integers: exact in binary16
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            const __half2 h = __floats2half2_rn(b.t[2 * j], b.t[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        uint16_t *q = static_cast<uint16_t *>(a.q) + t * k + i;
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+        if (first) a.d[(int64_t)(c / (QK / V)) * a.ldm + t] = b.d;
+    } else {
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+            w[j] = byte_of(b.t[4 * j]) | (byte_of(b.t[4 * j + 1]) << 8) | (byte_of(b.t[4 * j + 2]) << 16) |
+                   (byte_of(b.t[4 * j + 3]) << 24);
+        int8_t *q = static_cast<int8_t *>(a.q) + t * k + i;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(q) = w[0];
+        if (first) a.d[t * (k / QK) + c / (QK / V)] = b.d;
+    }
+}
+
+// The CTA's sum, the same in every thread.
+__device__ __forceinline__ float cta_sum(float s, float *part)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    float v = (int)(threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void add_residual(uint4 x, const uint4 *r, float (&v)[VEC<T>])
+{
+    unpack<T>(x, v);
     if (r) {
         float u[VEC<T>];
-        unpack<T>(*reinterpret_cast<const uint4 *>(r + i), u);
+        unpack<T>(*r, u);
 #pragma unroll
         for (int j = 0; j < VEC<T>; ++j) v[j] = __fadd_rn(v[j], u[j]);
     }
 }
 
-template <typename T, bool MMQ>
-__global__ void __launch_bounds__(THREADS) rmsnorm_q8_1_kernel(NormArgs a, int64_t m, int k)
+// A CTA per row, CH 16-byte chunks a thread.  chunks = k / V is a multiple of 32, so a warp's chunk
+// is inside the row for all of its lanes or for none, as the block's shuffles need.
+template <typename T, bool MMQ, int CH>
+__global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
 {
     constexpr int V = VEC<T>;
-    __shared__ float part[THREADS / 32];
+    __shared__ float part[32];
     griddep_enter();
     const int chunks = k / V;
-    for (int64_t t = blockIdx.x; t < m; t += gridDim.x) {
-        const T *x = static_cast<const T *>(a.x) + t * a.ldx;
-        const T *r = a.residual ? static_cast<const T *>(a.residual) + t * a.ldr : nullptr;
-        float ss = 0.0f;
-        for (int c = threadIdx.x; c < chunks; c += THREADS) {
-            float v[V];
-            load_sum<T>(x, r, (int64_t)c * V, v);
+    const int64_t t = blockIdx.x;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.ldx);
+    const uint4 *r = a.residual ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr) : nullptr;
+    uint4 xv[CH], rv[CH];
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
-        }
+    for (int i = 0; i < CH; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        xv[i] = c < chunks ? x[c] : make_uint4(0, 0, 0, 0);
+        rv[i] = r && c < chunks ? r[c] : make_uint4(0, 0, 0, 0);
+    }
+    float v[CH][V], ss = 0.0f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        float total = 0.0f;
+    for (int i = 0; i < CH; ++i) {
+        add_residual<T>(xv[i], r ? &rv[i] : nullptr, v[i]);
 #pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) total += part[i];
-        const float inv = __fdiv_rn(1.0f, sqrtf(total / (float)k + a.eps));
-        // chunks is a multiple of 32: a warp is inside the row or past it as a whole
-        for (int c = threadIdx.x; c < chunks; c += THREADS) {
-            const int64_t i = (int64_t)c * V;
-            float v[V];
-            load_sum<T>(x, r, i, v);
-            if (a.residual_out)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + t * a.ldro + i) = pack<T>(v);
+        for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    if (a.residual_out) {
+        T *out = static_cast<T *>(a.residual_out) + t * a.ldro;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = v[j] * inv;
-                if (a.weight) v[j] *= load_weight(a.weight, a.wtype, i + j);
-            }
-            if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + t * k + i) = pack<T>(v);
-            const BlockQ<V> b = quantize_block<V>(v);
-            const bool first = c % (QK / V) == 0;
-            if (MMQ) {
-                __half *q = reinterpret_cast<__half *>(a.q) + t * k + i;
-#pragma unroll
-                for (int j = 0; j < V; ++j) q[j] = __float2half_rn(b.t[j]);
-                if (first) a.d[(int64_t)(c / (QK / V)) * a.ldm + t] = b.d;
-            } else {
-                int8_t *q = reinterpret_cast<int8_t *>(a.q) + t * k + i;
-#pragma unroll
-                for (int j = 0; j < V; ++j) q[j] = (int8_t)b.t[j];
-                if (first) a.d[t * (k / QK) + c / (QK / V)] = b.d;
-            }
+        for (int i = 0; i < CH; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c < chunks) *reinterpret_cast<uint4 *>(out + (int64_t)c * V) = pack<T>(v[i]);
         }
     }
+    const float inv = __fdiv_rn(1.0f, sqrtf(cta_sum(ss, part) / (float)k + a.eps));
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < chunks) store_block<T, MMQ>(a, t, k, c, v[i], inv);
+    }
+}
+
+// Rows too long for registers: read twice (the second time from L2).
+template <typename T, bool MMQ>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
+{
+    constexpr int V = VEC<T>;
+    __shared__ float part[32];
+    griddep_enter();
+    const int chunks = k / V;
+    const int64_t t = blockIdx.x;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.ldx);
+    const uint4 *r = a.residual ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr) : nullptr;
+    float ss = 0.0f;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        float v[V];
+        add_residual<T>(x[c], r ? r + c : nullptr, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+    const float inv = __fdiv_rn(1.0f, sqrtf(cta_sum(ss, part) / (float)k + a.eps));
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        float v[V];
+        add_residual<T>(x[c], r ? r + c : nullptr, v);
+        if (a.residual_out)
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + t * a.ldro + (int64_t)c * V) = pack<T>(v);
+        store_block<T, MMQ>(a, t, k, c, v, inv);
+    }
+}
+
+template <typename T, bool MMQ>
+cudaError_t launch_rows(const DeviceInfo &dev, const NormArgs &a, int64_t m, int64_t k, cudaStream_t stream)
+{
+    const int chunks = (int)(k / VEC<T>);
+    const dim3 grid((unsigned)m);
+    // Few rows: every thread that a CTA can have, one chunk each if that is enough (latency).
+    // Many rows: 256 threads with up to 32 values each, several CTAs to an SM (throughput).
+    int threads = m <= 2 * dev.num_sms ? 1024 : 256;
+    while (threads < 1024 && chunks > threads * (32 / VEC<T>)) threads *= 2;
+    if (threads > chunks) threads = chunks;              // a multiple of 32
+    const int each = (chunks + threads - 1) / threads;
+    if (each == 1) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 1>, grid, threads, 0, stream, a, (int)k);
+    if (each == 2) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 2>, grid, threads, 0, stream, a, (int)k);
+    if (each <= 4) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 4>, grid, threads, 0, stream, a, (int)k);
+    if constexpr (VEC<T> == 4)
+        if (each <= 8) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 8>, grid, threads, 0, stream, a, (int)k);
+    return launch_dependent(rmsnorm_long_kernel<T, MMQ>, grid, 1024, 0, stream, a, (int)k);
 }
 
 }  // namespace
@@ -94,9 +198,7 @@ cudaError_t launch_rmsnorm_q8_1(const DeviceInfo &dev, const NormArgs &a, bool m
 {
     return with_type(type, [&](auto t) {
         using T = decltype(t);
-        const dim3 grid((unsigned)(m < (1 << 20) ? m : (1 << 20)));
-        return mmq ? launch_dependent(rmsnorm_q8_1_kernel<T, true>, grid, THREADS, 0, stream, a, m, (int)k)
-                   : launch_dependent(rmsnorm_q8_1_kernel<T, false>, grid, THREADS, 0, stream, a, m, (int)k);
+        return mmq ? launch_rows<T, true>(dev, a, m, k, stream) : launch_rows<T, false>(dev, a, m, k, stream);
     });
 }
 
