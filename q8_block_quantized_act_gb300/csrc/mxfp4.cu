@@ -7,12 +7,10 @@
 namespace q8 {
 namespace {
 
-constexpr int ROWS = 4;            // rows in flight per thread
-
 // A thread has 8 consecutive values of each of ROWS rows, 4 lanes a block; the four scale bytes of
 // 128 values leave as one word.  Rows m .. 128 ceil(m / 128) - 1 get zero scale bytes, so that the
 // whole scale array is defined.
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict__ x, int64_t ldx,
                                                              uint32_t *__restrict__ codes,
                                                              uint8_t *__restrict__ scales, int64_t m, int k)
@@ -67,7 +65,7 @@ __device__ __forceinline__ float mx_code_value(uint32_t code)
 }
 
 // A thread has 8 codes of each of ROWS rows.
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, T *__restrict__ y,
                                                             int64_t m, int k)
@@ -114,10 +112,17 @@ __global__ void __launch_bounds__(256) tile_mxfp4_scales_kernel(const uint8_t *_
     }
 }
 
-dim3 grid_rows(int64_t rows, int64_t chunks)
+dim3 grid_rows(int64_t rows, int64_t chunks, int each)
 {
-    const int64_t groups = (rows + ROWS - 1) / ROWS;
+    const int64_t groups = (rows + each - 1) / each;
     return dim3((unsigned)((chunks + 255) / 256), (unsigned)(groups < 65535 ? groups : 65535));
+}
+
+// Rows a thread has in flight: four where that still leaves the GPU full of threads (more bytes
+// under way), else one (a few rows are a matter of latency).
+bool four_rows(const DeviceInfo &dev, int64_t rows, int64_t chunks)
+{
+    return (rows + 3) / 4 * chunks >= (int64_t)dev.num_sms * 2048;
 }
 
 }  // namespace
@@ -128,8 +133,11 @@ cudaError_t launch_quantize_mxfp4(const DeviceInfo &dev, const void *x, int64_t 
     return with_type(type, [&](auto t) {
         using T = decltype(t);
         const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
-        return launch_dependent(quantize_mxfp4_kernel<T>, grid_rows(padded, k / 8), 256, 0, stream,
-                                static_cast<const T *>(x), ldx, reinterpret_cast<uint32_t *>(codes), scales, m, (int)k);
+        auto go = [&](auto kern, int each) {
+            return launch_dependent(kern, grid_rows(padded, k / 8, each), 256, 0, stream, static_cast<const T *>(x), ldx,
+                                    reinterpret_cast<uint32_t *>(codes), scales, m, (int)k);
+        };
+        return four_rows(dev, m, k / 8) ? go(quantize_mxfp4_kernel<T, 4>, 4) : go(quantize_mxfp4_kernel<T, 1>, 1);
     });
 }
 
@@ -138,8 +146,11 @@ cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, co
 {
     return with_type(type, [&](auto t) {
         using T = decltype(t);
-        return launch_dependent(dequant_mxfp4_kernel<T>, grid_rows(m, k / 8), 256, 0, stream,
-                                reinterpret_cast<const uint32_t *>(codes), scales, static_cast<T *>(y), m, (int)k);
+        auto go = [&](auto kern, int each) {
+            return launch_dependent(kern, grid_rows(m, k / 8, each), 256, 0, stream,
+                                    reinterpret_cast<const uint32_t *>(codes), scales, static_cast<T *>(y), m, (int)k);
+        };
+        return four_rows(dev, m, k / 8) ? go(dequant_mxfp4_kernel<T, 4>, 4) : go(dequant_mxfp4_kernel<T, 1>, 1);
     });
 }
 

@@ -91,12 +91,12 @@ __device__ __forceinline__ float cta_sum(float s, float *part)
 }
 
 template <typename T>
-__device__ __forceinline__ void add_residual(uint4 x, const uint4 *r, float (&v)[VEC<T>])
+__device__ __forceinline__ void add_residual(uint4 x, uint4 r, bool add, float (&v)[VEC<T>])
 {
     unpack<T>(x, v);
-    if (r) {
+    if (add) {
         float u[VEC<T>];
-        unpack<T>(*r, u);
+        unpack<T>(r, u);
 #pragma unroll
         for (int j = 0; j < VEC<T>; ++j) v[j] = __fadd_rn(v[j], u[j]);
     }
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
     float v[CH][V], ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        add_residual<T>(xv[i], r ? &rv[i] : nullptr, v[i]);
+        add_residual<T>(xv[i], rv[i], r != nullptr, v[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
@@ -158,14 +158,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
     float ss = 0.0f;
     for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
         float v[V];
-        add_residual<T>(x[c], r ? r + c : nullptr, v);
+        add_residual<T>(x[c], r ? r[c] : make_uint4(0, 0, 0, 0), r != nullptr, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
     }
     const float inv = __fdiv_rn(1.0f, sqrtf(cta_sum(ss, part) / (float)k + a.eps));
     for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
         float v[V];
-        add_residual<T>(x[c], r ? r + c : nullptr, v);
+        add_residual<T>(x[c], r ? r[c] : make_uint4(0, 0, 0, 0), r != nullptr, v);
         if (a.residual_out)
             *reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + t * a.ldro + (int64_t)c * V) = pack<T>(v);
         store_block<T, MMQ>(a, t, k, c, v, inv);
