@@ -28,29 +28,34 @@ __device__ __forceinline__ float div127(float a)
     return a == __int_as_float(0x7f800000) ? a : q1;
 }
 
-// One value of a block with scale d, rc = rcp_approx(d): its quant as an integer-valued float
-// (+0 for zero).  For a value whose approximate quotient qa = v * (1/d)
-// lies farther than 1e-3 from every half-integer, rint(qa) is round-half-away(fl(v / d)): qa
-// differs from v / d by under 4e-5 (|v / d| <= 127; the reciprocal's relative error is at most
-// 2^-23, the product's 2^-24) and fl(v / d) from v / d by under 8e-6, so all three round to the
-// same integer, and no tie is involved.  The test |qa - rint(qa)| < 0.499 selects exactly those
-// values; the rest (near a half-integer, or qa not finite) take the IEEE division and the
-// rounding of the scalar formula.  A block whose amax is 0 gives q = 0.
+// One value of a block with scale d: its quant as an integer-valued float (+0 for zero).  rc is
+// block_rcp(d).  For a value whose approximate quotient qa = v * rc lies farther than 1e-4 from
+// every half-integer, its nearest integer is round-half-away(fl(v / d)): qa differs from v / d by
+// under 4e-5 (|v / d| <= 127; the reciprocal's relative error is at most 2^-23, the product's 2^-24)
+// and fl(v / d) from v / d by under 8e-6, so all three round to the same integer, at most 127, and no
+// tie is involved.  The test |qa - t| < 0.4999 selects exactly those values; the rest (near a
+// half-integer, or qa not finite) take the IEEE division and the rounding of the scalar formula.
+// The nearest integer comes from adding and subtracting 1.5 * 2^23 (unit spacing there), which
+// unlike the rounding instruction runs at the adders' full rate.
 __device__ __forceinline__ float quantize_value(float v, float d, float rc)
 {
     const float qa = __fmul_rn(v, rc);
-    float t = rintf(qa);
-    if (d == 0.0f) {
-        t = 0.0f;
-    } else if (fabsf(__fsub_rn(qa, t)) < 0.499f) {
-        t = fminf(fmaxf(t, -127.0f), 127.0f);
-    } else {
+    float t = __fsub_rn(__fadd_rn(qa, 12582912.0f), 12582912.0f);
+    if (!(fabsf(__fsub_rn(qa, t)) < 0.4999f)) {
         t = roundf(__fdiv_rn(v, d));
         if (t > 127.0f) t = 127.0f;
         if (t < -127.0f) t = -127.0f;
         if (!(t == t)) t = 0.0f;       // NaN quantizes to 0
+        t = __fadd_rn(t, 0.0f);        // -0 -> +0
     }
-    return __fadd_rn(t, 0.0f);         // -0 -> +0
+    return t;
+}
+
+// 1 / d, approximately; 0 for d = 0 (every finite value of the block quantizes to 0), and NaN for a
+// subnormal d, whose rounding may leave quotients above 127: all its values take the division.
+__device__ __forceinline__ float block_rcp(float d)
+{
+    return d >= 1.17549435e-38f ? rcp_approx(d) : d == 0.0f ? 0.0f : __int_as_float(0x7fffffff);
 }
 
 // V consecutive values of a block whose 32 values are spread over 32 / V lanes.
@@ -70,7 +75,7 @@ __device__ __forceinline__ BlockQ<V> quantize_block(const float (&v)[V])
     for (int o = 1; o < 32 / V; o <<= 1) a = fmaxf(a, __shfl_xor_sync(FULL, a, o));
     BlockQ<V> r;
     r.d = div127(a);
-    const float rc = rcp_approx(r.d);
+    const float rc = block_rcp(r.d);
 #pragma unroll
     for (int i = 0; i < V; ++i) r.t[i] = quantize_value(v[i], r.d, rc);
     return r;

@@ -178,9 +178,9 @@ cudaError_t launch_rows(const DeviceInfo &dev, const NormArgs &a, int64_t m, int
     const int chunks = (int)(k / VEC<T>);
     const dim3 grid((unsigned)m);
     // Few rows: every thread that a CTA can have, one chunk each if that is enough (latency).
-    // Many rows: 256 threads with up to 32 values each, several CTAs to an SM (throughput).
+    // Many rows: 256 threads with up to 16 values each, several CTAs to an SM (throughput).
     int threads = m <= 2 * dev.num_sms ? 1024 : 256;
-    while (threads < 1024 && chunks > threads * (32 / VEC<T>)) threads *= 2;
+    while (threads < 1024 && chunks > threads * (16 / VEC<T>)) threads *= 2;
     if (threads > chunks) threads = chunks;              // a multiple of 32
     const int each = (chunks + threads - 1) / threads;
     if (each == 1) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 1>, grid, threads, 0, stream, a, (int)k);
