@@ -550,7 +550,7 @@ static int rmsnorm_common(const void *x, int64_t ldx, const void *residual, int6
     if (!aligned16(weight) || !aligned16(y) || !aligned16(q) || !aligned16(d)) return Q8ACT_ERR_ALIGN;
     const q8::DeviceInfo *dev;
     if ((rc = current_device(&dev))) return rc;
-    const q8::NormArgs a{x, residual, weight, residual_out, y, q, d, ldx, ldr, ldro, q8act_mmq_ldm(m), eps, wtype};
+    const q8::NormArgs a{x, residual, weight, residual_out, y, q, d, ldx, ldr, ldro, q8act_mmq_ldm(m), eps, 1.0f / (float)k, wtype};
     return cuda_rc(q8::launch_rmsnorm_q8_1(*dev, a, mmq, m, k, type, (cudaStream_t)stream));
 }
 

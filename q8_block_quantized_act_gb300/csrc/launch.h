@@ -103,7 +103,7 @@ struct NormArgs {
     void *residual_out, *y, *q;
     float *d;
     int64_t ldx, ldr, ldro, ldm;
-    float eps;
+    float eps, inv_k;   // inv_k = 1 / k
     int wtype;
 };
 cudaError_t launch_rmsnorm_q8_1(const DeviceInfo &dev, const NormArgs &a, bool mmq, int64_t m, int64_t k, int type,

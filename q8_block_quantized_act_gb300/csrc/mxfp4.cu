@@ -7,6 +7,26 @@
 namespace q8 {
 namespace {
 
+// The largest absolute bits of 8 values, as those of an f32 (infinities and NaN above all others):
+// in 16-bit types the comparison takes two values an instruction.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_bits(const uint4 (&u)[sizeof(T) / 2])
+{
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
+        return a;
+    } else {
+        const uint32_t keep = 0x7fff7fffu;
+        const uint32_t p = __vmaxu2(__vmaxu2(u[0].x & keep, u[0].y & keep), __vmaxu2(u[0].z & keep, u[0].w & keep));
+        const uint32_t a = max(p & 0xffffu, p >> 16);
+        if constexpr (std::is_same<T, __half>::value) return __float_as_uint(half_bits_to_float(a));
+        else return a << 16;
+    }
+}
+
 // A thread has 8 consecutive values of each of ROWS rows, 4 lanes a block; the four scale bytes of
 // 128 values leave as one word.  Rows m .. 128 ceil(m / 128) - 1 get zero scale bytes, so that the
 // whole scale array is defined.
@@ -30,6 +50,12 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict
                                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
+            uint32_t a = largest_bits<T>(in[j]);
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            const uint32_t b = mx_scale_byte(a);
+            uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
+            word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
             float v[8];
             if constexpr (sizeof(T) == 4) {
                 float lo[4], hi[4];
@@ -40,28 +66,38 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict
             } else {
                 unpack<T>(in[j][0], v);
             }
-            uint32_t a = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const uint32_t b = mx_scale_byte(a);
             const float inv = b == 255u ? 0.0f : mx_inverse(b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = b == 255u ? 0.0f : v[i] * inv;
-            uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
-            word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-            if (r0 + j < m) codes[(r0 + j) * chunks + c] = mx_codes8(v);
+            for (int i = 0; i < 8; i += 2) {
+                const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv));
+                v[i] = p.x;
+                v[i + 1] = p.y;
+            }
+            if (r0 + j < m) codes[(r0 + j) * chunks + c] = b == 255u ? 0u : mx_codes8(v);
             if ((c & 15) == 0)
                 *reinterpret_cast<uint32_t *>(scales + mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)) = r0 + j < m ? word : 0u;
         }
     }
 }
 
-// A code's value times 2^-126 is the f32 whose exponent and top fraction bits are the code's.
-__device__ __forceinline__ float mx_code_value(uint32_t code)
+// The values of eight codes (two at a time through binary16, which holds them exactly).
+__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8])
 {
-    return __uint_as_float(((code & 8u) << 28) | ((code & 7u) << 22)) * __uint_as_float(253u << 23);
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 
 // A thread has 8 codes of each of ROWS rows.
@@ -87,8 +123,13 @@ __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__re
             const float s = mx_scale(b[j]);
             uint4 *dst = reinterpret_cast<uint4 *>(y + (r0 + j) * k + (int64_t)c * 8);
             float v[8];
+            mx_values8(w[j], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mx_code_value(w[j] >> (4 * i)) * s;
+            for (int i = 0; i < 8; i += 2) {
+                const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(s, s));
+                v[i] = p.x;
+                v[i + 1] = p.y;
+            }
             if constexpr (sizeof(T) == 4) {
                 dst[0] = pack<T>({v[0], v[1], v[2], v[3]});
                 dst[1] = pack<T>({v[4], v[5], v[6], v[7]});

@@ -28,29 +28,6 @@ __device__ __forceinline__ float div127(float a)
     return a == __int_as_float(0x7f800000) ? a : q1;
 }
 
-// One value of a block with scale d: its quant as an integer-valued float (+0 for zero).  rc is
-// block_rcp(d).  For a value whose approximate quotient qa = v * rc lies farther than 1e-4 from
-// every half-integer, its nearest integer is round-half-away(fl(v / d)): qa differs from v / d by
-// under 4e-5 (|v / d| <= 127; the reciprocal's relative error is at most 2^-23, the product's 2^-24)
-// and fl(v / d) from v / d by under 8e-6, so all three round to the same integer, at most 127, and no
-// tie is involved.  The test |qa - t| < 0.4999 selects exactly those values; the rest (near a
-// half-integer, or qa not finite) take the IEEE division and the rounding of the scalar formula.
-// The nearest integer comes from adding and subtracting 1.5 * 2^23 (unit spacing there), which
-// unlike the rounding instruction runs at the adders' full rate.
-__device__ __forceinline__ float quantize_value(float v, float d, float rc)
-{
-    const float qa = __fmul_rn(v, rc);
-    float t = __fsub_rn(__fadd_rn(qa, 12582912.0f), 12582912.0f);
-    if (!(fabsf(__fsub_rn(qa, t)) < 0.4999f)) {
-        t = roundf(__fdiv_rn(v, d));
-        if (t > 127.0f) t = 127.0f;
-        if (t < -127.0f) t = -127.0f;
-        if (!(t == t)) t = 0.0f;       // NaN quantizes to 0
-        t = __fadd_rn(t, 0.0f);        // -0 -> +0
-    }
-    return t;
-}
-
 // 1 / d, approximately; 0 for d = 0 (every finite value of the block quantizes to 0), and NaN for a
 // subnormal d, whose rounding may leave quotients above 127: all its values take the division.
 __device__ __forceinline__ float block_rcp(float d)
@@ -58,13 +35,32 @@ __device__ __forceinline__ float block_rcp(float d)
     return d >= 1.17549435e-38f ? rcp_approx(d) : d == 0.0f ? 0.0f : __int_as_float(0x7fffffff);
 }
 
-// V consecutive values of a block whose 32 values are spread over 32 / V lanes.
+// The scalar formula for one value of a block with scale d: the IEEE division, round half away.
+// Rare, and kept out of the callers' unrolled code.
+static __device__ __noinline__ float quantize_exactly(float v, float d)
+{
+    float t = roundf(__fdiv_rn(v, d));
+    if (t > 127.0f) t = 127.0f;
+    if (t < -127.0f) t = -127.0f;
+    if (!(t == t)) t = 0.0f;           // NaN quantizes to 0
+    return __fadd_rn(t, 0.0f);         // -0 -> +0
+}
+
+// V consecutive values of a block whose 32 values are spread over 32 / V lanes: their quants as
+// integer-valued floats (+0 for zero).
 template <int V>
 struct BlockQ {
     float t[V];
     float d;
 };
 
+// For a value whose approximate quotient qa = v * block_rcp(d) lies farther than 1e-4 from every
+// half-integer, its nearest integer is round-half-away(fl(v / d)): qa differs from v / d by under
+// 4e-5 (|v / d| <= 127; the reciprocal's relative error is at most 2^-23, the product's 2^-24) and
+// fl(v / d) from v / d by under 8e-6, so all three round to the same integer, at most 127, and no tie
+// is involved.  The test |qa - t| < 0.4999 holds for exactly those values; a thread with one that
+// fails it (near a half-integer, or qa not finite) takes the scalar formula for that one.  The nearest integer
+// comes from adding and subtracting 1.5 * 2^23 (unit spacing there), two values an instruction.
 template <int V>
 __device__ __forceinline__ BlockQ<V> quantize_block(const float (&v)[V])
 {
@@ -76,8 +72,22 @@ __device__ __forceinline__ BlockQ<V> quantize_block(const float (&v)[V])
     BlockQ<V> r;
     r.d = div127(a);
     const float rc = block_rcp(r.d);
+    const float2 rc2 = make_float2(rc, rc), big = make_float2(12582912.0f, 12582912.0f);
+    bool fine = true;
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.t[i] = quantize_value(v[i], r.d, rc);
+    for (int i = 0; i < V; i += 2) {
+        const float2 qa = __fmul2_rn(make_float2(v[i], v[i + 1]), rc2);
+        const float2 t = __fadd2_rn(__fadd2_rn(qa, big), make_float2(-big.x, -big.y));
+        const float2 e = __ffma2_rn(t, make_float2(-1.0f, -1.0f), qa);          // qa - t, rounded once
+        fine = fine && fabsf(e.x) < 0.4999f && fabsf(e.y) < 0.4999f;
+        r.t[i] = t.x;
+        r.t[i + 1] = t.y;
+    }
+    if (!fine) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (!(fabsf(__fsub_rn(__fmul_rn(v[i], rc), r.t[i])) < 0.4999f)) r.t[i] = quantize_exactly(v[i], r.d);
+    }
     return r;
 }
 

@@ -33,21 +33,41 @@ __device__ __forceinline__ void load_weights(const W *w, float (&f)[V])
     }
 }
 
+// Two products an instruction.
+template <int V>
+__device__ __forceinline__ void times(float (&v)[V], const float (&w)[V])
+{
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        const float2 p = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(w[j], w[j + 1]));
+        v[j] = p.x;
+        v[j + 1] = p.y;
+    }
+}
+template <int V>
+__device__ __forceinline__ void times(float (&v)[V], float f)
+{
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        const float2 p = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(f, f));
+        v[j] = p.x;
+        v[j + 1] = p.y;
+    }
+}
+
 // y's quants and scale: V values of the block that starts at a multiple of 32 / V lanes.
 template <typename T, bool MMQ>
 __device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k, int c, float (&v)[VEC<T>], float inv)
 {
     constexpr int V = VEC<T>;
     const int64_t i = (int64_t)c * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = v[j] * inv;
+    times<V>(v, inv);
     if (a.weight) {
         float w[V];
         if (a.wtype == Q8ACT_F32) load_weights<V>(static_cast<const float *>(a.weight) + i, w);
         else if (a.wtype == Q8ACT_F16) load_weights<V>(static_cast<const __half *>(a.weight) + i, w);
         else load_weights<V>(static_cast<const __nv_bfloat16 *>(a.weight) + i, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] *= w[j];
+        times<V>(v, w);
     }
     if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + t * k + i) = pack<T>(v);
     const BlockQ<V> b = quantize_block<V>(v);
@@ -102,32 +122,38 @@ __device__ __forceinline__ void add_residual(uint4 x, uint4 r, bool add, float (
     }
 }
 
-// A CTA per row, CH 16-byte chunks a thread.  chunks = k / V is a multiple of 32, so a warp's chunk
+// CH 16-byte chunks of a row in each thread.  chunks = k / V is a multiple of 32, so a warp's chunk
 // is inside the row for all of its lanes or for none, as the block's shuffles need.
-template <typename T, bool MMQ, int CH>
-__global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
+template <int CH>
+struct RowRegs {
+    uint4 x[CH], r[CH];
+};
+
+template <typename T, int CH>
+__device__ __forceinline__ void load_row(const NormArgs &a, int64_t t, int chunks, RowRegs<CH> &v)
 {
-    constexpr int V = VEC<T>;
-    __shared__ float part[32];
-    griddep_enter();
-    const int chunks = k / V;
-    const int64_t t = blockIdx.x;
     const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.ldx);
-    const uint4 *r = a.residual ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr) : nullptr;
-    uint4 xv[CH], rv[CH];
+    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
-        xv[i] = c < chunks ? x[c] : make_uint4(0, 0, 0, 0);
-        rv[i] = r && c < chunks ? r[c] : make_uint4(0, 0, 0, 0);
+        v.x[i] = c < chunks ? x[c] : make_uint4(0, 0, 0, 0);
+        if (a.residual) v.r[i] = c < chunks ? r[c] : make_uint4(0, 0, 0, 0);
     }
-    float v[CH][V], ss = 0.0f;
+}
+
+template <typename T, bool MMQ, int CH>
+__device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t, int k, int chunks, float (&v)[CH][VEC<T>], float *part)
+{
+    constexpr int V = VEC<T>;
+    float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        add_residual<T>(xv[i], rv[i], r != nullptr, v[i]);
+    for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    }
+        for (int j = 0; j < V; j += 2) {
+            const float2 p = make_float2(v[i][j], v[i][j + 1]);
+            ss = __ffma2_rn(p, p, ss);
+        }
     if (a.residual_out) {
         T *out = static_cast<T *>(a.residual_out) + t * a.ldro;
 #pragma unroll
@@ -136,12 +162,27 @@ __global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
             if (c < chunks) *reinterpret_cast<uint4 *>(out + (int64_t)c * V) = pack<T>(v[i]);
         }
     }
-    const float inv = __fdiv_rn(1.0f, sqrtf(cta_sum(ss, part) / (float)k + a.eps));
+    const float inv = rsqrtf(cta_sum(ss.x + ss.y, part) * a.inv_k + a.eps);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c < chunks) store_block<T, MMQ>(a, t, k, c, v[i], inv);
     }
+}
+
+// A CTA per row.
+template <typename T, bool MMQ, int CH>
+__global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
+{
+    __shared__ float part[32];
+    griddep_enter();
+    const int chunks = k / VEC<T>;
+    RowRegs<CH> in;
+    load_row<T>(a, blockIdx.x, chunks, in);
+    float v[CH][VEC<T>];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) add_residual<T>(in.x[i], in.r[i], a.residual != nullptr, v[i]);
+    norm_row<T, MMQ, CH>(a, blockIdx.x, k, chunks, v, part);
 }
 
 // Rows too long for registers: read twice (the second time from L2).
@@ -162,7 +203,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
 #pragma unroll
         for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
     }
-    const float inv = __fdiv_rn(1.0f, sqrtf(cta_sum(ss, part) / (float)k + a.eps));
+    const float inv = rsqrtf(cta_sum(ss, part) * a.inv_k + a.eps);
     for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
         float v[V];
         add_residual<T>(x[c], r ? r[c] : make_uint4(0, 0, 0, 0), r != nullptr, v);
@@ -175,13 +216,16 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
 template <typename T, bool MMQ>
 cudaError_t launch_rows(const DeviceInfo &dev, const NormArgs &a, int64_t m, int64_t k, cudaStream_t stream)
 {
-    const int chunks = (int)(k / VEC<T>);
+    const int chunks = (int)(k / VEC<T>);                  // a multiple of 32
     const dim3 grid((unsigned)m);
-    // Few rows: every thread that a CTA can have, one chunk each if that is enough (latency).
-    // Many rows: 256 threads with up to 16 values each, several CTAs to an SM (throughput).
-    int threads = m <= 2 * dev.num_sms ? 1024 : 256;
-    while (threads < 1024 && chunks > threads * (16 / VEC<T>)) threads *= 2;
-    if (threads > chunks) threads = chunks;              // a multiple of 32
+    // Few rows: every thread that a CTA can have, one chunk each if that is enough (latency).  Many:
+    // small CTAs with 32 values a thread (8 of f32), so that several rows are under way on an SM and
+    // one row's barrier leaves the others working (4093 x 8192 f16: 256 threads 31.5 us, 512 threads
+    // 38.9; 4093 x 4096 f32: 512 threads of 8 values 22.2 us, 256 of 16 25.4).
+    constexpr int CHUNKS = VEC<T> == 8 ? 4 : 2;
+    int threads = m <= 4 * dev.num_sms ? 1024 : 256;
+    while (threads < 1024 && chunks > threads * CHUNKS) threads *= 2;
+    if (threads > chunks) threads = chunks;
     const int each = (chunks + threads - 1) / threads;
     if (each == 1) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 1>, grid, threads, 0, stream, a, (int)k);
     if (each == 2) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 2>, grid, threads, 0, stream, a, (int)k);
