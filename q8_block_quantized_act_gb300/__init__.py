@@ -29,7 +29,7 @@ from ._lib import (  # noqa: F401  (re-exported ABI)
     q8act_debug_gemv_q6_k_block_dots, q8act_debug_gemv_q4_k_block_dots, q8act_debug_gemv_q5_k_block_dots,
     Q8ACT_ERR_TYPE, Q8ACT_F32, Q8ACT_F16, Q8ACT_BF16, Q8ACT_MAX_TOP, q8act_rmsnorm_q8_1, q8act_rmsnorm_q8_1_mmq,
     q8act_mxfp4_scale_bytes, q8act_quantize_mxfp4, q8act_dequant_mxfp4, q8act_tile_mxfp4_scales,
-    q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq, q8act_logprobs)
+    q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq, q8act_logprobs, _s)
 
 QK = 32
 Q8_0_BYTES = 34
@@ -225,14 +225,23 @@ def gemv_kq(fmt: str, w, xq, xd, n: int, out=None):
     return y
 
 
+# The calls below take several element types, row strides and caller's buffers; they are made once
+# per layer and token, so their checks are kept to a few attribute reads (a microsecond or two a
+# call) and the addresses go straight to the C ABI.
 _TYPES: dict = {}
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _TYPES.update({torch.float32: Q8ACT_F32, torch.float16: Q8ACT_F16, torch.bfloat16: Q8ACT_BF16})
+    _torch = torch
+    return torch
 
 
 def _type(t, what: str) -> int:
     """The element type code of a tensor."""
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.float32: Q8ACT_F32, torch.float16: Q8ACT_F16, torch.bfloat16: Q8ACT_BF16})
     code = _TYPES.get(t.dtype)
     if code is None:
         raise Q8ActError(Q8ACT_ERR_TYPE, f"{what}: {t.dtype}")
@@ -249,45 +258,45 @@ def _rows(t, what: str) -> int:
 
 
 def _given(t, shape, dtype, what: str):
-    """Check a caller's buffer: the kernels write or read exactly `shape`."""
+    """The address of a caller's buffer: the kernels write or read exactly `shape`."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise Q8ActError(Q8ACT_ERR_TYPE, f"{what}: {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: contiguous {tuple(shape)}")
-    return t
+    raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: contiguous {tuple(shape)}")
 
 
 def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out):
-    import torch
-    what = "q8act_rmsnorm_q8_1_mmq" if mmq else "q8act_rmsnorm_q8_1"
+    torch = _torch or _load_torch()
     ldx, code = _rows(x, "x"), _type(x, "x")
     m, k = shape = x.shape
+    dtype = x.dtype
+    pr = pro = pw = py = None
     ldr = ldro = wtype = 0
     if residual is not None:
-        ldr = _rows(residual, "residual")
-        if residual.dtype != x.dtype or residual.shape != shape:
+        ldr, pr = _rows(residual, "residual"), residual.data_ptr()
+        if residual.dtype is not dtype or residual.shape != shape:
             raise Q8ActError(Q8ACT_ERR_TYPE, "residual: x's type and shape")
     if residual_out is not None:
-        ldro = _rows(residual_out, "residual_out")
-        if residual_out.dtype != x.dtype or residual_out.shape != shape:
+        ldro, pro = _rows(residual_out, "residual_out"), residual_out.data_ptr()
+        if residual_out.dtype is not dtype or residual_out.shape != shape:
             raise Q8ActError(Q8ACT_ERR_TYPE, "residual_out: x's type and shape")
     if weight is not None:
-        wtype = _type(weight, "weight")
-        _given(weight, (k,), weight.dtype, "weight")
+        wtype, pw = _type(weight, "weight"), _given(weight, (k,), weight.dtype, "weight")
     if y is not None:
-        _given(y, shape, x.dtype, "y")
+        py = _given(y, shape, dtype, "y")
     qtype, dshape = (torch.uint16, (k // QK, (m + 3) // 4 * 4)) if mmq else (torch.int8, (m, k // QK))
-    if out is not None:
-        q, d = _given(out[0], shape, qtype, "quants"), _given(out[1], dshape, torch.float32, "scales")
-    else:
-        q = torch.empty(shape, dtype=qtype, device=x.device)
-        d = torch.empty(dshape, dtype=torch.float32, device=x.device)
-    fn = q8act_rmsnorm_q8_1_mmq if mmq else q8act_rmsnorm_q8_1
-    rc = fn(x, ldx, residual, ldr, weight, wtype, eps, residual_out, ldro, y, q, d, m, k, code)
+    if out is None:
+        out = (torch.empty(shape, dtype=qtype, device=x.device), torch.empty(dshape, dtype=torch.float32, device=x.device))
+    q, d = out
+    pq, pd = _given(q, shape, qtype, "quants"), _given(d, dshape, torch.float32, "scales")
+    L = lib()
+    fn = L.q8act_rmsnorm_q8_1_mmq if mmq else L.q8act_rmsnorm_q8_1
+    rc = fn(x.data_ptr(), ldx, pr, ldr, pw, wtype, eps, pro, ldro, py, pq, pd, m, k, code, _s(None))
     if rc:
-        raise Q8ActError(rc, what)
+        raise Q8ActError(rc, "q8act_rmsnorm_q8_1_mmq" if mmq else "q8act_rmsnorm_q8_1")
     return q, d
 
 
@@ -306,24 +315,23 @@ def rmsnorm_q8_1_mmq(x, weight=None, eps: float = 1e-6, residual=None, residual_
 
 
 def _mxfp4_scales(rows: int, k: int):
-    nbytes = q8act_mxfp4_scale_bytes(rows, k)
-    if nbytes == 0:
+    """Shape of a tiled scale array (q8act_mxfp4_scale_bytes)."""
+    if rows < 1 or k < 1 or k % 256 or k > Q8ACT_MAX_K:
         raise Q8ActError(Q8ACT_ERR_DIMS, f"MXFP4 matrix of {rows} x {k}")
-    return (nbytes,)
+    return ((rows + 127) // 128 * (k // 128) * 512,)
 
 
 def quantize_mxfp4(x, out=None):
     """float32, float16 or bfloat16 [m, k] -> MXFP4 (codes uint8 [m, k/2], tiled scales uint8)."""
-    import torch
+    torch = _torch or _load_torch()
     ldx, code = _rows(x, "x"), _type(x, "x")
     m, k = x.shape
-    nsc = _mxfp4_scales(m, k)
-    if out is not None:
-        codes, scales = _given(out[0], (m, k // 2), torch.uint8, "codes"), _given(out[1], nsc, torch.uint8, "scales")
-    else:
-        codes = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(nsc, dtype=torch.uint8, device=x.device)
-    rc = q8act_quantize_mxfp4(x, ldx, code, codes, scales, m, k)
+    u8, nsc = torch.uint8, _mxfp4_scales(m, k)
+    if out is None:
+        out = (torch.empty((m, k // 2), dtype=u8, device=x.device), torch.empty(nsc, dtype=u8, device=x.device))
+    codes, scales = out
+    rc = lib().q8act_quantize_mxfp4(x.data_ptr(), ldx, code, _given(codes, (m, k // 2), u8, "codes"),
+                                    _given(scales, nsc, u8, "scales"), m, k, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_quantize_mxfp4")
     return codes, scales
@@ -331,28 +339,28 @@ def quantize_mxfp4(x, out=None):
 
 def dequant_mxfp4(codes, scales, dtype=None, out=None):
     """MXFP4 (codes, tiled scales) -> values [m, k] in dtype (default float16) or out's type."""
-    import torch
+    torch = _torch or _load_torch()
     m, half = codes.shape
-    k = 2 * half
-    _given(codes, (m, half), torch.uint8, "codes")
-    _given(scales, _mxfp4_scales(m, k), torch.uint8, "scales")
-    if out is not None:
-        y = _given(out, (m, k), out.dtype, "out")
-    else:
-        y = torch.empty((m, k), dtype=dtype or torch.float16, device=codes.device)
-    rc = q8act_dequant_mxfp4(codes, scales, y, _type(y, "out"), m, k)
+    k, u8 = 2 * half, torch.uint8
+    pc, ps = _given(codes, (m, half), u8, "codes"), _given(scales, _mxfp4_scales(m, k), u8, "scales")
+    if out is None:
+        out = torch.empty((m, k), dtype=dtype or torch.float16, device=codes.device)
+    code = _type(out, "out")
+    rc = lib().q8act_dequant_mxfp4(pc, ps, _given(out, (m, k), out.dtype, "out"), code, m, k, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_dequant_mxfp4")
-    return y
+    return out
 
 
 def tile_mxfp4_scales(scales):
     """Row-major e8m0 bytes [m, k/32] -> the tiled scales that the MXFP4 calls take."""
-    import torch
+    torch = _torch or _load_torch()
     m, kb = scales.shape
-    _given(scales, (m, kb), torch.uint8, "scales")
+    ps = _given(scales, (m, kb), torch.uint8, "scales")
     tiled = torch.empty(_mxfp4_scales(m, kb * QK), dtype=torch.uint8, device=scales.device)
-    check(q8act_tile_mxfp4_scales(scales, tiled, m, kb * QK), "q8act_tile_mxfp4_scales")
+    rc = lib().q8act_tile_mxfp4_scales(ps, tiled.data_ptr(), m, kb * QK, _s(None))
+    if rc:
+        raise Q8ActError(rc, "q8act_tile_mxfp4_scales")
     return tiled
 
 
@@ -365,52 +373,45 @@ def gemm_mxfp4_workspace(m: int, k: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _mxfp4_weights(w, wscales):
-    import torch
-    n, half = w.shape
-    _given(w, (n, half), torch.uint8, "w")
-    _given(wscales, _mxfp4_scales(n, 2 * half), torch.uint8, "wscales")
-    return n, 2 * half
-
-
 def gemm_mxfp4(w, wscales, x, ws=None, dtype=None, out=None):
     """x [m, k] (float32, float16, bfloat16; quantized to MXFP4 in the call) times MXFP4 weights
     (codes w [n, k/2], tiled scales): y [m, n] in dtype (default float32) or out's type."""
-    import torch
-    n, k = _mxfp4_weights(w, wscales)
+    torch = _torch or _load_torch()
+    n, half = w.shape
+    k, u8 = 2 * half, torch.uint8
+    pw, psc = _given(w, (n, half), u8, "w"), _given(wscales, _mxfp4_scales(n, k), u8, "wscales")
     ldx, code = _rows(x, "x"), _type(x, "x")
     m = x.shape[0]
     if x.shape[1] != k:
         raise Q8ActError(Q8ACT_ERR_DIMS, f"x: {x.shape[1]} columns for weights of {k}")
     if ws is None:
         ws = gemm_mxfp4_workspace(m, k, x.device)
-    elif not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
+    elif not (ws.is_cuda and ws.dtype is u8 and ws.is_contiguous()):
         raise Q8ActError(Q8ACT_ERR_WORKSPACE, "ws: contiguous uint8 on the GPU")
-    if out is not None:
-        y = _given(out, (m, n), out.dtype, "out")
-    else:
-        y = torch.empty((m, n), dtype=dtype or torch.float32, device=x.device)
-    rc = q8act_gemm_mxfp4(w, wscales, x, ldx, code, y, _type(y, "out"), m, n, k, ws, ws.numel())
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype or torch.float32, device=x.device)
+    ycode = _type(out, "out")
+    rc = lib().q8act_gemm_mxfp4(pw, psc, x.data_ptr(), ldx, code, _given(out, (m, n), out.dtype, "out"), ycode, m, n, k,
+                                ws.data_ptr(), ws.numel(), _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4")
-    return y
+    return out
 
 
 def gemm_mxfp4_preq(w, wscales, xq, xscales, dtype=None, out=None):
     """The product on an activation already in MXFP4 (quantize_mxfp4)."""
-    import torch
-    n, k = _mxfp4_weights(w, wscales)
-    m = xq.shape[0]
-    _given(xq, (m, k // 2), torch.uint8, "xq")
-    _given(xscales, _mxfp4_scales(m, k), torch.uint8, "xscales")
-    if out is not None:
-        y = _given(out, (m, n), out.dtype, "out")
-    else:
-        y = torch.empty((m, n), dtype=dtype or torch.float32, device=xq.device)
-    rc = q8act_gemm_mxfp4_preq(w, wscales, xq, xscales, y, _type(y, "out"), m, n, k)
+    torch = _torch or _load_torch()
+    n, half = w.shape
+    k, u8, m = 2 * half, torch.uint8, xq.shape[0]
+    pw, psc = _given(w, (n, half), u8, "w"), _given(wscales, _mxfp4_scales(n, k), u8, "wscales")
+    px, pxs = _given(xq, (m, half), u8, "xq"), _given(xscales, _mxfp4_scales(m, k), u8, "xscales")
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype or torch.float32, device=xq.device)
+    ycode = _type(out, "out")
+    rc = lib().q8act_gemm_mxfp4_preq(pw, psc, px, pxs, _given(out, (m, n), out.dtype, "out"), ycode, m, n, k, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4_preq")
-    return y
+    return out
 
 
 def logprobs(logits, tokens=None, top: int = 0, out=None):
@@ -418,28 +419,23 @@ def logprobs(logits, tokens=None, top: int = 0, out=None):
     probability of tokens[row] (int32; negative: none, 0), the entropy, and the `top` most likely
     ids (int32 [m, top], equal logits by the lower id, -1 beyond the unmasked ones) with their
     log probabilities.  Returns (logprob or None, entropy, ids, top_logprobs)."""
-    import torch
+    torch = _torch or _load_torch()
     ld, code = _rows(logits, "logits"), _type(logits, "logits")
     m, v = logits.shape
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    f32, i32 = torch.float32, torch.int32
+    ptok = plp = pids = ptlp = None
+    if out is None:
+        dev, n = logits.device, max(top, 0)
+        out = (torch.empty(m, dtype=f32, device=dev) if tokens is not None else None,
+               torch.empty(m, dtype=f32, device=dev), torch.empty((m, n), dtype=i32, device=dev),
+               torch.empty((m, n), dtype=f32, device=dev))
+    lp, ent, ids, tlp = out
     if tokens is not None:
-        _given(tokens, (m,), i32, "tokens")
-    if out is not None:
-        lp, ent, ids, tlp = out
-        if tokens is not None:
-            _given(lp, (m,), f32, "logprob")
-        _given(ent, (m,), f32, "entropy")
-        if top > 0:
-            _given(ids, (m, top), i32, "ids")
-            _given(tlp, (m, top), f32, "top_logprobs")
-    else:
-        n = max(top, 0)
-        lp = torch.empty(m, dtype=f32, device=dev) if tokens is not None else None
-        ent, ids = torch.empty(m, dtype=f32, device=dev), torch.empty((m, n), dtype=i32, device=dev)
-        tlp = torch.empty((m, n), dtype=f32, device=dev)
-    some = top > 0
-    rc = q8act_logprobs(logits, ld, code, tokens, lp if tokens is not None else None, ent, ids if some else None,
-                        tlp if some else None, m, v, top)
+        ptok, plp = _given(tokens, (m,), i32, "tokens"), _given(lp, (m,), f32, "logprob")
+    if top > 0:
+        pids, ptlp = _given(ids, (m, top), i32, "ids"), _given(tlp, (m, top), f32, "top_logprobs")
+    rc = lib().q8act_logprobs(logits.data_ptr(), ld, code, ptok, plp, _given(ent, (m,), f32, "entropy"), pids, ptlp, m, v,
+                              top, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_logprobs")
     return lp, ent, ids, tlp

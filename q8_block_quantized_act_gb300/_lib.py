@@ -71,6 +71,8 @@ _LIB = None
 def lib() -> ctypes.CDLL:
     """Load libq8act.so (once).  Raises if it has not been built."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             if not os.path.exists(LIB_PATH):
@@ -140,10 +142,19 @@ def _p(v):
     return v.data_ptr()
 
 
+_RAW_STREAM = None
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch's current stream on the current device, without building a Stream object (3 us)
+        global _RAW_STREAM
+        if _RAW_STREAM is None:
+            import torch
+            torch.cuda.current_stream()              # brings CUDA up
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _RAW_STREAM = lambda: raw(device())      # noqa: E731
+        return _RAW_STREAM()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
