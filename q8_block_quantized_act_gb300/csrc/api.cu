@@ -663,6 +663,13 @@ int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t 
     if (rc) return rc;
     if (!ws || ws_bytes < q8act_gemm_mxfp4_workspace_bytes(m, k)) return Q8ACT_ERR_WORKSPACE;
     if (!aligned16(w) || !aligned16(wscales) || !aligned16(y) || !aligned16(ws)) return Q8ACT_ERR_ALIGN;
+    if ((rc = check_rows(x, ldx, k, xtype))) return rc;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    if (q8::gemm_mxfp4_quantizes(*dev, m, n, k))
+        return cuda_rc(q8::launch_gemm_mxfp4_own(*dev, static_cast<const uint8_t *>(w),
+                                                 static_cast<const uint8_t *>(wscales), x, ldx, xtype, y, ytype, m, n, k,
+                                                 (cudaStream_t)stream));
     uint8_t *xq = static_cast<uint8_t *>(ws), *xsc = xq + ((size_t)m * k / 2 + 255) / 256 * 256;
     rc = q8act_quantize_mxfp4(x, ldx, xtype, xq, xsc, m, k, stream);
     if (rc) return rc;

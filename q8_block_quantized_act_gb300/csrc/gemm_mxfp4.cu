@@ -32,20 +32,24 @@ constexpr int SC_BYTES = BK / MX_TILE_K * MX_TILE_BYTES;   // a 128-row scale ti
 constexpr int THREADS = 192;
 constexpr int SMEM_MAX = 232448;
 
-template <int BN_, int STAGES_>
+// XSTEPS > 0: the CTA quantizes the activation itself and keeps its part of k (at most XSTEPS steps)
+// in shared memory for all of its tiles; the stages then hold weights alone.
+template <int BN_, int STAGES_, int XSTEPS_ = 0>
 struct Cfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
+    static constexpr int XSTEPS = XSTEPS_;
+    static constexpr int XSLOTS = XSTEPS > 0 ? XSTEPS : STAGES;
     static constexpr int NSB = BN > 128 ? 2 : 1;             // scale tiles that BN tokens touch
     static constexpr int B_BYTES = BN * ROW_BYTES;
     static constexpr bool SPLIT = BN <= 128;                 // room for the cluster's partial sums
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
-    static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_SA = OFF_B + XSLOTS * B_BYTES;
     static constexpr int OFF_SB = OFF_SA + STAGES * SC_BYTES;
-    static constexpr int OFF_RED = OFF_SB + STAGES * NSB * SC_BYTES;
+    static constexpr int OFF_RED = OFF_SB + XSLOTS * NSB * SC_BYTES;
     static constexpr int OFF_BAR = OFF_RED + (SPLIT ? BN * BM * 4 : 0);
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4 + 3) * 8;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4 + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;   // + slack for 1024-byte base alignment
     // Tensor memory: two accumulators, then two slots of scales (weights 8 columns, tokens 8 per
     // scale tile), so that a step's copies do not wait for the previous step's MMAs.
@@ -138,18 +142,20 @@ struct Work {
     int first_wait;   // 1: the weights too may come from the kernel before this one
 };
 
-template <typename C, typename T>
+// X: the activation's type where the CTA quantizes it (xf, rows ldx elements apart), else unused.
+template <typename C, typename T, typename X>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                      const uint8_t *__restrict__ wsc, const uint8_t *__restrict__ xsc, T *__restrict__ y, Work wk,
-                      int CL, int *status)
+                      const uint8_t *__restrict__ wsc, const uint8_t *__restrict__ xsc, const X *__restrict__ xf,
+                      int64_t ldx, T *__restrict__ y, Work wk, int CL, int *status)
 {
+    constexpr bool OWN_X = C::XSTEPS > 0;
     constexpr int BN = C::BN, STAGES = C::STAGES, NSB = C::NSB, B_BYTES = C::B_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + STAGES, *acc_full = empty + STAGES, *acc_empty = acc_full + 2;
-    uint64_t *red_full = acc_empty + 2, *red_empty = red_full + 1, *drained = red_empty + 1;
+    uint64_t *red_full = acc_empty + 2, *red_empty = red_full + 1, *drained = red_empty + 1, *x_ready = drained + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
@@ -166,13 +172,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(red_full, 4 * CL);
         mbar_init(red_empty, 4 * CL);
         mbar_init(drained, 1);
+        mbar_init(x_ready, 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 5) tc_alloc(tmem_slot, C::TMEM_COLS);
     if (warp == 4 && lane == 0) {
         prefetch_tensormap(&tm_w);
-        prefetch_tensormap(&tm_x);
+        if (!OWN_X) prefetch_tensormap(&tm_x);
     }
     tc_fence_before();
     __syncthreads();
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             nsb = min(NSB, last_sb - sb0);
             wsp = wsc + rt * sc_tile + ks0 * SC_BYTES;
             xsp = xsc + sb0 * sc_tile + ks0 * SC_BYTES;
-            bytes = A_BYTES + B_BYTES + SC_BYTES * (1 + nsb);
+            bytes = A_BYTES + SC_BYTES + (OWN_X ? 0 : B_BYTES + SC_BYTES * nsb);
         };
         auto load_w = [&](int st, int ks) {
             mbar_arrive_expect_tx(&full[st], bytes);
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (elect_one()) {
                     if (it >= early) load_w(st, ks);
-                    load_x(st, ks);
+                    if (!OWN_X) load_x(st, ks);
                 }
                 wsp += SC_BYTES;
                 xsp += SC_BYTES;
@@ -255,7 +262,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SB));
         // Steps go in pairs where the second one's data is there: the tensor pipe runs copies and
         // MMAs in order and pays for each change between them.
-        auto copy_scales = [&](int slot, int st) {
+        auto copy_scales = [&](int slot, int st, int ks) {
+            const int xs = OWN_X ? ks - ks0 : st;     // where the tokens' operand is
             const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {        // the step's two groups of 128 values
@@ -263,13 +271,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int b = 0; b < NSB; ++b)
                     tc_copy_scales(sb + 4 * (NSB * g + b),
-                                   sbdesc0 + (uint64_t)(((st * NSB + b) * SC_BYTES + g * MX_TILE_BYTES) >> 4));
+                                   sbdesc0 + (uint64_t)(((xs * NSB + b) * SC_BYTES + g * MX_TILE_BYTES) >> 4));
             }
         };
-        auto multiply = [&](int slot, int st, uint32_t d_tmem, uint32_t sb_shift, bool first) {
+        auto multiply = [&](int slot, int st, int ks, uint32_t d_tmem, uint32_t sb_shift) {
+            const int xs = OWN_X ? ks - ks0 : st;
+            const bool first = ks == ks0;
             const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8 + sb_shift;
             const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
-            const uint64_t bd = bdesc0 + (uint64_t)(st * (B_BYTES >> 4));
+            const uint64_t bd = bdesc0 + (uint64_t)(xs * (B_BYTES >> 4));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {        // 64 values: bytes 2 (j % 2) and next of each scale word
                 const uint32_t id = C::IDESC | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         int st = 0, i = 0;
         uint32_t phase = 0;
-        bool ok = true;
+        bool ok = !OWN_X || __all_sync(0xffffffffu, wait_or_abort(x_ready, 0, status, abort_flag));
         for (int tile = cluster; ok && tile < wk.tiles; tile += clusters, ++i) {
             const int acc = i & 1;
             ok = __all_sync(0xffffffffu, wait_or_abort(&acc_empty[acc], ((i >> 1) & 1) ^ 1, status, abort_flag));
@@ -294,10 +304,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  __all_sync(0xffffffffu, mbar_try_wait(&full[st1], st1 == 0 ? phase ^ 1 : phase));
                 tc_fence_after();
                 if (elect_one()) {
-                    copy_scales(0, st);
-                    if (two) copy_scales(1, st1);
-                    multiply(0, st, tmem + acc * BN, sb_shift, ks == ks0);
-                    if (two) multiply(1, st1, tmem + acc * BN, sb_shift, false);
+                    copy_scales(0, st, ks);
+                    if (two) copy_scales(1, st1, ks + 1);
+                    multiply(0, st, ks, tmem + acc * BN, sb_shift);
+                    if (two) multiply(1, st1, ks + 1, tmem + acc * BN, sb_shift);
                     if (ks + (two ? 2 : 1) == ks1) tc_commit(&acc_full[acc]);
                 }
                 for (int n = two ? 2 : 1; n; --n, ++ks)
@@ -315,6 +325,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
         const int row = 32 * warp + lane;
         float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
+        if constexpr (OWN_X) {
+            // First the activation: a warp has 256 values of a token at a time, and writes them as
+            // the TMA would have (token rows of 128 bytes, 16-byte units swizzled by the row).
+            griddep_wait();
+            const int tasks = wk.m * (ks1 - ks0);
+            constexpr int DEPTH = 4;                  // loads under way
+            for (int task0 = warp; task0 < tasks; task0 += 4 * DEPTH) {
+                uint4 in[DEPTH][sizeof(X) / 2];
+#pragma unroll
+                for (int d = 0; d < DEPTH; ++d) {
+                    const int task = task0 + 4 * d, t = task % wk.m, s = task / wk.m;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(xf + t * ldx + (int64_t)(ks0 + s) * BK + lane * 8);
+#pragma unroll
+                    for (int h = 0; h < (int)sizeof(X) / 2; ++h) in[d][h] = task < tasks ? src[h] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int d = 0; d < DEPTH; ++d) {
+                    const int task = task0 + 4 * d, t = task % wk.m, s = task / wk.m;
+                    if (task >= tasks) break;
+                    const MxChunk q = mx_quantize8<X>(in[d]);
+                    uint8_t *dst = smem + C::OFF_B + s * B_BYTES + t * ROW_BYTES + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t *>(dst) = q.codes;
+                    if ((lane & 15) == 0)
+                        *reinterpret_cast<uint32_t *>(smem + C::OFF_SB + s * SC_BYTES + (lane >> 4) * MX_TILE_BYTES + t * 16) = q.scales;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_ready);
+        }
         int i = 0;
         for (int tile = cluster; tile < wk.tiles; tile += clusters, ++i) {
             const int acc = i & 1;
@@ -338,36 +378,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[acc]);
             } else if constexpr (C::SPLIT) {
-                const int per = BN / CL;                                // columns that a rank owns
+                // BN and CL are powers of two: rank o owns the BN / CL columns from o BN / CL on.
+                const int per = BN / CL, shift = 31 - __clz(per);
                 if (!__all_sync(0xffffffffu, wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag))) break;
+                const uint32_t mine = smem_u32(red + (int)rank * per * BM + row);
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
                     uint32_t v[16];
                     tc_ld_x16(tmem + lane_base + acc * BN + c0, v);
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        if (c0 + c < cols) {
-                            const int owner = (c0 + c) / per, at = (c0 + c) % per;
-                            cluster_store(cluster_addr(smem_u32(red + ((int)rank * per + at) * BM + row), owner),
+                        if (c0 + c < cols)
+                            cluster_store(cluster_addr(mine + (uint32_t)(((c0 + c) & (per - 1)) * BM * 4), (c0 + c) >> shift),
                                           __uint_as_float(v[c]));
-                        }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&acc_empty[acc]);
-                    for (int c = 0; c < CL; ++c) cluster_arrive(cluster_addr(smem_u32(red_full), c));
-                }
+                if (lane == 0) mbar_arrive(&acc_empty[acc]);
+                if (lane < CL) cluster_arrive(cluster_addr(smem_u32(red_full), lane));
                 if (!__all_sync(0xffffffffu, wait_cluster(red_full, i & 1, status, abort_flag))) break;
                 const int own0 = (int)rank * per;
+#pragma unroll 2
                 for (int c = 0; c < per && own0 + c < cols; ++c) {
-                    float s = red[c * BM + row];
-                    for (int src = 1; src < CL; ++src) s += red[(src * per + c) * BM + row];
-                    if (r < wk.n) dst[(int64_t)(own0 + c) * wk.n] = from_f32<T>(s);
+                    float part[8];
+#pragma unroll
+                    for (int src = 0; src < 8; ++src) part[src] = src < CL ? red[(src * per + c) * BM + row] : 0.0f;
+                    float sum = part[0];
+#pragma unroll
+                    for (int src = 1; src < 8; ++src)
+                        if (src < CL) sum += part[src];                 // in rank order
+                    if (r < wk.n) dst[(int64_t)(own0 + c) * wk.n] = from_f32<T>(sum);
                 }
                 __syncwarp();
-                if (lane == 0)
-                    for (int c = 0; c < CL; ++c) cluster_arrive(cluster_addr(smem_u32(red_empty), c));
+                if (lane < CL) cluster_arrive(cluster_addr(smem_u32(red_empty), lane));
             }
         }
     }
@@ -382,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Clusters of CL CTAs that are resident at once (looked up once per device, kernel and CL).
-template <typename C, typename T>
+template <typename C, typename T, typename X>
 cudaError_t resident_clusters(const DeviceInfo &dev, int CL, int *count)
 {
     static std::atomic<int> known[kAttrDevices][4];
@@ -404,7 +447,7 @@ cudaError_t resident_clusters(const DeviceInfo &dev, int CL, int *count)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int got = 0;
-    cudaError_t e = cudaOccupancyMaxActiveClusters(&got, gemm_mxfp4_kernel<C, T>, &cfg);
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&got, gemm_mxfp4_kernel<C, T, X>, &cfg);
     if (e != cudaSuccess) return e;
     *count = got < dev.num_sms / CL ? got : dev.num_sms / CL;
     if (*count < 1) return cudaErrorInvalidConfiguration;
@@ -412,19 +455,24 @@ cudaError_t resident_clusters(const DeviceInfo &dev, int CL, int *count)
     return cudaSuccess;
 }
 
-template <typename C, typename T>
+// x, xsc: the quantized activation (C::XSTEPS = 0); else xf, ldx: the activation itself.
+template <typename C, typename T, typename X>
 cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
-                         const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, int CL, bool pdl, cudaStream_t stream)
+                         const uint8_t *xsc, const X *xf, int64_t ldx, T *y, int64_t m, int64_t n, int64_t k, int CL,
+                         bool pdl, cudaStream_t stream)
 {
-    cudaError_t e = set_kernel_smem<gemm_mxfp4_kernel<C, T>>(dev.device, C::SMEM_BYTES);
+    cudaError_t e = set_kernel_smem<gemm_mxfp4_kernel<C, T, X>>(dev.device, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int resident = 0;
-    if ((e = resident_clusters<C, T>(dev, CL, &resident)) != cudaSuccess) return e;
+    if ((e = resident_clusters<C, T, X>(dev, CL, &resident)) != cudaSuccess) return e;
     CUtensorMap tm_w, tm_x;
     if (!encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)k / 2, (uint64_t)n, (uint64_t)k / 2, ROW_BYTES, BM,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
-                   C::BN, CU_TENSOR_MAP_SWIZZLE_128B))
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    if (C::XSTEPS > 0)
+        tm_x = tm_w;                                   // unused
+    else if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
+                        C::BN, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     Work wk;
     wk.m = (int)m;
@@ -449,7 +497,7 @@ cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CL > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_kernel<C, T>, tm_w, tm_x, wsc, xsc, y, wk, CL, dev.status);
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_kernel<C, T, X>, tm_w, tm_x, wsc, xsc, xf, ldx, y, wk, CL, dev.status);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -771,6 +819,76 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
 
 }  // namespace
 
+namespace {
+
+// The tile shape of a product and how many CTAs share a tile's k: the least of
+//   waves * (steps of a CTA * time of a step + filling the pipeline and storing the tile + joining)
+// over the tile widths and the powers of two up to 8 that leave each CTA a step.  Times in ns, from
+// measurements: a step of 16 / 32 / 64 / 128 / 192 tokens takes 170 - 400 by its MMAs and 390 - 500
+// where all SMs load their operands at once; a pair's 256 x 256 step 330.  (131 x 4096 x 1280 in tiles
+// of 192 tokens 7.9 us, of 64 6.4; 300 x 1000 x 8192 by pairs 15.8, 128 tokens shared by four CTAs
+// 10.0; 5 x 64448 x 4096, 504 tiles: shared by two 36, not shared 26.)
+struct Plan {
+    int bn, CL;       // bn = 256: pairs
+};
+
+Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
+{
+    const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
+    static const struct { int bn, step, busy, tile; } shapes[] = {
+        {16, 170, 390, 1200}, {32, 200, 410, 1400}, {64, 250, 450, 1800}, {128, 330, 500, 2500}, {192, 400, 500, 3300}};
+    Plan best{256, 1};
+    int64_t least = INT64_MAX;
+    if (m > 128) {
+        const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + 255) / 256), at_once = dev.num_sms / 2;
+        least = (tiles + at_once - 1) / at_once * (steps * 330 + 2500);
+    }
+    for (const auto &s : shapes) {
+        if (s.bn < 64 && m > s.bn) continue;                      // narrow tiles start at a scale tile's first row
+        if (s.bn > 16 && s.bn >= 2 * m) continue;
+        const int64_t tiles = rows * ((m + s.bn - 1) / s.bn);
+        for (int CL = 1; CL <= 8 && CL <= steps; CL *= 2) {
+            if (CL > 1 && s.bn > 128) break;                      // no room for partial sums
+            const int64_t at_once = dev.num_sms / CL - (CL == 8 ? dev.num_sms / 32 : 0);   // GPCs hold few clusters of 8
+            const int64_t waves = (tiles + at_once - 1) / at_once, active = (tiles < at_once ? tiles : at_once) * CL;
+            const int64_t cost = waves * ((steps + CL - 1) / CL * (active * 2 > dev.num_sms ? s.busy : s.step) + s.tile +
+                                          (CL > 1 ? 1200 : 0));
+            if (cost < least) {
+                least = cost;
+                best = {s.bn, CL};
+            }
+        }
+    }
+    return best;
+}
+
+constexpr int OWN_STEPS = 16;       // steps of the activation that a CTA keeps
+constexpr int OWN_TASKS = 32;       // token-steps that four warps quantize in less than a launch's time
+
+}  // namespace
+
+bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
+{
+    const Plan p = plan_tiles(dev, m, n, k);
+    if (p.bn != 16) return false;
+    const int64_t steps = (k / BK + p.CL - 1) / p.CL;
+    return steps <= OWN_STEPS && m * steps <= OWN_TASKS;
+}
+
+cudaError_t launch_gemm_mxfp4_own(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const void *xf, int64_t ldx,
+                                  int xtype, void *y, int type, int64_t m, int64_t n, int64_t k, cudaStream_t stream)
+{
+    return with_type(type, [&](auto t) {
+        using T = decltype(t);
+        return with_type(xtype, [&](auto u) {
+            using X = decltype(u);
+            return launch_tiles<Cfg<16, 8, OWN_STEPS>, T, X>(dev, w, wsc, nullptr, nullptr, static_cast<const X *>(xf), ldx,
+                                                             static_cast<T *>(y), m, n, k, plan_tiles(dev, m, n, k).CL,
+                                                             false, stream);
+        });
+    });
+}
+
 cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
                               const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k, bool pdl,
                               cudaStream_t stream)
@@ -778,20 +896,16 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
     return with_type(type, [&](auto t) {
         using T = decltype(t);
         T *out = static_cast<T *>(y);
-        // As many CTAs to a tile as leave no more than one wave, each with a step at least.
-        const int64_t rows = (n + BM - 1) / BM;
-        auto split = [&](int bn) {
-            const int64_t tiles = rows * ((m + bn - 1) / bn);
-            int CL = 1;
-            while (CL < 8 && tiles * CL * 2 <= dev.num_sms && CL * 2 <= k / BK) CL *= 2;
-            return CL;
+        const Plan p = plan_tiles(dev, m, n, k);
+        auto go = [&](auto cfg) {
+            return launch_tiles<decltype(cfg), T, float>(dev, w, wsc, x, xsc, nullptr, 0, out, m, n, k, p.CL, pdl, stream);
         };
-        if (m <= 16) return launch_tiles<Cfg<16, 9>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(16), pdl, stream);
-        if (m <= 32) return launch_tiles<Cfg<32, 8>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(32), pdl, stream);
-        if (m <= 64) return launch_tiles<Cfg<64, 6>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(64), pdl, stream);
-        if (m <= 128) return launch_tiles<Cfg<128, 4>, T>(dev, w, wsc, x, xsc, out, m, n, k, split(128), pdl, stream);
-        if (m > 192) return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, stream);
-        return launch_tiles<Cfg<192, 5>, T>(dev, w, wsc, x, xsc, out, m, n, k, 1, pdl, stream);
+        if (p.bn == 16) return go(Cfg<16, 9>{});
+        if (p.bn == 32) return go(Cfg<32, 8>{});
+        if (p.bn == 64) return go(Cfg<64, 6>{});
+        if (p.bn == 128) return go(Cfg<128, 4>{});
+        if (p.bn == 192) return go(Cfg<192, 5>{});
+        return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, stream);
     });
 }
 

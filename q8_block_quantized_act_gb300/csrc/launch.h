@@ -122,6 +122,11 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
                               const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k, bool pdl,
                               cudaStream_t stream);
 
+// Few tokens: the product's CTAs quantize the activation themselves (bitwise the same y).
+bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k);
+cudaError_t launch_gemm_mxfp4_own(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const void *xf, int64_t ldx,
+                                  int xtype, void *y, int type, int64_t m, int64_t n, int64_t k, cudaStream_t stream);
+
 // Log probabilities of logits rows (stride ld elements): the given tokens' (tokens, logprob), the
 // entropy and the `top` most likely tokens; each of the three may be left out (null, top = 0).
 struct LogprobArgs {

@@ -7,26 +7,6 @@
 namespace q8 {
 namespace {
 
-// The largest absolute bits of 8 values, as those of an f32 (infinities and NaN above all others):
-// in 16-bit types the comparison takes two values an instruction.
-template <typename T>
-__device__ __forceinline__ uint32_t largest_bits(const uint4 (&u)[sizeof(T) / 2])
-{
-    if constexpr (sizeof(T) == 4) {
-        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
-        return a;
-    } else {
-        const uint32_t keep = 0x7fff7fffu;
-        const uint32_t p = __vmaxu2(__vmaxu2(u[0].x & keep, u[0].y & keep), __vmaxu2(u[0].z & keep, u[0].w & keep));
-        const uint32_t a = max(p & 0xffffu, p >> 16);
-        if constexpr (std::is_same<T, __half>::value) return __float_as_uint(half_bits_to_float(a));
-        else return a << 16;
-    }
-}
-
 // A thread has 8 consecutive values of each of ROWS rows, 4 lanes a block; the four scale bytes of
 // 128 values leave as one word.  Rows m .. 128 ceil(m / 128) - 1 get zero scale bytes, so that the
 // whole scale array is defined.
@@ -50,32 +30,10 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict
                                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            uint32_t a = largest_bits<T>(in[j]);
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const uint32_t b = mx_scale_byte(a);
-            uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
-            word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-            float v[8];
-            if constexpr (sizeof(T) == 4) {
-                float lo[4], hi[4];
-                unpack<T>(in[j][0], lo);
-                unpack<T>(in[j][1], hi);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
-            } else {
-                unpack<T>(in[j][0], v);
-            }
-            const float inv = b == 255u ? 0.0f : mx_inverse(b);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv));
-                v[i] = p.x;
-                v[i + 1] = p.y;
-            }
-            if (r0 + j < m) codes[(r0 + j) * chunks + c] = b == 255u ? 0u : mx_codes8(v);
+            const MxChunk q = mx_quantize8<T>(in[j]);
+            if (r0 + j < m) codes[(r0 + j) * chunks + c] = q.codes;
             if ((c & 15) == 0)
-                *reinterpret_cast<uint32_t *>(scales + mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)) = r0 + j < m ? word : 0u;
+                *reinterpret_cast<uint32_t *>(scales + mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)) = r0 + j < m ? q.scales : 0u;
         }
     }
 }

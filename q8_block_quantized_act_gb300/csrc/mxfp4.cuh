@@ -5,7 +5,7 @@
 // order that the block-scaled tensor-core product copies into tensor memory as it stands.
 #pragma once
 
-#include "common.cuh"
+#include "types.cuh"
 
 namespace q8 {
 
@@ -53,11 +53,58 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8])
     return r;
 }
 
-// Twice the value of a code (an integer), from its low four bits: magnitudes 0 1 2 3 4 6 8 12.
-__device__ __forceinline__ int mx_twice(uint32_t c)
+// The largest absolute bits of 8 values, as those of an f32 (infinities and NaN above all others):
+// in 16-bit types the comparison takes two values an instruction.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_bits(const uint4 (&u)[sizeof(T) / 2])
 {
-    const int mag = (int)((0xC8643210u >> (4 * (c & 7u))) & 15u);
-    return (c & 8u) ? -mag : mag;
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
+        return a;
+    } else {
+        const uint32_t keep = 0x7fff7fffu;
+        const uint32_t p = __vmaxu2(__vmaxu2(u[0].x & keep, u[0].y & keep), __vmaxu2(u[0].z & keep, u[0].w & keep));
+        const uint32_t a = max(p & 0xffffu, p >> 16);
+        if constexpr (std::is_same<T, __half>::value) return __float_as_uint(half_bits_to_float(a));
+        else return a << 16;
+    }
+}
+
+// A warp's 256 consecutive values, 8 a lane: this lane's codes, and in every 16th lane the four scale
+// bytes of its 128 values (a block with a NaN or an infinity: byte 255, codes 0).
+struct MxChunk {
+    uint32_t codes, scales;
+};
+template <typename T>
+__device__ __forceinline__ MxChunk mx_quantize8(const uint4 (&in)[sizeof(T) / 2])
+{
+    uint32_t a = largest_bits<T>(in);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const uint32_t b = mx_scale_byte(a);
+    uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
+    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
+    float v[8];
+    if constexpr (sizeof(T) == 4) {
+        float lo[4], hi[4];
+        unpack<T>(in[0], lo);
+        unpack<T>(in[1], hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
+    } else {
+        unpack<T>(in[0], v);
+    }
+    const float inv = b == 255u ? 0.0f : mx_inverse(b);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv));
+        v[i] = p.x;
+        v[i + 1] = p.y;
+    }
+    return {b == 255u ? 0u : mx_codes8(v), word};
 }
 
 }  // namespace q8

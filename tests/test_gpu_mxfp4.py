@@ -140,7 +140,9 @@ def check_product(y, wv, xv, kind):
                                    (16, 128, 4096), (17, 300, 2304), (33, 1000, 512), (64, 257, 1024),
                                    (65, 640, 8192), (128, 384, 256), (129, 130, 768), (191, 500, 512),
                                    (193, 1025, 1280), (300, 5152, 512), (700, 900, 1024), (1, 20493, 256),
-                                   (1024, 2500, 768), (1, 33, 65536)])
+                                   (1024, 2500, 768), (1, 33, 65536),
+                                   (131, 4096, 1280), (300, 1000, 8192), (60, 1432, 2560), (100, 300, 4096),
+                                   (16, 20480, 512), (193, 300, 2048), (130, 20480, 256), (12, 200, 20480)])
 def test_product_matches_64_bits(m, n, k, kind):
     """Every code and spread-out scales in both operands, straight from their packed form."""
     ensure_built()
