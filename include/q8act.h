@@ -1,6 +1,7 @@
 /*
  * q8act.h -- C ABI of libq8act.so: a GB300 (sm_103a) implementation of the Q8_0 weight x
- * q8_1 activation block-quantized matmul of an LLM decoder.
+ * q8_1 activation block-quantized matmul of an LLM decoder, and of what stands next to it: the
+ * norm in front of a product, MXFP4 weights and activations, log probabilities of logits.
  *
  * The operation, with the notation used throughout:
  *   W   Q8_0 weights, n rows ("out_f") of k/32 blocks ("in_f" = k).  A block is 34 bytes:
@@ -372,7 +373,8 @@ int q8act_debug_gemv_q5_k_block_dots(const void *w, const int8_t *xq, int32_t *D
  *       x's or residual's own rows.  The norm is taken of the unrounded f32 sum.
  *   weight [k] of `wtype`, or NULL (ones).  eps >= 0 (a row of zeros with eps = 0 divides 0 by
  *       0: its quants are 0, as the quantizers give for NaN).
- *   y: NULL, or [m][k] of `type`: the normed values, rounded once.
+ *   y: NULL, or [m][k] of `type`: the normed values, rounded once.  With y the quants and scales
+ *       may be NULL together (the norm alone).
  *   rmsnorm_q8_1:     xq [m][k] int8, xd [m][k/32] f32 (the GEMVs' activation);
  *   rmsnorm_q8_1_mmq: xqh [m][k] binary16 quants, xdt [k/32][q8act_mmq_ldm(m)] f32 (the GEMM's).
  */

@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) Q8_0 weight x q8_1 activation block-quantized matmul.
+"""GB300 (sm_103a) Q8_0 weight x q8_1 activation block-quantized matmul, and what stands next to it
+in a decoder: the norm that feeds it, MXFP4 products, log probabilities of logits.
 
 The compute lives in libq8act.so (hand-written CUDA kernels behind the C ABI of
 include/q8act.h).  This package is its Python face:
@@ -268,7 +269,7 @@ def _given(t, shape, dtype, what: str):
     raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: contiguous {tuple(shape)}")
 
 
-def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out):
+def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out, quants=True):
     torch = _torch or _load_torch()
     ldx, code = _rows(x, "x"), _type(x, "x")
     m, k = shape = x.shape
@@ -288,10 +289,14 @@ def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out):
     if y is not None:
         py = _given(y, shape, dtype, "y")
     qtype, dshape = (torch.uint16, (k // QK, (m + 3) // 4 * 4)) if mmq else (torch.int8, (m, k // QK))
-    if out is None:
-        out = (torch.empty(shape, dtype=qtype, device=x.device), torch.empty(dshape, dtype=torch.float32, device=x.device))
-    q, d = out
-    pq, pd = _given(q, shape, qtype, "quants"), _given(d, dshape, torch.float32, "scales")
+    if not quants:
+        q = d = pq = pd = None
+    else:
+        if out is None:
+            out = (torch.empty(shape, dtype=qtype, device=x.device),
+                   torch.empty(dshape, dtype=torch.float32, device=x.device))
+        q, d = out
+        pq, pd = _given(q, shape, qtype, "quants"), _given(d, dshape, torch.float32, "scales")
     L = lib()
     fn = L.q8act_rmsnorm_q8_1_mmq if mmq else L.q8act_rmsnorm_q8_1
     rc = fn(x.data_ptr(), ldx, pr, ldr, pw, wtype, eps, pro, ldro, py, pq, pd, m, k, code, _s(None))
@@ -312,6 +317,16 @@ def rmsnorm_q8_1(x, weight=None, eps: float = 1e-6, residual=None, residual_out=
 def rmsnorm_q8_1_mmq(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None, y=None, out=None):
     """rmsnorm_q8_1 with the GEMM's activation layout: (xqh uint16 [m, k], xdt f32 [k/32, ldm])."""
     return _rmsnorm(True, x, weight, eps, residual, residual_out, y, out)
+
+
+def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None, out=None):
+    """The norm alone: y in x's type (what rmsnorm_q8_1 gives as y), for a consumer that is not
+    quantized to q8_1, such as an MXFP4 product."""
+    torch = _torch or _load_torch()
+    _rows(x, "x")
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rmsnorm(False, x, weight, eps, residual, residual_out, y, None, quants=False)
+    return y
 
 
 def _mxfp4_scales(rows: int, k: int):

@@ -539,7 +539,7 @@ static int rmsnorm_common(const void *x, int64_t ldx, const void *residual, int6
                           float eps, void *residual_out, int64_t ldro, void *y, void *q, float *d, bool mmq, int64_t m,
                           int64_t k, int type, void *stream)
 {
-    if (!x || !q || !d) return Q8ACT_ERR_NULL;
+    if (!x || !q != !d || (!q && !y)) return Q8ACT_ERR_NULL;
     if (!known_type(type) || (weight && !known_type(wtype))) return Q8ACT_ERR_TYPE;
     if (check_k(k) != Q8ACT_OK || m < 1 || m > ((int64_t)1 << 34) / k || !(eps >= 0.0f)) return Q8ACT_ERR_DIMS;
     if (mmq && m * k > kMaxGemmElems) return Q8ACT_ERR_DIMS;

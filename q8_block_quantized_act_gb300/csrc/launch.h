@@ -96,7 +96,7 @@ cudaError_t launch_gemm_q8_0_repacked(const DeviceInfo &dev, const uint16_t *wq1
                                       void *split_ws, size_t split_bytes, bool pdl, cudaStream_t stream);
 
 // Residual addition + RMS norm + q8_1 quantization.  Strides in elements; residual,
-// residual_out, weight and y may be null.  q: int8 [m][k] with d [m][k/32], or (mmq) binary16
+// residual_out, weight and y may be null, q and d together when y is not.  q: int8 [m][k] with d [m][k/32], or (mmq) binary16
 // [m][k] with d [k/32][ldm].
 struct NormArgs {
     const void *x, *residual, *weight;

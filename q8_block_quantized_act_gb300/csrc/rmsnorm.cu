@@ -70,6 +70,7 @@ __device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k,
         times<V>(v, w);
     }
     if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + t * k + i) = pack<T>(v);
+    if (!a.q) return;
     const BlockQ<V> b = quantize_block<V>(v);
     const bool first = c % (QK / V) == 0;
     if constexpr (MMQ) {

@@ -6,7 +6,9 @@
 Kernels: quantize (q8_1), quantize_mmq, quantize_q8_0, gemv, gemm (fused quantize),
 gemm_preq, gemm_repacked (fused quantize, load-time repacked weights), repack, dequant,
 gemv_q4_0, dequant_q4_0, and the K-quant passes gemv_q6_k / gemv_q4_k / gemv_q5_k and
-dequant_q6_k / dequant_q4_k / dequant_q5_k (on seeded random superblocks).
+dequant_q6_k / dequant_q4_k / dequant_q5_k (on seeded random superblocks), norm and norm_mmq
+(residual and weight, f16), quantize_mxfp4 and dequant_mxfp4 (f16), gemm_mxfp4 (f16 activation
+quantized in the call, f16 out) and logprobs (m rows of n f16 logits, 8 alternatives).
 Inputs are the seeded synthetic ones of q8_block_quantized_act_gb300.inputs;
 one warm-up launch precedes the `--reps` launches.
 """
@@ -20,7 +22,8 @@ def main(argv=None):
     ap.add_argument("kernel", choices=("quantize", "quantize_mmq", "quantize_q8_0", "gemv", "gemm",
                                        "gemm_preq", "gemm_repacked", "repack", "dequant", "gemv_q4_0",
                                        "dequant_q4_0", "gemv_q6_k", "gemv_q4_k", "gemv_q5_k",
-                                       "dequant_q6_k", "dequant_q4_k", "dequant_q5_k"))
+                                       "dequant_q6_k", "dequant_q4_k", "dequant_q5_k", "norm", "norm_mmq",
+                                       "quantize_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "logprobs"))
     ap.add_argument("--m", type=int, default=1)
     ap.add_argument("--n", type=int, default=4096)
     ap.add_argument("--k", type=int, default=4096)
@@ -47,10 +50,33 @@ def main(argv=None):
     wk = torch.from_numpy(inputs.kquant_superblocks(kq, n, k)).to(dev) if kq else None
     ws = q8.gemm_workspace(m, k, dev) if a.kernel in ("gemm", "gemm_repacked") else None
     wq16, wdt = q8.repack_q8_0(w, n, k) if a.kernel in ("gemm_repacked", "repack") else (None, None)
+    x16 = x.half()
+    if a.kernel in ("norm", "norm_mmq"):
+        r16, g16 = x16.flip(0).contiguous(), torch.ones(k, dtype=torch.float16, device=dev)
+    if a.kernel == "dequant_mxfp4":
+        mx, out16 = q8.quantize_mxfp4(x16), torch.empty_like(x16)
+    if a.kernel == "gemm_mxfp4":
+        mx = q8.quantize_mxfp4(torch.from_numpy(inputs.weights_f32(n, k)).to(dev))
+        mws, y16 = q8.gemm_mxfp4_workspace(m, k, dev), torch.empty((m, n), dtype=torch.float16, device=dev)
+    if a.kernel == "logprobs":
+        logits = torch.randn((m, n), device=dev).mul_(2.5).half()
+        tok = torch.zeros(m, dtype=torch.int32, device=dev)
     torch.cuda.synchronize()
 
     def once():
-        if a.kernel == "quantize":
+        if a.kernel == "norm":
+            q8.rmsnorm_q8_1(x16, g16, residual=r16, residual_out=r16)
+        elif a.kernel == "norm_mmq":
+            q8.rmsnorm_q8_1_mmq(x16, g16, residual=r16, residual_out=r16)
+        elif a.kernel == "quantize_mxfp4":
+            q8.quantize_mxfp4(x16)
+        elif a.kernel == "dequant_mxfp4":
+            q8.dequant_mxfp4(*mx, out=out16)
+        elif a.kernel == "gemm_mxfp4":
+            q8.gemm_mxfp4(*mx, x16, ws=mws, out=y16)
+        elif a.kernel == "logprobs":
+            q8.logprobs(logits, tok, top=8)
+        elif a.kernel == "quantize":
             q8.quantize_q8_1(x)
         elif a.kernel == "quantize_mmq":
             q8.quantize_q8_1_mmq(x)

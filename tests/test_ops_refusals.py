@@ -47,6 +47,7 @@ def deq(c=A, s=A, y=A, t=F16, m=2, k=256):
     (lambda: norm(x=None), q8.Q8ACT_ERR_NULL),
     (lambda: norm(q=None), q8.Q8ACT_ERR_NULL),
     (lambda: norm(d=None, mmq=True), q8.Q8ACT_ERR_NULL),
+    (lambda: norm(q=None, d=None, y=None), q8.Q8ACT_ERR_NULL),
     (lambda: norm(t=3), q8.Q8ACT_ERR_TYPE),
     (lambda: norm(wt=-1), q8.Q8ACT_ERR_TYPE),
     (lambda: norm(k=288, ldx=288, ldr=288, ldro=288), q8.Q8ACT_ERR_DIMS),
