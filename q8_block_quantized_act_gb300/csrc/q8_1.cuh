@@ -8,10 +8,11 @@ namespace q8 {
 
 constexpr unsigned FULL = 0xffffffffu;
 
+// For normal x (the flushing form is one instruction).
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -46,13 +47,30 @@ static __device__ __noinline__ float quantize_exactly(float v, float d)
     return __fadd_rn(t, 0.0f);         // -0 -> +0
 }
 
-// V consecutive values of a block whose 32 values are spread over 32 / V lanes: their quants as
-// integer-valued floats (+0 for zero).
+// The larger of three magnitudes; NaN wins.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// V consecutive values of a block whose 32 values are spread over 32 / V lanes.  t: their quants plus
+// 1.5 * 2^23, where floats have unit spacing: quant_of is exact (+0 for zero), and the low byte of
+// the bits is the quant's two's complement.
+constexpr float QUANT_BIAS = 12582912.0f;
 template <int V>
 struct BlockQ {
     float t[V];
     float d;
 };
+__device__ __forceinline__ float quant_of(float t) { return __fsub_rn(t, QUANT_BIAS); }
+__device__ __forceinline__ uint32_t quant_bytes(const float *t)          // four quants as int8
+{
+    const uint32_t lo = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
 
 // For a value whose approximate quotient qa = v * block_rcp(d) lies farther than 1e-4 from every
 // half-integer, its nearest integer is round-half-away(fl(v / d)): qa differs from v / d by under
@@ -72,30 +90,24 @@ __device__ __forceinline__ BlockQ<V> quantize_block(const float (&v)[V])
     BlockQ<V> r;
     r.d = div127(a);
     const float rc = block_rcp(r.d);
-    const float2 rc2 = make_float2(rc, rc), big = make_float2(12582912.0f, 12582912.0f);
-    bool fine = true;
+    const float2 rc2 = make_float2(rc, rc), big = make_float2(QUANT_BIAS, QUANT_BIAS);
+    float off = 0.0f;                  // one test for the thread: a chain of V would be longer than the work
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
         const float2 qa = __fmul2_rn(make_float2(v[i], v[i + 1]), rc2);
-        const float2 t = __fadd2_rn(__fadd2_rn(qa, big), make_float2(-big.x, -big.y));
-        const float2 e = __ffma2_rn(t, make_float2(-1.0f, -1.0f), qa);          // qa - t, rounded once
-        fine = fine && fabsf(e.x) < 0.4999f && fabsf(e.y) < 0.4999f;
-        r.t[i] = t.x;
-        r.t[i + 1] = t.y;
+        const float2 b = __fadd2_rn(qa, big), n = __fadd2_rn(b, make_float2(-big.x, -big.y));
+        const float2 e = __ffma2_rn(n, make_float2(-1.0f, -1.0f), qa);          // qa - n, rounded once
+        off = max3_abs_nan(off, e.x, e.y);
+        r.t[i] = b.x;
+        r.t[i + 1] = b.y;
     }
-    if (!fine) {
+    if (!(off < 0.4999f)) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (!(fabsf(__fsub_rn(__fmul_rn(v[i], rc), r.t[i])) < 0.4999f)) r.t[i] = quantize_exactly(v[i], r.d);
+            if (!(fabsf(__fsub_rn(__fmul_rn(v[i], rc), quant_of(r.t[i]))) < 0.4999f))
+                r.t[i] = __fadd_rn(quantize_exactly(v[i], r.d), QUANT_BIAS);
     }
     return r;
-}
-
-// An integer-valued float t, |t| <= 127, as its int8 byte: the bits of t + 1.5 * 2^23 are
-// those of 1.5 * 2^23 plus t (unit spacing there), so the low byte is t's two's complement.
-__device__ __forceinline__ uint32_t byte_of(float t)
-{
-    return (uint32_t)__float_as_int(__fadd_rn(t, 12582912.0f)) & 0xFFu;
 }
 
 }  // namespace q8

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) quantize_q8_1_kernel(const float4 *__rest
             const int64_t c = i + h * stride;
             const float4 v = h ? v1 : v0;
             const BlockQ<4> b = quantize_block<4>({v.x, v.y, v.z, v.w});
-            xq[c] = byte_of(b.t[0]) | (byte_of(b.t[1]) << 8) | (byte_of(b.t[2]) << 16) | (byte_of(b.t[3]) << 24);
+            xq[c] = quant_bytes(b.t);
             if ((c & 7) == 0) xd[c >> 3] = b.d;
         }
     }
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(256) quantize_q8_1_mmq_kernel(const float4 *__
             const int64_t g = t * chunks_per_row + c;
             const BlockQ<4> b = quantize_block<4>({v[j].x, v[j].y, v[j].z, v[j].w});
             // the quants are small integers: exact in binary16
-            const __half2 h01 = __floats2half2_rn(b.t[0], b.t[1]);
-            const __half2 h23 = __floats2half2_rn(b.t[2], b.t[3]);
+            const __half2 h01 = __floats2half2_rn(quant_of(b.t[0]), quant_of(b.t[1]));
+            const __half2 h23 = __floats2half2_rn(quant_of(b.t[2]), quant_of(b.t[3]));
             xqh[g] = make_uint2(*reinterpret_cast<const uint32_t *>(&h01), *reinterpret_cast<const uint32_t *>(&h23));
             if ((c & 7) == 0) xdt[(int64_t)(c >> 3) * ldm + t] = b.d;
         }

@@ -55,21 +55,30 @@ __device__ __forceinline__ void times(float (&v)[V], float f)
     }
 }
 
-// y's quants and scale: V values of the block that starts at a multiple of 32 / V lanes.
+template <int V>
+__device__ __forceinline__ void weigh(const NormArgs &a, int64_t i, float (&v)[V])
+{
+    float w[V];
+    if (a.wtype == Q8ACT_F32) load_weights<V>(static_cast<const float *>(a.weight) + i, w);
+    else if (a.wtype == Q8ACT_F16) load_weights<V>(static_cast<const __half *>(a.weight) + i, w);
+    else load_weights<V>(static_cast<const __nv_bfloat16 *>(a.weight) + i, w);
+    times<V>(v, w);
+}
+
+template <typename T>
+__device__ __forceinline__ bool is_type(int type)
+{
+    return type == (sizeof(T) == 4 ? Q8ACT_F32 : std::is_same<T, __half>::value ? Q8ACT_F16 : Q8ACT_BF16);
+}
+
+// The quants and scale of chunk c of row t: V values of the block that starts at a multiple of
+// 32 / V lanes.
 template <typename T, bool MMQ>
-__device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k, int c, float (&v)[VEC<T>], float inv)
+__device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k, int c, const float (&v)[VEC<T>])
 {
     constexpr int V = VEC<T>;
-    const int64_t i = (int64_t)c * V;
-    times<V>(v, inv);
-    if (a.weight) {
-        float w[V];
-        if (a.wtype == Q8ACT_F32) load_weights<V>(static_cast<const float *>(a.weight) + i, w);
-        else if (a.wtype == Q8ACT_F16) load_weights<V>(static_cast<const __half *>(a.weight) + i, w);
-        else load_weights<V>(static_cast<const __nv_bfloat16 *>(a.weight) + i, w);
-        times<V>(v, w);
-    }
-    if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + t * k + i) = pack<T>(v);
+    const int64_t i = t * k + (int64_t)c * V;
+    if (a.y) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + i) = pack<T>(v);
     if (!a.q) return;
     const BlockQ<V> b = quantize_block<V>(v);
     const bool first = c % (QK / V) == 0;
@@ -77,22 +86,17 @@ __device__ __forceinline__ void store_block(const NormArgs &a, int64_t t, int k,
         uint32_t w[V / 2];                         // small integers: exact in binary16
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-            const __half2 h = __floats2half2_rn(b.t[2 * j], b.t[2 * j + 1]);
+            const __half2 h = __floats2half2_rn(quant_of(b.t[2 * j]), quant_of(b.t[2 * j + 1]));
             w[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        uint16_t *q = static_cast<uint16_t *>(a.q) + t * k + i;
+        uint16_t *q = static_cast<uint16_t *>(a.q) + i;
         if constexpr (V == 8) *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
         else *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
         if (first) a.d[(int64_t)(c / (QK / V)) * a.ldm + t] = b.d;
     } else {
-        uint32_t w[V / 4];
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j)
-            w[j] = byte_of(b.t[4 * j]) | (byte_of(b.t[4 * j + 1]) << 8) | (byte_of(b.t[4 * j + 2]) << 16) |
-                   (byte_of(b.t[4 * j + 3]) << 24);
-        int8_t *q = static_cast<int8_t *>(a.q) + t * k + i;
-        if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(q) = w[0];
+        int8_t *q = static_cast<int8_t *>(a.q) + i;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(quant_bytes(b.t), quant_bytes(b.t + 4));
+        else *reinterpret_cast<uint32_t *>(q) = quant_bytes(b.t);
         if (first) a.d[t * (k / QK) + c / (QK / V)] = b.d;
     }
 }
@@ -123,38 +127,52 @@ __device__ __forceinline__ void add_residual(uint4 x, uint4 r, bool add, float (
     }
 }
 
-// CH 16-byte chunks of a row in each thread.  chunks = k / V is a multiple of 32, so a warp's chunk
-// is inside the row for all of its lanes or for none, as the block's shuffles need.
-template <int CH>
-struct RowRegs {
-    uint4 x[CH], r[CH];
-};
-
-template <typename T, int CH>
-__device__ __forceinline__ void load_row(const NormArgs &a, int64_t t, int chunks, RowRegs<CH> &v)
-{
-    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.ldx);
-    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr);
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        v.x[i] = c < chunks ? x[c] : make_uint4(0, 0, 0, 0);
-        if (a.residual) v.r[i] = c < chunks ? r[c] : make_uint4(0, 0, 0, 0);
-    }
-}
-
-template <typename T, bool MMQ, int CH>
-__device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t, int k, int chunks, float (&v)[CH][VEC<T>], float *part)
+// A CTA per row, CH 16-byte chunks a thread.  chunks = k / V is a multiple of 32, so a warp's chunk
+// is inside the row for all of its lanes or for none, as the block's shuffles need.  Weights of x's
+// type are loaded beside the row, before the barrier.
+template <typename T, bool MMQ, int CH, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, 1024 / MAX_THREADS) rmsnorm_row_kernel(NormArgs a, int k)
 {
     constexpr int V = VEC<T>;
+    __shared__ float part[32];
+    griddep_enter();
+    const int chunks = k / V;
+    const int64_t t = blockIdx.x;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.ldx);
+    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + t * a.ldr);
+    const bool early = a.weight && is_type<T>(a.wtype);
+    uint4 xv[CH], rv[CH], wv[CH];
+    if ((int)blockDim.x * CH == chunks) {                 // no thread is without a chunk
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            xv[i] = x[threadIdx.x + i * blockDim.x];
+            if (a.residual) rv[i] = r[threadIdx.x + i * blockDim.x];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            xv[i] = c < chunks ? x[c] : make_uint4(0, 0, 0, 0);
+            if (a.residual) rv[i] = c < chunks ? r[c] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (early)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c < chunks) wv[i] = __ldg(static_cast<const uint4 *>(a.weight) + c);
+        }
+    float v[CH][V];
     float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < CH; ++i) {
+        add_residual<T>(xv[i], rv[i], a.residual != nullptr, v[i]);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
             const float2 p = make_float2(v[i][j], v[i][j + 1]);
             ss = __ffma2_rn(p, p, ss);
         }
+    }
     if (a.residual_out) {
         T *out = static_cast<T *>(a.residual_out) + t * a.ldro;
 #pragma unroll
@@ -167,23 +185,16 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t, int k, in
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
-        if (c < chunks) store_block<T, MMQ>(a, t, k, c, v[i], inv);
+        times<V>(v[i], inv);
+        if (early) {
+            float w[V];
+            unpack<T>(wv[i], w);
+            times<V>(v[i], w);
+        } else if (a.weight && c < chunks) {
+            weigh<V>(a, (int64_t)c * V, v[i]);
+        }
+        if (c < chunks) store_block<T, MMQ>(a, t, k, c, v[i]);
     }
-}
-
-// A CTA per row.
-template <typename T, bool MMQ, int CH>
-__global__ void __launch_bounds__(1024) rmsnorm_row_kernel(NormArgs a, int k)
-{
-    __shared__ float part[32];
-    griddep_enter();
-    const int chunks = k / VEC<T>;
-    RowRegs<CH> in;
-    load_row<T>(a, blockIdx.x, chunks, in);
-    float v[CH][VEC<T>];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) add_residual<T>(in.x[i], in.r[i], a.residual != nullptr, v[i]);
-    norm_row<T, MMQ, CH>(a, blockIdx.x, k, chunks, v, part);
 }
 
 // Rows too long for registers: read twice (the second time from L2).
@@ -210,7 +221,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
         add_residual<T>(x[c], r ? r[c] : make_uint4(0, 0, 0, 0), r != nullptr, v);
         if (a.residual_out)
             *reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + t * a.ldro + (int64_t)c * V) = pack<T>(v);
-        store_block<T, MMQ>(a, t, k, c, v, inv);
+        times<V>(v, inv);
+        if (a.weight) weigh<V>(a, (int64_t)c * V, v);
+        store_block<T, MMQ>(a, t, k, c, v);
     }
 }
 
@@ -228,11 +241,12 @@ cudaError_t launch_rows(const DeviceInfo &dev, const NormArgs &a, int64_t m, int
     while (threads < 1024 && chunks > threads * CHUNKS) threads *= 2;
     if (threads > chunks) threads = chunks;
     const int each = (chunks + threads - 1) / threads;
-    if (each == 1) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 1>, grid, threads, 0, stream, a, (int)k);
-    if (each == 2) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 2>, grid, threads, 0, stream, a, (int)k);
-    if (each <= 4) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 4>, grid, threads, 0, stream, a, (int)k);
+    auto go = [&](auto kern) { return launch_dependent(kern, grid, threads, 0, stream, a, (int)k); };
+    if (each == 1) return go(rmsnorm_row_kernel<T, MMQ, 1, 1024>);
+    if (each == 2) return go(rmsnorm_row_kernel<T, MMQ, 2, 1024>);
+    if (each <= 4) return threads <= 256 ? go(rmsnorm_row_kernel<T, MMQ, 4, 256>) : go(rmsnorm_row_kernel<T, MMQ, 4, 1024>);
     if constexpr (VEC<T> == 4)
-        if (each <= 8) return launch_dependent(rmsnorm_row_kernel<T, MMQ, 8>, grid, threads, 0, stream, a, (int)k);
+        if (each <= 8) return go(rmsnorm_row_kernel<T, MMQ, 8, 1024>);
     return launch_dependent(rmsnorm_long_kernel<T, MMQ>, grid, 1024, 0, stream, a, (int)k);
 }
 
