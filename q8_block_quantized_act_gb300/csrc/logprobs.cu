@@ -147,6 +147,7 @@ struct Shared {
     Stats stats[W];
     float slot[SLOTS][W * 32];         // each thread's maxima
     uint32_t best[W * MAX_J];          // each warp's J largest thread maxima
+    uint32_t bound;
     int n_chosen, n_found;
     uint64_t part_list[MAX_CL][32];    // rank 0: every rank's list and sums
     Stats part_stats[MAX_CL];
@@ -303,19 +304,25 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
         // ---- the alternatives ----
         uint64_t list = 0;
         if (a.top > 0) {
-            // every warp ranks the W J <= 64 values, two a lane, equal ones by their place
-            uint32_t mine[2] = {0, 0};
-            int place[2] = {0, 0};
+            // the first warp ranks the W J <= 64 values, two a lane, equal ones by their place
+            if (warp == 0) {
+                uint32_t mine[2] = {0, 0};
+                int place[2] = {0, 0};
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (lane + 32 * h < W * J) mine[h] = sh.best[lane + 32 * h];
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < W * J) mine[h] = sh.best[lane + 32 * h];
 #pragma unroll 8
-            for (int i = 0; i < W * J; ++i) {
-                const uint32_t other = sh.best[i];
+                for (int i = 0; i < W * J; ++i) {
+                    const uint32_t other = sh.best[i];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) place[h] += other > mine[h] || (other == mine[h] && i < lane + 32 * h);
+                    for (int h = 0; h < 2; ++h) place[h] += other > mine[h] || (other == mine[h] && i < lane + 32 * h);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (place[h] == a.top - 1 && lane + 32 * h < W * J) sh.bound = mine[h];
             }
-            uint32_t thr = __reduce_max_sync(ALL, place[0] == a.top - 1 ? mine[0] : place[1] == a.top - 1 ? mine[1] : 0u);
+            __syncthreads();
+            uint32_t thr = sh.bound;
             thr = max(thr, 1u);
             const float least = thr > 1u ? value_of((uint64_t)thr << 32) : LOWEST;
             sh.list[warp][lane] = 0;
@@ -345,19 +352,20 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
             // Each warp reads the U V elements of a chosen thread's step, one a lane (f32: two
             // steps at once), several in flight.
             constexpr int LANES = U * V, AT_ONCE = 32 / LANES, DEPTH = 8 / AT_ONCE;
-            const int total = sh.n_chosen * per_slot;
+            const int pairs = sh.n_chosen;
 #pragma unroll 1
-            for (int i0 = warp * AT_ONCE + lane / LANES; i0 - lane / LANES < total; i0 += W * AT_ONCE * DEPTH) {
+            for (int i0 = warp * AT_ONCE; i0 < pairs * per_slot; i0 += W * AT_ONCE * DEPTH) {
+                // per_slot is 1 up to SLOTS steps; longer rows go over a slot's steps one by one
                 float f[DEPTH];
                 int at[DEPTH];
 #pragma unroll
                 for (int d = 0; d < DEPTH; ++d) {
-                    const int i = i0 + d * W * AT_ONCE;
+                    const int i = i0 + d * W * AT_ONCE + lane / LANES;
                     f[d] = ninf;
                     at[d] = 0;
-                    if (i < total) {
-                        const int pair = sh.chosen[i / per_slot];
-                        const int step = pair % SLOTS * per_slot + i % per_slot;
+                    if (i < pairs * per_slot) {
+                        const int pair = sh.chosen[per_slot == 1 ? i : i / per_slot];
+                        const int step = per_slot == 1 ? pair % SLOTS : pair % SLOTS * per_slot + i % per_slot;
                         const int L = L0 + step * STEP + pair / SLOTS + lane % LANES / V * THREADS;
                         at[d] = head + L * V + lane % V;
                         if (L < L1) f[d] = to_f32(x[at[d]]);
