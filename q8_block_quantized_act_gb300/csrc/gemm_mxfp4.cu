@@ -634,24 +634,46 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 
     if (warp == C::EPI_WARPS) {
         // ------------------------------ producer ------------------------------
+        int row_tile, token_tile;
+        auto enter = [&](int tile) {
+            const int rt = tile / wk.token_tiles;
+            token_tile = tile - rt * wk.token_tiles;
+            row_tile = 2 * rt + (int)rank;                              // this CTA's 128 rows
+        };
+        auto load_w = [&](int st, int ks) {
+            const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], C::STAGE_TX);
+            pair_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, row_tile * BM, bar);
+            pair_load_2d(smem + C::OFF_SA + st * SC_BYTES, &tm_ws, ks * (SC_BYTES / 8), row_tile, bar);
+        };
+        auto load_x = [&](int st, int ks) {
+            const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
+            pair_load_2d(smem + C::OFF_B + st * C::B_BYTES, &tm_x, ks * ROW_BYTES, token_tile * BN + (int)rank * (BN / 2), bar);
+            pair_load_2d(smem + C::OFF_SB + st * C::SB_BYTES, &tm_xs, ks * (SC_BYTES / 8), 2 * token_tile, bar);
+        };
+        // As in gemm_mxfp4_kernel: the first stages' weights before the wait in a fused call.
+        if (wk.first_wait) griddep_wait();
+        int early = 0;
+        for (int tile = pair; tile < wk.tiles && early < STAGES; tile += pairs) {
+            enter(tile);
+            for (int ks = 0; ks < wk.steps && early < STAGES; ++ks, ++early)
+                if (elect_one()) load_w(early, ks);
+        }
+        if (!wk.first_wait) griddep_wait();
+        griddep_launch_dependents();
         int st = 0, it = 0;
         uint32_t phase = 1;
         bool ok = true;
-        griddep_wait();
-        griddep_launch_dependents();
         for (int tile = pair; ok && tile < wk.tiles; tile += pairs) {
-            const int rt = tile / wk.token_tiles, tt = tile - rt * wk.token_tiles;
-            const int rows = 2 * rt + (int)rank;                        // this CTA's 128-row tile
+            enter(tile);
             for (int ks = 0; ks < wk.steps; ++ks, ++it) {
-                ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], phase, status, abort_flag));
-                if (!ok) break;
+                if (it >= early) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], phase, status, abort_flag));
+                    if (!ok) break;
+                }
                 if (elect_one()) {
-                    const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[st], C::STAGE_TX);
-                    pair_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, rows * BM, bar);
-                    pair_load_2d(smem + C::OFF_B + st * C::B_BYTES, &tm_x, ks * ROW_BYTES, tt * BN + (int)rank * (BN / 2), bar);
-                    pair_load_2d(smem + C::OFF_SA + st * SC_BYTES, &tm_ws, ks * (SC_BYTES / 8), rows, bar);
-                    pair_load_2d(smem + C::OFF_SB + st * C::SB_BYTES, &tm_xs, ks * (SC_BYTES / 8), 2 * tt, bar);
+                    if (it >= early) load_w(st, ks);
+                    load_x(st, ks);
                 }
                 if (++st == STAGES) {
                     st = 0;
@@ -777,7 +799,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 
 template <typename T>
 cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
-                         const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, cudaStream_t stream)
+                         const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, bool pdl, cudaStream_t stream)
 {
     cudaError_t e = set_kernel_smem<gemm_mxfp4_pair_kernel<T>>(dev.device, PairCfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -800,6 +822,7 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * wk.token_tiles;
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     wk.tiles = (int)tiles;
+    wk.first_wait = pdl ? 0 : 1;
     const int64_t pairs = tiles < dev.num_sms / 2 ? tiles : dev.num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
@@ -905,7 +928,7 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
         if (p.bn == 64) return go(Cfg<64, 6>{});
         if (p.bn == 128) return go(Cfg<128, 4>{});
         if (p.bn == 192) return go(Cfg<192, 5>{});
-        return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, stream);
+        return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, pdl, stream);
     });
 }
 
