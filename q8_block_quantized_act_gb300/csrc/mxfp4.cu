@@ -38,8 +38,9 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const T *__restrict
     }
 }
 
-// The values of eight codes (two at a time through binary16, which holds them exactly).
-__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8])
+// The values of V = 8 or 4 codes (two at a time through binary16, which holds them exactly).
+template <int V>
+__device__ __forceinline__ void mx_values(uint32_t w, float (&v)[V])
 {
     uint32_t h[4];
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -51,49 +52,45 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8])
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
     }
 }
 
-// A thread has 8 codes of each of ROWS rows.
+// A thread makes 16 bytes of each of ROWS rows: 8 values, or 4 of f32.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t *__restrict__ codes,
+__global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, T *__restrict__ y,
                                                             int64_t m, int k)
 {
+    constexpr int V = VEC<T>;
+    using Codes = typename std::conditional<V == 8, uint32_t, uint16_t>::type;
     griddep_enter();
-    const int chunks = k / 8;
+    const int chunks = k / V;
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
     if (c >= chunks) return;
     for (int64_t r0 = (int64_t)blockIdx.y * ROWS; r0 < m; r0 += (int64_t)gridDim.y * ROWS) {
         uint32_t w[ROWS], b[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            w[j] = r0 + j < m ? codes[(r0 + j) * chunks + c] : 0u;
-            b[j] = r0 + j < m ? scales[mx_scale_at(r0 + j, c >> 2, k / MX_TILE_K)] : 0u;
+            w[j] = r0 + j < m ? reinterpret_cast<const Codes *>(codes)[(r0 + j) * chunks + c] : 0u;
+            b[j] = r0 + j < m ? scales[mx_scale_at(r0 + j, c / (QK / V), k / MX_TILE_K)] : 0u;
         }
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             if (r0 + j >= m) break;
             const float s = mx_scale(b[j]);
-            uint4 *dst = reinterpret_cast<uint4 *>(y + (r0 + j) * k + (int64_t)c * 8);
-            float v[8];
-            mx_values8(w[j], v);
+            float v[V];
+            mx_values<V>(w[j], v);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
+            for (int i = 0; i < V; i += 2) {
                 const float2 p = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(s, s));
                 v[i] = p.x;
                 v[i + 1] = p.y;
             }
-            if constexpr (sizeof(T) == 4) {
-                dst[0] = pack<T>({v[0], v[1], v[2], v[3]});
-                dst[1] = pack<T>({v[4], v[5], v[6], v[7]});
-            } else {
-                dst[0] = pack<T>(v);
-            }
+            *reinterpret_cast<uint4 *>(y + (r0 + j) * k + (int64_t)c * V) = pack<T>(v);
         }
     }
 }
@@ -146,10 +143,10 @@ cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, co
     return with_type(type, [&](auto t) {
         using T = decltype(t);
         auto go = [&](auto kern, int each) {
-            return launch_dependent(kern, grid_rows(m, k / 8, each), 256, 0, stream,
-                                    reinterpret_cast<const uint32_t *>(codes), scales, static_cast<T *>(y), m, (int)k);
+            return launch_dependent(kern, grid_rows(m, k / VEC<T>, each), 256, 0, stream, codes, scales,
+                                    static_cast<T *>(y), m, (int)k);
         };
-        return four_rows(dev, m, k / 8) ? go(dequant_mxfp4_kernel<T, 4>, 4) : go(dequant_mxfp4_kernel<T, 1>, 1);
+        return four_rows(dev, m, k / VEC<T>) ? go(dequant_mxfp4_kernel<T, 4>, 4) : go(dequant_mxfp4_kernel<T, 1>, 1);
     });
 }
 

@@ -65,9 +65,13 @@ __device__ __forceinline__ uint32_t largest_bits(const uint4 (&u)[sizeof(T) / 2]
         for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
         return a;
     } else {
-        const uint32_t keep = 0x7fff7fffu;
-        const uint32_t p = __vmaxu2(__vmaxu2(u[0].x & keep, u[0].y & keep), __vmaxu2(u[0].z & keep, u[0].w & keep));
-        const uint32_t a = max(p & 0xffffu, p >> 16);
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+        T2 q = __habs2(*reinterpret_cast<const T2 *>(&w[0]));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) q = __hmax2_nan(q, __habs2(*reinterpret_cast<const T2 *>(&w[i])));
+        const uint32_t p = *reinterpret_cast<const uint32_t *>(&q);
+        const uint32_t a = max(p & 0xffffu, p >> 16);          // NaN is above infinity
         if constexpr (std::is_same<T, __half>::value) return __float_as_uint(half_bits_to_float(a));
         else return a << 16;
     }
@@ -85,8 +89,6 @@ __device__ __forceinline__ MxChunk mx_quantize8(const uint4 (&in)[sizeof(T) / 2]
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
     const uint32_t b = mx_scale_byte(a);
-    uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
-    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
     float v[8];
     if constexpr (sizeof(T) == 4) {
         float lo[4], hi[4];
@@ -104,7 +106,10 @@ __device__ __forceinline__ MxChunk mx_quantize8(const uint4 (&in)[sizeof(T) / 2]
         v[i] = p.x;
         v[i + 1] = p.y;
     }
-    return {b == 255u ? 0u : mx_codes8(v), word};
+    const uint32_t codes = b == 255u ? 0u : mx_codes8(v);
+    uint32_t word = b | (__shfl_down_sync(0xffffffffu, b, 4) << 8);
+    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
+    return {codes, word};
 }
 
 }  // namespace q8
