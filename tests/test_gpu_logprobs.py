@@ -57,6 +57,18 @@ def test_logprobs_match_64_bits(m, v, top, kind):
     check(got, x, tokens, top)
 
 
+def test_logprobs_long_rows_one_cta_each():
+    """Rows long enough that a kept maximum stands for several steps, too many rows to share."""
+    ensure_built()
+    m, v = 320, 70001
+    x, tokens = make(m, v, "f32", seed=8)
+    x[7] = 0.5                                                # a row of equal logits: more keys than the list
+    x[11, 5::2048] = 30.0                                     # one thread's places
+    got = q8.logprobs(x.cuda(), tokens.cuda(), top=16)
+    device_ok()
+    check(got, x, tokens, 16)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("m,v", [(1, 64448), (33, 9001), (160, 1500)])
 def test_logprobs_masks(m, v, kind):

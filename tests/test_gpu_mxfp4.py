@@ -212,6 +212,21 @@ def test_product_nan_blocks_reach_their_outputs_only(m):
         check_product(y[:m - 1][:, torch.from_numpy(keep).cuda()], wv[keep], xv[:m - 1], "f32")
 
 
+@pytest.mark.parametrize("m,n", [(1, 200), (3, 200), (15, 20000), (200, 200)])
+def test_fused_call_keeps_nonfinite_tokens_apart(m, n):
+    """A NaN or an infinity in a token's activation reaches that token's outputs and no others."""
+    ensure_built()
+    k = 512
+    _, _, wp, wt = matrix(n, k, 5)
+    x = values(m, k, 9, spread=1.0)
+    clean = q8.gemm_mxfp4(cuda(wp), cuda(wt), x.cuda())
+    x[m - 1, 300] = float("nan") if m != 3 else float("-inf")
+    y = q8.gemm_mxfp4(cuda(wp), cuda(wt), x.cuda())
+    device_ok()
+    assert bool(torch.isnan(y[m - 1]).all())
+    assert torch.equal(y[:m - 1], clean[:m - 1])
+
+
 @pytest.mark.parametrize("m", [1, 6, 200])
 def test_product_of_zeros_and_of_extreme_scales(m):
     ensure_built()

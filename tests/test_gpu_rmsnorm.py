@@ -133,6 +133,21 @@ def test_norm_zero_tiny_and_nonfinite_rows():
     check_blocks(host(q[2:3]).astype(np.float64), host(d[2:3]).astype(np.float64), y64, k)
 
 
+@pytest.mark.parametrize("m,k", [(3, 1024), (700, 512), (2, 40960)])
+def test_norm_alone(m, k):
+    """The norm without quants is the quantizing norm's y, and updates the residual alike."""
+    ensure_built()
+    for kind in ("f32", "f16", "bf16"):
+        x, r, w = make(m, k, kind, seed=13)
+        x, r, w = x.cuda(), r.cuda(), w.cuda()
+        y, s, s2 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        q8.rmsnorm_q8_1(x, w, residual=r, residual_out=s, y=y)
+        out = torch.empty_like(x)
+        assert q8.rmsnorm(x, w, residual=r, residual_out=s2, out=out) is out
+        device_ok()
+        assert torch.equal(out, y) and torch.equal(s, s2)
+
+
 def test_norm_writes_only_its_outputs():
     ensure_built()
     m, k = 5, 768
