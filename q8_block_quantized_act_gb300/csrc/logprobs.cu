@@ -5,9 +5,10 @@
 // A row whose logits are all -inf has no distribution: log probabilities -inf, entropy 0, no
 // alternatives (id -1).  A row with a NaN or +inf: NaN everywhere, ids -1.
 //
-// Bound by memory; with 509 rows of 128896 bf16 (3.3 CTAs to an SM) the loads' latency is covered by
-// 2 x 16 KB on their way to each CTA's shared memory (a step ahead in registers alone: 26.6 us
-// without alternatives, 19.4 by bytes).
+// Bound by memory for many rows: 509 rows of 128896 bf16 take 24.3 us without alternatives, 28.2
+// with 8 (19.4 by bytes; 3.3 CTAs to an SM).  The loads' latency is covered by 2 x 16 KB on their way
+// to each CTA's shared memory (a step ahead in registers alone: 26.6 us).  One row: 6.0 us, latency
+// (the pass 3.3, ranking and the cluster's join 2.7).
 //
 // One pass over the row.  Every thread keeps its own running maximum, S and T (f32) of the
 // 16-byte vectors it owns, rescaled when its maximum rises.  The alternatives cost nothing in

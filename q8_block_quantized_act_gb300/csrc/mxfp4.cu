@@ -1,5 +1,8 @@
 // mxfp4.cu -- MXFP4 quantization (activations and weights), its mirror, and the tiling of
-// row-major scales.  Elementwise passes bound by memory.
+// row-major scales.  Elementwise passes bound by memory: at 20480 x 4096 bf16 the quantizer takes
+// 32.7 us and the mirror 32.6 (6.5 TB/s each, 0.96 of a copy).  Scaling by a power of two is exact,
+// so the conversion to a code is the only rounding of the quantizer, and the mirror's to its type
+// the only one there.
 #include "launch.h"
 #include "mxfp4.cuh"
 #include "types.cuh"
@@ -69,7 +72,8 @@ __device__ __forceinline__ void mx_values(uint32_t w, float (&v)[V])
     }
 }
 
-// A thread makes 16 bytes of each of ROWS rows: 8 values, or 4 of f32.
+// A thread makes 16 bytes of each of ROWS rows: 8 values, or 4 of f32 (8 of f32 would leave in two
+// stores 32 bytes apart: 42.4 us instead of 29.6 at 10240 x 4096).
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, T *__restrict__ y,
@@ -105,6 +109,7 @@ __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t *__res
     }
 }
 
+// Load-time: one byte a thread (0.3 % of the weights' values).
 __global__ void __launch_bounds__(256) tile_mxfp4_scales_kernel(const uint8_t *__restrict__ src,
                                                                 uint8_t *__restrict__ dst, int64_t m, int kb)
 {

@@ -2,7 +2,11 @@
 //   s = x + r (f32),  y = s * (mean(s^2) + eps)^-1/2 * w,  then the q8_1 blocks of y.
 //
 // Bound by memory: x, the residual in, the residual, the quants and scales out.  The row stays in
-// registers between the sum of squares and the quantization, so each is moved once.
+// registers between the sum of squares and the quantization, so each is moved once.  4093 x 8192
+// f16: 38.6 us with a residual to int8 (6.2 TB/s, 0.91 of a copy), 29.2 without (3.6: there the
+// instructions, about 25 a value, and the row's chain of loads, barrier and shuffles count).  All
+// arithmetic is f32; the residual is rounded once to its type, y once, the norm itself not at all
+// before the quantization.
 #include "launch.h"
 #include "q8_1.cuh"
 #include "types.cuh"
