@@ -11,10 +11,12 @@
 // (the pass 3.3, ranking and the cluster's join 2.7).
 //
 // One pass over the row.  Every thread keeps its own running maximum, S and T (f32) of the
-// 16-byte vectors it owns, rescaled when its maximum rises.  The alternatives cost nothing in
-// that pass: of each thread's maximum and the place where it rose, a bound follows that at least
-// `top` of the row's (logit, index) keys reach, and afterwards only the few threads whose maximum
-// reaches it have their vectors read again (from L2).
+// 16-byte vectors it owns, rescaled when its maximum rises, and stores the maximum of each slot of
+// its steps.  The threads' maxima give a bound that at least `top` logits reach; afterwards only the
+// few slots whose maximum reaches it are read again (from L2), and the keys (logit, index) found
+// there are ranked by counting.  Where more slots than the list has places reach it (rows of equal
+// logits, or all but a few at the type's lowest value), the warps go over the row once more with
+// sorted lists in registers, skipping what cannot enter them.
 // Few rows: a cluster of CTAs shares a row and joins its parts through distributed shared memory.
 #include "launch.h"
 #include "types.cuh"
@@ -29,7 +31,7 @@ constexpr int MAX_CL = 8;
 constexpr int CAP = 256;          // keys that the CTA's list holds
 constexpr int MAX_J = 8;
 constexpr int SLOTS = 16;         // maxima kept of each thread's steps
-constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+constexpr float LOG2E = 1.44269504f;
 constexpr float LOWEST = -3.4028235e38f;
 
 // Larger logits and, among equal ones, lower indexes have larger keys; 0 is below every key.
@@ -111,15 +113,15 @@ __device__ __forceinline__ uint4 none()
     return make_uint4(w, w, w, w);
 }
 
-// The largest element of U vectors (NaN ignored).
-template <typename T>
-__device__ __forceinline__ float largest(const uint4 (&r)[U])
+// The largest element of N vectors (NaN ignored).
+template <typename T, int N>
+__device__ __forceinline__ float largest(const uint4 (&r)[N])
 {
     float f[VEC<T>];
     if constexpr (sizeof(T) == 4) {
         float mx = __int_as_float(0xff800000);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < N; ++u) {
             unpack<T>(r[u], f);
             mx = fmaxf(mx, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
         }
@@ -128,7 +130,7 @@ __device__ __forceinline__ float largest(const uint4 (&r)[U])
         using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
         T2 mx = *reinterpret_cast<const T2 *>(&r[0].x);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < N; ++u) {
             const uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx = __hmax2(mx, *reinterpret_cast<const T2 *>(&w[i]));
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
             copies_wait<RING - 1>();
 #pragma unroll
             for (int u = 0; u < U; ++u) cur[u] = sh.ring[step % RING][u][threadIdx.x];
-            const float mx = largest<T>(cur);                         // every vector has been read
+            const float mx = largest<T, U>(cur);                         // every vector has been read
             fetch(step + RING);
             slot_max = fmaxf(slot_max, mx);
             if (--left == 0 || step + 1 == steps) {
@@ -353,9 +355,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
             // Each warp reads the U V elements of a chosen thread's step, one a lane (f32: two
             // steps at once), several in flight.
             constexpr int LANES = U * V, AT_ONCE = 32 / LANES, DEPTH = 8 / AT_ONCE;
-            const int pairs = sh.n_chosen;
+            const int pairs = sh.n_chosen;                            // each holds a key: more than CAP is too many
+            const int scan = pairs <= CAP ? pairs * per_slot : 0;
 #pragma unroll 1
-            for (int i0 = warp * AT_ONCE; i0 < pairs * per_slot; i0 += W * AT_ONCE * DEPTH) {
+            for (int i0 = warp * AT_ONCE; i0 < scan; i0 += W * AT_ONCE * DEPTH) {
                 // per_slot is 1 up to SLOTS steps; longer rows go over a slot's steps one by one
                 float f[DEPTH];
                 int at[DEPTH];
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
                     const int i = i0 + d * W * AT_ONCE + lane / LANES;
                     f[d] = ninf;
                     at[d] = 0;
-                    if (i < pairs * per_slot) {
+                    if (i < scan) {
                         const int pair = sh.chosen[per_slot == 1 ? i : i / per_slot];
                         const int step = per_slot == 1 ? pair % SLOTS : pair % SLOTS * per_slot + i % per_slot;
                         const int L = L0 + step * STEP + pair / SLOTS + lane % LANES / V * THREADS;
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
                     }
             }
             __syncthreads();
-            const int n = sh.n_found;
+            const int n = pairs <= CAP ? sh.n_found : CAP + 1;
             if (n <= CAP) {
                 // A key's place is the number of larger ones; the keys differ, so places do.
                 if ((int)threadIdx.x < n) {
@@ -401,11 +404,34 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(LogprobArgs a, int
                     unsigned some = __ballot_sync(ALL, f >= least && k > worst);
                     for (; some; some &= some - 1) insert32(list, __shfl_sync(ALL, k, __ffs(some) - 1), lane);
                 };
-                if (warp == 0) offer(edge, edge_at);
-                const int e1 = head + L1 * V;
+                // A warp goes through its elements by rising index (the tail last), 32 vectors at a
+                // time: once its list is full, a group without a larger logit than the list's last
+                // has nothing for it, equal ones included.
+                if (warp == 0) offer((int)threadIdx.x < head ? edge : ninf, edge_at);
 #pragma unroll 1
-                for (int e = head + L0 * V + warp * 32; e < e1; e += THREADS)
-                    offer(e + lane < e1 ? to_f32(x[e + lane]) : ninf, e + lane);
+                for (int base = L0 + warp * 32; base < L1; base += U * THREADS) {
+                    uint4 r[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int L = base + u * THREADS + lane;
+                        r[u] = L < L1 ? __ldg(vec + L) : none<T>();
+                    }
+#pragma unroll 1
+                    for (int u = 0; u < U; ++u) {
+                        const uint4 one[1] = {r[0]};
+#pragma unroll
+                        for (int i = 0; i + 1 < U; ++i) r[i] = r[i + 1];
+                        const float mx = largest<T, 1>(one);
+                        const uint64_t last = __shfl_sync(ALL, list, a.top - 1);
+                        if (!__any_sync(ALL, mx >= least && (last == 0 || mx > value_of(last)))) continue;
+                        float f[V];
+                        unpack<T>(one[0], f);
+                        const int at = head + (base + u * THREADS + lane) * V;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) offer(f[j], at + j);
+                    }
+                }
+                if (warp == 0) offer((int)threadIdx.x >= head ? edge : ninf, edge_at);
                 sh.list[warp][lane] = list;
                 __syncthreads();
                 join_lists(sh.list, W, list, warp, lane);
