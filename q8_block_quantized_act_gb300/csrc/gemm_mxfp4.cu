@@ -519,6 +519,10 @@ cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
 // SM keeping its 128 rows' results.  The accumulator takes half of tensor memory and the scales some,
 // so there is one: eight epilogue warps take it into registers at once (128 columns each) and let
 // the next tile's MMAs go, then store.
+//
+// Tiles that do not fill a last round of all pairs are cut into 2 or 4 parts of 128 or 64 tokens, so
+// that the round takes less: a part's MMA reads 8 KB of its 128 weight rows whatever its tokens are,
+// so a quarter costs 0.6 of a tile, not 0.25.
 // ---------------------------------------------------------------------------------------
 struct PairCfg {
     static constexpr int BN = 256, STAGES = 6;
@@ -532,9 +536,7 @@ struct PairCfg {
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr int EPI_WARPS = 8, THREADS = (EPI_WARPS + 2) * 32;
     static constexpr int COL_SC = BN, SC_COLS = 24, TMEM_COLS = 512;
-    static constexpr uint32_t STAGE_TX = 2 * (A_BYTES + B_BYTES + SC_BYTES + SB_BYTES);   // both CTAs' bytes
-    static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
-                                      ((uint32_t)(2 * BM >> 4) << 24);
+    static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(2 * BM >> 4) << 24);  // without N
     static_assert(SMEM_BYTES <= SMEM_MAX, "capacity");
 };
 
@@ -594,14 +596,41 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&a)[4][32])
         for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(a[i][j]));
 }
 
+// Units of work: whole tiles (token tile fastest), then the cut ones' parts.
+struct PairWork {
+    int m, n;
+    int steps;        // k / BK
+    int token_tiles;
+    int whole;        // tiles that stay whole: a multiple of the pairs, or all
+    int shift;        // the others are cut into 1 << shift parts
+    int units;
+    int first_wait;   // as Work's
+};
+
+struct PairUnit {
+    int row, tok, tokens;     // row tile of 256, first token, tokens (256 >> shift)
+};
+__device__ __forceinline__ PairUnit pair_unit(const PairWork &wk, int u)
+{
+    const bool cut = u >= wk.whole;
+    const int shift = cut ? wk.shift : 0, part = u - wk.whole;
+    const int tile = cut ? wk.whole + (part >> shift) : u;
+    PairUnit r;
+    r.row = tile / wk.token_tiles;
+    r.tokens = PairCfg::BN >> shift;
+    r.tok = (tile - r.row * wk.token_tiles) * PairCfg::BN + (cut ? part & ((1 << shift) - 1) : 0) * r.tokens;
+    return r;
+}
+
+// tm_xp: the tokens of a part (its box has fewer rows than tm_x's).
 template <typename T>
 __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     gemm_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                           const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
-                           T *__restrict__ y, Work wk, int *status)
+                           const __grid_constant__ CUtensorMap tm_xp, const __grid_constant__ CUtensorMap tm_ws,
+                           const __grid_constant__ CUtensorMap tm_xs, T *__restrict__ y, PairWork wk, int *status)
 {
     using C = PairCfg;
-    constexpr int BN = C::BN, STAGES = C::STAGES;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);        // used in the first CTA
@@ -629,6 +658,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     if (warp == C::EPI_WARPS && lane == 0) {
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_xp);
         prefetch_tensormap(&tm_ws);
         prefetch_tensormap(&tm_xs);
     }
@@ -640,28 +670,33 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 
     if (warp == C::EPI_WARPS) {
         // ------------------------------ producer ------------------------------
-        int row_tile, token_tile;
-        auto enter = [&](int tile) {
-            const int rt = tile / wk.token_tiles;
-            token_tile = tile - rt * wk.token_tiles;
-            row_tile = 2 * rt + (int)rank;                              // this CTA's 128 rows
+        int row_tile, tok, scale_row;
+        uint32_t bytes;                                                 // both CTAs' of a stage
+        const CUtensorMap *map_x;
+        auto enter = [&](int u) {
+            const PairUnit unit = pair_unit(wk, u);
+            row_tile = 2 * unit.row + (int)rank;                        // this CTA's 128 rows
+            tok = unit.tok + (int)rank * (unit.tokens / 2);             // and its half of the tokens
+            scale_row = unit.tok / C::BN * 2;
+            map_x = u < wk.whole ? &tm_x : &tm_xp;
+            bytes = 2 * (A_BYTES + SC_BYTES + C::SB_BYTES) + (uint32_t)unit.tokens * ROW_BYTES;
         };
         auto load_w = [&](int st, int ks) {
             const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[st], C::STAGE_TX);
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
             pair_load_2d(smem + C::OFF_A + st * A_BYTES, &tm_w, ks * ROW_BYTES, row_tile * BM, bar);
             pair_load_2d(smem + C::OFF_SA + st * SC_BYTES, &tm_ws, ks * (SC_BYTES / 8), row_tile, bar);
         };
         auto load_x = [&](int st, int ks) {
             const uint32_t bar = cluster_addr(smem_u32(&full[st]), 0);
-            pair_load_2d(smem + C::OFF_B + st * C::B_BYTES, &tm_x, ks * ROW_BYTES, token_tile * BN + (int)rank * (BN / 2), bar);
-            pair_load_2d(smem + C::OFF_SB + st * C::SB_BYTES, &tm_xs, ks * (SC_BYTES / 8), 2 * token_tile, bar);
+            pair_load_2d(smem + C::OFF_B + st * C::B_BYTES, map_x, ks * ROW_BYTES, tok, bar);
+            pair_load_2d(smem + C::OFF_SB + st * C::SB_BYTES, &tm_xs, ks * (SC_BYTES / 8), scale_row, bar);
         };
         // As in gemm_mxfp4_kernel: the first stages' weights before the wait in a fused call.
         if (wk.first_wait) griddep_wait();
         int early = 0;
-        for (int tile = pair; tile < wk.tiles && early < STAGES; tile += pairs) {
-            enter(tile);
+        for (int u = pair; u < wk.units && early < STAGES; u += pairs) {
+            enter(u);
             for (int ks = 0; ks < wk.steps && early < STAGES; ++ks, ++early)
                 if (elect_one()) load_w(early, ks);
         }
@@ -670,8 +705,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         int st = 0, it = 0;
         uint32_t phase = 1;
         bool ok = true;
-        for (int tile = pair; ok && tile < wk.tiles; tile += pairs) {
-            enter(tile);
+        for (int u = pair; ok && u < wk.units; u += pairs) {
+            enter(u);
             for (int ks = 0; ks < wk.steps; ++ks, ++it) {
                 if (it >= early) {
                     ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], phase, status, abort_flag));
@@ -713,13 +748,14 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                                          sbdesc0 + (uint64_t)((st * C::SB_BYTES + b * SC_BYTES + g * MX_TILE_BYTES) >> 4));
                 }
             };
+            uint32_t idesc = 0, sb_shift = 0;      // of the unit: N; its first token's column of scales
             auto multiply = [&](int slot, int st, bool first) {
-                const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8;
+                const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8 + sb_shift;
                 const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
                 const uint64_t bd = bdesc0 + (uint64_t)(st * (C::B_BYTES >> 4));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t id = C::IDESC | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
+                    const uint32_t id = idesc | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
                     pair_mma(tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 8 * (j >> 1), !first || j > 0);
                 }
                 pair_commit(&empty[st]);
@@ -727,7 +763,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             int st = 0, i = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < wk.tiles; tile += pairs, ++i) {
+            for (int u = pair; ok && u < wk.units; u += pairs, ++i) {
+                const PairUnit unit = pair_unit(wk, u);
+                idesc = C::IDESC | ((uint32_t)(unit.tokens >> 3) << 17);
+                sb_shift = (uint32_t)(unit.tok % C::BN / 32);
                 ok = __all_sync(0xffffffffu, wait_or_abort(acc_empty, (i & 1) ^ 1, status, abort_flag));
                 if (!ok) break;
                 for (int ks = 0; ks < wk.steps;) {
@@ -759,26 +798,26 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         }
     } else {
         // ------------------------------ epilogue ------------------------------
-        const int quarter = warp & 3, half = warp >> 2;                  // 32 lanes, 128 of the columns
+        const int quarter = warp & 3, half = warp >> 2;                  // 32 lanes, half of the columns
         int i = 0;
-        for (int tile = pair; tile < wk.tiles; tile += pairs, ++i) {
-            const int rt = tile / wk.token_tiles, tt = tile - rt * wk.token_tiles;
-            const int64_t r = (int64_t)(2 * rt + (int)rank) * BM + 32 * quarter + lane;
-            const int tok0 = tt * BN + half * (BN / 2);
-            const int cols = min(BN / 2, wk.m - tok0);
+        for (int u = pair; u < wk.units; u += pairs, ++i) {
+            const PairUnit unit = pair_unit(wk, u);
+            const int64_t r = (int64_t)(2 * unit.row + (int)rank) * BM + 32 * quarter + lane;
+            const int per = unit.tokens / 2, tok0 = unit.tok + half * per;
+            const int cols = min(per, wk.m - tok0);
             if (!__all_sync(0xffffffffu, wait_or_abort(acc_full, i & 1, status, abort_flag))) break;
             tc_fence_after();
             uint32_t v[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                tc_ld_x32(tmem + ((uint32_t)(32 * quarter) << 16) + half * (BN / 2) + 32 * q, v[q]);
+                if (32 * q < per) tc_ld_x32(tmem + ((uint32_t)(32 * quarter) << 16) + half * per + 32 * q, v[q]);
             tc_wait_ld(v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) cluster_arrive(cluster_addr(smem_u32(acc_empty), 0));
             if (r < wk.n) {
                 T *dst = y + (int64_t)tok0 * wk.n + r;
-                if (cols == BN / 2) {
+                if (cols == C::BN / 2) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -803,33 +842,46 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     }
 }
 
+// Into how many parts (1 << shift) the tiles of a last round that leaves pairs idle are cut: as many
+// as the pairs can take at once, at most 4 (64 tokens).
+int pair_shift(int64_t tiles, int64_t pairs)
+{
+    const int64_t left = tiles % pairs;
+    return left * 4 <= pairs ? 2 : left * 2 <= pairs ? 1 : 0;
+}
+
 template <typename T>
 cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
                          const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, bool pdl, cudaStream_t stream)
 {
     cudaError_t e = set_kernel_smem<gemm_mxfp4_pair_kernel<T>>(dev.device, PairCfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
+    const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + PairCfg::BN - 1) / PairCfg::BN);
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const int64_t at_once = dev.num_sms / 2;
+    PairWork wk{};
+    wk.m = (int)m;
+    wk.n = (int)n;
+    wk.steps = (int)(k / BK);
+    wk.token_tiles = (int)((m + PairCfg::BN - 1) / PairCfg::BN);
+    wk.shift = pair_shift(tiles, at_once);
+    wk.whole = (int)(wk.shift ? tiles / at_once * at_once : tiles);
+    wk.units = wk.whole + ((int)tiles - wk.whole) * (1 << wk.shift);
+    wk.first_wait = pdl ? 0 : 1;
+    const int64_t pairs = wk.units < at_once ? wk.units : at_once;
     const uint64_t sc_row = (uint64_t)k / MX_TILE_K * MX_TILE_BYTES;      // bytes of 128 rows' scales
-    CUtensorMap tm_w, tm_x, tm_ws, tm_xs;
+    CUtensorMap tm_w, tm_x, tm_xp, tm_ws, tm_xs;
     if (!encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)k / 2, (uint64_t)n, (uint64_t)k / 2, ROW_BYTES, BM,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
                    PairCfg::BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&tm_xp, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
+                   (PairCfg::BN / 2) >> wk.shift, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tm_ws, CU_TENSOR_MAP_DATA_TYPE_UINT64, wsc, sc_row / 8, (uint64_t)(n + 127) / 128, sc_row,
                    SC_BYTES / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !encode_2d(&tm_xs, CU_TENSOR_MAP_DATA_TYPE_UINT64, xsc, sc_row / 8, (uint64_t)(m + 127) / 128, sc_row,
                    SC_BYTES / 8, 2, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    Work wk{};
-    wk.m = (int)m;
-    wk.n = (int)n;
-    wk.steps = (int)(k / BK);
-    wk.token_tiles = (int)((m + PairCfg::BN - 1) / PairCfg::BN);
-    const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * wk.token_tiles;
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    wk.tiles = (int)tiles;
-    wk.first_wait = pdl ? 0 : 1;
-    const int64_t pairs = tiles < dev.num_sms / 2 ? tiles : dev.num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(PairCfg::THREADS);
@@ -843,7 +895,7 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<T>, tm_w, tm_x, tm_ws, tm_xs, y, wk, dev.status);
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<T>, tm_w, tm_x, tm_xp, tm_ws, tm_xs, y, wk, dev.status);
 }
 
 }  // namespace

@@ -154,6 +154,18 @@ def test_product_matches_64_bits(m, n, k, kind):
     check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), kind)
 
 
+@pytest.mark.parametrize("m,n,k", [(512, 20480, 512), (300, 20300, 256), (1100, 20480, 256), (257, 40000, 256),
+                                   (200, 64448, 512), (1000, 19457, 256)])
+def test_product_last_round(m, n, k):
+    """Tiles that do not fill a last round of all SMs, cut into two, into four, or whole; ragged in both."""
+    ensure_built()
+    wc, wb, wp, wt = matrix(n, k, 30 + n, 100, 124)
+    xc, xb, xp, xt = matrix(m, k, 40 + m, 124, 130)
+    y = q8.gemm_mxfp4_preq(cuda(wp), cuda(wt), cuda(xp), cuda(xt), dtype=torch.bfloat16)
+    device_ok()
+    check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), "bf16")
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(1, 640, 1024), (13, 333, 512), (200, 512, 768)])
 def test_fused_call_is_quantize_then_product(m, n, k, kind):
