@@ -18,7 +18,7 @@
 // the owner adds them in rank order, so the result does not depend on timing.
 //
 // What bounds it: the weight stream for few tokens (5 x 64448 x 4096: 26 us for 142 MB with the
-// activation's quantization; 1 x 4096 x 4096, 32 tiles shared by four CTAs each: 5.4 us, latency), the
+// activation's quantization; 1 x 4096 x 4096, 32 tiles shared by four CTAs each: 5.2 us, latency), the
 // MMAs for many (pairs of CTAs, below: 4095 x 20480 x 8192 in 210 us, 6.5 PFLOP/s with its quantizer).
 // No rounding between the codes and y: products of codes and scales are exact, sums are the tensor
 // cores' f32, y is rounded once.
@@ -903,12 +903,14 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
 namespace {
 
 // The tile shape of a product and how many CTAs share a tile's k: the least of
-//   waves * (steps of a CTA * time of a step + filling the pipeline and storing the tile + joining)
-// over the tile widths and the powers of two up to 8 that leave each CTA a step.  Times in ns, from
-// measurements: a step of 16 / 32 / 64 / 128 / 192 tokens takes 170 - 400 by its MMAs and 390 - 500
-// where all SMs load their operands at once; a pair's 256 x 256 step 330.  (131 x 4096 x 1280 in tiles
-// of 192 tokens 7.9 us, of 64 6.4; 300 x 1000 x 8192 by pairs 15.8, 128 tokens shared by four CTAs
-// 10.0; 5 x 64448 x 4096, 504 tiles: shared by two 36, not shared 26.)
+//   rounds * (steps of a CTA * time of a step + the tile's start and end + joining its partial sums)
+// over the tile widths, the powers of two up to 8 that leave each CTA a step, and pairs (a last
+// round of cut tiles with its own times).  The times, in ns, are fitted to every such choice measured
+// at 741 sizes (m from 1 to 1000, n from 1000 to 64448, k from 512 to 20480, weights from HBM):
+// what the formula takes is 0.4 % above the best choice on average, 19 % at worst (200 x 4096 x
+// 4096: 7.1 us in 64-token tiles, 14.8 in 128-token tiles shared by two, 8.3 by pairs; 1 x 2500 x
+// 20480: 12.1 shared by four, 21.2 not shared).  Joining is dear where tiles are wide: each column's
+// partial sums cross the cluster.
 struct Plan {
     int bn, CL;       // bn = 256: pairs
 };
@@ -916,24 +918,30 @@ struct Plan {
 Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
-    static const struct { int bn, step, busy, tile; } shapes[] = {
-        {16, 170, 390, 1200}, {32, 200, 410, 1400}, {64, 250, 450, 1800}, {128, 330, 500, 2500}, {192, 400, 500, 3300}};
+    static const struct { int bn, step, ends; } shapes[] = {
+        {16, 220, 0}, {32, 230, 50}, {64, 210, 640}, {128, 270, 1310}, {192, 290, 3550}};
+    static const struct { int step, ends; } parts[] = {{310, 2250}, {230, 2200}, {215, 1900}};   // by pair_shift
+    static const int join_start = 1650, join_column[] = {0, 47, 31, 21};                         // CL = 1, 2, 4, 8
     Plan best{256, 1};
     int64_t least = INT64_MAX;
-    if (m > 128) {
+    if (m > 64) {
         const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + 255) / 256), at_once = dev.num_sms / 2;
-        least = (tiles + at_once - 1) / at_once * (steps * 330 + 2500);
+        least = tiles / at_once * (steps * parts[0].step + parts[0].ends);
+        if (tiles % at_once) {
+            const auto &last = parts[pair_shift(tiles, at_once)];
+            least += steps * last.step + last.ends;
+        }
     }
     for (const auto &s : shapes) {
         if (s.bn < 64 && m > s.bn) continue;                      // narrow tiles start at a scale tile's first row
         if (s.bn > 16 && s.bn >= 2 * m) continue;
         const int64_t tiles = rows * ((m + s.bn - 1) / s.bn);
-        for (int CL = 1; CL <= 8 && CL <= steps; CL *= 2) {
+        for (int CL = 1, i = 0; CL <= 8 && CL <= steps; CL *= 2, ++i) {
             if (CL > 1 && s.bn > 128) break;                      // no room for partial sums
             const int64_t at_once = dev.num_sms / CL - (CL == 8 ? dev.num_sms / 32 : 0);   // GPCs hold few clusters of 8
-            const int64_t waves = (tiles + at_once - 1) / at_once, active = (tiles < at_once ? tiles : at_once) * CL;
-            const int64_t cost = waves * ((steps + CL - 1) / CL * (active * 2 > dev.num_sms ? s.busy : s.step) + s.tile +
-                                          (CL > 1 ? 1200 : 0));
+            const int64_t rounds = (tiles + at_once - 1) / at_once;
+            const int64_t cost = rounds * ((steps + CL - 1) / CL * s.step + s.ends +
+                                           (CL > 1 ? join_start + s.bn * join_column[i] : 0));
             if (cost < least) {
                 least = cost;
                 best = {s.bn, CL};
