@@ -236,21 +236,24 @@ cudaError_t launch_rows(const DeviceInfo &dev, const NormArgs &a, int64_t m, int
 {
     const int chunks = (int)(k / VEC<T>);                  // a multiple of 32
     const dim3 grid((unsigned)m);
-    // Few rows: every thread that a CTA can have, one chunk each if that is enough (latency).  Many:
-    // small CTAs with 32 values a thread (8 of f32), so that several rows are under way on an SM and
-    // one row's barrier leaves the others working (4093 x 8192 f16: 256 threads 31.5 us, 512 threads
-    // 38.9; 4093 x 4096 f32: 512 threads of 8 values 22.2 us, 256 of 16 25.4).
-    constexpr int CHUNKS = VEC<T> == 8 ? 4 : 2;
-    int threads = m <= 4 * dev.num_sms ? 1024 : 256;
-    while (threads < 1024 && chunks > threads * CHUNKS) threads *= 2;
-    if (threads > chunks) threads = chunks;
+    // A row to an SM at most: every thread that a CTA can have, one chunk each if that is enough
+    // (latency).  More: small CTAs with up to four chunks a thread, so that several rows are under way
+    // on an SM and one row's barrier leaves the others working (1024, 512, 256 threads: 64 x 8192 bf16
+    // 3.1, 3.4, 4.3 us; 256 x 8192 bf16 5.9, 4.6, 5.6; 304 x 4096 f32 3.9, 4.4; 512 x 4096 f32 5.7, 5.4,
+    // 4.8; 4093 x 8192 f32 67, 43, too long for 256; 8192 x 8192 bf16 137, 85, 67; 256, 128, 64 threads:
+    // 1024 x 4096 bf16 7.2, 7.7, 18; 8192 x 1024 f32 13.5, 11.3, 11.3).
+    const int sms = dev.num_sms;
+    const int about = m <= sms || (m <= 2 * sms && VEC<T> == 4 && chunks <= 1024) ? 1024
+                      : m <= 2 * sms ? 512 : m <= 20 * sms ? 256 : 128;
+    int share = (chunks + about / 2) / about;              // chunks a thread, to the nearest
+    share = share < 1 ? 1 : share > 4 ? 4 : share;
+    int threads = ((chunks + share - 1) / share + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
     const int each = (chunks + threads - 1) / threads;
     auto go = [&](auto kern) { return launch_dependent(kern, grid, threads, 0, stream, a, (int)k); };
     if (each == 1) return go(rmsnorm_row_kernel<T, MMQ, 1, 1024>);
     if (each == 2) return go(rmsnorm_row_kernel<T, MMQ, 2, 1024>);
     if (each <= 4) return threads <= 256 ? go(rmsnorm_row_kernel<T, MMQ, 4, 256>) : go(rmsnorm_row_kernel<T, MMQ, 4, 1024>);
-    if constexpr (VEC<T> == 4)
-        if (each <= 8) return go(rmsnorm_row_kernel<T, MMQ, 8, 1024>);
     return launch_dependent(rmsnorm_long_kernel<T, MMQ>, grid, 1024, 0, stream, a, (int)k);
 }
 
