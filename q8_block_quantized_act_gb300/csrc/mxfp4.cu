@@ -123,17 +123,16 @@ __global__ void __launch_bounds__(256) tile_mxfp4_scales_kernel(const uint8_t *_
     }
 }
 
-dim3 grid_rows(int64_t rows, int64_t chunks, int each)
+// CTAs of at most 256 threads that share a row's chunks (a multiple of 32) evenly.
+struct RowGrid {
+    dim3 grid;
+    int threads;
+};
+RowGrid grid_rows(int64_t rows, int64_t chunks, int each)
 {
-    const int64_t groups = (rows + each - 1) / each;
-    return dim3((unsigned)((chunks + 255) / 256), (unsigned)(groups < 65535 ? groups : 65535));
-}
-
-// Rows a thread has in flight: four where that still leaves the GPU full of threads (more bytes
-// under way), else one (a few rows are a matter of latency).
-bool four_rows(const DeviceInfo &dev, int64_t rows, int64_t chunks)
-{
-    return (rows + 3) / 4 * chunks >= (int64_t)dev.num_sms * 2048;
+    const int64_t groups = (rows + each - 1) / each, ctas = (chunks + 255) / 256;
+    return {dim3((unsigned)ctas, (unsigned)(groups < 65535 ? groups : 65535)),
+            (int)(((chunks + ctas - 1) / ctas + 31) / 32 * 32)};
 }
 
 }  // namespace
@@ -145,10 +144,15 @@ cudaError_t launch_quantize_mxfp4(const DeviceInfo &dev, const void *x, int64_t 
         using T = decltype(t);
         const int64_t padded = (m + MX_TILE_ROWS - 1) / MX_TILE_ROWS * MX_TILE_ROWS;
         auto go = [&](auto kern, int each) {
-            return launch_dependent(kern, grid_rows(padded, k / 8, each), 256, 0, stream, static_cast<const T *>(x), ldx,
+            const RowGrid g = grid_rows(padded, k / 8, each);
+            return launch_dependent(kern, g.grid, g.threads, 0, stream, static_cast<const T *>(x), ldx,
                                     reinterpret_cast<uint32_t *>(codes), scales, m, (int)k);
         };
-        return four_rows(dev, m, k / 8) ? go(quantize_mxfp4_kernel<T, 4>, 4) : go(quantize_mxfp4_kernel<T, 1>, 1);
+        // Four rows a thread (more bytes under way) from so many chunks an SM on; below, latency counts.
+        // One row and four: 256 x 4096 f32 2.3 and 2.7 us, 8192 x 4096 f32 24.2 and 23.5; 1024 x 4096 bf16
+        // 3.8 and 4.1, 2048 x 4096 bf16 6.4 and 5.4, 8192 x 4096 bf16 20.8 and 14.1.
+        const int64_t from = sizeof(T) == 4 ? 8192 : 4000;
+        return m * (k / 8) >= dev.num_sms * from ? go(quantize_mxfp4_kernel<T, 4>, 4) : go(quantize_mxfp4_kernel<T, 1>, 1);
     });
 }
 
@@ -158,10 +162,12 @@ cudaError_t launch_dequant_mxfp4(const DeviceInfo &dev, const uint8_t *codes, co
     return with_type(type, [&](auto t) {
         using T = decltype(t);
         auto go = [&](auto kern, int each) {
-            return launch_dependent(kern, grid_rows(m, k / VEC<T>, each), 256, 0, stream, codes, scales,
-                                    static_cast<T *>(y), m, (int)k);
+            const RowGrid g = grid_rows(m, k / VEC<T>, each);
+            return launch_dependent(kern, g.grid, g.threads, 0, stream, codes, scales, static_cast<T *>(y), m, (int)k);
         };
-        return four_rows(dev, m, k / VEC<T>) ? go(dequant_mxfp4_kernel<T, 4>, 4) : go(dequant_mxfp4_kernel<T, 1>, 1);
+        // One row a thread and four: 512 x 1024 bf16 1.6 and 1.8 us, 1024 x 4096 bf16 3.8 and 3.3,
+        // 8192 x 4096 bf16 20.8 and 13.5, 1024 x 4096 f32 5.7 and 4.6.
+        return m * (k / VEC<T>) >= (int64_t)dev.num_sms * 800 ? go(dequant_mxfp4_kernel<T, 4>, 4) : go(dequant_mxfp4_kernel<T, 1>, 1);
     });
 }
 
