@@ -107,6 +107,41 @@ __device__ __forceinline__ void tc_ld_x16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
+// 32 lanes x 32 columns, asynchronous: the registers are valid after tc_wait_ld.
+__device__ __forceinline__ void tc_ld_x32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's loads from tensor memory; binds the registers to the wait.
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&a)[N][32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(a[i][j]));
+}
+
+// 32 lanes x N columns.
+__device__ __forceinline__ void tc_columns(uint32_t taddr, uint32_t (&v)[1][16]) { tc_ld_x16(taddr, v[0]); }
+template <int N>
+__device__ __forceinline__ void tc_columns(uint32_t taddr, uint32_t (&v)[N][32])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) tc_ld_x32(taddr + 32 * i, v[i]);
+    tc_wait_ld(v);
+}
+
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -132,12 +167,19 @@ __device__ __forceinline__ void cluster_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// wait_or_abort whose success also orders what other CTAs of the cluster wrote before arriving.
+// wait_or_abort whose success also orders what other CTAs of the cluster did before arriving: the
+// completed phase is read once more with the cluster's scope (a fence would wait for this thread's
+// own stores to the other CTAs too).
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag)
 {
-    const bool ok = wait_or_abort(bar, parity, status, abort_flag);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return ok;
+    if (!wait_or_abort(bar, parity, status, abort_flag)) return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 struct Work {
@@ -167,7 +209,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // Warp-uniform to the compiler too: the roles' loops then live in uniform registers.
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = CL > 1 ? cluster_rank() : 0;
+    const bool shared = C::SPLIT && CL > 1;                   // a tile's k, by a cluster
+    const uint32_t rank = shared ? cluster_rank() : 0;
     const int cluster = blockIdx.x / CL, clusters = gridDim.x / CL;
     const int ks0 = wk.steps * (int)rank / CL, ks1 = wk.steps * ((int)rank + 1) / CL;
     const int ktiles = wk.steps * (BK / MX_TILE_K);
@@ -190,7 +233,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (CL > 1) cluster_sync_all();         // every rank's barriers exist before anyone arrives on them
+    // Every rank's barriers exist before anyone arrives on them: the epilogue waits for it, the others
+    // when they are done.
+    if (shared) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == 4) {
@@ -362,6 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(x_ready);
         }
         int i = 0;
+        bool met = false;                      // the cluster's first barrier has been waited for
         for (int tile = cluster; tile < wk.tiles; tile += clusters, ++i) {
             const int acc = i & 1;
             const int64_t r = (int64_t)(tile / wk.token_tiles) * BM + row;
@@ -370,15 +416,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[acc], (i >> 1) & 1, status, abort_flag))) break;
             tc_fence_after();
             T *dst = y + (int64_t)tok0 * wk.n + r;
-            if (CL == 1) {
+            // columns read from tensor memory at once
+            constexpr int LD = BN < 32 ? BN : 32, LDS = BN < 64 ? 1 : 2, PART = LD * LDS;
+            if (!shared) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    uint32_t v[16];
-                    tc_ld_x16(tmem + lane_base + acc * BN + c0, v);
-                    if (r < wk.n)
+                for (int c0 = 0; c0 < cols; c0 += PART) {
+                    uint32_t v[LDS][LD];
+                    tc_columns(tmem + lane_base + acc * BN + c0, v);
+                    if (r >= wk.n) continue;
+                    if (c0 + PART <= cols) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            if (c0 + c < cols) dst[(int64_t)(c0 + c) * wk.n] = from_f32<T>(__uint_as_float(v[c]));
+                        for (int c = 0; c < PART; ++c, dst += wk.n) *dst = from_f32<T>(__uint_as_float(v[c / LD][c % LD]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < PART; ++c, dst += wk.n)
+                            if (c0 + c < cols) *dst = from_f32<T>(__uint_as_float(v[c / LD][c % LD]));
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -386,17 +439,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             } else if constexpr (C::SPLIT) {
                 // BN and CL are powers of two: rank o owns the BN / CL columns from o BN / CL on.
                 const int per = BN / CL, shift = 31 - __clz(per);
-                if (!__all_sync(0xffffffffu, wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag))) break;
+                if (!met) {
+                    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                    met = true;
+                } else if (!__all_sync(0xffffffffu, wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag))) {
+                    break;
+                }
                 const uint32_t mine = smem_u32(red + (int)rank * per * BM + row);
 #pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    uint32_t v[16];
-                    tc_ld_x16(tmem + lane_base + acc * BN + c0, v);
+                for (int c0 = 0; c0 < cols; c0 += PART) {
+                    uint32_t v[LDS][LD];
+                    tc_columns(tmem + lane_base + acc * BN + c0, v);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < PART; ++c)
                         if (c0 + c < cols)
                             cluster_store(cluster_addr(mine + (uint32_t)(((c0 + c) & (per - 1)) * BM * 4), (c0 + c) >> shift),
-                                          __uint_as_float(v[c]));
+                                          __uint_as_float(v[c / LD][c % LD]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -419,11 +477,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane < CL) cluster_arrive(cluster_addr(smem_u32(red_empty), lane));
             }
         }
+        if (shared && !met) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 
+    __syncwarp();
+    if (shared && warp >= 4) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_before();
     __syncthreads();
-    if (CL > 1) cluster_sync_all();         // nobody leaves while others may still write to it
+    if (shared) cluster_sync_all();         // nobody leaves while others may still write to it
     if (warp == 5) {
         tc_fence_after();
         tc_dealloc(tmem, C::TMEM_COLS);
@@ -570,30 +631,6 @@ __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, 
         " [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
-}
-
-// 32 lanes x 32 columns, asynchronous: the registers are valid after tc_wait_ld.
-__device__ __forceinline__ void tc_ld_x32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-        "%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-// Waits for this thread's loads from tensor memory; binds the registers to the wait.
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&a)[4][32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(a[i][j]));
 }
 
 // Units of work: whole tiles (token tile fastest), then the cut ones' parts.
