@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr int OFF_SA = OFF_B + XSLOTS * B_BYTES;
     static constexpr int OFF_SB = OFF_SA + STAGES * SC_BYTES;
     static constexpr int OFF_RED = OFF_SB + XSLOTS * NSB * SC_BYTES;
-    static constexpr int OFF_BAR = OFF_RED + (SPLIT ? BN * BM * 4 : 0);
+    static constexpr int OFF_BAR = OFF_RED + (SPLIT ? (BN < 32 ? 32 : BN) * BM * 4 : 0);   // 4 columns a rank at least
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4 + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;   // + slack for 1024-byte base alignment
     // Tensor memory: two accumulators, then two slots of scales (weights 8 columns, tokens 8 per
@@ -159,9 +159,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void cluster_store(uint32_t addr, float v)
+__device__ __forceinline__ void cluster_store4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive(uint32_t bar)
 {
@@ -437,41 +437,55 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[acc]);
             } else if constexpr (C::SPLIT) {
-                // BN and CL are powers of two: rank o owns the BN / CL columns from o BN / CL on.
-                const int per = BN / CL, shift = 31 - __clz(per);
+                // BN and CL are powers of two: rank o owns the columns of BN / CL / 4 groups of four (at
+                // least one) from its first on; its partial sums stand as [rank][group][row][four].
+                const int groups = BN / 4 / CL > 0 ? BN / 4 / CL : 1, shift = 31 - __clz(groups);
                 if (!met) {
                     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
                     met = true;
                 } else if (!__all_sync(0xffffffffu, wait_cluster(red_empty, (i & 1) ^ 1, status, abort_flag))) {
                     break;
                 }
-                const uint32_t mine = smem_u32(red + (int)rank * per * BM + row);
+                const uint32_t mine = smem_u32(red + ((int)rank * groups * BM + row) * 4);
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += PART) {
                     uint32_t v[LDS][LD];
                     tc_columns(tmem + lane_base + acc * BN + c0, v);
 #pragma unroll
-                    for (int c = 0; c < PART; ++c)
+                    for (int c = 0; c < PART; c += 4) {
+                        const int g = (c0 + c) >> 2;
                         if (c0 + c < cols)
-                            cluster_store(cluster_addr(mine + (uint32_t)(((c0 + c) & (per - 1)) * BM * 4), (c0 + c) >> shift),
-                                          __uint_as_float(v[c / LD][c % LD]));
+                            cluster_store4(cluster_addr(mine + (uint32_t)((g & (groups - 1)) * BM * 16), g >> shift),
+                                           v[c / LD][c % LD], v[c / LD][c % LD + 1], v[c / LD][c % LD + 2],
+                                           v[c / LD][c % LD + 3]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[acc]);
                 if (lane < CL) cluster_arrive(cluster_addr(smem_u32(red_full), lane));
                 if (!__all_sync(0xffffffffu, wait_cluster(red_full, i & 1, status, abort_flag))) break;
-                const int own0 = (int)rank * per;
-#pragma unroll 2
-                for (int c = 0; c < per && own0 + c < cols; ++c) {
-                    float part[8];
+                const int own0 = (int)rank * groups * 4;
+                const float4 *parts = reinterpret_cast<const float4 *>(red) + row;
+#pragma unroll 1
+                for (int g = 0; g < groups && own0 + 4 * g < cols; ++g) {
+                    float4 part[8];
 #pragma unroll
-                    for (int src = 0; src < 8; ++src) part[src] = src < CL ? red[(src * per + c) * BM + row] : 0.0f;
-                    float sum = part[0];
+                    for (int src = 0; src < 8; ++src)
+                        part[src] = src < CL ? parts[(src * groups + g) * BM] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float sum[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
 #pragma unroll
                     for (int src = 1; src < 8; ++src)
-                        if (src < CL) sum += part[src];                 // in rank order
-                    if (r < wk.n) dst[(int64_t)(own0 + c) * wk.n] = from_f32<T>(sum);
+                        if (src < CL) {                                          // in rank order
+                            sum[0] += part[src].x;
+                            sum[1] += part[src].y;
+                            sum[2] += part[src].z;
+                            sum[3] += part[src].w;
+                        }
+                    if (r < wk.n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (own0 + 4 * g + c < cols) dst[(int64_t)(own0 + 4 * g + c) * wk.n] = from_f32<T>(sum[c]);
                 }
                 __syncwarp();
                 if (lane < CL) cluster_arrive(cluster_addr(smem_u32(red_empty), lane));
