@@ -958,10 +958,9 @@ namespace {
 // over the tile widths, the powers of two up to 8 that leave each CTA a step, and pairs (a last
 // round of cut tiles with its own times).  The times, in ns, are fitted to every such choice measured
 // at 741 sizes (m from 1 to 1000, n from 1000 to 64448, k from 512 to 20480, weights from HBM):
-// what the formula takes is 0.4 % above the best choice on average, 19 % at worst (200 x 4096 x
-// 4096: 7.1 us in 64-token tiles, 14.8 in 128-token tiles shared by two, 8.3 by pairs; 1 x 2500 x
-// 20480: 12.1 shared by four, 21.2 not shared).  Joining is dear where tiles are wide: each column's
-// partial sums cross the cluster.
+// what the formula takes is 0.6 % above the best choice on average, 21 % at worst (256 x 4096 x 4096:
+// 6.7 us in 64-token tiles, 8.2 in 128-token ones, 10.8 if two share those, 8.3 by pairs; 1 x 2500 x
+// 20480: 11.7 shared by four, 21.2 not shared).
 struct Plan {
     int bn, CL;       // bn = 256: pairs
 };
@@ -970,9 +969,9 @@ Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
     static const struct { int bn, step, ends; } shapes[] = {
-        {16, 220, 0}, {32, 230, 50}, {64, 210, 640}, {128, 270, 1310}, {192, 290, 3550}};
-    static const struct { int step, ends; } parts[] = {{310, 2250}, {230, 2200}, {215, 1900}};   // by pair_shift
-    static const int join_start = 1650, join_column[] = {0, 47, 31, 21};                         // CL = 1, 2, 4, 8
+        {16, 240, 200}, {32, 230, 200}, {64, 210, 380}, {128, 290, 590}, {192, 310, 1110}};
+    static const struct { int step, ends; } parts[] = {{290, 2370}, {230, 2260}, {240, 2060}};   // by pair_shift
+    static const int join_start = 940, join_column[] = {0, 25, 27, 21};                          // CL = 1, 2, 4, 8
     Plan best{256, 1};
     int64_t least = INT64_MAX;
     if (m > 64) {
@@ -992,7 +991,7 @@ Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
             const int64_t at_once = dev.num_sms / CL - (CL == 8 ? dev.num_sms / 32 : 0);   // GPCs hold few clusters of 8
             const int64_t rounds = (tiles + at_once - 1) / at_once;
             const int64_t cost = rounds * ((steps + CL - 1) / CL * s.step + s.ends +
-                                           (CL > 1 ? join_start + s.bn * join_column[i] : 0));
+                                           (CL > 1 ? join_start + (m < s.bn ? m : s.bn) * join_column[i] : 0));
             if (cost < least) {
                 least = cost;
                 best = {s.bn, CL};
