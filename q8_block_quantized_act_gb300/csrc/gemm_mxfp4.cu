@@ -582,37 +582,44 @@ cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
 }
 
 // ---------------------------------------------------------------------------------------
-// Many tokens: a pair of CTAs (two SMs) on one tile of 256 weight rows x 256 tokens.
+// Many tokens: a pair of CTAs (two SMs) on one tile of 256 weight rows x 256 or 192 tokens.
 //
 // What bounds one CTA's MMAs is reading their operands from shared memory: at 64 values of k,
 // 128 x N takes (128 + N) * 32 bytes, and the measured times (126, 151, 180 cycles for N = 128,
 // 192, 256) are 64 bytes a cycle.  A pair's MMA (cta_group::2) leaves half of the tokens' operand to
 // each SM: 8 KB for 128 x 256 outputs an SM, which is what its arithmetic takes (128 cycles).
 //
-// Each CTA loads its 128 weight rows, its 128 of the tokens, its rows' scales and all tokens' scales;
+// Each CTA loads its 128 weight rows, its half of the tokens, its rows' scales and all tokens' scales;
 // all copies of a stage arrive on the first CTA's barrier, whose issuer runs the MMAs of both, each
-// SM keeping its 128 rows' results.  The accumulator takes half of tensor memory and the scales some,
-// so there is one: eight epilogue warps take it into registers at once (128 columns each) and let
-// the next tile's MMAs go, then store.
+// SM keeping its 128 rows' results.  Eight epilogue warps take an accumulator into registers at once
+// (half of the columns each), release it, then store.  256 tokens: two accumulators would leave tensor
+// memory no room for the scales, so the next tile's MMAs wait for the hand-over (2.4 us a tile).  192
+// tokens: two, and no such wait, for 112 cycles of operands where the arithmetic takes 96.  So 192 is
+// faster up to k = 4096 (2048 x 12288 x 4096: 34.4 us, 41.2 by 256) and about equal at 8192.
 //
-// Tiles that do not fill a last round of all pairs are cut into 2 or 4 parts of 128 or 64 tokens, so
-// that the round takes less: a part's MMA reads 8 KB of its 128 weight rows whatever its tokens are,
-// so a quarter costs 0.6 of a tile, not 0.25.
+// Tiles that do not fill a last round of all pairs are cut into parts of 128 or 64 tokens, so that
+// the round takes less: a part's MMA reads 8 KB of its 128 weight rows whatever its tokens are, so a
+// quarter costs 0.6 of a tile, not 0.25.
 // ---------------------------------------------------------------------------------------
+template <int BN_>
 struct PairCfg {
-    static constexpr int BN = 256, STAGES = 6;
-    static constexpr int B_BYTES = BN / 2 * ROW_BYTES, SB_BYTES = 2 * SC_BYTES;
+    static constexpr int BN = BN_, ACCS = BN < 256 ? 2 : 1, STAGES = BN < 256 ? 7 : 6;
+    static constexpr int NSB = 2;                            // scale tiles that BN tokens touch
+    static constexpr int B_BYTES = BN / 2 * ROW_BYTES, SB_BYTES = NSB * SC_BYTES;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
     static constexpr int OFF_SB = OFF_SA + STAGES * SC_BYTES;
     static constexpr int OFF_BAR = OFF_SB + STAGES * SB_BYTES;
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 3) * 8;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr int EPI_WARPS = 8, THREADS = (EPI_WARPS + 2) * 32;
-    static constexpr int COL_SC = BN, SC_COLS = 24, TMEM_COLS = 512;
+    static constexpr int COL_SC = ACCS * BN, SC_COLS = 8 + 8 * NSB, TMEM_COLS = 512;
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(2 * BM >> 4) << 24);  // without N
-    static_assert(SMEM_BYTES <= SMEM_MAX, "capacity");
+    static_assert(SMEM_BYTES <= SMEM_MAX && COL_SC + 2 * SC_COLS <= TMEM_COLS && B_BYTES % 1024 == 0, "capacity");
+    // A tile's or part's first column of scales must be even (an MMA cannot start at an odd one), and
+    // its scales within two 128-row tiles.
+    static_assert(BN % 64 == 0 && (BN == 192 || BN == 256), "whole pairs of scale columns");
 };
 
 __device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint64_t sdesc)
@@ -653,39 +660,39 @@ struct PairWork {
     int steps;        // k / BK
     int token_tiles;
     int whole;        // tiles that stay whole: a multiple of the pairs, or all
-    int shift;        // the others are cut into 1 << shift parts
+    int parts;        // the others are cut into so many
     int units;
     int first_wait;   // as Work's
 };
 
 struct PairUnit {
-    int row, tok, tokens;     // row tile of 256, first token, tokens (256 >> shift)
+    int row, tok, tokens;     // row tile of 256, first token, tokens
 };
+template <int BN>
 __device__ __forceinline__ PairUnit pair_unit(const PairWork &wk, int u)
 {
     const bool cut = u >= wk.whole;
-    const int shift = cut ? wk.shift : 0, part = u - wk.whole;
-    const int tile = cut ? wk.whole + (part >> shift) : u;
+    const int part = u - wk.whole, above = cut ? part / wk.parts : 0;
+    const int tile = cut ? wk.whole + above : u;
     PairUnit r;
     r.row = tile / wk.token_tiles;
-    r.tokens = PairCfg::BN >> shift;
-    r.tok = (tile - r.row * wk.token_tiles) * PairCfg::BN + (cut ? part & ((1 << shift) - 1) : 0) * r.tokens;
+    r.tokens = cut ? BN / wk.parts : BN;
+    r.tok = (tile - r.row * wk.token_tiles) * BN + (cut ? part - above * wk.parts : 0) * r.tokens;
     return r;
 }
 
 // tm_xp: the tokens of a part (its box has fewer rows than tm_x's).
-template <typename T>
-__global__ void __launch_bounds__(PairCfg::THREADS, 1)
+template <typename C, typename T>
+__global__ void __launch_bounds__(C::THREADS, 1)
     gemm_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                            const __grid_constant__ CUtensorMap tm_xp, const __grid_constant__ CUtensorMap tm_ws,
                            const __grid_constant__ CUtensorMap tm_xs, T *__restrict__ y, PairWork wk, int *status)
 {
-    using C = PairCfg;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = C::STAGES, ACCS = C::ACCS, NSB = C::NSB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);        // used in the first CTA
-    uint64_t *empty = full + STAGES, *acc_full = empty + STAGES, *acc_empty = acc_full + 1, *drained = acc_empty + 1;
+    uint64_t *empty = full + STAGES, *acc_full = empty + STAGES, *acc_empty = acc_full + ACCS, *drained = acc_empty + ACCS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
@@ -695,8 +702,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 2 * C::EPI_WARPS);
+        for (int s = 0; s < ACCS; ++s) { mbar_init(&acc_full[s], 1); mbar_init(&acc_empty[s], 2 * C::EPI_WARPS); }
         mbar_init(drained, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -725,10 +731,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         uint32_t bytes;                                                 // both CTAs' of a stage
         const CUtensorMap *map_x;
         auto enter = [&](int u) {
-            const PairUnit unit = pair_unit(wk, u);
+            const PairUnit unit = pair_unit<C::BN>(wk, u);
             row_tile = 2 * unit.row + (int)rank;                        // this CTA's 128 rows
             tok = unit.tok + (int)rank * (unit.tokens / 2);             // and its half of the tokens
-            scale_row = unit.tok / C::BN * 2;
+            scale_row = unit.tok / MX_TILE_ROWS;
             map_x = u < wk.whole ? &tm_x : &tm_xp;
             bytes = 2 * (A_BYTES + SC_BYTES + C::SB_BYTES) + (uint32_t)unit.tokens * ROW_BYTES;
         };
@@ -794,20 +800,20 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                 for (int g = 0; g < 2; ++g) {
                     pair_copy_scales(sa + 4 * g, sadesc0 + (uint64_t)((st * SC_BYTES + g * MX_TILE_BYTES) >> 4));
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        pair_copy_scales(sb + 8 * g + 4 * b,
+                    for (int b = 0; b < NSB; ++b)
+                        pair_copy_scales(sb + 4 * (NSB * g + b),
                                          sbdesc0 + (uint64_t)((st * C::SB_BYTES + b * SC_BYTES + g * MX_TILE_BYTES) >> 4));
                 }
             };
             uint32_t idesc = 0, sb_shift = 0;      // of the unit: N; its first token's column of scales
-            auto multiply = [&](int slot, int st, bool first) {
+            auto multiply = [&](int slot, int st, uint32_t d_tmem, bool first) {
                 const uint32_t sa = tmem + C::COL_SC + slot * C::SC_COLS, sb = sa + 8 + sb_shift;
                 const uint64_t ad = adesc0 + (uint64_t)(st * (A_BYTES >> 4));
                 const uint64_t bd = bdesc0 + (uint64_t)(st * (C::B_BYTES >> 4));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t id = idesc | ((uint32_t)(2 * (j & 1)) << 4) | ((uint32_t)(2 * (j & 1)) << 29);
-                    pair_mma(tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 8 * (j >> 1), !first || j > 0);
+                    pair_mma(d_tmem, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * NSB * (j >> 1), !first || j > 0);
                 }
                 pair_commit(&empty[st]);
             };
@@ -815,10 +821,11 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int u = pair; ok && u < wk.units; u += pairs, ++i) {
-                const PairUnit unit = pair_unit(wk, u);
+                const PairUnit unit = pair_unit<C::BN>(wk, u);
                 idesc = C::IDESC | ((uint32_t)(unit.tokens >> 3) << 17);
-                sb_shift = (uint32_t)(unit.tok % C::BN / 32);
-                ok = __all_sync(0xffffffffu, wait_or_abort(acc_empty, (i & 1) ^ 1, status, abort_flag));
+                sb_shift = (uint32_t)(unit.tok % MX_TILE_ROWS / 32);
+                const int acc = i % ACCS;
+                ok = __all_sync(0xffffffffu, wait_or_abort(&acc_empty[acc], (i / ACCS & 1) ^ 1, status, abort_flag));
                 if (!ok) break;
                 for (int ks = 0; ks < wk.steps;) {
                     ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], phase, status, abort_flag));
@@ -830,9 +837,9 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     if (elect_one()) {
                         copy_scales(0, st);
                         if (two) copy_scales(1, st1);
-                        multiply(0, st, ks == 0);
-                        if (two) multiply(1, st1, false);
-                        if (ks + (two ? 2 : 1) == wk.steps) pair_commit(acc_full);
+                        multiply(0, st, tmem + acc * C::BN, ks == 0);
+                        if (two) multiply(1, st1, tmem + acc * C::BN, false);
+                        if (ks + (two ? 2 : 1) == wk.steps) pair_commit(&acc_full[acc]);
                     }
                     for (int n = two ? 2 : 1; n; --n, ++ks)
                         if (++st == STAGES) {
@@ -852,33 +859,32 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         const int quarter = warp & 3, half = warp >> 2;                  // 32 lanes, half of the columns
         int i = 0;
         for (int u = pair; u < wk.units; u += pairs, ++i) {
-            const PairUnit unit = pair_unit(wk, u);
+            const PairUnit unit = pair_unit<C::BN>(wk, u);
             const int64_t r = (int64_t)(2 * unit.row + (int)rank) * BM + 32 * quarter + lane;
             const int per = unit.tokens / 2, tok0 = unit.tok + half * per;
             const int cols = min(per, wk.m - tok0);
-            if (!__all_sync(0xffffffffu, wait_or_abort(acc_full, i & 1, status, abort_flag))) break;
+            const int acc = i % ACCS;
+            if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[acc], i / ACCS & 1, status, abort_flag))) break;
             tc_fence_after();
-            uint32_t v[4][32];
+            constexpr int HALF = C::BN / 2, NQ = HALF / 32;
+            uint32_t v[NQ][32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (32 * q < per) tc_ld_x32(tmem + ((uint32_t)(32 * quarter) << 16) + half * per + 32 * q, v[q]);
+            for (int q = 0; q < NQ; ++q)
+                if (32 * q < per)
+                    tc_ld_x32(tmem + ((uint32_t)(32 * quarter) << 16) + acc * C::BN + half * per + 32 * q, v[q]);
             tc_wait_ld(v);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) cluster_arrive(cluster_addr(smem_u32(acc_empty), 0));
+            if (lane == 0) cluster_arrive(cluster_addr(smem_u32(&acc_empty[acc]), 0));
             if (r < wk.n) {
                 T *dst = y + (int64_t)tok0 * wk.n + r;
-                if (cols == C::BN / 2) {
+                if (cols == HALF) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c, dst += wk.n) *dst = from_f32<T>(__uint_as_float(v[q][c]));
+                    for (int c = 0; c < HALF; ++c, dst += wk.n) *dst = from_f32<T>(__uint_as_float(v[c / 32][c % 32]));
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c, dst += wk.n)
-                            if (32 * q + c < cols) *dst = from_f32<T>(__uint_as_float(v[q][c]));
+                    for (int c = 0; c < HALF; ++c, dst += wk.n)
+                        if (c < cols) *dst = from_f32<T>(__uint_as_float(v[c / 32][c % 32]));
                 }
             }
         }
@@ -893,31 +899,32 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     }
 }
 
-// Into how many parts (1 << shift) the tiles of a last round that leaves pairs idle are cut: as many
-// as the pairs can take at once, at most 4 (64 tokens).
-int pair_shift(int64_t tiles, int64_t pairs)
+// Into how many parts the tiles of a last round that leaves pairs idle are cut: as many as the pairs
+// can take at once, down to 64 tokens (whole pairs of scale columns).
+int pair_parts(int bn, int64_t tiles, int64_t pairs)
 {
     const int64_t left = tiles % pairs;
-    return left * 4 <= pairs ? 2 : left * 2 <= pairs ? 1 : 0;
+    if (bn == 192) return left * 3 <= pairs ? 3 : 1;
+    return left * 4 <= pairs ? 4 : left * 2 <= pairs ? 2 : 1;
 }
 
-template <typename T>
+template <typename C, typename T>
 cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const uint8_t *x,
                          const uint8_t *xsc, T *y, int64_t m, int64_t n, int64_t k, bool pdl, cudaStream_t stream)
 {
-    cudaError_t e = set_kernel_smem<gemm_mxfp4_pair_kernel<T>>(dev.device, PairCfg::SMEM_BYTES);
+    cudaError_t e = set_kernel_smem<gemm_mxfp4_pair_kernel<C, T>>(dev.device, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + PairCfg::BN - 1) / PairCfg::BN);
+    const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + C::BN - 1) / C::BN);
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     const int64_t at_once = dev.num_sms / 2;
     PairWork wk{};
     wk.m = (int)m;
     wk.n = (int)n;
     wk.steps = (int)(k / BK);
-    wk.token_tiles = (int)((m + PairCfg::BN - 1) / PairCfg::BN);
-    wk.shift = pair_shift(tiles, at_once);
-    wk.whole = (int)(wk.shift ? tiles / at_once * at_once : tiles);
-    wk.units = wk.whole + ((int)tiles - wk.whole) * (1 << wk.shift);
+    wk.token_tiles = (int)((m + C::BN - 1) / C::BN);
+    wk.parts = pair_parts(C::BN, tiles, at_once);
+    wk.whole = (int)(wk.parts > 1 ? tiles / at_once * at_once : tiles);
+    wk.units = wk.whole + ((int)tiles - wk.whole) * wk.parts;
     wk.first_wait = pdl ? 0 : 1;
     const int64_t pairs = wk.units < at_once ? wk.units : at_once;
     const uint64_t sc_row = (uint64_t)k / MX_TILE_K * MX_TILE_BYTES;      // bytes of 128 rows' scales
@@ -925,18 +932,18 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     if (!encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)k / 2, (uint64_t)n, (uint64_t)k / 2, ROW_BYTES, BM,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
-                   PairCfg::BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                   C::BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tm_xp, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)k / 2, (uint64_t)m, (uint64_t)k / 2, ROW_BYTES,
-                   (PairCfg::BN / 2) >> wk.shift, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                   C::BN / 2 / wk.parts, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tm_ws, CU_TENSOR_MAP_DATA_TYPE_UINT64, wsc, sc_row / 8, (uint64_t)(n + 127) / 128, sc_row,
                    SC_BYTES / 8, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !encode_2d(&tm_xs, CU_TENSOR_MAP_DATA_TYPE_UINT64, xsc, sc_row / 8, (uint64_t)(m + 127) / 128, sc_row,
-                   SC_BYTES / 8, 2, CU_TENSOR_MAP_SWIZZLE_NONE))
+                   SC_BYTES / 8, C::NSB, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(PairCfg::THREADS);
-    cfg.dynamicSmemBytes = PairCfg::SMEM_BYTES;
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -946,7 +953,7 @@ cudaError_t launch_pairs(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<T>, tm_w, tm_x, tm_xp, tm_ws, tm_xs, y, wk, dev.status);
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<C, T>, tm_w, tm_x, tm_xp, tm_ws, tm_xs, y, wk, dev.status);
 }
 
 }  // namespace
@@ -955,31 +962,38 @@ namespace {
 
 // The tile shape of a product and how many CTAs share a tile's k: the least of
 //   rounds * (steps of a CTA * time of a step + the tile's start and end + joining its partial sums)
-// over the tile widths, the powers of two up to 8 that leave each CTA a step, and pairs (a last
-// round of cut tiles with its own times).  The times, in ns, are fitted to every such choice measured
-// at 741 sizes (m from 1 to 1000, n from 1000 to 64448, k from 512 to 20480, weights from HBM):
-// what the formula takes is 0.6 % above the best choice on average, 21 % at worst (256 x 4096 x 4096:
-// 6.7 us in 64-token tiles, 8.2 in 128-token ones, 10.8 if two share those, 8.3 by pairs; 1 x 2500 x
-// 20480: 11.7 shared by four, 21.2 not shared).
+// over the tile widths, the powers of two up to 8 that leave each CTA a step, and pairs (whose round
+// takes no less than their epilogue's stores, and whose last round of cut tiles has its own times).
+// The times, in ns, are fitted to every such choice measured at some 1000 sizes (m from 1 to 4095, n
+// from 1000 to 64448, k from 512 to 20480, weights from HBM): what the formula takes is 0.4 % above the
+// best choice on average, 21 % at worst (256 x 4096 x 4096: 6.7 us in 64-token tiles, 8.2 in 128-token
+// ones, 10.8 if two share those, 8.3 by pairs; 1 x 2500 x 20480: 11.7 shared by four, 21.2 not shared;
+// 4095 x 12288 x 4096: 63 by pairs with 192 tokens, 74 with 256, 80 in 192-token tiles of one CTA).
 struct Plan {
-    int bn, CL;       // bn = 256: pairs
+    int bn, CL;       // CL = 0: pairs
 };
 
 Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
     static const struct { int bn, step, ends; } shapes[] = {
-        {16, 240, 200}, {32, 230, 200}, {64, 210, 380}, {128, 290, 590}, {192, 310, 1110}};
-    static const struct { int step, ends; } parts[] = {{290, 2370}, {230, 2260}, {240, 2060}};   // by pair_shift
+        {16, 220, 100}, {32, 220, 200}, {64, 210, 360}, {128, 290, 590}, {192, 350, 950}};
+    static const struct { int bn, step, ends, least, start, part_step, part_ends; } pairs[] = {
+        {192, 235, 455, 2745, 1180, 210, 1130}, {256, 275, 2600, 3100, 100, 225, 2250}};
     static const int join_start = 940, join_column[] = {0, 25, 27, 21};                          // CL = 1, 2, 4, 8
-    Plan best{256, 1};
+    Plan best{256, 0};
     int64_t least = INT64_MAX;
-    if (m > 64) {
-        const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + 255) / 256), at_once = dev.num_sms / 2;
-        least = tiles / at_once * (steps * parts[0].step + parts[0].ends);
-        if (tiles % at_once) {
-            const auto &last = parts[pair_shift(tiles, at_once)];
-            least += steps * last.step + last.ends;
+    for (const auto &s : pairs) {
+        if (m <= 64) break;
+        const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + s.bn - 1) / s.bn), at_once = dev.num_sms / 2;
+        const bool cut = pair_parts(s.bn, tiles, at_once) > 1;
+        const int64_t whole = cut ? tiles / at_once : (tiles + at_once - 1) / at_once;
+        const int64_t round = steps * s.step + s.ends;
+        const int64_t cost = s.start + whole * (round > s.least ? round : s.least) +
+                             (cut && tiles % at_once ? steps * s.part_step + s.part_ends : 0);
+        if (cost < least) {
+            least = cost;
+            best = {s.bn, 0};
         }
     }
     for (const auto &s : shapes) {
@@ -1009,7 +1023,7 @@ constexpr int OWN_TASKS = 32;       // token-steps that four warps quantize in l
 bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 {
     const Plan p = plan_tiles(dev, m, n, k);
-    if (p.bn != 16) return false;
+    if (p.bn != 16) return false;                  // never pairs
     const int64_t steps = (k / BK + p.CL - 1) / p.CL;
     return steps <= OWN_STEPS && m * steps <= OWN_TASKS;
 }
@@ -1039,12 +1053,15 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
         auto go = [&](auto cfg) {
             return launch_tiles<decltype(cfg), T, float>(dev, w, wsc, x, xsc, nullptr, 0, out, m, n, k, p.CL, pdl, stream);
         };
+        auto pairs = [&](auto cfg) {
+            return launch_pairs<decltype(cfg), T>(dev, w, wsc, x, xsc, out, m, n, k, pdl, stream);
+        };
+        if (p.CL == 0) return p.bn == 192 ? pairs(PairCfg<192>{}) : pairs(PairCfg<256>{});
         if (p.bn == 16) return go(Cfg<16, 9>{});
         if (p.bn == 32) return go(Cfg<32, 8>{});
         if (p.bn == 64) return go(Cfg<64, 6>{});
         if (p.bn == 128) return go(Cfg<128, 4>{});
-        if (p.bn == 192) return go(Cfg<192, 5>{});
-        return launch_pairs<T>(dev, w, wsc, x, xsc, out, m, n, k, pdl, stream);
+        return go(Cfg<192, 5>{});
     });
 }
 

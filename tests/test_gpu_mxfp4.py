@@ -157,13 +157,26 @@ def test_product_matches_64_bits(m, n, k, kind):
 @pytest.mark.parametrize("m,n,k", [(512, 20480, 512), (300, 20300, 256), (1100, 20480, 256), (257, 40000, 256),
                                    (200, 64448, 512), (1000, 19457, 256)])
 def test_product_last_round(m, n, k):
-    """Tiles that do not fill a last round of all SMs, cut into two, into four, or whole; ragged in both."""
+    """Tiles that do not fill a last round of all SMs; ragged in both."""
     ensure_built()
     wc, wb, wp, wt = matrix(n, k, 30 + n, 100, 124)
     xc, xb, xp, xt = matrix(m, k, 40 + m, 124, 130)
     y = q8.gemm_mxfp4_preq(cuda(wp), cuda(wt), cuda(xp), cuda(xt), dtype=torch.bfloat16)
     device_ok()
     check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), "bf16")
+
+
+@pytest.mark.parametrize("m,n,k", [(130, 9817, 2304), (265, 19451, 1792), (258, 20503, 1536), (70, 20355, 2816),
+                                   (202, 9839, 1280), (791, 9628, 1280), (395, 13026, 2304), (193, 19483, 2304)])
+def test_product_of_many_tiles(m, n, k):
+    """Sizes that fill the GPU with wide tiles, k long enough for them to pay: one round and several,
+    left-over tiles whole and cut, last tiles with few tokens and rows."""
+    ensure_built()
+    wc, wb, wp, wt = matrix(n, k, 50 + n, 100, 124)
+    xc, xb, xp, xt = matrix(m, k, 60 + m, 124, 130)
+    y = q8.gemm_mxfp4_preq(cuda(wp), cuda(wt), cuda(xp), cuda(xt), dtype=torch.float32)
+    device_ok()
+    check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), "f32")
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
