@@ -253,9 +253,13 @@ def _rows(t, what: str) -> int:
     """Row stride in elements of a [rows, columns] CUDA tensor whose columns are adjacent."""
     if not t.is_cuda:
         raise Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not a CUDA tensor")
-    if t.dim() != 2 or t.shape[0] < 1 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: one row at least, with adjacent columns")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    shape = t.shape
+    if len(shape) == 2 and shape[0] > 0:
+        if t.is_contiguous():
+            return shape[1]
+        if t.stride(1) == 1 or shape[1] <= 1:
+            return t.stride(0)
+    raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: one row at least, with adjacent columns")
 
 
 def _given(t, shape, dtype, what: str):
