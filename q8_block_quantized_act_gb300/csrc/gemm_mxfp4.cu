@@ -13,7 +13,8 @@
 //               memory as they are stored (tcgen05.cp), then four K = 64 MMAs
 // Two accumulators in tensor memory: a tile's epilogue overlaps the next tile's MMAs.
 //
-// Few output tiles (decode): the CTAs of a cluster split a tile's k among them.  Each sends its
+// Few tokens: narrow stages, so two CTAs fit an SM where there are more row tiles than SMs.
+// Few output tiles: the CTAs of a cluster split a tile's k among them.  Each sends its
 // partial sums to the cluster's shared memories (rank c owns BN / CL of the tile's columns), and
 // the owner adds them in rank order, so the result does not depend on timing.
 //
@@ -40,15 +41,17 @@ constexpr int SMEM_MAX = 232448;
 
 // XSTEPS > 0: the CTA quantizes the activation itself and keeps its part of k (at most XSTEPS steps)
 // in shared memory for all of its tiles; the stages then hold weights alone.
-template <int BN_, int STAGES_, int XSTEPS_ = 0>
+// PER_SM = 2: two CTAs to an SM, which do not share tiles.
+template <int BN_, int STAGES_, int XSTEPS_ = 0, int PER_SM_ = 1>
 struct Cfg {
+    static constexpr int PER_SM = PER_SM_;
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
     static constexpr int XSTEPS = XSTEPS_;
     static constexpr int XSLOTS = XSTEPS > 0 ? XSTEPS : STAGES;
     static constexpr int NSB = BN > 128 ? 2 : 1;             // scale tiles that BN tokens touch
     static constexpr int B_BYTES = BN * ROW_BYTES;
-    static constexpr bool SPLIT = BN <= 128;                 // room for the cluster's partial sums
+    static constexpr bool SPLIT = BN <= 128 && PER_SM == 1;  // room for the cluster's partial sums
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_SA = OFF_B + XSLOTS * B_BYTES;
@@ -63,7 +66,7 @@ struct Cfg {
     static constexpr int COL_SC = 2 * BN;
     static constexpr int NEED = COL_SC + 2 * SC_COLS;
     static constexpr int TMEM_COLS = NEED <= 64 ? 64 : NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
-    static_assert(NEED <= 512 && SMEM_BYTES <= SMEM_MAX, "capacity");
+    static_assert(TMEM_COLS * PER_SM <= 512 && (SMEM_BYTES + 1024) * PER_SM <= SMEM_MAX + 1024, "capacity");
     // Instruction descriptor, block-scaled: B scale byte pair (bits 4-5), A and B e2m1 (bits 7-9,
     // 10-11 = 1), N >> 3 (17-22), scales e8m0 (23), M >> 4 (24-28), A scale byte pair (29-30).
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
@@ -192,7 +195,7 @@ struct Work {
 
 // X: the activation's type where the CTA quantizes it (xf, rows ldx elements apart), else unused.
 template <typename C, typename T, typename X>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, C::PER_SM)
     gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const uint8_t *__restrict__ wsc, const uint8_t *__restrict__ xsc, const X *__restrict__ xf,
                       int64_t ldx, T *__restrict__ y, Work wk, int CL, int *status)
@@ -513,7 +516,7 @@ cudaError_t resident_clusters(const DeviceInfo &dev, int CL, int *count)
     const int slot = CL == 1 ? 0 : CL == 2 ? 1 : CL == 4 ? 2 : 3;
     const bool cache = dev.device >= 0 && dev.device < kAttrDevices;
     if (CL == 1) {
-        *count = dev.num_sms;
+        *count = dev.num_sms * C::PER_SM;
         return cudaSuccess;
     }
     if (cache && (*count = known[dev.device][slot].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
@@ -971,11 +974,16 @@ namespace {
 // 4095 x 12288 x 4096: 63 by pairs with 192 tokens, 74 with 256, 80 in 192-token tiles of one CTA).
 struct Plan {
     int bn, CL;       // CL = 0: pairs
+    int per_sm = 1;   // CTAs to an SM
 };
 
 Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
+    // One token tile and more row tiles than SMs: two CTAs to an SM, so that the last tiles are read
+    // beside others and not at the end by a few SMs (1, 8, 32 x 20480 x 4096: 160 tiles, 10.0, 9.9, 10.4 us;
+    // 12.3, 12.6, 13.0 by one CTA to an SM; 8 x 64448 x 4096 25.0 and 27.0).
+    if (m <= 64 && rows > dev.num_sms) return {m <= 16 ? 16 : m <= 32 ? 32 : 64, 1, 2};
     static const struct { int bn, step, ends; } shapes[] = {
         {16, 220, 100}, {32, 220, 200}, {64, 210, 360}, {128, 290, 590}, {192, 350, 950}};
     static const struct { int bn, step, ends, least, start, part_step, part_ends; } pairs[] = {
@@ -1017,6 +1025,7 @@ Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
 
 constexpr int OWN_STEPS = 16;       // steps of the activation that a CTA keeps
 constexpr int OWN_TASKS = 32;       // token-steps that four warps quantize in less than a launch's time
+constexpr int OWN_TASKS_LONG = 12;  // the same where two CTAs to an SM could take the quantizer's output
 
 }  // namespace
 
@@ -1025,7 +1034,7 @@ bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k
     const Plan p = plan_tiles(dev, m, n, k);
     if (p.bn != 16) return false;                  // never pairs
     const int64_t steps = (k / BK + p.CL - 1) / p.CL;
-    return steps <= OWN_STEPS && m * steps <= OWN_TASKS;
+    return steps <= OWN_STEPS && m * steps <= (p.per_sm == 2 ? OWN_TASKS_LONG : OWN_TASKS);
 }
 
 cudaError_t launch_gemm_mxfp4_own(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const void *xf, int64_t ldx,
@@ -1057,6 +1066,8 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
             return launch_pairs<decltype(cfg), T>(dev, w, wsc, x, xsc, out, m, n, k, pdl, stream);
         };
         if (p.CL == 0) return p.bn == 192 ? pairs(PairCfg<192>{}) : pairs(PairCfg<256>{});
+        if (p.per_sm == 2)
+            return p.bn == 16 ? go(Cfg<16, 5, 0, 2>{}) : p.bn == 32 ? go(Cfg<32, 5, 0, 2>{}) : go(Cfg<64, 4, 0, 2>{});
         if (p.bn == 16) return go(Cfg<16, 9>{});
         if (p.bn == 32) return go(Cfg<32, 8>{});
         if (p.bn == 64) return go(Cfg<64, 6>{});

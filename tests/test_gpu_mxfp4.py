@@ -166,6 +166,23 @@ def test_product_last_round(m, n, k):
     check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), "bf16")
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 20480, 1024), (1, 20481, 4096), (7, 40000, 512), (16, 20353, 2304), (17, 20480, 768),
+                                   (32, 45000, 256), (33, 20353, 1280), (64, 20480, 4096)])
+def test_product_few_tokens_many_rows(m, n, k):
+    """More row tiles than SMs, through both calls."""
+    ensure_built()
+    wc, wb, wp, wt = matrix(n, k, 70 + n, 100, 124)
+    xc, xb, xp, xt = matrix(m, k, 80 + m, 124, 130)
+    y = q8.gemm_mxfp4_preq(cuda(wp), cuda(wt), cuda(xp), cuda(xt), dtype=torch.float32)
+    device_ok()
+    check_product(y, ref.mxfp4_values(wb, wc), ref.mxfp4_values(xb, xc), "f32")
+    x = values(m, k, 90 + m, "bf16").cuda()
+    fused = q8.gemm_mxfp4(cuda(wp), cuda(wt), x)
+    apart = q8.gemm_mxfp4_preq(cuda(wp), cuda(wt), *q8.quantize_mxfp4(x))
+    device_ok()
+    assert torch.equal(fused, apart)
+
+
 @pytest.mark.parametrize("m,n,k", [(130, 9817, 2304), (265, 19451, 1792), (258, 20503, 1536), (70, 20355, 2816),
                                    (202, 9839, 1280), (791, 9628, 1280), (395, 13026, 2304), (193, 19483, 2304)])
 def test_product_of_many_tiles(m, n, k):
