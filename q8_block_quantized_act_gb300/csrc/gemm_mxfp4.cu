@@ -18,9 +18,10 @@
 // partial sums to the cluster's shared memories (rank c owns BN / CL of the tile's columns), and
 // the owner adds them in rank order, so the result does not depend on timing.
 //
-// What bounds it: the weight stream for few tokens (5 x 64448 x 4096: 26 us for 142 MB with the
-// activation's quantization; 1 x 4096 x 4096, 32 tiles shared by four CTAs each: 5.0 us, latency), the
-// MMAs for many (pairs of CTAs, below: 4095 x 20480 x 8192 in 207 us, 6.6 PFLOP/s with its quantizer).
+// What bounds it: the weight stream for few tokens (5 x 64448 x 4096: 24.4 us for 142 MB with the
+// activation's quantization, 0.86 of the copy rate; 1 x 4096 x 4096, 32 tiles shared by four CTAs each:
+// 5.0 us, latency), the MMAs for many (pairs of CTAs, below: 4095 x 20480 x 8192 in 206 us, 6.7 PFLOP/s
+// with its quantizer).
 // No rounding between the codes and y: products of codes and scales are exact, sums are the tensor
 // cores' f32, y is rounded once.
 #include "launch.h"
