@@ -231,11 +231,13 @@ def gemv_kq(fmt: str, w, xq, xd, n: int, out=None):
 # call) and the addresses go straight to the C ABI.
 _TYPES: dict = {}
 _torch = None
+_current = None      # the current CUDA device's index, as a call
 
 
 def _load_torch():
-    global _torch
+    global _torch, _current
     import torch
+    _current = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2   # no tensor's
     _TYPES.update({torch.float32: Q8ACT_F32, torch.float16: Q8ACT_F16, torch.bfloat16: Q8ACT_BF16})
     _torch = torch
     return torch
@@ -249,10 +251,17 @@ def _type(t, what: str) -> int:
     return code
 
 
-def _rows(t, what: str) -> int:
-    """Row stride in elements of a [rows, columns] CUDA tensor whose columns are adjacent."""
-    if not t.is_cuda:
-        raise Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not a CUDA tensor")
+def _elsewhere(t, what: str, dev: int):
+    """The kernels run on the current device and its current stream: a tensor of another GPU would be a
+    foreign address there, unordered with the work that made it."""
+    return Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not on the current CUDA device (cuda:{dev})" if t.is_cuda
+                      else f"{what}: not a CUDA tensor")
+
+
+def _rows(t, what: str, dev: int) -> int:
+    """Row stride in elements of a [rows, columns] tensor on device dev whose columns are adjacent."""
+    if t.get_device() != dev:
+        raise _elsewhere(t, what, dev)
     shape = t.shape
     if len(shape) == 2 and shape[0] > 0:
         if t.is_contiguous():
@@ -262,12 +271,12 @@ def _rows(t, what: str) -> int:
     raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: one row at least, with adjacent columns")
 
 
-def _given(t, shape, dtype, what: str):
-    """The address of a caller's buffer: the kernels write or read exactly `shape`."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _given(t, shape, dtype, what: str, dev: int):
+    """The address of a caller's buffer on device dev: the kernels write or read exactly `shape`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    if not t.is_cuda:
-        raise Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not a CUDA tensor")
+    if t.get_device() != dev:
+        raise _elsewhere(t, what, dev)
     if t.dtype is not dtype:
         raise Q8ActError(Q8ACT_ERR_TYPE, f"{what}: {t.dtype}")
     raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: contiguous {tuple(shape)}")
@@ -275,23 +284,24 @@ def _given(t, shape, dtype, what: str):
 
 def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out, quants=True):
     torch = _torch or _load_torch()
-    ldx, code = _rows(x, "x"), _type(x, "x")
+    dev = _current()
+    ldx, code = _rows(x, "x", dev), _type(x, "x")
     m, k = shape = x.shape
     dtype = x.dtype
     pr = pro = pw = py = None
     ldr = ldro = wtype = 0
     if residual is not None:
-        ldr, pr = _rows(residual, "residual"), residual.data_ptr()
+        ldr, pr = _rows(residual, "residual", dev), residual.data_ptr()
         if residual.dtype is not dtype or residual.shape != shape:
             raise Q8ActError(Q8ACT_ERR_TYPE, "residual: x's type and shape")
     if residual_out is not None:
-        ldro, pro = _rows(residual_out, "residual_out"), residual_out.data_ptr()
+        ldro, pro = _rows(residual_out, "residual_out", dev), residual_out.data_ptr()
         if residual_out.dtype is not dtype or residual_out.shape != shape:
             raise Q8ActError(Q8ACT_ERR_TYPE, "residual_out: x's type and shape")
     if weight is not None:
-        wtype, pw = _type(weight, "weight"), _given(weight, (k,), weight.dtype, "weight")
+        wtype, pw = _type(weight, "weight"), _given(weight, (k,), weight.dtype, "weight", dev)
     if y is not None:
-        py = _given(y, shape, dtype, "y")
+        py = _given(y, shape, dtype, "y", dev)
     qtype, dshape = (torch.uint16, (k // QK, (m + 3) // 4 * 4)) if mmq else (torch.int8, (m, k // QK))
     if not quants:
         q = d = pq = pd = None
@@ -300,7 +310,7 @@ def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out, quants=True):
             out = (torch.empty(shape, dtype=qtype, device=x.device),
                    torch.empty(dshape, dtype=torch.float32, device=x.device))
         q, d = out
-        pq, pd = _given(q, shape, qtype, "quants"), _given(d, dshape, torch.float32, "scales")
+        pq, pd = _given(q, shape, qtype, "quants", dev), _given(d, dshape, torch.float32, "scales", dev)
     L = lib()
     fn = L.q8act_rmsnorm_q8_1_mmq if mmq else L.q8act_rmsnorm_q8_1
     rc = fn(x.data_ptr(), ldx, pr, ldr, pw, wtype, eps, pro, ldro, py, pq, pd, m, k, code, _s(None))
@@ -327,7 +337,8 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None,
     """The norm alone: y in x's type (what rmsnorm_q8_1 gives as y), for a consumer that is not
     quantized to q8_1, such as an MXFP4 product."""
     torch = _torch or _load_torch()
-    _rows(x, "x")
+    dev = _current()
+    _rows(x, "x", dev)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _rmsnorm(False, x, weight, eps, residual, residual_out, y, None, quants=False)
     return y
@@ -343,14 +354,15 @@ def _mxfp4_scales(rows: int, k: int):
 def quantize_mxfp4(x, out=None):
     """float32, float16 or bfloat16 [m, k] -> MXFP4 (codes uint8 [m, k/2], tiled scales uint8)."""
     torch = _torch or _load_torch()
-    ldx, code = _rows(x, "x"), _type(x, "x")
+    dev = _current()
+    ldx, code = _rows(x, "x", dev), _type(x, "x")
     m, k = x.shape
     u8, nsc = torch.uint8, _mxfp4_scales(m, k)
     if out is None:
         out = (torch.empty((m, k // 2), dtype=u8, device=x.device), torch.empty(nsc, dtype=u8, device=x.device))
     codes, scales = out
-    rc = lib().q8act_quantize_mxfp4(x.data_ptr(), ldx, code, _given(codes, (m, k // 2), u8, "codes"),
-                                    _given(scales, nsc, u8, "scales"), m, k, _s(None))
+    rc = lib().q8act_quantize_mxfp4(x.data_ptr(), ldx, code, _given(codes, (m, k // 2), u8, "codes", dev),
+                                    _given(scales, nsc, u8, "scales", dev), m, k, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_quantize_mxfp4")
     return codes, scales
@@ -359,13 +371,14 @@ def quantize_mxfp4(x, out=None):
 def dequant_mxfp4(codes, scales, dtype=None, out=None):
     """MXFP4 (codes, tiled scales) -> values [m, k] in dtype (default float16) or out's type."""
     torch = _torch or _load_torch()
+    dev = _current()
     m, half = codes.shape
     k, u8 = 2 * half, torch.uint8
-    pc, ps = _given(codes, (m, half), u8, "codes"), _given(scales, _mxfp4_scales(m, k), u8, "scales")
+    pc, ps = _given(codes, (m, half), u8, "codes", dev), _given(scales, _mxfp4_scales(m, k), u8, "scales", dev)
     if out is None:
         out = torch.empty((m, k), dtype=dtype or torch.float16, device=codes.device)
     code = _type(out, "out")
-    rc = lib().q8act_dequant_mxfp4(pc, ps, _given(out, (m, k), out.dtype, "out"), code, m, k, _s(None))
+    rc = lib().q8act_dequant_mxfp4(pc, ps, _given(out, (m, k), out.dtype, "out", dev), code, m, k, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_dequant_mxfp4")
     return out
@@ -374,8 +387,9 @@ def dequant_mxfp4(codes, scales, dtype=None, out=None):
 def tile_mxfp4_scales(scales):
     """Row-major e8m0 bytes [m, k/32] -> the tiled scales that the MXFP4 calls take."""
     torch = _torch or _load_torch()
+    dev = _current()
     m, kb = scales.shape
-    ps = _given(scales, (m, kb), torch.uint8, "scales")
+    ps = _given(scales, (m, kb), torch.uint8, "scales", dev)
     tiled = torch.empty(_mxfp4_scales(m, kb * QK), dtype=torch.uint8, device=scales.device)
     rc = lib().q8act_tile_mxfp4_scales(ps, tiled.data_ptr(), m, kb * QK, _s(None))
     if rc:
@@ -396,22 +410,25 @@ def gemm_mxfp4(w, wscales, x, ws=None, dtype=None, out=None):
     """x [m, k] (float32, float16, bfloat16; quantized to MXFP4 in the call) times MXFP4 weights
     (codes w [n, k/2], tiled scales): y [m, n] in dtype (default float32) or out's type."""
     torch = _torch or _load_torch()
+    dev = _current()
     n, half = w.shape
     k, u8 = 2 * half, torch.uint8
-    pw, psc = _given(w, (n, half), u8, "w"), _given(wscales, _mxfp4_scales(n, k), u8, "wscales")
-    ldx, code = _rows(x, "x"), _type(x, "x")
+    pw, psc = _given(w, (n, half), u8, "w", dev), _given(wscales, _mxfp4_scales(n, k), u8, "wscales", dev)
+    ldx, code = _rows(x, "x", dev), _type(x, "x")
     m = x.shape[0]
     if x.shape[1] != k:
         raise Q8ActError(Q8ACT_ERR_DIMS, f"x: {x.shape[1]} columns for weights of {k}")
     if ws is None:
         ws = gemm_mxfp4_workspace(m, k, x.device)
-    elif not (ws.is_cuda and ws.dtype is u8 and ws.is_contiguous()):
-        raise Q8ActError(Q8ACT_ERR_WORKSPACE, "ws: contiguous uint8 on the GPU")
+    elif ws.get_device() != dev:
+        raise _elsewhere(ws, "ws", dev)
+    elif not (ws.dtype is u8 and ws.is_contiguous()):
+        raise Q8ActError(Q8ACT_ERR_WORKSPACE, "ws: contiguous uint8")
     if out is None:
         out = torch.empty((m, n), dtype=dtype or torch.float32, device=x.device)
     ycode = _type(out, "out")
-    rc = lib().q8act_gemm_mxfp4(pw, psc, x.data_ptr(), ldx, code, _given(out, (m, n), out.dtype, "out"), ycode, m, n, k,
-                                ws.data_ptr(), ws.numel(), _s(None))
+    rc = lib().q8act_gemm_mxfp4(pw, psc, x.data_ptr(), ldx, code, _given(out, (m, n), out.dtype, "out", dev), ycode,
+                                m, n, k, ws.data_ptr(), ws.numel(), _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4")
     return out
@@ -420,14 +437,16 @@ def gemm_mxfp4(w, wscales, x, ws=None, dtype=None, out=None):
 def gemm_mxfp4_preq(w, wscales, xq, xscales, dtype=None, out=None):
     """The product on an activation already in MXFP4 (quantize_mxfp4)."""
     torch = _torch or _load_torch()
+    dev = _current()
     n, half = w.shape
     k, u8, m = 2 * half, torch.uint8, xq.shape[0]
-    pw, psc = _given(w, (n, half), u8, "w"), _given(wscales, _mxfp4_scales(n, k), u8, "wscales")
-    px, pxs = _given(xq, (m, half), u8, "xq"), _given(xscales, _mxfp4_scales(m, k), u8, "xscales")
+    pw, psc = _given(w, (n, half), u8, "w", dev), _given(wscales, _mxfp4_scales(n, k), u8, "wscales", dev)
+    px, pxs = _given(xq, (m, half), u8, "xq", dev), _given(xscales, _mxfp4_scales(m, k), u8, "xscales", dev)
     if out is None:
         out = torch.empty((m, n), dtype=dtype or torch.float32, device=xq.device)
     ycode = _type(out, "out")
-    rc = lib().q8act_gemm_mxfp4_preq(pw, psc, px, pxs, _given(out, (m, n), out.dtype, "out"), ycode, m, n, k, _s(None))
+    rc = lib().q8act_gemm_mxfp4_preq(pw, psc, px, pxs, _given(out, (m, n), out.dtype, "out", dev), ycode, m, n, k,
+                                     _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4_preq")
     return out
@@ -439,22 +458,23 @@ def logprobs(logits, tokens=None, top: int = 0, out=None):
     ids (int32 [m, top], equal logits by the lower id, -1 beyond the unmasked ones) with their
     log probabilities.  Returns (logprob or None, entropy, ids, top_logprobs)."""
     torch = _torch or _load_torch()
-    ld, code = _rows(logits, "logits"), _type(logits, "logits")
+    dev = _current()
+    ld, code = _rows(logits, "logits", dev), _type(logits, "logits")
     m, v = logits.shape
     f32, i32 = torch.float32, torch.int32
     ptok = plp = pids = ptlp = None
     if out is None:
-        dev, n = logits.device, max(top, 0)
-        out = (torch.empty(m, dtype=f32, device=dev) if tokens is not None else None,
-               torch.empty(m, dtype=f32, device=dev), torch.empty((m, n), dtype=i32, device=dev),
-               torch.empty((m, n), dtype=f32, device=dev))
+        at, n = logits.device, max(top, 0)
+        out = (torch.empty(m, dtype=f32, device=at) if tokens is not None else None,
+               torch.empty(m, dtype=f32, device=at), torch.empty((m, n), dtype=i32, device=at),
+               torch.empty((m, n), dtype=f32, device=at))
     lp, ent, ids, tlp = out
     if tokens is not None:
-        ptok, plp = _given(tokens, (m,), i32, "tokens"), _given(lp, (m,), f32, "logprob")
+        ptok, plp = _given(tokens, (m,), i32, "tokens", dev), _given(lp, (m,), f32, "logprob", dev)
     if top > 0:
-        pids, ptlp = _given(ids, (m, top), i32, "ids"), _given(tlp, (m, top), f32, "top_logprobs")
-    rc = lib().q8act_logprobs(logits.data_ptr(), ld, code, ptok, plp, _given(ent, (m,), f32, "entropy"), pids, ptlp, m, v,
-                              top, _s(None))
+        pids, ptlp = _given(ids, (m, top), i32, "ids", dev), _given(tlp, (m, top), f32, "top_logprobs", dev)
+    rc = lib().q8act_logprobs(logits.data_ptr(), ld, code, ptok, plp, _given(ent, (m,), f32, "entropy", dev), pids, ptlp,
+                              m, v, top, _s(None))
     if rc:
         raise Q8ActError(rc, "q8act_logprobs")
     return lp, ent, ids, tlp
