@@ -311,6 +311,9 @@ __global__ void __launch_bounds__(THREADS, C::PER_SM)
             mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1, status);
     } else if (warp == 5) {
         // ------------------------------ MMA issuer ------------------------------
+        // Every role waits for the previous kernel first: a pipeline wait's time limit is for this kernel's
+        // own copies and MMAs, not for what is left of that one.
+        griddep_wait();
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_A));
         const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
         const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
@@ -380,10 +383,10 @@ __global__ void __launch_bounds__(THREADS, C::PER_SM)
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
         const int row = 32 * warp + lane;
         float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
+        griddep_wait();
         if constexpr (OWN_X) {
             // First the activation: a warp has 256 values of a token at a time, and writes them as
             // the TMA would have (token rows of 128 bytes, 16-byte units swizzled by the row).
-            griddep_wait();
             const int tasks = wk.m * (ks1 - ks0);
             constexpr int DEPTH = 4;                  // loads under way
             for (int task0 = warp; task0 < tasks; task0 += 4 * DEPTH) {
@@ -794,6 +797,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (warp == C::EPI_WARPS + 1) {
         // ------------------------------ MMA issuer (first CTA) ------------------------------
         if (rank == 0) {
+            griddep_wait();                                             // as in gemm_mxfp4_kernel
             const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_A));
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_B));
             const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + C::OFF_SA));
@@ -860,6 +864,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else {
         // ------------------------------ epilogue ------------------------------
+        griddep_wait();
         const int quarter = warp & 3, half = warp >> 2;                  // 32 lanes, half of the columns
         int i = 0;
         for (int u = pair; u < wk.units; u += pairs, ++i) {
