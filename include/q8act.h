@@ -375,6 +375,7 @@ int q8act_debug_gemv_q5_k_block_dots(const void *w, const int8_t *xq, int32_t *D
  *       0: its quants are 0, as the quantizers give for NaN).
  *   y: NULL, or [m][k] of `type`: the normed values, rounded once.  With y the quants and scales
  *       may be NULL together (the norm alone).
+ *   Up to 16 rows, a row's results do not depend on m.
  *   rmsnorm_q8_1:     xq [m][k] int8, xd [m][k/32] f32 (the GEMVs' activation);
  *   rmsnorm_q8_1_mmq: xqh [m][k] binary16 quants, xdt [k/32][q8act_mmq_ldm(m)] f32 (the GEMM's).
  */
@@ -417,12 +418,22 @@ int q8act_tile_mxfp4_scales(const void *scales, void *tiled, int64_t m, int64_t 
  *     q8act_quantize_mxfp4 does, into ws (q8act_gemm_mxfp4_workspace_bytes(m, k) bytes; 0 for
  *     invalid dimensions), the product being a programmatic dependent of that quantizer;
  *   gemm_mxfp4_preq takes the quantized activation xq, xscales.
+ * Up to 16 tokens the result for a token does not depend on m (the decode == verify law that
+ * q8act_gemv_q8_0 keeps); beyond, the tiles and the split of k follow m, and with them the order of
+ * the f32 sums.  Both calls give the same bits, and the same ones each time.
  */
 size_t q8act_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k);
 int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t ldx, int xtype, void *y, int ytype,
                      int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);
 int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, const void *xscales, void *y, int ytype,
                           int64_t m, int64_t n, int64_t k, void *stream);
+
+/*
+ * Test hook, on the host alone: the tiles that the two calls choose on a GPU of `sms` SMs.  plan
+ * (HOST array): tokens of a tile, CTAs that share a tile's k (0: pairs of CTAs on one tile), CTAs to
+ * an SM, and 1 where gemm_mxfp4's CTAs quantize the activation themselves.
+ */
+int q8act_debug_gemm_mxfp4_plan(int sms, int64_t m, int64_t n, int64_t k, int32_t *plan);
 
 /*
  * What a decoder answers with: for each of m rows of v logits (`type`, rows ld >= v elements
@@ -435,6 +446,8 @@ int q8act_gemm_mxfp4_preq(const void *w, const void *wscales, const void *xq, co
  * Masked logits are -inf: they count nothing and are never an alternative; places of the list
  * beyond the unmasked tokens hold id -1 and -inf.  A row that is masked as a whole has entropy 0
  * and log probabilities -inf.  A row that holds a NaN or +inf has no softmax: NaN, ids -1.
+ * Up to 16 rows, a row's results do not depend on m for rows that start alike modulo 16 bytes (the
+ * f32 sums go by 16-byte vectors); ids never do.
  */
 #define Q8ACT_MAX_TOP 32
 int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *tokens, float *logprob, float *entropy,

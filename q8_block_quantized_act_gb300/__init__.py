@@ -30,7 +30,8 @@ from ._lib import (  # noqa: F401  (re-exported ABI)
     q8act_debug_gemv_q6_k_block_dots, q8act_debug_gemv_q4_k_block_dots, q8act_debug_gemv_q5_k_block_dots,
     Q8ACT_ERR_TYPE, Q8ACT_F32, Q8ACT_F16, Q8ACT_BF16, Q8ACT_MAX_TOP, q8act_rmsnorm_q8_1, q8act_rmsnorm_q8_1_mmq,
     q8act_mxfp4_scale_bytes, q8act_quantize_mxfp4, q8act_dequant_mxfp4, q8act_tile_mxfp4_scales,
-    q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq, q8act_logprobs, _s)
+    q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq,
+    q8act_debug_gemm_mxfp4_plan, q8act_logprobs, _s)
 
 QK = 32
 Q8_0_BYTES = 34

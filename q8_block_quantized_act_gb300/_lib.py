@@ -49,7 +49,8 @@ EXPORTED = (
     "q8act_debug_gemv_q6_k_block_dots", "q8act_debug_gemv_q4_k_block_dots", "q8act_debug_gemv_q5_k_block_dots",
     "q8act_rmsnorm_q8_1", "q8act_rmsnorm_q8_1_mmq",
     "q8act_mxfp4_scale_bytes", "q8act_quantize_mxfp4", "q8act_dequant_mxfp4", "q8act_tile_mxfp4_scales",
-    "q8act_gemm_mxfp4_workspace_bytes", "q8act_gemm_mxfp4", "q8act_gemm_mxfp4_preq", "q8act_logprobs",
+    "q8act_gemm_mxfp4_workspace_bytes", "q8act_gemm_mxfp4", "q8act_gemm_mxfp4_preq",
+    "q8act_debug_gemm_mxfp4_plan", "q8act_logprobs",
 )
 Q8ACT_GEMV_KQ_MAX_M = 8
 Q8ACT_MAX_TOP = 32
@@ -117,6 +118,7 @@ def lib() -> ctypes.CDLL:
                 "q8act_gemm_mxfp4_workspace_bytes": ([I64, I64], SZ),
                 "q8act_gemm_mxfp4": ([P, P, P, I64, I32, P, I32, I64, I64, I64, P, SZ, P], I32),
                 "q8act_gemm_mxfp4_preq": ([P, P, P, P, P, I32, I64, I64, I64, P], I32),
+                "q8act_debug_gemm_mxfp4_plan": ([I32, I64, I64, I64, P], I32),
                 "q8act_logprobs": ([P, I64, I32, P, P, P, P, P, I64, I64, I32, P], I32),
             }
             for f in ("q8act_rmsnorm_q8_1", "q8act_rmsnorm_q8_1_mmq"):
@@ -366,6 +368,11 @@ def q8act_gemm_mxfp4(w, wscales, x, ldx, xtype, y, ytype, m, n, k, ws, ws_bytes,
 
 def q8act_gemm_mxfp4_preq(w, wscales, xq, xscales, y, ytype, m, n, k, stream=None) -> int:
     return lib().q8act_gemm_mxfp4_preq(_p(w), _p(wscales), _p(xq), _p(xscales), _p(y), ytype, m, n, k, _s(stream))
+
+
+def q8act_debug_gemm_mxfp4_plan(sms, m, n, k, plan) -> int:
+    """plan: a ctypes array of four int32, or None."""
+    return lib().q8act_debug_gemm_mxfp4_plan(sms, m, n, k, plan)
 
 
 def q8act_logprobs(logits, ld, type, tokens, logprob, entropy, top_ids, top_logprobs, m, v, top, stream=None) -> int:

@@ -666,7 +666,7 @@ int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t 
     if ((rc = check_rows(x, ldx, k, xtype))) return rc;
     const q8::DeviceInfo *dev;
     if ((rc = current_device(&dev))) return rc;
-    if (q8::gemm_mxfp4_quantizes(*dev, m, n, k))
+    if (q8::gemm_mxfp4_quantizes(dev->num_sms, m, n, k))
         return cuda_rc(q8::launch_gemm_mxfp4_own(*dev, static_cast<const uint8_t *>(w),
                                                  static_cast<const uint8_t *>(wscales), x, ldx, xtype, y, ytype, m, n, k,
                                                  (cudaStream_t)stream));
@@ -674,6 +674,21 @@ int q8act_gemm_mxfp4(const void *w, const void *wscales, const void *x, int64_t 
     rc = q8act_quantize_mxfp4(x, ldx, xtype, xq, xsc, m, k, stream);
     if (rc) return rc;
     return gemm_mxfp4_core(w, wscales, xq, xsc, y, ytype, m, n, k, true, stream);
+}
+
+// Test hook, host only: the choice that the MXFP4 products make.
+int q8act_debug_gemm_mxfp4_plan(int sms, int64_t m, int64_t n, int64_t k, int32_t *plan)
+{
+    if (!plan) return Q8ACT_ERR_NULL;
+    const int rc = gemm_mxfp4_check(Q8ACT_F32, m, n, k);
+    if (rc) return rc;
+    if (sms < 32 || sms > 1024) return Q8ACT_ERR_DIMS;
+    const q8::GemmPlan p = q8::gemm_mxfp4_plan(sms, m, n, k);
+    plan[0] = p.bn;
+    plan[1] = p.CL;
+    plan[2] = p.per_sm;
+    plan[3] = q8::gemm_mxfp4_quantizes(sms, m, n, k);
+    return Q8ACT_OK;
 }
 
 // ---- log probabilities ----

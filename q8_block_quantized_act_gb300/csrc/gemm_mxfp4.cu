@@ -978,28 +978,27 @@ namespace {
 // best choice on average, 21 % at worst (256 x 4096 x 4096: 6.7 us in 64-token tiles, 8.2 in 128-token
 // ones, 10.8 if two share those, 8.3 by pairs; 1 x 2500 x 20480: 11.7 shared by four, 21.2 not shared;
 // 4095 x 12288 x 4096: 63 by pairs with 192 tokens, 74 with 256, 80 in 192-token tiles of one CTA).
-struct Plan {
-    int bn, CL;       // CL = 0: pairs
-    int per_sm = 1;   // CTAs to an SM
-};
-
-Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
+// Up to 16 tokens nothing of the choice depends on m, so that a token's sums are formed in the same order
+// for every m, decoding and verifying: the join's cost is then that of all 16 columns whatever m is (against
+// 6, at 40 sizes of the two choices: 7 % less on average at 1 token, 10 % at 15; 5073 x 2560 at 1 token 4.7 us
+// not shared, 5.2 by two; 2282 x 2304 4.2 not shared, 4.05 by four).
+GemmPlan plan_tiles(int sms, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rows = (n + BM - 1) / BM, steps = k / BK;
     // One token tile and more row tiles than SMs: two CTAs to an SM, so that the last tiles are read
     // beside others and not at the end by a few SMs (1, 8, 32 x 20480 x 4096: 160 tiles, 10.0, 9.9, 10.4 us;
     // 12.3, 12.6, 13.0 by one CTA to an SM; 8 x 64448 x 4096 25.0 and 27.0).
-    if (m <= 64 && rows > dev.num_sms) return {m <= 16 ? 16 : m <= 32 ? 32 : 64, 1, 2};
+    if (m <= 64 && rows > sms) return {m <= 16 ? 16 : m <= 32 ? 32 : 64, 1, 2};
     static const struct { int bn, step, ends; } shapes[] = {
         {16, 220, 100}, {32, 220, 200}, {64, 210, 360}, {128, 290, 590}, {192, 350, 950}};
     static const struct { int bn, step, ends, least, start, part_step, part_ends; } pairs[] = {
         {192, 235, 455, 2745, 1180, 210, 1130}, {256, 275, 2600, 3100, 100, 225, 2250}};
     static const int join_start = 940, join_column[] = {0, 25, 27, 21};                          // CL = 1, 2, 4, 8
-    Plan best{256, 0};
+    GemmPlan best{256, 0};
     int64_t least = INT64_MAX;
     for (const auto &s : pairs) {
         if (m <= 64) break;
-        const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + s.bn - 1) / s.bn), at_once = dev.num_sms / 2;
+        const int64_t tiles = (n + 2 * BM - 1) / (2 * BM) * ((m + s.bn - 1) / s.bn), at_once = sms / 2;
         const bool cut = pair_parts(s.bn, tiles, at_once) > 1;
         const int64_t whole = cut ? tiles / at_once : (tiles + at_once - 1) / at_once;
         const int64_t round = steps * s.step + s.ends;
@@ -1016,10 +1015,10 @@ Plan plan_tiles(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
         const int64_t tiles = rows * ((m + s.bn - 1) / s.bn);
         for (int CL = 1, i = 0; CL <= 8 && CL <= steps; CL *= 2, ++i) {
             if (CL > 1 && s.bn > 128) break;                      // no room for partial sums
-            const int64_t at_once = dev.num_sms / CL - (CL == 8 ? dev.num_sms / 32 : 0);   // GPCs hold few clusters of 8
+            const int64_t at_once = sms / CL - (CL == 8 ? sms / 32 : 0);   // GPCs hold few clusters of 8
             const int64_t rounds = (tiles + at_once - 1) / at_once;
             const int64_t cost = rounds * ((steps + CL - 1) / CL * s.step + s.ends +
-                                           (CL > 1 ? join_start + (m < s.bn ? m : s.bn) * join_column[i] : 0));
+                                           (CL > 1 ? join_start + (s.bn > 16 && m < s.bn ? m : s.bn) * join_column[i] : 0));
             if (cost < least) {
                 least = cost;
                 best = {s.bn, CL};
@@ -1035,9 +1034,11 @@ constexpr int OWN_TASKS_LONG = 12;  // the same where two CTAs to an SM could ta
 
 }  // namespace
 
-bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k)
+GemmPlan gemm_mxfp4_plan(int sms, int64_t m, int64_t n, int64_t k) { return plan_tiles(sms, m, n, k); }
+
+bool gemm_mxfp4_quantizes(int sms, int64_t m, int64_t n, int64_t k)
 {
-    const Plan p = plan_tiles(dev, m, n, k);
+    const GemmPlan p = plan_tiles(sms, m, n, k);
     if (p.bn != 16) return false;                  // never pairs
     const int64_t steps = (k / BK + p.CL - 1) / p.CL;
     return steps <= OWN_STEPS && m * steps <= (p.per_sm == 2 ? OWN_TASKS_LONG : OWN_TASKS);
@@ -1051,7 +1052,7 @@ cudaError_t launch_gemm_mxfp4_own(const DeviceInfo &dev, const uint8_t *w, const
         return with_type(xtype, [&](auto u) {
             using X = decltype(u);
             return launch_tiles<Cfg<16, 8, OWN_STEPS>, T, X>(dev, w, wsc, nullptr, nullptr, static_cast<const X *>(xf), ldx,
-                                                             static_cast<T *>(y), m, n, k, plan_tiles(dev, m, n, k).CL,
+                                                             static_cast<T *>(y), m, n, k, plan_tiles(dev.num_sms, m, n, k).CL,
                                                              false, stream);
         });
     });
@@ -1064,7 +1065,7 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
     return with_type(type, [&](auto t) {
         using T = decltype(t);
         T *out = static_cast<T *>(y);
-        const Plan p = plan_tiles(dev, m, n, k);
+        const GemmPlan p = plan_tiles(dev.num_sms, m, n, k);
         auto go = [&](auto cfg) {
             return launch_tiles<decltype(cfg), T, float>(dev, w, wsc, x, xsc, nullptr, 0, out, m, n, k, p.CL, pdl, stream);
         };

@@ -122,8 +122,16 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo &dev, const uint8_t *w, const uin
                               const uint8_t *xsc, void *y, int type, int64_t m, int64_t n, int64_t k, bool pdl,
                               cudaStream_t stream);
 
+// The product's tiles on a GPU of so many SMs: tokens a tile (bn), CTAs that share a tile's k (CL; 0:
+// pairs of CTAs), CTAs to an SM.
+struct GemmPlan {
+    int bn, CL;
+    int per_sm = 1;
+};
+GemmPlan gemm_mxfp4_plan(int sms, int64_t m, int64_t n, int64_t k);
+
 // Few tokens: the product's CTAs quantize the activation themselves (bitwise the same y).
-bool gemm_mxfp4_quantizes(const DeviceInfo &dev, int64_t m, int64_t n, int64_t k);
+bool gemm_mxfp4_quantizes(int sms, int64_t m, int64_t n, int64_t k);
 cudaError_t launch_gemm_mxfp4_own(const DeviceInfo &dev, const uint8_t *w, const uint8_t *wsc, const void *xf, int64_t ldx,
                                   int xtype, void *y, int type, int64_t m, int64_t n, int64_t k, cudaStream_t stream);
 
