@@ -37,13 +37,28 @@ def make_tail(norm1, proj, norm2, head) -> Tail:
     return Tail(norm1, q8.quantize_q8_0(proj), norm2, codes, scales)
 
 
+def project(w, xq, xd, n: int, out):
+    """The GEMV of up to Q8ACT_GEMV_MAX_M tokens for any k: it keeps the whole activation in shared memory
+    and refuses what does not fit, so long rows go through it in parts (a token's bits do not depend on
+    how many it comes with)."""
+    m = xq.shape[0]
+    try:
+        return q8.gemv_q8_0(w, xq, xd, n, out=out)
+    except q8.Q8ActError as e:
+        if e.rc != q8.Q8ACT_ERR_DIMS or m == 1:
+            raise
+    project(w, xq[:m // 2], xd[:m // 2], n, out[:m // 2])
+    project(w, xq[m // 2:], xd[m // 2:], n, out[m // 2:])
+    return out
+
+
 def score(tail: Tail, x, residual, tokens, top: int = 0, eps: float = 1e-6):
     """x, residual [m, k] float32 (the residual stream is updated in place), tokens [m] int32 ->
     (logprob [m], entropy [m], top ids, top log probabilities)."""
     m, k = x.shape
     if m <= q8.Q8ACT_GEMV_MAX_M:
         xq, xd = q8.rmsnorm_q8_1(x, tail.norm1, eps, residual=residual, residual_out=residual)
-        h = q8.gemv_q8_0(tail.proj, xq, xd, k)
+        h = project(tail.proj, xq, xd, k, x.new_empty((m, k)))
     else:
         xqh, xdt = q8.rmsnorm_q8_1_mmq(x, tail.norm1, eps, residual=residual, residual_out=residual)
         h = q8.gemm_q8_0_preq(tail.proj, xqh, xdt, k)

@@ -88,3 +88,17 @@ def test_decoders_end(k, vocab):
         device_ok()
         for a, b in zip(got, alone):
             assert torch.equal(bits(a), bits(b[:m])), m
+
+
+def test_decoders_end_of_long_rows():
+    """More tokens of a long row than the GEMV keeps at once."""
+    ensure_built()
+    k, vocab, m = 16384, 512, q8.Q8ACT_GEMV_MAX_M
+    tail = score_tokens.make_tail(1 + 0.1 * rnd(1, k), 0.02 * rnd(2, k, k), 1 + 0.1 * rnd(3, k), 0.05 * rnd(4, vocab, k))
+    x, r = rnd(5, m, k), rnd(6, m, k)
+    tokens = torch.arange(m, device="cuda", dtype=torch.int32)
+    parts = [score_tokens.score(tail, x[t:t + 1], r[t:t + 1].clone(), tokens[t:t + 1].clone(), top=4) for t in range(m)]
+    got = score_tokens.score(tail, x, r.clone(), tokens, top=4)
+    device_ok()
+    for a, b in zip(got, (torch.cat(p) for p in zip(*parts))):
+        assert torch.equal(bits(a), bits(b))
