@@ -31,7 +31,7 @@ from ._lib import (  # noqa: F401  (re-exported ABI)
     Q8ACT_ERR_TYPE, Q8ACT_F32, Q8ACT_F16, Q8ACT_BF16, Q8ACT_MAX_TOP, q8act_rmsnorm_q8_1, q8act_rmsnorm_q8_1_mmq,
     q8act_mxfp4_scale_bytes, q8act_quantize_mxfp4, q8act_dequant_mxfp4, q8act_tile_mxfp4_scales,
     q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq,
-    q8act_debug_gemm_mxfp4_plan, q8act_logprobs, _s)
+    q8act_debug_gemm_mxfp4_plan, q8act_logprobs)
 
 QK = 32
 Q8_0_BYTES = 34
@@ -233,12 +233,16 @@ def gemv_kq(fmt: str, w, xq, xd, n: int, out=None):
 _TYPES: dict = {}
 _torch = None
 _current = None      # the current CUDA device's index, as a call
+_stream = None       # torch's current stream on a device, as an address
 
 
 def _load_torch():
-    global _torch, _current
+    global _torch, _current, _stream
     import torch
-    _current = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2   # no tensor's
+    if torch.cuda.is_available():
+        _current, _stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    else:
+        _current = lambda: -2                    # noqa: E731  no tensor's
     _TYPES.update({torch.float32: Q8ACT_F32, torch.float16: Q8ACT_F16, torch.bfloat16: Q8ACT_BF16})
     _torch = torch
     return torch
@@ -314,7 +318,7 @@ def _rmsnorm(mmq, x, weight, eps, residual, residual_out, y, out, quants=True):
         pq, pd = _given(q, shape, qtype, "quants", dev), _given(d, dshape, torch.float32, "scales", dev)
     L = lib()
     fn = L.q8act_rmsnorm_q8_1_mmq if mmq else L.q8act_rmsnorm_q8_1
-    rc = fn(x.data_ptr(), ldx, pr, ldr, pw, wtype, eps, pro, ldro, py, pq, pd, m, k, code, _s(None))
+    rc = fn(x.data_ptr(), ldx, pr, ldr, pw, wtype, eps, pro, ldro, py, pq, pd, m, k, code, _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_rmsnorm_q8_1_mmq" if mmq else "q8act_rmsnorm_q8_1")
     return q, d
@@ -363,7 +367,7 @@ def quantize_mxfp4(x, out=None):
         out = (torch.empty((m, k // 2), dtype=u8, device=x.device), torch.empty(nsc, dtype=u8, device=x.device))
     codes, scales = out
     rc = lib().q8act_quantize_mxfp4(x.data_ptr(), ldx, code, _given(codes, (m, k // 2), u8, "codes", dev),
-                                    _given(scales, nsc, u8, "scales", dev), m, k, _s(None))
+                                    _given(scales, nsc, u8, "scales", dev), m, k, _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_quantize_mxfp4")
     return codes, scales
@@ -379,7 +383,7 @@ def dequant_mxfp4(codes, scales, dtype=None, out=None):
     if out is None:
         out = torch.empty((m, k), dtype=dtype or torch.float16, device=codes.device)
     code = _type(out, "out")
-    rc = lib().q8act_dequant_mxfp4(pc, ps, _given(out, (m, k), out.dtype, "out", dev), code, m, k, _s(None))
+    rc = lib().q8act_dequant_mxfp4(pc, ps, _given(out, (m, k), out.dtype, "out", dev), code, m, k, _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_dequant_mxfp4")
     return out
@@ -392,7 +396,7 @@ def tile_mxfp4_scales(scales):
     m, kb = scales.shape
     ps = _given(scales, (m, kb), torch.uint8, "scales", dev)
     tiled = torch.empty(_mxfp4_scales(m, kb * QK), dtype=torch.uint8, device=scales.device)
-    rc = lib().q8act_tile_mxfp4_scales(ps, tiled.data_ptr(), m, kb * QK, _s(None))
+    rc = lib().q8act_tile_mxfp4_scales(ps, tiled.data_ptr(), m, kb * QK, _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_tile_mxfp4_scales")
     return tiled
@@ -429,7 +433,7 @@ def gemm_mxfp4(w, wscales, x, ws=None, dtype=None, out=None):
         out = torch.empty((m, n), dtype=dtype or torch.float32, device=x.device)
     ycode = _type(out, "out")
     rc = lib().q8act_gemm_mxfp4(pw, psc, x.data_ptr(), ldx, code, _given(out, (m, n), out.dtype, "out", dev), ycode,
-                                m, n, k, ws.data_ptr(), ws.numel(), _s(None))
+                                m, n, k, ws.data_ptr(), ws.numel(), _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4")
     return out
@@ -447,7 +451,7 @@ def gemm_mxfp4_preq(w, wscales, xq, xscales, dtype=None, out=None):
         out = torch.empty((m, n), dtype=dtype or torch.float32, device=xq.device)
     ycode = _type(out, "out")
     rc = lib().q8act_gemm_mxfp4_preq(pw, psc, px, pxs, _given(out, (m, n), out.dtype, "out", dev), ycode, m, n, k,
-                                     _s(None))
+                                     _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_gemm_mxfp4_preq")
     return out
@@ -475,7 +479,7 @@ def logprobs(logits, tokens=None, top: int = 0, out=None):
     if top > 0:
         pids, ptlp = _given(ids, (m, top), i32, "ids", dev), _given(tlp, (m, top), f32, "top_logprobs", dev)
     rc = lib().q8act_logprobs(logits.data_ptr(), ld, code, ptok, plp, _given(ent, (m,), f32, "entropy", dev), pids, ptlp,
-                              m, v, top, _s(None))
+                              m, v, top, _stream(dev))
     if rc:
         raise Q8ActError(rc, "q8act_logprobs")
     return lp, ent, ids, tlp

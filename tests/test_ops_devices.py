@@ -70,7 +70,7 @@ def launches(monkeypatch):
 
     q8._load_torch()
     monkeypatch.setattr(q8, "_current", lambda: 0, raising=False)
-    monkeypatch.setattr(q8, "_s", lambda stream: 0)
+    monkeypatch.setattr(q8, "_stream", lambda device: 0, raising=False)
     monkeypatch.setattr(q8, "lib", Recorder)
     return seen
 
