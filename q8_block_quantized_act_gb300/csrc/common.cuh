@@ -89,11 +89,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
 // wait returns once that grid has completed and its writes are visible; without a
 // prerequisite grid it returns at once), and only then calls griddep_launch_dependents(),
 // which lets the next kernel become resident in turn.  So a dependent that starts early knows
-// that everything before its predecessor has completed.  The quantizers are ordinary launches
-// (grids of many small CTAs, beside which waiting dependents would take issue slots) that
-// trigger their dependents at entry; the second kernel of a fused call (the GEMV or GEMM
-// after the call's own quantizer) streams weights before its wait, which the quantizer does
-// not write.  Resident dependents cannot starve their predecessor: they launch only once every
+// that everything before its predecessor has completed.  The q8_1 quantizers are ordinary
+// launches (grids of many small CTAs, beside which waiting dependents would take issue slots)
+// that trigger their dependents at entry.  The second kernel of a fused call (the GEMV, GEMM or
+// MXFP4 product after the call's own quantizer) streams weights before its wait, which the
+// quantizer does not write: so the MXFP4 quantizer, a dependent itself, must wait before it
+// triggers, as the others do, or weights written right before the call could be read too early.
+// Resident dependents cannot starve their predecessor: they launch only once every
 // CTA of it has started.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

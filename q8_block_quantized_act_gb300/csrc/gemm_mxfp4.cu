@@ -20,8 +20,9 @@
 //
 // What bounds it: the weight stream for few tokens (5 x 64448 x 4096: 24.4 us for 142 MB with the
 // activation's quantization, 0.86 of the copy rate; 1 x 4096 x 4096, 32 tiles shared by four CTAs each:
-// 5.0 us, latency), the MMAs for many (pairs of CTAs, below: 4095 x 20480 x 8192 in 206 us, 6.7 PFLOP/s
-// with its quantizer).
+// 5.4 us with weights from HBM, latency), the MMAs for many (pairs of CTAs, below: 4095 x 20480 x 8192 with
+// its quantizer 207 us in a burst, 6.6 PFLOP/s, and 227-235 call after call, 5.9, at the clock that the power
+// limit then leaves).
 // No rounding between the codes and y: products of codes and scales are exact, sums are the tensor
 // cores' f32, y is rounded once.
 #include "launch.h"
@@ -602,11 +603,12 @@ cudaError_t launch_tiles(const DeviceInfo &dev, const uint8_t *w, const uint8_t 
 // (half of the columns each), release it, then store.  256 tokens: two accumulators would leave tensor
 // memory no room for the scales, so the next tile's MMAs wait for the hand-over (2.4 us a tile).  192
 // tokens: two, and no such wait, for 112 cycles of operands where the arithmetic takes 96.  So 192 is
-// faster up to k = 4096 (2048 x 12288 x 4096: 34.4 us, 41.2 by 256) and about equal at 8192.
+// faster up to k = 4096 (2048 x 12288 x 4096: 35.0 us, 41.0 by 256; call after call 37.4 and 40.9) and about
+// equal at 8192 (4095 x 20480: 187.5 and 190.8; call after call 214 and 212).
 //
 // Tiles that do not fill a last round of all pairs are cut into parts of 128 or 64 tokens, so that
-// the round takes less: a part's MMA reads 8 KB of its 128 weight rows whatever its tokens are, so a
-// quarter costs 0.6 of a tile, not 0.25.
+// the round takes less: a part's MMA reads 4 KB of its 128 weight rows whatever its tokens are (5 KB with
+// 64 of 256 tokens, 8 with all), so a quarter costs 0.6 of a tile, not 0.25.
 // ---------------------------------------------------------------------------------------
 template <int BN_>
 struct PairCfg {
@@ -977,7 +979,7 @@ namespace {
 // from 1000 to 64448, k from 512 to 20480, weights from HBM): what the formula takes is 0.4 % above the
 // best choice on average, 21 % at worst (256 x 4096 x 4096: 6.7 us in 64-token tiles, 8.2 in 128-token
 // ones, 10.8 if two share those, 8.3 by pairs; 1 x 2500 x 20480: 11.7 shared by four, 21.2 not shared;
-// 4095 x 12288 x 4096: 63 by pairs with 192 tokens, 74 with 256, 80 in 192-token tiles of one CTA).
+// 4095 x 12288 x 4096: 64 by pairs with 192 tokens, 74 with 256, 80 in 192-token tiles of one CTA).
 // Up to 16 tokens nothing of the choice depends on m, so that a token's sums are formed in the same order
 // for every m, decoding and verifying: the join's cost is then that of all 16 columns whatever m is (against
 // 6, at 40 sizes of the two choices: 7 % less on average at 1 token, 10 % at 15; 5073 x 2560 at 1 token 4.7 us

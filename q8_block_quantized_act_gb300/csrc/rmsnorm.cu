@@ -3,8 +3,11 @@
 //
 // Bound by memory: x, the residual in, the residual, the quants and scales out.  The row stays in
 // registers between the sum of squares and the quantization, so each is moved once.  4093 x 8192
-// f16: 38.6 us with a residual to int8 (6.2 TB/s, 0.91 of a copy), 29.2 without (3.6: there the
-// instructions, about 25 a value, and the row's chain of loads, barrier and shuffles count).  All
+// f16: 39.4 us with a residual to int8 (6.1 TB/s, 0.90 of a copy), the norm alone 41.9 (0.94).  Without
+// a residual 29.4 to int8, 30.7 to binary16 (0.52 and 0.66 of a copy): the instructions (21 a value)
+// would take 18 us and the bytes 20, but each row's loads, barrier and shuffles follow one another and 64
+// registers leave four rows an SM to overlap them (issue slots 62 % busy, no pipe above 31 %; most
+// waiting is for loads, then for fixed latencies).  All
 // arithmetic is f32; the residual is rounded once to its type, y once, the norm itself not at all
 // before the quantization.
 #include "launch.h"
@@ -201,7 +204,8 @@ __global__ void __launch_bounds__(MAX_THREADS, 1024 / MAX_THREADS) rmsnorm_row_k
     }
 }
 
-// Rows too long for registers: read twice (the second time from L2).
+// Rows too long for registers: read twice, the second time from L2 at best, with a chunk a thread under way
+// (4093 x 20480 f32: 245 us with a residual and no quants, 0.81 of a copy; 161 to int8 without, 0.39).
 template <typename T, bool MMQ>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a, int k)
 {
