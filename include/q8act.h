@@ -454,6 +454,70 @@ int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *toke
                    int32_t *top_ids, float *top_logprobs, int64_t m, int64_t v, int top, void *stream);
 
 /*
+ * A batch of sequences over a paged key/value cache, as q8act_append_kv and q8act_attention take it.
+ *   k, v: the cache: `pages` pages of [heads][page_size][dim] elements of `type` (Q8ACT_F16 or BF16),
+ *       page_stride elements apart in both (at least heads * page_size * dim; a multiple of 8).
+ *       dim: 64 or 128.  page_size: a power of two, 16 .. 1024.
+ *   table [seqs][table_width], rows table_ld entries apart: the pages of each sequence; its position p
+ *       is slot p % page_size of page table[seq][p / page_size].
+ *   starts [seqs + 1], ascending: sequence b's new tokens are rows starts[b] .. starts[b + 1] - 1 of the
+ *       calls' arrays (none where they are equal).
+ *   lens [seqs]: positions of each sequence, the new tokens included: its last new token has position
+ *       lens - 1, the others the positions before.
+ * table, starts and lens are device memory that the kernels read when they run, so a captured graph
+ * follows their contents.  seqs <= 2^20, table_width * page_size <= 2^30, pages < 2^31; the cache 16-byte
+ * aligned, the others as their type.
+ * Positions before 0, beyond the table or on a page outside 0 .. pages - 1 do not exist: nothing is written
+ * to them, and the attention takes them as masked.  Rows before starts[0] and from starts[seqs] on (padding of a
+ * batch) are left as they were.
+ */
+typedef struct q8act_paged_kv {
+    void *k, *v;
+    int64_t page_stride, pages;
+    const int32_t *table;
+    int64_t table_ld;
+    const int32_t *starts, *lens;
+    int32_t seqs, table_width, page_size, heads, dim, type;
+} q8act_paged_kv;
+
+/*
+ * The new tokens' keys and values into the cache, keys and queries rotated by their positions p:
+ *   pairs (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p turns[i] / 2^64 for pair i.
+ *   q [m][heads_q][dim], k, v [m][heads][dim]: elements of `type`, tokens ldq, ldk, ldv elements apart
+ *       (rows 16-byte aligned; the parts of a fused projection's rows, for instance).
+ *   q_out [m][heads_q][dim] of the cache's type, tokens ldqo apart: the rotated queries (it may be q
+ *       itself where the types agree).  q and q_out may both be NULL (heads_q 0).
+ *   turns [rot / 2]: each pair's fraction of a turn a position, times 2^64 (the angle is then exact modulo a
+ *       turn at any position).  rot <= dim, a multiple of 16: the head's first rot values are rotated, as
+ *       pairs (i, i + rot / 2), or (2i, 2i + 1) where interleaved is 1; the others are copied.  rot 0
+ *       with turns NULL: no rotation.
+ * f32 arithmetic, each value rounded once.  Two rows with the same place in the cache (a page that two
+ * sequences share and both append to) leave one of the two there.
+ */
+int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                    int64_t ldv, int type, void *q_out, int64_t ldqo, int heads_q, const uint64_t *turns, int rot,
+                    int interleaved, int64_t m, void *stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their own keys and values already):
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . k_j) v_j  over the positions j <= p of its sequence, and
+ *   p - window < j where window > 0; keys and values of head h * heads / heads_q.
+ *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
+ *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
+ *   scale > 0.  A token that sees no position gets zeros.  What is at masked places (beyond lens, behind the
+ *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
+ *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
+ *       to the cache's type for their product with the values.
+ *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
+ *       known).  It chooses the kernel and may be wrong.
+ *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses
+ *       until the call's work is done; it needs no preparation and holds nothing between calls.
+ */
+size_t q8act_attention_workspace_bytes(int heads_q, int heads, int dim);   /* 0 for invalid arguments */
+int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *out, int64_t ldo, int otype, int heads_q,
+                    float scale, int window, int max_new, int64_t m, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device-side status word that kernels set
  * when a pipeline wait times out.  Returns Q8ACT_OK, Q8ACT_ERR_DRAIN_TIMEOUT (a producer gave
  * up waiting for its own copies before its CTA exited), Q8ACT_ERR_TIMEOUT (a pipeline wait

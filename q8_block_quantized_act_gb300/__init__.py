@@ -1,5 +1,6 @@
 """GB300 (sm_103a) Q8_0 weight x q8_1 activation block-quantized matmul, and what stands next to it
-in a decoder: the norm that feeds it, MXFP4 products, log probabilities of logits.
+in a decoder: the norm that feeds it, the paged key/value cache and the attention over it, MXFP4
+products, log probabilities of logits.
 
 The compute lives in libq8act.so (hand-written CUDA kernels behind the C ABI of
 include/q8act.h).  This package is its Python face:
@@ -13,6 +14,8 @@ include/q8act.h).  This package is its Python face:
 There is no CPU or PyTorch fallback: without the built library every call raises.
 """
 from __future__ import annotations
+
+import ctypes
 
 from ._lib import (  # noqa: F401  (re-exported ABI)
     EXPORTED, LIB_PATH, Q8ACT_ERR_ALIGN, Q8ACT_ERR_CUDA_BASE, Q8ACT_ERR_DEVICE, Q8ACT_ERR_DIMS,
@@ -31,7 +34,8 @@ from ._lib import (  # noqa: F401  (re-exported ABI)
     Q8ACT_ERR_TYPE, Q8ACT_F32, Q8ACT_F16, Q8ACT_BF16, Q8ACT_MAX_TOP, q8act_rmsnorm_q8_1, q8act_rmsnorm_q8_1_mmq,
     q8act_mxfp4_scale_bytes, q8act_quantize_mxfp4, q8act_dequant_mxfp4, q8act_tile_mxfp4_scales,
     q8act_gemm_mxfp4_workspace_bytes, q8act_gemm_mxfp4, q8act_gemm_mxfp4_preq,
-    q8act_debug_gemm_mxfp4_plan, q8act_logprobs)
+    q8act_debug_gemm_mxfp4_plan, q8act_logprobs, q8act_paged_kv, q8act_append_kv, q8act_attention,
+    q8act_attention_workspace_bytes)
 
 QK = 32
 Q8_0_BYTES = 34
@@ -483,3 +487,187 @@ def logprobs(logits, tokens=None, top: int = 0, out=None):
     if rc:
         raise Q8ActError(rc, "q8act_logprobs")
     return lp, ent, ids, tlp
+
+
+class PagedKV:
+    """A batch of sequences over a paged key/value cache, checked once and kept as long as its tensors are.
+
+    k, v: [pages, heads, page_size, dim] float16 or bfloat16, dim 64 or 128, page_size a power of two from 16
+        to 1024; pages may stand apart (the halves of a [pages, 2, ...] tensor), what is inside one may not.
+    table: int32 [seqs, width], the pages of each sequence (its rows may stand apart).
+    starts: int32 [seqs + 1]; sequence b's new tokens are rows starts[b] .. starts[b + 1] - 1 of the calls' arrays.
+    lens: int32 [seqs], positions of each sequence with its new tokens.
+
+    The calls read table, starts and lens on the device when they run: change their contents in place and
+    use the same PagedKV (and the same captured graph) for the next step.  Page ids outside the cache (-1,
+    say) and positions beyond the table do not exist: nothing is written there, and they are masked."""
+
+    __slots__ = ("k", "v", "table", "starts", "lens", "c", "at", "device", "heads", "dim")
+
+    def __init__(self, k, v, table, starts, lens):
+        torch = _torch or _load_torch()
+        dev = _current()
+        for t, what in ((k, "k"), (v, "v"), (table, "table"), (starts, "starts"), (lens, "lens")):
+            if t.get_device() != dev:
+                raise _elsewhere(t, what, dev)
+        if k.dtype not in (torch.float16, torch.bfloat16) or v.dtype is not k.dtype:
+            raise Q8ActError(Q8ACT_ERR_TYPE, f"k, v: {k.dtype}, {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or k.numel() == 0:
+            raise Q8ActError(Q8ACT_ERR_DIMS, "k, v: [pages, heads, page_size, dim] both")
+        pages, heads, size, dim = k.shape
+        inner = (size * dim, dim, 1)
+        for t, what in ((k, "k"), (v, "v")):
+            if any(n > 1 and a != b for n, a, b in zip(t.shape[1:], t.stride()[1:], inner)):
+                raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: a page's values are adjacent")
+        stride = k.stride(0) if pages > 1 else heads * size * dim
+        if pages > 1 and v.stride(0) != stride:
+            raise Q8ActError(Q8ACT_ERR_DIMS, "k, v: the same distance between pages")
+        if table.dim() != 2 or table.numel() == 0 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise Q8ActError(Q8ACT_ERR_DIMS, "table: [seqs, width] with adjacent entries")
+        seqs, width = table.shape
+        for t, what, shape in ((starts, "starts", (seqs + 1,)), (lens, "lens", (seqs,))):
+            if t.shape != shape or not t.is_contiguous():
+                raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: contiguous {shape}")
+        for t, what in ((table, "table"), (starts, "starts"), (lens, "lens")):
+            if t.dtype is not torch.int32:
+                raise Q8ActError(Q8ACT_ERR_TYPE, f"{what}: {t.dtype}")
+        self.k, self.v, self.table, self.starts, self.lens = k, v, table, starts, lens
+        self.c = q8act_paged_kv(k.data_ptr(), v.data_ptr(), stride, pages, table.data_ptr(),
+                                table.stride(0) if seqs > 1 else width, starts.data_ptr(), lens.data_ptr(),
+                                min(seqs, 2 ** 31 - 1), min(width, 2 ** 31 - 1), min(size, 2 ** 31 - 1),
+                                min(heads, 2 ** 31 - 1), min(dim, 2 ** 31 - 1), _TYPES[k.dtype])
+        self.at = ctypes.addressof(self.c)
+        self.device, self.heads, self.dim = dev, heads, dim
+
+
+def rope_turns(inv_freq, device=None):
+    """What append_kv rotates by, from the angle in radians that each pair turns a position: int64 [pairs]
+    fractions of a turn times 2^64 (on inv_freq's device, or `device`).  inv_freq: a float64 tensor or a sequence, e.g.
+    base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim), scaled as the model scales it."""
+    import math
+
+    torch = _torch or _load_torch()
+    if isinstance(inv_freq, torch.Tensor):
+        device = inv_freq.device if device is None else device
+        inv_freq = inv_freq.double().tolist()
+    turns = []
+    for f in inv_freq:
+        if not math.isfinite(f):
+            raise Q8ActError(Q8ACT_ERR_DIMS, f"inv_freq: {f}")
+        t = round(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64
+        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
+
+
+def _heads(t, what: str, dev: int, heads: int, dim: int) -> int:
+    """Distance in elements of a [tokens, heads, dim] tensor's tokens; a token's values are adjacent."""
+    if t.get_device() != dev:
+        raise _elsewhere(t, what, dev)
+    shape = t.shape
+    if len(shape) == 3 and shape[0] > 0 and shape[1] == heads and shape[2] == dim:
+        if t.is_contiguous():
+            return heads * dim
+        a, b, c = t.stride()
+        if c == 1 and (b == dim or heads == 1):
+            return a if shape[0] > 1 else max(a, heads * dim)
+    raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: [tokens, {heads}, {dim}] with a token's values adjacent")
+
+
+def _batch(kv, what: str):
+    dev = _current()
+    if kv.device != dev:
+        raise Q8ActError(Q8ACT_ERR_DEVICE, f"{what}: not on the current CUDA device (cuda:{dev})")
+    return dev
+
+
+def append_kv(kv, q, k, v, turns=None, interleaved: bool = False, out=None):
+    """The new tokens' keys and values [m, heads, dim] into the cache of a PagedKV, keys and queries rotated
+    by their positions on the way; returns the rotated queries [m, query heads, dim] in the cache's type
+    (`out`, which may be q itself where the types agree), or None without q.
+    q, k, v: float32, float16 or bfloat16 alike, views of a fused projection's rows for instance.
+    turns: rope_turns(...) of the pairs that are rotated (2 * len(turns) <= dim values of each head, a
+    multiple of 16), as pairs (i, i + len(turns)) or, interleaved, (2i, 2i + 1); None: no rotation."""
+    torch = _torch or _load_torch()
+    dev = _batch(kv, "kv")
+    heads, dim = kv.heads, kv.dim
+    ldk, ldv, code = _heads(k, "k", dev, heads, dim), _heads(v, "v", dev, heads, dim), _type(k, "k")
+    m = k.shape[0]
+    if v.shape[0] != m:
+        raise Q8ActError(Q8ACT_ERR_DIMS, f"v: {v.shape[0]} tokens for {m} of k")
+    if v.dtype is not k.dtype:
+        raise Q8ActError(Q8ACT_ERR_TYPE, f"v: {v.dtype}, k: {k.dtype}")
+    pq = po = pt = None
+    ldq = ldo = hq = rot = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != m:
+            raise Q8ActError(Q8ACT_ERR_DIMS, f"q: [{m}, heads, {dim}]")
+        hq = q.shape[1]
+        ldq, pq = _heads(q, "q", dev, hq, dim), q.data_ptr()
+        if q.dtype is not k.dtype:
+            raise Q8ActError(Q8ACT_ERR_TYPE, f"q: {q.dtype}, k: {k.dtype}")
+        if out is None:
+            out = torch.empty((m, hq, dim), dtype=kv.k.dtype, device=q.device)
+        elif out.dtype is not kv.k.dtype:
+            raise Q8ActError(Q8ACT_ERR_TYPE, f"out: {out.dtype}")
+        elif out.shape != q.shape:
+            raise Q8ActError(Q8ACT_ERR_DIMS, f"out: {tuple(q.shape)}")
+        ldo, po = _heads(out, "out", dev, hq, dim), out.data_ptr()
+    elif out is not None:
+        raise Q8ActError(Q8ACT_ERR_NULL, "out without q")
+    if turns is not None:
+        rot = 2 * turns.numel()
+        pt = _given(turns, (rot // 2,), torch.int64, "turns", dev)
+    rc = lib().q8act_append_kv(kv.at, pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, code, po, ldo, hq, pt, rot,
+                               1 if interleaved else 0, m, _stream(dev))
+    if rc:
+        raise Q8ActError(rc, "q8act_append_kv")
+    return out
+
+
+def attention_workspace(kv, heads: int):
+    """A workspace for attention over a PagedKV with so many query heads: it suits every batch over caches of
+    the same heads and dim.  Calls that may run at the same time (on other streams) need one each."""
+    import torch
+    nbytes = q8act_attention_workspace_bytes(heads, kv.heads, kv.dim)
+    if nbytes == 0:
+        raise Q8ActError(Q8ACT_ERR_DIMS, "q8act_attention_workspace_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=kv.k.device)
+
+
+def attention(kv, q, scale=None, window: int = 0, max_new=None, ws=None, dtype=None, out=None):
+    """Causal attention of the new tokens q [m, query heads, dim] (the cache's type) over a PagedKV whose cache
+    holds their own keys and values already (append_kv): [m, query heads, dim] in dtype (default the cache's) or
+    out's type.  Query head i reads key/value head i * heads // query heads.
+    scale: of the scores, default dim ** -0.5.  window: how many positions a token sees, itself included (0: all).
+    max_new: the most new tokens that one sequence has, where the caller knows it (1 when decoding); it chooses
+    the kernel and may be wrong.  ws: attention_workspace(kv, heads); by default one is allocated."""
+    torch = _torch or _load_torch()
+    dev = _batch(kv, "kv")
+    if q.dim() != 3:
+        raise Q8ActError(Q8ACT_ERR_DIMS, "q: [tokens, heads, dim]")
+    m, hq, dim = q.shape
+    ldq = _heads(q, "q", dev, hq, kv.dim)
+    if q.dtype is not kv.k.dtype:
+        raise Q8ActError(Q8ACT_ERR_TYPE, f"q: {q.dtype}, the cache: {kv.k.dtype}")
+    if ws is None:
+        ws = attention_workspace(kv, hq)
+    elif ws.get_device() != dev:
+        raise _elsewhere(ws, "ws", dev)
+    elif not (ws.dtype is torch.uint8 and ws.is_contiguous()):
+        raise Q8ActError(Q8ACT_ERR_WORKSPACE, "ws: contiguous uint8")
+    if out is None:
+        out = torch.empty((m, hq, dim), dtype=dtype or q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise Q8ActError(Q8ACT_ERR_DIMS, f"out: {tuple(q.shape)}")
+    code = _type(out, "out")
+    if max_new is None:
+        max_new = m
+    for what, n in (("window", window), ("max_new", max_new)):
+        if not 0 <= n < 2 ** 31:
+            raise Q8ActError(Q8ACT_ERR_DIMS, f"{what}: {n}")
+    rc = lib().q8act_attention(kv.at, q.data_ptr(), ldq, out.data_ptr(), _heads(out, "out", dev, hq, dim), code, hq,
+                               dim ** -0.5 if scale is None else scale, window, max_new, m, ws.data_ptr(), ws.numel(),
+                               _stream(dev))
+    if rc:
+        raise Q8ActError(rc, "q8act_attention")
+    return out

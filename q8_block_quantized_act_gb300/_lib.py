@@ -51,11 +51,22 @@ EXPORTED = (
     "q8act_mxfp4_scale_bytes", "q8act_quantize_mxfp4", "q8act_dequant_mxfp4", "q8act_tile_mxfp4_scales",
     "q8act_gemm_mxfp4_workspace_bytes", "q8act_gemm_mxfp4", "q8act_gemm_mxfp4_preq",
     "q8act_debug_gemm_mxfp4_plan", "q8act_logprobs",
+    "q8act_append_kv", "q8act_attention", "q8act_attention_workspace_bytes",
 )
 Q8ACT_GEMV_KQ_MAX_M = 8
 Q8ACT_MAX_TOP = 32
 Q8ACT_NOALLOC_WS_BYTES = 24 << 20
 Q8ACT_GEMM_SPLIT_BYTES = 320 * 65536 + 160 * 64
+
+
+class q8act_paged_kv(ctypes.Structure):
+    """The C struct: a batch of sequences over a paged key/value cache (HOST memory; its pointers are
+    device addresses)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64),
+                ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 class Q8ActError(RuntimeError):
@@ -120,6 +131,9 @@ def lib() -> ctypes.CDLL:
                 "q8act_gemm_mxfp4_preq": ([P, P, P, P, P, I32, I64, I64, I64, P], I32),
                 "q8act_debug_gemm_mxfp4_plan": ([I32, I64, I64, I64, P], I32),
                 "q8act_logprobs": ([P, I64, I32, P, P, P, P, P, I64, I64, I32, P], I32),
+                "q8act_append_kv": ([P, P, I64, P, I64, P, I64, I32, P, I64, I32, P, I32, I32, I64, P], I32),
+                "q8act_attention": ([P, P, I64, P, I64, I32, I32, F32, I32, I32, I64, P, SZ, P], I32),
+                "q8act_attention_workspace_bytes": ([I32, I32, I32], SZ),
             }
             for f in ("q8act_rmsnorm_q8_1", "q8act_rmsnorm_q8_1_mmq"):
                 sig[f] = ([P, I64, P, I64, P, I32, F32, P, I64, P, P, P, I64, I64, I32, P], I32)
@@ -378,3 +392,23 @@ def q8act_debug_gemm_mxfp4_plan(sms, m, n, k, plan) -> int:
 def q8act_logprobs(logits, ld, type, tokens, logprob, entropy, top_ids, top_logprobs, m, v, top, stream=None) -> int:
     return lib().q8act_logprobs(_p(logits), ld, type, _p(tokens), _p(logprob), _p(entropy), _p(top_ids),
                                 _p(top_logprobs), m, v, top, _s(stream))
+
+
+def _kv(kv):
+    return None if kv is None else ctypes.addressof(kv)
+
+
+def q8act_append_kv(kv, q, ldq, k, ldk, v, ldv, type, q_out, ldqo, heads_q, turns, rot, interleaved, m, stream=None) -> int:
+    """kv: a q8act_paged_kv, or None."""
+    return lib().q8act_append_kv(_kv(kv), _p(q), ldq, _p(k), ldk, _p(v), ldv, type, _p(q_out), ldqo, heads_q, _p(turns),
+                                 rot, interleaved, m, _s(stream))
+
+
+def q8act_attention(kv, q, ldq, out, ldo, otype, heads_q, scale, window, max_new, m, ws, ws_bytes, stream=None) -> int:
+    """kv: a q8act_paged_kv, or None."""
+    return lib().q8act_attention(_kv(kv), _p(q), ldq, _p(out), ldo, otype, heads_q, scale, window, max_new, m, _p(ws),
+                                 ws_bytes, _s(stream))
+
+
+def q8act_attention_workspace_bytes(heads_q, heads, dim) -> int:
+    return lib().q8act_attention_workspace_bytes(heads_q, heads, dim)

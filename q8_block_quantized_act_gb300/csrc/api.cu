@@ -712,6 +712,84 @@ int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *toke
     return cuda_rc(q8::launch_logprobs(*dev, a, m, v, type, (cudaStream_t)stream));
 }
 
+// ---- the paged key/value cache ----
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The batch, for m rows of heads_q query heads.
+static int check_paged(const q8act_paged_kv *kv, int64_t m, int64_t heads_q)
+{
+    if (!kv || !kv->k || !kv->v || !kv->table || !kv->starts || !kv->lens) return Q8ACT_ERR_NULL;
+    if (kv->type != Q8ACT_F16 && kv->type != Q8ACT_BF16) return Q8ACT_ERR_TYPE;
+    const int64_t ps = kv->page_size;
+    if ((kv->dim != 64 && kv->dim != 128) || ps < 16 || ps > 1024 || (ps & (ps - 1)) || kv->heads < 1 || kv->heads > 1024 ||
+        kv->pages < 1 || kv->pages >= INT32_MAX || kv->page_stride < kv->heads * ps * kv->dim ||
+        kv->page_stride >= ((int64_t)1 << 38) || kv->seqs < 1 || kv->seqs > (1 << 20) || kv->table_width < 1 ||
+        kv->table_width * ps > (1 << 30) || kv->table_ld < kv->table_width || kv->table_ld >= ((int64_t)1 << 40))
+        return Q8ACT_ERR_DIMS;
+    if (m < 1 || heads_q < 0 || heads_q > 4096 || m * (heads_q + 2 * kv->heads) > (1 << 30)) return Q8ACT_ERR_DIMS;
+    if (!aligned16(kv->k) || !aligned16(kv->v) || kv->page_stride % 8 || !aligned4(kv->table) || !aligned4(kv->starts) ||
+        !aligned4(kv->lens))
+        return Q8ACT_ERR_ALIGN;
+    return Q8ACT_OK;
+}
+
+int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                    int64_t ldv, int type, void *q_out, int64_t ldqo, int heads_q, const uint64_t *turns, int rot,
+                    int interleaved, int64_t m, void *stream)
+{
+    if (!k || !v || !q != !q_out || !q != !heads_q || !turns != !rot) return Q8ACT_ERR_NULL;
+    if (m < 1 || m > (1 << 30)) return Q8ACT_ERR_DIMS;
+    int rc = check_paged(kv, m, heads_q);
+    if (rc) return rc;
+    if (!known_type(type)) return Q8ACT_ERR_TYPE;
+    if (rot < 0 || rot > kv->dim || rot % 16 || (interleaved != 0 && interleaved != 1)) return Q8ACT_ERR_DIMS;
+    if ((rc = check_rows(k, ldk, (int64_t)kv->heads * kv->dim, type)) ||
+        (rc = check_rows(v, ldv, (int64_t)kv->heads * kv->dim, type)))
+        return rc;
+    if (q && ((rc = check_rows(q, ldq, (int64_t)heads_q * kv->dim, type)) ||
+              (rc = check_rows(q_out, ldqo, (int64_t)heads_q * kv->dim, kv->type))))
+        return rc;
+    if (reinterpret_cast<uintptr_t>(turns) & 7u) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    const q8::AppendArgs a{q, k, v, q_out, ldq, ldk, ldv, ldqo, turns, type, heads_q, rot, interleaved};
+    return cuda_rc(q8::launch_append_kv(*dev, *kv, a, m, (cudaStream_t)stream));
+}
+
+static bool attention_heads(int64_t heads_q, int64_t heads, int64_t dim)
+{
+    return heads >= 1 && heads <= 1024 && heads_q >= heads && heads_q <= 4096 && heads_q % heads == 0 &&
+           (dim == 64 || dim == 128);
+}
+
+size_t q8act_attention_workspace_bytes(int heads_q, int heads, int dim)
+{
+    return attention_heads(heads_q, heads, dim) ? q8::attention_workspace_bytes(dim) : 0;
+}
+
+int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *out, int64_t ldo, int otype, int heads_q,
+                    float scale, int window, int max_new, int64_t m, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!q || !out) return Q8ACT_ERR_NULL;
+    if (m < 1 || m > (1 << 30)) return Q8ACT_ERR_DIMS;
+    int rc = check_paged(kv, m, heads_q);
+    if (rc) return rc;
+    if (!known_type(otype)) return Q8ACT_ERR_TYPE;
+    if (!attention_heads(heads_q, kv->heads, kv->dim) || !(scale > 0.0f) || scale > 3e38f || window < 0 ||
+        window > (1 << 30) || max_new < 0)
+        return Q8ACT_ERR_DIMS;
+    if ((rc = check_rows(q, ldq, (int64_t)heads_q * kv->dim, kv->type)) ||
+        (rc = check_rows(out, ldo, (int64_t)heads_q * kv->dim, otype)))
+        return rc;
+    if (!ws || ws_bytes < q8::attention_workspace_bytes(kv->dim)) return Q8ACT_ERR_WORKSPACE;
+    if (!aligned16(ws)) return Q8ACT_ERR_ALIGN;
+    const q8::DeviceInfo *dev;
+    if ((rc = current_device(&dev))) return rc;
+    const q8::AttentionArgs a{q, out, ws, ldq, ldo, otype, heads_q, window, max_new, scale};
+    return cuda_rc(q8::launch_attention(*dev, *kv, a, m, (cudaStream_t)stream));
+}
+
 // Test hook: one thread waits on an mbarrier that nothing arrives on, through the pipelines'
 // own bounded wait, until limit_ns passes; the wait then records STATUS_TIMEOUT.  Nothing
 // else is in flight (no copies, no tensor-core work), so the exit is clean.

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "q8act.h"
+
 namespace q8 {
 
 struct DeviceInfo {
@@ -148,5 +150,28 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const DeviceInfo &dev, const LogprobArgs &a, int64_t m, int64_t v, int type,
                             cudaStream_t stream);
+
+// The paged cache: rotation and append of new tokens (strides in elements; q, q_out null together; turns
+// null with rot 0: no rotation), attention of new tokens over it.
+struct AppendArgs {
+    const void *q, *k, *v;
+    void *q_out;
+    int64_t ldq, ldk, ldv, ldqo;
+    const uint64_t *turns;
+    int type, hq, rot, interleaved;
+};
+cudaError_t launch_append_kv(const DeviceInfo &dev, const q8act_paged_kv &kv, const AppendArgs &a, int64_t m,
+                             cudaStream_t stream);
+
+struct AttentionArgs {
+    const void *q;
+    void *out, *ws;
+    int64_t ldq, ldo;
+    int otype, hq, window, max_new;
+    float scale;
+};
+size_t attention_workspace_bytes(int dim);
+cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &a, int64_t m,
+                             cudaStream_t stream);
 
 }  // namespace q8
