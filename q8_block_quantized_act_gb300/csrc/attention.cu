@@ -9,8 +9,9 @@
 // the warp-level tensor-core MMA: 16 rows are too few for tcgen05's 128, and it is not what bounds.
 // Scores, statistics and sums are f32; the weights e^(s - mx) <= 1 are rounded to the cache's type for
 // the second product, whose operands have one type.
+#include <algorithm>
+
 #include "attention.cuh"
-#include "tcgen05.cuh"
 
 namespace q8 {
 namespace {
@@ -19,6 +20,7 @@ constexpr int TILE = 64;             // positions a stage
 constexpr int CONSUMERS = 4;         // warps, 16 positions each
 constexpr int THREADS = 32 * (CONSUMERS + 1);
 constexpr int ROWS = 16;
+constexpr int COUNTERS = 128;        // threads that count the units
 constexpr float NEG = -INFINITY;
 
 template <int D>
@@ -30,7 +32,7 @@ struct Cfg {
 };
 
 struct Shared {
-    PlanSmem<THREADS> plan;
+    PlanSmem<COUNTERS> plan;
     uint64_t full[8], empty[8];
     uint32_t ok[8];                       // a stage's 16-position blocks whose page exists
     float mx[2][CONSUMERS][ROWS], sum[2][CONSUMERS][ROWS];
@@ -102,9 +104,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     griddep_wait();
     griddep_launch_dependents();
-    Plan<ROWS, TILE, THREADS> plan;
+    Plan<ROWS, TILE, COUNTERS> plan;
     plan.make(a, sm.plan);                                       // and the barriers exist for all
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = sm.plan.items[THREADS];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = sm.plan.items[COUNTERS];
 
     if (warp == CONSUMERS) {
         // ------------------------------ producer ------------------------------
@@ -452,32 +454,26 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
     }
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
 }  // namespace
+
+cudaError_t launch_attention_join(const DeviceInfo &dev, const Attn &a, int dim, int rows, cudaStream_t stream)
+{
+    auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a); };
+    if (rows == ROWS) return dim == 64 ? go(attention_join_kernel<64, ROWS>) : go(attention_join_kernel<128, ROWS>);
+    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS>) : go(attention_join_kernel<128, CHUNK_ROWS>);
+}
 
 // Parts to aim at: a few for each of the two CTAs on a GB300's 152 SMs, so that uneven ones even out.
 constexpr int ROWS_TARGET = 4 * 2 * 152;
 
-// A row tile of p > 1 parts has more than (p - 1) * length >= p * length / 2 key tiles, so there are
-// fewer slots than twice the target and half as many items.
 size_t attention_workspace_bytes(int dim)
 {
-    const size_t slots = 2 * (size_t)ROWS_TARGET;
-    return 256 + up256(slots / 2 * sizeof(Item)) + up256(slots * ROWS * sizeof(float2)) + slots * ROWS * (size_t)dim * sizeof(float);
+    return std::max(attention_space(ROWS_TARGET, ROWS, dim), attention_chunk_space(dim));
 }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &s, int64_t m,
                              cudaStream_t stream)
 {
-    CUtensorMap tk, tv;
-    const CUtensorMapDataType dt = kv.type == Q8ACT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const uint64_t dims[4] = {(uint64_t)kv.dim, (uint64_t)kv.page_size, (uint64_t)kv.heads, (uint64_t)kv.pages};
-    const uint64_t strides[3] = {(uint64_t)kv.dim * 2, (uint64_t)kv.dim * 2 * kv.page_size, (uint64_t)kv.page_stride * 2};
-    const uint32_t box[4] = {64, (uint32_t)(kv.page_size < TILE ? kv.page_size : TILE), 1, 1};
-    if (!encode_4d(&tk, dt, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_4d(&tv, dt, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
     Attn a{};
     a.p = paged_of(kv, m);
     a.kc = kv.k;
@@ -489,16 +485,14 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.group = s.hq / kv.heads;
     a.otype = s.otype;
     a.window = s.window;
-    a.target = ROWS_TARGET;
-    a.least = 1;
     a.scale = s.scale * 1.4426950408889634f;
-    const size_t slots = 2 * (size_t)a.target;
-    uint8_t *ws = static_cast<uint8_t *>(s.ws);
-    a.count = reinterpret_cast<int32_t *>(ws);
-    a.items = reinterpret_cast<Item *>(ws + 256);
-    a.ml = reinterpret_cast<float2 *>(ws + 256 + up256(slots / 2 * sizeof(Item)));
-    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.ml) + up256(slots * ROWS * sizeof(float2)));
     a.status = dev.status;
+    const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
+    if (most * a.group > ROWS) return launch_attention_chunk(dev, kv, a, s.ws, stream);
+    a.least = 1;
+    attention_place(a, s.ws, ROWS_TARGET, ROWS);
+    CUtensorMap tk, tv;
+    if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     return with_type(kv.type, [&](auto x) -> cudaError_t {
         using T = decltype(x);
         if constexpr (sizeof(T) == 4) {
@@ -510,8 +504,7 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
                 cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
                 e = launch_dependent(attention_rows_kernel<T, D>, dim3(2 * dev.num_sms), THREADS, smem, stream, tk, tv, a);
-                if (e != cudaSuccess) return e;
-                return launch_dependent(attention_join_kernel<D, ROWS>, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a);
+                return e == cudaSuccess ? launch_attention_join(dev, a, D, ROWS, stream) : e;
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
         }

@@ -13,6 +13,7 @@
 
 #include "launch.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 #include "types.cuh"
 
 namespace q8 {
@@ -64,7 +65,8 @@ __device__ __forceinline__ Span span_of(const Attn &a, const Seq &s, int r0, int
 }
 
 // ---------------------------------------------------------------------------------------
-// The units of a batch, counted by the whole CTA.  Thread j counts sequences j * per ... of the batch.
+// The units of a batch, counted by the CTA's first NT threads: thread j counts sequences j * per ... of the
+// batch.  The last row tiles come first, which are the longest.
 // ---------------------------------------------------------------------------------------
 template <int NT>
 struct PlanSmem {
@@ -93,12 +95,13 @@ struct Plan {
         parts = tiles ? max(1, (span_of<TILE>(a, s, (tiles - 1) * ROWS, rows - 1).n + length - 1) / length) : 0;
     }
 
-    // Called by all NT threads.
+    // Called by all threads of the CTA.
     __device__ __forceinline__ void make(const Attn &a, PlanSmem<NT> &sm)
     {
         const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        const bool counts = t < NT;
         per = (a.p.seqs + NT - 1) / NT;
-        const int b0 = t * per, b1 = min(b0 + per, a.p.seqs);
+        const int b0 = counts ? min(t * per, a.p.seqs) : 0, b1 = counts ? min(b0 + per, a.p.seqs) : 0;
         long long w = 0;
         for (int b = b0; b < b1; ++b) {
             const Seq s = seq_of(a.p, b);
@@ -108,7 +111,7 @@ struct Plan {
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        if (lane == 0) sm.work[warp] = w;
+        if (counts && lane == 0) sm.work[warp] = w;
         __syncthreads();
         w = 0;
 #pragma unroll
@@ -137,7 +140,7 @@ struct Plan {
                 const int u = __shfl_up_sync(0xffffffffu, sum[i], o);
                 if (lane >= o) sum[i] += u;
             }
-            if (lane == 31) sm.sums[i][warp] = sum[i];
+            if (counts && lane == 31) sm.sums[i][warp] = sum[i];
         }
         __syncthreads();
 #pragma unroll
@@ -146,9 +149,11 @@ struct Plan {
             for (int j = 0; j < NT / 32; ++j)
                 if (j < warp) sum[i] += sm.sums[i][j];
         }
-        sm.units[t] = sum[0] - v[0];
-        sm.slots[t] = sum[1] - v[1];
-        sm.items[t] = sum[2] - v[2];
+        if (counts) {
+            sm.units[t] = sum[0] - v[0];
+            sm.slots[t] = sum[1] - v[1];
+            sm.items[t] = sum[2] - v[2];
+        }
         if (t == NT - 1) {
             sm.units[NT] = sum[0];
             sm.slots[NT] = sum[1];
@@ -184,8 +189,8 @@ struct Plan {
         x.parts = parts;
         x.part = left % parts;
         const int it = left / parts;
-        x.tile = it % tiles;
-        x.h = it / tiles;
+        x.tile = tiles - 1 - it / a.p.heads;
+        x.h = it % a.p.heads;
         x.slot += it * parts;
         x.item += it;
         return x;
@@ -236,5 +241,47 @@ __device__ __noinline__ void exact_values(const Attn &a, int b, int h, const T *
         for (int j = 0; j < N; ++j) acc[j] = fmaf(p, to_f32(vc[at + col(j)]), acc[j]);
     }
 }
+
+// ---------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------
+inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace for `target` parts of `rows` rows: a row tile of p > 1 parts has more than
+// (p - 1) * length >= p * length / 2 key tiles, so there are fewer slots than twice the target, and half as
+// many items.
+inline size_t attention_space(int target, int rows, int dim)
+{
+    const size_t slots = 2 * (size_t)target;
+    return 256 + up256(slots / 2 * sizeof(Item)) + up256(slots * rows * sizeof(float2)) + slots * rows * (size_t)dim * sizeof(float);
+}
+inline void attention_place(Attn &a, void *ws, int target, int rows)
+{
+    const size_t slots = 2 * (size_t)target;
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    a.target = target;
+    a.count = reinterpret_cast<int32_t *>(p);
+    a.items = reinterpret_cast<Item *>(p + 256);
+    a.ml = reinterpret_cast<float2 *>(p + 256 + up256(slots / 2 * sizeof(Item)));
+    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.ml) + up256(slots * rows * sizeof(float2)));
+}
+
+// Tensor maps of the cache, boxes of 64 values x `rows` positions of a page.
+inline bool attention_maps(const q8act_paged_kv &kv, int rows, CUtensorMap *tk, CUtensorMap *tv)
+{
+    const CUtensorMapDataType dt = kv.type == Q8ACT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t dims[4] = {(uint64_t)kv.dim, (uint64_t)kv.page_size, (uint64_t)kv.heads, (uint64_t)kv.pages};
+    const uint64_t strides[3] = {(uint64_t)kv.dim * 2, (uint64_t)kv.dim * 2 * kv.page_size, (uint64_t)kv.page_stride * 2};
+    const uint32_t box[4] = {64, (uint32_t)(kv.page_size < rows ? kv.page_size : rows), 1, 1};
+    return encode_4d(tk, dt, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_4d(tv, dt, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The kernel for chunks (attention_tc.cu): its workspace, its launch (a: all but the workspace's places), and
+// the joining kernel behind either.
+constexpr int CHUNK_ROWS = 256;
+size_t attention_chunk_space(int dim);
+cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &kv, Attn a, void *ws, cudaStream_t stream);
+cudaError_t launch_attention_join(const DeviceInfo &dev, const Attn &a, int dim, int rows, cudaStream_t stream);
 
 }  // namespace q8
