@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             const Unit x = plan.find(a, sm.plan, u);
             const int rows = x.s.n * a.group, r0 = x.tile * ROWS, r1 = min(r0 + ROWS, rows) - 1;
             const Span span = span_of<TILE>(a, x.s, r0, r1);
-            const int t0 = span.first + (int)((int64_t)span.n * x.part / x.parts);
-            const int t1 = span.first + (int)((int64_t)span.n * (x.part + 1) / x.parts);
+            int t0, t1;
+            span.part(x.part, x.parts, t0, t1);
             for (int t = t0; t < t1; ++t, ++it) {
                 const int pos = t * TILE;
                 const int64_t page = lane < per_tile ? page_of(a.p, x.b, (pos >> a.p.page_shift) + lane) : -1;
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         const Unit x = plan.find(a, sm.plan, u);
         const int rows = x.s.n * a.group, r0 = x.tile * ROWS, valid = min(ROWS, rows - r0);
         const Span span = span_of<TILE>(a, x.s, r0, r0 + valid - 1);
-        const int t0 = span.first + (int)((int64_t)span.n * x.part / x.parts);
-        const int t1 = span.first + (int)((int64_t)span.n * (x.part + 1) / x.parts);
+        int t0, t1;
+        span.part(x.part, x.parts, t0, t1);
         const int first = x.s.pos0 + r0 / a.group, last = x.s.pos0 + (r0 + valid - 1) / a.group;    // positions of its rows
 
         // Two rows a lane: g and g + 8.
@@ -483,6 +483,8 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.ldq = s.ldq;
     a.ldo = s.ldo;
     a.group = s.hq / kv.heads;
+    a.by_group = Divide(a.group);
+    a.by_heads = Divide(kv.heads);
     a.otype = s.otype;
     a.window = s.window;
     a.scale = s.scale * 1.4426950408889634f;

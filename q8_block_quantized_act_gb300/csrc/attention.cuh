@@ -23,8 +23,21 @@ struct Item {
     int slot, parts, row0, first, h, rows, unused[2];    // first: its first row among the sequence's, which start at row0
 };
 
+// Division of 0 .. 2^31 - 1 by a number that the launch fixes.
+struct Divide {
+    uint32_t by, factor, shift;
+    explicit Divide(uint32_t d = 1) : by(d)
+    {
+        shift = 0;
+        while ((1u << shift) < d) ++shift;
+        factor = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi(factor, (uint32_t)n) + (uint32_t)n) >> shift); }
+};
+
 struct Attn {
     Paged p;
+    Divide by_group, by_heads;
     const void *kc, *vc, *q;
     void *out;
     int64_t ldq, ldo;
@@ -50,12 +63,20 @@ __device__ __forceinline__ float attn_ex2(float x)
 struct Span {
     int first, n;
     int lo, hi;       // positions lo .. hi that at least one of the rows sees
+
+    // The tiles of one of so many parts: the first so many have one more.
+    __device__ __forceinline__ void part(int i, int parts, int &t0, int &t1) const
+    {
+        const int each = n / parts, more = n - each * parts;
+        t0 = first + i * each + min(i, more);
+        t1 = t0 + each + (i < more);
+    }
 };
 
 template <int TILE>
 __device__ __forceinline__ Span span_of(const Attn &a, const Seq &s, int r0, int r1)
 {
-    const int i0 = r0 / a.group, i1 = r1 / a.group;
+    const int i0 = a.by_group(r0), i1 = a.by_group(r1);
     Span t;
     t.hi = min(s.pos0 + i1, s.end - 1);
     t.lo = a.window ? max(s.pos0 + i0 - a.window + 1, 0) : 0;
@@ -189,8 +210,8 @@ struct Plan {
         x.parts = parts;
         x.part = left % parts;
         const int it = left / parts;
-        x.tile = tiles - 1 - it / a.p.heads;
-        x.h = it % a.p.heads;
+        x.tile = tiles - 1 - a.by_heads(it);
+        x.h = it - a.by_heads(it) * a.p.heads;
         x.slot += it * parts;
         x.item += it;
         return x;

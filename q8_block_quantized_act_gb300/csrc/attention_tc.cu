@@ -8,8 +8,8 @@
 //   warps 0-3, 4-7  a row tile each: a thread a row, so maxima and sums need no exchange
 //   warp 8          issues the MMAs: P0 V, Q0 K', P1 V, Q1 K' (K' the next tile's keys)
 //   warp 9          brings pages of keys and values to shared memory (TMA, 128-byte swizzled)
-//   warps 10, 11    values of tiles that some row does not see as a whole: clear those that no row sees, look
-//                   for infinities and NaN among the others (attention.cuh)
+//   warps 10, 11    bring a row tile's queries each; in tiles of values that some row does not see as a whole they
+//                   clear those that no row sees and look for infinities and NaN among the others (attention.cuh)
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
 #include <algorithm>
@@ -25,6 +25,7 @@ constexpr int ROWS = CHUNK_ROWS;         // of a unit: two row tiles
 constexpr int COUNTERS = 64;             // threads that count the units
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;      // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
+constexpr int PARTS = 2;                 // of a tile's weights, handed to the MMAs one by one
 constexpr float NEG = -INFINITY;
 constexpr float SLACK = 8.0f;
 
@@ -35,7 +36,7 @@ struct Cfg {
     static constexpr int STAGES = 160 * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                      // columns of 128 bytes
     static constexpr int HALF_BYTES = TILE * 128;
-    static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * STAGE_BYTES;
+    static constexpr int STAGES_END = 2 * Q_BYTES + STAGES * STAGE_BYTES;
     static constexpr uint32_t COL_S = 0, COL_O = 2 * TILE;     // tensor memory: S0 S1 O0 O1
     // Instruction descriptor, kind::f16: D f32 (bits 4-5), types of A and B (7-9, 10-12), B's major (16; 1: its
     // rows are K), N >> 3 (17-22), M >> 4 (24-28).
@@ -47,7 +48,8 @@ struct Cfg {
 struct Shared {
     PlanSmem<COUNTERS> plan;
     uint64_t full[10], empty[10], fixed[10];         // stages; fixed: a tile of values that warps 10, 11 have seen
-    uint64_t s_full[2], p_full[2], q_full[2], o_full[2], drained;
+    uint64_t s_full[2], p_full[2][PARTS], q_full[2], q_empty[2], o_full[2], drained;
+    uint32_t pages[8];                               // tile n of the CTA in word n % 8: its 16-position blocks whose page exists
     uint32_t tmem;
     // Unit n of the CTA, counting those with positions, has a non-finite value that not all rows see: n + 1 in word
     // n % 16.  Warps 10 and 11 are ahead of the softmax by the stages' tiles at most, 5 and one.
@@ -101,6 +103,14 @@ __device__ __forceinline__ void wait_ld(float *r)
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *u)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+          "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *u)
 {
     asm volatile(
@@ -114,6 +124,29 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *u)
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 16 bytes from global to shared memory, of which the first `bytes` are read and the others zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// 32 consecutive values, rounded to `type`.
+__device__ __forceinline__ void store32(void *p, int type, const float (&v)[32])
+{
+    if (type == Q8ACT_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) static_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[8 * j + i];
+        static_cast<uint4 *>(p)[j] = type == Q8ACT_F16 ? pack<__half>(w) : pack<__nv_bfloat16>(w);
+    }
+}
+
 // A unit's tiles: [t0, t1), and those that row tile q sees, [a[q], b[q]).
 struct Range {
     int t0, t1, a[2], b[2];
@@ -124,12 +157,11 @@ struct Range {
     {
         const int rows = x.s.n * at.group, r0 = x.tile * ROWS, r1 = min(r0 + ROWS, rows) - 1;
         const Span s = span_of<TILE>(at, x.s, r0, r1);
-        t0 = s.first + (int)((int64_t)s.n * x.part / x.parts);
-        t1 = s.first + (int)((int64_t)s.n * (x.part + 1) / x.parts);
+        s.part(x.part, x.parts, t0, t1);
         lo = s.lo;
         hi = s.hi;
-        first = x.s.pos0 + r0 / at.group;
-        last = x.s.pos0 + r1 / at.group;
+        first = x.s.pos0 + at.by_group(r0);
+        last = x.s.pos0 + at.by_group(r1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int q0 = r0 + q * QROWS;
@@ -140,6 +172,13 @@ struct Range {
                 b[q] = max(a[q], min(t1, z.first + z.n));
             }
         }
+    }
+    // The same in all lanes to the compiler too: the MMA warp's loops then stay in uniform registers.
+    __device__ __forceinline__ void uniform()
+    {
+        int *v[] = {&t0, &t1, &a[0], &a[1], &b[0], &b[1], &lo, &hi, &first, &last};
+#pragma unroll
+        for (int *i : v) *i = __shfl_sync(0xffffffffu, *i, 0);
     }
     // Whether some row does not see some of a tile.
     __device__ __forceinline__ bool masked(const Attn &at, int t) const
@@ -155,6 +194,19 @@ __device__ __forceinline__ int64_t unit_of(int round)
     return (int64_t)round * g + (round & 1 ? g - 1 - c : c);
 }
 
+// Columns c0 .. c0 + 31 of a row's sums, taken again (attention.cuh).
+template <typename T, int D>
+__device__ __noinline__ void exact_part(const Attn &a, const Plan<ROWS, TILE, COUNTERS> &plan, const PlanSmem<COUNTERS> &sm, int u,
+                                        int row, int c0, float mx, float (&o)[32])
+{
+    const Unit x = plan.find(a, sm, u);
+    const Range rg(a, x);
+    const int r = x.tile * ROWS + row, tok = a.by_group(r), pos = x.s.pos0 + tok;
+    const int k0 = max(a.window ? pos - a.window + 1 : 0, rg.t0 * TILE), k1 = min(min(pos, x.s.end - 1), rg.t1 * TILE - 1);
+    exact_values<T, D>(a, x.b, x.h, static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D,
+                       k0, k1, mx == NEG ? 0.0f : mx, [&](int j) { return c0 + j; }, o);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
@@ -163,16 +215,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int STAGES = C::STAGES;
     constexpr uint32_t IDESC_QK = C::IDESC_QK | (BF16 ? C::IDESC_BF16 : 0), IDESC_PV = C::IDESC_PV | (BF16 ? C::IDESC_BF16 : 0);
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *stages = smem + 2 * C::Q_BYTES;
-    __shared__ Shared sm;
+    Shared &sm = *reinterpret_cast<Shared *>(smem + C::STAGES_END);
     volatile int *abort_flag = &sm.abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 3); mbar_init(&sm.fixed[s], 2); }
-        for (int q = 0; q < 2; ++q) { mbar_init(&sm.s_full[q], 1); mbar_init(&sm.p_full[q], 4); mbar_init(&sm.q_full[q], 4); mbar_init(&sm.o_full[q], 1); }
+        for (int q = 0; q < 2; ++q) {
+            mbar_init(&sm.s_full[q], 1);
+            for (int i = 0; i < PARTS; ++i) mbar_init(&sm.p_full[q][i], 4);
+            mbar_init(&sm.q_full[q], 1);
+            mbar_init(&sm.q_empty[q], 1);
+            mbar_init(&sm.o_full[q], 1);
+        }
         mbar_init(&sm.drained, 1);
         for (int i = 0; i < 16; ++i) sm.spoilt[i] = 0;
         sm.abort_flag = 0;
@@ -198,96 +255,92 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp >> 2, row = (warp & 3) * 32 + lane;         // of the row tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // the warp's lanes of tensor memory
         const uint32_t col_s = tmem + lanes + C::COL_S + q * TILE, col_o = tmem + lanes + C::COL_O + q * D;
-        uint8_t *qs = smem + q * C::Q_BYTES;
-        uint32_t s_phase = 0, o_phase = 0, n = 0;
+        uint32_t s_phase = 0, o_phase = 0, n = 0, tiles = 0;
         bool ok = true;
         for (int round = 0; ok; ++round) {
             const int64_t u = unit_of(round);
             if (u >= plan.total) break;
-            const Unit x = plan.find(a, sm.plan, (int)u);
-            const Range rg(a, x);
-            const int rows = x.s.n * a.group, r0 = x.tile * ROWS + q * QROWS;
-            const bool some = rg.b[q] > rg.a[q];
-            const bool live = r0 + row < rows;
-            const int tok = live ? (r0 + row) / a.group : 0, head = x.h * a.group + (live ? (r0 + row) % a.group : 0);
-            const int pos = x.s.pos0 + tok;
-            const int hi = live ? min(pos, x.s.end - 1) : INT_MAX, lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
-            float mx = NEG, sum = 0.0f;
-            if (some) {
-                // Queries: 8 or 16 lanes a row, rows behind the last one as zeros.
-                constexpr int VECS = D / 8;                  // 16-byte vectors of a row
-#pragma unroll 4
-                for (int i = lane; i < 32 * VECS; i += 32) {
-                    const int rr = (warp & 3) * 32 + i / VECS, v = i % VECS, r = r0 + rr;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (x.s.row0 + r / a.group) * a.ldq +
-                                                                  (x.h * a.group + r % a.group) * D) + v);
-                    *reinterpret_cast<uint4 *>(qs + (v >> 3) * (QROWS * 128) + rr * 128 + (((v & 7) ^ (rr & 7)) << 4)) = w;
+            int t, end, count, from, hi, lo;       // tiles from t to end of the unit's `count`, positions that the row sees
+            int64_t out_at, slot = -1;             // the row in `out`, and in the partial results
+            bool some, live;
+            {
+                const Unit x = plan.find(a, sm.plan, (int)u);
+                const Range rg(a, x);
+                const int rows = x.s.n * a.group, r = x.tile * ROWS + q * QROWS + row;
+                t = rg.a[q];
+                end = rg.b[q];
+                count = rg.t1 - rg.t0;
+                some = end > t;
+                live = r < rows;
+                const int tok = live ? a.by_group(r) : 0, pos = x.s.pos0 + tok;
+                hi = live ? min(pos, x.s.end - 1) : INT_MAX;
+                lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
+                out_at = (x.s.row0 + tok) * a.ldo + (x.h * a.group + (live ? r - tok * a.group : 0)) * D;
+                if (x.parts > 1) {
+                    slot = (int64_t)(x.slot + x.part) * ROWS + q * QROWS + row;
+                    if (x.part == 0 && threadIdx.x == 0)
+                        a.items[x.item] = Item{x.slot, x.parts, x.s.row0, x.tile * ROWS, x.h, min(ROWS, rows - x.tile * ROWS), {0, 0}};
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_full[q]);
-                // Pages that do not exist, among all that the unit reads.
-                const int e0 = (rg.a[q] * TILE) >> a.p.page_shift, e1 = (min(rg.b[q] * TILE, x.s.end) - 1 >> a.p.page_shift) + 1;
-                bool bad = false;
-                for (int e = e0 + lane; e < e1; e += 32) bad |= page_of(a.p, x.b, e) < 0;
-                bad = __any_sync(0xffffffffu, bad);
-
-                for (int t = rg.a[q]; t < rg.b[q]; ++t) {
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[q], s_phase, a.status, abort_flag));
-                    if (!ok) break;
-                    s_phase ^= 1;
-                    tc_fence_after();
-                    float s[TILE];
+                tiles -= rg.t0;                    // tile t of the sequence is tile tiles + t of the CTA
+                from = rg.t0;
+            }
+            bool first = true;
+            const bool some_tiles = count > 0;
+            float mx = NEG, sum = 0.0f;
+            for (; t < end; ++t) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[q], s_phase, a.status, abort_flag));
+                if (!ok) break;
+                s_phase ^= 1;
+                tc_fence_after();
+                float s[TILE];
 #pragma unroll
-                    for (int i = 0; i < TILE / 32; ++i) ld32(col_s + 32 * i, s + 32 * i);
-                    wait_ld<TILE>(s);
-                    const int k0 = t * TILE;
-                    if (__any_sync(0xffffffffu, k0 + TILE - 1 > hi || k0 < lo)) {
-                        const int from = lo - k0, to = hi - k0;
+                for (int i = 0; i < TILE / 32; ++i) ld32(col_s + 32 * i, s + 32 * i);
+                const int k0 = t * TILE;
+                const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(tiles + t) & 7]);
+                const bool edge = __any_sync(0xffffffffu, k0 + TILE - 1 > hi || k0 < lo) || pages != 0xff;
+                wait_ld<TILE>(s);
+                if (edge) {
+                    const int from = lo - k0, to = hi - k0;
 #pragma unroll
-                        for (int j = 0; j < TILE; ++j)
-                            if (j < from || j > to) s[j] = NEG;
+                    for (int j = 0; j < TILE; ++j)
+                        if (j < from || j > to || !(pages >> (j / 16) & 1)) s[j] = NEG;
+                }
+                float m4[4] = {NEG, NEG, NEG, NEG};
+#pragma unroll
+                for (int j = 0; j < TILE; j += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[j + 2 * i]), s[j + 2 * i + 1]);
+                const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale);
+                if (first) {
+                    mx = m;
+                    first = false;
+                } else if (__any_sync(0xffffffffu, m > mx + SLACK)) {
+                    // (mx may be -inf: nothing seen so far, O and the sum are zeros)
+                    const float f = attn_ex2(mx - (m == NEG ? 0.0f : m));
+                    sum *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        float o[32];
+                        ld32(col_o + 32 * i, o);
+                        wait_ld<32>(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] *= f;
+                        st32(col_o + 32 * i, reinterpret_cast<const uint32_t *>(o));
                     }
-                    if (bad) {
-                        const int ps = a.p.page_shift, first = k0 >> ps;
-                        const uint32_t good = __ballot_sync(
-                            0xffffffffu, lane < TILE / 16 && page_of(a.p, x.b, ps >= 7 ? first : first + (lane >> (ps - 4))) >= 0);
+                    mx = m;
+                }
+                const float base = mx == NEG ? 0.0f : mx;
+                const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
+                float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int j = 0; j < TILE; ++j)
-                            if (!(good >> (j / 16) & 1)) s[j] = NEG;
-                    }
-                    float m4[4] = {s[0], s[1], s[2], s[3]};
+                for (int i = 0; i < PARTS; ++i) {
 #pragma unroll
-                    for (int j = 4; j < TILE; ++j) m4[j & 3] = fmaxf(m4[j & 3], s[j]);
-                    const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale);
-                    if (t == rg.a[q]) {
-                        mx = m;
-                    } else if (__any_sync(0xffffffffu, m > mx + SLACK)) {
-                        // (mx may be -inf: nothing seen so far, O and the sum are zeros)
-                        const float f = attn_ex2(mx - (m == NEG ? 0.0f : m));
-                        sum *= f;
+                    for (int h = 0; h < 4 / PARTS; ++h) {
+                        const int at = 32 * (4 / PARTS * i + h);
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            float o[32];
-                            ld32(col_o + 32 * i, o);
-                            wait_ld<32>(o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= f;
-                            st32(col_o + 32 * i, reinterpret_cast<const uint32_t *>(o));
-                        }
-                        mx = m;
-                    }
-                    const float base = mx == NEG ? 0.0f : mx;
-                    const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
-                    float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int i = 0; i < TILE / 64; ++i) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float2 e = __ffma2_rn(make_float2(s[64 * i + 2 * j], s[64 * i + 2 * j + 1]), scale2, base2);
+                        for (int j = 0; j < 16; ++j) {
+                            float2 e = __ffma2_rn(make_float2(s[at + 2 * j], s[at + 2 * j + 1]), scale2, base2);
                             e = make_float2(attn_ex2(e.x), attn_ex2(e.y));
                             sum2[j & 1] = __fadd2_rn(sum2[j & 1], e);
                             if constexpr (BF16) {
@@ -298,28 +351,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 p[j] = *reinterpret_cast<const uint32_t *>(&h);
                             }
                         }
-                        st32(col_s + 32 * i, p);
+                        st16(col_s + at / 2, p);
                     }
                     wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[q]);
-                    sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+                    if (lane == 0) mbar_arrive(&sm.p_full[q][i]);
                 }
+                sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+            }
+            tiles += count + from;
+            if (some) {
                 if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[q], o_phase, a.status, abort_flag));
                 o_phase ^= 1;
                 tc_fence_after();
             }
             // What warps 10 and 11 have found was written before the unit's last values went to the MMAs.
             const bool spoilt = some && *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) == n + 1;
-            n += rg.t1 > rg.t0;
+            n += some_tiles;
             if (ok) {
-                const float base = mx == NEG ? 0.0f : mx;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;         // a row that sees nothing: 0
-                const int64_t at = (int64_t)(x.slot + x.part) * ROWS + q * QROWS + row;
-                uint8_t *dst = static_cast<uint8_t *>(a.out) + ((x.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
-                if (x.parts > 1 && live) a.ml[at] = make_float2(mx, sum);
-#pragma unroll 1
+                if (slot >= 0 && live) a.ml[slot] = make_float2(mx, sum);
+#pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     float o[32];
                     if (some) {
@@ -330,26 +383,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < 32; ++j) o[j] = 0.0f;
                     }
                     if (spoilt && live) {
-                        const int k0 = max(a.window ? pos - a.window + 1 : 0, rg.t0 * TILE), k1 = min(min(pos, x.s.end - 1), rg.t1 * TILE - 1);
-                        exact_values<T, D>(a, x.b, x.h, static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + head * D, k0, k1,
-                                           base, [&](int j) { return 32 * i + j; }, o);
+                        float e[32];
+                        exact_part<T, D>(a, plan, sm.plan, (int)u, q * QROWS + row, 32 * i, mx, e);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = e[j];
                     }
-                    if (live) {
-                        if (x.parts > 1) {
+                    if (live && slot >= 0) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(a.part + at * D + 32 * i + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                        } else {
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(a.part + slot * D + 32 * i + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    } else if (live) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                store4(dst + (32 * i + j) * out_size(a.otype), a.otype,
-                                       make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv));
-                        }
+                        for (int j = 0; j < 32; ++j) o[j] *= inv;
+                        store32(static_cast<uint8_t *>(a.out) + (out_at + 32 * i) * out_size(a.otype), a.otype, o);
                     }
                     __syncwarp();
                 }
-                if (x.parts > 1 && x.part == 0 && threadIdx.x == 0)
-                    a.items[x.item] = Item{x.slot, x.parts, x.s.row0, x.tile * ROWS, x.h, min(ROWS, rows - x.tile * ROWS), {0, 0}};
             }
         }
     } else {
@@ -374,8 +423,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int round = 0; ok; ++round) {
                 const int64_t u = unit_of(round);
                 if (u >= plan.total) break;
-                const Unit x = plan.find(a, sm.plan, (int)u);
-                const Range rg(a, x);
+                Range rg(a, plan.find(a, sm.plan, (int)u));
+                rg.uniform();
                 // S = Q K^T of the tile at stage st.
                 auto scores = [&](int q, int t) {
                     if (t < rg.a[q] || t >= rg.b[q] || !ok) return;
@@ -385,30 +434,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!ok) return;
                     }
                     tc_fence_after();
+                    const uint64_t kd = kdesc + (uint32_t)(__shfl_sync(0xffffffffu, st, 0) * (C::STAGE_BYTES >> 4));
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
                             mma_ss(tmem + C::COL_S + q * TILE, qdesc + ((q * C::Q_BYTES + (i >> 2) * (QROWS * 128) + (i & 3) * 32) >> 4),
-                                   kdesc + ((st * C::STAGE_BYTES + (i >> 2) * C::HALF_BYTES + (i & 3) * 32) >> 4),
+                                   kd + ((i >> 2) * C::HALF_BYTES + (i & 3) * 32 >> 4),
                                    IDESC_QK, i > 0);
                         tc_commit(&sm.s_full[q]);
+                        if (t + 1 == rg.b[q]) tc_commit(&sm.q_empty[q]);
                     }
                     __syncwarp();
                 };
                 auto weighted = [&](int q, int t, int vst) {
                     if (t < rg.a[q] || t >= rg.b[q] || !ok) return;
-                    wait(&sm.p_full[q], p_phase >> q & 1);
-                    p_phase ^= 1u << q;
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
+                    const uint64_t vd = vdesc + (uint32_t)(__shfl_sync(0xffffffffu, vst, 0) * (C::STAGE_BYTES >> 4));
+                    const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)(t > rg.a[q]), 0);
 #pragma unroll
-                        for (int i = 0; i < TILE / 16; ++i)
-                            mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_S + q * TILE + 8 * i,
-                                   vdesc + ((vst * C::STAGE_BYTES + i * 2048) >> 4), IDESC_PV, t > rg.a[q] || i > 0);
-                        if (t + 1 == rg.b[q]) tc_commit(&sm.o_full[q]);
+                    for (int part = 0; part < PARTS; ++part) {
+                        constexpr int N = TILE / 16 / PARTS;
+                        wait(&sm.p_full[q][part], p_phase >> q & 1);
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = N * part; i < N * part + N; ++i)
+                                mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_S + q * TILE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
+                                       i > 0 ? 1u : more);
+                            if (part == PARTS - 1 && t + 1 == rg.b[q]) tc_commit(&sm.o_full[q]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    p_phase ^= 1u << q;
                 };
                 auto release = [&](int stage) {
                     if (ok && elect_one()) tc_commit(&sm.empty[stage]);
@@ -452,7 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------ loader ------------------------------
             const int ps = 1 << a.p.page_shift, per_tile = ps < TILE ? TILE / ps : 1;
             int it = 0, st = 0;
-            uint32_t phase = 1;
+            uint32_t phase = 1, tiles = 0;
             bool ok = true;
             for (int round = 0; ok; ++round) {
                 const int64_t u = unit_of(round);
@@ -464,11 +521,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int pos = t * TILE;
                     // A page that does not exist: a box outside the tensor, which reads as zeros.
                     const int id = page < 0 ? (int)a.p.pages : (int)page;
+                    const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+                    uint32_t pages = 0;
+                    for (int j = 0; j < per_tile; ++j)
+                        if (good >> j & 1) pages |= ((1u << (8 / per_tile)) - 1) << (j * (8 / per_tile));
                     if (t + 1 < rg.t1 && lane < per_tile) page = page_of(a.p, x.b, ((pos + TILE) >> a.p.page_shift) + lane);
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         ok = __all_sync(0xffffffffu, wait_or_abort(&sm.empty[st], phase, a.status, abort_flag));
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], C::STAGE_BYTES);
+                        if (lane == 0) {
+                            if (kv == 0) *const_cast<volatile uint32_t *>(&sm.pages[tiles++ & 7]) = pages;
+                            mbar_arrive_expect_tx(&sm.full[st], C::STAGE_BYTES);
+                        }
                         __syncwarp();
                         const int j = lane / C::HALVES, half = lane % C::HALVES;
                         const int box_page = __shfl_sync(0xffffffffu, id, j & 31);
@@ -489,15 +553,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
             // ------------------------------ masked values ------------------------------
             constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
-            const int half_warp = warp - 10;
+            const int q = warp - 10;                 // row tile whose queries it brings, half of a tile that it looks at
             int st = 0;
-            uint32_t phase = 0, n = 0;
+            uint32_t phase = 0, q_phase = 1, n = 0;
             bool ok = true;
             for (int round = 0; ok; ++round) {
                 const int64_t u = unit_of(round);
                 if (u >= plan.total) break;
                 const Unit x = plan.find(a, sm.plan, (int)u);
                 const Range rg(a, x);
+                if (rg.b[q] > rg.a[q]) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[q], q_phase, a.status, abort_flag));
+                    if (!ok) break;
+                    q_phase ^= 1;
+                    // Rows behind the last one as zeros.
+                    const int rows = x.s.n * a.group, r0 = x.tile * ROWS + q * QROWS;
+                    constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
+                    const uint32_t dst0 = smem_u32(smem + q * C::Q_BYTES);
+#pragma unroll 1
+                    for (int i = 0; i < QROWS; i += 32) {
+                        const int r = r0 + i + lane, tok = a.by_group(r);
+                        const int64_t off = r < rows ? (x.s.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D : -1;
+#pragma unroll 8
+                        for (int j = 0; j < 32; j += AT_ONCE) {
+                            const int rr = i + j + lane / VECS, v = lane % VECS;
+                            const int64_t o = __shfl_sync(0xffffffffu, off, j + lane / VECS);
+                            cp_async16(dst0 + (v >> 3) * (QROWS * 128) + rr * 128 + (((v & 7) ^ (rr & 7)) << 4),
+                                       static_cast<const T *>(a.q) + (o < 0 ? 0 : o) + v * 8, o < 0 ? 0 : 16);
+                        }
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_full[q]);
+                }
                 // Every stage is waited for and handed back, so that these warps keep the pipeline's pace.
                 for (int i = 0; i < 2 * (rg.t1 - rg.t0); ++i) {
                     const int t = rg.t0 + (i >> 1);
@@ -507,7 +596,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         bool found = false;
                         uint8_t *v = stages + st * C::STAGE_BYTES;
 #pragma unroll 4
-                        for (int j = half_warp * 32 + lane; j < C::STAGE_BYTES / 16; j += 64) {
+                        for (int j = q * 32 + lane; j < C::STAGE_BYTES / 16; j += 64) {
                             const int key = t * TILE + (j >> 3) % TILE;          // 8 vectors a position and half
                             uint4 *p = reinterpret_cast<uint4 *>(v) + j;
                             if (key < rg.lo || key > rg.hi) {
@@ -561,9 +650,11 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
         } else {
             auto go = [&](auto d) -> cudaError_t {
                 constexpr int D = decltype(d)::value;
-                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, Cfg<D>::SMEM);
+                constexpr size_t smem = Cfg<D>::STAGES_END + sizeof(Shared);
+                static_assert(smem <= 227 * 1024, "shared memory");
+                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, Cfg<D>::SMEM, stream, tk, tv, a);
+                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, smem, stream, tk, tv, a);
                 return e == cudaSuccess ? launch_attention_join(dev, a, D, ROWS, stream) : e;
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
