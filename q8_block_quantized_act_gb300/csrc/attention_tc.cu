@@ -47,7 +47,10 @@ struct Cfg {
 
 struct Shared {
     PlanSmem<COUNTERS> plan;
-    uint64_t full[10], empty[10], fixed[10];         // stages; fixed: a tile of values that warps 10, 11 have seen
+    uint64_t full[10], empty[10];                    // stages
+    // Tile n of the CTA, in barrier n % 8: its values, and the next tile's keys, are there.  The stages hold five tiles
+    // at most, so six barriers would do.
+    uint64_t ready[8];
     uint64_t s_full[2], p_full[2][PARTS], q_full[2], q_empty[2], o_full[2], drained;
     uint32_t pages[8];                               // tile n of the CTA in word n % 8: its 16-position blocks whose page exists
     uint32_t tmem;
@@ -222,7 +225,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 3); mbar_init(&sm.fixed[s], 2); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 3); }
+        for (int i = 0; i < 8; ++i) mbar_init(&sm.ready[i], 2);
         for (int q = 0; q < 2; ++q) {
             mbar_init(&sm.s_full[q], 1);
             for (int i = 0; i < PARTS; ++i) mbar_init(&sm.p_full[q][i], 4);
@@ -405,14 +409,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp == 8) {
             // ------------------------------ MMA issuer ------------------------------
-            uint32_t q_phase = 0, p_phase = 0, fixed_phase = 0;     // a bit a row tile, a row tile, a stage
+            uint32_t q_phase = 0, p_phase = 0, tiles = 0;           // a bit a row tile; tiles so far
             int st = 0;
             uint32_t phase = 0;
             bool ok = true;
             const uint64_t qdesc = smem_desc_sw128(smem_u32(smem)), kdesc = smem_desc_sw128(smem_u32(stages));
             const uint64_t vdesc = smem_desc_mn_sw128(smem_u32(stages), C::HALF_BYTES);
+            // This warp's instructions pace the tensor cores (it shares its scheduler with softmax warps), so a wait
+            // that is over takes one look, and there are few of them.
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, a.status, abort_flag));
+                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+                    ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, a.status, abort_flag));
+                return ok;
             };
             auto next = [&] {
                 if (++st == STAGES) {
@@ -420,83 +428,73 @@ __global__ void __launch_bounds__(THREADS, 1)
                     phase ^= 1;
                 }
             };
+            auto at = [&](uint64_t desc, int stage) { return desc + (uint32_t)(__shfl_sync(0xffffffffu, stage, 0) * (C::STAGE_BYTES >> 4)); };
             for (int round = 0; ok; ++round) {
                 const int64_t u = unit_of(round);
                 if (u >= plan.total) break;
                 Range rg(a, plan.find(a, sm.plan, (int)u));
                 rg.uniform();
-                // S = Q K^T of the tile at stage st.
-                auto scores = [&](int q, int t) {
-                    if (t < rg.a[q] || t >= rg.b[q] || !ok) return;
+                if (rg.t0 == rg.t1) continue;
+                // S = Q K^T of the tile whose keys are at kd.
+                auto scores = [&](int q, int t, uint64_t kd) {
+                    if (t < rg.a[q] || t >= rg.b[q]) return true;
                     if (t == rg.a[q]) {
-                        wait(&sm.q_full[q], q_phase >> q & 1);
+                        if (!wait(&sm.q_full[q], q_phase >> q & 1)) return false;
                         q_phase ^= 1u << q;
-                        if (!ok) return;
                     }
                     tc_fence_after();
-                    const uint64_t kd = kdesc + (uint32_t)(__shfl_sync(0xffffffffu, st, 0) * (C::STAGE_BYTES >> 4));
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
                             mma_ss(tmem + C::COL_S + q * TILE, qdesc + ((q * C::Q_BYTES + (i >> 2) * (QROWS * 128) + (i & 3) * 32) >> 4),
-                                   kd + ((i >> 2) * C::HALF_BYTES + (i & 3) * 32 >> 4),
-                                   IDESC_QK, i > 0);
+                                   kd + ((i >> 2) * C::HALF_BYTES + (i & 3) * 32 >> 4), IDESC_QK, i > 0);
                         tc_commit(&sm.s_full[q]);
                         if (t + 1 == rg.b[q]) tc_commit(&sm.q_empty[q]);
                     }
                     __syncwarp();
+                    return true;
                 };
-                auto weighted = [&](int q, int t, int vst) {
-                    if (t < rg.a[q] || t >= rg.b[q] || !ok) return;
-                    const uint64_t vd = vdesc + (uint32_t)(__shfl_sync(0xffffffffu, vst, 0) * (C::STAGE_BYTES >> 4));
-                    const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)(t > rg.a[q]), 0);
+                auto weighted = [&](int q, int t, uint64_t vd) {
+                    if (t < rg.a[q] || t >= rg.b[q]) return true;
+                    const uint32_t add = t > rg.a[q];
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         constexpr int N = TILE / 16 / PARTS;
-                        wait(&sm.p_full[q][part], p_phase >> q & 1);
-                        if (!ok) return;
+                        if (!wait(&sm.p_full[q][part], p_phase >> q & 1)) return false;
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
                             for (int i = N * part; i < N * part + N; ++i)
                                 mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_S + q * TILE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
-                                       i > 0 ? 1u : more);
+                                       i > 0 ? 1u : add);
                             if (part == PARTS - 1 && t + 1 == rg.b[q]) tc_commit(&sm.o_full[q]);
                         }
                         __syncwarp();
                     }
                     p_phase ^= 1u << q;
+                    return true;
                 };
                 auto release = [&](int stage) {
-                    if (ok && elect_one()) tc_commit(&sm.empty[stage]);
+                    if (elect_one()) tc_commit(&sm.empty[stage]);
                     __syncwarp();
                 };
-                if (rg.t0 < rg.t1) {
-                    wait(&sm.full[st], phase);
-                    scores(0, rg.t0);
-                    scores(1, rg.t0);
-                    release(st);
-                    next();
-                }
-                for (int t = rg.t0; ok && t < rg.t1; ++t) {
+                if (!wait(&sm.full[st], phase) || !scores(0, rg.t0, at(kdesc, st)) || !scores(1, rg.t0, at(kdesc, st))) break;
+                release(st);
+                next();
+                for (int t = rg.t0; t < rg.t1; ++t, ++tiles) {
                     const int vst = st;
-                    wait(&sm.full[st], phase);
-                    if (rg.masked(a, t)) {
-                        wait(&sm.fixed[st], fixed_phase >> st & 1);
-                        fixed_phase ^= 1u << st;
-                    }
                     next();
-                    weighted(0, t, vst);
-                    if (t + 1 < rg.t1) {
-                        wait(&sm.full[st], phase);
-                        scores(0, t + 1);
-                    }
-                    weighted(1, t, vst);
+                    const int kst = st;
+                    const bool more = t + 1 < rg.t1;
+                    if (more) next();
+                    const uint64_t vd = at(vdesc, vst), kd = at(kdesc, kst);
+                    if (!wait(&sm.ready[tiles & 7], tiles >> 3 & 1) || !weighted(0, t, vd)) break;
+                    if (more && !scores(0, t + 1, kd)) break;
+                    if (!weighted(1, t, vd)) break;
                     release(vst);
-                    if (t + 1 < rg.t1) {
-                        scores(1, t + 1);
-                        release(st);
-                        next();
+                    if (more) {
+                        if (!scores(1, t + 1, kd)) break;
+                        release(kst);
                     }
                 }
             }
@@ -555,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
             const int q = warp - 10;                 // row tile whose queries it brings, half of a tile that it looks at
             int st = 0;
-            uint32_t phase = 0, q_phase = 1, n = 0;
+            uint32_t phase = 0, q_phase = 1, n = 0, tiles = 0;
             bool ok = true;
             for (int round = 0; ok; ++round) {
                 const int64_t u = unit_of(round);
@@ -610,11 +608,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         if (found) *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) = n + 1;
                         fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.fixed[st]);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.empty[st]);
+                    if (lane == 0) {
+                        // Values and the next keys are there (the last values: no keys follow).
+                        if (i > 0 && (!(i & 1) || t + 1 == rg.t1)) mbar_arrive(&sm.ready[tiles++ & 7]);
+                        mbar_arrive(&sm.empty[st]);
+                    }
                     if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
