@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         const Span span = span_of<TILE>(a, x.s, r0, r0 + valid - 1);
         int t0, t1;
         span.part(x.part, x.parts, t0, t1);
-        const int first = x.s.pos0 + r0 / a.group, last = x.s.pos0 + (r0 + valid - 1) / a.group;    // positions of its rows
+        const int first = x.s.pos0 + a.by_group(r0), last = x.s.pos0 + a.by_group(r0 + valid - 1);    // positions of its rows
 
         // Two rows a lane: g and g + 8.
         uint32_t q[D / 16][4];
@@ -179,12 +179,12 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int i = 0; i < 2; ++i) {
             const int r = r0 + g + 8 * i;
             const bool live = r < rows;
-            const int tok = live ? r / a.group : 0;
+            const int tok = live ? a.by_group(r) : 0;
             const int pos = x.s.pos0 + tok;
             hi[i] = live ? min(pos, x.s.end - 1) : -1;
             lo[i] = a.window ? max(pos - a.window + 1, 0) : 0;
             const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + (x.h * a.group + (live ? r % a.group : 0)) * D) + c;
+                static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + (x.h * a.group + (live ? r - tok * a.group : 0)) * D) + c;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 q[kk][i] = live ? __ldg(src + kk * 8) : 0u;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                             acc[4 * j + 3] += v.w;
                         }
                 }
-                const int row = r0 + r, tok = row / a.group, head = x.h * a.group + row % a.group;
+                const int row = r0 + r, tok = a.by_group(row), head = x.h * a.group + row - tok * a.group;
                 const int *sp = sm.spoilt[flip];
                 if (sp[0] | sp[1] | sp[2] | sp[3]) {
                     const int pos = x.s.pos0 + tok;
@@ -386,71 +386,84 @@ __global__ void __launch_bounds__(THREADS, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// Row tiles in several parts: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i, a row a CTA, the
-// parts shared by its warps and added in their order.
+// Row tiles in several parts: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i, added in the parts' order.
+// Few rows come in many parts (decoding), which W warps of a CTA share; many rows in few, a row a warp.
 // ---------------------------------------------------------------------------------------
 constexpr int JOIN_WARPS = 4;
 
-template <int D, int ROWS_>
+template <int D, int ROWS_, int W>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
 {
     constexpr int V = D / 32;                // values a lane
-    __shared__ float acc[JOIN_WARPS][D], mw[JOIN_WARPS], lw[JOIN_WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float acc[W > 1 ? W : 1][D], mw[W], lw[W];
+    const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
     griddep_enter();
-    const int64_t work = (int64_t)*a.count * ROWS_;
-    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-        const int n = (int)(work / ROWS_), r = (int)(i / n);
-        const Item it = a.items[i % n];
+    const int n = *a.count;
+    const int64_t work = (int64_t)n * ROWS_, step = (int64_t)gridDim.x * (JOIN_WARPS / W);
+    for (int64_t i = (int64_t)blockIdx.x * (JOIN_WARPS / W) + (W > 1 ? 0 : threadIdx.x >> 5); i < work; i += step) {
+        const int r = (int)(i / n);
+        const Item it = a.items[i - (int64_t)r * n];
         if (r >= it.rows) continue;
+        const float2 *ml = a.ml + (int64_t)it.slot * ROWS_ + r;
+        const float *part = a.part + ((int64_t)it.slot * ROWS_ + r) * D + V * lane;
         float m = NEG;
-        for (int s = warp * 32 + lane; s < it.parts; s += 32 * JOIN_WARPS)
-            m = fmaxf(m, a.ml[(int64_t)(it.slot + s) * ROWS_ + r].x);
+        for (int s = warp * 32 + lane; s < it.parts; s += 32 * W) m = fmaxf(m, ml[(int64_t)s * ROWS_].x);
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) mw[warp] = m;
-        __syncthreads();
+        if constexpr (W > 1) {
+            if (lane == 0) mw[warp] = m;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, mw[w]);
+            for (int w = 0; w < W; ++w) m = fmaxf(m, mw[w]);
+        }
         const float base = m == NEG ? 0.0f : m;
         float l = 0.0f, v[V] = {};
-        const int s0 = it.parts * warp / JOIN_WARPS, s1 = it.parts * (warp + 1) / JOIN_WARPS;
+        const int s0 = it.parts * warp / W, s1 = it.parts * (warp + 1) / W;
 #pragma unroll 4
         for (int s = s0; s < s1; ++s) {
-            const int64_t at = (int64_t)(it.slot + s) * ROWS_ + r;
-            const float2 ml = a.ml[at];
-            const float f = attn_ex2(ml.x - base);
-            l = fmaf(ml.y, f, l);
+            const float2 ms = ml[(int64_t)s * ROWS_];
+            const float f = attn_ex2(ms.x - base);
+            l = fmaf(ms.y, f, l);
             float w[V];
             if constexpr (V == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
+                const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)s * ROWS_ * D);
                 w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
             } else {
-                const float2 u = *reinterpret_cast<const float2 *>(a.part + at * D + 2 * lane);
+                const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS_ * D);
                 w[0] = u.x; w[1] = u.y;
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
         }
+        const int row = it.first + r, tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
+        uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
+        if constexpr (W > 1) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
-        if (lane == 0) lw[warp] = l;
-        __syncthreads();
-        if (threadIdx.x < D / 4) {
-            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            l = 0.0f;
+            for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
+            if (lane == 0) lw[warp] = l;
+            __syncthreads();
+            if (threadIdx.x < D / 4) {
+                float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                l = 0.0f;
 #pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) {
-                const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
-                t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-                l += lw[w];
+                for (int w = 0; w < W; ++w) {
+                    const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
+                    t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+                    l += lw[w];
+                }
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
             }
+            __syncthreads();
+        } else {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int row = it.first + r, tok = row / a.group, head = it.h * a.group + row % a.group;
-            uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.row0 + tok) * a.ldo + head * D + 4 * threadIdx.x) * out_size(a.otype);
-            store4(dst, a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+            if constexpr (V == 4) {
+                store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+            } else {
+                const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
+                if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
+            }
         }
-        __syncthreads();
     }
 }
 
@@ -459,8 +472,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
 cudaError_t launch_attention_join(const DeviceInfo &dev, const Attn &a, int dim, int rows, cudaStream_t stream)
 {
     auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a); };
-    if (rows == ROWS) return dim == 64 ? go(attention_join_kernel<64, ROWS>) : go(attention_join_kernel<128, ROWS>);
-    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS>) : go(attention_join_kernel<128, CHUNK_ROWS>);
+    if (rows == ROWS) return dim == 64 ? go(attention_join_kernel<64, ROWS, JOIN_WARPS>) : go(attention_join_kernel<128, ROWS, JOIN_WARPS>);
+    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS, 1>) : go(attention_join_kernel<128, CHUNK_ROWS, 1>);
 }
 
 // Parts to aim at: a few for each of the two CTAs on a GB300's 152 SMs, so that uneven ones even out.

@@ -26,7 +26,7 @@ struct Item {
 // Division of 0 .. 2^31 - 1 by a number that the launch fixes.
 struct Divide {
     uint32_t by, factor, shift;
-    explicit Divide(uint32_t d = 1) : by(d)
+    Divide(uint32_t d = 1) : by(d)
     {
         shift = 0;
         while ((1u << shift) < d) ++shift;
@@ -184,14 +184,12 @@ struct Plan {
         total = sm.units[NT];
     }
 
+    // Called by whole warps.
     __device__ __forceinline__ Unit find(const Attn &a, const PlanSmem<NT> &sm, int u) const
     {
-        int lo = 0, hi = NT;                        // the last thread that starts at or before u
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sm.units[mid] <= u) lo = mid;
-            else hi = mid;
-        }
+        int lo = -1;                                // the last thread that starts at or before u
+#pragma unroll
+        for (int i = 0; i < NT; i += 32) lo += __popc(__ballot_sync(0xffffffffu, sm.units[i + (threadIdx.x & 31)] <= u));
         Unit x;
         int left = u - sm.units[lo], tiles, parts;
         x.slot = sm.slots[lo];

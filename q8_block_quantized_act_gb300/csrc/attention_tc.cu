@@ -133,21 +133,52 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// 32 consecutive values, rounded to `type`.
-__device__ __forceinline__ void store32(void *p, int type, const float (&v)[32])
+// 64 bytes of each lane's row at `off`, four lanes to a row at a time: a store then touches 8 rows, not 32, and
+// whole sectors of them.  rows: of the quad's lanes (null: not stored).
+__device__ __forceinline__ void quad_store(uint4 (&v)[4], uint8_t *const (&rows)[4], int off)
 {
+    const int lane = threadIdx.x & 3;
+    uint32_t(*w)[4] = reinterpret_cast<uint32_t(*)[4]>(v);
+#pragma unroll
+    for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & bit) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & bit ? w[i][k] : w[i | bit][k], bit);
+                if (lane & bit) w[i][k] = got;
+                else w[i | bit][k] = got;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (rows[i]) *reinterpret_cast<uint4 *>(rows[i] + off + lane * 16) = v[i];
+}
+
+// 32 consecutive values of each lane's row, from value `at` on, rounded to `type`.
+__device__ __forceinline__ void store32(uint8_t *const (&rows)[4], int type, int at, const float (&v)[32])
+{
+    uint4 w[4];
     if (type == Q8ACT_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) static_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
+                                  __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
+            quad_store(w, rows, (at + 16 * h) * 4);
+        }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float w[8];
+        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = v[8 * j + i];
-        static_cast<uint4 *>(p)[j] = type == Q8ACT_F16 ? pack<__half>(w) : pack<__nv_bfloat16>(w);
+        for (int i = 0; i < 8; ++i) f[i] = v[8 * j + i];
+        w[j] = type == Q8ACT_F16 ? pack<__half>(f) : pack<__nv_bfloat16>(f);
     }
+    quad_store(w, rows, at * 2);
 }
 
 // A unit's tiles: [t0, t1), and those that row tile q sees, [a[q], b[q]).
@@ -197,12 +228,13 @@ __device__ __forceinline__ int64_t unit_of(int round)
     return (int64_t)round * g + (round & 1 ? g - 1 - c : c);
 }
 
-// Columns c0 .. c0 + 31 of a row's sums, taken again (attention.cuh).
+// Columns c0 .. c0 + 31 of each lane's row's sums, taken again (attention.cuh).
 template <typename T, int D>
 __device__ __noinline__ void exact_part(const Attn &a, const Plan<ROWS, TILE, COUNTERS> &plan, const PlanSmem<COUNTERS> &sm, int u,
-                                        int row, int c0, float mx, float (&o)[32])
+                                        int row, bool live, int c0, float mx, float (&o)[32])
 {
     const Unit x = plan.find(a, sm, u);
+    if (!live) return;
     const Range rg(a, x);
     const int r = x.tile * ROWS + row, tok = a.by_group(r), pos = x.s.pos0 + tok;
     const int k0 = max(a.window ? pos - a.window + 1 : 0, rg.t0 * TILE), k1 = min(min(pos, x.s.end - 1), rg.t1 * TILE - 1);
@@ -261,37 +293,53 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t col_s = tmem + lanes + C::COL_S + q * TILE, col_o = tmem + lanes + C::COL_O + q * D;
         uint32_t s_phase = 0, o_phase = 0, n = 0, tiles = 0;
         bool ok = true;
-        for (int round = 0; ok; ++round) {
-            const int64_t u = unit_of(round);
-            if (u >= plan.total) break;
-            int t, end, count, from, hi, lo;       // tiles from t to end of the unit's `count`, positions that the row sees
-            int64_t out_at, slot = -1;             // the row in `out`, and in the partial results
-            bool some, live;
-            {
-                const Unit x = plan.find(a, sm.plan, (int)u);
-                const Range rg(a, x);
-                const int rows = x.s.n * a.group, r = x.tile * ROWS + q * QROWS + row;
-                t = rg.a[q];
-                end = rg.b[q];
-                count = rg.t1 - rg.t0;
-                some = end > t;
-                live = r < rows;
-                const int tok = live ? a.by_group(r) : 0, pos = x.s.pos0 + tok;
-                hi = live ? min(pos, x.s.end - 1) : INT_MAX;
-                lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
-                out_at = (x.s.row0 + tok) * a.ldo + (x.h * a.group + (live ? r - tok * a.group : 0)) * D;
-                if (x.parts > 1) {
-                    slot = (int64_t)(x.slot + x.part) * ROWS + q * QROWS + row;
-                    if (x.part == 0 && threadIdx.x == 0)
-                        a.items[x.item] = Item{x.slot, x.parts, x.s.row0, x.tile * ROWS, x.h, min(ROWS, rows - x.tile * ROWS), {0, 0}};
+        struct Work {
+            int64_t u;                         // the unit, or beyond the last
+            int t, end;                        // tiles of the row tile
+            int from, count;                   // the unit's first tile and how many
+            int hi, lo;                        // positions that the row sees
+            bool live;
+            int64_t slot;                      // of the row in the partial results, or -1
+            uint8_t *dst;                      // where the row goes, or null
+        };
+        auto enter = [&](int64_t u) {
+            Work w;
+            w.u = u;
+            if (u >= plan.total) return w;
+            const Unit x = plan.find(a, sm.plan, (int)u);
+            const Range rg(a, x);
+            const int rows = x.s.n * a.group, r = x.tile * ROWS + q * QROWS + row;
+            w.t = rg.a[q];
+            w.end = rg.b[q];
+            w.from = rg.t0;
+            w.count = rg.t1 - rg.t0;
+            w.live = r < rows;
+            const int tok = w.live ? a.by_group(r) : 0, pos = x.s.pos0 + tok;
+            w.hi = w.live ? min(pos, x.s.end - 1) : INT_MAX;
+            w.lo = w.live && a.window ? max(pos - a.window + 1, 0) : 0;
+            w.slot = -1;
+            w.dst = nullptr;
+            if (x.parts > 1) {
+                if (x.part == 0 && threadIdx.x == 0)
+                    a.items[x.item] = Item{x.slot, x.parts, x.s.row0, x.tile * ROWS, x.h, min(ROWS, rows - x.tile * ROWS), {0, 0}};
+                if (w.live) {
+                    w.slot = (int64_t)(x.slot + x.part) * ROWS + q * QROWS + row;
+                    w.dst = reinterpret_cast<uint8_t *>(a.part + w.slot * D);
                 }
-                tiles -= rg.t0;                    // tile t of the sequence is tile tiles + t of the CTA
-                from = rg.t0;
+            } else if (w.live) {
+                w.dst = static_cast<uint8_t *>(a.out) +
+                        ((x.s.row0 + tok) * a.ldo + (x.h * a.group + r - tok * a.group) * D) * out_size(a.otype);
             }
+            return w;
+        };
+        Work w = enter(unit_of(0));
+        for (int round = 1; w.u < plan.total; ++round) {
+            const int hi = w.hi, lo = w.lo, end = w.end;
+            const bool some = end > w.t;
+            tiles -= w.from;                   // tile t of the sequence is tile tiles + t of the CTA
             bool first = true;
-            const bool some_tiles = count > 0;
             float mx = NEG, sum = 0.0f;
-            for (; t < end; ++t) {
+            for (int t = w.t; t < end; ++t) {
                 ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[q], s_phase, a.status, abort_flag));
                 if (!ok) break;
                 s_phase ^= 1;
@@ -364,46 +412,49 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
             }
-            tiles += count + from;
+            if (!ok) break;
+            tiles += w.from + w.count;
+            // The next unit while the last products run.
+            const Work next = enter(unit_of(round));
             if (some) {
-                if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[q], o_phase, a.status, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[q], o_phase, a.status, abort_flag));
+                if (!ok) break;
                 o_phase ^= 1;
                 tc_fence_after();
             }
             // What warps 10 and 11 have found was written before the unit's last values went to the MMAs.
             const bool spoilt = some && *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) == n + 1;
-            n += some_tiles;
-            if (ok) {
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;         // a row that sees nothing: 0
-                if (slot >= 0 && live) a.ml[slot] = make_float2(mx, sum);
+            n += w.count > 0;
+            const bool split = w.slot >= 0;
+            if (split) a.ml[w.slot] = make_float2(mx, sum);
+            const float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;          // a row that sees nothing: 0
+            // (rows that are not there follow their warp's first, which decides the type)
+            const int type = __any_sync(0xffffffffu, split) ? Q8ACT_F32 : a.otype;
+            uint8_t *rows[4];
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    float o[32];
-                    if (some) {
-                        ld32(col_o + 32 * i, o);
-                        wait_ld<32>(o);
-                    } else {
+            for (int i = 0; i < 4; ++i)
+                rows[i] = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(w.dst), (lane & ~3) + i));
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                    }
-                    if (spoilt && live) {
-                        float e[32];
-                        exact_part<T, D>(a, plan, sm.plan, (int)u, q * QROWS + row, 32 * i, mx, e);
+            for (int i = 0; i < D / 32; ++i) {
+                float o[32];
+                if (some) {
+                    ld32(col_o + 32 * i, o);
+                    wait_ld<32>(o);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = e[j];
-                    }
-                    if (live && slot >= 0) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(a.part + slot * D + 32 * i + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                    } else if (live) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] *= inv;
-                        store32(static_cast<uint8_t *>(a.out) + (out_at + 32 * i) * out_size(a.otype), a.otype, o);
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 32; ++j) o[j] = 0.0f;
                 }
+                if (spoilt) {
+                    float e[32];
+                    exact_part<T, D>(a, plan, sm.plan, (int)w.u, q * QROWS + row, w.live, 32 * i, mx, e);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = e[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= inv;
+                store32(rows, type, 32 * i, o);
             }
+            w = next;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
