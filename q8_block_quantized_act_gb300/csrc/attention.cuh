@@ -261,6 +261,26 @@ __device__ __noinline__ void exact_values(const Attn &a, int b, int h, const T *
     }
 }
 
+// A row's maximum and sum over the same positions.
+template <typename T, int D>
+__device__ __noinline__ float2 exact_statistics(const Attn &a, int b, int h, const T *q, int k0, int k1)
+{
+    const T *kc = static_cast<const T *>(a.kc);
+    const int64_t head_stride = (int64_t)D << a.p.page_shift;
+    float mx = -INFINITY, sum = 0.0f;
+    for (int k = k0; k <= k1; ++k) {
+        const int64_t page = page_of(a.p, b, k >> a.p.page_shift);
+        if (page < 0) continue;
+        const int64_t at = page * a.p.page_stride + h * head_stride + (int64_t)(k & ((1 << a.p.page_shift) - 1)) * D;
+        float s = 0.0f;
+        for (int i = 0; i < D; ++i) s = fmaf(to_f32(q[i]), to_f32(kc[at + i]), s);
+        const float m = fmaxf(mx, s * a.scale), base = m == -INFINITY ? 0.0f : m;
+        sum = sum * attn_ex2(mx - base) + attn_ex2(fmaf(s, a.scale, -base));
+        mx = m;
+    }
+    return make_float2(mx, sum);
+}
+
 // ---------------------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------------------

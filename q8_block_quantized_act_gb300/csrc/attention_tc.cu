@@ -8,8 +8,9 @@
 //   warps 0-3, 4-7  a row tile each: a thread a row, so maxima and sums need no exchange
 //   warp 8          issues the MMAs: P0 V, Q0 K', P1 V, Q1 K' (K' the next tile's keys)
 //   warp 9          brings pages of keys and values to shared memory (TMA, 128-byte swizzled)
-//   warps 10, 11    bring a row tile's queries each; in tiles of values that some row does not see as a whole they
-//                   clear those that no row sees and look for infinities and NaN among the others (attention.cuh)
+//   warp 10         in tiles of values that some row does not see as a whole clears those that no row sees and
+//                   looks for infinities and NaN among those that only some see (attention.cuh)
+//   warp 11         works out the CTA's next units for the others, and brings their queries
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
 #include <algorithm>
@@ -22,21 +23,23 @@ namespace {
 constexpr int TILE = 128;                // positions a step
 constexpr int QROWS = 128;               // rows of a row tile
 constexpr int ROWS = CHUNK_ROWS;         // of a unit: two row tiles
-constexpr int COUNTERS = 64;             // threads that count the units
+constexpr int COUNTERS = 32;             // threads that count the units
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;      // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
 constexpr int PARTS = 2;                 // of a tile's weights, handed to the MMAs one by one
 constexpr float NEG = -INFINITY;
 constexpr float SLACK = 8.0f;
+constexpr int OUT_BYTES = 32 * 128;
 
 template <int D>
 struct Cfg {
     static constexpr int Q_BYTES = QROWS * D * 2;              // a row tile's queries
     static constexpr int STAGE_BYTES = TILE * D * 2;           // a tile of keys or of values
-    static constexpr int STAGES = 160 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = 128 * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                      // columns of 128 bytes
     static constexpr int HALF_BYTES = TILE * 128;
-    static constexpr int STAGES_END = 2 * Q_BYTES + STAGES * STAGE_BYTES;
+    static constexpr int OFF_OUT = 2 * Q_BYTES + STAGES * STAGE_BYTES;      // a softmax warp's 32 rows x 128 bytes on their way out
+    static constexpr int OFF_SHARED = OFF_OUT + 8 * OUT_BYTES;
     static constexpr uint32_t COL_S = 0, COL_O = 2 * TILE;     // tensor memory: S0 S1 O0 O1
     // Instruction descriptor, kind::f16: D f32 (bits 4-5), types of A and B (7-9, 10-12), B's major (16; 1: its
     // rows are K), N >> 3 (17-22), M >> 4 (24-28).
@@ -45,17 +48,37 @@ struct Cfg {
     static constexpr uint32_t IDESC_BF16 = (1u << 7) | (1u << 10);
 };
 
+// A unit, as its roles need it: tiles [t0, t1) (t0 < 0: no more units), those that row tile q sees, [a[q], b[q]).
+struct Record {
+    int t0, t1, a[2], b[2];
+    int lo, hi;              // positions that at least one row sees
+    int first, last;         // positions of the first and the last row
+    int row0, rows, r0, h;   // the sequence's first token, its rows, the unit's first one; head of keys and values
+    int pos0, end, seq;      // position of the sequence's first row, positions in the cache, sequence
+    int slot;                // of the unit in the partial results, or -1
+
+    // Whether some row does not see some of a tile.
+    __device__ __forceinline__ bool masked(const Attn &at, int t) const
+    {
+        return t * TILE < lo || t * TILE + TILE - 1 > min(first, hi) || (at.window && t * TILE <= last - at.window);
+    }
+};
+constexpr int RECORDS = 4;                         // units known in advance, at most
+constexpr int READERS = 8 + 1 + 1 + 1;             // warps that read them: all but warp 11
+
 struct Shared {
     PlanSmem<COUNTERS> plan;
-    uint64_t full[10], empty[10];                    // stages
-    // Tile n of the CTA, in barrier n % 8: its values, and the next tile's keys, are there.  The stages hold five tiles
-    // at most, so six barriers would do.
+    uint64_t full[8], empty[8];                      // stages
+    // Tile n of the CTA, in barrier n % 8: its values, and the next tile's keys, are there.  The stages hold four tiles
+    // at most, so five barriers would do.
     uint64_t ready[8];
     uint64_t s_full[2], p_full[2][PARTS], q_full[2], q_empty[2], o_full[2], drained;
+    uint64_t unit_full[RECORDS], unit_empty[RECORDS];
+    Record units[RECORDS];
     uint32_t pages[8];                               // tile n of the CTA in word n % 8: its 16-position blocks whose page exists
     uint32_t tmem;
     // Unit n of the CTA, counting those with positions, has a non-finite value that not all rows see: n + 1 in word
-    // n % 16.  Warps 10 and 11 are ahead of the softmax by the stages' tiles at most, 5 and one.
+    // n % 16.  Warp 10 is ahead of the softmax by the stages' tiles at most, 4 and one.
     uint32_t spoilt[16];
     int abort_flag;
 };
@@ -133,93 +156,22 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// 64 bytes of each lane's row at `off`, four lanes to a row at a time: a store then touches 8 rows, not 32, and
-// whole sectors of them.  rows: of the quad's lanes (null: not stored).
-__device__ __forceinline__ void quad_store(uint4 (&v)[4], uint8_t *const (&rows)[4], int off)
+// 128 bytes of each lane's row, through the warp's part of shared memory: a store then writes four rows' whole
+// lines instead of 16 bytes of 32.  dst: where the lane's row goes (null: nowhere).
+__device__ __forceinline__ void store_rows(uint8_t *out, const uint4 (&v)[8], uint8_t *dst, int off)
 {
-    const int lane = threadIdx.x & 3;
-    uint32_t(*w)[4] = reinterpret_cast<uint32_t(*)[4]>(v);
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int bit = 1; bit < 4; bit <<= 1)
+    for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = v[k];
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & bit) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & bit ? w[i][k] : w[i | bit][k], bit);
-                if (lane & bit) w[i][k] = got;
-                else w[i | bit][k] = got;
-            }
-        }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (rows[i]) *reinterpret_cast<uint4 *>(rows[i] + off + lane * 16) = v[i];
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3), k = lane & 7;
+        uint8_t *p = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+        if (p) *reinterpret_cast<uint4 *>(p + off + k * 16) = *reinterpret_cast<const uint4 *>(out + row * 128 + ((k ^ (row & 7)) << 4));
+    }
+    __syncwarp();
 }
-
-// 32 consecutive values of each lane's row, from value `at` on, rounded to `type`.
-__device__ __forceinline__ void store32(uint8_t *const (&rows)[4], int type, int at, const float (&v)[32])
-{
-    uint4 w[4];
-    if (type == Q8ACT_F32) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]), __float_as_uint(v[16 * h + 4 * j + 1]),
-                                  __float_as_uint(v[16 * h + 4 * j + 2]), __float_as_uint(v[16 * h + 4 * j + 3]));
-            quad_store(w, rows, (at + 16 * h) * 4);
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = v[8 * j + i];
-        w[j] = type == Q8ACT_F16 ? pack<__half>(f) : pack<__nv_bfloat16>(f);
-    }
-    quad_store(w, rows, at * 2);
-}
-
-// A unit's tiles: [t0, t1), and those that row tile q sees, [a[q], b[q]).
-struct Range {
-    int t0, t1, a[2], b[2];
-    int lo, hi;              // positions that at least one row sees
-    int first, last;         // positions of the first and the last row
-
-    __device__ __forceinline__ Range(const Attn &at, const Unit &x)
-    {
-        const int rows = x.s.n * at.group, r0 = x.tile * ROWS, r1 = min(r0 + ROWS, rows) - 1;
-        const Span s = span_of<TILE>(at, x.s, r0, r1);
-        s.part(x.part, x.parts, t0, t1);
-        lo = s.lo;
-        hi = s.hi;
-        first = x.s.pos0 + at.by_group(r0);
-        last = x.s.pos0 + at.by_group(r1);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int q0 = r0 + q * QROWS;
-            a[q] = b[q] = t0;
-            if (q0 <= r1) {
-                const Span z = span_of<TILE>(at, x.s, q0, min(q0 + QROWS - 1, r1));
-                a[q] = max(t0, z.first);
-                b[q] = max(a[q], min(t1, z.first + z.n));
-            }
-        }
-    }
-    // The same in all lanes to the compiler too: the MMA warp's loops then stay in uniform registers.
-    __device__ __forceinline__ void uniform()
-    {
-        int *v[] = {&t0, &t1, &a[0], &a[1], &b[0], &b[1], &lo, &hi, &first, &last};
-#pragma unroll
-        for (int *i : v) *i = __shfl_sync(0xffffffffu, *i, 0);
-    }
-    // Whether some row does not see some of a tile.
-    __device__ __forceinline__ bool masked(const Attn &at, int t) const
-    {
-        return t * TILE < lo || t * TILE + TILE - 1 > min(first, hi) || (at.window && t * TILE <= last - at.window);
-    }
-};
 
 // The unit of this CTA's round: rounds run forwards and backwards in turn, since earlier units are longer.
 __device__ __forceinline__ int64_t unit_of(int round)
@@ -228,18 +180,47 @@ __device__ __forceinline__ int64_t unit_of(int round)
     return (int64_t)round * g + (round & 1 ? g - 1 - c : c);
 }
 
-// Columns c0 .. c0 + 31 of each lane's row's sums, taken again (attention.cuh).
+// A row's maximum, sum and columns c0 .. c0 + 63 taken again (attention.cuh).
 template <typename T, int D>
-__device__ __noinline__ void exact_part(const Attn &a, const Plan<ROWS, TILE, COUNTERS> &plan, const PlanSmem<COUNTERS> &sm, int u,
-                                        int row, bool live, int c0, float mx, float (&o)[32])
+__device__ __noinline__ void exact_part(const Attn &a, const Record &x, int row, int c0, float2 &ml, float (&o)[64])
 {
-    const Unit x = plan.find(a, sm, u);
-    if (!live) return;
-    const Range rg(a, x);
-    const int r = x.tile * ROWS + row, tok = a.by_group(r), pos = x.s.pos0 + tok;
-    const int k0 = max(a.window ? pos - a.window + 1 : 0, rg.t0 * TILE), k1 = min(min(pos, x.s.end - 1), rg.t1 * TILE - 1);
-    exact_values<T, D>(a, x.b, x.h, static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D,
-                       k0, k1, mx == NEG ? 0.0f : mx, [&](int j) { return c0 + j; }, o);
+    const int r = x.r0 + row, tok = a.by_group(r), pos = x.pos0 + tok;
+    const int k0 = max(a.window ? pos - a.window + 1 : 0, x.t0 * TILE), k1 = min(min(pos, x.end - 1), x.t1 * TILE - 1);
+    const T *q = static_cast<const T *>(a.q) + (x.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D;
+    ml = exact_statistics<T, D>(a, x.seq, x.h, q, k0, k1);
+    exact_values<T, D>(a, x.seq, x.h, q, k0, k1, ml.x == NEG ? 0.0f : ml.x, [&](int j) { return c0 + j; }, o);
+}
+
+// Rows r0 .. r1 - 1 of a tile of values, by a warp: cleared outside lo .. hi; whether one inside holds an infinity
+// or NaN (in this lane's part).
+template <typename T, int D>
+__device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, int hi)
+{
+    using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+    constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;           // 16-byte vectors of a row, rows a round of lanes
+    const int lane = threadIdx.x & 31, v = lane % VECS;
+    uint8_t *p = tile + (v >> 3) * (TILE * 128) + (v & 7) * 16;
+    uint32_t top[4] = {0, 0, 0, 0};                              // largest magnitudes, NaN above all
+#pragma unroll 4
+    for (int r = r0 + lane / VECS; r < r1; r += AT_ONCE) {
+        uint4 *w = reinterpret_cast<uint4 *>(p + r * 128);
+        if (r < lo || r > hi) {
+            *w = make_uint4(0, 0, 0, 0);
+        } else {
+            const uint4 u = *w;
+            const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const T2 m = __hmax2_nan(*reinterpret_cast<const T2 *>(&top[i]), __habs2(*reinterpret_cast<const T2 *>(&us[i])));
+                top[i] = *reinterpret_cast<const uint32_t *>(&m);
+            }
+        }
+    }
+    constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) found |= (top[i] & E) == E || (top[i] >> 16 & E) == E;
+    return found;
 }
 
 template <typename T, int D>
@@ -252,13 +233,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t IDESC_QK = C::IDESC_QK | (BF16 ? C::IDESC_BF16 : 0), IDESC_PV = C::IDESC_PV | (BF16 ? C::IDESC_BF16 : 0);
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *stages = smem + 2 * C::Q_BYTES;
-    Shared &sm = *reinterpret_cast<Shared *>(smem + C::STAGES_END);
+    Shared &sm = *reinterpret_cast<Shared *>(smem + C::OFF_SHARED);
     volatile int *abort_flag = &sm.abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 3); }
-        for (int i = 0; i < 8; ++i) mbar_init(&sm.ready[i], 2);
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 2); }
+        for (int i = 0; i < 8; ++i) mbar_init(&sm.ready[i], 1);
+        for (int i = 0; i < RECORDS; ++i) { mbar_init(&sm.unit_full[i], 1); mbar_init(&sm.unit_empty[i], READERS); }
         for (int q = 0; q < 2; ++q) {
             mbar_init(&sm.s_full[q], 1);
             for (int i = 0; i < PARTS; ++i) mbar_init(&sm.p_full[q][i], 4);
@@ -291,55 +273,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp >> 2, row = (warp & 3) * 32 + lane;         // of the row tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // the warp's lanes of tensor memory
         const uint32_t col_s = tmem + lanes + C::COL_S + q * TILE, col_o = tmem + lanes + C::COL_O + q * D;
-        uint32_t s_phase = 0, o_phase = 0, n = 0, tiles = 0;
+        uint32_t s_phase = 0, o_phase = 0, n = 0, tiles = 0;          // n: units with positions so far
         bool ok = true;
-        struct Work {
-            int64_t u;                         // the unit, or beyond the last
-            int t, end;                        // tiles of the row tile
-            int from, count;                   // the unit's first tile and how many
-            int hi, lo;                        // positions that the row sees
-            bool live;
-            int64_t slot;                      // of the row in the partial results, or -1
-            uint8_t *dst;                      // where the row goes, or null
-        };
-        auto enter = [&](int64_t u) {
-            Work w;
-            w.u = u;
-            if (u >= plan.total) return w;
-            const Unit x = plan.find(a, sm.plan, (int)u);
-            const Range rg(a, x);
-            const int rows = x.s.n * a.group, r = x.tile * ROWS + q * QROWS + row;
-            w.t = rg.a[q];
-            w.end = rg.b[q];
-            w.from = rg.t0;
-            w.count = rg.t1 - rg.t0;
-            w.live = r < rows;
-            const int tok = w.live ? a.by_group(r) : 0, pos = x.s.pos0 + tok;
-            w.hi = w.live ? min(pos, x.s.end - 1) : INT_MAX;
-            w.lo = w.live && a.window ? max(pos - a.window + 1, 0) : 0;
-            w.slot = -1;
-            w.dst = nullptr;
-            if (x.parts > 1) {
-                if (x.part == 0 && threadIdx.x == 0)
-                    a.items[x.item] = Item{x.slot, x.parts, x.s.row0, x.tile * ROWS, x.h, min(ROWS, rows - x.tile * ROWS), {0, 0}};
-                if (w.live) {
-                    w.slot = (int64_t)(x.slot + x.part) * ROWS + q * QROWS + row;
-                    w.dst = reinterpret_cast<uint8_t *>(a.part + w.slot * D);
-                }
-            } else if (w.live) {
-                w.dst = static_cast<uint8_t *>(a.out) +
-                        ((x.s.row0 + tok) * a.ldo + (x.h * a.group + r - tok * a.group) * D) * out_size(a.otype);
-            }
-            return w;
-        };
-        Work w = enter(unit_of(0));
-        for (int round = 1; w.u < plan.total; ++round) {
-            const int hi = w.hi, lo = w.lo, end = w.end;
-            const bool some = end > w.t;
-            tiles -= w.from;                   // tile t of the sequence is tile tiles + t of the CTA
-            bool first = true;
+        for (int round = 0;; ++round) {
+            ok = __all_sync(0xffffffffu, wait_or_abort(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag));
+            const Record &x = sm.units[round % RECORDS];
+            if (!ok || x.t0 < 0) break;
+            const int from = x.a[q], end = x.b[q], r = x.r0 + q * QROWS + row;
+            const bool live = r < x.rows;
+            const int pos = x.pos0 + a.by_group(live ? r : 0);
+            const int hi = live ? min(pos, x.end - 1) : INT_MAX, lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
+            const int count = tiles - x.t0;              // tile t of the sequence is tile count + t of the CTA
+            const bool some = end > from;
+            tiles += x.t1 - x.t0;
             float mx = NEG, sum = 0.0f;
-            for (int t = w.t; t < end; ++t) {
+            bool first = true;
+            for (int t = from; t < end; ++t) {
                 ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[q], s_phase, a.status, abort_flag));
                 if (!ok) break;
                 s_phase ^= 1;
@@ -348,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < TILE / 32; ++i) ld32(col_s + 32 * i, s + 32 * i);
                 const int k0 = t * TILE;
-                const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(tiles + t) & 7]);
+                const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(count + t) & 7]);
                 const bool edge = __any_sync(0xffffffffu, k0 + TILE - 1 > hi || k0 < lo) || pages != 0xff;
                 wait_ld<TILE>(s);
                 if (edge) {
@@ -385,76 +334,100 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
                 float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i) {
+                for (int c = 0; c < 4; ++c) {
+                    const float *v = s + 32 * c;
+                    uint32_t p[16];
 #pragma unroll
-                    for (int h = 0; h < 4 / PARTS; ++h) {
-                        const int at = 32 * (4 / PARTS * i + h);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 e = __ffma2_rn(make_float2(s[at + 2 * j], s[at + 2 * j + 1]), scale2, base2);
-                            e = make_float2(attn_ex2(e.x), attn_ex2(e.y));
-                            sum2[j & 1] = __fadd2_rn(sum2[j & 1], e);
-                            if constexpr (BF16) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
-                                p[j] = *reinterpret_cast<const uint32_t *>(&h);
-                            } else {
-                                const __half2 h = __floats2half2_rn(e.x, e.y);
-                                p[j] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
+                    for (int j = 0; j < 16; ++j) {
+                        float2 e = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), scale2, base2);
+                        e = make_float2(attn_ex2(e.x), attn_ex2(e.y));
+                        sum2[j & 1] = __fadd2_rn(sum2[j & 1], e);
+                        if constexpr (BF16) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+                            p[j] = *reinterpret_cast<const uint32_t *>(&h);
+                        } else {
+                            const __half2 h = __floats2half2_rn(e.x, e.y);
+                            p[j] = *reinterpret_cast<const uint32_t *>(&h);
                         }
-                        st16(col_s + at / 2, p);
                     }
-                    wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[q][i]);
+                    st16(col_s + 16 * c, p);
+                    if (c % (4 / PARTS) == 4 / PARTS - 1) {
+                        wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.p_full[q][c / (4 / PARTS)]);
+                    }
                 }
                 sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
             }
             if (!ok) break;
-            tiles += w.from + w.count;
-            // The next unit while the last products run.
-            const Work next = enter(unit_of(round));
             if (some) {
                 ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[q], o_phase, a.status, abort_flag));
                 if (!ok) break;
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            // What warps 10 and 11 have found was written before the unit's last values went to the MMAs.
+            // What warp 10 has found was written before the unit's last values went to the MMAs.
             const bool spoilt = some && *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) == n + 1;
-            n += w.count > 0;
-            const bool split = w.slot >= 0;
-            if (split) a.ml[w.slot] = make_float2(mx, sum);
-            const float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;          // a row that sees nothing: 0
-            // (rows that are not there follow their warp's first, which decides the type)
-            const int type = __any_sync(0xffffffffu, split) ? Q8ACT_F32 : a.otype;
-            uint8_t *rows[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                rows[i] = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(w.dst), (lane & ~3) + i));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float o[32];
+            n += x.t1 > x.t0;
+            const bool split = x.slot >= 0;
+            uint8_t *dst = nullptr;
+            if (live && split) {
+                const int64_t slot = (int64_t)x.slot * ROWS + q * QROWS + row;
+                a.ml[slot] = make_float2(mx, sum);
+                dst = reinterpret_cast<uint8_t *>(a.part + slot * D);
+            } else if (live) {
+                const int tok = a.by_group(r);
+                dst = static_cast<uint8_t *>(a.out) + ((x.row0 + tok) * a.ldo + (x.h * a.group + r - tok * a.group) * D) * out_size(a.otype);
+            }
+            float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;           // a row that sees nothing: 0
+            const int type = split ? Q8ACT_F32 : a.otype;
+            uint8_t *out = smem + C::OFF_OUT + warp * OUT_BYTES;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 64) {
+                float o[64];
                 if (some) {
-                    ld32(col_o + 32 * i, o);
-                    wait_ld<32>(o);
+                    ld32(col_o + i, o);
+                    ld32(col_o + i + 32, o + 32);
+                    wait_ld<64>(o);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                    for (int j = 0; j < 64; ++j) o[j] = 0.0f;
                 }
-                if (spoilt) {
-                    float e[32];
-                    exact_part<T, D>(a, plan, sm.plan, (int)w.u, q * QROWS + row, w.live, 32 * i, mx, e);
+                if (spoilt && live) {
+                    float e[64];
+                    float2 ml;
+                    exact_part<T, D>(a, x, q * QROWS + row, i, ml, e);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = e[j];
+                    for (int j = 0; j < 64; ++j) o[j] = e[j];
+                    if (split) a.ml[(int64_t)x.slot * ROWS + q * QROWS + row] = ml;
+                    else inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= inv;
-                store32(rows, type, 32 * i, o);
+                for (int j = 0; j < 64; ++j) o[j] *= inv;
+                uint4 v[8];
+                if (type == Q8ACT_F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = make_uint4(__float_as_uint(o[32 * h + 4 * k]), __float_as_uint(o[32 * h + 4 * k + 1]),
+                                              __float_as_uint(o[32 * h + 4 * k + 2]), __float_as_uint(o[32 * h + 4 * k + 3]));
+                        store_rows(out, v, dst, (i + 32 * h) * 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = o[8 * k + j];
+                        v[k] = type == Q8ACT_F16 ? pack<__half>(f) : pack<__nv_bfloat16>(f);
+                    }
+                    store_rows(out, v, dst, i * 2);
+                }
             }
-            w = next;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.unit_empty[round % RECORDS]);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
@@ -481,10 +454,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             auto at = [&](uint64_t desc, int stage) { return desc + (uint32_t)(__shfl_sync(0xffffffffu, stage, 0) * (C::STAGE_BYTES >> 4)); };
             for (int round = 0; ok; ++round) {
-                const int64_t u = unit_of(round);
-                if (u >= plan.total) break;
-                Range rg(a, plan.find(a, sm.plan, (int)u));
-                rg.uniform();
+                if (!wait(&sm.unit_full[round % RECORDS], round / RECORDS & 1)) break;
+                // The same in all lanes to the compiler too: the loops then stay in uniform registers.
+                struct { int t0, t1, a[2], b[2]; } rg;
+                {
+                    const Record &x = sm.units[round % RECORDS];
+                    rg.t0 = __shfl_sync(0xffffffffu, x.t0, 0);
+                    rg.t1 = __shfl_sync(0xffffffffu, x.t1, 0);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        rg.a[q] = __shfl_sync(0xffffffffu, x.a[q], 0);
+                        rg.b[q] = __shfl_sync(0xffffffffu, x.b[q], 0);
+                    }
+                }
+                if (rg.t0 < 0) break;
+                if (lane == 0) mbar_arrive(&sm.unit_empty[round % RECORDS]);
                 if (rg.t0 == rg.t1) continue;
                 // S = Q K^T of the tile whose keys are at kd.
                 auto scores = [&](int q, int t, uint64_t kd) {
@@ -561,12 +545,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t phase = 1, tiles = 0;
             bool ok = true;
             for (int round = 0; ok; ++round) {
-                const int64_t u = unit_of(round);
-                if (u >= plan.total) break;
-                const Unit x = plan.find(a, sm.plan, (int)u);
-                const Range rg(a, x);
-                int64_t page = lane < per_tile && rg.t0 < rg.t1 ? page_of(a.p, x.b, (rg.t0 * TILE >> a.p.page_shift) + lane) : -1;
-                for (int t = rg.t0; ok && t < rg.t1; ++t) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag));
+                const Record &rc = sm.units[round % RECORDS];
+                if (!ok || rc.t0 < 0) break;
+                const int t0 = rc.t0, t1 = rc.t1, seq = rc.seq, h = rc.h;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.unit_empty[round % RECORDS]);
+                int64_t page = lane < per_tile && t0 < t1 ? page_of(a.p, seq, (t0 * TILE >> a.p.page_shift) + lane) : -1;
+                for (int t = t0; ok && t < t1; ++t) {
                     const int pos = t * TILE;
                     // A page that does not exist: a box outside the tensor, which reads as zeros.
                     const int id = page < 0 ? (int)a.p.pages : (int)page;
@@ -574,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t pages = 0;
                     for (int j = 0; j < per_tile; ++j)
                         if (good >> j & 1) pages |= ((1u << (8 / per_tile)) - 1) << (j * (8 / per_tile));
-                    if (t + 1 < rg.t1 && lane < per_tile) page = page_of(a.p, x.b, ((pos + TILE) >> a.p.page_shift) + lane);
+                    if (t + 1 < t1 && lane < per_tile) page = page_of(a.p, seq, ((pos + TILE) >> a.p.page_shift) + lane);
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         ok = __all_sync(0xffffffffu, wait_or_abort(&sm.empty[st], phase, a.status, abort_flag));
                         if (!ok) break;
@@ -587,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int box_page = __shfl_sync(0xffffffffu, id, j & 31);
                         if (j < per_tile)
                             tma_load_4d(stages + st * C::STAGE_BYTES + half * C::HALF_BYTES + j * ps * 128, kv ? &tm_v : &tm_k,
-                                        half * 64, ps > TILE ? pos & (ps - 1) : 0, x.h, box_page, &sm.full[st]);
+                                        half * 64, ps > TILE ? pos & (ps - 1) : 0, h, box_page, &sm.full[st]);
                         __syncwarp();
                         if (++st == STAGES) {
                             st = 0;
@@ -599,30 +585,104 @@ __global__ void __launch_bounds__(THREADS, 1)
             // Never leave with a copy into this CTA's shared memory in flight.
             for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
                 mbar_wait_drain(&sm.full[i % STAGES], (i / STAGES) & 1, a.status);
-        } else {
+        } else if (warp == 10) {
             // ------------------------------ masked values ------------------------------
-            constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
-            const int q = warp - 10;                 // row tile whose queries it brings, half of a tile that it looks at
             int st = 0;
-            uint32_t phase = 0, q_phase = 1, n = 0, tiles = 0;
+            uint32_t phase = 0, n = 0, tiles = 0;
             bool ok = true;
             for (int round = 0; ok; ++round) {
-                const int64_t u = unit_of(round);
-                if (u >= plan.total) break;
-                const Unit x = plan.find(a, sm.plan, (int)u);
-                const Range rg(a, x);
-                if (rg.b[q] > rg.a[q]) {
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[q], q_phase, a.status, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag));
+                const Record &x = sm.units[round % RECORDS];
+                if (!ok || x.t0 < 0) break;
+                // Every stage is waited for and handed back, so that this warp keeps the pipeline's pace.
+                for (int i = 0; i < 2 * (x.t1 - x.t0); ++i) {
+                    const int t = x.t0 + (i >> 1);
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
                     if (!ok) break;
-                    q_phase ^= 1;
+                    if ((i & 1) && x.masked(a, t)) {
+                        // Positions of the tile that not all rows see: before `from`, behind the window, and from
+                        // `to` on.
+                        const int k0 = t * TILE;
+                        const int to = min(max(min(x.first, x.hi) + 1 - k0, 0), TILE);
+                        const int from = min(max(a.window ? x.last - a.window + 1 : 0, x.lo) - k0, TILE);
+                        const bool found = fix_rows<T, D>(stages + st * C::STAGE_BYTES, 0, from, x.lo - k0, x.hi - k0) |
+                                           fix_rows<T, D>(stages + st * C::STAGE_BYTES, max(to, from), TILE, x.lo - k0, x.hi - k0);
+                        if (found) *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) = n + 1;
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        // Values and the next keys are there (the last values: no keys follow).
+                        if (i > 0 && (!(i & 1) || t + 1 == x.t1)) mbar_arrive(&sm.ready[tiles++ & 7]);
+                        mbar_arrive(&sm.empty[st]);
+                    }
+                    if (++st == STAGES) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+                n += x.t1 > x.t0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.unit_empty[round % RECORDS]);
+            }
+        } else {
+            // ------------------------------ units, queries ------------------------------
+            uint32_t q_phase = 3;                            // a bit a row tile
+            bool ok = true;
+            for (int round = 0;; ++round) {
+                if (!__all_sync(0xffffffffu, wait_or_abort(&sm.unit_empty[round % RECORDS], (round / RECORDS & 1) ^ 1, a.status, abort_flag)))
+                    break;
+                const int64_t u = unit_of(round);
+                Record rc;
+                rc.t0 = -1;
+                if (u < plan.total) {
+                    const Unit x = plan.find(a, sm.plan, (int)u);
+                    rc.rows = x.s.n * a.group;
+                    rc.r0 = x.tile * ROWS;
+                    const int r1 = min(rc.r0 + ROWS, rc.rows) - 1;
+                    const Span s = span_of<TILE>(a, x.s, rc.r0, r1);
+                    s.part(x.part, x.parts, rc.t0, rc.t1);
+                    rc.lo = s.lo;
+                    rc.hi = s.hi;
+                    rc.first = x.s.pos0 + a.by_group(rc.r0);
+                    rc.last = x.s.pos0 + a.by_group(r1);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int q0 = rc.r0 + q * QROWS;
+                        rc.a[q] = rc.b[q] = rc.t0;
+                        if (q0 <= r1) {
+                            const Span z = span_of<TILE>(a, x.s, q0, min(q0 + QROWS - 1, r1));
+                            rc.a[q] = max(rc.t0, z.first);
+                            rc.b[q] = max(rc.a[q], min(rc.t1, z.first + z.n));
+                        }
+                    }
+                    rc.row0 = x.s.row0;
+                    rc.h = x.h;
+                    rc.pos0 = x.s.pos0;
+                    rc.end = x.s.end;
+                    rc.seq = x.b;
+                    rc.slot = x.parts > 1 ? x.slot + x.part : -1;
+                    if (x.parts > 1 && x.part == 0 && lane == 0)
+                        a.items[x.item] = Item{x.slot, x.parts, x.s.row0, rc.r0, x.h, min(ROWS, rc.rows - rc.r0), {0, 0}};
+                }
+                if (lane == 0) {
+                    sm.units[round % RECORDS] = rc;
+                    mbar_arrive(&sm.unit_full[round % RECORDS]);
+                }
+                if (rc.t0 < 0) break;
+                for (int q = 0; q < 2; ++q) {
+                    if (q ? rc.b[1] <= rc.a[1] : rc.b[0] <= rc.a[0]) continue;
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[q], q_phase >> q & 1, a.status, abort_flag));
+                    if (!ok) break;
+                    q_phase ^= 1u << q;
                     // Rows behind the last one as zeros.
-                    const int rows = x.s.n * a.group, r0 = x.tile * ROWS + q * QROWS;
+                    const int rows = rc.rows, r0 = rc.r0 + q * QROWS;
                     constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
                     const uint32_t dst0 = smem_u32(smem + q * C::Q_BYTES);
 #pragma unroll 1
                     for (int i = 0; i < QROWS; i += 32) {
                         const int r = r0 + i + lane, tok = a.by_group(r);
-                        const int64_t off = r < rows ? (x.s.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D : -1;
+                        const int64_t off = r < rows ? (rc.row0 + tok) * a.ldq + (rc.h * a.group + r - tok * a.group) * D : -1;
 #pragma unroll 8
                         for (int j = 0; j < 32; j += AT_ONCE) {
                             const int rr = i + j + lane / VECS, v = lane % VECS;
@@ -636,42 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.q_full[q]);
                 }
-                // Every stage is waited for and handed back, so that these warps keep the pipeline's pace.
-                for (int i = 0; i < 2 * (rg.t1 - rg.t0); ++i) {
-                    const int t = rg.t0 + (i >> 1);
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
-                    if (!ok) break;
-                    if ((i & 1) && rg.masked(a, t)) {
-                        bool found = false;
-                        uint8_t *v = stages + st * C::STAGE_BYTES;
-#pragma unroll 4
-                        for (int j = q * 32 + lane; j < C::STAGE_BYTES / 16; j += 64) {
-                            const int key = t * TILE + (j >> 3) % TILE;          // 8 vectors a position and half
-                            uint4 *p = reinterpret_cast<uint4 *>(v) + j;
-                            if (key < rg.lo || key > rg.hi) {
-                                *p = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 w = *p;
-                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int l = 0; l < 4; ++l) found |= (ws[l] & E) == E || (ws[l] >> 16 & E) == E;
-                            }
-                        }
-                        if (found) *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) = n + 1;
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        // Values and the next keys are there (the last values: no keys follow).
-                        if (i > 0 && (!(i & 1) || t + 1 == rg.t1)) mbar_arrive(&sm.ready[tiles++ & 7]);
-                        mbar_arrive(&sm.empty[st]);
-                    }
-                    if (++st == STAGES) {
-                        st = 0;
-                        phase ^= 1;
-                    }
-                }
-                n += rg.t1 > rg.t0;
+                if (!ok) break;
             }
         }
     }
@@ -701,7 +726,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
         } else {
             auto go = [&](auto d) -> cudaError_t {
                 constexpr int D = decltype(d)::value;
-                constexpr size_t smem = Cfg<D>::STAGES_END + sizeof(Shared);
+                constexpr size_t smem = Cfg<D>::OFF_SHARED + sizeof(Shared);
                 static_assert(smem <= 227 * 1024, "shared memory");
                 cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
