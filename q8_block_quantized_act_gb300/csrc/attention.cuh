@@ -305,15 +305,20 @@ inline void attention_place(Attn &a, void *ws, int target, int rows)
     a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.ml) + up256(slots * rows * sizeof(float2)));
 }
 
+inline CUtensorMapDataType attention_type(const q8act_paged_kv &kv)
+{
+    return kv.type == Q8ACT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
 // Tensor maps of the cache, boxes of 64 values x `rows` positions of a page.
 inline bool attention_maps(const q8act_paged_kv &kv, int rows, CUtensorMap *tk, CUtensorMap *tv)
 {
-    const CUtensorMapDataType dt = kv.type == Q8ACT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType dt = attention_type(kv);
     const uint64_t dims[4] = {(uint64_t)kv.dim, (uint64_t)kv.page_size, (uint64_t)kv.heads, (uint64_t)kv.pages};
     const uint64_t strides[3] = {(uint64_t)kv.dim * 2, (uint64_t)kv.dim * 2 * kv.page_size, (uint64_t)kv.page_stride * 2};
     const uint32_t box[4] = {64, (uint32_t)(kv.page_size < rows ? kv.page_size : rows), 1, 1};
-    return encode_4d(tk, dt, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           encode_4d(tv, dt, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_tiled(tk, dt, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_tiled(tv, dt, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The kernel for chunks (attention_tc.cu): its workspace, its launch (a: all but the workspace's places), and

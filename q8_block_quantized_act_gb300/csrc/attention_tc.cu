@@ -225,7 +225,8 @@ __device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    attention_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
+    attention_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ CUtensorMap tm_q, int q_boxes, Attn a)
 {
     using C = Cfg<D>;
     constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 9 && lane == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        if (q_boxes) prefetch_tensormap(&tm_q);
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -334,11 +336,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
                 float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float *v = s + 32 * c;
-                    uint32_t p[16];
+                for (int c = 0; c < PARTS; ++c) {
+                    constexpr int N = TILE / 2 / PARTS;
+                    const float *v = s + 2 * N * c;
+                    uint32_t p[N];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < N; ++j) {
                         float2 e = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), scale2, base2);
                         e = make_float2(attn_ex2(e.x), attn_ex2(e.y));
                         sum2[j & 1] = __fadd2_rn(sum2[j & 1], e);
@@ -350,13 +353,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                             p[j] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                     }
-                    st16(col_s + 16 * c, p);
-                    if (c % (4 / PARTS) == 4 / PARTS - 1) {
-                        wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.p_full[q][c / (4 / PARTS)]);
-                    }
+                    st32(col_s + N * c, p);
+                    wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[q][c]);
                 }
                 sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
             }
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else {
             // ------------------------------ units, queries ------------------------------
-            uint32_t q_phase = 3;                            // a bit a row tile
+            uint32_t q_phase = 3, q_loads = 0;               // a bit a row tile
             bool ok = true;
             for (int round = 0;; ++round) {
                 if (!__all_sync(0xffffffffu, wait_or_abort(&sm.unit_empty[round % RECORDS], (round / RECORDS & 1) ^ 1, a.status, abort_flag)))
@@ -675,6 +676,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[q], q_phase >> q & 1, a.status, abort_flag));
                     if (!ok) break;
                     q_phase ^= 1u << q;
+                    if (q_boxes) {
+                        // Whole tokens: a box of a row tile's.  (Rows behind the sequence's last hold others' queries,
+                        // or zeros; what comes of them goes nowhere.)
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sm.q_full[q], C::Q_BYTES);
+                            for (int half = 0; half < C::HALVES; ++half)
+                                tma_load_3d(smem + q * C::Q_BYTES + half * (QROWS * 128), &tm_q, half * 64, rc.h * a.group,
+                                            rc.row0 + a.by_group(rc.r0 + q * QROWS), &sm.q_full[q]);
+                        }
+                        __syncwarp();
+                        q_loads |= 1u << q;
+                        continue;
+                    }
                     // Rows behind the last one as zeros.
                     const int rows = rc.rows, r0 = rc.r0 + q * QROWS;
                     constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
@@ -698,6 +712,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!ok) break;
             }
+            // Never leave with a copy into this CTA's shared memory in flight: the last unit's queries (of the units
+            // before, the MMAs have waited for them).
+            if (q_boxes)
+                for (int q = 0; q < 2; ++q)
+                    if (q_loads >> q & 1) mbar_wait_drain(&sm.q_full[q], q_phase >> q & 1, a.status);
         }
     }
     __syncthreads();
@@ -715,8 +734,18 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
 {
     attention_place(a, ws, TARGET, ROWS);
     a.least = 2;
-    CUtensorMap tk, tv;
+    CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
+    // Row tiles of whole tokens come as one box; others are gathered row by row.
+    const int q_boxes = QROWS % a.group == 0;
+    if (q_boxes) {
+        const uint64_t dims[3] = {(uint64_t)kv.dim, (uint64_t)a.group * kv.heads, (uint64_t)a.p.m};
+        const uint64_t strides[2] = {(uint64_t)kv.dim * 2, (uint64_t)a.ldq * 2};
+        const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)(QROWS / a.group)};
+        if (!encode_tiled(&tq, attention_type(kv), a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    } else {
+        tq = tk;
+    }
     const int64_t units = (int64_t)kv.heads * ((int64_t)a.p.m * a.group / ROWS + std::min(kv.seqs, a.p.m)) + TARGET;    // at most
     const unsigned grid = (unsigned)std::min<int64_t>(units, dev.num_sms);
     return with_type(kv.type, [&](auto x) -> cudaError_t {
@@ -730,7 +759,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
                 static_assert(smem <= 227 * 1024, "shared memory");
                 cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, smem, stream, tk, tv, a);
+                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
                 return e == cudaSuccess ? launch_attention_join(dev, a, D, ROWS, stream) : e;
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});

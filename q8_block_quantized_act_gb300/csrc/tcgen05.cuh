@@ -111,17 +111,22 @@ inline bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// strides: of dimensions 1 .. 3, in bytes.
-inline bool encode_4d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[4],
-                      const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swz)
+// strides: of the dimensions but the first, in bytes.
+template <size_t N>
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[N],
+                  const uint64_t (&strides)[N - 1], const uint32_t (&box)[N], CUtensorMapSwizzle swz)
 {
     EncodeTiledFn fn = get_encode_fn();
     if (!fn) return false;
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 4; ++i) { d[i] = dims[i]; b[i] = box[i]; }
-    for (int i = 0; i < 3; ++i) st[i] = strides[i];
-    return fn(map, dt, 4, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+    cuuint64_t d[N], st[N - 1];
+    cuuint32_t b[N], estr[N];
+    for (size_t i = 0; i < N; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        estr[i] = 1;
+    }
+    for (size_t i = 0; i + 1 < N; ++i) st[i] = strides[i];
+    return fn(map, dt, (cuuint32_t)N, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
