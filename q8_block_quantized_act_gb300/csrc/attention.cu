@@ -106,7 +106,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     griddep_launch_dependents();
     Plan<ROWS, TILE, COUNTERS> plan;
     plan.make(a, sm.plan);                                       // and the barriers exist for all
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = sm.plan.items[COUNTERS];
 
     if (warp == CONSUMERS) {
         // ------------------------------ producer ------------------------------
@@ -367,8 +366,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                                make_float4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv, acc[4 * j + 3] * inv));
                 }
             }
-            if (x.parts > 1 && x.part == 0 && threadIdx.x == 0)
-                a.items[x.item] = Item{x.slot, x.parts, x.s.row0, r0, x.h, valid, {0, 0}};
         }
         if (some) {
             fence_proxy_async_smem();            // the join's words before the next copies to the stage
@@ -389,99 +386,115 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Row tiles in several parts: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i, added in the parts' order.
 // Few rows come in many parts (decoding), which W warps of a CTA share; many rows in few, a row a warp.
 // ---------------------------------------------------------------------------------------
+// The kernel works out which rows it joins while the parts are still being computed.
+// ---------------------------------------------------------------------------------------
 constexpr int JOIN_WARPS = 4;
 
-template <int D, int ROWS_, int W>
+template <int D, int ROWS_, int TILE_, int NT, int W>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
 {
     constexpr int V = D / 32;                // values a lane
-    __shared__ float acc[W > 1 ? W : 1][D], mw[W], lw[W];
+    __shared__ PlanSmem<NT> sm;
+    __shared__ alignas(16) float acc[W > 1 ? W : 1][D];
+    __shared__ float mw[W], lw[W];
     const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
-    griddep_enter();
-    const int n = *a.count;
-    const int64_t work = (int64_t)n * ROWS_, step = (int64_t)gridDim.x * (JOIN_WARPS / W);
-    for (int64_t i = (int64_t)blockIdx.x * (JOIN_WARPS / W) + (W > 1 ? 0 : threadIdx.x >> 5); i < work; i += step) {
-        const int r = (int)(i / n);
-        const Item it = a.items[i - (int64_t)r * n];
-        if (r >= it.rows) continue;
-        const float2 *ml = a.ml + (int64_t)it.slot * ROWS_ + r;
-        const float *part = a.part + ((int64_t)it.slot * ROWS_ + r) * D + V * lane;
-        float m = NEG;
-        for (int s = warp * 32 + lane; s < it.parts; s += 32 * W) m = fmaxf(m, ml[(int64_t)s * ROWS_].x);
+    // (what starts, lens and the table hold was there before the kernel in front, which has waited for it)
+    Plan<ROWS_, TILE_, NT> plan;
+    plan.make(a, sm);
+    const int n = sm.items[NT];
+    // A CTA's rows one by one, first rows first (the last of a row tile may not be there); or a warp's in fours.
+    constexpr int R = W > 1 ? 1 : 4;
+    const int work = n * (ROWS_ / R), step = gridDim.x * (JOIN_WARPS / W);
+    bool waited = false;
+    for (int i = blockIdx.x * (JOIN_WARPS / W) + (W > 1 ? 0 : threadIdx.x >> 5); i < work; i += step) {
+        const int i0 = W > 1 ? i / n : i % (ROWS_ / R) * R;
+        const Unit it = plan.find_item(a, sm, W > 1 ? i - i0 * n : i / (ROWS_ / R));
+        if (!waited) griddep_enter();
+        waited = true;
+        const int rows = it.s.n * a.group - it.tile * ROWS_;
+#pragma unroll 1
+        for (int r = i0; r < min(i0 + R, rows); ++r) {
+            const int row = it.tile * ROWS_ + r;
+            const float2 *ml = a.ml + (int64_t)it.slot * ROWS_ + r;
+            const float *part = a.part + ((int64_t)it.slot * ROWS_ + r) * D + V * lane;
+            float m = NEG;
+            for (int s = warp * 32 + lane; s < it.parts; s += 32 * W) m = fmaxf(m, ml[(int64_t)s * ROWS_].x);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if constexpr (W > 1) {
-            if (lane == 0) mw[warp] = m;
-            __syncthreads();
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if constexpr (W > 1) {
+                if (lane == 0) mw[warp] = m;
+                __syncthreads();
 #pragma unroll
-            for (int w = 0; w < W; ++w) m = fmaxf(m, mw[w]);
-        }
-        const float base = m == NEG ? 0.0f : m;
-        float l = 0.0f, v[V] = {};
-        const int s0 = it.parts * warp / W, s1 = it.parts * (warp + 1) / W;
+                for (int w = 0; w < W; ++w) m = fmaxf(m, mw[w]);
+            }
+            const float base = m == NEG ? 0.0f : m;
+            float l = 0.0f, v[V] = {};
+            const int s0 = it.parts * warp / W, s1 = it.parts * (warp + 1) / W;
 #pragma unroll 4
-        for (int s = s0; s < s1; ++s) {
-            const float2 ms = ml[(int64_t)s * ROWS_];
-            const float f = attn_ex2(ms.x - base);
-            l = fmaf(ms.y, f, l);
-            float w[V];
-            if constexpr (V == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)s * ROWS_ * D);
-                w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-            } else {
-                const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS_ * D);
-                w[0] = u.x; w[1] = u.y;
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
-        }
-        const int row = it.first + r, tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
-        uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
-        if constexpr (W > 1) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
-            if (lane == 0) lw[warp] = l;
-            __syncthreads();
-            if (threadIdx.x < D / 4) {
-                float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                l = 0.0f;
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
-                    t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-                    l += lw[w];
+            for (int s = s0; s < s1; ++s) {
+                const float2 ms = ml[(int64_t)s * ROWS_];
+                const float f = attn_ex2(ms.x - base);
+                l = fmaf(ms.y, f, l);
+                float w[V];
+                if constexpr (V == 4) {
+                    const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)s * ROWS_ * D);
+                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                } else {
+                    const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS_ * D);
+                    w[0] = u.x; w[1] = u.y;
                 }
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
             }
-            __syncthreads();
-        } else {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if constexpr (V == 4) {
-                store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+            const int tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
+            uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
+            if constexpr (W > 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
+                if (lane == 0) lw[warp] = l;
+                __syncthreads();
+                if (threadIdx.x < D / 4) {
+                    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
+                        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+                        l += lw[w];
+                    }
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+                }
+                __syncthreads();
             } else {
-                const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
-                if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if constexpr (V == 4) {
+                    store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+                } else {
+                    const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
+                    if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
+                }
             }
         }
     }
+    if (!waited) griddep_enter();
 }
 
 }  // namespace
 
-cudaError_t launch_attention_join(const DeviceInfo &dev, const Attn &a, int dim, int rows, cudaStream_t stream)
+cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream)
 {
     auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a); };
-    if (rows == ROWS) return dim == 64 ? go(attention_join_kernel<64, ROWS, JOIN_WARPS>) : go(attention_join_kernel<128, ROWS, JOIN_WARPS>);
-    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS, 1>) : go(attention_join_kernel<128, CHUNK_ROWS, 1>);
+    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS, CHUNK_TILE, CHUNK_COUNTERS, 1>)
+                     : go(attention_join_kernel<128, CHUNK_ROWS, CHUNK_TILE, CHUNK_COUNTERS, 1>);
 }
 
-// Parts to aim at: a few for each of the two CTAs on a GB300's 152 SMs, so that uneven ones even out.
-constexpr int ROWS_TARGET = 4 * 2 * 152;
+// Partial results: of four rounds of a GB300's 152 SMs at two CTAs each, twice (Plan::make).
+constexpr int SLOTS = 2 * 4 * 2 * 152;
 
 size_t attention_workspace_bytes(int dim)
 {
-    return std::max(attention_space(ROWS_TARGET, ROWS, dim), attention_chunk_space(dim));
+    return std::max(attention_space(SLOTS, ROWS, dim), attention_chunk_space(dim));
 }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &s, int64_t m,
@@ -504,8 +517,10 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.status = dev.status;
     const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
     if (most * a.group > ROWS) return launch_attention_chunk(dev, kv, a, s.ws, stream);
+    attention_place(a, s.ws, SLOTS, ROWS);
+    a.ctas = 2 * dev.num_sms;
     a.least = 1;
-    attention_place(a, s.ws, ROWS_TARGET, ROWS);
+    a.unit_cost = 2.0f;
     CUtensorMap tk, tv;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     return with_type(kv.type, [&](auto x) -> cudaError_t {
@@ -519,7 +534,8 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
                 cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
                 e = launch_dependent(attention_rows_kernel<T, D>, dim3(2 * dev.num_sms), THREADS, smem, stream, tk, tv, a);
-                return e == cudaSuccess ? launch_attention_join(dev, a, D, ROWS, stream) : e;
+                if (e != cudaSuccess) return e;
+                return launch_dependent(attention_join_kernel<D, ROWS, TILE, COUNTERS, JOIN_WARPS>, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a);
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
         }

@@ -18,11 +18,6 @@
 
 namespace q8 {
 
-// A row tile in several parts, as the joining kernel needs it: the slot of its first part, its place.
-struct Item {
-    int slot, parts, row0, first, h, rows, unused[2];    // first: its first row among the sequence's, which start at row0
-};
-
 // Division of 0 .. 2^31 - 1 by a number that the launch fixes.
 struct Divide {
     uint32_t by, factor, shift;
@@ -42,11 +37,12 @@ struct Attn {
     void *out;
     int64_t ldq, ldo;
     int group, otype, window;    // window 0: all earlier positions
-    int target, least;           // parts to aim at, and the fewest key tiles that a part is worth
     float scale;                 // of scores, times log2 e
+    // How units are cut (Plan): CTAs that take them, the fewest key tiles that a part is worth, what a unit costs beside
+    // its tiles (in tiles), partial results that the workspace has room for.
+    int ctas, least, slots;
+    float unit_cost;
     // partial results of row tiles in several parts (attention_workspace)
-    int32_t *count;              // of such row tiles
-    Item *items;
     float2 *ml;                  // [slot][ROWS]: running maximum and sum
     float *part;                 // [slot][ROWS][D]
     int *status;
@@ -91,14 +87,15 @@ __device__ __forceinline__ Span span_of(const Attn &a, const Seq &s, int r0, int
 // ---------------------------------------------------------------------------------------
 template <int NT>
 struct PlanSmem {
-    int units[NT + 1], slots[NT + 1], items[NT + 1];    // before thread j's sequences
+    int units[NT + 1], slots[NT + 1], items[NT + 1];    // before thread j's sequences; items: row tiles in several parts
     long long work[NT / 32];
     int sums[3][NT / 32];
+    int length;
 };
 
 struct Unit {
     int b, h, tile, part, parts;
-    int slot, item;                 // of the row tile's first part (parts > 1)
+    int slot;                       // of the row tile's first part (parts > 1)
     Seq s;
 };
 
@@ -116,6 +113,49 @@ struct Plan {
         parts = tiles ? max(1, (span_of<TILE>(a, s, (tiles - 1) * ROWS, rows - 1).n + length - 1) / length) : 0;
     }
 
+    // Up to 32 sequences, by one warp, a sequence a lane: the length of a part by trying 32 of them, a lane
+    // each, on an estimate of the time of the slowest CTA.  A batch of equal units takes whole rounds of the CTAs;
+    // one of unequal units its average and one more unit.
+    __device__ __forceinline__ int best_length(const Attn &a, int rows, int first, int last) const
+    {
+        const int lane = threadIdx.x & 31, tiles = (rows + ROWS - 1) / ROWS * a.p.heads;     // of the lane's sequence
+        int most = last, items = tiles;
+        float work = 0.5f * (float)tiles * (float)(first + last);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+            work += __shfl_xor_sync(0xffffffffu, work, o);
+        }
+        if (most <= a.least || items <= 0) return max(most, 1);
+        // Parts of the longest row tile: what makes 1/8 .. 32/8 rounds of the CTAs; one is always tried.
+        int p = lane ? (int)min((long long)(lane + 1) * a.ctas / (8 * (long long)items), (long long)(most / a.least)) : 1;
+        p = max(p, 1);
+        const int len = (most + p - 1) / p;
+        long long units = 0, slots = 0;
+        for (int b = 0; b < a.p.seqs; ++b) {
+            const int t = __shfl_sync(0xffffffffu, tiles, b), n = __shfl_sync(0xffffffffu, last, b);
+            const int parts = max((n + len - 1) / len, 1);
+            units += (long long)t * parts;
+            if (parts > 1) slots += (long long)t * parts;
+        }
+        const float g = (float)a.ctas, longest = (float)len + a.unit_cost;
+        float cost = min(ceilf((float)units / g) * longest, (work + a.unit_cost * (float)units) / g + longest);
+        if (slots) cost += a.unit_cost;
+        if (slots > a.slots) cost = INFINITY;
+        int best = len;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+            const int l = __shfl_xor_sync(0xffffffffu, best, o);
+            if (c < cost || (c == cost && l > best)) {
+                cost = c;
+                best = l;
+            }
+        }
+        return best;
+    }
+
     // Called by all threads of the CTA.
     __device__ __forceinline__ void make(const Attn &a, PlanSmem<NT> &sm)
     {
@@ -123,22 +163,41 @@ struct Plan {
         const bool counts = t < NT;
         per = (a.p.seqs + NT - 1) / NT;
         const int b0 = counts ? min(t * per, a.p.seqs) : 0, b1 = counts ? min(b0 + per, a.p.seqs) : 0;
-        long long w = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(a.p, b);
-            const int rows = s.n * a.group;
-            if (rows) w += (long long)((rows + ROWS - 1) / ROWS) *
-                           span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
+        if (a.p.seqs <= 32) {
+            if (warp == 0) {
+                int rows = 0, first = 0, last = 0;
+                if (lane < a.p.seqs) {
+                    const Seq s = seq_of(a.p, lane);
+                    rows = s.n * a.group;
+                    if (rows) {
+                        first = span_of<TILE>(a, s, 0, min(rows, ROWS) - 1).n;
+                        last = span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
+                    }
+                }
+                const int l = best_length(a, rows, first, last);
+                if (lane == 0) sm.length = l;
+            }
+            __syncthreads();
+            length = sm.length;
+        } else {
+            // Parts of equal length, as many as the workspace has room for: a row tile of p > 1 parts has more than
+            // (p - 1) * length >= p * length / 2 key tiles, so there are fewer than twice work / length of them.
+            long long w = 0;
+            for (int b = b0; b < b1; ++b) {
+                const Seq s = seq_of(a.p, b);
+                const int rows = s.n * a.group;
+                if (rows) w += (long long)((rows + ROWS - 1) / ROWS) * span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (counts && lane == 0) sm.work[warp] = w;
+            __syncthreads();
+            w = 0;
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) w += sm.work[i];
+            w = (2 * w * a.p.heads + a.slots - 1) / a.slots;
+            length = (int)min(max(w, (long long)a.least), (long long)INT_MAX / 2);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        if (counts && lane == 0) sm.work[warp] = w;
-        __syncthreads();
-        w = 0;
-#pragma unroll
-        for (int i = 0; i < NT / 32; ++i) w += sm.work[i];
-        w = (w * a.p.heads + a.target - 1) / a.target;
-        length = (int)min(max(w, (long long)a.least), (long long)INT_MAX / 2);
 
         int v[3] = {0, 0, 0};
         for (int b = b0; b < b1; ++b) {
@@ -163,12 +222,14 @@ struct Plan {
             }
             if (counts && lane == 31) sm.sums[i][warp] = sum[i];
         }
-        __syncthreads();
+        if constexpr (NT > 32) {
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < 3; ++i) {
 #pragma unroll
-            for (int j = 0; j < NT / 32; ++j)
-                if (j < warp) sum[i] += sm.sums[i][j];
+                for (int j = 0; j < NT / 32; ++j)
+                    if (j < warp) sum[i] += sm.sums[i][j];
+            }
         }
         if (counts) {
             sm.units[t] = sum[0] - v[0];
@@ -184,34 +245,51 @@ struct Plan {
         total = sm.units[NT];
     }
 
-    // Called by whole warps.
-    __device__ __forceinline__ Unit find(const Attn &a, const PlanSmem<NT> &sm, int u) const
+    // The sequence of unit (or, of those in several parts, row tile) u, and what is left of u in it.  Called by
+    // whole warps.
+    template <bool ITEMS>
+    __device__ __forceinline__ Unit sequence(const Attn &a, const PlanSmem<NT> &sm, int u, int &left, int &tiles) const
     {
+        const int *before = ITEMS ? sm.items : sm.units;
         int lo = -1;                                // the last thread that starts at or before u
 #pragma unroll
-        for (int i = 0; i < NT; i += 32) lo += __popc(__ballot_sync(0xffffffffu, sm.units[i + (threadIdx.x & 31)] <= u));
+        for (int i = 0; i < NT; i += 32) lo += __popc(__ballot_sync(0xffffffffu, before[i + (threadIdx.x & 31)] <= u));
         Unit x;
-        int left = u - sm.units[lo], tiles, parts;
+        left = u - before[lo];
         x.slot = sm.slots[lo];
-        x.item = sm.items[lo];
         for (x.b = lo * per;; ++x.b) {              // ends: u < total
             x.s = seq_of(a.p, x.b);
-            shape(a, x.s, tiles, parts);
-            const int n = tiles * parts * a.p.heads;
-            if (left < n || x.b + 1 >= a.p.seqs) break;
-            left -= n;
-            if (parts > 1) {
-                x.slot += n;
-                x.item += tiles * a.p.heads;
-            }
+            shape(a, x.s, tiles, x.parts);
+            const int n = tiles * a.p.heads, units = n * x.parts, mine = !ITEMS ? units : x.parts > 1 ? n : 0;
+            if (left < mine || x.b + 1 >= a.p.seqs) break;
+            left -= mine;
+            if (x.parts > 1) x.slot += units;
         }
-        x.parts = parts;
-        x.part = left % parts;
-        const int it = left / parts;
-        x.tile = tiles - 1 - a.by_heads(it);
-        x.h = it - a.by_heads(it) * a.p.heads;
-        x.slot += it * parts;
-        x.item += it;
+        return x;
+    }
+    __device__ __forceinline__ void place(const Attn &a, Unit &x, int item, int tiles) const
+    {
+        x.tile = tiles - 1 - a.by_heads(item);
+        x.h = item - a.by_heads(item) * a.p.heads;
+        x.slot += item * x.parts;
+    }
+
+    __device__ __forceinline__ Unit find(const Attn &a, const PlanSmem<NT> &sm, int u) const
+    {
+        int left, tiles;
+        Unit x = sequence<false>(a, sm, u, left, tiles);
+        const int item = left / x.parts;
+        x.part = left - item * x.parts;
+        place(a, x, item, tiles);
+        return x;
+    }
+    // Row tile i of those in several parts.
+    __device__ __forceinline__ Unit find_item(const Attn &a, const PlanSmem<NT> &sm, int i) const
+    {
+        int left, tiles;
+        Unit x = sequence<true>(a, sm, i, left, tiles);
+        x.part = 0;
+        place(a, x, left, tiles);
         return x;
     }
 };
@@ -286,23 +364,16 @@ __device__ __noinline__ float2 exact_statistics(const Attn &a, int b, int h, con
 // ---------------------------------------------------------------------------------------
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace for `target` parts of `rows` rows: a row tile of p > 1 parts has more than
-// (p - 1) * length >= p * length / 2 key tiles, so there are fewer slots than twice the target, and half as
-// many items.
-inline size_t attention_space(int target, int rows, int dim)
+// Workspace for so many partial results of row tiles.
+inline size_t attention_space(int slots, int rows, int dim)
 {
-    const size_t slots = 2 * (size_t)target;
-    return 256 + up256(slots / 2 * sizeof(Item)) + up256(slots * rows * sizeof(float2)) + slots * rows * (size_t)dim * sizeof(float);
+    return up256((size_t)slots * rows * sizeof(float2)) + (size_t)slots * rows * dim * sizeof(float);
 }
-inline void attention_place(Attn &a, void *ws, int target, int rows)
+inline void attention_place(Attn &a, void *ws, int slots, int rows)
 {
-    const size_t slots = 2 * (size_t)target;
-    uint8_t *p = static_cast<uint8_t *>(ws);
-    a.target = target;
-    a.count = reinterpret_cast<int32_t *>(p);
-    a.items = reinterpret_cast<Item *>(p + 256);
-    a.ml = reinterpret_cast<float2 *>(p + 256 + up256(slots / 2 * sizeof(Item)));
-    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.ml) + up256(slots * rows * sizeof(float2)));
+    a.slots = slots;
+    a.ml = static_cast<float2 *>(ws);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + up256((size_t)slots * rows * sizeof(float2)));
 }
 
 inline CUtensorMapDataType attention_type(const q8act_paged_kv &kv)
@@ -321,11 +392,11 @@ inline bool attention_maps(const q8act_paged_kv &kv, int rows, CUtensorMap *tk, 
            encode_tiled(tv, dt, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The kernel for chunks (attention_tc.cu): its workspace, its launch (a: all but the workspace's places), and
-// the joining kernel behind either.
-constexpr int CHUNK_ROWS = 256;
+// The kernel for chunks (attention_tc.cu): its workspace, its launch (a: all but how units are cut), and the joining
+// kernel behind either.
+constexpr int CHUNK_ROWS = 256, CHUNK_TILE = 128, CHUNK_COUNTERS = 32;
 size_t attention_chunk_space(int dim);
 cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &kv, Attn a, void *ws, cudaStream_t stream);
-cudaError_t launch_attention_join(const DeviceInfo &dev, const Attn &a, int dim, int rows, cudaStream_t stream);
+cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream);
 
 }  // namespace q8

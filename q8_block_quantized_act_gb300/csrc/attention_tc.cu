@@ -20,10 +20,10 @@
 namespace q8 {
 namespace {
 
-constexpr int TILE = 128;                // positions a step
+constexpr int TILE = CHUNK_TILE;         // positions a step
 constexpr int QROWS = 128;               // rows of a row tile
 constexpr int ROWS = CHUNK_ROWS;         // of a unit: two row tiles
-constexpr int COUNTERS = 32;             // threads that count the units
+constexpr int COUNTERS = CHUNK_COUNTERS; // threads that count the units
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;      // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
 constexpr int PARTS = 2;                 // of a tile's weights, handed to the MMAs one by one
@@ -266,7 +266,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     plan.make(a, sm.plan);                           // its barriers: the ones above exist for all
     tc_fence_after();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = sm.plan.items[COUNTERS];
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
 
     if (warp < 8) {
@@ -663,8 +662,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     rc.end = x.s.end;
                     rc.seq = x.b;
                     rc.slot = x.parts > 1 ? x.slot + x.part : -1;
-                    if (x.parts > 1 && x.part == 0 && lane == 0)
-                        a.items[x.item] = Item{x.slot, x.parts, x.s.row0, rc.r0, x.h, min(ROWS, rc.rows - rc.r0), {0, 0}};
                 }
                 if (lane == 0) {
                     sm.units[round % RECORDS] = rc;
@@ -725,15 +722,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-// A part for each of a GB300's 152 SMs.
-constexpr int TARGET = 152;
+// Partial results: of three rounds of a GB300's 152 SMs.
+constexpr int SLOTS = 3 * 152;
 
-size_t attention_chunk_space(int dim) { return attention_space(TARGET, ROWS, dim); }
+size_t attention_chunk_space(int dim) { return attention_space(SLOTS, ROWS, dim); }
 
 cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &kv, Attn a, void *ws, cudaStream_t stream)
 {
-    attention_place(a, ws, TARGET, ROWS);
+    attention_place(a, ws, SLOTS, ROWS);
+    a.ctas = dev.num_sms;
     a.least = 2;
+    a.unit_cost = 8.0f;
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     // Row tiles of whole tokens come as one box; others are gathered row by row.
@@ -746,7 +745,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     } else {
         tq = tk;
     }
-    const int64_t units = (int64_t)kv.heads * ((int64_t)a.p.m * a.group / ROWS + std::min(kv.seqs, a.p.m)) + TARGET;    // at most
+    const int64_t units = (int64_t)kv.heads * ((int64_t)a.p.m * a.group / ROWS + std::min(kv.seqs, a.p.m)) + SLOTS;    // at most
     const unsigned grid = (unsigned)std::min<int64_t>(units, dev.num_sms);
     return with_type(kv.type, [&](auto x) -> cudaError_t {
         using T = decltype(x);
@@ -760,7 +759,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
                 cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
                 e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
-                return e == cudaSuccess ? launch_attention_join(dev, a, D, ROWS, stream) : e;
+                return e == cudaSuccess ? launch_attention_chunk_join(dev, a, D, stream) : e;
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
         }
