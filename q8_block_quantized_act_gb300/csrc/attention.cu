@@ -1,14 +1,16 @@
 // attention.cu -- causal attention of a few new tokens a sequence (one: decoding) over a paged cache.
 //   s_j = scale q . k_j,  o = sum_j e^(s_j - mx) v_j / sum_j e^(s_j - mx)  over the visible positions j
 //
-// Bound by memory: each key and value is read once and serves the group's query heads.  A CTA walks
-// over the units of the batch (attention.cuh), so that 152 SMs are filled whatever the number and the
-// lengths of the sequences.  One warp brings 64 positions at a time to shared memory (TMA boxes of up to
-// a page, 128-byte swizzled, several stages ahead across units); four warps take 16 positions each,
-// with their own running maximum and sum, so they meet only at the end of a unit.  The products run on
-// the warp-level tensor-core MMA: 16 rows are too few for tcgen05's 128, and it is not what bounds.
-// Scores, statistics and sums are f32; the weights e^(s - mx) <= 1 are rounded to the cache's type for
-// the second product, whose operands have one type.
+// Bound by memory: each key and value is read once and serves the group's query heads.  All (row tile, 64
+// positions) pairs of the batch stand in one line, and each CTA takes an equal stretch of it, so that 152 SMs
+// are filled evenly whatever the number and the lengths of the sequences.  A row tile that a stretch cuts
+// has parts in several CTAs, which attention_rows_join adds up.
+//
+// One warp brings 64 positions at a time to shared memory (TMA boxes of up to a page, 128-byte swizzled, several
+// stages ahead across row tiles).  Four warps take 16 positions each, with their own running maximum and sum, so
+// they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16 to 64
+// rows are too few for tcgen05's 128, and it is not what bounds.  Scores, statistics and sums are f32; the weights
+// e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -17,27 +19,151 @@ namespace q8 {
 namespace {
 
 constexpr int TILE = 64;             // positions a stage
-constexpr int CONSUMERS = 4;         // warps, 16 positions each
-constexpr int THREADS = 32 * (CONSUMERS + 1);
-constexpr int ROWS = 16;
-constexpr int COUNTERS = 128;        // threads that count the units
+constexpr int KEY_WARPS = 4;         // 16 positions each
+constexpr int COUNTERS = 128;        // threads that count the work
 constexpr float NEG = -INFINITY;
 
-template <int D>
+// MT: 16-row tiles a warp, RG: groups of warps with rows of their own.
+template <int D, int MT, int RG>
 struct Cfg {
+    static constexpr int ROWS = 16 * MT * RG;
+    static constexpr int CTAS = MT * RG == 1 ? 2 : 1;           // to an SM
+    static constexpr int CONSUMERS = KEY_WARPS * RG, THREADS = 32 * (CONSUMERS + 1);
     static constexpr int TILE_BYTES = TILE * D * 2;             // of keys, and of values
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int STAGES = 96 * 1024 / STAGE_BYTES;      // two CTAs to an SM
+    static constexpr int STAGES = (CTAS == 2 ? 96 : RG == 1 ? 192 : 160) * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                       // 128-byte wide columns of a tile
+    static constexpr int Q_STRIDE = D * 2 + 16;                 // bytes: rows in different banks
+    static constexpr int Q_BYTES = ROWS * Q_STRIDE;
+    static constexpr int OFF_Q = STAGES * STAGE_BYTES, OFF_SHARED = OFF_Q + 2 * Q_BYTES;
 };
 
+template <int ROWS>
 struct Shared {
-    PlanSmem<COUNTERS> plan;
-    uint64_t full[8], empty[8];
-    uint32_t ok[8];                       // a stage's 16-position blocks whose page exists
-    float mx[2][CONSUMERS][ROWS], sum[2][CONSUMERS][ROWS];
-    int spoilt[2][CONSUMERS];             // a non-finite value that not all rows see
+    long long before[COUNTERS + 1];       // work before thread j's sequences
+    long long sums[COUNTERS / 32];
+    uint64_t full[12], empty[12], q_full[2], q_empty[2];
+    uint32_t ok[12];                      // a stage's 16-position blocks whose page exists
+    float mx[2][KEY_WARPS][ROWS], sum[2][KEY_WARPS][ROWS];
+    int spoilt[2][KEY_WARPS * 2];         // a non-finite value that not all rows see
     int abort_flag;
+};
+
+// ---------------------------------------------------------------------------------------
+// The line of work: the sequences one after another, in each the row tiles and in these the heads, each with
+// the key tiles that its longest row tile sees (one at least, so that rows that see nothing are written too).
+// ---------------------------------------------------------------------------------------
+struct Line {
+    int per;               // sequences a counting thread
+    long long total, length;      // key tiles, and of a CTA's stretch
+
+    // Row tiles x heads of a sequence, and key tiles of each.
+    template <int ROWS>
+    static __device__ __forceinline__ void shape(const Attn &a, const Seq &s, int &items, int &n)
+    {
+        const int rows = s.n * a.group, tiles = (rows + ROWS - 1) / ROWS;
+        items = tiles * a.p.heads;
+        n = 0;
+        if (!tiles) return;
+        n = span_of<TILE>(a, s, (tiles - 1) * ROWS, rows - 1).n;
+        if (tiles > 1 && a.window) {        // another row tile's window may touch one tile more
+            const int tokens = (ROWS + a.group - 2) / a.group + 1;
+            n = min(min(s.pos0 + s.n, s.end), 0x3fffffff) / TILE + 1;
+            n = min(n, (int)((a.window + (long long)tokens + TILE - 3) / TILE) + 1);
+        }
+        n = max(n, 1);
+    }
+
+    // Called by all threads of the CTA.
+    template <int ROWS>
+    __device__ __forceinline__ void make(const Attn &a, long long *before, long long *sums)
+    {
+        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        per = (a.p.seqs + COUNTERS - 1) / COUNTERS;
+        long long w = 0;
+        if (t < COUNTERS) {
+            for (int b = t * per; b < min(t * per + per, a.p.seqs); ++b) {
+                int items, n;
+                shape<ROWS>(a, seq_of(a.p, b), items, n);
+                w += (long long)items * n;
+            }
+        }
+        long long sum = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (t < COUNTERS && lane == 31) sums[warp] = sum;
+        __syncthreads();
+        if (t < COUNTERS) {
+#pragma unroll
+            for (int j = 0; j < COUNTERS / 32; ++j)
+                if (j < warp) sum += sums[j];
+            before[t] = sum - w;
+            if (t == COUNTERS - 1) before[COUNTERS] = sum;
+        }
+        __syncthreads();
+        total = before[COUNTERS];
+        length = max((total + a.ctas - 1) / a.ctas, (long long)a.least);
+    }
+};
+
+// A place on the line.
+template <int ROWS>
+struct Place {
+    int b, item, items, n, tile;       // sequence, row tile and head of so many, key tile of so many
+    Seq s;
+
+    // Key tile x of the line (x < total).  Called by whole warps.
+    __device__ __forceinline__ Place(const Attn &a, const Line &line, const long long *before, long long x)
+    {
+        int lo = -1;                   // the last thread that starts at or before x
+#pragma unroll
+        for (int i = 0; i < COUNTERS; i += 32) lo += __popc(__ballot_sync(0xffffffffu, before[i + (threadIdx.x & 31)] <= x));
+        long long left = x - before[lo];
+        for (b = lo * line.per;; ++b) {
+            s = seq_of(a.p, b);
+            Line::shape<ROWS>(a, s, items, n);
+            if (left < (long long)items * n || b + 1 >= a.p.seqs) break;
+            left -= (long long)items * n;
+        }
+        item = n ? (int)(left / n) : 0;
+        tile = (int)(left - (long long)item * n);
+    }
+    // The next row tile's first key tile (not behind the line's end).
+    __device__ __forceinline__ void next(const Attn &a)
+    {
+        tile = 0;
+        if (++item < items) return;
+        item = 0;
+        do {
+            if (++b >= a.p.seqs) return;
+            s = seq_of(a.p, b);
+            Line::shape<ROWS>(a, s, items, n);
+        } while (items == 0);
+    }
+};
+
+// The part of a row tile that a CTA's stretch holds.
+template <int ROWS>
+struct Part {
+    int h, r0, valid;                  // head of keys and values; first row and how many
+    int t0, t1;                        // key tiles
+    Span span;
+    bool whole;
+
+    __device__ __forceinline__ Part(const Attn &a, const Place<ROWS> &p, long long left)
+    {
+        const int tile = a.by_heads(p.item), end = (int)min((long long)p.n, p.tile + left);
+        h = p.item - tile * a.p.heads;
+        r0 = tile * ROWS;
+        valid = min(ROWS, p.s.n * a.group - r0);
+        span = span_of<TILE>(a, p.s, r0, r0 + valid - 1);
+        t0 = span.first + min(p.tile, span.n);
+        t1 = span.first + min(end, span.n);
+        whole = p.tile == 0 && end == p.n;
+    }
 };
 
 template <typename T>
@@ -86,42 +212,64 @@ __device__ __forceinline__ bool non_finite2(uint32_t w)
     return (w & E) == E || (w >> 16 & E) == E;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS, 2)
+template <typename T, int D, int MT, int RG>
+__global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
 {
-    using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    Shared &sm = *reinterpret_cast<Shared *>(stages + C::STAGES * C::STAGE_BYTES);
+    using C = Cfg<D, MT, RG>;
+    constexpr int ROWS = C::ROWS;
+    extern __shared__ __align__(1024) uint8_t stages[];
+    Shared<ROWS> &sm = *reinterpret_cast<Shared<ROWS> *>(stages + C::OFF_SHARED);
     volatile int *abort_flag = &sm.abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], CONSUMERS); }
+        for (int s = 0; s < C::STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], C::CONSUMERS); }
+        for (int s = 0; s < 2; ++s) { mbar_init(&sm.q_full[s], 1); mbar_init(&sm.q_empty[s], C::CONSUMERS); }
         sm.abort_flag = 0;
         fence_mbar_init();
     }
+    if (warp == C::CONSUMERS && lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
     griddep_wait();
     griddep_launch_dependents();
-    Plan<ROWS, TILE, COUNTERS> plan;
-    plan.make(a, sm.plan);                                       // and the barriers exist for all
+    Line line{};
+    line.make<ROWS>(a, sm.before, sm.sums);                      // and the barriers exist for all
+    long long x = blockIdx.x * line.length;
+    const long long x1 = min(x + line.length, line.total);
+    if (x >= x1) return;
+    Place<ROWS> place(a, line, sm.before, x);
 
-    if (warp == CONSUMERS) {
+    if (warp == C::CONSUMERS) {
         // ------------------------------ producer ------------------------------
         const int ps = 1 << a.p.page_shift, per_tile = ps < TILE ? TILE / ps : 1, blocks = 4 / per_tile;
-        int it = 0, st = 0;
+        int it = 0, st = 0, parts = 0;
         uint32_t phase = 1;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < plan.total; u += gridDim.x) {
-            const Unit x = plan.find(a, sm.plan, u);
-            const int rows = x.s.n * a.group, r0 = x.tile * ROWS, r1 = min(r0 + ROWS, rows) - 1;
-            const Span span = span_of<TILE>(a, x.s, r0, r1);
-            int t0, t1;
-            span.part(x.part, x.parts, t0, t1);
-            for (int t = t0; t < t1; ++t, ++it) {
+        for (; ok && x < x1; ++parts) {
+            const Part<ROWS> p(a, place, x1 - x);
+            const Seq s = place.s;
+            const int b = place.b;
+            x += min((long long)(place.n - place.tile), x1 - x);
+            place.next(a);
+            // Queries, a row a lane (rows behind the last one hold anything: what comes of them goes nowhere).
+            const int qb = parts & 1;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[qb], (parts >> 1 & 1) ^ 1, a.status, abort_flag));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[qb], p.valid * D * 2);
+            __syncwarp();
+            for (int i = lane; i < p.valid; i += 32) {
+                const int r = p.r0 + i, tok = a.by_group(r);
+                bulk_g2s(stages + C::OFF_Q + qb * C::Q_BYTES + i * C::Q_STRIDE,
+                         static_cast<const T *>(a.q) + (s.row0 + tok) * a.ldq + (p.h * a.group + r - tok * a.group) * D, D * 2,
+                         &sm.q_full[qb]);
+            }
+            __syncwarp();
+            for (int t = p.t0; t < p.t1; ++t, ++it) {
                 const int pos = t * TILE;
-                const int64_t page = lane < per_tile ? page_of(a.p, x.b, (pos >> a.p.page_shift) + lane) : -1;
+                const int64_t page = lane < per_tile ? page_of(a.p, b, (pos >> a.p.page_shift) + lane) : -1;
                 const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
                 uint32_t okm = 0;
                 for (int j = 0; j < per_tile; ++j)
@@ -135,14 +283,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                     mbar_arrive_expect_tx(&sm.full[st], C::STAGE_BYTES);
                 }
                 __syncwarp();
-                for (int i0 = 0; i0 < 2 * C::HALVES * per_tile; i0 += 32) {
-                    const int i = i0 + lane, j = i / (2 * C::HALVES), half = i % C::HALVES, is_v = i / C::HALVES % 2;
-                    const int box_page = __shfl_sync(0xffffffffu, id, j & 31);
-                    if (i < 2 * C::HALVES * per_tile)
-                        tma_load_4d(stages + st * C::STAGE_BYTES + is_v * C::TILE_BYTES + half * (TILE * 128) + j * ps * 128,
-                                    is_v ? &tm_v : &tm_k, half * 64, ps > TILE ? pos & (ps - 1) : 0, x.h, box_page,
-                                    &sm.full[st]);
-                }
+                const int j = lane / (2 * C::HALVES), half = lane % C::HALVES, is_v = lane / C::HALVES % 2;
+                const int box_page = __shfl_sync(0xffffffffu, id, j);
+                if (j < per_tile)
+                    tma_load_4d(stages + st * C::STAGE_BYTES + is_v * C::TILE_BYTES + half * (TILE * 128) + j * ps * 128,
+                                is_v ? &tm_v : &tm_k, half * 64, ps > TILE ? pos & (ps - 1) : 0, p.h, box_page, &sm.full[st]);
                 if (++st == C::STAGES) {
                     st = 0;
                     phase ^= 1;
@@ -152,102 +297,120 @@ __global__ void __launch_bounds__(THREADS, 2)
         // Never leave with a copy into this CTA's shared memory in flight.
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
             mbar_wait_drain(&sm.full[i % C::STAGES], (i / C::STAGES) & 1, a.status);
+        for (int i = parts > 2 ? parts - 2 : 0; i < parts; ++i) mbar_wait_drain(&sm.q_full[i & 1], i >> 1 & 1, a.status);
         return;
     }
 
     // ------------------------------ consumers ------------------------------
-    const int g = lane >> 2, c = lane & 3;
+    const int g = lane >> 2, c = lane & 3, kw = warp % KEY_WARPS, rg = warp / KEY_WARPS;
     const uint32_t stage0 = smem_u32(stages);
-    // Rows of this lane's ldmatrix addresses: keys in their own order, values transposed.
-    const int krow = warp * 16 + (lane & 7) + (lane >> 4) * 8, kchunk = lane >> 3 & 1;
-    const int vrow = warp * 16 + (lane & 7) + (lane >> 3 & 1) * 8, vchunk = lane >> 4;
-    int it = 0, st = 0, flip = 0;
+    // Rows of this lane's ldmatrix addresses: queries, keys in their own order, values transposed.
+    const uint32_t q0 = stage0 + C::OFF_Q + (rg * MT * 16 + (lane & 7) + (lane >> 3 & 1) * 8) * C::Q_STRIDE + (lane >> 4) * 16;
+    const int krow = kw * 16 + (lane & 7) + (lane >> 4) * 8, kchunk = lane >> 3 & 1;
+    const int vrow = kw * 16 + (lane & 7) + (lane >> 3 & 1) * 8, vchunk = lane >> 4;
+    const long long x0 = x;
+    int st = 0;
     uint32_t phase = 0;
-    for (int u = blockIdx.x; u < plan.total; u += gridDim.x) {
-        const Unit x = plan.find(a, sm.plan, u);
-        const int rows = x.s.n * a.group, r0 = x.tile * ROWS, valid = min(ROWS, rows - r0);
-        const Span span = span_of<TILE>(a, x.s, r0, r0 + valid - 1);
-        int t0, t1;
-        span.part(x.part, x.parts, t0, t1);
-        const int first = x.s.pos0 + a.by_group(r0), last = x.s.pos0 + a.by_group(r0 + valid - 1);    // positions of its rows
+    for (int parts = 0; x < x1; ++parts) {
+        const Part<ROWS> p(a, place, x1 - x);
+        const Seq s0 = place.s;
+        const int b = place.b, flip = parts & 1;
+        const int slot = p.whole ? -1 : 2 * (int)blockIdx.x + (x != x0);
+        x += min((long long)(place.n - place.tile), x1 - x);
+        place.next(a);
+        const int first = s0.pos0 + a.by_group(p.r0), last = s0.pos0 + a.by_group(p.r0 + p.valid - 1);    // positions of its rows
 
-        // Two rows a lane: g and g + 8.
-        uint32_t q[D / 16][4];
-        int lo[2], hi[2];
+        // Two rows a lane and 16-row tile: g and g + 8.
+        int lo[MT][2], hi[MT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = r0 + g + 8 * i;
-            const bool live = r < rows;
-            const int tok = live ? a.by_group(r) : 0;
-            const int pos = x.s.pos0 + tok;
-            hi[i] = live ? min(pos, x.s.end - 1) : -1;
-            lo[i] = a.window ? max(pos - a.window + 1, 0) : 0;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + (x.h * a.group + (live ? r - tok * a.group : 0)) * D) + c;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                q[kk][i] = live ? __ldg(src + kk * 8) : 0u;
-                q[kk][i + 2] = live ? __ldg(src + kk * 8 + 4) : 0u;
+            for (int i = 0; i < 2; ++i) {
+                const int r = (rg * MT + mt) * 16 + g + 8 * i, pos = s0.pos0 + a.by_group(p.r0 + r);
+                hi[mt][i] = r < p.valid ? min(pos, s0.end - 1) : -1;
+                lo[mt][i] = a.window ? max(pos - a.window + 1, 0) : 0;
             }
+        float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            mx[mt][0] = mx[mt][1] = NEG;
+            sum[mt][0] = sum[mt][1] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.0f;
         }
-        float o[D / 8][4], mx[2] = {NEG, NEG}, sum[2] = {0.0f, 0.0f};
+        bool spoilt = false;
+        bool aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.q_full[flip], parts >> 1 & 1, a.status, abort_flag));
+        const uint32_t qs = q0 + flip * C::Q_BYTES;
+        // One 16-row tile's queries stay in registers; of more, they are read from shared memory again.
+        uint32_t q[MT == 1 ? D / 16 : 1][4];
+        if constexpr (MT == 1) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-        bool aborted = false, spoilt = false;
+            for (int kk = 0; kk < D / 16; ++kk) ldmatrix_x4(q[kk], qs + kk * 32);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_empty[flip]);
+        }
 
-        for (int t = t0; t < t1; ++t, ++it) {
-            aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
+        for (int t = p.t0; t < p.t1; ++t) {
+            if (!aborted) aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
             if (aborted) break;
             const uint32_t kt = stage0 + st * C::STAGE_BYTES, vt = kt + C::TILE_BYTES;
-            const bool page_ok = sm.ok[st] >> warp & 1;
-            float s[2][4] = {};
+            const bool page_ok = sm.ok[st] >> kw & 1;
+            float s[MT][2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t kf[4];
                 const int chunk = kk * 2 + kchunk;
                 ldmatrix_x4(kf, kt + (chunk >> 3) * (TILE * 128) + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4));
-                mma_16816<T>(s[0], q[kk], kf[0], kf[1]);
-                mma_16816<T>(s[1], q[kk], kf[2], kf[3]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    if constexpr (MT > 1) ldmatrix_x4(q[0], qs + mt * (16 * C::Q_STRIDE) + kk * 32);
+                    const uint32_t(&qf)[4] = q[MT == 1 ? kk : 0];
+                    mma_16816<T>(s[mt][0], qf, kf[0], kf[1]);
+                    mma_16816<T>(s[mt][1], qf, kf[2], kf[3]);
+                }
             }
             // Columns of s[n]: positions key0 + 8 n + 2 c and the next; rows g (0, 1) and g + 8 (2, 3).
-            const int key0 = t * TILE + warp * 16;
+            const int key0 = t * TILE + kw * 16;
             // Whether some row does not see some of the 16.
-            const bool part = key0 < span.lo || key0 + 15 > min(first, span.hi) || (a.window && key0 <= last - a.window) || !page_ok;
-            if (part) {
+            const bool part = key0 < p.span.lo || key0 + 15 > min(first, p.span.hi) || (a.window && key0 <= last - a.window) || !page_ok;
+            uint32_t pf[MT][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+            for (int mt = 0; mt < MT; ++mt) {
+                if (part) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0 + 8 * n + 2 * c + (i & 1);
-                        if (key < lo[i >> 1] || key > hi[i >> 1] || !page_ok) s[n][i] = NEG;
-                    }
-            }
-            uint32_t p[4];
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                m = fmaxf(mx[i], m * a.scale);
-                if (__any_sync(0xffffffffu, m > mx[i])) {
-                    const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
-                    sum[i] *= f;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][2 * i] *= f;
-                        o[n][2 * i + 1] *= f;
-                    }
-                    mx[i] = m;
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = key0 + 8 * n + 2 * c + (i & 1);
+                            if (key < lo[mt][i >> 1] || key > hi[mt][i >> 1] || !page_ok) s[mt][n][i] = NEG;
+                        }
                 }
-                const float base = m == NEG ? 0.0f : m;
-                float e[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[j >> 1][2 * i + (j & 1)], a.scale, -base));
-                sum[i] += (e[0] + e[1]) + (e[2] + e[3]);
-                p[i] = pack2<T>(e[0], e[1]);
-                p[i + 2] = pack2<T>(e[2], e[3]);
+                for (int i = 0; i < 2; ++i) {
+                    float m = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    m = fmaxf(mx[mt][i], m * a.scale);
+                    if (__any_sync(0xffffffffu, m > mx[mt][i])) {
+                        const float f = attn_ex2(mx[mt][i] - (m == NEG ? 0.0f : m));
+                        sum[mt][i] *= f;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[mt][n][2 * i] *= f;
+                            o[mt][n][2 * i + 1] *= f;
+                        }
+                        mx[mt][i] = m;
+                    }
+                    const float base = m == NEG ? 0.0f : m;
+                    float e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[mt][j >> 1][2 * i + (j & 1)], a.scale, -base));
+                    sum[mt][i] += (e[0] + e[1]) + (e[2] + e[3]);
+                    pf[mt][i] = pack2<T>(e[0], e[1]);
+                    pf[mt][i + 2] = pack2<T>(e[2], e[3]);
+                }
             }
             // Values of positions that no row sees are cleared.
             uint32_t keep[2] = {~0u, ~0u};
@@ -255,8 +418,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int key = key0 + 8 * i + 2 * c;
-                    keep[i] = (key >= span.lo && key <= span.hi ? 0xffffu : 0u) |
-                              (key + 1 >= span.lo && key + 1 <= span.hi ? 0xffff0000u : 0u);
+                    keep[i] = (key >= p.span.lo && key <= p.span.hi ? 0xffffu : 0u) |
+                              (key + 1 >= p.span.lo && key + 1 <= p.span.hi ? 0xffff0000u : 0u);
                 }
             }
 #pragma unroll
@@ -271,11 +434,14 @@ __global__ void __launch_bounds__(THREADS, 2)
                         spoilt |= non_finite2<T>(vf[i]);
                     }
                 }
-                mma_16816<T>(o[2 * n], p, vf[0], vf[1]);
-                mma_16816<T>(o[2 * n + 1], p, vf[2], vf[3]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma_16816<T>(o[mt][2 * n], pf[mt], vf[0], vf[1]);
+                    mma_16816<T>(o[mt][2 * n + 1], pf[mt], vf[2], vf[3]);
+                }
             }
-            // The unit's last stage is handed back after the join, which uses its memory.
-            if (t + 1 < t1) {
+            // The last stage is handed back after the join, which uses its memory.
+            if (t + 1 < p.t1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
                 if (++st == C::STAGES) {
@@ -285,72 +451,89 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
         }
 
-        // ---- join of the four warps ----
+        // ---- join of the four warps with the same rows ----
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-            if (c == 0) {
-                sm.mx[flip][warp][g + 8 * i] = mx[i];
-                sm.sum[flip][warp][g + 8 * i] = sum[i];
-            }
-        }
-        spoilt = __any_sync(0xffffffffu, spoilt);
-        if (lane == 0) sm.spoilt[flip][warp] = spoilt;
-        if (bar_red_or(1, 32 * CONSUMERS, aborted)) return;
-        const bool some = t1 > t0;
-        float *join = reinterpret_cast<float *>(stages + st * C::STAGE_BYTES);      // [warp][row][D], 16-byte words swizzled by row
-        if (some) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = g + 8 * i;
-                float m = NEG;
-#pragma unroll
-                for (int w = 0; w < CONSUMERS; ++w) m = fmaxf(m, sm.mx[flip][w][r]);
-                const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    const int col = (8 * n + 2 * c) ^ ((r & 7) << 2);
-                    *reinterpret_cast<float2 *>(join + (warp * ROWS + r) * D + col) = make_float2(o[n][2 * i] * f, o[n][2 * i + 1] * f);
+                sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 1);
+                sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 2);
+                if (c == 0) {
+                    sm.mx[flip][kw][(rg * MT + mt) * 16 + g + 8 * i] = mx[mt][i];
+                    sm.sum[flip][kw][(rg * MT + mt) * 16 + g + 8 * i] = sum[mt][i];
                 }
             }
-            named_bar_sync(2, 32 * CONSUMERS);
-        }
-        {
-            const int r = threadIdx.x >> 3, c8 = threadIdx.x & 7;        // a row, and every eighth vector of it
-            if (r < valid) {
+        spoilt = __any_sync(0xffffffffu, spoilt);
+        if (lane == 0) sm.spoilt[flip][warp] = spoilt;
+        // (the next part's words go to the other flip: some warps may still read these.  They are written again only
+        // behind the next part's barrier)
+        if (bar_red_or(1, 32 * C::CONSUMERS, aborted)) return;
+        if (MT > 1 && lane == 0) mbar_arrive(&sm.q_empty[flip]);
+        const bool some = p.t1 > p.t0;
+        float *join = reinterpret_cast<float *>(stages + st * C::STAGE_BYTES);      // [warp][row][D], 16-byte words swizzled by row
+#pragma unroll
+        for (int m16 = 0; m16 < MT * RG; ++m16) {
+            if (m16 * 16 >= p.valid) break;
+            if (some) {
+                if (m16 > 0) named_bar_sync(2, 32 * C::CONSUMERS);
+                if (rg == m16 / MT) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = g + 8 * i;
+                        float m = NEG;
+#pragma unroll
+                        for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][m16 * 16 + r]);
+                        const float f = attn_ex2(mx[m16 % MT][i] - (m == NEG ? 0.0f : m));
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            const int col = (8 * n + 2 * c) ^ ((r & 7) << 2);
+                            *reinterpret_cast<float2 *>(join + (kw * 16 + r) * D + col) =
+                                make_float2(o[m16 % MT][n][2 * i] * f, o[m16 % MT][n][2 * i + 1] * f);
+                        }
+                    }
+                }
+                named_bar_sync(2, 32 * C::CONSUMERS);
+            }
+            const int r = (threadIdx.x >> 3) & 15, c8 = threadIdx.x & 7;        // a row, and every eighth vector of it
+            const int rr = m16 * 16 + r;
+            if (rg == m16 / MT && rr < p.valid) {
                 float m = NEG, l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < CONSUMERS; ++w) m = fmaxf(m, sm.mx[flip][w][r]);
+                for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][rr]);
                 const float base = m == NEG ? 0.0f : m;
 #pragma unroll
-                for (int w = 0; w < CONSUMERS; ++w) l += sm.sum[flip][w][r] * attn_ex2(sm.mx[flip][w][r] - base);
+                for (int w = 0; w < KEY_WARPS; ++w) l += sm.sum[flip][w][rr] * attn_ex2(sm.mx[flip][w][rr] - base);
                 float acc[D / 8];
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) acc[j] = 0.0f;
                 if (some) {
 #pragma unroll
-                    for (int w = 0; w < CONSUMERS; ++w)
+                    for (int w = 0; w < KEY_WARPS; ++w)
 #pragma unroll
                         for (int j = 0; j < D / 32; ++j) {
                             const float4 v = *reinterpret_cast<const float4 *>(
-                                join + (w * ROWS + r) * D + (((j * 8 + c8) ^ (r & 7)) << 2));
+                                join + (w * 16 + r) * D + (((j * 8 + c8) ^ (r & 7)) << 2));
                             acc[4 * j] += v.x;
                             acc[4 * j + 1] += v.y;
                             acc[4 * j + 2] += v.z;
                             acc[4 * j + 3] += v.w;
                         }
                 }
-                const int row = r0 + r, tok = a.by_group(row), head = x.h * a.group + row - tok * a.group;
-                const int *sp = sm.spoilt[flip];
-                if (sp[0] | sp[1] | sp[2] | sp[3]) {
-                    const int pos = x.s.pos0 + tok;
-                    const int k0 = max(a.window ? pos - a.window + 1 : 0, t0 * TILE), k1 = min(min(pos, x.s.end - 1), t1 * TILE - 1);
-                    exact_values<T, D>(a, x.b, x.h, static_cast<const T *>(a.q) + (x.s.row0 + tok) * a.ldq + head * D, k0, k1,
-                                       base, [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); }, acc);
+                const int row = p.r0 + rr, tok = a.by_group(row), head = p.h * a.group + row - tok * a.group;
+                int sp = 0;
+#pragma unroll
+                for (int w = 0; w < C::CONSUMERS; ++w) sp |= sm.spoilt[flip][w];
+                if (sp) {
+                    const int pos = s0.pos0 + tok;
+                    const int k0 = max(a.window ? pos - a.window + 1 : 0, p.t0 * TILE), k1 = min(min(pos, s0.end - 1), p.t1 * TILE - 1);
+                    float e[D / 8];
+                    exact_values<T, D>(a, b, p.h, static_cast<const T *>(a.q) + (s0.row0 + tok) * a.ldq + head * D, k0, k1,
+                                       base, [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); }, e);
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) acc[j] = e[j];
                 }
-                if (x.parts > 1) {
-                    const int64_t at = (int64_t)(x.slot + x.part) * ROWS + r;
+                if (slot >= 0) {
+                    const int64_t at = (int64_t)slot * ROWS + rr;
                     if (c8 == 0) a.ml[at] = make_float2(m, l);
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j)
@@ -359,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 } else {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // a row that sees nothing: 0
                     uint8_t *dst = static_cast<uint8_t *>(a.out) +
-                                   ((x.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
+                                   ((s0.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j)
                         store4(dst + (j * 8 + c8) * 4 * out_size(a.otype), a.otype,
@@ -376,104 +559,144 @@ __global__ void __launch_bounds__(THREADS, 2)
                 phase ^= 1;
             }
         }
-        // The next unit's statistics go to the other words: some warps may still read these.  They are
-        // written again only behind the next unit's barrier.
-        flip ^= 1;
     }
 }
 
-// ---------------------------------------------------------------------------------------
-// Row tiles in several parts: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i, added in the parts' order.
-// Few rows come in many parts (decoding), which W warps of a CTA share; many rows in few, a row a warp.
-// ---------------------------------------------------------------------------------------
-// The kernel works out which rows it joins while the parts are still being computed.
-// ---------------------------------------------------------------------------------------
-constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_WARPS = 4, JOIN_Y = 4;
 
-template <int D, int ROWS_, int TILE_, int NT, int W>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
+// A row's parts, added in their order by four warps: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i.
+// slot(i): where part i is.
+template <int D, int ROWS, typename Slot>
+__device__ __forceinline__ void join_row(const Attn &a, int parts, Slot slot, int r, uint8_t *dst, float (&acc)[JOIN_WARPS][D],
+                                         float (&mw)[JOIN_WARPS], float (&lw)[JOIN_WARPS])
 {
     constexpr int V = D / 32;                // values a lane
-    __shared__ PlanSmem<NT> sm;
-    __shared__ alignas(16) float acc[W > 1 ? W : 1][D];
-    __shared__ float mw[W], lw[W];
-    const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
-    // (what starts, lens and the table hold was there before the kernel in front, which has waited for it)
-    Plan<ROWS_, TILE_, NT> plan;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float m = NEG;
+    for (int s = warp * 32 + lane; s < parts; s += 32 * JOIN_WARPS) m = fmaxf(m, a.ml[(int64_t)slot(s) * ROWS + r].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) mw[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, mw[w]);
+    const float base = m == NEG ? 0.0f : m;
+    float l = 0.0f, v[V] = {};
+    const int s0 = parts * warp / JOIN_WARPS, s1 = parts * (warp + 1) / JOIN_WARPS;
+#pragma unroll 8
+    for (int s = s0; s < s1; ++s) {
+        const int64_t at = (int64_t)slot(s) * ROWS + r;
+        const float2 ms = a.ml[at];
+        const float f = attn_ex2(ms.x - base);
+        l = fmaf(ms.y, f, l);
+        float w[V];
+        if constexpr (V == 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
+            const float2 u = *reinterpret_cast<const float2 *>(a.part + at * D + 2 * lane);
+            w[0] = u.x; w[1] = u.y;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
+    if (lane == 0) lw[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) {
+            const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
+            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+            l += lw[w];
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+    }
+    __syncthreads();
+}
+
+// CTA (c, y) joins the row tile that the end of stretch c cuts first, rows y, y + 4, ...  It works out which one while
+// the parts are still being computed (what starts and lens hold was there before the kernel in front, which
+// has waited for it).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(Attn a)
+{
+    __shared__ long long before[COUNTERS + 1], sums[COUNTERS / 32];
+    __shared__ alignas(16) float acc[JOIN_WARPS][D];
+    __shared__ float mw[JOIN_WARPS], lw[JOIN_WARPS];
+    Line line{};
+    line.make<ROWS>(a, before, sums);
+    const long long len = line.length, x = (blockIdx.x + 1) * len;
+    if (x < line.total) {
+        const Place<ROWS> p(a, line, before, x);
+        const long long start = x - p.tile;                  // of the row tile
+        if (p.tile > 0 && x - len <= start) {
+            const int k0 = blockIdx.x, parts = (int)((start + p.n - 1) / len) - k0 + 1;
+            const int tile = a.by_heads(p.item), h = p.item - tile * a.p.heads, valid = min(ROWS, p.s.n * a.group - tile * ROWS);
+            griddep_wait();
+            for (int r = blockIdx.y; r < valid; r += JOIN_Y) {
+                const int row = tile * ROWS + r, tok = a.by_group(row), head = h * a.group + row - tok * a.group;
+                // Its first part is its stretch's last one, unless the stretch begins with it; the others are first.
+                join_row<D, ROWS>(a, parts, [&](int i) { return 2 * (k0 + i) + (i == 0 && x - len < start); }, r,
+                                  static_cast<uint8_t *>(a.out) + ((p.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype), acc, mw, lw);
+            }
+        }
+    }
+    griddep_enter();
+}
+
+// ---------------------------------------------------------------------------------------
+// The same for row tiles of chunks, which have many rows in few parts: four rows at a time a warp.
+// ---------------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) attention_chunk_join_kernel(Attn a)
+{
+    constexpr int V = D / 32, ROWS = CHUNK_ROWS, R = 4;
+    __shared__ PlanSmem<CHUNK_COUNTERS> sm;
+    const int lane = threadIdx.x & 31;
+    Plan<ROWS, CHUNK_TILE, CHUNK_COUNTERS> plan;
     plan.make(a, sm);
-    const int n = sm.items[NT];
-    // A CTA's rows one by one, first rows first (the last of a row tile may not be there); or a warp's in fours.
-    constexpr int R = W > 1 ? 1 : 4;
-    const int work = n * (ROWS_ / R), step = gridDim.x * (JOIN_WARPS / W);
+    const int work = sm.items[CHUNK_COUNTERS] * (ROWS / R);
     bool waited = false;
-    for (int i = blockIdx.x * (JOIN_WARPS / W) + (W > 1 ? 0 : threadIdx.x >> 5); i < work; i += step) {
-        const int i0 = W > 1 ? i / n : i % (ROWS_ / R) * R;
-        const Unit it = plan.find_item(a, sm, W > 1 ? i - i0 * n : i / (ROWS_ / R));
+    for (int i = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5); i < work; i += gridDim.x * JOIN_WARPS) {
+        const Unit it = plan.find_item(a, sm, i / (ROWS / R));
         if (!waited) griddep_enter();
         waited = true;
-        const int rows = it.s.n * a.group - it.tile * ROWS_;
+        const int i0 = i % (ROWS / R) * R, rows = it.s.n * a.group - it.tile * ROWS;
 #pragma unroll 1
         for (int r = i0; r < min(i0 + R, rows); ++r) {
-            const int row = it.tile * ROWS_ + r;
-            const float2 *ml = a.ml + (int64_t)it.slot * ROWS_ + r;
-            const float *part = a.part + ((int64_t)it.slot * ROWS_ + r) * D + V * lane;
+            const float2 *ml = a.ml + (int64_t)it.slot * ROWS + r;
+            const float *part = a.part + ((int64_t)it.slot * ROWS + r) * D + V * lane;
             float m = NEG;
-            for (int s = warp * 32 + lane; s < it.parts; s += 32 * W) m = fmaxf(m, ml[(int64_t)s * ROWS_].x);
+            for (int s = lane; s < it.parts; s += 32) m = fmaxf(m, ml[(int64_t)s * ROWS].x);
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if constexpr (W > 1) {
-                if (lane == 0) mw[warp] = m;
-                __syncthreads();
-#pragma unroll
-                for (int w = 0; w < W; ++w) m = fmaxf(m, mw[w]);
-            }
             const float base = m == NEG ? 0.0f : m;
             float l = 0.0f, v[V] = {};
-            const int s0 = it.parts * warp / W, s1 = it.parts * (warp + 1) / W;
 #pragma unroll 4
-            for (int s = s0; s < s1; ++s) {
-                const float2 ms = ml[(int64_t)s * ROWS_];
+            for (int s = 0; s < it.parts; ++s) {
+                const float2 ms = ml[(int64_t)s * ROWS];
                 const float f = attn_ex2(ms.x - base);
                 l = fmaf(ms.y, f, l);
-                float w[V];
-                if constexpr (V == 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(part + (int64_t)s * ROWS_ * D);
-                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-                } else {
-                    const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS_ * D);
-                    w[0] = u.x; w[1] = u.y;
-                }
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
+                for (int j = 0; j < V; j += 2) {
+                    const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS * D + j);
+                    v[j] = fmaf(u.x, f, v[j]);
+                    v[j + 1] = fmaf(u.y, f, v[j + 1]);
+                }
             }
-            const int tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
+            const int row = it.tile * ROWS + r, tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
             uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
-            if constexpr (W > 1) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
-                if (lane == 0) lw[warp] = l;
-                __syncthreads();
-                if (threadIdx.x < D / 4) {
-                    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    l = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
-                        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-                        l += lw[w];
-                    }
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
-                }
-                __syncthreads();
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if constexpr (V == 4) {
+                store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
             } else {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                if constexpr (V == 4) {
-                    store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
-                } else {
-                    const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
-                    if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
-                }
+                const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
+                if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
             }
         }
     }
@@ -485,17 +708,16 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_join_kernel(Attn a)
 cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream)
 {
     auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a); };
-    return dim == 64 ? go(attention_join_kernel<64, CHUNK_ROWS, CHUNK_TILE, CHUNK_COUNTERS, 1>)
-                     : go(attention_join_kernel<128, CHUNK_ROWS, CHUNK_TILE, CHUNK_COUNTERS, 1>);
+    return dim == 64 ? go(attention_chunk_join_kernel<64>) : go(attention_chunk_join_kernel<128>);
 }
 
-// Partial results: of four rounds of a GB300's 152 SMs at two CTAs each, twice (Plan::make).
-constexpr int SLOTS = 2 * 4 * 2 * 152;
-
-size_t attention_workspace_bytes(int dim)
+// Two parts at most of each CTA that a GB300's 152 SMs hold.
+static size_t rows_space(int dim)
 {
-    return std::max(attention_space(SLOTS, ROWS, dim), attention_chunk_space(dim));
+    return std::max(attention_space(2 * 2 * 152, 16, dim), attention_space(2 * 152, 64, dim));
 }
+
+size_t attention_workspace_bytes(int dim) { return std::max(rows_space(dim), attention_chunk_space(dim)); }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &s, int64_t m,
                              cudaStream_t stream)
@@ -516,11 +738,8 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.scale = s.scale * 1.4426950408889634f;
     a.status = dev.status;
     const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
-    if (most * a.group > ROWS) return launch_attention_chunk(dev, kv, a, s.ws, stream);
-    attention_place(a, s.ws, SLOTS, ROWS);
-    a.ctas = 2 * dev.num_sms;
-    a.least = 1;
-    a.unit_cost = 2.0f;
+    const int64_t rows = most * a.group;
+    if (rows > 64) return launch_attention_chunk(dev, kv, a, s.ws, stream);
     CUtensorMap tk, tv;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     return with_type(kv.type, [&](auto x) -> cudaError_t {
@@ -528,16 +747,26 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
         if constexpr (sizeof(T) == 4) {
             return cudaErrorInvalidValue;
         } else {
-            auto go = [&](auto d) -> cudaError_t {
-                constexpr int D = decltype(d)::value;
-                constexpr size_t smem = 1024 + Cfg<D>::STAGES * Cfg<D>::STAGE_BYTES + sizeof(Shared);
-                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D>>(dev.device, smem);
+            auto go = [&](auto d, auto mt, auto rg) -> cudaError_t {
+                constexpr int D = decltype(d)::value, MT = decltype(mt)::value, RG = decltype(rg)::value;
+                using C = Cfg<D, MT, RG>;
+                constexpr size_t smem = C::OFF_SHARED + sizeof(Shared<C::ROWS>);
+                static_assert(smem <= (C::CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+                a.ctas = std::min(C::CTAS * dev.num_sms, C::CTAS * 152);
+                a.least = 2;
+                attention_place(a, s.ws, 2 * a.ctas, C::ROWS);
+                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D, MT, RG>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_rows_kernel<T, D>, dim3(2 * dev.num_sms), THREADS, smem, stream, tk, tv, a);
+                e = launch_dependent(attention_rows_kernel<T, D, MT, RG>, dim3(a.ctas), C::THREADS, smem, stream, tk, tv, a);
                 if (e != cudaSuccess) return e;
-                return launch_dependent(attention_join_kernel<D, ROWS, TILE, COUNTERS, JOIN_WARPS>, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a);
+                return launch_dependent(attention_rows_join_kernel<D, C::ROWS>, dim3(a.ctas - 1, JOIN_Y), 32 * JOIN_WARPS, 0, stream, a);
             };
-            return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
+            using I1 = std::integral_constant<int, 1>;
+            using I2 = std::integral_constant<int, 2>;
+            auto pick = [&](auto d) {
+                return rows <= 16 ? go(d, I1{}, I1{}) : rows <= 32 ? go(d, I2{}, I1{}) : go(d, I2{}, I2{});
+            };
+            return kv.dim == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
         }
     });
 }

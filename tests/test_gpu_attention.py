@@ -11,8 +11,9 @@ from gpu_util import device_ok, ensure_built
 
 pytestmark = pytest.mark.gpu
 
-# max_new: 1 lets the call take the kernel for few tokens whatever the batch holds, None the one for chunks.
-HINTS = pytest.mark.parametrize("hint", [1, None])
+# Rows of a unit that max_new announces: the kernels for up to 16, 32 and 64 rows, whatever the batch holds, and the
+# one for chunks.
+HINTS = pytest.mark.parametrize("hint", [16, 32, 64, 1000])
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -20,9 +21,14 @@ def built():
     ensure_built()
 
 
+def new(hint, q, hk):
+    """max_new of so many rows (the call itself takes no more than there are)."""
+    return max(1, hint * hk // q.shape[1])
+
+
 def run(batch, q, hint, window=0, out_t=None, scale=None, out=None, ws=None):
     kv = q8.PagedKV(*batch.cuda())
-    got = q8.attention(kv, q.cuda(), scale=scale, window=window, max_new=hint, dtype=out_t, out=out, ws=ws)
+    got = q8.attention(kv, q.cuda(), scale=scale, window=window, max_new=new(hint, q, batch.hk), dtype=out_t, out=out, ws=ws)
     device_ok()
     return got
 
@@ -191,7 +197,7 @@ def test_strided_arguments(hint):
     table[:, :batch.width] = batch.table.cuda()
     kv = q8.PagedKV(both[:, 0], both[:, 1], table[:, :batch.width], batch.starts.cuda(), batch.lens.cuda())
     out = torch.full((m, 6, 64), 7.0, device="cuda")
-    q8.attention(kv, wide.cuda()[:, 2:6], out=out[:, 1:5], max_new=hint)
+    q8.attention(kv, wide.cuda()[:, 2:6], out=out[:, 1:5], max_new=new(hint, q, 2))
     device_ok()
     ref.close(out[:, 1:5], want, tol)
     assert bool((out[:, 0] == 7).all()) and bool((out[:, 5] == 7).all())
@@ -215,11 +221,11 @@ def test_graph_follows_lengths(hint):
     kv = q8.PagedKV(kd, vd, table, starts, lens)
     q = batch.randn(5, hq, d)
     qd, out, ws = q.cuda(), torch.empty((5, hq, d), dtype=torch.float16, device="cuda"), q8.attention_workspace(kv, hq)
-    q8.attention(kv, qd, max_new=hint, ws=ws, out=out)
+    q8.attention(kv, qd, max_new=new(hint, q, hk), ws=ws, out=out)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        q8.attention(kv, qd, max_new=hint, ws=ws, out=out)
+        q8.attention(kv, qd, max_new=new(hint, q, hk), ws=ws, out=out)
     for n in ([1, 3, 1], [2991, 73, 1], [100, 20, 0], [2000, 5, 1]):
         batch.lens = torch.tensor(n, dtype=torch.int32)
         lens.copy_(batch.lens)
