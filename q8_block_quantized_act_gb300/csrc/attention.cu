@@ -8,7 +8,7 @@
 //
 // One warp brings 64 positions at a time to shared memory (TMA boxes of up to a page, 128-byte swizzled, several
 // stages ahead across row tiles).  Four warps take 16 positions each, with their own running maximum and sum, so
-// they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16 to 64
+// they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16 or 32
 // rows are too few for tcgen05's 128, and it is not what bounds.  Scores, statistics and sums are f32; the weights
 // e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type.
 #include <algorithm>
@@ -23,29 +23,29 @@ constexpr int KEY_WARPS = 4;         // 16 positions each
 constexpr int COUNTERS = 128;        // threads that count the work
 constexpr float NEG = -INFINITY;
 
-// MT: 16-row tiles a warp, RG: groups of warps with rows of their own.
-template <int D, int MT, int RG>
+// MT: 16-row tiles.
+template <int D, int MT>
 struct Cfg {
-    static constexpr int ROWS = 16 * MT * RG;
-    static constexpr int CTAS = MT * RG == 1 ? 2 : 1;           // to an SM
-    static constexpr int CONSUMERS = KEY_WARPS * RG, THREADS = 32 * (CONSUMERS + 1);
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int CTAS = 2;                              // to an SM
+    static constexpr int THREADS = 32 * (KEY_WARPS + 1);
     static constexpr int TILE_BYTES = TILE * D * 2;             // of keys, and of values
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int STAGES = (CTAS == 2 ? 96 : RG == 1 ? 192 : 160) * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = 96 * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                       // 128-byte wide columns of a tile
     static constexpr int Q_STRIDE = D * 2 + 16;                 // bytes: rows in different banks
-    static constexpr int Q_BYTES = ROWS * Q_STRIDE;
-    static constexpr int OFF_Q = STAGES * STAGE_BYTES, OFF_SHARED = OFF_Q + 2 * Q_BYTES;
+    static constexpr int Q_BYTES = ROWS * Q_STRIDE, Q_BUFFERS = MT == 1 ? 2 : 1;
+    static constexpr int OFF_Q = STAGES * STAGE_BYTES, OFF_SHARED = OFF_Q + Q_BUFFERS * Q_BYTES;
 };
 
 template <int ROWS>
 struct Shared {
     long long before[COUNTERS + 1];       // work before thread j's sequences
     long long sums[COUNTERS / 32];
-    uint64_t full[12], empty[12], q_full[2], q_empty[2];
-    uint32_t ok[12];                      // a stage's 16-position blocks whose page exists
+    uint64_t full[6], empty[6], q_full[2], q_empty[2];
+    uint32_t ok[6];                       // a stage's 16-position blocks whose page exists
     float mx[2][KEY_WARPS][ROWS], sum[2][KEY_WARPS][ROWS];
-    int spoilt[2][KEY_WARPS * 2];         // a non-finite value that not all rows see
+    int spoilt[2][KEY_WARPS];             // a non-finite value that not all rows see
     int abort_flag;
 };
 
@@ -53,9 +53,20 @@ struct Shared {
 // The line of work: the sequences one after another, in each the row tiles and in these the heads, each with
 // the key tiles that its longest row tile sees (one at least, so that rows that see nothing are written too).
 // ---------------------------------------------------------------------------------------
+// 64-bit division, mostly of numbers that fit 32 bits.
+__device__ __forceinline__ long long divide(long long x, long long by)
+{
+    return ((x | by) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)by) : x / by;
+}
+
 struct Line {
-    int per;               // sequences a counting thread
     long long total, length;      // key tiles, and of a CTA's stretch
+    // Up to 32 sequences: each lane of each warp has one, and the work before it.  More: counting thread j has `per`.
+    bool few;
+    int per;
+    long long before;
+    int items, n;
+    Seq s;
 
     // Row tiles x heads of a sequence, and key tiles of each.
     template <int ROWS>
@@ -67,25 +78,33 @@ struct Line {
         if (!tiles) return;
         n = span_of<TILE>(a, s, (tiles - 1) * ROWS, rows - 1).n;
         if (tiles > 1 && a.window) {        // another row tile's window may touch one tile more
-            const int tokens = (ROWS + a.group - 2) / a.group + 1;
+            const int tokens = a.by_group(ROWS + a.group - 2) + 1;
             n = min(min(s.pos0 + s.n, s.end), 0x3fffffff) / TILE + 1;
             n = min(n, (int)((a.window + (long long)tokens + TILE - 3) / TILE) + 1);
         }
         n = max(n, 1);
     }
 
-    // Called by all threads of the CTA.
+    // Called by all threads of the CTA.  (Few sequences: no barrier.)
     template <int ROWS>
-    __device__ __forceinline__ void make(const Attn &a, long long *before, long long *sums)
+    __device__ __forceinline__ void make(const Attn &a, long long *starts, long long *sums)
     {
         const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        few = a.p.seqs <= 32;
         per = (a.p.seqs + COUNTERS - 1) / COUNTERS;
+        items = n = 0;
         long long w = 0;
-        if (t < COUNTERS) {
+        if (few) {
+            if (lane < a.p.seqs) {
+                s = seq_of(a.p, lane);
+                shape<ROWS>(a, s, items, n);
+                w = (long long)items * n;
+            }
+        } else if (t < COUNTERS) {
             for (int b = t * per; b < min(t * per + per, a.p.seqs); ++b) {
-                int items, n;
-                shape<ROWS>(a, seq_of(a.p, b), items, n);
-                w += (long long)items * n;
+                int i, k;
+                shape<ROWS>(a, seq_of(a.p, b), i, k);
+                w += (long long)i * k;
             }
         }
         long long sum = w;
@@ -94,53 +113,77 @@ struct Line {
             const long long u = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += u;
         }
-        if (t < COUNTERS && lane == 31) sums[warp] = sum;
-        __syncthreads();
-        if (t < COUNTERS) {
+        if (few) {
+            before = sum - w;
+            total = __shfl_sync(0xffffffffu, sum, 31);
+        } else {
+            if (t < COUNTERS && lane == 31) sums[warp] = sum;
+            __syncthreads();
+            if (t < COUNTERS) {
 #pragma unroll
-            for (int j = 0; j < COUNTERS / 32; ++j)
-                if (j < warp) sum += sums[j];
-            before[t] = sum - w;
-            if (t == COUNTERS - 1) before[COUNTERS] = sum;
+                for (int j = 0; j < COUNTERS / 32; ++j)
+                    if (j < warp) sum += sums[j];
+                starts[t] = sum - w;
+                if (t == COUNTERS - 1) starts[COUNTERS] = sum;
+            }
+            __syncthreads();
+            total = starts[COUNTERS];
         }
-        __syncthreads();
-        total = before[COUNTERS];
-        length = max((total + a.ctas - 1) / a.ctas, (long long)a.least);
+        length = max(divide(total + a.ctas - 1, a.ctas), (long long)a.least);
     }
 };
 
-// A place on the line.
+// A place on the line.  Its calls are made by whole warps.
 template <int ROWS>
 struct Place {
     int b, item, items, n, tile;       // sequence, row tile and head of so many, key tile of so many
     Seq s;
 
-    // Key tile x of the line (x < total).  Called by whole warps.
-    __device__ __forceinline__ Place(const Attn &a, const Line &line, const long long *before, long long x)
+    __device__ __forceinline__ void enter(const Attn &a, const Line &line)
     {
-        int lo = -1;                   // the last thread that starts at or before x
-#pragma unroll
-        for (int i = 0; i < COUNTERS; i += 32) lo += __popc(__ballot_sync(0xffffffffu, before[i + (threadIdx.x & 31)] <= x));
-        long long left = x - before[lo];
-        for (b = lo * line.per;; ++b) {
+        if (line.few) {
+            items = __shfl_sync(0xffffffffu, line.items, b);
+            n = __shfl_sync(0xffffffffu, line.n, b);
+            s.row0 = __shfl_sync(0xffffffffu, line.s.row0, b);
+            s.n = __shfl_sync(0xffffffffu, line.s.n, b);
+            s.pos0 = __shfl_sync(0xffffffffu, line.s.pos0, b);
+            s.end = __shfl_sync(0xffffffffu, line.s.end, b);
+        } else {
             s = seq_of(a.p, b);
             Line::shape<ROWS>(a, s, items, n);
-            if (left < (long long)items * n || b + 1 >= a.p.seqs) break;
-            left -= (long long)items * n;
         }
-        item = n ? (int)(left / n) : 0;
+    }
+    // Key tile x of the line (x < total).
+    __device__ __forceinline__ Place(const Attn &a, const Line &line, const long long *starts, long long x)
+    {
+        long long left;
+        if (line.few) {
+            b = __popc(__ballot_sync(0xffffffffu, line.before <= x)) - 1;    // (those behind the last hold the total)
+            left = x - __shfl_sync(0xffffffffu, line.before, b);
+            enter(a, line);
+        } else {
+            int lo = -1;                   // the last thread that starts at or before x
+#pragma unroll
+            for (int i = 0; i < COUNTERS; i += 32) lo += __popc(__ballot_sync(0xffffffffu, starts[i + (threadIdx.x & 31)] <= x));
+            left = x - starts[lo];
+            for (b = lo * line.per;; ++b) {
+                enter(a, line);
+                if (left < (long long)items * n || b + 1 >= a.p.seqs) break;
+                left -= (long long)items * n;
+            }
+        }
+        item = n ? (int)divide(left, n) : 0;
         tile = (int)(left - (long long)item * n);
     }
     // The next row tile's first key tile (not behind the line's end).
-    __device__ __forceinline__ void next(const Attn &a)
+    __device__ __forceinline__ void next(const Attn &a, const Line &line)
     {
         tile = 0;
         if (++item < items) return;
         item = 0;
         do {
             if (++b >= a.p.seqs) return;
-            s = seq_of(a.p, b);
-            Line::shape<ROWS>(a, s, items, n);
+            enter(a, line);
         } while (items == 0);
     }
 };
@@ -212,11 +255,11 @@ __device__ __forceinline__ bool non_finite2(uint32_t w)
     return (w & E) == E || (w >> 16 & E) == E;
 }
 
-template <typename T, int D, int MT, int RG>
-__global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
 {
-    using C = Cfg<D, MT, RG>;
+    using C = Cfg<D, MT>;
     constexpr int ROWS = C::ROWS;
     extern __shared__ __align__(1024) uint8_t stages[];
     Shared<ROWS> &sm = *reinterpret_cast<Shared<ROWS> *>(stages + C::OFF_SHARED);
@@ -224,25 +267,26 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], C::CONSUMERS); }
-        for (int s = 0; s < 2; ++s) { mbar_init(&sm.q_full[s], 1); mbar_init(&sm.q_empty[s], C::CONSUMERS); }
+        for (int s = 0; s < C::STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], KEY_WARPS); }
+        for (int s = 0; s < 2; ++s) { mbar_init(&sm.q_full[s], 1); mbar_init(&sm.q_empty[s], KEY_WARPS); }
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == C::CONSUMERS && lane == 0) {
+    if (warp == KEY_WARPS && lane == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
     griddep_wait();
     griddep_launch_dependents();
     Line line{};
-    line.make<ROWS>(a, sm.before, sm.sums);                      // and the barriers exist for all
+    line.make<ROWS>(a, sm.before, sm.sums);
+    __syncthreads();                                             // the barriers exist for all
     long long x = blockIdx.x * line.length;
     const long long x1 = min(x + line.length, line.total);
     if (x >= x1) return;
     Place<ROWS> place(a, line, sm.before, x);
 
-    if (warp == C::CONSUMERS) {
+    if (warp == KEY_WARPS) {
         // ------------------------------ producer ------------------------------
         const int ps = 1 << a.p.page_shift, per_tile = ps < TILE ? TILE / ps : 1, blocks = 4 / per_tile;
         int it = 0, st = 0, parts = 0;
@@ -253,10 +297,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
             const Seq s = place.s;
             const int b = place.b;
             x += min((long long)(place.n - place.tile), x1 - x);
-            place.next(a);
+            place.next(a, line);
             // Queries, a row a lane (rows behind the last one hold anything: what comes of them goes nowhere).
-            const int qb = parts & 1;
-            ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[qb], (parts >> 1 & 1) ^ 1, a.status, abort_flag));
+            const int qb = parts % C::Q_BUFFERS;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[qb], (parts / C::Q_BUFFERS & 1) ^ 1, a.status, abort_flag));
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[qb], p.valid * D * 2);
             __syncwarp();
@@ -297,15 +341,16 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
         // Never leave with a copy into this CTA's shared memory in flight.
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
             mbar_wait_drain(&sm.full[i % C::STAGES], (i / C::STAGES) & 1, a.status);
-        for (int i = parts > 2 ? parts - 2 : 0; i < parts; ++i) mbar_wait_drain(&sm.q_full[i & 1], i >> 1 & 1, a.status);
+        for (int i = max(parts - C::Q_BUFFERS, 0); i < parts; ++i)
+            mbar_wait_drain(&sm.q_full[i % C::Q_BUFFERS], i / C::Q_BUFFERS & 1, a.status);
         return;
     }
 
     // ------------------------------ consumers ------------------------------
-    const int g = lane >> 2, c = lane & 3, kw = warp % KEY_WARPS, rg = warp / KEY_WARPS;
+    const int g = lane >> 2, c = lane & 3, kw = warp;
     const uint32_t stage0 = smem_u32(stages);
     // Rows of this lane's ldmatrix addresses: queries, keys in their own order, values transposed.
-    const uint32_t q0 = stage0 + C::OFF_Q + (rg * MT * 16 + (lane & 7) + (lane >> 3 & 1) * 8) * C::Q_STRIDE + (lane >> 4) * 16;
+    const uint32_t q0 = stage0 + C::OFF_Q + ((lane & 7) + (lane >> 3 & 1) * 8) * C::Q_STRIDE + (lane >> 4) * 16;
     const int krow = kw * 16 + (lane & 7) + (lane >> 4) * 8, kchunk = lane >> 3 & 1;
     const int vrow = kw * 16 + (lane & 7) + (lane >> 3 & 1) * 8, vchunk = lane >> 4;
     const long long x0 = x;
@@ -314,10 +359,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
     for (int parts = 0; x < x1; ++parts) {
         const Part<ROWS> p(a, place, x1 - x);
         const Seq s0 = place.s;
-        const int b = place.b, flip = parts & 1;
+        const int b = place.b, flip = parts & 1, qb = parts % C::Q_BUFFERS;
         const int slot = p.whole ? -1 : 2 * (int)blockIdx.x + (x != x0);
         x += min((long long)(place.n - place.tile), x1 - x);
-        place.next(a);
+        place.next(a, line);
         const int first = s0.pos0 + a.by_group(p.r0), last = s0.pos0 + a.by_group(p.r0 + p.valid - 1);    // positions of its rows
 
         // Two rows a lane and 16-row tile: g and g + 8.
@@ -326,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = (rg * MT + mt) * 16 + g + 8 * i, pos = s0.pos0 + a.by_group(p.r0 + r);
+                const int r = mt * 16 + g + 8 * i, pos = s0.pos0 + a.by_group(p.r0 + r);
                 hi[mt][i] = r < p.valid ? min(pos, s0.end - 1) : -1;
                 lo[mt][i] = a.window ? max(pos - a.window + 1, 0) : 0;
             }
@@ -341,15 +386,15 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
                 for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.0f;
         }
         bool spoilt = false;
-        bool aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.q_full[flip], parts >> 1 & 1, a.status, abort_flag));
-        const uint32_t qs = q0 + flip * C::Q_BYTES;
+        bool aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.q_full[qb], parts / C::Q_BUFFERS & 1, a.status, abort_flag));
+        const uint32_t qs = q0 + qb * C::Q_BYTES;
         // One 16-row tile's queries stay in registers; of more, they are read from shared memory again.
         uint32_t q[MT == 1 ? D / 16 : 1][4];
         if constexpr (MT == 1) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) ldmatrix_x4(q[kk], qs + kk * 32);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_empty[flip]);
+            if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
         }
 
         for (int t = p.t0; t < p.t1; ++t) {
@@ -357,39 +402,37 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
             if (aborted) break;
             const uint32_t kt = stage0 + st * C::STAGE_BYTES, vt = kt + C::TILE_BYTES;
             const bool page_ok = sm.ok[st] >> kw & 1;
-            float s[MT][2][4] = {};
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t kf[4];
-                const int chunk = kk * 2 + kchunk;
-                ldmatrix_x4(kf, kt + (chunk >> 3) * (TILE * 128) + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if constexpr (MT > 1) ldmatrix_x4(q[0], qs + mt * (16 * C::Q_STRIDE) + kk * 32);
-                    const uint32_t(&qf)[4] = q[MT == 1 ? kk : 0];
-                    mma_16816<T>(s[mt][0], qf, kf[0], kf[1]);
-                    mma_16816<T>(s[mt][1], qf, kf[2], kf[3]);
-                }
-            }
+            // A 16-row tile's scores at a time; its keys come from shared memory again for the next one.
+            uint32_t pf[MT][4];
             // Columns of s[n]: positions key0 + 8 n + 2 c and the next; rows g (0, 1) and g + 8 (2, 3).
             const int key0 = t * TILE + kw * 16;
             // Whether some row does not see some of the 16.
             const bool part = key0 < p.span.lo || key0 + 15 > min(first, p.span.hi) || (a.window && key0 <= last - a.window) || !page_ok;
-            uint32_t pf[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
+                float s[2][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t kf[4];
+                    const int chunk = kk * 2 + kchunk;
+                    ldmatrix_x4(kf, kt + (chunk >> 3) * (TILE * 128) + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4));
+                    if constexpr (MT > 1) ldmatrix_x4(q[0], qs + mt * (16 * C::Q_STRIDE) + kk * 32);
+                    const uint32_t(&qf)[4] = q[MT == 1 ? kk : 0];
+                    mma_16816<T>(s[0], qf, kf[0], kf[1]);
+                    mma_16816<T>(s[1], qf, kf[2], kf[3]);
+                }
                 if (part) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = key0 + 8 * n + 2 * c + (i & 1);
-                            if (key < lo[mt][i >> 1] || key > hi[mt][i >> 1] || !page_ok) s[mt][n][i] = NEG;
+                            if (key < lo[mt][i >> 1] || key > hi[mt][i >> 1] || !page_ok) s[n][i] = NEG;
                         }
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float m = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+                    float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                     m = fmaxf(mx[mt][i], m * a.scale);
@@ -406,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
                     const float base = m == NEG ? 0.0f : m;
                     float e[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[mt][j >> 1][2 * i + (j & 1)], a.scale, -base));
+                    for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[j >> 1][2 * i + (j & 1)], a.scale, -base));
                     sum[mt][i] += (e[0] + e[1]) + (e[2] + e[3]);
                     pf[mt][i] = pack2<T>(e[0], e[1]);
                     pf[mt][i + 2] = pack2<T>(e[2], e[3]);
@@ -459,44 +502,44 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
                 sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 1);
                 sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 2);
                 if (c == 0) {
-                    sm.mx[flip][kw][(rg * MT + mt) * 16 + g + 8 * i] = mx[mt][i];
-                    sm.sum[flip][kw][(rg * MT + mt) * 16 + g + 8 * i] = sum[mt][i];
+                    sm.mx[flip][kw][mt * 16 + g + 8 * i] = mx[mt][i];
+                    sm.sum[flip][kw][mt * 16 + g + 8 * i] = sum[mt][i];
                 }
             }
         spoilt = __any_sync(0xffffffffu, spoilt);
         if (lane == 0) sm.spoilt[flip][warp] = spoilt;
         // (the next part's words go to the other flip: some warps may still read these.  They are written again only
         // behind the next part's barrier)
-        if (bar_red_or(1, 32 * C::CONSUMERS, aborted)) return;
-        if (MT > 1 && lane == 0) mbar_arrive(&sm.q_empty[flip]);
+        if (bar_red_or(1, 32 * KEY_WARPS, aborted)) return;
+        if (MT > 1 && lane == 0) mbar_arrive(&sm.q_empty[qb]);
         const bool some = p.t1 > p.t0;
         float *join = reinterpret_cast<float *>(stages + st * C::STAGE_BYTES);      // [warp][row][D], 16-byte words swizzled by row
 #pragma unroll
-        for (int m16 = 0; m16 < MT * RG; ++m16) {
+        for (int m16 = 0; m16 < MT; ++m16) {
             if (m16 * 16 >= p.valid) break;
             if (some) {
-                if (m16 > 0) named_bar_sync(2, 32 * C::CONSUMERS);
-                if (rg == m16 / MT) {
+                if (m16 > 0) named_bar_sync(2, 32 * KEY_WARPS);
+                {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int r = g + 8 * i;
                         float m = NEG;
 #pragma unroll
                         for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][m16 * 16 + r]);
-                        const float f = attn_ex2(mx[m16 % MT][i] - (m == NEG ? 0.0f : m));
+                        const float f = attn_ex2(mx[m16][i] - (m == NEG ? 0.0f : m));
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n) {
                             const int col = (8 * n + 2 * c) ^ ((r & 7) << 2);
                             *reinterpret_cast<float2 *>(join + (kw * 16 + r) * D + col) =
-                                make_float2(o[m16 % MT][n][2 * i] * f, o[m16 % MT][n][2 * i + 1] * f);
+                                make_float2(o[m16][n][2 * i] * f, o[m16][n][2 * i + 1] * f);
                         }
                     }
                 }
-                named_bar_sync(2, 32 * C::CONSUMERS);
+                named_bar_sync(2, 32 * KEY_WARPS);
             }
             const int r = (threadIdx.x >> 3) & 15, c8 = threadIdx.x & 7;        // a row, and every eighth vector of it
             const int rr = m16 * 16 + r;
-            if (rg == m16 / MT && rr < p.valid) {
+            if (rr < p.valid) {
                 float m = NEG, l = 0.0f;
 #pragma unroll
                 for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][rr]);
@@ -522,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
                 const int row = p.r0 + rr, tok = a.by_group(row), head = p.h * a.group + row - tok * a.group;
                 int sp = 0;
 #pragma unroll
-                for (int w = 0; w < C::CONSUMERS; ++w) sp |= sm.spoilt[flip][w];
+                for (int w = 0; w < KEY_WARPS; ++w) sp |= sm.spoilt[flip][w];
                 if (sp) {
                     const int pos = s0.pos0 + tok;
                     const int k0 = max(a.window ? pos - a.window + 1 : 0, p.t0 * TILE), k1 = min(min(pos, s0.end - 1), p.t1 * TILE - 1);
@@ -564,54 +607,66 @@ __global__ void __launch_bounds__(Cfg<D, MT, RG>::THREADS, Cfg<D, MT, RG>::CTAS)
 
 constexpr int JOIN_WARPS = 4, JOIN_Y = 4;
 
-// A row's parts, added in their order by four warps: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i.
-// slot(i): where part i is.
+// A row's parts, added in their order by four warps: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i.  A
+// warp takes its parts relative to its own maximum, eight loads at a time.  slot(i): where part i is.
 template <int D, int ROWS, typename Slot>
 __device__ __forceinline__ void join_row(const Attn &a, int parts, Slot slot, int r, uint8_t *dst, float (&acc)[JOIN_WARPS][D],
                                          float (&mw)[JOIN_WARPS], float (&lw)[JOIN_WARPS])
 {
-    constexpr int V = D / 32;                // values a lane
+    constexpr int V = D / 32, U = 8;         // values a lane, parts at a time
+    using Vec = std::conditional_t<V == 4, float4, float2>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float m = NEG;
-    for (int s = warp * 32 + lane; s < parts; s += 32 * JOIN_WARPS) m = fmaxf(m, a.ml[(int64_t)slot(s) * ROWS + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) mw[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, mw[w]);
-    const float base = m == NEG ? 0.0f : m;
-    float l = 0.0f, v[V] = {};
     const int s0 = parts * warp / JOIN_WARPS, s1 = parts * (warp + 1) / JOIN_WARPS;
-#pragma unroll 8
-    for (int s = s0; s < s1; ++s) {
-        const int64_t at = (int64_t)slot(s) * ROWS + r;
-        const float2 ms = a.ml[at];
-        const float f = attn_ex2(ms.x - base);
-        l = fmaf(ms.y, f, l);
-        float w[V];
-        if constexpr (V == 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
-            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-        } else {
-            const float2 u = *reinterpret_cast<const float2 *>(a.part + at * D + 2 * lane);
-            w[0] = u.x; w[1] = u.y;
-        }
+    float m = NEG, l = 0.0f, v[V] = {};
+    for (int s = s0; s < s1; s += U) {
+        float2 ml[U];
+        Vec w[U];
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = fmaf(w[j], f, v[j]);
+        for (int i = 0; i < U; ++i) {
+            const int64_t at = (int64_t)slot(min(s + i, s1 - 1)) * ROWS + r;
+            ml[i] = a.ml[at];
+            w[i] = *reinterpret_cast<const Vec *>(a.part + at * D + V * lane);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < U; ++i) top = fmaxf(top, ml[i].x);
+        const float base = top == NEG ? 0.0f : top, f0 = attn_ex2(m - base);
+        m = top;
+        l *= f0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] *= f0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (s + i >= s1) break;
+            const float f = attn_ex2(ml[i].x - base);
+            l = fmaf(ml[i].y, f, l);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = fmaf(reinterpret_cast<const float *>(&w[i])[j], f, v[j]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[warp][V * lane + j] = v[j];
-    if (lane == 0) lw[warp] = l;
+    if (lane == 0) {
+        mw[warp] = m;
+        lw[warp] = l;
+    }
     __syncthreads();
     if (threadIdx.x < D / 4) {
         float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        m = NEG;
         l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, mw[w]);
+        const float base = m == NEG ? 0.0f : m;
 #pragma unroll
         for (int w = 0; w < JOIN_WARPS; ++w) {
             const float4 u = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
-            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-            l += lw[w];
+            const float f = attn_ex2(mw[w] - base);
+            t.x = fmaf(u.x, f, t.x);
+            t.y = fmaf(u.y, f, t.y);
+            t.z = fmaf(u.z, f, t.z);
+            t.w = fmaf(u.w, f, t.w);
+            l = fmaf(lw[w], f, l);
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         store4(dst + 4 * threadIdx.x * out_size(a.otype), a.otype, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
@@ -635,7 +690,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(At
         const Place<ROWS> p(a, line, before, x);
         const long long start = x - p.tile;                  // of the row tile
         if (p.tile > 0 && x - len <= start) {
-            const int k0 = blockIdx.x, parts = (int)((start + p.n - 1) / len) - k0 + 1;
+            const int k0 = blockIdx.x, parts = (int)divide(start + p.n - 1, len) - k0 + 1;
             const int tile = a.by_heads(p.item), h = p.item - tile * a.p.heads, valid = min(ROWS, p.s.n * a.group - tile * ROWS);
             griddep_wait();
             for (int r = blockIdx.y; r < valid; r += JOIN_Y) {
@@ -711,13 +766,8 @@ cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, in
     return dim == 64 ? go(attention_chunk_join_kernel<64>) : go(attention_chunk_join_kernel<128>);
 }
 
-// Two parts at most of each CTA that a GB300's 152 SMs hold.
-static size_t rows_space(int dim)
-{
-    return std::max(attention_space(2 * 2 * 152, 16, dim), attention_space(2 * 152, 64, dim));
-}
-
-size_t attention_workspace_bytes(int dim) { return std::max(rows_space(dim), attention_chunk_space(dim)); }
+// Two partial results at most of each of the CTAs that a GB300's 152 SMs hold.
+size_t attention_workspace_bytes(int dim) { return std::max(attention_space(2 * 2 * 152, 32, dim), attention_chunk_space(dim)); }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &s, int64_t m,
                              cudaStream_t stream)
@@ -739,7 +789,7 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.status = dev.status;
     const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
     const int64_t rows = most * a.group;
-    if (rows > 64) return launch_attention_chunk(dev, kv, a, s.ws, stream);
+    if (rows > 32) return launch_attention_chunk(dev, kv, a, s.ws, stream);
     CUtensorMap tk, tv;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     return with_type(kv.type, [&](auto x) -> cudaError_t {
@@ -747,24 +797,24 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
         if constexpr (sizeof(T) == 4) {
             return cudaErrorInvalidValue;
         } else {
-            auto go = [&](auto d, auto mt, auto rg) -> cudaError_t {
-                constexpr int D = decltype(d)::value, MT = decltype(mt)::value, RG = decltype(rg)::value;
-                using C = Cfg<D, MT, RG>;
+            auto go = [&](auto d, auto mt) -> cudaError_t {
+                constexpr int D = decltype(d)::value, MT = decltype(mt)::value;
+                using C = Cfg<D, MT>;
                 constexpr size_t smem = C::OFF_SHARED + sizeof(Shared<C::ROWS>);
-                static_assert(smem <= (C::CTAS == 2 ? 113 : 227) * 1024, "shared memory");
-                a.ctas = std::min(C::CTAS * dev.num_sms, C::CTAS * 152);
+                static_assert(smem <= 113 * 1024, "two CTAs to an SM");
+                a.ctas = C::CTAS * std::min(dev.num_sms, 152);
                 a.least = 2;
                 attention_place(a, s.ws, 2 * a.ctas, C::ROWS);
-                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D, MT, RG>>(dev.device, smem);
+                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D, MT>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_rows_kernel<T, D, MT, RG>, dim3(a.ctas), C::THREADS, smem, stream, tk, tv, a);
+                e = launch_dependent(attention_rows_kernel<T, D, MT>, dim3(a.ctas), C::THREADS, smem, stream, tk, tv, a);
                 if (e != cudaSuccess) return e;
                 return launch_dependent(attention_rows_join_kernel<D, C::ROWS>, dim3(a.ctas - 1, JOIN_Y), 32 * JOIN_WARPS, 0, stream, a);
             };
             using I1 = std::integral_constant<int, 1>;
             using I2 = std::integral_constant<int, 2>;
             auto pick = [&](auto d) {
-                return rows <= 16 ? go(d, I1{}, I1{}) : rows <= 32 ? go(d, I2{}, I1{}) : go(d, I2{}, I2{});
+                return rows <= 16 ? go(d, I1{}) : go(d, I2{});
             };
             return kv.dim == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
         }

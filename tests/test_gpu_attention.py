@@ -11,9 +11,9 @@ from gpu_util import device_ok, ensure_built
 
 pytestmark = pytest.mark.gpu
 
-# Rows of a unit that max_new announces: the kernels for up to 16, 32 and 64 rows, whatever the batch holds, and the
+# Rows of a unit that max_new announces: the kernels for up to 16 and 32 rows, whatever the batch holds, and the
 # one for chunks.
-HINTS = pytest.mark.parametrize("hint", [16, 32, 64, 1000])
+HINTS = pytest.mark.parametrize("hint", [16, 32, 1000])
 
 
 @pytest.fixture(scope="module", autouse=True)
