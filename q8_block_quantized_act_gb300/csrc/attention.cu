@@ -711,14 +711,13 @@ template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_chunk_join_kernel(Attn a)
 {
     constexpr int V = D / 32, ROWS = CHUNK_ROWS, R = 4;
-    __shared__ PlanSmem<CHUNK_COUNTERS> sm;
     const int lane = threadIdx.x & 31;
-    Plan<ROWS, CHUNK_TILE, CHUNK_COUNTERS> plan;
-    plan.make(a, sm);
-    const int work = sm.items[CHUNK_COUNTERS] * (ROWS / R);
+    Plan<ROWS, CHUNK_TILE> plan;
+    plan.make(a);
+    const int work = plan.split * (ROWS / R);
     bool waited = false;
     for (int i = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5); i < work; i += gridDim.x * JOIN_WARPS) {
-        const Unit it = plan.find_item(a, sm, i / (ROWS / R));
+        const Unit it = plan.find_item(a, i / (ROWS / R));
         if (!waited) griddep_enter();
         waited = true;
         const int i0 = i % (ROWS / R) * R, rows = it.s.n * a.group - it.tile * ROWS;

@@ -82,67 +82,64 @@ __device__ __forceinline__ Span span_of(const Attn &a, const Seq &s, int r0, int
 }
 
 // ---------------------------------------------------------------------------------------
-// The units of a batch, counted by the CTA's first NT threads: thread j counts sequences j * per ... of the
-// batch.  The last row tiles come first, which are the longest.
+// The units of a batch of chunks, counted by a warp: lane j counts sequences j * per ... of the batch.  The
+// last row tiles come first, which are the longest.  Every member is called by whole warps.
 // ---------------------------------------------------------------------------------------
-template <int NT>
-struct PlanSmem {
-    int units[NT + 1], slots[NT + 1], items[NT + 1];    // before thread j's sequences; items: row tiles in several parts
-    long long work[NT / 32];
-    int sums[3][NT / 32];
-    int length;
-};
-
 struct Unit {
     int b, h, tile, part, parts;
     int slot;                       // of the row tile's first part (parts > 1)
     Seq s;
 };
 
-template <int ROWS, int TILE, int NT>
+template <int ROWS, int TILE>
 struct Plan {
-    int per;       // sequences a thread
-    int length;    // key tiles a part
-    int total;     // units
+    int per;                        // sequences a lane
+    int length;                     // key tiles a part
+    int total, split;               // units; row tiles in several parts
+    // Before the lane's first sequence: units, slots, row tiles in several parts.  And, of one sequence a lane, what it is.
+    int units, slots, items;
+    Seq s;
+    int tiles, parts;
 
     // Row tiles of a sequence and the parts of each.
-    __device__ __forceinline__ void shape(const Attn &a, const Seq &s, int &tiles, int &parts) const
+    __device__ __forceinline__ void shape(const Attn &a, const Seq &q, int &t, int &p) const
     {
-        const int rows = s.n * a.group;
-        tiles = (rows + ROWS - 1) / ROWS;
-        parts = tiles ? max(1, (span_of<TILE>(a, s, (tiles - 1) * ROWS, rows - 1).n + length - 1) / length) : 0;
+        const int rows = q.n * a.group;
+        t = (rows + ROWS - 1) / ROWS;
+        p = t ? max(1, (span_of<TILE>(a, q, (t - 1) * ROWS, rows - 1).n + length - 1) / length) : 0;
     }
 
-    // Up to 32 sequences, by one warp, a sequence a lane: the length of a part by trying 32 of them, a lane
-    // each, on an estimate of the time of the slowest CTA.  A batch of equal units takes whole rounds of the CTAs;
-    // one of unequal units its average and one more unit.
+    // Up to 32 sequences: the length of a part by trying 32 of them, a lane each, on an estimate of the time of
+    // the slowest CTA.  A batch of equal units takes whole rounds of the CTAs; one of unequal units its average and
+    // one more unit.
     __device__ __forceinline__ int best_length(const Attn &a, int rows, int first, int last) const
     {
-        const int lane = threadIdx.x & 31, tiles = (rows + ROWS - 1) / ROWS * a.p.heads;     // of the lane's sequence
-        int most = last, items = tiles;
-        float work = 0.5f * (float)tiles * (float)(first + last);
+        const int lane = threadIdx.x & 31, mine = (rows + ROWS - 1) / ROWS * a.p.heads;     // row tiles of the lane's sequence
+        int most = last, all = mine;
+        float work = 0.5f * (float)mine * (float)(first + last);
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-            items += __shfl_xor_sync(0xffffffffu, items, o);
+            all += __shfl_xor_sync(0xffffffffu, all, o);
             work += __shfl_xor_sync(0xffffffffu, work, o);
         }
-        if (most <= a.least || items <= 0) return max(most, 1);
+        if (most <= a.least || all <= 0) return max(most, 1);
         // Parts of the longest row tile: what makes 1/8 .. 32/8 rounds of the CTAs; one is always tried.
-        int p = lane ? (int)min((long long)(lane + 1) * a.ctas / (8 * (long long)items), (long long)(most / a.least)) : 1;
+        int p = lane ? min((int)((float)(lane + 1) * (float)a.ctas / (8.0f * (float)all)), most / a.least) : 1;
         p = max(p, 1);
         const int len = (most + p - 1) / p;
-        long long units = 0, slots = 0;
+        float count = 0.0f, cut = 0.0f;             // units, and those of row tiles in several parts (exact below 2^24)
         for (int b = 0; b < a.p.seqs; ++b) {
-            const int t = __shfl_sync(0xffffffffu, tiles, b), n = __shfl_sync(0xffffffffu, last, b);
-            const int parts = max((n + len - 1) / len, 1);
-            units += (long long)t * parts;
-            if (parts > 1) slots += (long long)t * parts;
+            const int t = __shfl_sync(0xffffffffu, mine, b), n = __shfl_sync(0xffffffffu, last, b);
+            const int k = max((n + len - 1) / len, 1);
+            const float c = (float)t * (float)k;
+            count += c;
+            if (k > 1) cut += c;
         }
         const float g = (float)a.ctas, longest = (float)len + a.unit_cost;
-        float cost = min(ceilf((float)units / g) * longest, (work + a.unit_cost * (float)units) / g + longest);
-        if (slots) cost += a.unit_cost;
-        if (slots > a.slots) cost = INFINITY;
+        float cost = min(ceilf(count / g) * longest, (work + a.unit_cost * count) / g + longest);
+        if (cut > 0.0f) cost += a.unit_cost;
+        if (cut > (float)a.slots) cost = INFINITY;
         int best = len;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -156,59 +153,50 @@ struct Plan {
         return best;
     }
 
-    // Called by all threads of the CTA.
-    __device__ __forceinline__ void make(const Attn &a, PlanSmem<NT> &sm)
+    __device__ __forceinline__ void make(const Attn &a)
     {
-        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-        const bool counts = t < NT;
-        per = (a.p.seqs + NT - 1) / NT;
-        const int b0 = counts ? min(t * per, a.p.seqs) : 0, b1 = counts ? min(b0 + per, a.p.seqs) : 0;
-        if (a.p.seqs <= 32) {
-            if (warp == 0) {
-                int rows = 0, first = 0, last = 0;
-                if (lane < a.p.seqs) {
-                    const Seq s = seq_of(a.p, lane);
-                    rows = s.n * a.group;
-                    if (rows) {
-                        first = span_of<TILE>(a, s, 0, min(rows, ROWS) - 1).n;
-                        last = span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
-                    }
+        const int lane = threadIdx.x & 31;
+        per = (a.p.seqs + 31) / 32;
+        const int b0 = min(lane * per, a.p.seqs), b1 = min(b0 + per, a.p.seqs);
+        int v[3] = {0, 0, 0};
+        if (per == 1) {
+            s = Seq{0, 0, 0, 0};
+            int rows = 0, first = 0, last = 0;
+            if (lane < a.p.seqs) {
+                s = seq_of(a.p, lane);
+                rows = s.n * a.group;
+                if (rows) {
+                    first = span_of<TILE>(a, s, 0, min(rows, ROWS) - 1).n;
+                    last = span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
                 }
-                const int l = best_length(a, rows, first, last);
-                if (lane == 0) sm.length = l;
             }
-            __syncthreads();
-            length = sm.length;
+            length = best_length(a, rows, first, last);
+            tiles = (rows + ROWS - 1) / ROWS;
+            parts = tiles ? max(1, (last + length - 1) / length) : 0;
+            v[0] = tiles * parts * a.p.heads;
+            v[1] = parts > 1 ? v[0] : 0;
+            v[2] = parts > 1 ? tiles * a.p.heads : 0;
         } else {
             // Parts of equal length, as many as the workspace has room for: a row tile of p > 1 parts has more than
             // (p - 1) * length >= p * length / 2 key tiles, so there are fewer than twice work / length of them.
             long long w = 0;
             for (int b = b0; b < b1; ++b) {
-                const Seq s = seq_of(a.p, b);
-                const int rows = s.n * a.group;
-                if (rows) w += (long long)((rows + ROWS - 1) / ROWS) * span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
+                const Seq q = seq_of(a.p, b);
+                const int rows = q.n * a.group;
+                if (rows) w += (long long)((rows + ROWS - 1) / ROWS) * span_of<TILE>(a, q, (rows - 1) / ROWS * ROWS, rows - 1).n;
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            if (counts && lane == 0) sm.work[warp] = w;
-            __syncthreads();
-            w = 0;
-#pragma unroll
-            for (int i = 0; i < NT / 32; ++i) w += sm.work[i];
             w = (2 * w * a.p.heads + a.slots - 1) / a.slots;
             length = (int)min(max(w, (long long)a.least), (long long)INT_MAX / 2);
-        }
-
-        int v[3] = {0, 0, 0};
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(a.p, b);
-            int tiles, parts;
-            shape(a, s, tiles, parts);
-            tiles *= a.p.heads;
-            v[0] += tiles * parts;
-            if (parts > 1) {
-                v[1] += tiles * parts;
-                v[2] += tiles;
+            for (int b = b0; b < b1; ++b) {
+                int t, p;
+                shape(a, seq_of(a.p, b), t, p);
+                v[0] += t * a.p.heads * p;
+                if (p > 1) {
+                    v[1] += t * a.p.heads * p;
+                    v[2] += t * a.p.heads;
+                }
             }
         }
         int sum[3];
@@ -220,76 +208,66 @@ struct Plan {
                 const int u = __shfl_up_sync(0xffffffffu, sum[i], o);
                 if (lane >= o) sum[i] += u;
             }
-            if (counts && lane == 31) sm.sums[i][warp] = sum[i];
         }
-        if constexpr (NT > 32) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-#pragma unroll
-                for (int j = 0; j < NT / 32; ++j)
-                    if (j < warp) sum[i] += sm.sums[i][j];
-            }
-        }
-        if (counts) {
-            sm.units[t] = sum[0] - v[0];
-            sm.slots[t] = sum[1] - v[1];
-            sm.items[t] = sum[2] - v[2];
-        }
-        if (t == NT - 1) {
-            sm.units[NT] = sum[0];
-            sm.slots[NT] = sum[1];
-            sm.items[NT] = sum[2];
-        }
-        __syncthreads();
-        total = sm.units[NT];
+        units = sum[0] - v[0];
+        slots = sum[1] - v[1];
+        items = sum[2] - v[2];
+        total = __shfl_sync(0xffffffffu, sum[0], 31);
+        split = __shfl_sync(0xffffffffu, sum[2], 31);
     }
 
-    // The sequence of unit (or, of those in several parts, row tile) u, and what is left of u in it.  Called by
-    // whole warps.
+    // The sequence of unit (or, of those in several parts, row tile) u, and what is left of u in it.
     template <bool ITEMS>
-    __device__ __forceinline__ Unit sequence(const Attn &a, const PlanSmem<NT> &sm, int u, int &left, int &tiles) const
+    __device__ __forceinline__ Unit sequence(const Attn &a, int u, int &left, int &t) const
     {
-        const int *before = ITEMS ? sm.items : sm.units;
-        int lo = -1;                                // the last thread that starts at or before u
-#pragma unroll
-        for (int i = 0; i < NT; i += 32) lo += __popc(__ballot_sync(0xffffffffu, before[i + (threadIdx.x & 31)] <= u));
+        const int before = ITEMS ? items : units;
+        const int lo = __popc(__ballot_sync(0xffffffffu, before <= u)) - 1;       // the last lane that starts at or before u
         Unit x;
-        left = u - before[lo];
-        x.slot = sm.slots[lo];
+        left = u - __shfl_sync(0xffffffffu, before, lo);
+        x.slot = __shfl_sync(0xffffffffu, slots, lo);
+        x.b = lo;
+        if (per == 1) {
+            x.s.row0 = __shfl_sync(0xffffffffu, s.row0, lo);
+            x.s.n = __shfl_sync(0xffffffffu, s.n, lo);
+            x.s.pos0 = __shfl_sync(0xffffffffu, s.pos0, lo);
+            x.s.end = __shfl_sync(0xffffffffu, s.end, lo);
+            t = __shfl_sync(0xffffffffu, tiles, lo);
+            x.parts = __shfl_sync(0xffffffffu, parts, lo);
+            return x;
+        }
         for (x.b = lo * per;; ++x.b) {              // ends: u < total
             x.s = seq_of(a.p, x.b);
-            shape(a, x.s, tiles, x.parts);
-            const int n = tiles * a.p.heads, units = n * x.parts, mine = !ITEMS ? units : x.parts > 1 ? n : 0;
+            shape(a, x.s, t, x.parts);
+            const int n = t * a.p.heads, k = n * x.parts, mine = !ITEMS ? k : x.parts > 1 ? n : 0;
             if (left < mine || x.b + 1 >= a.p.seqs) break;
             left -= mine;
-            if (x.parts > 1) x.slot += units;
+            if (x.parts > 1) x.slot += k;
         }
         return x;
     }
-    __device__ __forceinline__ void place(const Attn &a, Unit &x, int item, int tiles) const
+    __device__ __forceinline__ void place(const Attn &a, Unit &x, int item, int t) const
     {
-        x.tile = tiles - 1 - a.by_heads(item);
+        x.tile = t - 1 - a.by_heads(item);
         x.h = item - a.by_heads(item) * a.p.heads;
         x.slot += item * x.parts;
     }
 
-    __device__ __forceinline__ Unit find(const Attn &a, const PlanSmem<NT> &sm, int u) const
+    __device__ __forceinline__ Unit find(const Attn &a, int u) const
     {
-        int left, tiles;
-        Unit x = sequence<false>(a, sm, u, left, tiles);
-        const int item = left / x.parts;
+        int left, t;
+        Unit x = sequence<false>(a, u, left, t);
+        const int item = x.parts == 1 ? left : left / x.parts;
         x.part = left - item * x.parts;
-        place(a, x, item, tiles);
+        place(a, x, item, t);
         return x;
     }
     // Row tile i of those in several parts.
-    __device__ __forceinline__ Unit find_item(const Attn &a, const PlanSmem<NT> &sm, int i) const
+    __device__ __forceinline__ Unit find_item(const Attn &a, int i) const
     {
-        int left, tiles;
-        Unit x = sequence<true>(a, sm, i, left, tiles);
+        int left, t;
+        Unit x = sequence<true>(a, i, left, t);
         x.part = 0;
-        place(a, x, left, tiles);
+        place(a, x, left, t);
         return x;
     }
 };
@@ -394,7 +372,7 @@ inline bool attention_maps(const q8act_paged_kv &kv, int rows, CUtensorMap *tk, 
 
 // The kernel for chunks (attention_tc.cu): its workspace, its launch (a: all but how units are cut), and the joining
 // kernel behind either.
-constexpr int CHUNK_ROWS = 256, CHUNK_TILE = 128, CHUNK_COUNTERS = 32;
+constexpr int CHUNK_ROWS = 256, CHUNK_TILE = 128;
 size_t attention_chunk_space(int dim);
 cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &kv, Attn a, void *ws, cudaStream_t stream);
 cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream);

@@ -23,7 +23,6 @@ namespace {
 constexpr int TILE = CHUNK_TILE;         // positions a step
 constexpr int QROWS = 128;               // rows of a row tile
 constexpr int ROWS = CHUNK_ROWS;         // of a unit: two row tiles
-constexpr int COUNTERS = CHUNK_COUNTERS; // threads that count the units
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;      // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
 constexpr int PARTS = 2;                 // of a tile's weights, handed to the MMAs one by one
@@ -67,7 +66,6 @@ constexpr int RECORDS = 4;                         // units known in advance, at
 constexpr int READERS = 8 + 1 + 1 + 1;             // warps that read them: all but warp 11
 
 struct Shared {
-    PlanSmem<COUNTERS> plan;
     uint64_t full[8], empty[8];                      // stages
     // Tile n of the CTA, in barrier n % 8: its values, and the next tile's keys, are there.  The stages hold four tiles
     // at most, so five barriers would do.
@@ -128,14 +126,6 @@ __device__ __forceinline__ void wait_ld(float *r)
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
-}
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *u)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
-          "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
 }
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *u)
 {
@@ -262,9 +252,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     griddep_wait();
     griddep_launch_dependents();
-    Plan<ROWS, TILE, COUNTERS> plan;
     tc_fence_before();
-    plan.make(a, sm.plan);                           // its barriers: the ones above exist for all
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
 
@@ -627,6 +616,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else {
             // ------------------------------ units, queries ------------------------------
+            Plan<ROWS, TILE> plan;
+            plan.make(a);
             uint32_t q_phase = 3, q_loads = 0;               // a bit a row tile
             bool ok = true;
             for (int round = 0;; ++round) {
@@ -636,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 Record rc;
                 rc.t0 = -1;
                 if (u < plan.total) {
-                    const Unit x = plan.find(a, sm.plan, (int)u);
+                    const Unit x = plan.find(a, (int)u);
                     rc.rows = x.s.n * a.group;
                     rc.r0 = x.tile * ROWS;
                     const int r1 = min(rc.r0 + ROWS, rc.rows) - 1;
