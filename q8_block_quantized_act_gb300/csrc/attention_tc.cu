@@ -2,11 +2,14 @@
 //   S = Q K^T,  P = e^(scale S - mx),  O = P V,  out = O / sum P
 //
 // A CTA holds two tiles of 128 rows (query heads of a group x tokens) and walks over tiles of 128
-// positions.  S and O are accumulators in tensor memory; P, rounded to the cache's type, takes the place
-// of S there and is the second product's first operand, so only Q, K and V go through shared memory.
-// While the four warps of one row tile turn S into P, the tensor cores work for the other tile.
+// positions.  S and O are accumulators in tensor memory; P, rounded to the cache's type, is the second product's
+// first operand from there, so only Q, K and V go through shared memory.  With 128 values a head the 512 columns
+// are full with two S and two O, so P takes the place of S: while the four warps of one row tile turn S into P,
+// the tensor cores work for the other tile.  With 64 values P has columns of its own, and the next S is computed
+// while its row tile's warps are still at work on this one.
 //   warps 0-3, 4-7  a row tile each: a thread a row, so maxima and sums need no exchange
-//   warp 8          issues the MMAs: P0 V, Q0 K', P1 V, Q1 K' (K' the next tile's keys)
+//   warp 8          issues the MMAs, K' the next tile's keys: P0 V, Q0 K', P1 V, Q1 K', or (P apart) Q0 K', P1 V of
+//                   the tile before, Q1 K', P0 V
 //   warp 9          brings pages of keys and values to shared memory (TMA, 128-byte swizzled)
 //   warp 10         in tiles of values that some row does not see as a whole clears those that no row sees and
 //                   looks for infinities and NaN among those that only some see (attention.cuh)
@@ -39,7 +42,9 @@ struct Cfg {
     static constexpr int HALF_BYTES = TILE * 128;
     static constexpr int OFF_OUT = 2 * Q_BYTES + STAGES * STAGE_BYTES;      // a softmax warp's 32 rows x 128 bytes on their way out
     static constexpr int OFF_SHARED = OFF_OUT + 8 * OUT_BYTES;
-    static constexpr uint32_t COL_S = 0, COL_O = 2 * TILE;     // tensor memory: S0 S1 O0 O1
+    // Tensor memory: S0 S1 O0 O1, and P0 P1 where there is room for them.  Where there is not, P takes the place of S.
+    static constexpr bool OWN_P = 2 * (TILE + D + TILE / 2) <= 512;
+    static constexpr uint32_t COL_S = 0, COL_O = 2 * TILE, COL_P = OWN_P ? COL_O + 2 * D : COL_S, P_STRIDE = OWN_P ? TILE / 2 : TILE;
     // Instruction descriptor, kind::f16: D f32 (bits 4-5), types of A and B (7-9, 10-12), B's major (16; 1: its
     // rows are K), N >> 3 (17-22), M >> 4 (24-28).
     static constexpr uint32_t IDESC_QK = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(QROWS >> 4) << 24);
@@ -71,6 +76,7 @@ struct Shared {
     // at most, so five barriers would do.
     uint64_t ready[8];
     uint64_t s_full[2], p_full[2][PARTS], q_full[2], q_empty[2], o_full[2], drained;
+    uint64_t s_empty[2], p_empty[2];                 // (P apart) S is in registers, P V is done
     uint64_t unit_full[RECORDS], unit_empty[RECORDS];
     Record units[RECORDS];
     uint32_t pages[8];                               // tile n of the CTA in word n % 8: its 16-position blocks whose page exists
@@ -138,6 +144,8 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *u)
           "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
         : "memory");
 }
+// The lowest n bits of a word, none or all where n is out of range.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16 bytes from global to shared memory, of which the first `bytes` are read and the others zeros.
@@ -238,6 +246,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&sm.q_full[q], 1);
             mbar_init(&sm.q_empty[q], 1);
             mbar_init(&sm.o_full[q], 1);
+            mbar_init(&sm.s_empty[q], 4);
+            mbar_init(&sm.p_empty[q], 1);
         }
         mbar_init(&sm.drained, 1);
         for (int i = 0; i < 16; ++i) sm.spoilt[i] = 0;
@@ -263,7 +273,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp >> 2, row = (warp & 3) * 32 + lane;         // of the row tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // the warp's lanes of tensor memory
         const uint32_t col_s = tmem + lanes + C::COL_S + q * TILE, col_o = tmem + lanes + C::COL_O + q * D;
-        uint32_t s_phase = 0, o_phase = 0, n = 0, tiles = 0;          // n: units with positions so far
+        const uint32_t col_p = tmem + lanes + C::COL_P + q * C::P_STRIDE;
+        uint32_t s_phase = 0, o_phase = 0, p_phase = 1, n = 0, tiles = 0;          // n: units with positions so far
         bool ok = true;
         for (int round = 0;; ++round) {
             ok = __all_sync(0xffffffffu, wait_or_abort(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag));
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int from = x.a[q], end = x.b[q], r = x.r0 + q * QROWS + row;
             const bool live = r < x.rows;
             const int pos = x.pos0 + a.by_group(live ? r : 0);
-            const int hi = live ? min(pos, x.end - 1) : INT_MAX, lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
+            const int hi = live ? min(pos, x.end - 1) : INT_MAX - 1, lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
             const int count = tiles - x.t0;              // tile t of the sequence is tile count + t of the CTA
             const bool some = end > from;
             tiles += x.t1 - x.t0;
@@ -290,11 +301,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(count + t) & 7]);
                 const bool edge = __any_sync(0xffffffffu, k0 + TILE - 1 > hi || k0 < lo) || pages != 0xff;
                 wait_ld<TILE>(s);
+                if constexpr (C::OWN_P) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.s_empty[q]);
+                }
                 if (edge) {
-                    const int from = lo - k0, to = hi - k0;
 #pragma unroll
-                    for (int j = 0; j < TILE; ++j)
-                        if (j < from || j > to || !(pages >> (j / 16) & 1)) s[j] = NEG;
+                    for (int c = 0; c < TILE / 32; ++c) {
+                        const uint32_t seen = bits_below(hi + 1 - k0 - 32 * c) & ~bits_below(lo - k0 - 32 * c) &
+                                              ((pages >> (2 * c) & 1 ? 0xffffu : 0u) | (pages >> (2 * c) & 2 ? 0xffff0000u : 0u));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(seen >> j & 1)) s[32 * c + j] = NEG;
+                    }
                 }
                 float m4[4] = {NEG, NEG, NEG, NEG};
 #pragma unroll
@@ -302,6 +322,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[j + 2 * i]), s[j + 2 * i + 1]);
                 const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale);
+                if constexpr (C::OWN_P) {           // the last products have taken P, and added to O
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.p_empty[q], p_phase, a.status, abort_flag));
+                    if (!ok) break;
+                    p_phase ^= 1;
+                    tc_fence_after();
+                }
                 if (first) {
                     mx = m;
                     first = false;
@@ -341,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             p[j] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                     }
-                    st32(col_s + N * c, p);
+                    st32(col_p + N * c, p);
                     wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -422,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp == 8) {
             // ------------------------------ MMA issuer ------------------------------
-            uint32_t q_phase = 0, p_phase = 0, tiles = 0;           // a bit a row tile; tiles so far
+            uint32_t q_phase = 0, p_phase = 0, s_phase = 3, tiles = 0;      // a bit a row tile; tiles so far
             int st = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -466,6 +492,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!wait(&sm.q_full[q], q_phase >> q & 1)) return false;
                         q_phase ^= 1u << q;
                     }
+                    if constexpr (C::OWN_P) {          // the last S (of the unit before, too) is in registers
+                        if (!wait(&sm.s_empty[q], s_phase >> q & 1)) return false;
+                        s_phase ^= 1u << q;
+                    }
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -489,8 +519,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (elect_one()) {
 #pragma unroll
                             for (int i = N * part; i < N * part + N; ++i)
-                                mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_S + q * TILE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
+                                mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_P + q * C::P_STRIDE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
                                        i > 0 ? 1u : add);
+                            if (C::OWN_P && part == PARTS - 1) tc_commit(&sm.p_empty[q]);
                             if (part == PARTS - 1 && t + 1 == rg.b[q]) tc_commit(&sm.o_full[q]);
                         }
                         __syncwarp();
@@ -505,20 +536,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait(&sm.full[st], phase) || !scores(0, rg.t0, at(kdesc, st)) || !scores(1, rg.t0, at(kdesc, st))) break;
                 release(st);
                 next();
-                for (int t = rg.t0; t < rg.t1; ++t, ++tiles) {
-                    const int vst = st;
-                    next();
-                    const int kst = st;
-                    const bool more = t + 1 < rg.t1;
-                    if (more) next();
-                    const uint64_t vd = at(vdesc, vst), kd = at(kdesc, kst);
-                    if (!wait(&sm.ready[tiles & 7], tiles >> 3 & 1) || !weighted(0, t, vd)) break;
-                    if (more && !scores(0, t + 1, kd)) break;
-                    if (!weighted(1, t, vd)) break;
-                    release(vst);
-                    if (more) {
-                        if (!scores(1, t + 1, kd)) break;
-                        release(kst);
+                if constexpr (C::OWN_P) {
+                    uint64_t v_last = 0;
+                    int st_last = 0;
+                    for (int t = rg.t0; t <= rg.t1; ++t) {
+                        const int vst = st;
+                        int kst = st;
+                        const bool here = t < rg.t1, more = t + 1 < rg.t1;
+                        if (here) next();
+                        kst = st;
+                        if (more) next();
+                        const uint64_t vd = at(vdesc, vst), kd = at(kdesc, kst);
+                        if (here && !wait(&sm.ready[tiles & 7], tiles >> 3 & 1)) break;
+                        tiles += here;
+                        if (more && !scores(0, t + 1, kd)) break;
+                        if (t > rg.t0) {
+                            if (!weighted(1, t - 1, v_last)) break;
+                            release(st_last);
+                        }
+                        if (more) {
+                            if (!scores(1, t + 1, kd)) break;
+                            release(kst);
+                        }
+                        if (here && !weighted(0, t, vd)) break;
+                        v_last = vd;
+                        st_last = vst;
+                    }
+                } else {
+                    for (int t = rg.t0; t < rg.t1; ++t, ++tiles) {
+                        const int vst = st;
+                        next();
+                        const int kst = st;
+                        const bool more = t + 1 < rg.t1;
+                        if (more) next();
+                        const uint64_t vd = at(vdesc, vst), kd = at(kdesc, kst);
+                        if (!wait(&sm.ready[tiles & 7], tiles >> 3 & 1) || !weighted(0, t, vd)) break;
+                        if (more && !scores(0, t + 1, kd)) break;
+                        if (!weighted(1, t, vd)) break;
+                        release(vst);
+                        if (more) {
+                            if (!scores(1, t + 1, kd)) break;
+                            release(kst);
+                        }
                     }
                 }
             }
