@@ -7,8 +7,13 @@
 // (2^-24 of the angle) and go through sincospif.
 //
 // A thread owns 16 values of a head: two vectors of 8 that are rotated against each other (halves), or
-// 16 consecutive ones.  A CTA takes a few tokens, so that a token's sines and cosines are computed once
-// and serve its heads; few tokens are spread over several CTAs by heads.
+// 16 consecutive ones.  A CTA takes one or two tokens, so that a token's sines and cosines are computed once
+// and serve its heads; few tokens are spread over several CTAs by heads.  The first values' loads are issued
+// before the chain starts -> length -> page -> angle, which no bytes pass during.
+//
+// Bound by memory: 8191 tokens of 32 + 8 heads x 128 bf16 36.5 us (5.5 TB/s, 0.81 of a copy; one token 3.4 us: launch
+// and that chain).  What is missing is that chain, about 1 us of each CTA's 5: more values ahead in registers leave
+// fewer CTAs to an SM and lost (256 threads x 4 tokens ahead 46.7 us, x 2 40.7).
 #include "launch.h"
 #include "paged.cuh"
 #include "types.cuh"
@@ -16,7 +21,7 @@
 namespace q8 {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 struct Args {
     Paged p;
@@ -32,29 +37,30 @@ struct Token {
     int row;             // or -1: behind the last sequence
 };
 
-// 16 values of T as f32, in two groups of 8.
+// 16 values of T, two groups of 8, on their way.
 template <typename T>
-__device__ __forceinline__ void load16(const T *a, const T *b, float (&x)[16])
-{
+struct Sixteen {
+    uint4 w[sizeof(T)];
+    __device__ __forceinline__ void load(const T *a, const T *b)
+    {
+        constexpr int N = sizeof(T) / 2;             // vectors of 8 values
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(h ? b : a);
-        if constexpr (sizeof(T) == 4) {
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                unpack<T>(__ldg(p + i), f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[8 * h + 4 * i + j] = f[j];
-            }
-        } else {
-            float f[8];
-            unpack<T>(__ldg(p), f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * h + j] = f[j];
+        for (int i = 0; i < N; ++i) {
+            w[i] = __ldcs(reinterpret_cast<const uint4 *>(a) + i);
+            w[N + i] = __ldcs(reinterpret_cast<const uint4 *>(b) + i);
         }
     }
-}
+    __device__ __forceinline__ void values(float (&x)[16]) const
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+            float f[VEC<T>];
+            unpack<T>(w[i], f);
+#pragma unroll
+            for (int j = 0; j < VEC<T>; ++j) x[VEC<T> * i + j] = f[j];
+        }
+    }
+};
 
 template <typename C>
 __device__ __forceinline__ void store16(C *a, C *b, const float (&x)[16])
@@ -68,6 +74,34 @@ __device__ __forceinline__ void store16(C *a, C *b, const float (&x)[16])
     }
 }
 
+// A thread's 16 values of a token: where they are read and, of each token, written.
+template <typename T, typename C, int D>
+struct Place {
+    const T *src;            // of token row 0
+    C *dst;                  // of row 0, or of the cache's first slot
+    int64_t ld;
+    int at0, at1, u;
+    bool is_q, halves, rotated;
+
+    __device__ __forceinline__ Place(const Args &a, int unit)
+    {
+        constexpr int UNITS = D / 16;
+        const int hk = a.p.heads, head = unit / UNITS;
+        u = unit % UNITS;
+        is_q = head < a.hq;
+        const bool is_v = head >= a.hq + hk;
+        const int h = is_q ? head : is_v ? head - a.hq - hk : head - a.hq;
+        ld = is_q ? a.ldq : is_v ? a.ldv : a.ldk;
+        rotated = !is_v && 16 * u < a.rot;
+        halves = rotated && !a.interleaved;
+        at0 = halves ? 8 * u : 16 * u;
+        at1 = halves ? (a.rot >> 1) + 8 * u : 16 * u + 8;
+        src = static_cast<const T *>(is_q ? a.q : is_v ? a.v : a.k) + h * D;
+        dst = is_q ? static_cast<C *>(a.qo) + h * D
+                   : static_cast<C *>(is_v ? a.vc : a.kc) + h * ((int64_t)D << a.p.page_shift);
+    }
+};
+
 // T: the projection's type, C: the cache's, D: values a head, TOK: tokens a CTA.
 template <typename T, typename C, int D, int TOK>
 __global__ void __launch_bounds__(THREADS) append_kernel(Args a)
@@ -79,6 +113,17 @@ __global__ void __launch_bounds__(THREADS) append_kernel(Args a)
     griddep_enter();
     const Paged &p = a.p;
     const int first = blockIdx.x * TOK;
+    // This CTA's part of the heads.  The first values are under way while positions, pages and angles are worked out.
+    const int units = (a.hq + 2 * p.heads) * UNITS;
+    const int u0 = (int)((int64_t)units * blockIdx.y / gridDim.y), u1 = (int)((int64_t)units * (blockIdx.y + 1) / gridDim.y);
+    int unit = u0 + threadIdx.x;
+    Sixteen<T> w[TOK];
+    auto load = [&](const Place<T, C, D> &at) {
+#pragma unroll
+        for (int t = 0; t < TOK; ++t)
+            if (first + t < p.m) w[t].load(at.src + (first + t) * at.ld + at.at0, at.src + (first + t) * at.ld + at.at1);
+    };
+    if (unit < u1) load(Place<T, C, D>(a, unit));
     if (threadIdx.x < TOK) {
         const int row = first + threadIdx.x;
         Token t{-1, -1};
@@ -114,59 +159,40 @@ __global__ void __launch_bounds__(THREADS) append_kernel(Args a)
     }
     __syncthreads();
 
-    const int hk = p.heads, heads = a.hq + 2 * hk, units = heads * UNITS;
-    const int64_t head_stride = (int64_t)D << p.page_shift;
-    // This CTA's part of the heads.
-    const int u0 = (int)((int64_t)units * blockIdx.y / gridDim.y), u1 = (int)((int64_t)units * (blockIdx.y + 1) / gridDim.y);
-    const int per = u1 - u0;
-#pragma unroll 2
-    for (int i = threadIdx.x; i < per * TOK; i += THREADS) {
-        const int t = i / per, unit = u0 + i - t * per;
-        const Token tk = tok[t];
-        if (tk.row < 0) continue;
-        const int head = unit / UNITS, u = unit % UNITS;
-        const bool is_q = head < a.hq, is_v = head >= a.hq + hk;
-        const int h = is_q ? head : is_v ? head - a.hq - hk : head - a.hq;
-        const T *src = is_q   ? static_cast<const T *>(a.q) + tk.row * a.ldq
-                       : is_v ? static_cast<const T *>(a.v) + tk.row * a.ldv
-                              : static_cast<const T *>(a.k) + tk.row * a.ldk;
-        const bool rotated = !is_v && 16 * u < a.rot;
-        const bool halves = rotated && !a.interleaved;
-        const int at0 = halves ? 8 * u : 16 * u, at1 = halves ? half + 8 * u : 16 * u + 8;
-        src += h * D;
-        C *dst;
-        if (is_q) {
-            dst = static_cast<C *>(a.qo) + tk.row * a.ldqo + h * D;
-        } else {
-            if (tk.offset < 0) continue;
-            dst = static_cast<C *>(is_v ? a.vc : a.kc) + tk.offset + h * head_stride;
-        }
-        float x[16];
-        load16(src + at0, src + at1, x);
-        if (halves) {
-            const float4 *r = reinterpret_cast<const float4 *>(&rotation[t][8 * u]);
+    for (; unit < u1; unit += THREADS) {
+        const Place<T, C, D> at(a, unit);
+        if (unit >= u0 + THREADS) load(at);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float4 cs = r[j / 2];
-                const float a0 = x[j], b0 = x[8 + j], a1 = x[j + 1], b1 = x[9 + j];
-                x[j] = a0 * cs.x - b0 * cs.y;
-                x[8 + j] = b0 * cs.x + a0 * cs.y;
-                x[j + 1] = a1 * cs.z - b1 * cs.w;
-                x[9 + j] = b1 * cs.z + a1 * cs.w;
-            }
-        } else if (rotated) {
-            const float4 *r = reinterpret_cast<const float4 *>(&rotation[t][8 * u]);
+        for (int t = 0; t < TOK; ++t) {
+            const Token tk = tok[t];
+            if (tk.row < 0 || (!at.is_q && tk.offset < 0)) continue;
+            C *dst = at.dst + (at.is_q ? tk.row * a.ldqo : tk.offset);
+            float x[16];
+            w[t].values(x);
+            const float4 *r = reinterpret_cast<const float4 *>(&rotation[t][8 * at.u]);
+            if (at.halves) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float4 cs = r[j / 2];
-                const float a0 = x[2 * j], b0 = x[2 * j + 1], a1 = x[2 * j + 2], b1 = x[2 * j + 3];
-                x[2 * j] = a0 * cs.x - b0 * cs.y;
-                x[2 * j + 1] = b0 * cs.x + a0 * cs.y;
-                x[2 * j + 2] = a1 * cs.z - b1 * cs.w;
-                x[2 * j + 3] = b1 * cs.z + a1 * cs.w;
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 cs = r[j / 2];
+                    const float a0 = x[j], b0 = x[8 + j], a1 = x[j + 1], b1 = x[9 + j];
+                    x[j] = a0 * cs.x - b0 * cs.y;
+                    x[8 + j] = b0 * cs.x + a0 * cs.y;
+                    x[j + 1] = a1 * cs.z - b1 * cs.w;
+                    x[9 + j] = b1 * cs.z + a1 * cs.w;
+                }
+            } else if (at.rotated) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 cs = r[j / 2];
+                    const float a0 = x[2 * j], b0 = x[2 * j + 1], a1 = x[2 * j + 2], b1 = x[2 * j + 3];
+                    x[2 * j] = a0 * cs.x - b0 * cs.y;
+                    x[2 * j + 1] = b0 * cs.x + a0 * cs.y;
+                    x[2 * j + 2] = a1 * cs.z - b1 * cs.w;
+                    x[2 * j + 3] = b1 * cs.z + a1 * cs.w;
+                }
             }
+            store16(dst + at.at0, dst + at.at1, x);
         }
-        store16(dst + at0, dst + at1, x);
     }
 }
 
@@ -192,8 +218,10 @@ cudaError_t launch_append_kv(const DeviceInfo &dev, const q8act_paged_kv &kv, co
                     parts = parts < 1 ? 1 : parts > most ? most : parts;
                     return launch_dependent(kern, dim3((unsigned)blocks, (unsigned)parts), THREADS, 0, stream, a);
                 };
-                if (m >= 4 * 4 * (int64_t)dev.num_sms)
-                    return kv.dim == 64 ? go(append_kernel<T, C, 64, 4>, 4) : go(append_kernel<T, C, 128, 4>, 4);
+                // Two tokens a CTA share its sines' latency: 8191 tokens of 32 + 8 heads x 128 bf16 36.5 us, one by one
+                // 37.8, four 39.6.  Few tokens are worth a CTA each (62 tokens: the same 3.8 us).
+                if (m >= 4 * (int64_t)dev.num_sms)
+                    return kv.dim == 64 ? go(append_kernel<T, C, 64, 2>, 2) : go(append_kernel<T, C, 128, 2>, 2);
                 return kv.dim == 64 ? go(append_kernel<T, C, 64, 1>, 1) : go(append_kernel<T, C, 128, 1>, 1);
             }
         });
