@@ -153,6 +153,21 @@ def test_hidden_values_do_not_matter(bad, t, hint):
 
 
 @HINTS
+@pytest.mark.parametrize("d", [64, 128])
+def test_hidden_values_in_long_sequences(d, hint):
+    """The same where several CTAs, and both halves of one, have parts of a row: values in tiles of either half."""
+    t = torch.float16
+    batch = ref.Batch([(1500, 9), (2430, 3)], 1, d, 32, t, seed=19, filler=math.nan)
+    for b, p in ((0, 1503), (0, 1507), (1, 2431), (1, 2432)):
+        at, slot = batch.place(b, p)
+        batch.v[at, :, slot, 3] = math.inf
+    q = batch.randn(batch.m, 3, d)
+    for window in (0, 1300):
+        want, tol = ref.attention(batch, q, d ** -0.5, window, t)
+        ref.close(run(batch, q, hint, window), want, tol)
+
+
+@HINTS
 def test_lowest_values_and_large_scores(hint):
     """Scores that overflow to -inf count nothing, large ones pick one position."""
     batch = ref.Batch([(100, 2), (0, 30)], 1, 64, 16, torch.float16, seed=11)
