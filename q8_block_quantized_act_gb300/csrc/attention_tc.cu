@@ -485,6 +485,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (rg.t0 < 0) break;
                 if (lane == 0) mbar_arrive(&sm.unit_empty[round % RECORDS]);
                 if (rg.t0 == rg.t1) continue;
+                auto issue_qk = [&](int q, uint64_t kd) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        mma_ss(tmem + C::COL_S + q * TILE, qdesc + ((q * C::Q_BYTES + (i >> 2) * (QROWS * 128) + (i & 3) * 32) >> 4),
+                               kd + ((i >> 2) * C::HALF_BYTES + (i & 3) * 32 >> 4), IDESC_QK, i > 0);
+                };
+                auto issue_pv = [&](int q, uint64_t vd, int from, int to, uint32_t add) {
+#pragma unroll
+                    for (int i = from; i < to; ++i)
+                        mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_P + q * C::P_STRIDE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
+                               i > 0 ? 1u : add);
+                };
                 // S = Q K^T of the tile whose keys are at kd.
                 auto scores = [&](int q, int t, uint64_t kd) {
                     if (t < rg.a[q] || t >= rg.b[q]) return true;
@@ -498,10 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            mma_ss(tmem + C::COL_S + q * TILE, qdesc + ((q * C::Q_BYTES + (i >> 2) * (QROWS * 128) + (i & 3) * 32) >> 4),
-                                   kd + ((i >> 2) * C::HALF_BYTES + (i & 3) * 32 >> 4), IDESC_QK, i > 0);
+                        issue_qk(q, kd);
                         tc_commit(&sm.s_full[q]);
                         if (t + 1 == rg.b[q]) tc_commit(&sm.q_empty[q]);
                     }
@@ -517,10 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!wait(&sm.p_full[q][part], p_phase >> q & 1)) return false;
                         tc_fence_after();
                         if (elect_one()) {
-#pragma unroll
-                            for (int i = N * part; i < N * part + N; ++i)
-                                mma_ts(tmem + C::COL_O + q * D, tmem + C::COL_P + q * C::P_STRIDE + 8 * i, vd + (i * 2048 >> 4), IDESC_PV,
-                                       i > 0 ? 1u : add);
+                            issue_pv(q, vd, N * part, N * part + N, add);
                             if (C::OWN_P && part == PARTS - 1) tc_commit(&sm.p_empty[q]);
                             if (part == PARTS - 1 && t + 1 == rg.b[q]) tc_commit(&sm.o_full[q]);
                         }
@@ -563,7 +569,42 @@ __global__ void __launch_bounds__(THREADS, 1)
                         st_last = vst;
                     }
                 } else {
+                    // Tiles that both row tiles take, with a next one that they take too, and neither's first or
+                    // last but one: no questions asked.  (This warp's instructions pace the tensor cores.)
+                    const int plain0 = max(rg.a[0], rg.a[1]) + 1, plain1 = min(rg.b[0], rg.b[1]) - 2;
                     for (int t = rg.t0; t < rg.t1; ++t, ++tiles) {
+#pragma unroll 1
+                        for (; t >= plain0 && t < plain1; ++t, ++tiles) {
+                            const int vst = st;
+                            next();
+                            const int kst = st;
+                            next();
+                            const uint64_t vd = at(vdesc, vst), kd = at(kdesc, kst);
+                            if (!wait(&sm.ready[tiles & 7], tiles >> 3 & 1)) break;
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                                for (int part = 0; part < PARTS; ++part) {
+                                    constexpr int N = TILE / 16 / PARTS;
+                                    if (!wait(&sm.p_full[q][part], p_phase >> q & 1)) break;
+                                    tc_fence_after();
+                                    if (elect_one()) {
+                                        issue_pv(q, vd, N * part, N * part + N, 1u);
+                                        if (part == PARTS - 1) {
+                                            if (q == 1) tc_commit(&sm.empty[vst]);
+                                            issue_qk(q, kd);
+                                            tc_commit(&sm.s_full[q]);
+                                            if (q == 1) tc_commit(&sm.empty[kst]);
+                                        }
+                                    }
+                                    __syncwarp();
+                                }
+                                if (!ok) break;
+                            }
+                            p_phase ^= 3;
+                            if (!ok) break;
+                        }
+                        if (!ok) break;
                         const int vst = st;
                         next();
                         const int kst = st;
