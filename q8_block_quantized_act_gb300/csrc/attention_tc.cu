@@ -171,6 +171,13 @@ __device__ __forceinline__ void store_rows(uint8_t *out, const uint4 (&v)[8], ui
     __syncwarp();
 }
 
+// A whole warp's wait for one barrier; one look where it is over.
+__device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           __all_sync(0xffffffffu, wait_or_abort(bar, parity, status, abort_flag));
+}
+
 // The unit of this CTA's round: rounds run forwards and backwards in turn, since earlier units are longer.
 __device__ __forceinline__ int64_t unit_of(int round)
 {
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t s_phase = 0, o_phase = 0, p_phase = 1, n = 0, tiles = 0;          // n: units with positions so far
         bool ok = true;
         for (int round = 0;; ++round) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag));
+            ok = arrived(&sm.unit_full[round % RECORDS], round / RECORDS & 1, a.status, abort_flag);
             const Record &x = sm.units[round % RECORDS];
             if (!ok || x.t0 < 0) break;
             const int from = x.a[q], end = x.b[q], r = x.r0 + q * QROWS + row;
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float mx = NEG, sum = 0.0f;
             bool first = true;
             for (int t = from; t < end; ++t) {
-                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[q], s_phase, a.status, abort_flag));
+                ok = arrived(&sm.s_full[q], s_phase, a.status, abort_flag);
                 if (!ok) break;
                 s_phase ^= 1;
                 tc_fence_after();
@@ -316,14 +323,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (!(seen >> j & 1)) s[32 * c + j] = NEG;
                     }
                 }
-                float m4[4] = {NEG, NEG, NEG, NEG};
+                float m4[8] = {NEG, NEG, NEG, NEG, NEG, NEG, NEG, NEG};
 #pragma unroll
-                for (int j = 0; j < TILE; j += 8)
+                for (int j = 0; j < TILE; j += 16)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[j + 2 * i]), s[j + 2 * i + 1]);
-                const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale);
+                    for (int i = 0; i < 8; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[j + 2 * i]), s[j + 2 * i + 1]);
+                const float m = fmaxf(mx, fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), fmaxf(fmaxf(m4[4], m4[5]), fmaxf(m4[6], m4[7]))) * a.scale);
                 if constexpr (C::OWN_P) {           // the last products have taken P, and added to O
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&sm.p_empty[q], p_phase, a.status, abort_flag));
+                    ok = arrived(&sm.p_empty[q], p_phase, a.status, abort_flag);
                     if (!ok) break;
                     p_phase ^= 1;
                     tc_fence_after();
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok) break;
             if (some) {
-                ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[q], o_phase, a.status, abort_flag));
+                ok = arrived(&sm.o_full[q], o_phase, a.status, abort_flag);
                 if (!ok) break;
                 o_phase ^= 1;
                 tc_fence_after();
@@ -452,15 +459,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             int st = 0;
             uint32_t phase = 0;
             bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = arrived(bar, parity, a.status, abort_flag); };
             const uint64_t qdesc = smem_desc_sw128(smem_u32(smem)), kdesc = smem_desc_sw128(smem_u32(stages));
             const uint64_t vdesc = smem_desc_mn_sw128(smem_u32(stages), C::HALF_BYTES);
-            // This warp's instructions pace the tensor cores (it shares its scheduler with softmax warps), so a wait
-            // that is over takes one look, and there are few of them.
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-                    ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, a.status, abort_flag));
-                return ok;
-            };
+            // This warp's instructions pace the tensor cores (it shares its scheduler with softmax warps): few waits, no
+            // questions that can be spared.
             auto next = [&] {
                 if (++st == STAGES) {
                     st = 0;
