@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
             const int b = place.b;
             x += min((long long)(place.n - place.tile), x1 - x);
             place.next(a, line);
+            // (on its way while the queries' copies are set up, as the next tile's is while this one's are)
+            int64_t page = lane < per_tile && p.t0 < p.t1 ? page_of(a.p, b, (p.t0 * TILE >> a.p.page_shift) + lane) : -1;
             // Queries, a row a lane (rows behind the last one hold anything: what comes of them goes nowhere).
             const int qb = parts % C::Q_BUFFERS;
             ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[qb], (parts / C::Q_BUFFERS & 1) ^ 1, a.status, abort_flag));
@@ -313,13 +315,13 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
             __syncwarp();
             for (int t = p.t0; t < p.t1; ++t, ++it) {
                 const int pos = t * TILE;
-                const int64_t page = lane < per_tile ? page_of(a.p, b, (pos >> a.p.page_shift) + lane) : -1;
                 const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
                 uint32_t okm = 0;
                 for (int j = 0; j < per_tile; ++j)
                     if (good >> j & 1) okm |= ((1u << blocks) - 1) << (j * blocks);
                 // A page that does not exist: a box outside the tensor, which reads as zeros.
                 const int id = page < 0 ? (int)a.p.pages : (int)page;
+                if (t + 1 < p.t1 && lane < per_tile) page = page_of(a.p, b, ((pos + TILE) >> a.p.page_shift) + lane);
                 ok = __all_sync(0xffffffffu, wait_or_abort(&sm.empty[st], phase, a.status, abort_flag));
                 if (!ok) break;
                 if (lane == 0) {
