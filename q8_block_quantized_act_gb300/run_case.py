@@ -8,7 +8,8 @@ gemm_preq, gemm_repacked (fused quantize, load-time repacked weights), repack, d
 gemv_q4_0, dequant_q4_0, and the K-quant passes gemv_q6_k / gemv_q4_k / gemv_q5_k and
 dequant_q6_k / dequant_q4_k / dequant_q5_k (on seeded random superblocks), norm and norm_mmq
 (residual and weight, f16), quantize_mxfp4 and dequant_mxfp4 (f16), gemm_mxfp4 (f16 activation
-quantized in the call, f16 out) and logprobs (m rows of n f16 logits, 8 alternatives).
+quantized in the call, f16 out), logprobs (m rows of n f16 logits, 8 alternatives), and append_kv and
+attention (m new tokens of one sequence of n positions, k / 128 query heads, k / 512 of keys, bf16, pages of 128).
 Inputs are the seeded synthetic ones of q8_block_quantized_act_gb300.inputs;
 one warm-up launch precedes the `--reps` launches.
 """
@@ -23,7 +24,7 @@ def main(argv=None):
                                        "gemm_preq", "gemm_repacked", "repack", "dequant", "gemv_q4_0",
                                        "dequant_q4_0", "gemv_q6_k", "gemv_q4_k", "gemv_q5_k",
                                        "dequant_q6_k", "dequant_q4_k", "dequant_q5_k", "norm", "norm_mmq",
-                                       "quantize_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "logprobs"))
+                                       "quantize_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "logprobs", "append_kv", "attention"))
     ap.add_argument("--m", type=int, default=1)
     ap.add_argument("--n", type=int, default=4096)
     ap.add_argument("--k", type=int, default=4096)
@@ -61,10 +62,21 @@ def main(argv=None):
     if a.kernel == "logprobs":
         logits = torch.randn((m, n), device=dev).mul_(2.5).half()
         tok = torch.zeros(m, dtype=torch.int32, device=dev)
+    if a.kernel in ("append_kv", "attention"):
+        hq, hk, pages, i32 = k // 128, max(1, k // 512), -(-n // 128), dict(dtype=torch.int32, device=dev)
+        kc, vc = (torch.randn((pages, hk, 128, 128), device=dev, dtype=torch.bfloat16) for _ in range(2))
+        kv = q8.PagedKV(kc, vc, torch.arange(pages, **i32).view(1, -1), torch.tensor([0, m], **i32), torch.tensor([n], **i32))
+        qkv = torch.randn((m, hq + 2 * hk, 128), device=dev, dtype=torch.bfloat16)
+        parts = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        turns, aws, q16 = q8.rope_turns([10000.0 ** (-i / 64) for i in range(64)], dev), q8.attention_workspace(kv, hq), parts[0].contiguous()
     torch.cuda.synchronize()
 
     def once():
-        if a.kernel == "norm":
+        if a.kernel == "append_kv":
+            q8.append_kv(kv, *parts, turns=turns, out=q16)
+        elif a.kernel == "attention":
+            q8.attention(kv, q16, max_new=m, ws=aws)
+        elif a.kernel == "norm":
             q8.rmsnorm_q8_1(x16, g16, residual=r16, residual_out=r16)
         elif a.kernel == "norm_mmq":
             q8.rmsnorm_q8_1_mmq(x16, g16, residual=r16, residual_out=r16)
