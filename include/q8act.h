@@ -1,7 +1,8 @@
 /*
  * q8act.h -- C ABI of libq8act.so: a GB300 (sm_103a) implementation of the Q8_0 weight x
  * q8_1 activation block-quantized matmul of an LLM decoder, and of what stands next to it: the
- * norm in front of a product, MXFP4 weights and activations, log probabilities of logits.
+ * norm in front of a product, the paged key/value cache and the attention over it, MXFP4 weights and
+ * activations, log probabilities of logits.
  *
  * The operation, with the notation used throughout:
  *   W   Q8_0 weights, n rows ("out_f") of k/32 blocks ("in_f" = k).  A block is 34 bytes:
@@ -504,12 +505,15 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   p - window < j where window > 0; keys and values of head h * heads / heads_q.
  *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
  *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
+ *       It must not overlap q.
  *   scale > 0.  A token that sees no position gets zeros.  What is at masked places (beyond lens, behind the
- *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
+ *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.  (A
+ *       non-finite value at a position that some rows of a tile see and others do not is exact but slow: their sums
+ *       are taken again one by one, about 0.1 s for 32768 positions.)
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
  *       to the cache's type for their product with the values.
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
- *       known).  It chooses the kernel and may be wrong.
+ *       known).  It chooses the kernel (max_new * heads_q / heads up to 32: the one for few rows) and may be wrong.
  *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses
  *       until the call's work is done; it needs no preparation and holds nothing between calls.
  */

@@ -16,6 +16,18 @@
 //   warp 11         works out the CTA's next units for the others, and brings their queries
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
+//
+// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 322 us
+// (1.71 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
+// cycles and takes about 2450, the chain of one row tile: S 230 cycles after its MMAs, maximum 490, weights 1000 (P in two
+// parts, the products of the first under way), products and next S 800.  64 values: 64 + 8 heads, 8000 tokens, window 1024 f16
+// 174 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
+// rest of the softmax 1900; ten tiles a unit, of which three are masked, leave 3400 cycles between units beside them.
+// What was tried without gain: a thread half a row (640 threads: registers spill), S twice through registers
+// (the loads' latency), P in four parts, a warp of its own for the output (512 threads leave 128 registers), an MMA
+// warp a row tile (they fall into step: 457 us), both halves on the same rows with every other tile (35 rows, 6000
+// positions: 31 -> 42 us), equal stretches as for few tokens (a cut costs two f32 outputs, a change of units and the
+// join: 509 tokens at 16384 110 -> 125 us).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -826,7 +838,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     attention_place(a, ws, SLOTS, ROWS);
     a.ctas = dev.num_sms;
     a.least = 2;
-    a.unit_cost = 8.0f;
+    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and takes 132 us, 8 in 2 and 115)
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     // Row tiles of whole tokens come as one box; others are gathered row by row.
@@ -839,8 +851,6 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     } else {
         tq = tk;
     }
-    const int64_t units = (int64_t)kv.heads * ((int64_t)a.p.m * a.group / ROWS + std::min(kv.seqs, a.p.m)) + SLOTS;    // at most
-    const unsigned grid = (unsigned)std::min<int64_t>(units, dev.num_sms);
     return with_type(kv.type, [&](auto x) -> cudaError_t {
         using T = decltype(x);
         if constexpr (sizeof(T) == 4) {
@@ -852,7 +862,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
                 static_assert(smem <= 227 * 1024, "shared memory");
                 cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(grid), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
+                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(a.ctas), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
                 return e == cudaSuccess ? launch_attention_chunk_join(dev, a, D, stream) : e;
             };
             return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});

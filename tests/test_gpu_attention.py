@@ -81,6 +81,13 @@ def test_output_types_and_scale(t, out_t, hint):
 
 
 @HINTS
+@pytest.mark.parametrize("hq,hk,d", [(40, 1, 64), (96, 2, 128), (300, 1, 64), (6, 6, 128)])
+def test_groups_of_any_size(hq, hk, d, hint):
+    """More query heads to a key head than a row tile has rows, and none to share with."""
+    check(ref.Batch([(70, 3), (5, 1), (0, 20)], hk, d, 16, torch.float16, seed=hq), hq, hint)
+
+
+@HINTS
 def test_long_sequences_in_parts(hint):
     """Few rows over many positions: the sequence is shared by many CTAs and joined."""
     check(ref.Batch([(20000, 1)], 1, 128, 64, torch.bfloat16, seed=1), 4, hint)
