@@ -506,10 +506,8 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
  *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
  *       It must not overlap q.
- *   scale > 0.  A token that sees no position gets zeros.  What is at masked places (beyond lens, behind the
- *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.  (A
- *       non-finite value at a position that some rows of a tile see and others do not is exact but slow: their sums
- *       are taken again one by one, about 0.1 s for 32768 positions.)
+ *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros.  What is at masked places (beyond lens, behind the
+ *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
  *       to the cache's type for their product with the values.
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not

@@ -776,7 +776,7 @@ int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *
     int rc = check_paged(kv, m, heads_q);
     if (rc) return rc;
     if (!known_type(otype)) return Q8ACT_ERR_TYPE;
-    if (!attention_heads(heads_q, kv->heads, kv->dim) || !(scale > 0.0f) || scale > 3e38f || window < 0 ||
+    if (!attention_heads(heads_q, kv->heads, kv->dim) || !(scale > 0.0f) || scale > 0x1p100f || window < 0 ||
         window > (1 << 30) || max_new < 0)
         return Q8ACT_ERR_DIMS;
     if ((rc = check_rows(q, ldq, (int64_t)heads_q * kv->dim, kv->type)) ||

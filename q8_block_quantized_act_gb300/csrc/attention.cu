@@ -51,7 +51,7 @@ struct Shared {
     uint64_t full[6], empty[6], q_full[2], q_empty[2];
     uint32_t ok[6];                       // a stage's 16-position blocks whose page exists
     float mx[2][KEY_WARPS][ROWS], sum[2][KEY_WARPS][ROWS];
-    int spoilt[2][KEY_WARPS];             // a non-finite value that not all rows see
+    int spoilt[2][KEY_WARPS];             // a non-finite value that some rows see has been cleared
     int abort_flag;
 };
 
@@ -253,12 +253,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
-// Whether a word's low or high half is an infinity or NaN.
+// A word's halves, zeros in place of infinities and NaN.
 template <typename T>
-__device__ __forceinline__ bool non_finite2(uint32_t w)
+__device__ __forceinline__ uint32_t finite2(uint32_t w)
 {
     constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    return (w & E) == E || (w >> 16 & E) == E;
+    return w & ((w & E) == E ? 0xffff0000u : ~0u) & ((w >> 16 & E) == E ? 0x0000ffffu : ~0u);
 }
 
 template <typename T, int D, int MT>
@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
                     pf[mt][i + 2] = pack2<T>(e[2], e[3]);
                 }
             }
-            // Values of positions that no row sees are cleared.
+            // Values of positions that no row sees are cleared, and in blocks that not all rows see as a whole non-finite
+            // ones.
             uint32_t keep[2] = {~0u, ~0u};
             if (part) {
 #pragma unroll
@@ -482,7 +483,9 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         vf[i] &= keep[i & 1];
-                        spoilt |= non_finite2<T>(vf[i]);
+                        const uint32_t w = finite2<T>(vf[i]);
+                        spoilt |= w != vf[i];
+                        vf[i] = w;
                     }
                 }
 #pragma unroll
@@ -578,10 +581,14 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
                     const int pos = s0.pos0 + tok;
                     const int k0 = max(a.window ? pos - a.window + 1 : 0, p.t0 * TILE), k1 = min(min(pos, s0.end - 1), p.t1 * TILE - 1);
                     float e[D / 8];
-                    exact_values<T, D>(a, b, p.h, static_cast<const T *>(a.q) + (s0.row0 + tok) * a.ldq + head * D, k0, k1,
-                                       base, [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); }, e);
+                    for (int j = 0; j < D / 8; ++j) e[j] = 0.0f;
+                    const T *qr = static_cast<const T *>(a.q) + (s0.row0 + tok) * a.ldq + head * D;
+                    auto col = [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); };
+                    // The blocks of 16 that were taken as not seen by all rows.
+                    if (a.window) add_non_finite<T, D>(a, b, p.h, qr, k0, min(k1, (last - a.window) | 15), base, col, e);
+                    add_non_finite<T, D>(a, b, p.h, qr, max(k0, (min(first, p.span.hi) + 1) & ~15), k1, base, col, e);
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j) acc[j] = e[j];
+                    for (int j = 0; j < D / 8; ++j) acc[j] += e[j];
                 }
                 if (slot >= 0) {
                     const int64_t at = (int64_t)slot * ROWS + rr;

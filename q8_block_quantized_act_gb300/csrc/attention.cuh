@@ -1,5 +1,5 @@
 // attention.cuh -- what the attention kernels share: how a batch is cut into units of work, masks,
-// the exact way round non-finite values, partial results and output.
+// the way round non-finite values, partial results and output.
 //
 // Rows: the query heads that share a key/value head are rows of one matrix, row r of a sequence being
 // query head r % group of its new token r / group; ROWS consecutive rows are a row tile.  A row tile's
@@ -192,7 +192,7 @@ struct Plan {
             for (int b = b0; b < b1; ++b) {
                 int t, p;
                 shape(a, seq_of(a.p, b), t, p);
-                v[0] += t * a.p.heads * p;
+                v[0] = min(v[0] + t * a.p.heads * p, (1 << 26) - 1);     // (more only where starts do not ascend)
                 if (p > 1) {
                     v[1] += t * a.p.heads * p;
                     v[2] += t * a.p.heads;
@@ -294,47 +294,33 @@ __device__ __forceinline__ int out_size(int type) { return type == Q8ACT_F32 ? 4
 // ---------------------------------------------------------------------------------------
 // Non-finite values in places that only some rows of a tile see.  The tensor cores multiply every
 // value of a tile by every row's weight, and 0 times infinity or NaN is NaN: a row would be spoilt by a
-// value that its mask hides from it.  Values that no row of the unit sees are cleared; where some rows
-// see a non-finite one, the unit's sums of weighted values are taken again here, value by value and
-// only over what the row sees.  Slow, and reached by such inputs only.
-// acc[j] = sum over positions k0 .. k1 of exp2(score - mx) v[position][col(j)]
+// value that its mask hides from it.  So values that no row of the unit sees are cleared, and so are non-finite ones of
+// positions that only some rows see; what the latter give the rows that see them is added here:
+//   acc[j] += exp2(score - mx) v[position][col(j)]  over the non-finite v of positions k0 .. k1
+// These positions are no more than the unit's tokens, at either end of what it sees.  (A position added twice
+// changes nothing: what it adds is not finite.)
 // ---------------------------------------------------------------------------------------
 template <typename T, int D, int N, typename Col>
-__device__ __noinline__ void exact_values(const Attn &a, int b, int h, const T *q, int k0, int k1, float mx, Col col,
-                                          float (&acc)[N])
+__device__ __noinline__ void add_non_finite(const Attn &a, int b, int h, const T *q, int k0, int k1, float mx, Col col,
+                                            float (&acc)[N])
 {
     const T *kc = static_cast<const T *>(a.kc), *vc = static_cast<const T *>(a.vc);
     const int64_t head_stride = (int64_t)D << a.p.page_shift;
-    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
     for (int k = k0; k <= k1; ++k) {
         const int64_t page = page_of(a.p, b, k >> a.p.page_shift);
         if (page < 0) continue;
         const int64_t at = page * a.p.page_stride + h * head_stride + (int64_t)(k & ((1 << a.p.page_shift) - 1)) * D;
+        bool some = false;
+        for (int j = 0; j < N; ++j) some |= !isfinite(to_f32(vc[at + col(j)]));
+        if (!some) continue;
         float s = 0.0f;
         for (int i = 0; i < D; ++i) s = fmaf(to_f32(q[i]), to_f32(kc[at + i]), s);
         const float p = attn_ex2(fmaf(s, a.scale, -mx));
-        for (int j = 0; j < N; ++j) acc[j] = fmaf(p, to_f32(vc[at + col(j)]), acc[j]);
+        for (int j = 0; j < N; ++j) {
+            const float v = to_f32(vc[at + col(j)]);
+            if (!isfinite(v)) acc[j] = fmaf(p, v, acc[j]);
+        }
     }
-}
-
-// A row's maximum and sum over the same positions.
-template <typename T, int D>
-__device__ __noinline__ float2 exact_statistics(const Attn &a, int b, int h, const T *q, int k0, int k1)
-{
-    const T *kc = static_cast<const T *>(a.kc);
-    const int64_t head_stride = (int64_t)D << a.p.page_shift;
-    float mx = -INFINITY, sum = 0.0f;
-    for (int k = k0; k <= k1; ++k) {
-        const int64_t page = page_of(a.p, b, k >> a.p.page_shift);
-        if (page < 0) continue;
-        const int64_t at = page * a.p.page_stride + h * head_stride + (int64_t)(k & ((1 << a.p.page_shift) - 1)) * D;
-        float s = 0.0f;
-        for (int i = 0; i < D; ++i) s = fmaf(to_f32(q[i]), to_f32(kc[at + i]), s);
-        const float m = fmaxf(mx, s * a.scale), base = m == -INFINITY ? 0.0f : m;
-        sum = sum * attn_ex2(mx - base) + attn_ex2(fmaf(s, a.scale, -base));
-        mx = m;
-    }
-    return make_float2(mx, sum);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -11,8 +11,8 @@
 //   warp 8          issues the MMAs, K' the next tile's keys: P0 V, Q0 K', P1 V, Q1 K', or (P apart) Q0 K', P1 V of
 //                   the tile before, Q1 K', P0 V
 //   warp 9          brings pages of keys and values to shared memory (TMA, 128-byte swizzled)
-//   warp 10         in tiles of values that some row does not see as a whole clears those that no row sees and
-//                   looks for infinities and NaN among those that only some see (attention.cuh)
+//   warp 10         in tiles of values that some row does not see as a whole clears those that no row sees, and
+//                   infinities and NaN among those that only some see (attention.cuh)
 //   warp 11         works out the CTA's next units for the others, and brings their queries
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
@@ -93,7 +93,7 @@ struct Shared {
     Record units[RECORDS];
     uint32_t pages[8];                               // tile n of the CTA in word n % 8: its 16-position blocks whose page exists
     uint32_t tmem;
-    // Unit n of the CTA, counting those with positions, has a non-finite value that not all rows see: n + 1 in word
+    // Unit n of the CTA, counting those with positions, has had a non-finite value cleared that some rows see: n + 1 in word
     // n % 16.  Warp 10 is ahead of the softmax by the stages' tiles at most, 4 and one.
     uint32_t spoilt[16];
     int abort_flag;
@@ -197,19 +197,21 @@ __device__ __forceinline__ int64_t unit_of(int round)
     return (int64_t)round * g + (round & 1 ? g - 1 - c : c);
 }
 
-// A row's maximum, sum and columns c0 .. c0 + 63 taken again (attention.cuh).
+// What cleared non-finite values give columns c0 .. c0 + 63 of a row (attention.cuh).
 template <typename T, int D>
-__device__ __noinline__ void exact_part(const Attn &a, const Record &x, int row, int c0, float2 &ml, float (&o)[64])
+__device__ __noinline__ void cleared_part(const Attn &a, const Record &x, int row, int c0, float base, float (&o)[64])
 {
     const int r = x.r0 + row, tok = a.by_group(r), pos = x.pos0 + tok;
     const int k0 = max(a.window ? pos - a.window + 1 : 0, x.t0 * TILE), k1 = min(min(pos, x.end - 1), x.t1 * TILE - 1);
     const T *q = static_cast<const T *>(a.q) + (x.row0 + tok) * a.ldq + (x.h * a.group + r - tok * a.group) * D;
-    ml = exact_statistics<T, D>(a, x.seq, x.h, q, k0, k1);
-    exact_values<T, D>(a, x.seq, x.h, q, k0, k1, ml.x == NEG ? 0.0f : ml.x, [&](int j) { return c0 + j; }, o);
+    auto col = [&](int j) { return c0 + j; };
+    for (int j = 0; j < 64; ++j) o[j] = 0.0f;
+    if (a.window) add_non_finite<T, D>(a, x.seq, x.h, q, k0, min(k1, x.last - a.window), base, col, o);
+    add_non_finite<T, D>(a, x.seq, x.h, q, max(k0, min(x.first, x.hi) + 1), k1, base, col, o);
 }
 
-// Rows r0 .. r1 - 1 of a tile of values, by a warp: cleared outside lo .. hi; whether one inside holds an infinity
-// or NaN (in this lane's part).
+// Rows r0 .. r1 - 1 of a tile of values, by a warp: cleared outside lo .. hi, inside infinities and NaN; whether
+// there were any (in this lane's part).
 template <typename T, int D>
 __device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, int hi)
 {
@@ -237,6 +239,13 @@ __device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, 
     bool found = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) found |= (top[i] & E) == E || (top[i] >> 16 & E) == E;
+    if (found) {
+        for (int r = r0 + lane / VECS; r < r1; r += AT_ONCE) {
+            if (r < lo || r > hi) continue;
+            uint32_t *w = reinterpret_cast<uint32_t *>(p + r * 128);
+            for (int i = 0; i < 4; ++i) w[i] &= ((w[i] & E) == E ? 0xffff0000u : ~0u) & ((w[i] >> 16 & E) == E ? 0x0000ffffu : ~0u);
+        }
+    }
     return found;
 }
 
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int tok = a.by_group(r);
                 dst = static_cast<uint8_t *>(a.out) + ((x.row0 + tok) * a.ldo + (x.h * a.group + r - tok * a.group) * D) * out_size(a.otype);
             }
-            float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;           // a row that sees nothing: 0
+            const float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;           // a row that sees nothing: 0
             const int type = split ? Q8ACT_F32 : a.otype;
             uint8_t *out = smem + C::OFF_OUT + warp * OUT_BYTES;
 #pragma unroll 1
@@ -430,12 +439,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (spoilt && live) {
                     float e[64];
-                    float2 ml;
-                    exact_part<T, D>(a, x, q * QROWS + row, i, ml, e);
+                    cleared_part<T, D>(a, x, q * QROWS + row, i, mx == NEG ? 0.0f : mx, e);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) o[j] = e[j];
-                    if (split) a.ml[(int64_t)x.slot * ROWS + q * QROWS + row] = ml;
-                    else inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+                    for (int j = 0; j < 64; ++j) o[j] += e[j];
                 }
 #pragma unroll
                 for (int j = 0; j < 64; ++j) o[j] *= inv;

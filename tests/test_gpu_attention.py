@@ -175,6 +175,24 @@ def test_hidden_values_in_long_sequences(d, hint):
 
 
 @HINTS
+def test_non_finite_value_in_many_long_sequences(hint):
+    """Units of whole long sequences (there are too many to cut), whose newest value is an infinity: every sequence is the
+    first one again."""
+    one = ref.Batch([(9000, 3)], 1, 128, 64, torch.bfloat16, seed=20)
+    at, slot = one.place(0, 9001)
+    one.v[at, 0, slot, 7] = math.inf
+    one.v[at, 0, slot, 70] = math.nan
+    n, q = 500, one.randn(3, 2, 128)
+    want, tol = ref.attention(one, q, 128 ** -0.5, 0, one.t)
+    kd, vd, table, _, _ = one.cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kv = q8.PagedKV(kd, vd, table.expand(n, -1).contiguous(), 3 * torch.arange(n + 1, **i32), torch.full((n,), 9003, **i32))
+    got = q8.attention(kv, q.cuda().repeat(n, 1, 1), max_new=new(hint, q, 1)).view(n, 3, 2, 128)
+    device_ok()
+    ref.close(got, want.expand(n, -1, -1, -1), tol.expand(n, -1, -1, -1))
+
+
+@HINTS
 def test_lowest_values_and_large_scores(hint):
     """Scores that overflow to -inf count nothing, large ones pick one position."""
     batch = ref.Batch([(100, 2), (0, 30)], 1, 64, 16, torch.float16, seed=11)

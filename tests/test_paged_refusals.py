@@ -77,7 +77,7 @@ def test_append(rc, args):
 @pytest.mark.parametrize("rc,args", [
     (NULL, dict(q=None)), (NULL, dict(out=None)), (TYPE, dict(ot=3)), (DIMS, dict(hq=3)), (DIMS, dict(hq=0)),
     (DIMS, dict(hq=1)), (DIMS, dict(hq=8192)), (DIMS, dict(scale=0.0)), (DIMS, dict(scale=-1.0)), (DIMS, dict(scale=float("nan"))),
-    (DIMS, dict(scale=float("inf"))), (DIMS, dict(window=-1)), (DIMS, dict(window=2 ** 31 - 1)), (DIMS, dict(max_new=-1)),
+    (DIMS, dict(scale=float("inf"))), (DIMS, dict(scale=2.0 ** 101)), (DIMS, dict(window=-1)), (DIMS, dict(window=2 ** 31 - 1)), (DIMS, dict(max_new=-1)),
     (DIMS, dict(ldq=255)), (DIMS, dict(ldo=128)), (ALIGN, dict(ldq=260)), (ALIGN, dict(ldo=257)), (ALIGN, dict(q=MIS)),
     (ALIGN, dict(out=MIS)), (WS, dict(ws=None)), (WS, dict(nb=100)), (ALIGN, dict(ws=MIS)),
 ], ids=str)
