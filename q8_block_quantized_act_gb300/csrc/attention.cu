@@ -261,6 +261,33 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w)
     return w & ((w & E) == E ? 0xffff0000u : ~0u) & ((w >> 16 & E) == E ? 0x0000ffffu : ~0u);
 }
 
+// A warp's 16 positions of a tile of values: cleared outside lo .. hi, and inside where not finite; whether something
+// was (in this lane's part).  (128-byte rows swizzle within themselves, so where a value stands does not matter.)
+template <typename T, int D>
+__device__ __forceinline__ bool clear_block(uint8_t *values, int lo, int hi)
+{
+    constexpr int VECS = D / 8;                     // 16-byte vectors of a position
+    const int lane = threadIdx.x & 31, v = lane % VECS;
+    uint8_t *p = values + (v >> 3) * (TILE * 128) + (v & 7) * 16;
+    bool found = false;
+#pragma unroll
+    for (int r = lane / VECS; r < 16; r += 32 / VECS) {
+        uint4 *w = reinterpret_cast<uint4 *>(p + r * 128), u = *w;
+        if (r < lo || r > hi) {
+            u = make_uint4(0, 0, 0, 0);
+            *w = u;
+        }
+        const uint4 f = make_uint4(finite2<T>(u.x), finite2<T>(u.y), finite2<T>(u.z), finite2<T>(u.w));
+        if (f.x != u.x || f.y != u.y || f.z != u.z || f.w != u.w) {
+            found = true;
+            *w = f;
+        }
+    }
+    fence_proxy_async_smem();                       // before the next copies to the stage
+    __syncwarp();
+    return found;
+}
+
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
@@ -463,31 +490,12 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
                     pf[mt][i + 2] = pack2<T>(e[2], e[3]);
                 }
             }
-            // Values of positions that no row sees are cleared, and in blocks that not all rows see as a whole non-finite
-            // ones.
-            uint32_t keep[2] = {~0u, ~0u};
-            if (part) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int key = key0 + 8 * i + 2 * c;
-                    keep[i] = (key >= p.span.lo && key <= p.span.hi ? 0xffffu : 0u) |
-                              (key + 1 >= p.span.lo && key + 1 <= p.span.hi ? 0xffff0000u : 0u);
-                }
-            }
+            if (part) spoilt |= clear_block<T, D>(stages + (vt - stage0) + kw * (16 * 128), p.span.lo - key0, p.span.hi - key0);
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
                 uint32_t vf[4];
                 const int chunk = 2 * n + vchunk;
                 ldmatrix_x4_trans(vf, vt + (chunk >> 3) * (TILE * 128) + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4));
-                if (part) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        vf[i] &= keep[i & 1];
-                        const uint32_t w = finite2<T>(vf[i]);
-                        spoilt |= w != vf[i];
-                        vf[i] = w;
-                    }
-                }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     mma_16816<T>(o[mt][2 * n], pf[mt], vf[0], vf[1]);

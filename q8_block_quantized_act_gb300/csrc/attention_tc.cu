@@ -210,8 +210,8 @@ __device__ __noinline__ void cleared_part(const Attn &a, const Record &x, int ro
     add_non_finite<T, D>(a, x.seq, x.h, q, max(k0, min(x.first, x.hi) + 1), k1, base, col, o);
 }
 
-// Rows r0 .. r1 - 1 of a tile of values, by a warp: cleared outside lo .. hi, inside infinities and NaN; whether
-// there were any (in this lane's part).
+// Rows r0 .. r1 - 1 of a tile of values, by a warp: cleared outside lo .. hi; whether one inside holds an infinity
+// or NaN (in this lane's part).
 template <typename T, int D>
 __device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, int hi)
 {
@@ -239,14 +239,21 @@ __device__ __forceinline__ bool fix_rows(uint8_t *tile, int r0, int r1, int lo, 
     bool found = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) found |= (top[i] & E) == E || (top[i] >> 16 & E) == E;
-    if (found) {
-        for (int r = r0 + lane / VECS; r < r1; r += AT_ONCE) {
-            if (r < lo || r > hi) continue;
-            uint32_t *w = reinterpret_cast<uint32_t *>(p + r * 128);
-            for (int i = 0; i < 4; ++i) w[i] &= ((w[i] & E) == E ? 0xffff0000u : ~0u) & ((w[i] >> 16 & E) == E ? 0x0000ffffu : ~0u);
-        }
-    }
     return found;
+}
+
+// Infinities and NaN cleared in rows lo .. hi of a tile but from .. to - 1.
+template <typename T, int D>
+__device__ __forceinline__ void clear_non_finite(uint8_t *tile, int lo, int hi, int from, int to)
+{
+    constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < TILE * D / 2; i += 32) {           // 4-byte words, a half of the columns after the other
+        const int r = i / 32 % TILE;
+        if (r < lo || r > hi || (r >= from && r < to)) continue;
+        uint32_t &w = reinterpret_cast<uint32_t *>(tile)[i];
+        w &= ((w & E) == E ? 0xffff0000u : ~0u) & ((w >> 16 & E) == E ? 0x0000ffffu : ~0u);
+    }
 }
 
 template <typename T, int D>
@@ -717,7 +724,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int from = min(max(a.window ? x.last - a.window + 1 : 0, x.lo) - k0, TILE);
                         const bool found = fix_rows<T, D>(stages + st * C::STAGE_BYTES, 0, from, x.lo - k0, x.hi - k0) |
                                            fix_rows<T, D>(stages + st * C::STAGE_BYTES, max(to, from), TILE, x.lo - k0, x.hi - k0);
-                        if (found) *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) = n + 1;
+                        if (__any_sync(0xffffffffu, found)) {
+                            clear_non_finite<T, D>(stages + st * C::STAGE_BYTES, x.lo - k0, x.hi - k0, from, to);
+                            if (lane == 0) *const_cast<volatile uint32_t *>(&sm.spoilt[n & 15]) = n + 1;
+                        }
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
