@@ -511,7 +511,7 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
  *       to the cache's type for their product with the values.
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
- *       known).  It chooses the kernel (max_new * heads_q / heads up to 32: the one for few rows) and may be wrong.
+ *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.
  *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses
  *       until the call's work is done; it needs no preparation and holds nothing between calls.
  */

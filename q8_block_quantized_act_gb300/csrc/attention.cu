@@ -8,15 +8,14 @@
 //
 // One warp brings 64 positions at a time to shared memory (TMA boxes of up to a page, 128-byte swizzled, several
 // stages ahead across row tiles).  Four warps take 16 positions each, with their own running maximum and sum, so
-// they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16 or 32
+// they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16
 // rows are too few for tcgen05's 128, and it is not what bounds.  Scores, statistics and sums are f32; the weights
 // e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type.
 //
 // One token over 131071 positions of 32 + 8 heads x 128 bf16: 87 us (6.2 TB/s, 0.91 of a copy); 64 sequences of 500 to
 // 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 46 us (0.39: 7.5 row tiles a CTA, whose ends, joins and outputs cost about
 // 1.5 us each); one over 4096: 12 us (0.21: 6 us from launch to output, of which the first keys' way 2, then the
-// joining kernel).  16 sequences x 2 to 4 tokens of 28 + 4 heads at 6000, 14 to 28 rows: 42-55 us of 29 by bytes;
-// beyond 32 rows the kernel for chunks is faster (35 rows: 57 us, with 64 rows a tile here 84).
+// joining kernel).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -29,10 +28,10 @@ constexpr int KEY_WARPS = 4;         // 16 positions each
 constexpr int COUNTERS = 128;        // threads that count the work
 constexpr float NEG = -INFINITY;
 
-// MT: 16-row tiles.
-template <int D, int MT>
+constexpr int ROWS = 16;              // of a row tile
+
+template <int D>
 struct Cfg {
-    static constexpr int ROWS = 16 * MT;
     static constexpr int CTAS = 2;                              // to an SM
     static constexpr int THREADS = 32 * (KEY_WARPS + 1);
     static constexpr int TILE_BYTES = TILE * D * 2;             // of keys, and of values
@@ -40,11 +39,10 @@ struct Cfg {
     static constexpr int STAGES = 96 * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                       // 128-byte wide columns of a tile
     static constexpr int Q_STRIDE = D * 2 + 16;                 // bytes: rows in different banks
-    static constexpr int Q_BYTES = ROWS * Q_STRIDE, Q_BUFFERS = MT == 1 ? 2 : 1;
+    static constexpr int Q_BYTES = ROWS * Q_STRIDE, Q_BUFFERS = 2;
     static constexpr int OFF_Q = STAGES * STAGE_BYTES, OFF_SHARED = OFF_Q + Q_BUFFERS * Q_BYTES;
 };
 
-template <int ROWS>
 struct Shared {
     long long before[COUNTERS + 1];       // work before thread j's sequences
     long long sums[COUNTERS / 32];
@@ -75,7 +73,6 @@ struct Line {
     Seq s;
 
     // Row tiles x heads of a sequence, and key tiles of each.
-    template <int ROWS>
     static __device__ __forceinline__ void shape(const Attn &a, const Seq &s, int &items, int &n)
     {
         const int rows = s.n * a.group, tiles = (rows + ROWS - 1) / ROWS;
@@ -92,7 +89,6 @@ struct Line {
     }
 
     // Called by all threads of the CTA.  (Few sequences: no barrier.)
-    template <int ROWS>
     __device__ __forceinline__ void make(const Attn &a, long long *starts, long long *sums)
     {
         const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -103,13 +99,13 @@ struct Line {
         if (few) {
             if (lane < a.p.seqs) {
                 s = seq_of(a.p, lane);
-                shape<ROWS>(a, s, items, n);
+                shape(a, s, items, n);
                 w = (long long)items * n;
             }
         } else if (t < COUNTERS) {
             for (int b = t * per; b < min(t * per + per, a.p.seqs); ++b) {
                 int i, k;
-                shape<ROWS>(a, seq_of(a.p, b), i, k);
+                shape(a, seq_of(a.p, b), i, k);
                 w += (long long)i * k;
             }
         }
@@ -140,7 +136,6 @@ struct Line {
 };
 
 // A place on the line.  Its calls are made by whole warps.
-template <int ROWS>
 struct Place {
     int b, item, items, n, tile;       // sequence, row tile and head of so many, key tile of so many
     Seq s;
@@ -156,7 +151,7 @@ struct Place {
             s.end = __shfl_sync(0xffffffffu, line.s.end, b);
         } else {
             s = seq_of(a.p, b);
-            Line::shape<ROWS>(a, s, items, n);
+            Line::shape(a, s, items, n);
         }
     }
     // Key tile x of the line (x < total).
@@ -195,14 +190,13 @@ struct Place {
 };
 
 // The part of a row tile that a CTA's stretch holds.
-template <int ROWS>
 struct Part {
     int h, r0, valid;                  // head of keys and values; first row and how many
     int t0, t1;                        // key tiles
     Span span;
     bool whole;
 
-    __device__ __forceinline__ Part(const Attn &a, const Place<ROWS> &p, long long left)
+    __device__ __forceinline__ Part(const Attn &a, const Place &p, long long left)
     {
         const int tile = a.by_heads(p.item), end = (int)min((long long)p.n, p.tile + left);
         h = p.item - tile * a.p.heads;
@@ -288,14 +282,13 @@ __device__ __forceinline__ bool clear_block(uint8_t *values, int lo, int hi)
     return found;
 }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
+template <typename T, int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Attn a)
 {
-    using C = Cfg<D, MT>;
-    constexpr int ROWS = C::ROWS;
+    using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t stages[];
-    Shared<ROWS> &sm = *reinterpret_cast<Shared<ROWS> *>(stages + C::OFF_SHARED);
+    Shared &sm = *reinterpret_cast<Shared *>(stages + C::OFF_SHARED);
     volatile int *abort_flag = &sm.abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -312,12 +305,12 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     griddep_wait();
     griddep_launch_dependents();
     Line line{};
-    line.make<ROWS>(a, sm.before, sm.sums);
+    line.make(a, sm.before, sm.sums);
     __syncthreads();                                             // the barriers exist for all
     long long x = blockIdx.x * line.length;
     const long long x1 = min(x + line.length, line.total);
     if (x >= x1) return;
-    Place<ROWS> place(a, line, sm.before, x);
+    Place place(a, line, sm.before, x);
 
     if (warp == KEY_WARPS) {
         // ------------------------------ producer ------------------------------
@@ -326,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
         uint32_t phase = 1;
         bool ok = true;
         for (; ok && x < x1; ++parts) {
-            const Part<ROWS> p(a, place, x1 - x);
+            const Part p(a, place, x1 - x);
             const Seq s = place.s;
             const int b = place.b;
             x += min((long long)(place.n - place.tile), x1 - x);
@@ -392,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
     int st = 0;
     uint32_t phase = 0;
     for (int parts = 0; x < x1; ++parts) {
-        const Part<ROWS> p(a, place, x1 - x);
+        const Part p(a, place, x1 - x);
         const Seq s0 = place.s;
         const int b = place.b, flip = parts & 1, qb = parts % C::Q_BUFFERS;
         const int slot = p.whole ? -1 : 2 * (int)blockIdx.x + (x != x0);
@@ -400,106 +393,90 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
         place.next(a, line);
         const int first = s0.pos0 + a.by_group(p.r0), last = s0.pos0 + a.by_group(p.r0 + p.valid - 1);    // positions of its rows
 
-        // Two rows a lane and 16-row tile: g and g + 8.
-        int lo[MT][2], hi[MT][2];
+        // Two rows a lane: g and g + 8.
+        int lo[2], hi[2];
+        float o[D / 8][4], mx[2], sum[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = mt * 16 + g + 8 * i, pos = s0.pos0 + a.by_group(p.r0 + r);
-                hi[mt][i] = r < p.valid ? min(pos, s0.end - 1) : -1;
-                lo[mt][i] = a.window ? max(pos - a.window + 1, 0) : 0;
-            }
-        float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            mx[mt][0] = mx[mt][1] = NEG;
-            sum[mt][0] = sum[mt][1] = 0.0f;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.0f;
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i, pos = s0.pos0 + a.by_group(p.r0 + r);
+            hi[i] = r < p.valid ? min(pos, s0.end - 1) : -1;
+            lo[i] = a.window ? max(pos - a.window + 1, 0) : 0;
+            mx[i] = NEG;
+            sum[i] = 0.0f;
         }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
         bool spoilt = false;
         bool aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.q_full[qb], parts / C::Q_BUFFERS & 1, a.status, abort_flag));
         const uint32_t qs = q0 + qb * C::Q_BYTES;
-        // One 16-row tile's queries stay in registers; of more, they are read from shared memory again.
-        uint32_t q[MT == 1 ? D / 16 : 1][4];
-        if constexpr (MT == 1) {
+        uint32_t q[D / 16][4];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) ldmatrix_x4(q[kk], qs + kk * 32);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
-        }
+        for (int kk = 0; kk < D / 16; ++kk) ldmatrix_x4(q[kk], qs + kk * 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
 
         for (int t = p.t0; t < p.t1; ++t) {
             if (!aborted) aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
             if (aborted) break;
             const uint32_t kt = stage0 + st * C::STAGE_BYTES, vt = kt + C::TILE_BYTES;
-            const bool page_ok = sm.ok[st] >> kw & 1;
-            // A 16-row tile's scores at a time; its keys come from shared memory again for the next one.
-            uint32_t pf[MT][4];
-            // Columns of s[n]: positions key0 + 8 n + 2 c and the next; rows g (0, 1) and g + 8 (2, 3).
             const int key0 = t * TILE + kw * 16;
-            // Whether some row does not see some of the 16.
-            const bool part = key0 < p.span.lo || key0 + 15 > min(first, p.span.hi) || (a.window && key0 <= last - a.window) || !page_ok;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            // The warp's 16 positions, unless no row sees one.
+            if ((sm.ok[st] >> kw & 1) && key0 <= p.span.hi && key0 + 15 >= p.span.lo) {
+                // Columns of s[n]: positions key0 + 8 n + 2 c and the next; rows g (0, 1) and g + 8 (2, 3).
                 float s[2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     uint32_t kf[4];
                     const int chunk = kk * 2 + kchunk;
                     ldmatrix_x4(kf, kt + (chunk >> 3) * (TILE * 128) + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4));
-                    if constexpr (MT > 1) ldmatrix_x4(q[0], qs + mt * (16 * C::Q_STRIDE) + kk * 32);
-                    const uint32_t(&qf)[4] = q[MT == 1 ? kk : 0];
-                    mma_16816<T>(s[0], qf, kf[0], kf[1]);
-                    mma_16816<T>(s[1], qf, kf[2], kf[3]);
+                    mma_16816<T>(s[0], q[kk], kf[0], kf[1]);
+                    mma_16816<T>(s[1], q[kk], kf[2], kf[3]);
                 }
-                if (part) {
+                // Some row does not see some of them.
+                if (key0 < p.span.lo || key0 + 15 > min(first, p.span.hi) || (a.window && key0 <= last - a.window)) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = key0 + 8 * n + 2 * c + (i & 1);
-                            if (key < lo[mt][i >> 1] || key > hi[mt][i >> 1] || !page_ok) s[n][i] = NEG;
+                            if (key < lo[i >> 1] || key > hi[i >> 1]) s[n][i] = NEG;
                         }
+                    spoilt |= clear_block<T, D>(stages + (vt - stage0) + kw * (16 * 128), p.span.lo - key0, p.span.hi - key0);
                 }
+                uint32_t pf[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    m = fmaxf(mx[mt][i], m * a.scale);
-                    if (__any_sync(0xffffffffu, m > mx[mt][i])) {
-                        const float f = attn_ex2(mx[mt][i] - (m == NEG ? 0.0f : m));
-                        sum[mt][i] *= f;
+                    m = fmaxf(mx[i], m * a.scale);
+                    if (__any_sync(0xffffffffu, m > mx[i])) {
+                        const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
+                        sum[i] *= f;
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n) {
-                            o[mt][n][2 * i] *= f;
-                            o[mt][n][2 * i + 1] *= f;
+                            o[n][2 * i] *= f;
+                            o[n][2 * i + 1] *= f;
                         }
-                        mx[mt][i] = m;
+                        mx[i] = m;
                     }
                     const float base = m == NEG ? 0.0f : m;
                     float e[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[j >> 1][2 * i + (j & 1)], a.scale, -base));
-                    sum[mt][i] += (e[0] + e[1]) + (e[2] + e[3]);
-                    pf[mt][i] = pack2<T>(e[0], e[1]);
-                    pf[mt][i + 2] = pack2<T>(e[2], e[3]);
+                    sum[i] += (e[0] + e[1]) + (e[2] + e[3]);
+                    pf[i] = pack2<T>(e[0], e[1]);
+                    pf[i + 2] = pack2<T>(e[2], e[3]);
                 }
-            }
-            if (part) spoilt |= clear_block<T, D>(stages + (vt - stage0) + kw * (16 * 128), p.span.lo - key0, p.span.hi - key0);
 #pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                uint32_t vf[4];
-                const int chunk = 2 * n + vchunk;
-                ldmatrix_x4_trans(vf, vt + (chunk >> 3) * (TILE * 128) + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma_16816<T>(o[mt][2 * n], pf[mt], vf[0], vf[1]);
-                    mma_16816<T>(o[mt][2 * n + 1], pf[mt], vf[2], vf[3]);
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t vf[4];
+                    const int chunk = 2 * n + vchunk;
+                    ldmatrix_x4_trans(vf, vt + (chunk >> 3) * (TILE * 128) + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4));
+                    mma_16816<T>(o[2 * n], pf, vf[0], vf[1]);
+                    mma_16816<T>(o[2 * n + 1], pf, vf[2], vf[3]);
                 }
             }
             // The last stage is handed back after the join, which uses its memory.
@@ -515,105 +492,93 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, Cfg<D, MT>::CTAS)
 
         // ---- join of the four warps with the same rows ----
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 1);
-                sum[mt][i] += __shfl_xor_sync(0xffffffffu, sum[mt][i], 2);
-                if (c == 0) {
-                    sm.mx[flip][kw][mt * 16 + g + 8 * i] = mx[mt][i];
-                    sm.sum[flip][kw][mt * 16 + g + 8 * i] = sum[mt][i];
-                }
+        for (int i = 0; i < 2; ++i) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+            if (c == 0) {
+                sm.mx[flip][kw][g + 8 * i] = mx[i];
+                sm.sum[flip][kw][g + 8 * i] = sum[i];
             }
+        }
         spoilt = __any_sync(0xffffffffu, spoilt);
         if (lane == 0) sm.spoilt[flip][warp] = spoilt;
         // (the next part's words go to the other flip: some warps may still read these.  They are written again only
         // behind the next part's barrier)
         if (bar_red_or(1, 32 * KEY_WARPS, aborted)) return;
-        if (MT > 1 && lane == 0) mbar_arrive(&sm.q_empty[qb]);
         const bool some = p.t1 > p.t0;
         float *join = reinterpret_cast<float *>(stages + st * C::STAGE_BYTES);      // [warp][row][D], 16-byte words swizzled by row
+        if (some) {
 #pragma unroll
-        for (int m16 = 0; m16 < MT; ++m16) {
-            if (m16 * 16 >= p.valid) break;
-            if (some) {
-                if (m16 > 0) named_bar_sync(2, 32 * KEY_WARPS);
-                {
+            for (int i = 0; i < 2; ++i) {
+                const int r = g + 8 * i;
+                float m = NEG;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = g + 8 * i;
-                        float m = NEG;
+                for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][r]);
+                const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
 #pragma unroll
-                        for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][m16 * 16 + r]);
-                        const float f = attn_ex2(mx[m16][i] - (m == NEG ? 0.0f : m));
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            const int col = (8 * n + 2 * c) ^ ((r & 7) << 2);
-                            *reinterpret_cast<float2 *>(join + (kw * 16 + r) * D + col) =
-                                make_float2(o[m16][n][2 * i] * f, o[m16][n][2 * i + 1] * f);
-                        }
-                    }
+                for (int n = 0; n < D / 8; ++n) {
+                    const int col = (8 * n + 2 * c) ^ ((r & 7) << 2);
+                    *reinterpret_cast<float2 *>(join + (kw * 16 + r) * D + col) = make_float2(o[n][2 * i] * f, o[n][2 * i + 1] * f);
                 }
-                named_bar_sync(2, 32 * KEY_WARPS);
             }
-            const int r = (threadIdx.x >> 3) & 15, c8 = threadIdx.x & 7;        // a row, and every eighth vector of it
-            const int rr = m16 * 16 + r;
-            if (rr < p.valid) {
-                float m = NEG, l = 0.0f;
+            named_bar_sync(2, 32 * KEY_WARPS);
+        }
+        const int r = (threadIdx.x >> 3) & 15, c8 = threadIdx.x & 7;        // a row, and every eighth vector of it
+        if (r < p.valid) {
+            float m = NEG, l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][rr]);
-                const float base = m == NEG ? 0.0f : m;
+            for (int w = 0; w < KEY_WARPS; ++w) m = fmaxf(m, sm.mx[flip][w][r]);
+            const float base = m == NEG ? 0.0f : m;
 #pragma unroll
-                for (int w = 0; w < KEY_WARPS; ++w) l += sm.sum[flip][w][rr] * attn_ex2(sm.mx[flip][w][rr] - base);
-                float acc[D / 8];
+            for (int w = 0; w < KEY_WARPS; ++w) l += sm.sum[flip][w][r] * attn_ex2(sm.mx[flip][w][r] - base);
+            float acc[D / 8];
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) acc[j] = 0.0f;
-                if (some) {
+            for (int j = 0; j < D / 8; ++j) acc[j] = 0.0f;
+            if (some) {
 #pragma unroll
-                    for (int w = 0; w < KEY_WARPS; ++w)
+                for (int w = 0; w < KEY_WARPS; ++w)
 #pragma unroll
-                        for (int j = 0; j < D / 32; ++j) {
-                            const float4 v = *reinterpret_cast<const float4 *>(
-                                join + (w * 16 + r) * D + (((j * 8 + c8) ^ (r & 7)) << 2));
-                            acc[4 * j] += v.x;
-                            acc[4 * j + 1] += v.y;
-                            acc[4 * j + 2] += v.z;
-                            acc[4 * j + 3] += v.w;
-                        }
-                }
-                const int row = p.r0 + rr, tok = a.by_group(row), head = p.h * a.group + row - tok * a.group;
-                int sp = 0;
+                    for (int j = 0; j < D / 32; ++j) {
+                        const float4 v = *reinterpret_cast<const float4 *>(
+                            join + (w * 16 + r) * D + (((j * 8 + c8) ^ (r & 7)) << 2));
+                        acc[4 * j] += v.x;
+                        acc[4 * j + 1] += v.y;
+                        acc[4 * j + 2] += v.z;
+                        acc[4 * j + 3] += v.w;
+                    }
+            }
+            const int row = p.r0 + r, tok = a.by_group(row), head = p.h * a.group + row - tok * a.group;
+            int sp = 0;
 #pragma unroll
-                for (int w = 0; w < KEY_WARPS; ++w) sp |= sm.spoilt[flip][w];
-                if (sp) {
-                    const int pos = s0.pos0 + tok;
-                    const int k0 = max(a.window ? pos - a.window + 1 : 0, p.t0 * TILE), k1 = min(min(pos, s0.end - 1), p.t1 * TILE - 1);
-                    float e[D / 8];
-                    for (int j = 0; j < D / 8; ++j) e[j] = 0.0f;
-                    const T *qr = static_cast<const T *>(a.q) + (s0.row0 + tok) * a.ldq + head * D;
-                    auto col = [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); };
-                    // The blocks of 16 that were taken as not seen by all rows.
-                    if (a.window) add_non_finite<T, D>(a, b, p.h, qr, k0, min(k1, (last - a.window) | 15), base, col, e);
-                    add_non_finite<T, D>(a, b, p.h, qr, max(k0, (min(first, p.span.hi) + 1) & ~15), k1, base, col, e);
+            for (int w = 0; w < KEY_WARPS; ++w) sp |= sm.spoilt[flip][w];
+            if (sp) {
+                const int pos = s0.pos0 + tok;
+                const int k0 = max(a.window ? pos - a.window + 1 : 0, p.t0 * TILE), k1 = min(min(pos, s0.end - 1), p.t1 * TILE - 1);
+                float e[D / 8];
+                for (int j = 0; j < D / 8; ++j) e[j] = 0.0f;
+                const T *qr = static_cast<const T *>(a.q) + (s0.row0 + tok) * a.ldq + head * D;
+                auto col = [&](int j) { return ((j >> 2) * 8 + c8) * 4 + (j & 3); };
+                // The blocks of 16 that were taken as not seen by all rows.
+                if (a.window) add_non_finite<T, D>(a, b, p.h, qr, k0, min(k1, (last - a.window) | 15), base, col, e);
+                add_non_finite<T, D>(a, b, p.h, qr, max(k0, (min(first, p.span.hi) + 1) & ~15), k1, base, col, e);
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j) acc[j] += e[j];
-                }
-                if (slot >= 0) {
-                    const int64_t at = (int64_t)slot * ROWS + rr;
-                    if (c8 == 0) a.ml[at] = make_float2(m, l);
+                for (int j = 0; j < D / 8; ++j) acc[j] += e[j];
+            }
+            if (slot >= 0) {
+                const int64_t at = (int64_t)slot * ROWS + r;
+                if (c8 == 0) a.ml[at] = make_float2(m, l);
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-                        *reinterpret_cast<float4 *>(a.part + at * D + (j * 8 + c8) * 4) =
-                            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-                } else {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // a row that sees nothing: 0
-                    uint8_t *dst = static_cast<uint8_t *>(a.out) +
-                                   ((s0.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
+                for (int j = 0; j < D / 32; ++j)
+                    *reinterpret_cast<float4 *>(a.part + at * D + (j * 8 + c8) * 4) =
+                        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            } else {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // a row that sees nothing: 0
+                uint8_t *dst = static_cast<uint8_t *>(a.out) +
+                               ((s0.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-                        store4(dst + (j * 8 + c8) * 4 * out_size(a.otype), a.otype,
-                               make_float4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv, acc[4 * j + 3] * inv));
-                }
+                for (int j = 0; j < D / 32; ++j)
+                    store4(dst + (j * 8 + c8) * 4 * out_size(a.otype), a.otype,
+                           make_float4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv, acc[4 * j + 3] * inv));
             }
         }
         if (some) {
@@ -632,7 +597,7 @@ constexpr int JOIN_WARPS = 4, JOIN_Y = 4;
 
 // A row's parts, added in their order by four warps: o = sum_i e^(mx_i - mx) o_i / sum_i e^(mx_i - mx) sum_i.  A
 // warp takes its parts relative to its own maximum, eight loads at a time.  slot(i): where part i is.
-template <int D, int ROWS, typename Slot>
+template <int D, typename Slot>
 __device__ __forceinline__ void join_row(const Attn &a, int parts, Slot slot, int r, uint8_t *dst, float (&acc)[JOIN_WARPS][D],
                                          float (&mw)[JOIN_WARPS], float (&lw)[JOIN_WARPS])
 {
@@ -700,17 +665,17 @@ __device__ __forceinline__ void join_row(const Attn &a, int parts, Slot slot, in
 // CTA (c, y) joins the row tile that the end of stretch c cuts first, rows y, y + 4, ...  It works out which one while
 // the parts are still being computed (what starts and lens hold was there before the kernel in front, which
 // has waited for it).
-template <int D, int ROWS>
+template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(Attn a)
 {
     __shared__ long long before[COUNTERS + 1], sums[COUNTERS / 32];
     __shared__ alignas(16) float acc[JOIN_WARPS][D];
     __shared__ float mw[JOIN_WARPS], lw[JOIN_WARPS];
     Line line{};
-    line.make<ROWS>(a, before, sums);
+    line.make(a, before, sums);
     const long long len = line.length, x = (blockIdx.x + 1) * len;
     if (x < line.total) {
-        const Place<ROWS> p(a, line, before, x);
+        const Place p(a, line, before, x);
         const long long start = x - p.tile;                  // of the row tile
         if (p.tile > 0 && x - len <= start) {
             const int k0 = blockIdx.x, parts = (int)divide(start + p.n - 1, len) - k0 + 1;
@@ -719,7 +684,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(At
             for (int r = blockIdx.y; r < valid; r += JOIN_Y) {
                 const int row = tile * ROWS + r, tok = a.by_group(row), head = h * a.group + row - tok * a.group;
                 // Its first part is its stretch's last one, unless the stretch begins with it; the others are first.
-                join_row<D, ROWS>(a, parts, [&](int i) { return 2 * (k0 + i) + (i == 0 && x - len < start); }, r,
+                join_row<D>(a, parts, [&](int i) { return 2 * (k0 + i) + (i == 0 && x - len < start); }, r,
                                   static_cast<uint8_t *>(a.out) + ((p.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype), acc, mw, lw);
             }
         }
@@ -788,8 +753,8 @@ cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, in
     return dim == 64 ? go(attention_chunk_join_kernel<64>) : go(attention_chunk_join_kernel<128>);
 }
 
-// Two partial results at most of each of the CTAs that a GB300's 152 SMs hold.
-size_t attention_workspace_bytes(int dim) { return std::max(attention_space(2 * 2 * 152, 32, dim), attention_chunk_space(dim)); }
+// Enough for either kernel: of few rows, two partial results at most of each of the two CTAs on each of 152 SMs.
+size_t attention_workspace_bytes(int dim) { return std::max(attention_space(2 * 2 * 152, ROWS, dim), attention_chunk_space(dim)); }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, const AttentionArgs &s, int64_t m,
                              cudaStream_t stream)
@@ -810,8 +775,12 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.scale = s.scale * 1.4426950408889634f;
     a.status = dev.status;
     const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
-    const int64_t rows = most * a.group;
-    if (rows > 32) return launch_attention_chunk(dev, kv, a, s.ws, stream);
+    // One row tile of 16 a head here, or half full ones of 256 there: 16 sequences at 6000 of 28 + 4 heads x 128, 14
+    // rows 43 us here and 56 there; 100 at 1000 of 64 + 8 heads x 64, 16 rows 47 and 67; one at 6000, 14 rows 22 and
+    // 29.  From 17 rows on a sequence's keys would be read and multiplied for two row tiles here: two row tiles side
+    // by side in registers took 54 us for 57 there at 21 rows of the first, but 33 for 29 of the last, and at 28 to 32
+    // rows up to a third more (16 at 600 24 us, there 17).
+    if (most * a.group > ROWS) return launch_attention_chunk(dev, kv, a, s.ws, stream);
     CUtensorMap tk, tv;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     return with_type(kv.type, [&](auto x) -> cudaError_t {
@@ -819,26 +788,21 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
         if constexpr (sizeof(T) == 4) {
             return cudaErrorInvalidValue;
         } else {
-            auto go = [&](auto d, auto mt) -> cudaError_t {
-                constexpr int D = decltype(d)::value, MT = decltype(mt)::value;
-                using C = Cfg<D, MT>;
-                constexpr size_t smem = C::OFF_SHARED + sizeof(Shared<C::ROWS>);
+            auto go = [&](auto d) -> cudaError_t {
+                constexpr int D = decltype(d)::value;
+                using C = Cfg<D>;
+                constexpr size_t smem = C::OFF_SHARED + sizeof(Shared);
                 static_assert(smem <= 113 * 1024, "two CTAs to an SM");
                 a.ctas = C::CTAS * std::min(dev.num_sms, 152);
                 a.least = 2;
-                attention_place(a, s.ws, 2 * a.ctas, C::ROWS);
-                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D, MT>>(dev.device, smem);
+                attention_place(a, s.ws, 2 * a.ctas, ROWS);
+                cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_rows_kernel<T, D, MT>, dim3(a.ctas), C::THREADS, smem, stream, tk, tv, a);
+                e = launch_dependent(attention_rows_kernel<T, D>, dim3(a.ctas), C::THREADS, smem, stream, tk, tv, a);
                 if (e != cudaSuccess) return e;
-                return launch_dependent(attention_rows_join_kernel<D, C::ROWS>, dim3(a.ctas - 1, JOIN_Y), 32 * JOIN_WARPS, 0, stream, a);
+                return launch_dependent(attention_rows_join_kernel<D>, dim3(a.ctas - 1, JOIN_Y), 32 * JOIN_WARPS, 0, stream, a);
             };
-            using I1 = std::integral_constant<int, 1>;
-            using I2 = std::integral_constant<int, 2>;
-            auto pick = [&](auto d) {
-                return rows <= 16 ? go(d, I1{}) : go(d, I2{});
-            };
-            return kv.dim == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
+            return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
         }
     });
 }
