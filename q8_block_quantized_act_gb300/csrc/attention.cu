@@ -13,8 +13,8 @@
 // e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type.
 //
 // One token over 131071 positions of 32 + 8 heads x 128 bf16: 87 us (6.2 TB/s, 0.91 of a copy); 64 sequences of 500 to
-// 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 46 us (0.39: 7.5 row tiles a CTA, whose ends, joins and outputs cost about
-// 1.5 us each); one over 4096: 12 us (0.21: 6 us from launch to output, of which the first keys' way 2, then the
+// 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 33 us (0.55: 7 us of launches, planning and joining kernel, the rest
+// row tiles' ends: 7.5 a CTA, about 1.2 us each); one over 4096: 11 us (0.22: 6 us from launch to output, of which the first keys' way 2, then the
 // joining kernel).
 #include <algorithm>
 
@@ -55,7 +55,9 @@ struct Shared {
 
 // ---------------------------------------------------------------------------------------
 // The line of work: the sequences one after another, in each the row tiles and in these the heads, each with
-// the key tiles that its longest row tile sees (one at least, so that rows that see nothing are written too).
+// the key tiles that its longest row tile sees (one at least, so that rows that see nothing are written too) behind
+// `extra` that stand for what a row tile costs beside them.  A stretch that ends among the latter has nothing of
+// the row tile, and one that begins there has all of its beginning.
 // ---------------------------------------------------------------------------------------
 // 64-bit division, mostly of numbers that fit 32 bits.
 __device__ __forceinline__ long long divide(long long x, long long by)
@@ -85,7 +87,7 @@ struct Line {
             n = min(min(s.pos0 + s.n, s.end), 0x3fffffff) / TILE + 1;
             n = min(n, (int)((a.window + (long long)tokens + TILE - 3) / TILE) + 1);
         }
-        n = max(n, 1);
+        n = max(n, 1) + a.extra;
     }
 
     // Called by all threads of the CTA.  (Few sequences: no barrier.)
@@ -137,7 +139,7 @@ struct Line {
 
 // A place on the line.  Its calls are made by whole warps.
 struct Place {
-    int b, item, items, n, tile;       // sequence, row tile and head of so many, key tile of so many
+    int b, item, items, n, tile;       // sequence, row tile and head of so many, key tile of so many (extra ones included)
     Seq s;
 
     __device__ __forceinline__ void enter(const Attn &a, const Line &line)
@@ -198,13 +200,13 @@ struct Part {
 
     __device__ __forceinline__ Part(const Attn &a, const Place &p, long long left)
     {
-        const int tile = a.by_heads(p.item), end = (int)min((long long)p.n, p.tile + left);
+        const int tile = a.by_heads(p.item), end = (int)min((long long)p.n, p.tile + left);      // end > extra
         h = p.item - tile * a.p.heads;
         r0 = tile * ROWS;
         valid = min(ROWS, p.s.n * a.group - r0);
         span = span_of<TILE>(a, p.s, r0, r0 + valid - 1);
-        t0 = span.first + min(p.tile, span.n);
-        t1 = span.first + min(end, span.n);
+        t0 = span.first + min(max(p.tile - a.extra, 0), span.n);
+        t1 = span.first + min(end - a.extra, span.n);
         whole = p.tile == 0 && end == p.n;
     }
 };
@@ -311,6 +313,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     const long long x1 = min(x + line.length, line.total);
     if (x >= x1) return;
     Place place(a, line, sm.before, x);
+    if (place.tile <= a.extra) {
+        x -= place.tile;
+        place.tile = 0;
+    }
+    auto more = [&] { return x < x1 && place.tile + (x1 - x) > a.extra; };
 
     if (warp == KEY_WARPS) {
         // ------------------------------ producer ------------------------------
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         int it = 0, st = 0, parts = 0;
         uint32_t phase = 1;
         bool ok = true;
-        for (; ok && x < x1; ++parts) {
+        for (; ok && more(); ++parts) {
             const Part p(a, place, x1 - x);
             const Seq s = place.s;
             const int b = place.b;
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     const long long x0 = x;
     int st = 0;
     uint32_t phase = 0;
-    for (int parts = 0; x < x1; ++parts) {
+    for (int parts = 0; more(); ++parts) {
         const Part p(a, place, x1 - x);
         const Seq s0 = place.s;
         const int b = place.b, flip = parts & 1, qb = parts % C::Q_BUFFERS;
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(At
     if (x < line.total) {
         const Place p(a, line, before, x);
         const long long start = x - p.tile;                  // of the row tile
-        if (p.tile > 0 && x - len <= start) {
+        if (p.tile > a.extra && x - len - start <= a.extra) {
             const int k0 = blockIdx.x, parts = (int)divide(start + p.n - 1, len) - k0 + 1;
             const int tile = a.by_heads(p.item), h = p.item - tile * a.p.heads, valid = min(ROWS, p.s.n * a.group - tile * ROWS);
             griddep_wait();
@@ -795,6 +802,7 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
                 static_assert(smem <= 113 * 1024, "two CTAs to an SM");
                 a.ctas = C::CTAS * std::min(dev.num_sms, 152);
                 a.least = 2;
+                a.extra = 2;             // (190 of 37 to 600, 12 heads x 64: none 46 us, 1 36, 2 33, 3 34; longer ones the same)
                 attention_place(a, s.ws, 2 * a.ctas, ROWS);
                 cudaError_t e = set_kernel_smem<attention_rows_kernel<T, D>>(dev.device, smem);
                 if (e != cudaSuccess) return e;

@@ -42,6 +42,7 @@ struct Attn {
     // its tiles (in tiles), partial results that the workspace has room for.
     int ctas, least, slots;
     float unit_cost;
+    int extra;                   // (few rows) what a row tile costs beside its key tiles, in these
     // partial results of row tiles in several parts (attention_workspace)
     float2 *ml;                  // [slot][ROWS]: running maximum and sum
     float *part;                 // [slot][ROWS][D]
