@@ -700,63 +700,88 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(At
 }
 
 // ---------------------------------------------------------------------------------------
-// The same for row tiles of chunks, which have many rows in few parts: four rows at a time a warp.
+// The same for row tiles of chunks, which have many rows in few parts: a row a warp, as many consecutive ones as there
+// are more rows than warps.  Latency: what finds the rows ran ahead, then one load's time a row (2240 rows of seven parts at
+// most 10 us -> 4 by spreading the rows that exist; 16384 rows of two parts 5 us, two rows at a time the same).
 // ---------------------------------------------------------------------------------------
+constexpr int CHUNK_JOIN_THREADS = 256;
+
 template <int D>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) attention_chunk_join_kernel(Attn a)
+__global__ void __launch_bounds__(CHUNK_JOIN_THREADS) attention_chunk_join_kernel(Attn a)
 {
-    constexpr int V = D / 32, ROWS = CHUNK_ROWS, R = 4;
-    const int lane = threadIdx.x & 31;
-    Plan<ROWS, CHUNK_TILE> plan;
-    plan.make(a);
-    const int work = plan.split * (ROWS / R);
-    bool waited = false;
-    for (int i = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5); i < work; i += gridDim.x * JOIN_WARPS) {
-        const Unit it = plan.find_item(a, i / (ROWS / R));
-        if (!waited) griddep_enter();
-        waited = true;
-        const int i0 = i % (ROWS / R) * R, rows = it.s.n * a.group - it.tile * ROWS;
-#pragma unroll 1
-        for (int r = i0; r < min(i0 + R, rows); ++r) {
-            const float2 *ml = a.ml + (int64_t)it.slot * ROWS + r;
-            const float *part = a.part + ((int64_t)it.slot * ROWS + r) * D + V * lane;
-            float m = NEG;
-            for (int s = lane; s < it.parts; s += 32) m = fmaxf(m, ml[(int64_t)s * ROWS].x);
+    constexpr int V = D / 32, U = 4;             // values a lane, parts at a time
+    using Vec = std::conditional_t<V == 4, float4, float2>;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (CHUNK_JOIN_THREADS / 32);
+    using P = Plan<CHUNK_ROWS, CHUNK_TILE>;
+    __shared__ P plans[32];                      // one warp's, for all
+    if (threadIdx.x < 32) {
+        P p;
+        p.make(a);
+        plans[lane] = p;
+    }
+    __syncthreads();
+    const P plan = plans[lane];
+    const int each = (plan.split + warps - 1) / warps;
+    int i = (blockIdx.x * (CHUNK_JOIN_THREADS / 32) + (threadIdx.x >> 5)) * each;
+    const int end = min(i + each, plan.split);
+    Unit x;
+    int row = 0, left = 0;                       // of the sequence and head; how many more
+    if (i < end) {
+        x = plan.find_row(a, i, row);
+        left = x.s.n * a.group - row;
+    }
+    griddep_enter();
+    for (; i < end; ++i, ++row, --left) {
+        if (!left) {
+            x = plan.find_row(a, i, row);
+            left = x.s.n * a.group - row;
+        }
+        const int tile = row / CHUNK_ROWS;
+        const int64_t at = (int64_t)(x.slot + ((x.tile - 1 - tile) * a.p.heads + x.h) * x.parts) * CHUNK_ROWS + (row - tile * CHUNK_ROWS);
+        float m = NEG, l = 0.0f, v[V] = {};
+        for (int s = 0; s < x.parts; s += U) {
+            float2 ml[U];
+            Vec w[U];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == NEG ? 0.0f : m;
-            float l = 0.0f, v[V] = {};
-#pragma unroll 4
-            for (int s = 0; s < it.parts; ++s) {
-                const float2 ms = ml[(int64_t)s * ROWS];
-                const float f = attn_ex2(ms.x - base);
-                l = fmaf(ms.y, f, l);
-#pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float2 u = *reinterpret_cast<const float2 *>(part + (int64_t)s * ROWS * D + j);
-                    v[j] = fmaf(u.x, f, v[j]);
-                    v[j + 1] = fmaf(u.y, f, v[j + 1]);
-                }
+            for (int k = 0; k < U; ++k) {
+                const int64_t p = at + (int64_t)min(s + k, x.parts - 1) * CHUNK_ROWS;
+                ml[k] = a.ml[p];
+                w[k] = *reinterpret_cast<const Vec *>(a.part + p * D + V * lane);
             }
-            const int row = it.tile * ROWS + r, tok = a.by_group(row), head = it.h * a.group + row - tok * a.group;
-            uint8_t *dst = static_cast<uint8_t *>(a.out) + ((it.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if constexpr (V == 4) {
-                store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
-            } else {
-                const float x = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), y = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
-                if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, x, y));
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < U; ++k) top = fmaxf(top, ml[k].x);
+            const float base = top == NEG ? 0.0f : top, f0 = attn_ex2(m - base);
+            m = top;
+            l *= f0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] *= f0;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (s + k >= x.parts) break;
+                const float f = attn_ex2(ml[k].x - base);
+                l = fmaf(ml[k].y, f, l);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = fmaf(reinterpret_cast<const float *>(&w[k])[j], f, v[j]);
             }
         }
+        const int tok = a.by_group(row), head = x.h * a.group + row - tok * a.group;
+        uint8_t *dst = static_cast<uint8_t *>(a.out) + ((x.s.row0 + tok) * a.ldo + head * D) * out_size(a.otype);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if constexpr (V == 4) {
+            store4(dst + 4 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+        } else {
+            const float y = __shfl_down_sync(0xffffffffu, v[0] * inv, 1), z = __shfl_down_sync(0xffffffffu, v[1] * inv, 1);
+            if (!(lane & 1)) store4(dst + 2 * lane * out_size(a.otype), a.otype, make_float4(v[0] * inv, v[1] * inv, y, z));
+        }
     }
-    if (!waited) griddep_enter();
 }
 
 }  // namespace
 
 cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream)
 {
-    auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), 32 * JOIN_WARPS, 0, stream, a); };
+    auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), CHUNK_JOIN_THREADS, 0, stream, a); };
     return dim == 64 ? go(attention_chunk_join_kernel<64>) : go(attention_chunk_join_kernel<128>);
 }
 

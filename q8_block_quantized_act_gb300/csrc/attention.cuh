@@ -96,9 +96,9 @@ template <int ROWS, int TILE>
 struct Plan {
     int per;                        // sequences a lane
     int length;                     // key tiles a part
-    int total, split;               // units; row tiles in several parts
-    // Before the lane's first sequence: units, slots, row tiles in several parts.  And, of one sequence a lane, what it is.
-    int units, slots, items;
+    int total, split;               // units; rows of row tiles in several parts
+    // Before the lane's first sequence: units, slots, rows in several parts.  And, of one sequence a lane, what it is.
+    int units, slots, rows;
     Seq s;
     int tiles, parts;
 
@@ -162,29 +162,29 @@ struct Plan {
         int v[3] = {0, 0, 0};
         if (per == 1) {
             s = Seq{0, 0, 0, 0};
-            int rows = 0, first = 0, last = 0;
+            int n = 0, first = 0, last = 0;
             if (lane < a.p.seqs) {
                 s = seq_of(a.p, lane);
-                rows = s.n * a.group;
-                if (rows) {
-                    first = span_of<TILE>(a, s, 0, min(rows, ROWS) - 1).n;
-                    last = span_of<TILE>(a, s, (rows - 1) / ROWS * ROWS, rows - 1).n;
+                n = s.n * a.group;
+                if (n) {
+                    first = span_of<TILE>(a, s, 0, min(n, ROWS) - 1).n;
+                    last = span_of<TILE>(a, s, (n - 1) / ROWS * ROWS, n - 1).n;
                 }
             }
-            length = best_length(a, rows, first, last);
-            tiles = (rows + ROWS - 1) / ROWS;
+            length = best_length(a, n, first, last);
+            tiles = (n + ROWS - 1) / ROWS;
             parts = tiles ? max(1, (last + length - 1) / length) : 0;
             v[0] = tiles * parts * a.p.heads;
             v[1] = parts > 1 ? v[0] : 0;
-            v[2] = parts > 1 ? tiles * a.p.heads : 0;
+            v[2] = parts > 1 ? n * a.p.heads : 0;           // (few: the workspace has room for their row tiles)
         } else {
             // Parts of equal length, as many as the workspace has room for: a row tile of p > 1 parts has more than
             // (p - 1) * length >= p * length / 2 key tiles, so there are fewer than twice work / length of them.
             long long w = 0;
             for (int b = b0; b < b1; ++b) {
                 const Seq q = seq_of(a.p, b);
-                const int rows = q.n * a.group;
-                if (rows) w += (long long)((rows + ROWS - 1) / ROWS) * span_of<TILE>(a, q, (rows - 1) / ROWS * ROWS, rows - 1).n;
+                const int n = q.n * a.group;
+                if (n) w += (long long)((n + ROWS - 1) / ROWS) * span_of<TILE>(a, q, (n - 1) / ROWS * ROWS, n - 1).n;
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -192,11 +192,12 @@ struct Plan {
             length = (int)min(max(w, (long long)a.least), (long long)INT_MAX / 2);
             for (int b = b0; b < b1; ++b) {
                 int t, p;
-                shape(a, seq_of(a.p, b), t, p);
+                const Seq q = seq_of(a.p, b);
+                shape(a, q, t, p);
                 v[0] = min(v[0] + t * a.p.heads * p, (1 << 26) - 1);     // (more only where starts do not ascend)
                 if (p > 1) {
                     v[1] += t * a.p.heads * p;
-                    v[2] += t * a.p.heads;
+                    v[2] += q.n * a.group * a.p.heads;
                 }
             }
         }
@@ -212,16 +213,16 @@ struct Plan {
         }
         units = sum[0] - v[0];
         slots = sum[1] - v[1];
-        items = sum[2] - v[2];
+        rows = sum[2] - v[2];
         total = __shfl_sync(0xffffffffu, sum[0], 31);
         split = __shfl_sync(0xffffffffu, sum[2], 31);
     }
 
-    // The sequence of unit (or, of those in several parts, row tile) u, and what is left of u in it.
-    template <bool ITEMS>
+    // The sequence of unit (or, of row tiles in several parts, row) u, and what is left of u in it.
+    template <bool JOIN>
     __device__ __forceinline__ Unit sequence(const Attn &a, int u, int &left, int &t) const
     {
-        const int before = ITEMS ? items : units;
+        const int before = JOIN ? rows : units;
         const int lo = __popc(__ballot_sync(0xffffffffu, before <= u)) - 1;       // the last lane that starts at or before u
         Unit x;
         left = u - __shfl_sync(0xffffffffu, before, lo);
@@ -239,36 +240,34 @@ struct Plan {
         for (x.b = lo * per;; ++x.b) {              // ends: u < total
             x.s = seq_of(a.p, x.b);
             shape(a, x.s, t, x.parts);
-            const int n = t * a.p.heads, k = n * x.parts, mine = !ITEMS ? k : x.parts > 1 ? n : 0;
+            const int k = t * a.p.heads * x.parts, mine = !JOIN ? k : x.parts > 1 ? x.s.n * a.group * a.p.heads : 0;
             if (left < mine || x.b + 1 >= a.p.seqs) break;
             left -= mine;
             if (x.parts > 1) x.slot += k;
         }
         return x;
     }
-    __device__ __forceinline__ void place(const Attn &a, Unit &x, int item, int t) const
-    {
-        x.tile = t - 1 - a.by_heads(item);
-        x.h = item - a.by_heads(item) * a.p.heads;
-        x.slot += item * x.parts;
-    }
-
     __device__ __forceinline__ Unit find(const Attn &a, int u) const
     {
         int left, t;
         Unit x = sequence<false>(a, u, left, t);
         const int item = x.parts == 1 ? left : left / x.parts;
         x.part = left - item * x.parts;
-        place(a, x, item, t);
+        x.tile = t - 1 - a.by_heads(item);
+        x.h = item - a.by_heads(item) * a.p.heads;
+        x.slot += item * x.parts;
         return x;
     }
-    // Row tile i of those in several parts.
-    __device__ __forceinline__ Unit find_item(const Attn &a, int i) const
+    // Where row i of those in several parts stands: its sequence, head and row of these; tile is how many row tiles there
+    // are, slot that of the sequence's first part.
+    __device__ __forceinline__ Unit find_row(const Attn &a, int i, int &row) const
     {
         int left, t;
         Unit x = sequence<true>(a, i, left, t);
+        x.tile = t;
         x.part = 0;
-        place(a, x, left, t);
+        x.h = left / (x.s.n * a.group);
+        row = left - x.h * x.s.n * a.group;
         return x;
     }
 };

@@ -808,12 +808,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         q_loads |= 1u << q;
                         continue;
                     }
-                    // Rows behind the last one as zeros.
+                    // Rows behind the last one as zeros, or, of whole warps of them, as they were.
                     const int rows = rc.rows, r0 = rc.r0 + q * QROWS;
                     constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
                     const uint32_t dst0 = smem_u32(smem + q * C::Q_BYTES);
 #pragma unroll 1
-                    for (int i = 0; i < QROWS; i += 32) {
+                    for (int i = 0; i < min(QROWS, rows - r0); i += 32) {
                         const int r = r0 + i + lane, tok = a.by_group(r);
                         const int64_t off = r < rows ? (rc.row0 + tok) * a.ldq + (rc.h * a.group + r - tok * a.group) * D : -1;
 #pragma unroll 8
