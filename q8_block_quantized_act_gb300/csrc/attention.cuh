@@ -83,8 +83,10 @@ __device__ __forceinline__ Span span_of(const Attn &a, const Seq &s, int r0, int
 }
 
 // ---------------------------------------------------------------------------------------
-// The units of a batch of chunks, counted by a warp: lane j counts sequences j * per ... of the batch.  The
-// last row tiles come first, which are the longest.  Every member is called by whole warps.
+// The units of a batch of chunks, counted by a warp: lane j counts sequences j * per ... of the batch.  In a
+// sequence the last row tiles come first, which are the longest; of up to 32 sequences the longest of all come first,
+// where the CTAs take several units each (4 prompts of 1505 tokens: units of 12 to 1 key tiles; sequence by sequence a CTA
+// would have up to 26 tiles, so 14).  Every member is called by whole warps.
 // ---------------------------------------------------------------------------------------
 struct Unit {
     int b, h, tile, part, parts;
@@ -101,6 +103,7 @@ struct Plan {
     int units, slots, rows;
     Seq s;
     int tiles, parts;
+    int top;                        // the last key tile of all, plus 1; 0: units stand sequence by sequence
 
     // Row tiles of a sequence and the parts of each.
     __device__ __forceinline__ void shape(const Attn &a, const Seq &q, int &t, int &p) const
@@ -215,6 +218,8 @@ struct Plan {
         slots = sum[1] - v[1];
         rows = sum[2] - v[2];
         total = __shfl_sync(0xffffffffu, sum[0], 31);
+        top = 0;
+        if (per == 1 && a.p.seqs > 1 && total > a.ctas) top = __reduce_max_sync(0xffffffffu, tiles ? (s.pos0 + s.n - 1) / TILE + 1 : 1);
         split = __shfl_sync(0xffffffffu, sum[2], 31);
     }
 
@@ -247,8 +252,53 @@ struct Plan {
         }
         return x;
     }
+    // (top > 0) How many row tiles of the lane's sequence have their last row at key tile l - 1 or a later one.
+    __device__ __forceinline__ int at_least(const Attn &a, int l) const
+    {
+        const long long x = l ? (long long)(l - 1) * TILE - s.pos0 : 0;      // a row tile has a row of token x or a later one
+        return x <= 0 ? tiles : x >= s.n ? 0 : tiles - (int)x * a.group / ROWS;
+    }
+    // Unit u of them by where their last rows are, latest first.
+    __device__ __forceinline__ Unit find_by_length(const Attn &a, int u) const
+    {
+        const int each = parts * a.p.heads;           // units of a row tile of the lane's sequence
+        int lo = 0, hi = top + 1, later = 0;          // more than u units at lo or later, no more than u at hi: `later`
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1, n = __reduce_add_sync(0xffffffffu, at_least(a, mid) * each);
+            if (n > u) {
+                lo = mid;
+            } else {
+                hi = mid;
+                later = n;
+            }
+        }
+        const int behind = at_least(a, hi), mine = (at_least(a, lo) - behind) * each;
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if ((threadIdx.x & 31) >= o) sum += v;
+        }
+        Unit x;
+        x.b = __popc(__ballot_sync(0xffffffffu, sum <= u - later));          // the first lane that reaches beyond u
+        const int left = u - later - __shfl_sync(0xffffffffu, sum - mine, x.b);
+        x.s.row0 = __shfl_sync(0xffffffffu, s.row0, x.b);
+        x.s.n = __shfl_sync(0xffffffffu, s.n, x.b);
+        x.s.pos0 = __shfl_sync(0xffffffffu, s.pos0, x.b);
+        x.s.end = __shfl_sync(0xffffffffu, s.end, x.b);
+        x.parts = __shfl_sync(0xffffffffu, parts, x.b);
+        const int item = left / x.parts;
+        x.part = left - item * x.parts;
+        const int k = a.by_heads(item) + __shfl_sync(0xffffffffu, behind, x.b);      // row tiles of the sequence behind it
+        x.tile = __shfl_sync(0xffffffffu, tiles, x.b) - 1 - k;
+        x.h = item - a.by_heads(item) * a.p.heads;
+        x.slot = __shfl_sync(0xffffffffu, slots, x.b) + (k * a.p.heads + x.h) * x.parts;
+        return x;
+    }
+
     __device__ __forceinline__ Unit find(const Attn &a, int u) const
     {
+        if (top > 0) return find_by_length(a, u);
         int left, t;
         Unit x = sequence<false>(a, u, left, t);
         const int item = x.parts == 1 ? left : left / x.parts;

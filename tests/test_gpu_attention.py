@@ -95,6 +95,15 @@ def test_long_sequences_in_parts(hint):
     check(ref.Batch([(6000, 90)], 1, 64, 128, torch.float16, seed=3), 4, hint)
 
 
+@pytest.mark.parametrize("window", [0, 260])
+@pytest.mark.parametrize("seqs,heads", [
+    ([(0, 600), (700, 300), (0, 0), (100, 450), (0, 900)], 8),
+    ([(0, 500)] * 5, 16), ([(5000, 330), (0, 1), (40, 700), (2000, 128)], 16)], ids=["ragged", "even", "long"])
+def test_more_units_than_ctas(seqs, heads, window):
+    """Several chunks whose units the CTAs take longest first, some of them parts of row tiles; also none at all on one."""
+    check(ref.Batch(seqs, heads, 64, 16, torch.float16, seed=heads), 2 * heads, 1000, window=window)
+
+
 @HINTS
 def test_many_sequences(hint):
     """More sequences than a CTA has threads, some without tokens."""
@@ -273,6 +282,32 @@ def test_graph_follows_lengths(hint):
         g.replay()
         device_ok()
         want, tol = ref.attention(batch, q, 0.125, 0, torch.float16)
+        ref.close(out, want, tol)
+
+
+@HINTS
+def test_two_graphs_share_a_workspace(hint):
+    """Replayed in turn on one stream, over different batches."""
+    ws, graphs = None, []
+    for seed, seqs in ((21, [(2000, 1), (90, 3)]), (22, [(0, 150), (700, 2), (3000, 1)])):
+        batch = ref.Batch(seqs, 2, 64, 16, torch.float16, seed=seed)
+        q = batch.randn(batch.m, 4, 64)
+        kv, qd = q8.PagedKV(*batch.cuda()), q.cuda()
+        ws = q8.attention_workspace(kv, 4) if ws is None else ws
+        out = torch.empty_like(qd)
+        call = lambda: q8.attention(kv, qd, max_new=new(hint, q, 2), ws=ws, out=out)     # noqa: B023, E731
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, kv, qd, out, ref.attention(batch, q, 0.125, 0, torch.float16)))
+    for _ in range(3):
+        for g, _, _, out, _ in graphs:
+            out.fill_(7.0)
+            g.replay()
+    device_ok()
+    for _, _, _, out, (want, tol) in graphs:
         ref.close(out, want, tol)
 
 
