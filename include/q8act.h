@@ -466,7 +466,7 @@ int q8act_logprobs(const void *logits, int64_t ld, int type, const int32_t *toke
  *   lens [seqs]: positions of each sequence, the new tokens included: its last new token has position
  *       lens - 1, the others the positions before.
  * table, starts and lens are device memory that the kernels read when they run, so a captured graph
- * follows their contents.  seqs <= 2^20, table_width * page_size <= 2^30, pages < 2^31; the cache 16-byte
+ * follows their contents.  seqs <= 2^16, table_width * page_size <= 2^30, pages < 2^31; the cache 16-byte
  * aligned, the others as their type.
  * Positions before 0, beyond the table or on a page outside 0 .. pages - 1 do not exist: nothing is written
  * to them, and the attention takes them as masked.  Rows before starts[0] and from starts[seqs] on (padding of a
@@ -487,7 +487,7 @@ typedef struct q8act_paged_kv {
  *   q [m][heads_q][dim], k, v [m][heads][dim]: elements of `type`, tokens ldq, ldk, ldv elements apart
  *       (rows 16-byte aligned; the parts of a fused projection's rows, for instance).
  *   q_out [m][heads_q][dim] of the cache's type, tokens ldqo apart: the rotated queries (it may be q
- *       itself where the types agree).  q and q_out may both be NULL (heads_q 0).
+ *       itself where types and distances agree).  q and q_out may both be NULL (heads_q 0).
  *   turns [rot / 2]: each pair's fraction of a turn a position, times 2^64 (the angle is then exact modulo a
  *       turn at any position).  rot <= dim, a multiple of 16: the head's first rot values are rotated, as
  *       pairs (i, i + rot / 2), or (2i, 2i + 1) where interleaved is 1; the others are copied.  rot 0
@@ -505,7 +505,7 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   p - window < j where window > 0; keys and values of head h * heads / heads_q.
  *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
  *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
- *       It must not overlap q.
+ *       It must not overlap q (q itself is refused).
  *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros.  What is at masked places (beyond lens, behind the
  *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded

@@ -724,7 +724,7 @@ static int check_paged(const q8act_paged_kv *kv, int64_t m, int64_t heads_q)
     const int64_t ps = kv->page_size;
     if ((kv->dim != 64 && kv->dim != 128) || ps < 16 || ps > 1024 || (ps & (ps - 1)) || kv->heads < 1 || kv->heads > 1024 ||
         kv->pages < 1 || kv->pages >= INT32_MAX || kv->page_stride < kv->heads * ps * kv->dim ||
-        kv->page_stride >= ((int64_t)1 << 38) || kv->seqs < 1 || kv->seqs > (1 << 20) || kv->table_width < 1 ||
+        kv->page_stride >= ((int64_t)1 << 38) || kv->seqs < 1 || kv->seqs > (1 << 16) || kv->table_width < 1 ||
         kv->table_width * ps > (1 << 30) || kv->table_ld < kv->table_width || kv->table_ld >= ((int64_t)1 << 40))
         return Q8ACT_ERR_DIMS;
     if (m < 1 || heads_q < 0 || heads_q > 4096 || m * (heads_q + 2 * kv->heads) > (1 << 30)) return Q8ACT_ERR_DIMS;
@@ -751,6 +751,8 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
               (rc = check_rows(q_out, ldqo, (int64_t)heads_q * kv->dim, kv->type))))
         return rc;
     if (reinterpret_cast<uintptr_t>(turns) & 7u) return Q8ACT_ERR_ALIGN;
+    if (q && q == q_out && type != kv->type) return Q8ACT_ERR_TYPE;
+    if (q && q == q_out && ldq != ldqo) return Q8ACT_ERR_DIMS;
     const q8::DeviceInfo *dev;
     if ((rc = current_device(&dev))) return rc;
     const q8::AppendArgs a{q, k, v, q_out, ldq, ldk, ldv, ldqo, turns, type, heads_q, rot, interleaved};
@@ -772,7 +774,7 @@ int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *
                     float scale, int window, int max_new, int64_t m, void *ws, size_t ws_bytes, void *stream)
 {
     if (!q || !out) return Q8ACT_ERR_NULL;
-    if (m < 1 || m > (1 << 30)) return Q8ACT_ERR_DIMS;
+    if (m < 1 || m > (1 << 30) || q == out) return Q8ACT_ERR_DIMS;
     int rc = check_paged(kv, m, heads_q);
     if (rc) return rc;
     if (!known_type(otype)) return Q8ACT_ERR_TYPE;

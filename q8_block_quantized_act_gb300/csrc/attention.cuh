@@ -184,6 +184,7 @@ struct Plan {
             // Parts of equal length, as many as the workspace has room for: a row tile of p > 1 parts has more than
             // (p - 1) * length >= p * length / 2 key tiles, so there are fewer than twice work / length of them.
             long long w = 0;
+#pragma unroll 4
             for (int b = b0; b < b1; ++b) {
                 const Seq q = seq_of(a.p, b);
                 const int n = q.n * a.group;
@@ -193,6 +194,7 @@ struct Plan {
             for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
             w = (2 * w * a.p.heads + a.slots - 1) / a.slots;
             length = (int)min(max(w, (long long)a.least), (long long)INT_MAX / 2);
+#pragma unroll 4
             for (int b = b0; b < b1; ++b) {
                 int t, p;
                 const Seq q = seq_of(a.p, b);
@@ -242,13 +244,43 @@ struct Plan {
             x.parts = __shfl_sync(0xffffffffu, parts, lo);
             return x;
         }
-        for (x.b = lo * per;; ++x.b) {              // ends: u < total
-            x.s = seq_of(a.p, x.b);
-            shape(a, x.s, t, x.parts);
-            const int k = t * a.p.heads * x.parts, mine = !JOIN ? k : x.parts > 1 ? x.s.n * a.group * a.p.heads : 0;
-            if (left < mine || x.b + 1 >= a.p.seqs) break;
-            left -= mine;
-            if (x.parts > 1) x.slot += k;
+        // 32 of the lane's sequences at a time (ends: u < total).
+        const int end = min(lo * per + per, a.p.seqs);
+        for (int b0 = lo * per;; b0 += 32) {
+            const int lane = threadIdx.x & 31;
+            Seq q{0, 0, 0, 0};
+            int n = 0, p = 0;
+            if (b0 + lane < end) {
+                q = seq_of(a.p, b0 + lane);
+                shape(a, q, n, p);
+            }
+            const int k = n * a.p.heads * p, mine = !JOIN ? k : p > 1 ? q.n * a.group * a.p.heads : 0, cut = p > 1 ? k : 0;
+            int sum = mine, sum_cut = cut;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o), w = __shfl_up_sync(0xffffffffu, sum_cut, o);
+                if (lane >= o) {
+                    sum += v;
+                    sum_cut += w;
+                }
+            }
+            const int all = __shfl_sync(0xffffffffu, sum, 31);
+            if (left >= all && b0 + 32 < end) {
+                left -= all;
+                x.slot += __shfl_sync(0xffffffffu, sum_cut, 31);
+                continue;
+            }
+            const int at = min(__popc(__ballot_sync(0xffffffffu, sum <= left)), 31);        // the first that reaches beyond it
+            left -= __shfl_sync(0xffffffffu, sum - mine, at);
+            x.slot += __shfl_sync(0xffffffffu, sum_cut - cut, at);
+            x.b = b0 + at;
+            x.s.row0 = __shfl_sync(0xffffffffu, q.row0, at);
+            x.s.n = __shfl_sync(0xffffffffu, q.n, at);
+            x.s.pos0 = __shfl_sync(0xffffffffu, q.pos0, at);
+            x.s.end = __shfl_sync(0xffffffffu, q.end, at);
+            t = __shfl_sync(0xffffffffu, n, at);
+            x.parts = __shfl_sync(0xffffffffu, p, at);
+            break;
         }
         return x;
     }

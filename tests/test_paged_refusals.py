@@ -8,7 +8,7 @@ import torch
 import q8_block_quantized_act_gb300 as q8
 from q8_block_quantized_act_gb300 import build as q8build
 
-A = 1 << 20          # a fake, 16-byte aligned address: never dereferenced by these calls
+A, B = 1 << 20, 1 << 21          # fake, 16-byte aligned addresses: never dereferenced by these calls
 MIS = A + 4
 F32, F16, BF16 = q8.Q8ACT_F32, q8.Q8ACT_F16, q8.Q8ACT_BF16
 NULL, DIMS, ALIGN, WS, TYPE = (q8.Q8ACT_ERR_NULL, q8.Q8ACT_ERR_DIMS, q8.Q8ACT_ERR_ALIGN, q8.Q8ACT_ERR_WORKSPACE,
@@ -25,12 +25,12 @@ def batch(k=A, v=A, stride=2 * 16 * 64, pages=4, table=A, table_ld=3, starts=A, 
     return q8.q8act_paged_kv(k, v, stride, pages, table, table_ld, starts, lens, seqs, width, page, heads, dim, type)
 
 
-def append(kv=None, q=A, ldq=256, k=A, ldk=128, v=A, ldv=128, t=F32, qo=A, ldqo=256, hq=4, turns=A, rot=64, il=0, m=3, **b):
+def append(kv=None, q=A, ldq=256, k=A, ldk=128, v=A, ldv=128, t=F32, qo=B, ldqo=256, hq=4, turns=A, rot=64, il=0, m=3, **b):
     kv = batch(**b) if kv is None else kv
     return q8.q8act_append_kv(kv or None, q, ldq, k, ldk, v, ldv, t, qo, ldqo, hq, turns, rot, il, m, 0)
 
 
-def attend(kv=None, q=A, ldq=256, out=A, ldo=256, ot=F16, hq=4, scale=0.125, window=0, max_new=1, m=3, ws=A, nb=None, **b):
+def attend(kv=None, q=A, ldq=256, out=B, ldo=256, ot=F16, hq=4, scale=0.125, window=0, max_new=1, m=3, ws=A, nb=None, **b):
     kv = batch(**b) if kv is None else kv
     nb = 1 << 40 if nb is None else nb
     return q8.q8act_attention(kv or None, q, ldq, out, ldo, ot, hq, scale, window, max_new, m, ws, nb, 0)
@@ -42,7 +42,7 @@ BATCH = [
     (DIMS, dict(dim=32)), (DIMS, dict(dim=96)), (DIMS, dict(dim=256)), (DIMS, dict(page=8)), (DIMS, dict(page=48)),
     (DIMS, dict(page=2048)), (DIMS, dict(page=0)), (DIMS, dict(page=-16)), (DIMS, dict(heads=0)), (DIMS, dict(heads=-1)),
     (DIMS, dict(heads=4096)), (DIMS, dict(pages=0)), (DIMS, dict(pages=2 ** 31)), (DIMS, dict(stride=2 * 16 * 64 - 8)),
-    (DIMS, dict(stride=1 << 40)), (DIMS, dict(seqs=0)), (DIMS, dict(seqs=1 << 21)), (DIMS, dict(width=0)),
+    (DIMS, dict(stride=1 << 40)), (DIMS, dict(seqs=0)), (DIMS, dict(seqs=(1 << 16) + 1)), (DIMS, dict(width=0)),
     (DIMS, dict(width=1 << 27, table_ld=1 << 27)), (DIMS, dict(table_ld=2)), (DIMS, dict(m=0)), (DIMS, dict(m=-1)),
     (DIMS, dict(m=1 << 40)), (DIMS, dict(m=1 << 28)),
     (ALIGN, dict(k=MIS)), (ALIGN, dict(stride=2 * 16 * 64 + 4)), (ALIGN, dict(table=A + 2)), (ALIGN, dict(starts=A + 1)),
@@ -62,6 +62,7 @@ def test_batch(call, rc, args):
     (DIMS, dict(rot=8)), (DIMS, dict(rot=72)), (DIMS, dict(rot=80)), (DIMS, dict(rot=-16)), (DIMS, dict(il=2)),
     (DIMS, dict(hq=5000)), (DIMS, dict(hq=-1)), (DIMS, dict(ldq=255)), (DIMS, dict(ldk=127)), (DIMS, dict(ldv=64)),
     (DIMS, dict(ldqo=128)), (ALIGN, dict(ldq=258)), (ALIGN, dict(ldk=129)), (ALIGN, dict(ldv=130)), (ALIGN, dict(ldqo=260)),
+    (TYPE, dict(qo=A)), (TYPE, dict(qo=A, t=BF16)), (DIMS, dict(qo=A, t=F16, ldq=512)),
     (ALIGN, dict(q=MIS)), (ALIGN, dict(v=MIS)), (ALIGN, dict(qo=MIS)), (ALIGN, dict(turns=A + 4)),
 ], ids=str)
 def test_append(rc, args):
@@ -75,7 +76,7 @@ def test_append(rc, args):
 
 
 @pytest.mark.parametrize("rc,args", [
-    (NULL, dict(q=None)), (NULL, dict(out=None)), (TYPE, dict(ot=3)), (DIMS, dict(hq=3)), (DIMS, dict(hq=0)),
+    (NULL, dict(q=None)), (NULL, dict(out=None)), (DIMS, dict(out=A)), (TYPE, dict(ot=3)), (DIMS, dict(hq=3)), (DIMS, dict(hq=0)),
     (DIMS, dict(hq=1)), (DIMS, dict(hq=8192)), (DIMS, dict(scale=0.0)), (DIMS, dict(scale=-1.0)), (DIMS, dict(scale=float("nan"))),
     (DIMS, dict(scale=float("inf"))), (DIMS, dict(scale=2.0 ** 101)), (DIMS, dict(window=-1)), (DIMS, dict(window=2 ** 31 - 1)), (DIMS, dict(max_new=-1)),
     (DIMS, dict(ldq=255)), (DIMS, dict(ldo=128)), (ALIGN, dict(ldq=260)), (ALIGN, dict(ldo=257)), (ALIGN, dict(q=MIS)),
