@@ -17,17 +17,18 @@
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
 //
-// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 322 us
-// (1.71 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
+// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 324 us
+// (1.70 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
 // cycles and takes about 2450, the chain of one row tile: S 230 cycles after its MMAs, maximum 490, weights 1000 (P in two
 // parts, the products of the first under way), products and next S 800.  64 values: 64 + 8 heads, 8000 tokens, window 1024 f16
-// 174 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
+// 178 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
 // rest of the softmax 1900; ten tiles a unit, of which three are masked, leave 3400 cycles between units beside them.
 // What was tried without gain: a thread half a row (640 threads: registers spill), S twice through registers
 // (the loads' latency), P in four parts, a warp of its own for the output (512 threads leave 128 registers), an MMA
 // warp a row tile (they fall into step: 457 us), both halves on the same rows with every other tile (35 rows, 6000
 // positions: 31 -> 42 us), equal stretches as for few tokens (a cut costs two f32 outputs, a change of units and the
-// join: 509 tokens at 16384 110 -> 125 us).
+// join: 509 tokens at 16384 110 -> 125 us), the next S of a row tile alone in the other's place (16 x 5 tokens at 6000, one row
+// tile each, 24.1 -> 23.7 us: 1.2 us a key tile of 152 CTAs is the copy rate).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -854,7 +855,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     attention_place(a, ws, SLOTS, ROWS);
     a.ctas = dev.num_sms;
     a.least = 2;
-    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and takes 132 us, 8 in 2 and 115)
+    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 107)
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     // Row tiles of whole tokens come as one box; others are gathered row by row.
