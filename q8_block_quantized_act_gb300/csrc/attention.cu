@@ -706,13 +706,13 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attention_rows_join_kernel(At
 // ---------------------------------------------------------------------------------------
 constexpr int CHUNK_JOIN_THREADS = 256;
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(CHUNK_JOIN_THREADS) attention_chunk_join_kernel(Attn a)
 {
     constexpr int V = D / 32, U = 4;             // values a lane, parts at a time
     using Vec = std::conditional_t<V == 4, float4, float2>;
     const int lane = threadIdx.x & 31, warps = gridDim.x * (CHUNK_JOIN_THREADS / 32);
-    using P = Plan<CHUNK_ROWS, CHUNK_TILE>;
+    using P = Plan<CHUNK_ROWS, CHUNK_TILE, FEW>;
     __shared__ P plans[32];                      // one warp's, for all
     if (threadIdx.x < 32) {
         P p;
@@ -782,7 +782,8 @@ __global__ void __launch_bounds__(CHUNK_JOIN_THREADS) attention_chunk_join_kerne
 cudaError_t launch_attention_chunk_join(const DeviceInfo &dev, const Attn &a, int dim, cudaStream_t stream)
 {
     auto go = [&](auto kern) { return launch_dependent(kern, dim3(4 * dev.num_sms), CHUNK_JOIN_THREADS, 0, stream, a); };
-    return dim == 64 ? go(attention_chunk_join_kernel<64>) : go(attention_chunk_join_kernel<128>);
+    if (a.p.seqs <= 32) return dim == 64 ? go(attention_chunk_join_kernel<64, true>) : go(attention_chunk_join_kernel<128, true>);
+    return dim == 64 ? go(attention_chunk_join_kernel<64, false>) : go(attention_chunk_join_kernel<128, false>);
 }
 
 // Enough for either kernel: of few rows, two partial results at most of each of the two CTAs on each of 152 SMs.

@@ -94,7 +94,9 @@ struct Unit {
     Seq s;
 };
 
-template <int ROWS, int TILE>
+// FEW: up to 32 sequences, one a lane.  (Kernels of their own: a CTA meets the code for the first time, and waits for it;
+// 509 tokens at 16384 110 us with both in one, 103 so; 8192 tokens 326, 321.)
+template <int ROWS, int TILE, bool FEW>
 struct Plan {
     int per;                        // sequences a lane
     int length;                     // key tiles a part
@@ -163,7 +165,7 @@ struct Plan {
         per = (a.p.seqs + 31) / 32;
         const int b0 = min(lane * per, a.p.seqs), b1 = min(b0 + per, a.p.seqs);
         int v[3] = {0, 0, 0};
-        if (per == 1) {
+        if constexpr (FEW) {
             s = Seq{0, 0, 0, 0};
             int n = 0, first = 0, last = 0;
             if (lane < a.p.seqs) {
@@ -221,7 +223,7 @@ struct Plan {
         rows = sum[2] - v[2];
         total = __shfl_sync(0xffffffffu, sum[0], 31);
         top = 0;
-        if (per == 1 && a.p.seqs > 1 && total > a.ctas) top = __reduce_max_sync(0xffffffffu, tiles ? (s.pos0 + s.n - 1) / TILE + 1 : 1);
+        if (FEW && a.p.seqs > 1 && total > a.ctas) top = __reduce_max_sync(0xffffffffu, tiles ? (s.pos0 + s.n - 1) / TILE + 1 : 1);
         split = __shfl_sync(0xffffffffu, sum[2], 31);
     }
 
@@ -235,7 +237,7 @@ struct Plan {
         left = u - __shfl_sync(0xffffffffu, before, lo);
         x.slot = __shfl_sync(0xffffffffu, slots, lo);
         x.b = lo;
-        if (per == 1) {
+        if constexpr (FEW) {
             x.s.row0 = __shfl_sync(0xffffffffu, s.row0, lo);
             x.s.n = __shfl_sync(0xffffffffu, s.n, lo);
             x.s.pos0 = __shfl_sync(0xffffffffu, s.pos0, lo);
@@ -330,7 +332,8 @@ struct Plan {
 
     __device__ __forceinline__ Unit find(const Attn &a, int u) const
     {
-        if (top > 0) return find_by_length(a, u);
+        if constexpr (FEW)
+            if (top > 0) return find_by_length(a, u);
         int left, t;
         Unit x = sequence<false>(a, u, left, t);
         const int item = x.parts == 1 ? left : left / x.parts;

@@ -17,11 +17,11 @@
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
 //
-// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 324 us
-// (1.70 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
+// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 321 us
+// (1.71 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
 // cycles and takes about 2450, the chain of one row tile: S 230 cycles after its MMAs, maximum 490, weights 1000 (P in two
 // parts, the products of the first under way), products and next S 800.  64 values: 64 + 8 heads, 8000 tokens, window 1024 f16
-// 178 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
+// 176 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
 // rest of the softmax 1900; ten tiles a unit, of which three are masked, leave 3400 cycles between units beside them.
 // What was tried without gain: a thread half a row (640 threads: registers spill), S twice through registers
 // (the loads' latency), P in four parts, a warp of its own for the output (512 threads leave 128 registers), an MMA
@@ -257,7 +257,7 @@ __device__ __forceinline__ void clear_non_finite(uint8_t *tile, int lo, int hi, 
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_q, int q_boxes, Attn a)
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool live = r < x.rows;
             const int pos = x.pos0 + a.by_group(live ? r : 0);
             const int hi = live ? min(pos, x.end - 1) : INT_MAX - 1, lo = live && a.window ? max(pos - a.window + 1, 0) : 0;
-            const int count = tiles - x.t0;              // tile t of the sequence is tile count + t of the CTA
+            const uint32_t tiles0 = tiles;               // tile t of the sequence is tile tiles0 + t - t0 of the CTA
             const bool some = end > from;
             tiles += x.t1 - x.t0;
             float mx = NEG, sum = 0.0f;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < TILE / 32; ++i) ld32(col_s + 32 * i, s + 32 * i);
                 const int k0 = t * TILE;
-                const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(count + t) & 7]);
+                const uint32_t pages = *const_cast<volatile uint32_t *>(&sm.pages[(tiles0 + t - x.t0) & 7]);
                 const bool edge = __any_sync(0xffffffffu, k0 + TILE - 1 > hi || k0 < lo) || pages != 0xff;
                 wait_ld<TILE>(s);
                 if constexpr (C::OWN_P) {
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else {
             // ------------------------------ units, queries ------------------------------
-            Plan<ROWS, TILE> plan;
+            Plan<ROWS, TILE, FEW> plan;
             plan.make(a);
             uint32_t q_phase = 3, q_loads = 0;               // a bit a row tile
             bool ok = true;
@@ -855,7 +855,7 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     attention_place(a, ws, SLOTS, ROWS);
     a.ctas = dev.num_sms;
     a.least = 2;
-    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 107)
+    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 103)
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     // Row tiles of whole tokens come as one box; others are gathered row by row.
@@ -873,16 +873,18 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
         if constexpr (sizeof(T) == 4) {
             return cudaErrorInvalidValue;
         } else {
-            auto go = [&](auto d) -> cudaError_t {
+            auto go = [&](auto d, auto few) -> cudaError_t {
                 constexpr int D = decltype(d)::value;
+                constexpr bool FEW = decltype(few)::value;
                 constexpr size_t smem = Cfg<D>::OFF_SHARED + sizeof(Shared);
                 static_assert(smem <= 227 * 1024, "shared memory");
-                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D>>(dev.device, smem);
+                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D, FEW>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_chunk_kernel<T, D>, dim3(a.ctas), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
+                e = launch_dependent(attention_chunk_kernel<T, D, FEW>, dim3(a.ctas), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
                 return e == cudaSuccess ? launch_attention_chunk_join(dev, a, D, stream) : e;
             };
-            return kv.dim == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
+            auto pick = [&](auto d) { return kv.seqs <= 32 ? go(d, std::true_type{}) : go(d, std::false_type{}); };
+            return kv.dim == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
         }
     });
 }
