@@ -95,7 +95,7 @@ struct Unit {
 };
 
 // FEW: up to 32 sequences, one a lane.  (Kernels of their own: a CTA meets the code for the first time, and waits for it;
-// 509 tokens at 16384 110 us with both in one, 103 so; 8192 tokens 326, 321.)
+// 509 tokens at 16384 110 us with both in one, 103 so; 8192 tokens 326 and 321.)
 template <int ROWS, int TILE, bool FEW>
 struct Plan {
     int per;                        // sequences a lane

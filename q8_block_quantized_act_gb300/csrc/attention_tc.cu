@@ -17,11 +17,11 @@
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
 // at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
 //
-// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 321 us
-// (1.71 PFLOP/s, 0.90 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
+// Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 318 us
+// (1.73 PFLOP/s, 0.92 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
 // cycles and takes about 2450, the chain of one row tile: S 230 cycles after its MMAs, maximum 490, weights 1000 (P in two
 // parts, the products of the first under way), products and next S 800.  64 values: 64 + 8 heads, 8000 tokens, window 1024 f16
-// 176 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
+// 168 us, where the exponentials bound: 2 x 128 a thread of the four schedulers' 8 a cycle are 1024 cycles a step, with the
 // rest of the softmax 1900; ten tiles a unit, of which three are masked, leave 3400 cycles between units beside them.
 // What was tried without gain: a thread half a row (640 threads: registers spill), S twice through registers
 // (the loads' latency), P in four parts, a warp of its own for the output (512 threads leave 128 registers), an MMA
@@ -257,10 +257,13 @@ __device__ __forceinline__ void clear_non_finite(uint8_t *tile, int lo, int hi, 
     }
 }
 
-template <typename T, int D, bool FEW>
+// FEW: up to 32 sequences (Plan).  BOXES: a row tile holds whole tokens, so its queries come as one TMA box; otherwise they are
+// gathered row by row.  Kernels of their own, since less code is faster by itself here (64 + 8 heads x 64, window 1024 of
+// 8000: 176 us with both ways of queries in one, 168 so).
+template <typename T, int D, bool FEW, bool BOXES>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                           const __grid_constant__ CUtensorMap tm_q, int q_boxes, Attn a)
+                           const __grid_constant__ CUtensorMap tm_q, Attn a)
 {
     using C = Cfg<D>;
     constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 9 && lane == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
-        if (q_boxes) prefetch_tensormap(&tm_q);
+        if (BOXES) prefetch_tensormap(&tm_q);
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_empty[q], q_phase >> q & 1, a.status, abort_flag));
                     if (!ok) break;
                     q_phase ^= 1u << q;
-                    if (q_boxes) {
+                    if constexpr (BOXES) {
                         // Whole tokens: a box of a row tile's.  (Rows behind the sequence's last hold others' queries,
                         // or zeros; what comes of them goes nowhere.)
                         if (lane == 0) {
@@ -807,34 +810,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         __syncwarp();
                         q_loads |= 1u << q;
-                        continue;
-                    }
-                    // Rows behind the last one as zeros, or, of whole warps of them, as they were.
-                    const int rows = rc.rows, r0 = rc.r0 + q * QROWS;
-                    constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
-                    const uint32_t dst0 = smem_u32(smem + q * C::Q_BYTES);
+                    } else {
+                        // Rows behind the last one as zeros, or, of whole warps of them, as they were.
+                        const int rows = rc.rows, r0 = rc.r0 + q * QROWS;
+                        constexpr int VECS = D / 8, AT_ONCE = 32 / VECS;       // 16-byte vectors of a row, rows a round of lanes
+                        const uint32_t dst0 = smem_u32(smem + q * C::Q_BYTES);
 #pragma unroll 1
-                    for (int i = 0; i < min(QROWS, rows - r0); i += 32) {
-                        const int r = r0 + i + lane, tok = a.by_group(r);
-                        const int64_t off = r < rows ? (rc.row0 + tok) * a.ldq + (rc.h * a.group + r - tok * a.group) * D : -1;
+                        for (int i = 0; i < min(QROWS, rows - r0); i += 32) {
+                            const int r = r0 + i + lane, tok = a.by_group(r);
+                            const int64_t off = r < rows ? (rc.row0 + tok) * a.ldq + (rc.h * a.group + r - tok * a.group) * D : -1;
 #pragma unroll 8
-                        for (int j = 0; j < 32; j += AT_ONCE) {
-                            const int rr = i + j + lane / VECS, v = lane % VECS;
-                            const int64_t o = __shfl_sync(0xffffffffu, off, j + lane / VECS);
-                            cp_async16(dst0 + (v >> 3) * (QROWS * 128) + rr * 128 + (((v & 7) ^ (rr & 7)) << 4),
-                                       static_cast<const T *>(a.q) + (o < 0 ? 0 : o) + v * 8, o < 0 ? 0 : 16);
+                            for (int j = 0; j < 32; j += AT_ONCE) {
+                                const int rr = i + j + lane / VECS, v = lane % VECS;
+                                const int64_t o = __shfl_sync(0xffffffffu, off, j + lane / VECS);
+                                cp_async16(dst0 + (v >> 3) * (QROWS * 128) + rr * 128 + (((v & 7) ^ (rr & 7)) << 4),
+                                           static_cast<const T *>(a.q) + (o < 0 ? 0 : o) + v * 8, o < 0 ? 0 : 16);
+                            }
                         }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.q_full[q]);
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.q_full[q]);
                 }
                 if (!ok) break;
             }
             // Never leave with a copy into this CTA's shared memory in flight: the last unit's queries (of the units
             // before, the MMAs have waited for them).
-            if (q_boxes)
+            if (BOXES)
                 for (int q = 0; q < 2; ++q)
                     if (q_loads >> q & 1) mbar_wait_drain(&sm.q_full[q], q_phase >> q & 1, a.status);
         }
@@ -855,11 +858,10 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     attention_place(a, ws, SLOTS, ROWS);
     a.ctas = dev.num_sms;
     a.least = 2;
-    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 103)
+    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 102)
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
-    // Row tiles of whole tokens come as one box; others are gathered row by row.
-    const int q_boxes = QROWS % a.group == 0;
+    const bool q_boxes = QROWS % a.group == 0;
     if (q_boxes) {
         const uint64_t dims[3] = {(uint64_t)kv.dim, (uint64_t)a.group * kv.heads, (uint64_t)a.p.m};
         const uint64_t strides[2] = {(uint64_t)kv.dim * 2, (uint64_t)a.ldq * 2};
@@ -873,17 +875,18 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
         if constexpr (sizeof(T) == 4) {
             return cudaErrorInvalidValue;
         } else {
-            auto go = [&](auto d, auto few) -> cudaError_t {
+            auto go = [&](auto d, auto few, auto boxes) -> cudaError_t {
                 constexpr int D = decltype(d)::value;
-                constexpr bool FEW = decltype(few)::value;
+                constexpr bool FEW = decltype(few)::value, BOXES = decltype(boxes)::value;
                 constexpr size_t smem = Cfg<D>::OFF_SHARED + sizeof(Shared);
                 static_assert(smem <= 227 * 1024, "shared memory");
-                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D, FEW>>(dev.device, smem);
+                cudaError_t e = set_kernel_smem<attention_chunk_kernel<T, D, FEW, BOXES>>(dev.device, smem);
                 if (e != cudaSuccess) return e;
-                e = launch_dependent(attention_chunk_kernel<T, D, FEW>, dim3(a.ctas), THREADS, smem, stream, tk, tv, tq, q_boxes, a);
+                e = launch_dependent(attention_chunk_kernel<T, D, FEW, BOXES>, dim3(a.ctas), THREADS, smem, stream, tk, tv, tq, a);
                 return e == cudaSuccess ? launch_attention_chunk_join(dev, a, D, stream) : e;
             };
-            auto pick = [&](auto d) { return kv.seqs <= 32 ? go(d, std::true_type{}) : go(d, std::false_type{}); };
+            auto by_queries = [&](auto d, auto few) { return q_boxes ? go(d, few, std::true_type{}) : go(d, few, std::false_type{}); };
+            auto pick = [&](auto d) { return kv.seqs <= 32 ? by_queries(d, std::true_type{}) : by_queries(d, std::false_type{}); };
             return kv.dim == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
         }
     });
