@@ -112,6 +112,15 @@ def test_many_sequences(hint):
 
 
 @HINTS
+@pytest.mark.parametrize("n,every", [(33, 13), (45, 13), (100, 13), (1100, 401)])
+def test_parts_among_many_sequences(n, every, hint):
+    """More than 32 sequences of which a few are long, so that some row tiles come in parts and most do not."""
+    seqs = [(2500 + i, 5) if i % every == 2 else (i * 7 % 90, i % 3) for i in range(n)]
+    check(ref.Batch(seqs, 2, 64, 16, torch.bfloat16, seed=n), 6, hint)
+    check(ref.Batch(seqs, 2, 64, 16, torch.float16, seed=n), 8, hint, window=1500)
+
+
+@HINTS
 def test_padding_rows_are_left(hint):
     check(ref.Batch([(20, 3), (0, 2)], 2, 64, 16, torch.float16, seed=7, first=4, pad=9), 4, hint)
 
