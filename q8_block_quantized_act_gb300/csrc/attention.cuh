@@ -20,10 +20,9 @@ namespace q8 {
 
 // Division of 0 .. 2^31 - 1 by a number that the launch fixes.
 struct Divide {
-    uint32_t by, factor, shift;
-    Divide(uint32_t d = 1) : by(d)
+    uint32_t factor, shift = 0;
+    Divide(uint32_t d = 1)
     {
-        shift = 0;
         while ((1u << shift) < d) ++shift;
         factor = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
     }
