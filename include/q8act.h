@@ -509,7 +509,8 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros.  What is at masked places (beyond lens, behind the
  *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
- *       to the cache's type for their product with the values.
+ *       to the cache's type for their product with the values: by half a step of the type at most, in f16 also by 2^-32
+ *       of the largest weight.  (The sum of the weights takes them unrounded.)
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
  *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.
  *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses

@@ -10,7 +10,8 @@
 // stages ahead across row tiles).  Four warps take 16 positions each, with their own running maximum and sum, so
 // they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16
 // rows are too few for tcgen05's 128, and it is not what bounds.  Scores, statistics and sums are f32; the weights
-// e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type.
+// e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type
+// (f16: 2^15 e^(s - mx), so that they fill its range).
 //
 // One token over 131071 positions of 32 + 8 heads x 128 bf16: 87 us (6.2 TB/s, 0.91 of a copy); 64 sequences of 500 to
 // 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 33 us (0.55: 7 us of launches, planning and joining kernel, the rest
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
                         }
                         mx[i] = m;
                     }
-                    const float base = m == NEG ? 0.0f : m;
+                    const float base = (m == NEG ? 0.0f : m) - weight_shift<T>(0.0f);
                     float e[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[j >> 1][2 * i + (j & 1)], a.scale, -base));

@@ -55,6 +55,12 @@ __device__ __forceinline__ float attn_ex2(float x)
     return r;
 }
 
+// The weights e^(s - mx) are rounded to T for the second product.  f16 ends at 2^-24: weights are taken 2^(15 - lag) fold in both
+// sums, where they reach up to 2^lag by themselves (a maximum that is behind by so much), so that they fill the type's
+// range and many small ones are not lost beside a large one.  bf16 has the range.
+template <typename T>
+__device__ constexpr float weight_shift(float lag) { return std::is_same<T, __half>::value ? 15.0f - lag : 0.0f; }
+
 // Key tiles that rows r0 .. r1 of a sequence see: the first one and how many.
 struct Span {
     int first, n;

@@ -15,7 +15,7 @@
 //                   infinities and NaN among those that only some see (attention.cuh)
 //   warp 11         works out the CTA's next units for the others, and brings their queries
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
-// at most 2^8 and nothing is lost (f32 sums, the type's relative precision).
+// at most 2^8 and nothing is lost (f32 sums, the type's relative precision; f16 weights are taken 2^7 fold, up to 2^15).
 //
 // Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 318 us
 // (1.73 PFLOP/s, 0.92 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     mx = m;
                 }
-                const float base = mx == NEG ? 0.0f : mx;
+                const float base = (mx == NEG ? 0.0f : mx) - weight_shift<T>(SLACK);
                 const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
                 float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
