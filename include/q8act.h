@@ -506,11 +506,14 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
  *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
  *       It must not overlap q (q itself is refused).
- *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros.  What is at masked places (beyond lens, behind the
- *       window, on pages that do not exist, at later positions) does not matter, NaN and infinities included.
+ *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros; one that sees a score
+ *       whose product with scale * log2(e) is beyond f32 gets NaN, as one does that sees a NaN among its scores.  What is at masked
+ *       places (beyond lens, behind the window, on pages that do not exist, at later positions) does not matter, NaN and
+ *       infinities included.
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
  *       to the cache's type for their product with the values: by half a step of the type at most, in f16 also by 2^-32
- *       of the largest weight.  (The sum of the weights takes them unrounded.)
+ *       of the largest weight.  (The sum of the weights takes them unrounded.)  The sums
+ *       are divided last: 2^8 times the positions times the largest value has to stay within f32 (bf16 values could pass it).
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
  *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.
  *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses

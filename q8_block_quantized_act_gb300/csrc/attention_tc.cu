@@ -434,7 +434,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int tok = a.by_group(r);
                 dst = static_cast<uint8_t *>(a.out) + ((x.row0 + tok) * a.ldo + (x.h * a.group + r - tok * a.group) * D) * out_size(a.otype);
             }
-            const float inv = split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;           // a row that sees nothing: 0
+            // A row that sees nothing: 0.  A score times scale beyond f32: mx is infinite and so no weight counts, NaN (joined
+            // parts, and warps in attention.cu, get it from the difference of two infinities).
+            const float none = mx == -NEG ? NAN : 0.0f;
+            const float inv = split ? 1.0f : sum == 0.0f ? none : 1.0f / sum;
             const int type = split ? Q8ACT_F32 : a.otype;
             uint8_t *out = smem + C::OFF_OUT + warp * OUT_BYTES;
 #pragma unroll 1

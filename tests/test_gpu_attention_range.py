@@ -64,3 +64,25 @@ def test_many_small_weights(t, bits, n, max_new):
     tol = a * rel + floor * size / total + ref.half(torch.float32) * want.abs()
     assert bool((tol < 0.25 * want).all())
     ref.close(got, want[:, None].expand(-1, HQ, -1), tol[:, None].expand(-1, HQ, -1))
+
+
+@KERNELS
+@pytest.mark.parametrize("n", [40, 700, 6000])
+@pytest.mark.parametrize("t,big,scale", [("bf16", 2.0 ** 50, 2.0 ** 30), ("f16", 2.0 ** 15, 2.0 ** 99)])
+def test_scores_beyond_f32(t, big, scale, n, max_new):
+    """A finite product whose scaled score is beyond f32: NaN where it is positive, nothing where it is negative."""
+    t = ref.TYPES[t]
+    k, v = torch.zeros((n, D), dtype=t), torch.randn((n, D), generator=torch.Generator().manual_seed(n)).to(t)
+    k[n // 2, 0] = big
+    q = torch.zeros((NEW, HQ, D), dtype=t)
+    q[:, 1, 0], q[:, 2, 0] = big, -big
+    got = q8.attention(one_sequence(k, v), q.cuda(), scale=scale, max_new=max_new, dtype=torch.float32).cpu()
+    device_ok()
+    assert bool(torch.isnan(got[:, 1]).all())
+    for h, left_out in ((0, False), (2, True), (3, False)):
+        x = v.double()
+        if left_out:
+            x[n // 2] = 0
+        seen = torch.arange(n - NEW, n)[:, None] + 1.0
+        mean = lambda y: y.cumsum(0)[n - NEW:] / (seen - int(left_out))           # noqa: E731
+        ref.close(got[:, h], mean(x), mean(x.abs()) * (2 * seen + 16) * 2.0 ** -23, f"head {h}")
