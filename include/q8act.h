@@ -486,8 +486,9 @@ typedef struct q8act_paged_kv {
  *   pairs (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p turns[i] / 2^64 for pair i.
  *   q [m][heads_q][dim], k, v [m][heads][dim]: elements of `type`, tokens ldq, ldk, ldv elements apart
  *       (rows 16-byte aligned; the parts of a fused projection's rows, for instance).
- *   q_out [m][heads_q][dim] of the cache's type, tokens ldqo apart: the rotated queries (it may be q
- *       itself where types and distances agree).  q and q_out may both be NULL (heads_q 0).
+ *   q_out [m][heads_q][dim] of the cache's type, tokens ldqo apart: the rotated queries.  It may be q
+ *       itself where types and distances agree, and otherwise shares no values with q, k and v (refused; parts of the same
+ *       wider rows are fine where they are equally many bytes apart), nor with the cache.  q and q_out may both be NULL (heads_q 0).
  *   turns [rot / 2]: each pair's fraction of a turn a position, times 2^64 (the angle is then exact modulo a
  *       turn at any position).  rot <= dim, a multiple of 16: the head's first rot values are rotated, as
  *       pairs (i, i + rot / 2), or (2i, 2i + 1) where interleaved is 1; the others are copied.  rot 0
@@ -505,7 +506,8 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   p - window < j where window > 0; keys and values of head h * heads / heads_q.
  *   q [m][heads_q][dim] of the cache's type, tokens ldq elements apart; heads_q a multiple of heads.
  *   out [m][heads_q][dim] of `otype`, tokens ldo apart, rounded once.
- *       It must not overlap q (q itself is refused).
+ *       It shares no values with q (refused; rows of both in the same wider rows are fine where ldq and ldo are the same
+ *       number of bytes), nor with the cache or ws.
  *   scale > 0, <= 2^100.  A token that sees no position, or only scores of -infinity, gets zeros; one that sees a score
  *       whose product with scale * log2(e) is beyond f32 gets NaN, as one does that sees a NaN among its scores.  What is at masked
  *       places (beyond lens, behind the window, on pages that do not exist, at later positions) does not matter, NaN and

@@ -583,7 +583,7 @@ def _batch(kv, what: str):
 def append_kv(kv, q, k, v, turns=None, interleaved: bool = False, out=None):
     """The new tokens' keys and values [m, heads, dim] into the cache of a PagedKV, keys and queries rotated
     by their positions on the way; returns the rotated queries [m, query heads, dim] in the cache's type
-    (`out`, which may be q itself where the types agree), or None without q.
+    (`out`, which may be q itself where the types agree but shares no values with k, v or other tokens' q), or None without q.
     q, k, v: float32, float16 or bfloat16 alike, views of a fused projection's rows for instance.
     turns: rope_turns(...) of the pairs that are rotated (2 * len(turns) <= dim values of each head, a
     multiple of 16), as pairs (i, i + len(turns)) or, interleaved, (2i, 2i + 1); None: no rotation."""
@@ -637,7 +637,7 @@ def attention_workspace(kv, heads: int):
 def attention(kv, q, scale=None, window: int = 0, max_new=None, ws=None, dtype=None, out=None):
     """Causal attention of the new tokens q [m, query heads, dim] (the cache's type) over a PagedKV whose cache
     holds their own keys and values already (append_kv): [m, query heads, dim] in dtype (default the cache's) or
-    out's type.  Query head i reads key/value head i * heads // query heads.
+    out's type.  Query head i reads key/value head i * heads // query heads.  out shares no values with q.
     scale: of the scores, default dim ** -0.5.  window: how many positions a token sees, itself included (0: all).
     max_new: the most new tokens that one sequence has, where the caller knows it (1 when decoding); it chooses
     the kernel and may be wrong.  ws: attention_workspace(kv, heads); by default one is allocated."""

@@ -734,6 +734,28 @@ static int check_paged(const q8act_paged_kv *kv, int64_t m, int64_t heads_q)
     return Q8ACT_OK;
 }
 
+// m rows of token values in memory, in bytes.
+struct Rows {
+    intptr_t at;
+    int64_t ld, size;
+};
+static Rows rows_of(const void *p, int64_t ld, int64_t values, int type)
+{
+    return Rows{reinterpret_cast<intptr_t>(p), ld * type_size(type), values * type_size(type)};
+}
+
+// Whether m rows of a and of b share a byte (rows equally far apart: exactly; otherwise where one begins before the other's end).
+// Beside each other in the same wider rows they do not.
+static bool rows_overlap(const Rows &a, const Rows &b, int64_t m)
+{
+    using Wide = __int128;                       // m and distances of 2^40 elements pass 64 bits
+    auto end = [&](const Rows &r) { return (Wide)r.at + (Wide)(m - 1) * r.ld + r.size; };
+    if (a.at >= end(b) || b.at >= end(a)) return false;
+    if (m == 1 || a.ld != b.ld) return true;
+    const Wide d = (((Wide)b.at - a.at) % a.ld + a.ld) % a.ld;       // from a row of a to the next beginning of one of b
+    return d < a.size || d + b.size > a.ld;
+}
+
 int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
                     int64_t ldv, int type, void *q_out, int64_t ldqo, int heads_q, const uint64_t *turns, int rot,
                     int interleaved, int64_t m, void *stream)
@@ -750,9 +772,16 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
     if (q && ((rc = check_rows(q, ldq, (int64_t)heads_q * kv->dim, type)) ||
               (rc = check_rows(q_out, ldqo, (int64_t)heads_q * kv->dim, kv->type))))
         return rc;
-    if (reinterpret_cast<uintptr_t>(turns) & 7u) return Q8ACT_ERR_ALIGN;
     if (q && q == q_out && type != kv->type) return Q8ACT_ERR_TYPE;
     if (q && q == q_out && ldq != ldqo) return Q8ACT_ERR_DIMS;
+    if (q) {             // a thread writes the 16 values that it has read, and no others
+        const int64_t n = (int64_t)kv->heads * kv->dim, nq = (int64_t)heads_q * kv->dim;
+        const Rows o = rows_of(q_out, ldqo, nq, kv->type);
+        if ((q != q_out && rows_overlap(rows_of(q, ldq, nq, type), o, m)) || rows_overlap(rows_of(k, ldk, n, type), o, m) ||
+            rows_overlap(rows_of(v, ldv, n, type), o, m))
+            return Q8ACT_ERR_DIMS;
+    }
+    if (reinterpret_cast<uintptr_t>(turns) & 7u) return Q8ACT_ERR_ALIGN;
     const q8::DeviceInfo *dev;
     if ((rc = current_device(&dev))) return rc;
     const q8::AppendArgs a{q, k, v, q_out, ldq, ldk, ldv, ldqo, turns, type, heads_q, rot, interleaved};
@@ -774,7 +803,7 @@ int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *
                     float scale, int window, int max_new, int64_t m, void *ws, size_t ws_bytes, void *stream)
 {
     if (!q || !out) return Q8ACT_ERR_NULL;
-    if (m < 1 || m > (1 << 30) || q == out) return Q8ACT_ERR_DIMS;
+    if (m < 1 || m > (1 << 30)) return Q8ACT_ERR_DIMS;
     int rc = check_paged(kv, m, heads_q);
     if (rc) return rc;
     if (!known_type(otype)) return Q8ACT_ERR_TYPE;
@@ -784,6 +813,9 @@ int q8act_attention(const q8act_paged_kv *kv, const void *q, int64_t ldq, void *
     if ((rc = check_rows(q, ldq, (int64_t)heads_q * kv->dim, kv->type)) ||
         (rc = check_rows(out, ldo, (int64_t)heads_q * kv->dim, otype)))
         return rc;
+    // (a unit's output may be written before another one has read its queries)
+    if (rows_overlap(rows_of(q, ldq, (int64_t)heads_q * kv->dim, kv->type), rows_of(out, ldo, (int64_t)heads_q * kv->dim, otype), m))
+        return Q8ACT_ERR_DIMS;
     if (!ws || ws_bytes < q8::attention_workspace_bytes(kv->dim)) return Q8ACT_ERR_WORKSPACE;
     if (!aligned16(ws)) return Q8ACT_ERR_ALIGN;
     const q8::DeviceInfo *dev;
