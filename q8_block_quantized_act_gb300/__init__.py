@@ -636,8 +636,8 @@ def attention_workspace(kv, heads: int):
 
 def attention(kv, q, scale=None, window: int = 0, max_new=None, ws=None, dtype=None, out=None):
     """Causal attention of the new tokens q [m, query heads, dim] (the cache's type) over a PagedKV whose cache
-    holds their own keys and values already (append_kv): [m, query heads, dim] in dtype (default the cache's) or
-    out's type.  Query head i reads key/value head i * heads // query heads.  out shares no values with q.
+    holds their own keys and values already (append_kv): [m, query heads, dim] in dtype (default the cache's, or
+    out's).  Query head i reads key/value head i * heads // query heads.  out shares no values with q.
     scale: of the scores, default dim ** -0.5.  window: how many positions a token sees, itself included (0: all).
     max_new: the most new tokens that one sequence has, where the caller knows it (1 when decoding); it chooses
     the kernel and may be wrong.  ws: attention_workspace(kv, heads); by default one is allocated."""
@@ -659,6 +659,8 @@ def attention(kv, q, scale=None, window: int = 0, max_new=None, ws=None, dtype=N
         out = torch.empty((m, hq, dim), dtype=dtype or q.dtype, device=q.device)
     elif out.shape != q.shape:
         raise Q8ActError(Q8ACT_ERR_DIMS, f"out: {tuple(q.shape)}")
+    elif dtype is not None and out.dtype is not dtype:
+        raise Q8ActError(Q8ACT_ERR_TYPE, f"out: {out.dtype}, dtype: {dtype}")
     code = _type(out, "out")
     if max_new is None:
         max_new = m

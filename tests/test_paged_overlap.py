@@ -93,7 +93,7 @@ def test_append_keys_and_values():
 
 
 def test_helper_says_so(monkeypatch):
-    """The same through the helpers, on tensors of this machine's memory; a type beside `out` that it does not have."""
+    """The same through the helpers, on tensors of this machine's memory."""
     q8._load_torch()
     monkeypatch.setattr(q8, "_current", lambda: -1)
     monkeypatch.setattr(q8, "_stream", lambda dev: 0)
@@ -108,4 +108,23 @@ def test_helper_says_so(monkeypatch):
     with pytest.raises(q8.Q8ActError) as e:
         q8.append_kv(kv, rows[:3], cache[0, :, :3].transpose(0, 1).contiguous(), cache[0, :, :3].transpose(0, 1).contiguous(),
                      out=rows[1:])
+    assert e.value.rc == DIMS
+
+
+def test_helper_refuses_two_types(monkeypatch):
+    """A dtype that `out` does not have (the same one passes: a later check refuses the window)."""
+    q8._load_torch()
+    monkeypatch.setattr(q8, "_current", lambda: -1)
+    monkeypatch.setattr(q8, "_stream", lambda dev: 0)
+    monkeypatch.setattr(q8, "lib", lambda: pytest.fail("reached the library"))
+    cache = torch.zeros((4, 2, 16, D), dtype=torch.float16)
+    i32 = dict(dtype=torch.int32)
+    kv = q8.PagedKV(cache, cache.clone(), torch.zeros((2, 3), **i32), torch.zeros(3, **i32), torch.zeros(2, **i32))
+    q, ws = torch.zeros((3, 4, D), dtype=torch.float16), torch.zeros(64, dtype=torch.uint8)
+    for out in (torch.zeros((3, 4, D)), torch.zeros((3, 4, D), dtype=torch.bfloat16)):
+        with pytest.raises(q8.Q8ActError) as e:
+            q8.attention(kv, q, ws=ws, out=out, dtype=torch.float16)
+        assert e.value.rc == TYPE
+    with pytest.raises(q8.Q8ActError) as e:
+        q8.attention(kv, q, ws=ws, out=torch.zeros((3, 4, D)), dtype=torch.float32, window=-1)
     assert e.value.rc == DIMS
