@@ -493,8 +493,8 @@ typedef struct q8act_paged_kv {
  *       turn at any position).  rot <= dim, a multiple of 16: the head's first rot values are rotated, as
  *       pairs (i, i + rot / 2), or (2i, 2i + 1) where interleaved is 1; the others are copied.  rot 0
  *       with turns NULL: no rotation.
- * f32 arithmetic, each value rounded once.  Two rows with the same place in the cache (a page that two
- * sequences share and both append to) leave one of the two there.
+ * f32 arithmetic, each value rounded once.  Where two rows have the same place in the cache (a page that two
+ * sequences share and both append to), each 16 bytes of it are from one of the two, not all of them from the same.
  */
 int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
                     int64_t ldv, int type, void *q_out, int64_t ldqo, int heads_q, const uint64_t *turns, int rot,
