@@ -517,7 +517,9 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *       of the largest weight.  (The sum of the weights takes them unrounded.)  The sums
  *       are divided last: 2^8 times the positions times the largest value has to stay within f32 (bf16 values could pass it).
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
- *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.
+ *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.  Not
+ *       known is taken as m, so that a batch of single tokens takes the kernel for chunks: 64 at 500 to 8192 positions 215 us
+ *       instead of 109, 190 at 37 to 600 92 instead of 34.
  *   ws: q8act_attention_workspace_bytes(heads_q, heads, dim) bytes, 16-byte aligned, which nothing else uses
  *       until the call's work is done; it needs no preparation and holds nothing between calls.
  */

@@ -639,8 +639,9 @@ def attention(kv, q, scale=None, window: int = 0, max_new=None, ws=None, dtype=N
     holds their own keys and values already (append_kv): [m, query heads, dim] in dtype (default the cache's, or
     out's).  Query head i reads key/value head i * heads // query heads.  out shares no values with q.
     scale: of the scores, default dim ** -0.5.  window: how many positions a token sees, itself included (0: all).
-    max_new: the most new tokens that one sequence has, where the caller knows it (1 when decoding); it chooses
-    the kernel and may be wrong.  ws: attention_workspace(kv, heads); by default one is allocated."""
+    max_new: the most new tokens that one sequence has, where the caller knows it; it chooses the kernel and may be
+    wrong.  Pass 1 when decoding: by default it is m, which gives a batch of single tokens the kernel for chunks, 1.4 to
+    2.7 times slower.  ws: attention_workspace(kv, heads); by default one is allocated."""
     torch = _torch or _load_torch()
     dev = _batch(kv, "kv")
     if q.dim() != 3:

@@ -43,7 +43,7 @@ def make_block(norm, qkv, out, heads_q: int, heads: int, dim: int, base: float =
 
 def attend(block: Block, kv, x, residual, max_new=None, ws=None, eps: float = 1e-6):
     """x, residual [m, k] float32 (the residual stream is updated in place), kv a PagedKV of the m new
-    tokens -> the block's output [m, k] float32."""
+    tokens, max_new as attention takes it (1 when decoding) -> the block's output [m, k] float32."""
     m, k = x.shape
     hq, hk, d = block.heads_q, block.heads, block.dim
     n = (hq + 2 * hk) * d

@@ -219,7 +219,9 @@ cudaError_t launch_append_kv(const DeviceInfo &dev, const q8act_paged_kv &kv, co
                     return launch_dependent(kern, dim3((unsigned)blocks, (unsigned)parts), THREADS, 0, stream, a);
                 };
                 // Two tokens a CTA share its sines' latency: 8191 tokens of 32 + 8 heads x 128 bf16 36.5 us, one by one
-                // 37.8, four 39.6.  Few tokens are worth a CTA each (62 tokens: the same 3.8 us).
+                // 37.8, four 39.6; 64 values 18.4 and 20.8; 1000 tokens of 128 values 7.4 and 8.3.  From f32 rows two need 74
+                // registers, one 58, and lose: 8191 tokens 49.4 (0.90 of a copy) and 48.3, 1000 tokens 10.8 and 8.5, 64 values
+                // the same 24.5.  Few tokens are worth a CTA each (62 tokens: the same 3.8 us).
                 if (m >= 4 * (int64_t)dev.num_sms)
                     return kv.dim == 64 ? go(append_kernel<T, C, 64, 2>, 2) : go(append_kernel<T, C, 128, 2>, 2);
                 return kv.dim == 64 ? go(append_kernel<T, C, 64, 1>, 1) : go(append_kernel<T, C, 128, 1>, 1);

@@ -365,7 +365,7 @@ struct Plan {
 // ---------------------------------------------------------------------------------------
 // Output
 // ---------------------------------------------------------------------------------------
-// N consecutive values of `type` (4, 8 or 16 of them, 16-byte aligned where they fill 16 bytes).
+// Four consecutive values of `type`, 16-byte aligned as f32 and 8-byte aligned otherwise.
 __device__ __forceinline__ void store4(void *p, int type, float4 v)
 {
     if (type == Q8ACT_F32) {

@@ -861,7 +861,10 @@ cudaError_t launch_attention_chunk(const DeviceInfo &dev, const q8act_paged_kv &
     attention_place(a, ws, SLOTS, ROWS);
     a.ctas = dev.num_sms;
     a.least = 2;
-    a.unit_cost = 8.0f;          // (509 tokens at 16384: 4 cuts each row tile in 7 and took 132 us when 8, in 2, took 115; now 102)
+    // 128 values a head, f16: 509 tokens at 16384 (32 + 8 heads) 4 cuts each row tile in 7 and takes 116 us, 8 and 16 in 2: 101; 200 at
+    // 30000 2: 109, 4: 97, 8 and 16: 90.  64 values: 2, 4, 8 and 16 within 1.5 % of each other (509 at 16384, 64 + 8 heads 148, 20 + 4
+    // heads 60.5; 200 at 30000, 12 + 12 heads 36; window, verification and mixed batches, too).
+    a.unit_cost = 8.0f;
     CUtensorMap tk, tv, tq;
     if (!attention_maps(kv, TILE, &tk, &tv)) return cudaErrorInvalidValue;
     const bool q_boxes = QROWS % a.group == 0;
