@@ -456,10 +456,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
                 uint32_t pf[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                    // Products rounded before mx is subtracted, and mx upwards: the largest score's exponent is 15 in f16 and 0 in
+                    // bf16 at most whatever its size, where an fma's would be what the product in mx has been rounded by.
+                    float e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] = __fmul_rn(s[j >> 1][2 * i + (j & 1)], a.scale);
+                    float m = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    m = fmaxf(mx[i], m * a.scale);
+                    m = fmaxf(mx[i], __fadd_ru(m, -weight_shift<T>(0)));
                     if (__any_sync(0xffffffffu, m > mx[i])) {
                         const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
                         sum[i] *= f;
@@ -470,10 +475,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
                         }
                         mx[i] = m;
                     }
-                    const float base = (m == NEG ? 0.0f : m) - weight_shift<T>(0.0f);
-                    float e[4];
+                    const float base = m == NEG ? 0.0f : m;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) e[j] = attn_ex2(fmaf(s[j >> 1][2 * i + (j & 1)], a.scale, -base));
+                    for (int j = 0; j < 4; ++j) e[j] = attn_ex2(__fsub_rn(e[j], base));
                     sum[i] += (e[0] + e[1]) + (e[2] + e[3]);
                     pf[i] = pack2<T>(e[0], e[1]);
                     pf[i + 2] = pack2<T>(e[2], e[3]);
@@ -807,6 +811,7 @@ cudaError_t launch_attention(const DeviceInfo &dev, const q8act_paged_kv &kv, co
     a.otype = s.otype;
     a.window = s.window;
     a.scale = s.scale * 1.4426950408889634f;
+    a.far_scale = exp2f(floorf(log2f(a.scale)) + 1.0f);
     a.status = dev.status;
     const int64_t most = s.max_new && s.max_new < m ? s.max_new : m;     // new tokens of a sequence
     // One row tile of 16 a head here, or half full ones of 256 there: 16 sequences at 6000 of 28 + 4 heads x 128, 14

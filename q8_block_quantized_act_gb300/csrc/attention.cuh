@@ -37,6 +37,7 @@ struct Attn {
     int64_t ldq, ldo;
     int group, otype, window;    // window 0: all earlier positions
     float scale;                 // of scores, times log2 e
+    float far_scale;             // the next power of two above it (attention_tc.cu)
     // How units are cut (Plan): CTAs that take them, the fewest key tiles that a part is worth, what a unit costs beside
     // its tiles (in tiles), partial results that the workspace has room for.
     int ctas, least, slots;
@@ -55,11 +56,11 @@ __device__ __forceinline__ float attn_ex2(float x)
     return r;
 }
 
-// The weights e^(s - mx) are rounded to T for the second product.  f16 ends at 2^-24: weights are taken 2^(15 - lag) fold in both
-// sums, where they reach up to 2^lag by themselves (a maximum that is behind by so much), so that they fill the type's
-// range and many small ones are not lost beside a large one.  bf16 has the range.
+// The weights 2^(s scale - mx) are rounded to T for the second product.  f16 ends at 2^-24: mx is 15 - lag below the largest
+// score, where weights reach up to 2^lag by themselves (of a score that passes the largest one that mx knows of), so that they fill
+// the type's range and many small ones are not lost beside a large one.  bf16 has the range.
 template <typename T>
-__device__ constexpr float weight_shift(float lag) { return std::is_same<T, __half>::value ? 15.0f - lag : 0.0f; }
+__device__ constexpr float weight_shift(int lag) { return std::is_same<T, __half>::value ? 15 - lag : 0; }
 
 // Key tiles that rows r0 .. r1 of a sequence see: the first one and how many.
 struct Span {

@@ -43,7 +43,7 @@ constexpr int THREADS = 384;
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;      // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
 constexpr int PARTS = 2;                 // of a tile's weights, handed to the MMAs one by one
 constexpr float NEG = -INFINITY;
-constexpr float SLACK = 8.0f;
+constexpr int SLACK = 8;
 constexpr int OUT_BYTES = 32 * 128;
 
 template <int D>
@@ -191,6 +191,39 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, int *sta
            __all_sync(0xffffffffu, wait_or_abort(bar, parity, status, abort_flag));
 }
 
+// What a row's weights 2^(s scale - mx) are relative to.
+//
+// The exponent is one fma, exact but for its result's rounding, so for the largest score it is what the product in mx has been
+// rounded by: upwards, and less than 8 up to FAR (so that an f16 weight is 2^15 at most, the slack rounded downwards).  Beyond, scores themselves are 4 and more apart, and mx would be rounded by what
+// leaves no weight at all: a power of two takes the scale's place there, whose products are exact.  So equal scores have equal
+// weights, whatever their size.  (Parts of a row on either side of FAR: the larger score's has all the weight.)  A rounded
+// product and a subtraction, as in attention.cu, are twice the instructions on the 128 scores of a thread.
+constexpr float FAR = 0x1p26f;
+
+template <typename T>
+struct Reference {
+    static constexpr float SHIFT = weight_shift<T>(SLACK);
+    float mx = NEG, scale;
+
+    __device__ __forceinline__ explicit Reference(const Attn &a) : scale(a.scale) {}
+    __device__ __forceinline__ float base() const { return mx == NEG ? 0.0f : mx; }
+    // mx if the largest score were s.  (Beyond FAR nothing is subtracted in the end, so that mx may be behind by 15 there.)
+    __device__ __forceinline__ float with(float s) const { return fmaxf(mx, __fmaf_ru(s, scale, -SHIFT)); }
+    // The largest score is s now, m = with(s): what the sums so far are to be multiplied by.  (mx may be -inf: they are zeros.)
+    __device__ __forceinline__ float rise(const Attn &a, float s, float m)
+    {
+        if (m > mx) {
+            m = __fmaf_ru(s, a.scale, -SHIFT);
+            const bool far = fabsf(m) > FAR;
+            scale = far ? a.far_scale : a.scale;
+            if (far) m = s * a.far_scale;
+        }
+        const float f = attn_ex2(mx - (m == NEG ? 0.0f : m));
+        mx = m;
+        return f;
+    }
+};
+
 // The unit of this CTA's round: rounds run forwards and backwards in turn, since earlier units are longer.
 __device__ __forceinline__ int64_t unit_of(int round)
 {
@@ -326,7 +359,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t tiles0 = tiles;               // tile t of the sequence is tile tiles0 + t - t0 of the CTA
             const bool some = end > from;
             tiles += x.t1 - x.t0;
-            float mx = NEG, sum = 0.0f;
+            Reference<T> at(a);
+            float sum = 0.0f;
             bool first = true;
             for (int t = from; t < end; ++t) {
                 ok = arrived(&sm.s_full[q], s_phase, a.status, abort_flag);
@@ -360,7 +394,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < TILE; j += 16)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[j + 2 * i]), s[j + 2 * i + 1]);
-                const float m = fmaxf(mx, fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), fmaxf(fmaxf(m4[4], m4[5]), fmaxf(m4[6], m4[7]))) * a.scale);
+                const float largest = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), fmaxf(fmaxf(m4[4], m4[5]), fmaxf(m4[6], m4[7])));
+                const float m = at.with(largest);
                 if constexpr (C::OWN_P) {           // the last products have taken P, and added to O
                     ok = arrived(&sm.p_empty[q], p_phase, a.status, abort_flag);
                     if (!ok) break;
@@ -368,11 +403,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                 }
                 if (first) {
-                    mx = m;
+                    at.rise(a, largest, m);
                     first = false;
-                } else if (__any_sync(0xffffffffu, m > mx + SLACK)) {
-                    // (mx may be -inf: nothing seen so far, O and the sum are zeros)
-                    const float f = attn_ex2(mx - (m == NEG ? 0.0f : m));
+                } else if (__any_sync(0xffffffffu, m > __fadd_rd(at.mx, SLACK))) {
+                    const float f = at.rise(a, largest, m);
                     sum *= f;
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
@@ -383,10 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < 32; ++j) o[j] *= f;
                         st32(col_o + 32 * i, reinterpret_cast<const uint32_t *>(o));
                     }
-                    mx = m;
                 }
-                const float base = (mx == NEG ? 0.0f : mx) - weight_shift<T>(SLACK);
-                const float2 scale2 = make_float2(a.scale, a.scale), base2 = make_float2(-base, -base);
+                const float base = at.base();
+                const float2 scale2 = make_float2(at.scale, at.scale), base2 = make_float2(-base, -base);
                 float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < PARTS; ++c) {
@@ -428,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint8_t *dst = nullptr;
             if (live && split) {
                 const int64_t slot = (int64_t)x.slot * ROWS + q * QROWS + row;
-                a.ml[slot] = make_float2(mx, sum);
+                a.ml[slot] = make_float2(at.mx, sum);
                 dst = reinterpret_cast<uint8_t *>(a.part + slot * D);
             } else if (live) {
                 const int tok = a.by_group(r);
@@ -436,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // A row that sees nothing: 0.  A score times scale beyond f32: mx is infinite and so no weight counts, NaN (joined
             // parts, and warps in attention.cu, get it from the difference of two infinities).
-            const float none = mx == -NEG ? NAN : 0.0f;
+            const float none = at.mx == -NEG ? NAN : 0.0f;
             const float inv = split ? 1.0f : sum == 0.0f ? none : 1.0f / sum;
             const int type = split ? Q8ACT_F32 : a.otype;
             uint8_t *out = smem + C::OFF_OUT + warp * OUT_BYTES;
@@ -453,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (spoilt && live) {
                     float e[64];
-                    cleared_part<T, D>(a, x, q * QROWS + row, i, mx == NEG ? 0.0f : mx, e);
+                    cleared_part<T, D>(a, x, q * QROWS + row, i, at.base(), e);
 #pragma unroll
                     for (int j = 0; j < 64; ++j) o[j] += e[j];
                 }

@@ -86,3 +86,62 @@ def test_scores_beyond_f32(t, big, scale, n, max_new):
         seen = torch.arange(n - NEW, n)[:, None] + 1.0
         mean = lambda y: y.cumsum(0)[n - NEW:] / (seen - int(left_out))           # noqa: E731
         ref.close(got[:, h], mean(x), mean(x.abs()) * (2 * seen + 16) * 2.0 ** -23, f"head {h}")
+
+
+@KERNELS
+@pytest.mark.parametrize("n", [40, 700, 6000])
+@pytest.mark.parametrize("t,size", [("f16", 2.0 ** 8), ("f16", 1800.0), ("f16", 2.0 ** 13 + 8), ("f16", 65504.0),
+                                    ("bf16", 1e4), ("bf16", 1e8), ("bf16", 1e17)])
+def test_large_equal_scores(t, size, n, max_new):
+    """Finite scores whose products with the scale lie between numbers of f32 that are far apart: equal ones weigh the same,
+    those that are far below nothing."""
+    t = ref.TYPES[t]
+    g = torch.Generator().manual_seed(n)
+    v = torch.randn((n, D), generator=g).to(t)
+    high = torch.rand(n, generator=g) < 0.4
+    high[n // 3] = True
+    k = torch.where(high[:, None], size, -size).expand(n, D).to(t).contiguous()
+    q = torch.full((NEW, HQ, D), size).to(t)
+    q[:, 1] = -q[:, 1]                                                           # the others win
+    q[:, 2] *= 0.5
+    q[:, 3] = 0
+    for scale in (0.125, 0.1, 0.3):
+        got = q8.attention(one_sequence(k, v), q.cuda(), scale=scale, max_new=max_new, dtype=torch.float32).cpu()
+        device_ok()
+        for h, mine in ((0, high), (1, ~high), (2, high), (3, torch.ones_like(high))):
+            x = torch.where(mine[:, None], v.double(), 0.0)
+            count = mine.double().cumsum(0)[n - NEW:, None]
+            mean = lambda y: y.cumsum(0)[n - NEW:] / count                        # noqa: B023, E731
+            # equal weights below 1, each rounded to the type once (in f16 at 2^-32 of the largest, at the least)
+            tol = mean(x.abs()) * (ref.half(t) + (2 * n + 16) * 2.0 ** -23)
+            ref.close(got[:, h], mean(x), tol, f"head {h}, scale {scale}")
+
+
+@KERNELS
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("steps", [1, 4])
+@pytest.mark.parametrize("e", [20, 24, 25, 26, 27, 28, 30])
+def test_large_rising_scores(e, steps, t, max_new):
+    """Scores of 2^e (to the base of 2) that rise by so many steps of f32 every 128 positions: the last ones have the weight.
+    A scaled score is known to half a step, so one below them may weigh 2^step times as much."""
+    t, n = ref.TYPES[t], 900
+    step = 2.0 ** (e - 23)
+    k = torch.zeros((n, D))
+    k[:, 0], k[:, 1] = 2.0 ** (e - 15), (torch.arange(n) // 128).float() * steps
+    v = torch.randn((n, D), generator=torch.Generator().manual_seed(e)).to(t)
+    q = torch.zeros((NEW, HQ, D))
+    q[:, :, 0], q[:, :, 1] = 2.0 ** 15, step
+    q[:, 1, 1] = 0                                                               # all the same
+    got = q8.attention(one_sequence(k.to(t), v), q.to(t).cuda(), scale=math.log(2.0), max_new=max_new, dtype=torch.float32).cpu()
+    device_ok()
+    for i in range(NEW):
+        seen = n - NEW + 1 + i
+        x = v[:seen].double()
+        for h in range(HQ):
+            s = k[:seen, 1].double() * (0.0 if h == 1 else step)
+            w = 2.0 ** (s - s.max())
+            below = torch.where(s < s.max(), w, torch.zeros_like(w)).sum() * (2.0 ** step if step > 2.0 ** -3 else 4 * step)
+            w = w / w.sum()
+            a = (w[:, None] * x.abs()).sum(0)
+            tol = a * (ref.half(t) + (2 * seen + 16) * 2.0 ** -23) + below / w.sum() * (x.abs().amax(0) + a)
+            ref.close(got[i, h], (w[:, None] * x).sum(0), tol, f"token {i}, head {h}")
