@@ -515,7 +515,7 @@ int q8act_append_kv(const q8act_paged_kv *kv, const void *q, int64_t ldq, const 
  *   Scores and sums are f32; the softmax's weights, relative to the largest score met so far, are rounded
  *       to the cache's type for their product with the values: by half a step of the type at most, in f16 also by 2^-32
  *       of the largest weight.  (The sum of the weights takes them unrounded.)  The sums
- *       are divided last: 2^8 times the positions times the largest value has to stay within f32 (bf16 values could pass it).
+ *       are divided last: beyond 2^20 positions bf16 values near the type's largest may pass f32.
  *   max_new: the most new tokens that a sequence of the batch has, as far as the caller knows (0: not
  *       known).  It chooses the kernel (max_new * heads_q / heads up to 16: the one for few rows) and may be wrong.  Not
  *       known is taken as m, so that a batch of single tokens takes the kernel for chunks: 64 at 500 to 8192 positions 215 us

@@ -11,7 +11,7 @@
 // they meet only at the end of a row tile.  The products run on the warp-level tensor-core MMA: 16
 // rows are too few for tcgen05's 128, and it is not what bounds.  Scores, statistics and sums are f32; the weights
 // e^(s - mx) <= 1 are rounded to the cache's type for the second product, whose operands have one type
-// (f16: 2^15 e^(s - mx), so that they fill its range).
+// (times a power of two, weight_shift).
 //
 // One token over 131071 positions of 32 + 8 heads x 128 bf16: 87 us (6.2 TB/s, 0.91 of a copy); 64 sequences of 500 to
 // 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 33 us (0.55: 7 us of launches, planning and joining kernel, the rest
@@ -456,15 +456,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
                 uint32_t pf[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // Products rounded before mx is subtracted, and mx upwards: the largest score's exponent is 15 in f16 and 0 in
-                    // bf16 at most whatever its size, where an fma's would be what the product in mx has been rounded by.
+                    // Products rounded before mx is subtracted: the largest score's exponent is within the shift whatever its size,
+                    // where an fma's would be what the product in mx has been rounded by.
                     float e[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) e[j] = __fmul_rn(s[j >> 1][2 * i + (j & 1)], a.scale);
                     float m = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    m = fmaxf(mx[i], __fadd_ru(m, -weight_shift<T>(0)));
+                    m = fmaxf(mx[i], shifted<T>(m, 1.0f, 0));
                     if (__any_sync(0xffffffffu, m > mx[i])) {
                         const float f = attn_ex2(mx[i] - (m == NEG ? 0.0f : m));
                         sum[i] *= f;

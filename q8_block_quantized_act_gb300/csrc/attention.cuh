@@ -56,11 +56,20 @@ __device__ __forceinline__ float attn_ex2(float x)
     return r;
 }
 
-// The weights 2^(s scale - mx) are rounded to T for the second product.  f16 ends at 2^-24: mx is 15 - lag below the largest
-// score, where weights reach up to 2^lag by themselves (of a score that passes the largest one that mx knows of), so that they fill
-// the type's range and many small ones are not lost beside a large one.  bf16 has the range.
+// The weights 2^(s scale - mx) are rounded to T for the second product, and mx is not the largest score itself but `shift` below it;
+// lag: by how much a score may pass the largest one that mx knows of.
+// f16 ends at 2^-24: weights reach up to 2^15, so that they fill the type's range and many small ones are not lost beside a large one.
+// bf16 has the range in its values, too: weights stay below 2^-20, so that the sum of a million of the largest values is still
+// within f32 before it is divided (and values down to 2^-100 keep their precision there).
 template <typename T>
-__device__ constexpr float weight_shift(int lag) { return std::is_same<T, __half>::value ? 15 - lag : 0; }
+__device__ constexpr float weight_shift(int lag) { return (std::is_same<T, __half>::value ? 15 : -20) - lag; }
+// mx of the largest score's product with its scale: rounded towards that product, so that the weight is not beyond 1 and 2^shift
+// however far apart the numbers of f32 are there.
+template <typename T>
+__device__ __forceinline__ float shifted(float s, float scale, int lag)
+{
+    return std::is_same<T, __half>::value ? __fmaf_ru(s, scale, -weight_shift<T>(lag)) : __fmaf_rd(s, scale, -weight_shift<T>(lag));
+}
 
 // Key tiles that rows r0 .. r1 of a sequence see: the first one and how many.
 struct Span {

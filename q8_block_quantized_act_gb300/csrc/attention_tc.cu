@@ -15,7 +15,7 @@
 //                   infinities and NaN among those that only some see (attention.cuh)
 //   warp 11         works out the CTA's next units for the others, and brings their queries
 // O is rescaled only when a row's maximum has risen by more than 2^8 since the last time: until then P is
-// at most 2^8 and nothing is lost (f32 sums, the type's relative precision; f16 weights are taken 2^7 fold, up to 2^15).
+// at most 2^8 (times a power of two, weight_shift) and nothing is lost (f32 sums, the type's relative precision).
 //
 // Bound by the tensor cores and by what they wait for.  128 values a head: 8192 tokens of 32 + 8 heads bf16 318 us
 // (1.73 PFLOP/s, 0.92 of cuBLAS's bf16 burst rate), the tensor pipe 76 % busy; a step of both row tiles is 2048 tensor
@@ -191,32 +191,31 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, int *sta
            __all_sync(0xffffffffu, wait_or_abort(bar, parity, status, abort_flag));
 }
 
-// What a row's weights 2^(s scale - mx) are relative to.
+// What a row's weights 2^(s scale - mx) are relative to, and the scale.
 //
-// The exponent is one fma, exact but for its result's rounding, so for the largest score it is what the product in mx has been
-// rounded by: upwards, and less than 8 up to FAR (so that an f16 weight is 2^15 at most, the slack rounded downwards).  Beyond, scores themselves are 4 and more apart, and mx would be rounded by what
-// leaves no weight at all: a power of two takes the scale's place there, whose products are exact.  So equal scores have equal
-// weights, whatever their size.  (Parts of a row on either side of FAR: the larger score's has all the weight.)  A rounded
-// product and a subtraction, as in attention.cu, are twice the instructions on the 128 scores of a thread.
+// The exponent is one fma, exact but for its result's rounding, so for the largest score it is the shift and what the product in mx
+// has been rounded by: less than 8 up to FAR.  Beyond, scores themselves are 4 and more apart, and that would leave no weight at
+// all: a power of two takes the scale's place there, whose products are exact.  So equal scores have equal weights, whatever their
+// size.  (Parts of a row on either side of FAR: the larger score's has all the weight.)  A rounded product and a subtraction, as in
+// attention.cu, are twice the instructions on the 128 scores of a thread.
 constexpr float FAR = 0x1p26f;
 
 template <typename T>
 struct Reference {
-    static constexpr float SHIFT = weight_shift<T>(SLACK);
     float mx = NEG, scale;
 
     __device__ __forceinline__ explicit Reference(const Attn &a) : scale(a.scale) {}
     __device__ __forceinline__ float base() const { return mx == NEG ? 0.0f : mx; }
-    // mx if the largest score were s.  (Beyond FAR nothing is subtracted in the end, so that mx may be behind by 15 there.)
-    __device__ __forceinline__ float with(float s) const { return fmaxf(mx, __fmaf_ru(s, scale, -SHIFT)); }
+    // mx if the largest score were s.
+    __device__ __forceinline__ float with(float s) const { return fmaxf(mx, shifted<T>(s, scale, SLACK)); }
     // The largest score is s now, m = with(s): what the sums so far are to be multiplied by.  (mx may be -inf: they are zeros.)
     __device__ __forceinline__ float rise(const Attn &a, float s, float m)
     {
         if (m > mx) {
-            m = __fmaf_ru(s, a.scale, -SHIFT);
+            m = shifted<T>(s, a.scale, SLACK);
             const bool far = fabsf(m) > FAR;
             scale = far ? a.far_scale : a.scale;
-            if (far) m = s * a.far_scale;
+            if (far) m = shifted<T>(s, a.far_scale, SLACK);
         }
         const float f = attn_ex2(mx - (m == NEG ? 0.0f : m));
         mx = m;

@@ -145,3 +145,33 @@ def test_large_rising_scores(e, steps, t, max_new):
             a = (w[:, None] * x.abs()).sum(0)
             tol = a * (ref.half(t) + (2 * seen + 16) * 2.0 ** -23) + below / w.sum() * (x.abs().amax(0) + a)
             ref.close(got[i, h], (w[:, None] * x).sum(0), tol, f"token {i}, head {h}")
+
+
+@KERNELS
+@pytest.mark.parametrize("n", [40, 6000, 131071])
+@pytest.mark.parametrize("t,size", [("bf16", torch.finfo(torch.bfloat16).max), ("bf16", 2.0 ** 120), ("bf16", 2.0 ** -100),
+                                    ("f16", 65504.0), ("f16", 2.0 ** -24)])
+def test_values_of_any_size(t, size, n, max_new):
+    """An average is as large as its values, however many of the largest there are, and however small they are."""
+    t = ref.TYPES[t]
+    g = torch.Generator().manual_seed(n)
+    k, v = torch.randn((n, D), generator=g).to(t), torch.full((n, D), size)
+    v[:, 1::2] *= torch.where(torch.rand((n, D // 2), generator=g) < 0.25, -1.0, 1.0)
+    v = v.to(t)
+    q = torch.randn((NEW, HQ, D), generator=g).to(t)
+    q[:, 0] = 0                                                                  # equal weights
+    got = q8.attention(one_sequence(k, v), q.cuda(), max_new=max_new, dtype=torch.float32).cpu()
+    device_ok()
+    U, unit = 2.0 ** -23, v.double() / size
+    for i in range(NEW):
+        seen = n - NEW + 1 + i
+        s = (q[i].double() @ k[:seen].double().T) * D ** -0.5
+        w = torch.softmax(s, -1)
+        want = w @ unit[:seen]
+        ds = (D + 4) * U * (q[i].double().abs() @ k[:seen].double().abs().T).amax(-1, keepdim=True) * D ** -0.5
+        tol = ref.half(t) + 2 * ds + (2 * seen + 16) * U                         # (every |unit| is 1)
+        # where products with weights are below f32's normal numbers: each to 2^-149, of weights relative to 2^-28
+        tol = tol + seen * 2.0 ** -149 / (2.0 ** -28 * size)
+        if t is torch.float16:
+            tol = tol + seen * 2.0 ** -32
+        ref.close(got[i].double() / size, want, tol.expand_as(want), f"token {i}")
