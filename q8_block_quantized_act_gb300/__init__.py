@@ -498,8 +498,8 @@ class PagedKV:
     starts: int32 [seqs + 1]; sequence b's new tokens are rows starts[b] .. starts[b + 1] - 1 of the calls' arrays.
     lens: int32 [seqs], positions of each sequence with its new tokens.
 
-    The calls read table, starts and lens on the device when they run: change their contents in place and
-    use the same PagedKV (and the same captured graph) for the next step.  Page ids outside the cache (-1,
+    The calls read table, starts and lens on the device when they run: change their contents in place (other tensors
+    in their place are refused) and use the same PagedKV (and the same captured graph) for the next step.  Page ids outside the cache (-1,
     say) and positions beyond the table do not exist: nothing is written there, and they are masked."""
 
     __slots__ = ("k", "v", "table", "starts", "lens", "c", "at", "device", "heads", "dim")
@@ -538,6 +538,12 @@ class PagedKV:
                                 min(heads, 2 ** 31 - 1), min(dim, 2 ** 31 - 1), _TYPES[k.dtype])
         self.at = ctypes.addressof(self.c)
         self.device, self.heads, self.dim = dev, heads, dim
+
+    def __setattr__(self, name, value):
+        # The calls go by the addresses that were checked: another tensor would be read by none of them.
+        if getattr(self, name, value) is not value:
+            raise AttributeError(f"PagedKV.{name} stays what it was made of: change a tensor's contents in place")
+        object.__setattr__(self, name, value)
 
 
 def rope_turns(inv_freq, device=None):
