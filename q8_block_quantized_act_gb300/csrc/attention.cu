@@ -14,7 +14,7 @@
 // (times a power of two, weight_shift).
 //
 // One token over 131071 positions of 32 + 8 heads x 128 bf16: 87 us (6.2 TB/s, 0.91 of a copy); 64 sequences of 500 to
-// 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 33 us (0.55: 7 us of launches, planning and joining kernel, the rest
+// 8192: 108 us (0.91); 190 of 37 to 600, 12 heads x 64: 33.8 us (0.53: 7 us of launches, planning and joining kernel, the rest
 // row tiles' ends: 7.5 a CTA, about 1.2 us each); one over 4096: 11 us (0.22: 6 us from launch to output, of which the first keys' way 2, then the
 // joining kernel).
 #include <algorithm>
