@@ -40,14 +40,14 @@ struct Cfg {
     static constexpr int STAGES = 96 * 1024 / STAGE_BYTES;
     static constexpr int HALVES = D / 64;                       // 128-byte wide columns of a tile
     static constexpr int Q_STRIDE = D * 2 + 16;                 // bytes: rows in different banks
-    static constexpr int Q_BYTES = ROWS * Q_STRIDE, Q_BUFFERS = 2;
+    static constexpr int Q_BYTES = ROWS * Q_STRIDE, Q_BUFFERS = 3;
     static constexpr int OFF_Q = STAGES * STAGE_BYTES, OFF_SHARED = OFF_Q + Q_BUFFERS * Q_BYTES;
 };
 
 struct Shared {
     long long before[COUNTERS + 1];       // work before thread j's sequences
     long long sums[COUNTERS / 32];
-    uint64_t full[6], empty[6], q_full[2], q_empty[2];
+    uint64_t full[6], empty[6], q_full[3], q_empty[3];
     uint32_t ok[6];                       // a stage's 16-position blocks whose page exists
     float mx[2][KEY_WARPS][ROWS], sum[2][KEY_WARPS][ROWS];
     int spoilt[2][KEY_WARPS];             // a non-finite value that some rows see has been cleared
@@ -280,7 +280,6 @@ __device__ __forceinline__ bool clear_block(uint8_t *values, int lo, int hi)
             *w = f;
         }
     }
-    fence_proxy_async_smem();                       // before the next copies to the stage
     __syncwarp();
     return found;
 }
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], KEY_WARPS); }
-        for (int s = 0; s < 2; ++s) { mbar_init(&sm.q_full[s], 1); mbar_init(&sm.q_empty[s], KEY_WARPS); }
+        for (int s = 0; s < C::Q_BUFFERS; ++s) { mbar_init(&sm.q_full[s], 1); mbar_init(&sm.q_empty[s], KEY_WARPS); }
         sm.abort_flag = 0;
         fence_mbar_init();
     }
@@ -422,8 +421,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         uint32_t q[D / 16][4];
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) ldmatrix_x4(q[kk], qs + kk * 32);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
 
         for (int t = p.t0; t < p.t1; ++t) {
             if (!aborted) aborted = !__all_sync(0xffffffffu, wait_or_abort(&sm.full[st], phase, a.status, abort_flag));
@@ -493,6 +490,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
             }
             // The last stage is handed back after the join, which uses its memory.
             if (t + 1 < p.t1) {
+                fence_proxy_async_smem();                // reads before the next copies to the stage
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
                 if (++st == C::STAGES) {
@@ -516,7 +514,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         if (lane == 0) sm.spoilt[flip][warp] = spoilt;
         // (the next part's words go to the other flip: some warps may still read these.  They are written again only
         // behind the next part's barrier)
+        // The queries are handed back behind this barrier, where what has become of them has been exchanged.  (An arrival right
+        // behind their loads passed these where another CTA's filled the load queue, and the next queries came in between: of 10000
+        // sequences three rows a call.)
+        fence_proxy_async_smem();
         if (bar_red_or(1, 32 * KEY_WARPS, aborted)) return;
+        if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
         const bool some = p.t1 > p.t0;
         float *join = reinterpret_cast<float *>(stages + st * C::STAGE_BYTES);      // [warp][row][D], 16-byte words swizzled by row
         if (some) {
